@@ -387,6 +387,92 @@ int ssm_out_proj_bwd(const void *y, const void *W, const void *dout, void *dy, v
                      int64_t d_inner, int64_t d_model, int64_t L, int dtype, void *stream);
 
 /*
+ * ssm_head_scan_fwd -- the selective scan with one decay per head and a
+ * matrix state (linear attention with a decay for each head), on the matrix
+ * cores.  q plays the part of C, k of B and v of Delta * u of ssm_scan_fwd:
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,      o_t = scale * S_t^T q_t,
+ * S the head's [d_key, d_value] state, S_0 = h0.
+ *   q, k : [batch, L, n_qk_heads, d_key], dtype `dtype`; head h of the n_heads
+ *          heads reads head h / (n_heads / n_qk_heads).
+ *   v    : [batch, L, n_heads, d_value], dtype `dtype`.
+ *          Each of the three is dense over a token's row; *_token and *_batch
+ *          are its strides in elements between tokens and batch rows (views of
+ *          one projection's output), and its pointer needs the alignment of
+ *          its type only (16-byte aligned rows are the fast path).
+ *   g    : [batch, L, n_heads], dtype `dtype`: log decays, <= 0; -inf starts
+ *          the head's state anew at that token (packed sequences).  Nullable.
+ *   g_head : [n_heads] float32, a fixed log decay per head.  Nullable; at most
+ *          one of g and g_head is given, neither means no decay.
+ *   h0   : [batch, n_heads, d_key, d_value] float32 start state, nullable (zero).
+ *   lengths : [batch] int32 on the device, nullable (all L): tokens at and past
+ *          a row's length (clamped to 0 .. L) do not exist for the state, are
+ *          not read, and their o is zero.
+ *   scale : finite.
+ *   o    : [batch, L, n_heads, d_value], dtype `dtype`, dense output.
+ *   last_state : as h0, output, nullable: the state after the last token.
+ *   workspace : device memory of ssm_head_scan_workspace(..., backward = 0)
+ *          bytes (may be 0 and NULL), the caller's; calls that may run at the
+ *          same time need one each.
+ *   d_key, d_value <= 256; batch * n_heads <= 65535; n_heads a multiple of
+ *   n_qk_heads.
+ * Rounding: sums, decays and the state are float32.  With SSM_BF16 the scores
+ * q_i . k_j (decayed) are rounded to bfloat16 once and the state enters o's
+ * product as a pair of bfloat16.  A non-finite k or v reaches every output of its
+ * token's chunk (64 tokens, 32 for float32), those before it included.
+ * Errors: SSM_EINVAL, SSM_EUNSUPPORTED, SSM_EHIP.  No memory is allocated.
+ */
+int ssm_head_scan_fwd(const void *q, int64_t q_batch, int64_t q_token, const void *k, int64_t k_batch, int64_t k_token,
+                      const void *v, int64_t v_batch, int64_t v_token, const void *g, const float *g_head,
+                      const float *h0, const int32_t *lengths, float scale, void *o, float *last_state,
+                      void *workspace, int64_t workspace_bytes, int64_t batch, int64_t L, int64_t n_heads,
+                      int64_t n_qk_heads, int64_t d_key, int64_t d_value, int dtype, void *stream);
+
+/*
+ * ssm_head_scan_bwd -- gradients of ssm_head_scan_fwd for the loss
+ * sum(do * o) + sum(dlast * last_state).  With R_t = dLoss/dS_t,
+ *     R_t  = scale q_t do_t^T + exp(g_{t+1}) R_{t+1},    R_L += dlast
+ *     dq_t = scale S_t do_t,   dk_t = R_t v_t,   dv_t = R_t^T k_t
+ *     dg_t = exp(g_t) <R_t, S_{t-1}>,                    dh0 = exp(g_1) R_1
+ * dq and dk summed over the heads that share a q and k head.
+ *   do    : [batch, L, n_heads, d_value], dtype `dtype`, dense (`dout` here).
+ *   dlast : as h0, float32, nullable (zero).
+ *   dq, dk: [batch, L, n_qk_heads, d_key], dv: [batch, L, n_heads, d_value],
+ *           dtype `dtype`, dense outputs.  Tokens past a row's length get zero.
+ *   dg    : [batch, L, n_heads], dtype `dtype`, output, nullable; needs g.
+ *   dh0   : as h0, output, nullable.
+ *   workspace : ssm_head_scan_workspace(..., backward = 1) bytes.
+ * Every sum is taken in a fixed order: repeated calls give identical bits.
+ * Other arguments and errors as ssm_head_scan_fwd.
+ */
+int ssm_head_scan_bwd(const void *q, int64_t q_batch, int64_t q_token, const void *k, int64_t k_batch, int64_t k_token,
+                      const void *v, int64_t v_batch, int64_t v_token, const void *g, const float *g_head,
+                      const float *h0, const int32_t *lengths, float scale, const void *dout, const float *dlast,
+                      void *dq, void *dk, void *dv, void *dg, float *dh0, void *workspace, int64_t workspace_bytes,
+                      int64_t batch, int64_t L, int64_t n_heads, int64_t n_qk_heads, int64_t d_key, int64_t d_value,
+                      int dtype, void *stream);
+
+/*
+ * ssm_head_scan_workspace -- bytes of workspace that ssm_head_scan_fwd
+ * (backward = 0) or ssm_head_scan_bwd (1) needs for a size (host only).
+ */
+int ssm_head_scan_workspace(int64_t batch, int64_t L, int64_t n_heads, int64_t n_qk_heads, int64_t d_key,
+                            int64_t d_value, int dtype, int backward, int64_t *bytes);
+
+/*
+ * ssm_head_step -- one token of the head scan for every sequence:
+ *     S <- exp(g) S + k v^T,   o = scale * S^T q.
+ *   q, k : [batch, n_qk_heads, d_key], v, o: [batch, n_heads, d_value], g:
+ *   [batch, n_heads] (nullable), dtype `dtype`; g_head: [n_heads] float32,
+ *   nullable; state_in, state_out: [batch, n_heads, d_key, d_value] float32,
+ *   state_out equal to state_in (in place) or disjoint from it.  All dense and
+ *   16-byte aligned.
+ * Sizes and errors as ssm_head_scan_fwd.
+ */
+int ssm_head_step(const void *q, const void *k, const void *v, const void *g, const float *g_head, float scale,
+                  const float *state_in, float *state_out, void *o, int64_t batch, int64_t n_heads, int64_t n_qk_heads,
+                  int64_t d_key, int64_t d_value, int dtype, void *stream);
+
+/*
  * affine_scan -- inclusive scan of affine pairs along each row
  * ([Scan page] §1.2 and §2.1; [Mamba-2 page] §2.2).
  * A pair (a, b) is the map h -> a*h + b; composition, later step first, is

@@ -17,8 +17,8 @@ from typing import Optional, Tuple
 import torch
 
 __all__ = ["SSMError", "ssm_scan_fwd", "ssm_scan_fwd_states", "ssm_scan_fwd_conv", "ssm_scan_bwd",
-           "ssm_scan_bwd_conv", "ssm_step", "ssm_step_conv", "ssm_out_proj", "ssm_out_proj_bwd", "affine_scan",
-           "affine_scan_order", "plan_for", "library_path", "load_library", "PLANS"]
+           "ssm_scan_bwd_conv", "ssm_step", "ssm_step_conv", "ssm_out_proj", "ssm_out_proj_bwd", "ssm_head_scan_fwd",
+           "ssm_head_scan_bwd", "ssm_head_step", "affine_scan", "affine_scan_order", "plan_for", "library_path", "load_library", "PLANS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libssmscan.so")
@@ -82,6 +82,16 @@ def load_library():
     lib.ssm_out_proj.restype = I
     lib.ssm_out_proj_bwd.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I, P]
     lib.ssm_out_proj_bwd.restype = I
+    F = ctypes.c_float
+    strided = [P, I64, I64] * 3
+    lib.ssm_head_scan_fwd.argtypes = strided + [P, P, P, P, F, P, P, P, I64] + [I64] * 6 + [I, P]
+    lib.ssm_head_scan_fwd.restype = I
+    lib.ssm_head_scan_bwd.argtypes = strided + [P, P, P, P, F, P, P, P, P, P, P, P, P, I64] + [I64] * 6 + [I, P]
+    lib.ssm_head_scan_bwd.restype = I
+    lib.ssm_head_scan_workspace.argtypes = [I64] * 6 + [I, I, ctypes.POINTER(I64)]
+    lib.ssm_head_scan_workspace.restype = I
+    lib.ssm_head_step.argtypes = [P, P, P, P, P, F, P, P, P] + [I64] * 5 + [I, P]
+    lib.ssm_head_step.restype = I
     lib.affine_scan.argtypes = [P, P, P, P, I64, I64, P]
     lib.affine_scan.restype = I
     lib.affine_scan_order.argtypes = [ctypes.POINTER(I)] * 4
@@ -618,6 +628,171 @@ def ssm_out_proj_bwd(y: torch.Tensor, W: torch.Tensor, dout: torch.Tensor, want_
                                   SSM_F32 if dt == torch.float32 else SSM_BF16, _stream(device))
     _check(rc)
     return dy, dW
+
+
+def _head_operand(t: torch.Tensor, name: str, dtype, device, shape):
+    """[b, L, heads, d], dense over a token's row; the strides of tokens and batch rows are the caller's."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    h, d = shape[-2:]
+    if (d > 1 and t.stride(-1) != 1) or (h > 1 and t.stride(-2) != d):
+        raise ValueError(f"{name} must be dense over a token's heads (only the strides of batch rows and tokens are free)")
+    # a stride over a size of one addresses nothing
+    token = t.stride(1) if shape[1] > 1 else h * d
+    return _ptr(t), t.stride(0) if shape[0] > 1 else shape[1] * token, token
+
+
+def _head_sizes(q: torch.Tensor, v: torch.Tensor, name: str, dims: int):
+    if q.device.type != "cuda":
+        raise ValueError(f"{name} needs CUDA/HIP tensors")
+    if q.dim() != dims or v.dim() != dims:
+        raise ValueError("q and k must be [b, {0}n_qk_heads, d_key] and v [b, {0}n_heads, d_value]".format(
+            "L, " if dims == 4 else ""))
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("q must be float32 or bfloat16")
+
+
+def _head_decay(g, g_head, shape, heads, dtype, device):
+    if g is not None and g_head is not None:
+        raise ValueError("give g or g_head, not both")
+    if g is not None:
+        _need(g, "g", dtype, device, shape)
+    if g_head is not None:
+        _need(g_head, "g_head", torch.float32, device, (heads,))
+
+
+def _workspace(lib, device, sizes, dt, backward: bool) -> Optional[torch.Tensor]:
+    n = ctypes.c_int64()
+    _check(lib.ssm_head_scan_workspace(*sizes, SSM_F32 if dt == torch.float32 else SSM_BF16, int(backward),
+                                       ctypes.byref(n)))
+    return torch.empty(n.value, device=device, dtype=torch.uint8) if n.value else None
+
+
+def ssm_head_scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor] = None,
+                      g_head: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                      lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                      return_last_state: bool = True, o: Optional[torch.Tensor] = None,
+                      last_state: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Scan with one decay per head and a matrix state, S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t
+    (see ``ssm_head_scan_fwd`` in include/ssm_scan.h).
+
+    q, k: [b, L, n_qk_heads, d_key]; v: [b, L, n_heads, d_value] -- all float32 or all bfloat16, dense over a token's
+    heads (slices of one projection's rows are used in place).  g: [b, L, n_heads] log decays in that dtype, or
+    g_head: [n_heads] float32, or neither.  h0: [b, n_heads, d_key, d_value] float32 or None; lengths: [b] int32 on
+    the device or None; scale: d_key ** -0.5 by default.
+    Returns (o [b, L, n_heads, d_value], last_state float32 or None).
+    """
+    _head_sizes(q, v, "ssm_head_scan_fwd", 4)
+    device, dt = q.device, q.dtype
+    b, L, hk, dk = q.shape
+    h, dv = v.shape[2:]
+    ops = [_head_operand(t, n, dt, device, s) for t, n, s in ((q, "q", (b, L, hk, dk)), (k, "k", (b, L, hk, dk)),
+                                                              (v, "v", (b, L, h, dv)))]
+    _head_decay(g, g_head, (b, L, h), h, dt, device)
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, device, (b, h, dk, dv))
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, device, (b,))
+    if o is None:
+        o = torch.empty((b, L, h, dv), device=device, dtype=dt)
+    else:
+        _need(o, "o", dt, device, (b, L, h, dv))
+    if last_state is not None:
+        _need(last_state, "last_state", torch.float32, device, (b, h, dk, dv))
+    elif return_last_state:
+        last_state = torch.empty((b, h, dk, dv), device=device, dtype=torch.float32)
+    lib = load_library()
+    sizes = (b, L, h, hk, dk, dv)
+    with torch.cuda.device(device):
+        ws = _workspace(lib, device, sizes, dt, False)
+        rc = lib.ssm_head_scan_fwd(*ops[0], *ops[1], *ops[2], _ptr(g), _ptr(g_head), _ptr(h0), _ptr(lengths),
+                                   dk ** -0.5 if scale is None else float(scale), _ptr(o), _ptr(last_state), _ptr(ws),
+                                   0 if ws is None else ws.numel(), *sizes, SSM_F32 if dt == torch.float32 else SSM_BF16,
+                                   _stream(device))
+    _check(rc)
+    return o, last_state
+
+
+def ssm_head_scan_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, do: torch.Tensor,
+                      g: Optional[torch.Tensor] = None, g_head: Optional[torch.Tensor] = None,
+                      h0: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                      dlast: Optional[torch.Tensor] = None, scale: Optional[float] = None, want_dg: bool = True,
+                      want_dh0: bool = True) -> dict:
+    """Gradients of ssm_head_scan_fwd (see ``ssm_head_scan_bwd`` in include/ssm_scan.h) for do [b, L, n_heads, d_value]
+    (dense, dtype of v) and dlast (float32, or None).  Returns a dict with dq, dk, dv and dg (dtype of q; dg None
+    without g or when not asked for) and dh0 (float32, or None)."""
+    _head_sizes(q, v, "ssm_head_scan_bwd", 4)
+    device, dt = q.device, q.dtype
+    b, L, hk, dk = q.shape
+    h, dv = v.shape[2:]
+    ops = [_head_operand(t, n, dt, device, s) for t, n, s in ((q, "q", (b, L, hk, dk)), (k, "k", (b, L, hk, dk)),
+                                                              (v, "v", (b, L, h, dv)))]
+    _need(do, "do", dt, device, (b, L, h, dv))
+    _head_decay(g, g_head, (b, L, h), h, dt, device)
+    for t, n in ((h0, "h0"), (dlast, "dlast")):
+        if t is not None:
+            _need(t, n, torch.float32, device, (b, h, dk, dv))
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, device, (b,))
+    out = {
+        "dq": torch.empty((b, L, hk, dk), device=device, dtype=dt),
+        "dk": torch.empty((b, L, hk, dk), device=device, dtype=dt),
+        "dv": torch.empty((b, L, h, dv), device=device, dtype=dt),
+        "dg": torch.empty((b, L, h), device=device, dtype=dt) if want_dg and g is not None else None,
+        "dh0": torch.empty((b, h, dk, dv), device=device, dtype=torch.float32) if want_dh0 else None,
+    }
+    lib = load_library()
+    sizes = (b, L, h, hk, dk, dv)
+    with torch.cuda.device(device):
+        ws = _workspace(lib, device, sizes, dt, True)
+        rc = lib.ssm_head_scan_bwd(*ops[0], *ops[1], *ops[2], _ptr(g), _ptr(g_head), _ptr(h0), _ptr(lengths),
+                                   dk ** -0.5 if scale is None else float(scale), _ptr(do), _ptr(dlast), _ptr(out["dq"]),
+                                   _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dh0"]), _ptr(ws),
+                                   ws.numel(), *sizes, SSM_F32 if dt == torch.float32 else SSM_BF16, _stream(device))
+    _check(rc)
+    return out
+
+
+def ssm_head_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torch.Tensor,
+                  g: Optional[torch.Tensor] = None, g_head: Optional[torch.Tensor] = None,
+                  scale: Optional[float] = None, state_out: Optional[torch.Tensor] = None,
+                  o: Optional[torch.Tensor] = None):
+    """One token of the head scan (see ``ssm_head_step`` in include/ssm_scan.h).
+
+    q, k: [b, n_qk_heads, d_key]; v: [b, n_heads, d_value]; g: [b, n_heads] or g_head: [n_heads] float32, or neither;
+    state: [b, n_heads, d_key, d_value] float32.  The new state goes to ``state_out`` (default: ``state`` itself,
+    updated in place).  Returns (o [b, n_heads, d_value], state_out).
+    """
+    _head_sizes(q, v, "ssm_head_step", 3)
+    device, dt = q.device, q.dtype
+    b, hk, dk = q.shape
+    h, dv = v.shape[1:]
+    _need(q, "q", dt, device, (b, hk, dk))
+    _need(k, "k", dt, device, (b, hk, dk))
+    _need(v, "v", dt, device, (b, h, dv))
+    _head_decay(g, g_head, (b, h), h, dt, device)
+    _need(state, "state", torch.float32, device, (b, h, dk, dv))
+    if state_out is None:
+        state_out = state
+    else:
+        _need(state_out, "state_out", torch.float32, device, (b, h, dk, dv))
+    if o is None:
+        o = torch.empty((b, h, dv), device=device, dtype=dt)
+    else:
+        _need(o, "o", dt, device, (b, h, dv))
+    lib = load_library()
+    with torch.cuda.device(device):
+        rc = lib.ssm_head_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(g_head), dk ** -0.5 if scale is None else float(scale),
+                               _ptr(state), _ptr(state_out), _ptr(o), b, h, hk, dk, dv,
+                               SSM_F32 if dt == torch.float32 else SSM_BF16, _stream(device))
+    _check(rc)
+    return o, state_out
 
 
 def affine_scan(a: torch.Tensor, b: torch.Tensor, return_a: bool = True,

@@ -7,6 +7,7 @@ marshalling only; every step runs in the library's kernels.
                                    delta_softplus=True, h0=None, state_chunk=128)
     y, last_state = selective_scan_conv(x, conv_w, conv_b, delta, A, B, C, D, z, ...)
     out = out_proj(y, W)          # the Linear after the gate, [b, L, d_model]
+    o, last_state = head_scan(q, k, v, g=g)   # one decay per head, matrix state
 
 Gradients flow to every tensor argument that requires them (dB and dC are
 computed in float32 and returned in the dtype of B and C).
@@ -17,10 +18,10 @@ from typing import Optional
 
 import torch
 
-from . import (ssm_out_proj, ssm_out_proj_bwd, ssm_scan_bwd, ssm_scan_bwd_conv, ssm_scan_fwd_conv,
-               ssm_scan_fwd_states)
+from . import (ssm_head_scan_bwd, ssm_head_scan_fwd, ssm_out_proj, ssm_out_proj_bwd, ssm_scan_bwd, ssm_scan_bwd_conv,
+               ssm_scan_fwd_conv, ssm_scan_fwd_states)
 
-__all__ = ["selective_scan", "selective_scan_conv", "out_proj"]
+__all__ = ["selective_scan", "selective_scan_conv", "out_proj", "head_scan"]
 
 
 def _grad_or_zero(g, like):
@@ -107,3 +108,31 @@ def out_proj(y: torch.Tensor, W: torch.Tensor) -> torch.Tensor:
     (y [b, d_inner, L] as the scan writes it, W [d_model, d_inner]); returns
     [b, L, d_model]."""
     return _OutProj.apply(y, W)
+
+
+class _HeadScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, g, h0, g_head, lengths, scale):
+        ctx.set_materialize_grads(False)
+        o, last = ssm_head_scan_fwd(q, k, v, g=g, g_head=g_head, h0=h0, lengths=lengths, scale=scale)
+        ctx.save_for_backward(q, k, v, g, h0, g_head, lengths)
+        ctx.scale = scale
+        return o, last
+
+    @staticmethod
+    def backward(ctx, do, dlast):
+        q, k, v, g, h0, g_head, lengths = ctx.saved_tensors
+        r = ssm_head_scan_bwd(q, k, v, v.new_zeros(v.shape) if do is None else do.contiguous(), g=g, g_head=g_head, h0=h0, lengths=lengths,
+                              dlast=None if dlast is None else dlast.contiguous(), scale=ctx.scale,
+                              want_dg=ctx.needs_input_grad[3], want_dh0=ctx.needs_input_grad[4])
+        return r["dq"], r["dk"], r["dv"], r["dg"], r["dh0"], None, None, None
+
+
+def head_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor] = None,
+              g_head: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+              lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None):
+    """Differentiable head scan: returns (o, last_state).  g_head is a constant (a fixed decay per head takes no
+    gradient); a learned one is expanded to g."""
+    if g_head is not None and g_head.requires_grad:
+        raise ValueError("g_head takes no gradient: expand a learned decay to g [b, L, n_heads]")
+    return _HeadScan.apply(q, k, v, g, h0, g_head, lengths, scale)

@@ -2,56 +2,15 @@
 // (all before any HIP call), plan selection, two-pass workspace, launches.
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
 #include <cstdint>
-#include <cstdio>
-#include <string>
 
+#include "capi_common.h"
 #include "ssm_kernels.h"
 #include "ssm_scan.h"
 
+using namespace ssm::capi;
+
 namespace {
-
-thread_local std::string g_err;
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return code;
-}
-
-int hip_fail(hipError_t e, const char* what) {
-  return fail(SSM_EHIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Byte range [p, p + n) of a possibly-null pointer.
-struct Range {
-  uintptr_t lo, hi;
-  bool valid;
-};
-Range range_of(const void* p, uint64_t bytes) {
-  Range r;
-  r.valid = p != nullptr && bytes > 0;
-  r.lo = reinterpret_cast<uintptr_t>(p);
-  r.hi = r.lo + bytes;
-  return r;
-}
-bool overlap(const Range& a, const Range& b) { return a.valid && b.valid && a.lo < b.hi && b.lo < a.hi; }
-
-// x*y with an overflow check against 2^62.
-bool mul_ok(int64_t x, int64_t y, int64_t* out) {
-  const int64_t lim = int64_t(1) << 62;
-  if (x < 0 || y < 0) return false;
-  if (x != 0 && y > lim / x) return false;
-  *out = x * y;
-  return true;
-}
 
 constexpr int64_t kCUs = 256;      // MI355X: 256 CUs of 4 SIMDs
 constexpr int64_t kMaxChunks = 65535;

@@ -1,0 +1,466 @@
+// The head scan: a selective scan whose decay is one number per head and
+// whose state is a matrix [d_key][d_value] (linear attention with a decay),
+//
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,
+//
+// its gradients and its step for single tokens.  With R_t = dLoss/dS_t,
+//
+//   R_t = scale q_t do_t^T + e^{g_{t+1}} R_{t+1}          (R_L += dlast)
+//   dq_t = scale S_t do_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dh0 = e^{g_1} R_1
+//
+// each of which is the chunk kernel of ssm_head_kernel.h with other operands:
+//
+//            x    y    z    state           time
+//   o        q    k    v    S   [dk][dv]    forwards
+//   dq       do   v    k    S^T [dv][dk]    forwards
+//   dk       v    do   q    R^T [dv][dk]    backwards
+//   dv       k    q    do   R   [dk][dv]    backwards
+//
+// The gradient of the decays needs no pass of its own: <R_t, S_t> taken with
+// either recurrence gives dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t, a sum
+// from the end.  The dq and dk passes hand out those dots in float32; the
+// sum starts anew at every segment's end from <R, S> there, so that its
+// rounding does not grow with the length.
+//
+// Long sequences with few heads are cut into segments: every segment's own
+// end state first (kState), then the states are carried over the segments
+// (ssm_head_carry_kernel), then all segments at once from their start states.
+//
+// Page cited: [Mamba-2 page] "Mamba (part 2): parallel scan and
+// hardware-aware optimisation" (scwacadex.pages.dev, blog8_mamba_parallel_scan)
+// §4.3 on chunked recomputation, §7 on the constant-time step.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ssm_device.h"
+#include "ssm_head_kernel.h"
+#include "ssm_kernels.h"
+
+namespace ssm {
+namespace {
+
+using namespace dev;
+using headk::HeadDev;
+
+constexpr int64_t kHeadSlots = 512;       // workgroups that fill the chip: two per CU
+constexpr int64_t kHeadMinSegment = 256;  // tokens
+constexpr int64_t kHeadMaxDgSegment = 1024;  // tokens that the running sum of dg covers
+
+// States carried over the segments, in order: state <- decay * (carried) + own.
+// Segment `first` holds its final state already.
+__global__ void __launch_bounds__(256) ssm_head_carry_kernel(float* state, const float* decay, int64_t nseg, int64_t n,
+                                                            int64_t ssize, int rev) {
+  const int64_t bh = blockIdx.y, e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (e >= ssize) return;
+  const int64_t step = rev ? -1 : 1, first = rev ? nseg - 1 : 0;
+  float* s = state + bh * nseg * ssize + e;
+  const float* d = decay + bh * nseg;
+  float c = s[first * ssize];
+#pragma unroll 4
+  for (int64_t i = 1; i < n; ++i) {
+    const int64_t at = first + i * step;
+    c = __builtin_fmaf(d[at], c, s[at * ssize]);
+    s[at * ssize] = c;
+  }
+}
+
+// dg of one segment: <R, S> at its end, then the sum of q . dq - k . dk from the end.
+template <typename IO>
+__global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, const float* r_seg, const float* s_last,
+                                                         const float* dlast, const float* rq, const float* rk,
+                                                         int64_t ntile, HeadDev p, int64_t seg_len, void* dg) {
+  __shared__ double sh[4];
+  const int64_t bh = blockIdx.y, k = blockIdx.x, b = bh / p.H, h = bh % p.H, ssize = p.rows * p.cols;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int64_t len = p.L;
+  if (p.lengths != nullptr) {
+    const int64_t n = p.lengths[b];
+    len = n < 0 ? 0 : (n < p.L ? n : p.L);
+  }
+  const int64_t t0 = k * seg_len, t1 = t0 + seg_len < p.L ? t0 + seg_len : p.L;
+  const float* S = k + 1 < p.nseg ? s_seg + (bh * p.nseg + k) * ssize : s_last + bh * ssize;
+  const float* R = k + 1 < p.nseg ? r_seg + (bh * p.nseg + k + 1) * ssize : (dlast ? dlast + bh * ssize : nullptr);
+  double x = 0;
+  if (R != nullptr)
+    for (int64_t i = tid; i < ssize; i += 256) x += static_cast<double>(R[i]) * S[i];
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
+  if (lane == 0) sh[wave] = x;
+  __syncthreads();
+  double carry = (sh[0] + sh[1]) + (sh[2] + sh[3]);
+  if (k + 1 < p.nseg && t1 < len) carry *= __builtin_amdgcn_exp2f(headk::decay_at<IO>(p, b, h, t1));
+  const int64_t nbh = p.batch * p.H;
+  for (int64_t e = t1; e > t0; e -= 256) {
+    const int64_t t = e - 1 - tid;  // thread 0 has the last token
+    double v = 0;
+    if (t >= t0)
+      for (int64_t c = 0; c < ntile; ++c)
+        v += static_cast<double>(rq[(c * nbh + bh) * p.L + t]) - rk[(c * nbh + bh) * p.L + t];
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const double o = __shfl_up(v, d);
+      if (lane >= d) v += o;
+    }
+    __syncthreads();
+    if (lane == 63) sh[wave] = v;
+    __syncthreads();
+    double before = carry;
+    for (int w = 0; w < wave; ++w) before += sh[w];
+    carry += (sh[0] + sh[1]) + (sh[2] + sh[3]);
+    if (t >= t0) {
+      const float out = t < len ? static_cast<float>(before + v) : 0.f;
+      IO::template st<1>(static_cast<typename IO::T*>(dg) + (b * p.L + t) * p.H + h, &out);
+    }
+  }
+}
+
+// out[t][hk][e] = sum over the heads that share hk of part[t][h][e]
+template <typename IO>
+__global__ void __launch_bounds__(256) ssm_head_group_sum_kernel(const float* part, void* out, int64_t n, int64_t d,
+                                                                int64_t rep) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += stride) {
+    const float* src = part + (i / d) * rep * d + i % d;
+    float s = 0.f;
+    for (int64_t r = 0; r < rep; ++r) s += src[r * d];
+    IO::template st<1>(static_cast<typename IO::T*>(out) + i, &s);
+  }
+}
+
+// One token.  A workgroup owns one (batch row, head) and 32 columns of the
+// state: thread (rg, c) takes rows rg + 32 i, columns 4 c .. 4 c + 3.  Every
+// load is issued before the first store (the update may be in place); the
+// bound is the state's traffic, 8 bytes per value.
+struct HeadStepDev {
+  const char* q;
+  const char* k;
+  const char* v;
+  const char* g;
+  const float* g_head;
+  const float* in;
+  float* out;
+  char* o;
+  int64_t H, Hk, dk, dv, ntile;
+  float scale;
+};
+
+template <typename IO, bool VEC>
+__global__ void __launch_bounds__(256) ssm_head_step_kernel(HeadStepDev p) {
+  using T = typename IO::T;
+  constexpr int kRows = 8;  // rows per thread: d_key <= 256
+  __shared__ float sh[4][32];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t ct = blockIdx.x % p.ntile, bh = blockIdx.x / p.ntile, b = bh / p.H, h = bh % p.H;
+  const int64_t c = ct * 32 + 4 * (tid & 7);
+  const int rg = tid >> 3;
+  const T* q = reinterpret_cast<const T*>(p.q) + (b * p.Hk + h / (p.H / p.Hk)) * p.dk;
+  const T* k = reinterpret_cast<const T*>(p.k) + (b * p.Hk + h / (p.H / p.Hk)) * p.dk;
+  const T* v = reinterpret_cast<const T*>(p.v) + bh * p.dv;
+  float s[kRows][4], kk[kRows], qq[kRows], vv[4];
+  const int64_t base = bh * p.dk * p.dv + c;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t r = rg + 32 * i;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+    kk[i] = qq[i] = 0.f;
+    if (r < p.dk) {
+      if constexpr (VEC) {
+        if (c < p.dv) {
+          const headk::f32x4 x = __builtin_nontemporal_load(reinterpret_cast<const headk::f32x4*>(p.in + base + r * p.dv));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][e] = x[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < p.dv) s[i][e] = p.in[base + r * p.dv + e];
+      }
+      IO::template ld<1>(k + r, &kk[i]);
+      IO::template ld<1>(q + r, &qq[i]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    vv[e] = 0.f;
+    if (c + e < p.dv) IO::template ld<1>(v + c + e, &vv[e]);
+  }
+  float a = 1.f;
+  if (p.g != nullptr) {
+    IO::template ld<1>(reinterpret_cast<const T*>(p.g) + bh, &a);
+    a = __builtin_amdgcn_exp2f(headk::clamp_decay(a * kLog2e));
+  } else if (p.g_head != nullptr) {
+    a = __builtin_amdgcn_exp2f(headk::clamp_decay(p.g_head[h] * kLog2e));
+  }
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t r = rg + 32 * i;
+    if (r < p.dk) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[i][e] = __builtin_fmaf(a, s[i][e], kk[i] * vv[e]);
+        o[e] = __builtin_fmaf(qq[i], s[i][e], o[e]);
+      }
+      if constexpr (VEC) {
+        if (c < p.dv) {
+          const headk::f32x4 x = {s[i][0], s[i][1], s[i][2], s[i][3]};
+          __builtin_nontemporal_store(x, reinterpret_cast<headk::f32x4*>(p.out + base + r * p.dv));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < p.dv) p.out[base + r * p.dv + e] = s[i][e];
+      }
+    }
+  }
+  // over the wavefront's 8 row groups, then over the wavefronts
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+#pragma unroll
+    for (int d = 8; d < 64; d *= 2) o[e] += __shfl_xor(o[e], d);
+    if (lane < 8) sh[wave][4 * lane + e] = o[e];
+  }
+  __syncthreads();
+  if (tid < 32 && ct * 32 + tid < p.dv) {
+    const float y = p.scale * ((sh[0][tid] + sh[1][tid]) + (sh[2][tid] + sh[3][tid]));
+    IO::template st<1>(reinterpret_cast<T*>(p.o) + bh * p.dv + ct * 32 + tid, &y);
+  }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+// 64-column tiles per workgroup for an operand pair: two where the state then
+// still fits the registers of two workgroups per CU.
+int nc_for(int64_t rows, int64_t cols) { return rows > 32 && rows <= 128 && cols > 64 ? 2 : 1; }
+int64_t tiles_for(int64_t rows, int64_t cols) { return cdiv(cols, 64 * nc_for(rows, cols)); }
+
+struct Plan {
+  int64_t C, nch, cps, nseg;
+};
+Plan plan_of(int64_t batch, int64_t H, int64_t tiles, int64_t L, bool bf16, bool dg) {
+  Plan p;
+  p.C = bf16 ? headk::HeadCfg<BF16>::C : headk::HeadCfg<F32>::C;
+  p.nch = cdiv(L, p.C);
+  int64_t want = kHeadSlots / (batch * H * tiles);
+  const int64_t most = L / kHeadMinSegment;
+  if (want > most) want = most;
+  if (want < 1) want = 1;
+  p.cps = cdiv(p.nch, want);
+  if (dg && p.cps * p.C > kHeadMaxDgSegment) p.cps = kHeadMaxDgSegment / p.C;
+  p.nseg = cdiv(p.nch, p.cps);
+  return p;
+}
+
+struct Operand {
+  const void* p;
+  int64_t b, t;
+  int rep;
+};
+
+hipError_t launch_pass(const HeadDev& p, bool bf16, int mode, hipStream_t st) {
+  const int nc = nc_for(p.rows, p.cols);
+  return bf16 ? launch_head_bf16(p, mode, nc, st) : launch_head_f32(p, mode, nc, st);
+}
+
+bool vec16(const Operand& o, int64_t width, int64_t es) {
+  return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.b * es % 16 == 0 && o.t * es % 16 == 0 && width * es % 16 == 0;
+}
+
+// A pass' operands: x and y of width `rows`, z and the output of width `cols`.
+HeadDev pass_of(const HeadArgs& a, const Plan& pl, const Operand& x, const Operand& y, const Operand& z, void* o,
+                int64_t rows, int64_t cols, bool bf16) {
+  const int64_t es = bf16 ? 2 : 4;
+  HeadDev d{};
+  d.x = static_cast<const char*>(x.p); d.y = static_cast<const char*>(y.p); d.z = static_cast<const char*>(z.p);
+  d.o = static_cast<char*>(o);
+  d.x_b = x.b; d.x_t = x.t; d.y_b = y.b; d.y_t = y.t; d.z_b = z.b; d.z_t = z.t;
+  d.x_rep = x.rep; d.y_rep = y.rep; d.z_rep = z.rep;
+  d.g = static_cast<const char*>(a.g); d.g_head = a.g_head; d.lengths = a.lengths;
+  d.batch = a.batch; d.H = a.H; d.L = a.L; d.rows = rows; d.cols = cols;
+  d.nch = pl.nch; d.cps = pl.cps; d.nseg = pl.nseg; d.ntile = tiles_for(rows, cols);
+  d.ps = d.ss = d.us = 1.f;
+  d.vec_x = vec16(x, rows, es); d.vec_y = vec16(y, rows, es); d.vec_z = vec16(z, cols, es);
+  d.vec_o = cols % 4 == 0;
+  return d;
+}
+
+hipError_t launch_carry(const HeadDev& d, hipStream_t st) {
+  if (d.nseg <= 2) return hipSuccess;
+  const int64_t ssize = d.rows * d.cols;
+  hipLaunchKernelGGL(ssm_head_carry_kernel, dim3(static_cast<unsigned>(cdiv(ssize, 256)),
+                                                 static_cast<unsigned>(d.batch * d.H)), dim3(256), 0, st, d.seg_state,
+                     d.seg_decay, d.nseg, d.nseg - 1, ssize, d.rev);
+  return hipGetLastError();
+}
+
+// Where the workspace's parts are, in bytes from its start.
+struct FwdSpace {
+  int64_t state, decay, total;
+};
+FwdSpace fwd_space(const HeadArgs& a, const Plan& pl) {
+  FwdSpace w{};
+  if (pl.nseg > 1) {
+    w.decay = up16(4 * a.batch * a.H * pl.nseg * a.dk * a.dv);
+    w.total = w.decay + up16(4 * a.batch * a.H * pl.nseg);
+  }
+  return w;
+}
+struct BwdSpace {
+  int64_t s, r, sdec, rdec, slast, rq, rk, pq, pk, total;
+};
+BwdSpace bwd_space(const HeadArgs& a, const Plan& pl) {
+  BwdSpace w{};
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t r = at;
+    at += up16(bytes);
+    return r;
+  };
+  const int64_t bh = a.batch * a.H, ss = a.dk * a.dv, nt = tiles_for(a.dv, a.dk);
+  if (pl.nseg > 1) {
+    w.s = take(4 * bh * pl.nseg * ss);
+    w.r = take(4 * bh * pl.nseg * ss);
+    w.sdec = take(4 * bh * pl.nseg);
+    w.rdec = take(4 * bh * pl.nseg);
+  }
+  w.slast = take(4 * bh * ss);
+  w.rq = take(4 * nt * bh * a.L);
+  w.rk = take(4 * nt * bh * a.L);
+  if (a.Hk != a.H) {
+    w.pq = take(4 * bh * a.L * a.dk);
+    w.pk = take(4 * bh * a.L * a.dk);
+  }
+  w.total = at;
+  return w;
+}
+Plan fwd_plan(const HeadArgs& a, bool bf16) { return plan_of(a.batch, a.H, tiles_for(a.dk, a.dv), a.L, bf16, false); }
+Plan bwd_plan(const HeadArgs& a, bool bf16) {
+  const int64_t t1 = tiles_for(a.dk, a.dv), t2 = tiles_for(a.dv, a.dk);
+  return plan_of(a.batch, a.H, t1 < t2 ? t1 : t2, a.L, bf16, true);
+}
+
+template <typename IO>
+hipError_t launch_group_sum(const float* part, void* out, const HeadArgs& a, hipStream_t st) {
+  const int64_t n = a.batch * a.L * a.Hk * a.dk, blocks = cdiv(n, 256);
+  hipLaunchKernelGGL(ssm_head_group_sum_kernel<IO>, dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)), dim3(256),
+                     0, st, part, out, n, a.dk, a.H / a.Hk);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t head_workspace_bytes(const HeadArgs& a, bool bf16, bool backward) {
+  return backward ? bwd_space(a, bwd_plan(a, bf16)).total : fwd_space(a, fwd_plan(a, bf16)).total;
+}
+
+int64_t head_workgroups(const HeadArgs& a, bool bf16) {
+  const int64_t t1 = tiles_for(a.dk, a.dv), t2 = tiles_for(a.dv, a.dk);
+  return a.batch * a.H * (t1 > t2 ? t1 : t2) * bwd_plan(a, bf16).nseg;
+}
+
+hipError_t launch_head_fwd(const HeadArgs& a, bool bf16, char* work, hipStream_t st) {
+  const Plan pl = fwd_plan(a, bf16);
+  const FwdSpace w = fwd_space(a, pl);
+  const int rep = static_cast<int>(a.H / a.Hk);
+  HeadDev d = pass_of(a, pl, {a.q, a.q_b, a.q_t, rep}, {a.k, a.k_b, a.k_t, rep}, {a.v, a.v_b, a.v_t, 1}, a.o, a.dk, a.dv,
+                      bf16);
+  d.ps = d.ss = a.scale;
+  d.s_r = a.dv; d.s_c = 1;
+  d.h0 = a.h0;
+  d.last = a.last; d.last_bh = a.dk * a.dv;
+  d.seg_state = reinterpret_cast<float*>(work + w.state);
+  d.seg_decay = reinterpret_cast<float*>(work + w.decay);
+  if (pl.nseg > 1) {
+    hipError_t e = launch_pass(d, bf16, headk::kState, st);
+    if (e == hipSuccess) e = launch_carry(d, st);
+    if (e != hipSuccess) return e;
+  }
+  return launch_pass(d, bf16, headk::kOut, st);
+}
+
+hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t st) {
+  const Plan pl = bwd_plan(a, bf16);
+  const BwdSpace w = bwd_space(a, pl);
+  const int rep = static_cast<int>(a.H / a.Hk);
+  const bool shared = rep > 1, dg = a.dg != nullptr;
+  const Operand q{a.q, a.q_b, a.q_t, rep}, k{a.k, a.k_b, a.k_t, rep}, v{a.v, a.v_b, a.v_t, 1};
+  const Operand go{a.dout, a.L * a.H * a.dv, a.H * a.dv, 1};
+  float* s_seg = reinterpret_cast<float*>(work + w.s);
+  float* r_seg = reinterpret_cast<float*>(work + w.r);
+  float* s_last = reinterpret_cast<float*>(work + w.slast);
+  float* rq = reinterpret_cast<float*>(work + w.rq);
+  float* rk = reinterpret_cast<float*>(work + w.rk);
+  void* pq = shared ? static_cast<void*>(work + w.pq) : a.dq;
+  void* pk = shared ? static_cast<void*>(work + w.pk) : a.dk_out;
+
+  HeadDev dq = pass_of(a, pl, go, v, k, pq, a.dv, a.dk, bf16);
+  dq.ps = dq.ss = a.scale;
+  dq.s_r = 1; dq.s_c = a.dv;
+  dq.h0 = a.h0;
+  dq.seg_state = s_seg; dq.seg_decay = reinterpret_cast<float*>(work + w.sdec);
+  dq.last = dg ? s_last : nullptr; dq.last_bh = a.dk * a.dv;
+  dq.out_f32 = shared;
+
+  HeadDev dv = pass_of(a, pl, k, q, go, a.dv_out, a.dk, a.dv, bf16);
+  dv.ps = dv.us = a.scale;
+  dv.s_r = a.dv; dv.s_c = 1;
+  dv.rev = 1;
+  dv.h0 = a.dlast;
+  dv.seg_state = r_seg; dv.seg_decay = reinterpret_cast<float*>(work + w.rdec);
+  dv.last = a.dh0; dv.last_bh = a.dk * a.dv; dv.end_decay = 1;
+
+  HeadDev dk = pass_of(a, pl, v, go, q, pk, a.dv, a.dk, bf16);
+  dk.ps = dk.us = a.scale;
+  dk.s_r = 1; dk.s_c = a.dv;
+  dk.rev = 1;
+  dk.h0 = a.dlast;
+  dk.seg_state = r_seg; dk.seg_decay = dv.seg_decay;
+  dk.out_f32 = shared;
+
+  if (dg) {
+    dq.dotv = static_cast<const char*>(a.q); dq.dot_b = a.q_b; dq.dot_t = a.q_t; dq.dot_rep = rep; dq.dot_out = rq;
+    dk.dotv = static_cast<const char*>(a.k); dk.dot_b = a.k_b; dk.dot_t = a.k_t; dk.dot_rep = rep; dk.dot_out = rk;
+  }
+  hipError_t e = hipSuccess;
+  if (pl.nseg > 1) {
+    e = launch_pass(dq, bf16, headk::kState, st);
+    if (e == hipSuccess) e = launch_carry(dq, st);
+    if (e == hipSuccess) e = launch_pass(dv, bf16, headk::kState, st);
+    if (e == hipSuccess) e = launch_carry(dv, st);
+  }
+  if (e == hipSuccess) e = launch_pass(dq, bf16, headk::kOut, st);
+  if (e == hipSuccess) e = launch_pass(dk, bf16, headk::kOut, st);
+  if (e == hipSuccess) e = launch_pass(dv, bf16, headk::kOut, st);
+  if (e != hipSuccess) return e;
+  if (dg) {
+    auto kern = bf16 ? ssm_head_dg_kernel<BF16> : ssm_head_dg_kernel<F32>;
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(pl.nseg), static_cast<unsigned>(a.batch * a.H)), dim3(256), 0, st,
+                       s_seg, r_seg, s_last, a.dlast, rq, rk, dq.ntile, dq, pl.cps * pl.C, a.dg);
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess && shared) {
+    e = bf16 ? launch_group_sum<BF16>(static_cast<const float*>(pq), a.dq, a, st)
+             : launch_group_sum<F32>(static_cast<const float*>(pq), a.dq, a, st);
+    if (e == hipSuccess)
+      e = bf16 ? launch_group_sum<BF16>(static_cast<const float*>(pk), a.dk_out, a, st)
+               : launch_group_sum<F32>(static_cast<const float*>(pk), a.dk_out, a, st);
+  }
+  return e;
+}
+
+hipError_t launch_head_step(const HeadStepArgs& a, bool bf16, hipStream_t st) {
+  HeadStepDev d{};
+  d.q = static_cast<const char*>(a.q); d.k = static_cast<const char*>(a.k); d.v = static_cast<const char*>(a.v);
+  d.g = static_cast<const char*>(a.g); d.g_head = a.g_head;
+  d.in = a.state_in; d.out = a.state_out; d.o = static_cast<char*>(a.o);
+  d.H = a.H; d.Hk = a.Hk; d.dk = a.dk; d.dv = a.dv; d.ntile = cdiv(a.dv, 32); d.scale = a.scale;
+  const bool vec = a.dv % 4 == 0;
+  auto kern = bf16 ? (vec ? ssm_head_step_kernel<BF16, true> : ssm_head_step_kernel<BF16, false>)
+                   : (vec ? ssm_head_step_kernel<F32, true> : ssm_head_step_kernel<F32, false>);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(a.batch * a.H * d.ntile)), dim3(256), 0, st, d);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

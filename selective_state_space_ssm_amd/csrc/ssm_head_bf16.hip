@@ -1,0 +1,10 @@
+// The head scan's chunk kernels for bfloat16 storage (one source file per type: they compile side by side).
+#include "ssm_head_kernel.h"
+
+namespace ssm {
+
+hipError_t launch_head_bf16(const headk::HeadDev& p, int mode, int nc, hipStream_t st) {
+  return headk::launch_head_io<dev::BF16>(p, mode, nc, st);
+}
+
+}  // namespace ssm

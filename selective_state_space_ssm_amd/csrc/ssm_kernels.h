@@ -184,4 +184,51 @@ size_t proj_bwd_workspace_bytes(bool bf16, const ProjBwdArgs& a);
 int64_t proj_bwd_tiles(bool bf16, const ProjBwdArgs& a);
 hipError_t launch_out_proj_bwd(const ProjBwdArgs& a, bool bf16, float* work, size_t work_bytes, hipStream_t st);
 
+// Head scan (ssm_head.hip): S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale
+// S_t^T q_t, state [dk][dv] per head.  q, k: [batch][L][Hk][dk], v:
+// [batch][L][H][dv] with batch and token strides in elements; everything else
+// dense.  The backward fields are read by launch_head_bwd only.
+struct HeadArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_b, q_t, k_b, k_t, v_b, v_t;
+  const void* g;           // [batch][L][H], nullable
+  const float* g_head;     // [H], nullable
+  const int32_t* lengths;  // [batch], nullable
+  const float* h0;         // [batch][H][dk][dv], nullable
+  void* o;                 // [batch][L][H][dv]
+  float* last;             // [batch][H][dk][dv], nullable
+  const void* dout;        // [batch][L][H][dv]
+  const float* dlast;      // [batch][H][dk][dv], nullable
+  void* dq;                // [batch][L][Hk][dk]
+  void* dk_out;            // [batch][L][Hk][dk]
+  void* dv_out;            // [batch][L][H][dv]
+  void* dg;                // [batch][L][H], nullable
+  float* dh0;              // [batch][H][dk][dv], nullable
+  int64_t batch, L, H, Hk, dk, dv;
+  float scale;
+};
+constexpr int64_t kHeadMaxDim = 256;
+int64_t head_workspace_bytes(const HeadArgs& a, bool bf16, bool backward);
+// workgroups of the largest launch
+int64_t head_workgroups(const HeadArgs& a, bool bf16);
+hipError_t launch_head_fwd(const HeadArgs& a, bool bf16, char* work, hipStream_t st);
+hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t st);
+
+// One token of the head scan; state_out may equal state_in.
+struct HeadStepArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* g;
+  const float* g_head;
+  const float* state_in;
+  float* state_out;
+  void* o;
+  int64_t batch, H, Hk, dk, dv;
+  float scale;
+};
+hipError_t launch_head_step(const HeadStepArgs& a, bool bf16, hipStream_t st);
+
 }  // namespace ssm
