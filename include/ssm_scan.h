@@ -473,6 +473,81 @@ int ssm_head_step(const void *q, const void *k, const void *v, const void *g, co
                   int64_t d_key, int64_t d_value, int dtype, void *stream);
 
 /*
+ * ssm_gate_norm -- grouped norm of token rows (channels last) with a SiLU gate,
+ * what follows the head scan in its block.  Every row of `channels` values is
+ * cut into `groups` groups; with n^ = (u - mu) / sqrt(mean((u - mu)^2) + eps)
+ * over a group (mu its mean with center = 1, else 0),
+ *     gate_first 0:  u = x,           y = weight * n^ * silu(z)
+ *     gate_first 1:  u = x silu(z),   y = weight * n^
+ *   x, z : [rows, channels], dtype `dtype`; z nullable (no gate).
+ *   weight : [channels] float32, nullable (ones).
+ *   y    : [rows, channels], dtype `dtype`, output.
+ *   channels a multiple of groups, at most 8192 channels per group; eps >= 0.
+ * Arithmetic is float32, the result rounded once.
+ * Errors: SSM_EINVAL, SSM_EUNSUPPORTED, SSM_EHIP.
+ */
+int ssm_gate_norm(const void *x, const void *z, const float *weight, void *y, int64_t rows, int64_t channels,
+                  int64_t groups, float eps, int center, int gate_first, int dtype, void *stream);
+
+/*
+ * ssm_gate_norm_bwd -- gradients of ssm_gate_norm for dy; the statistics are
+ * taken again from x and z.
+ *   dx, dz : [rows, channels], dtype `dtype`; dz given if and only if z is.
+ *   dweight : [channels] float32, nullable (not computed): a sum over the rows
+ *           in a fixed order.  The gradient at ones when weight is NULL.
+ *   workspace : ssm_gate_norm_workspace bytes (not needed without dweight).
+ * Other arguments and errors as ssm_gate_norm.
+ */
+int ssm_gate_norm_bwd(const void *x, const void *z, const float *weight, const void *dy, void *dx, void *dz,
+                      float *dweight, void *workspace, int64_t workspace_bytes, int64_t rows, int64_t channels,
+                      int64_t groups, float eps, int center, int gate_first, int dtype, void *stream);
+
+/* Bytes of workspace ssm_gate_norm_bwd needs for a size (host only). */
+int ssm_gate_norm_workspace(int64_t rows, int64_t channels, int64_t groups, int dtype, int64_t *bytes);
+
+/* Activations of ssm_linear. */
+#define SSM_ACT_NONE 0
+#define SSM_ACT_SILU 1
+#define SSM_ACT_GELU 2  /* p (1 + erf(p / sqrt 2)) / 2 */
+
+/*
+ * ssm_linear -- linear layer on token rows with its epilogue, on the matrix
+ * cores (ssm_out_proj is the same product read from the scan's channel-major y):
+ *     pre = x W^T + bias,    out = act(pre) + residual
+ *   x    : [rows, d_in], W: [d_out, d_in], bias: [d_out] (nullable), residual:
+ *          [rows, d_out] (nullable), all of dtype `dtype`.
+ *   act  : SSM_ACT_*.
+ *   out  : [rows, d_out], dtype `dtype`, output.
+ *   pre  : as out, output, nullable: the value before act, for ssm_linear_bwd.
+ *   workspace : ssm_linear_workspace(..., backward = 0) bytes (may be 0).
+ *   d_in, d_out < 2^21.  Any size is accepted; the fastest path needs d_in and
+ *   d_out multiples of 8 (bfloat16) or 4 (float32).
+ * Sums are float32; the epilogue works on the unrounded sum.
+ * Errors: SSM_EINVAL, SSM_EUNSUPPORTED, SSM_EHIP.
+ */
+int ssm_linear(const void *x, const void *W, const void *bias, const void *residual, int act, void *out, void *pre,
+               void *workspace, int64_t workspace_bytes, int64_t rows, int64_t d_in, int64_t d_out, int dtype,
+               void *stream);
+
+/*
+ * ssm_linear_bwd -- gradients of ssm_linear for dout (that of residual is dout
+ * itself): dpre = dout act'(pre), dx = dpre W, dW = dpre^T x, dbias = sum of
+ * dpre over the rows.
+ *   pre  : as ssm_linear wrote it; may be NULL with SSM_ACT_NONE.
+ *   dx   : [rows, d_in], dW: [d_out, d_in], dbias: [d_out], dtype `dtype`,
+ *          each nullable (not computed), at least one given.
+ *   workspace : ssm_linear_workspace(..., backward = 1) bytes.
+ * With SSM_BF16 dpre is rounded to bfloat16 for the two products (dbias sums it
+ * unrounded).  Sums are taken in a fixed order.
+ */
+int ssm_linear_bwd(const void *x, const void *W, const void *pre, int act, const void *dout, void *dx, void *dW,
+                   void *dbias, void *workspace, int64_t workspace_bytes, int64_t rows, int64_t d_in, int64_t d_out,
+                   int dtype, void *stream);
+
+/* Bytes of workspace ssm_linear (backward = 0) or ssm_linear_bwd (1) needs for a size (host only). */
+int ssm_linear_workspace(int64_t rows, int64_t d_in, int64_t d_out, int act, int dtype, int backward, int64_t *bytes);
+
+/*
  * affine_scan -- inclusive scan of affine pairs along each row
  * ([Scan page] §1.2 and §2.1; [Mamba-2 page] §2.2).
  * A pair (a, b) is the map h -> a*h + b; composition, later step first, is

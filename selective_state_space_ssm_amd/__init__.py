@@ -18,7 +18,7 @@ import torch
 
 __all__ = ["SSMError", "ssm_scan_fwd", "ssm_scan_fwd_states", "ssm_scan_fwd_conv", "ssm_scan_bwd",
            "ssm_scan_bwd_conv", "ssm_step", "ssm_step_conv", "ssm_out_proj", "ssm_out_proj_bwd", "ssm_head_scan_fwd",
-           "ssm_head_scan_bwd", "ssm_head_step", "affine_scan", "affine_scan_order", "plan_for", "library_path", "load_library", "PLANS"]
+           "ssm_head_scan_bwd", "ssm_head_step", "ssm_gate_norm", "ssm_gate_norm_bwd", "ssm_linear", "ssm_linear_bwd", "affine_scan", "affine_scan_order", "plan_for", "library_path", "load_library", "PLANS", "ACTS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libssmscan.so")
@@ -27,6 +27,7 @@ _lib = None
 SSM_OK, SSM_EINVAL, SSM_EUNSUPPORTED, SSM_EHIP, SSM_ENOMEM = 0, 1, 2, 3, 4
 SSM_F32, SSM_BF16 = 0, 1
 PLANS = {"auto": 0, "carry": 1, "twopass": 2, "mixed": 3, "lpar": 4}
+ACTS = {"none": 0, "silu": 1, "gelu": 2}
 _PLAN_NAMES = {v: k for k, v in PLANS.items()}
 _STATUS = {SSM_EINVAL: "invalid argument", SSM_EUNSUPPORTED: "unsupported", SSM_EHIP: "HIP error",
            SSM_ENOMEM: "out of memory"}
@@ -92,6 +93,18 @@ def load_library():
     lib.ssm_head_scan_workspace.restype = I
     lib.ssm_head_step.argtypes = [P, P, P, P, P, F, P, P, P] + [I64] * 5 + [I, P]
     lib.ssm_head_step.restype = I
+    lib.ssm_gate_norm.argtypes = [P, P, P, P, I64, I64, I64, F, I, I, I, P]
+    lib.ssm_gate_norm.restype = I
+    lib.ssm_gate_norm_bwd.argtypes = [P] * 8 + [I64, I64, I64, I64, F, I, I, I, P]
+    lib.ssm_gate_norm_bwd.restype = I
+    lib.ssm_gate_norm_workspace.argtypes = [I64, I64, I64, I, ctypes.POINTER(I64)]
+    lib.ssm_gate_norm_workspace.restype = I
+    lib.ssm_linear.argtypes = [P, P, P, P, I, P, P, P, I64, I64, I64, I64, I, P]
+    lib.ssm_linear.restype = I
+    lib.ssm_linear_bwd.argtypes = [P, P, P, I, P, P, P, P, P, I64, I64, I64, I64, I, P]
+    lib.ssm_linear_bwd.restype = I
+    lib.ssm_linear_workspace.argtypes = [I64, I64, I64, I, I, I, ctypes.POINTER(I64)]
+    lib.ssm_linear_workspace.restype = I
     lib.affine_scan.argtypes = [P, P, P, P, I64, I64, P]
     lib.affine_scan.restype = I
     lib.affine_scan_order.argtypes = [ctypes.POINTER(I)] * 4
@@ -667,11 +680,15 @@ def _head_decay(g, g_head, shape, heads, dtype, device):
         _need(g_head, "g_head", torch.float32, device, (heads,))
 
 
-def _workspace(lib, device, sizes, dt, backward: bool) -> Optional[torch.Tensor]:
+def _workspace(query, device, *sizes) -> Optional[torch.Tensor]:
+    """Device memory of the size that a ``*_workspace`` query names (torch's allocator keeps it in stream order)."""
     n = ctypes.c_int64()
-    _check(lib.ssm_head_scan_workspace(*sizes, SSM_F32 if dt == torch.float32 else SSM_BF16, int(backward),
-                                       ctypes.byref(n)))
+    _check(query(*sizes, ctypes.byref(n)))
     return torch.empty(n.value, device=device, dtype=torch.uint8) if n.value else None
+
+
+def _bytes(ws: Optional[torch.Tensor]) -> int:
+    return 0 if ws is None else ws.numel()
 
 
 def ssm_head_scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor] = None,
@@ -708,13 +725,12 @@ def ssm_head_scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Opti
     elif return_last_state:
         last_state = torch.empty((b, h, dk, dv), device=device, dtype=torch.float32)
     lib = load_library()
-    sizes = (b, L, h, hk, dk, dv)
+    sizes, code = (b, L, h, hk, dk, dv), SSM_F32 if dt == torch.float32 else SSM_BF16
     with torch.cuda.device(device):
-        ws = _workspace(lib, device, sizes, dt, False)
+        ws = _workspace(lib.ssm_head_scan_workspace, device, *sizes, code, 0)
         rc = lib.ssm_head_scan_fwd(*ops[0], *ops[1], *ops[2], _ptr(g), _ptr(g_head), _ptr(h0), _ptr(lengths),
                                    dk ** -0.5 if scale is None else float(scale), _ptr(o), _ptr(last_state), _ptr(ws),
-                                   0 if ws is None else ws.numel(), *sizes, SSM_F32 if dt == torch.float32 else SSM_BF16,
-                                   _stream(device))
+                                   _bytes(ws), *sizes, code, _stream(device))
     _check(rc)
     return o, last_state
 
@@ -748,13 +764,13 @@ def ssm_head_scan_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, do: tor
         "dh0": torch.empty((b, h, dk, dv), device=device, dtype=torch.float32) if want_dh0 else None,
     }
     lib = load_library()
-    sizes = (b, L, h, hk, dk, dv)
+    sizes, code = (b, L, h, hk, dk, dv), SSM_F32 if dt == torch.float32 else SSM_BF16
     with torch.cuda.device(device):
-        ws = _workspace(lib, device, sizes, dt, True)
+        ws = _workspace(lib.ssm_head_scan_workspace, device, *sizes, code, 1)
         rc = lib.ssm_head_scan_bwd(*ops[0], *ops[1], *ops[2], _ptr(g), _ptr(g_head), _ptr(h0), _ptr(lengths),
                                    dk ** -0.5 if scale is None else float(scale), _ptr(do), _ptr(dlast), _ptr(out["dq"]),
                                    _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dh0"]), _ptr(ws),
-                                   ws.numel(), *sizes, SSM_F32 if dt == torch.float32 else SSM_BF16, _stream(device))
+                                   _bytes(ws), *sizes, code, _stream(device))
     _check(rc)
     return out
 
@@ -793,6 +809,135 @@ def ssm_head_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torc
                                SSM_F32 if dt == torch.float32 else SSM_BF16, _stream(device))
     _check(rc)
     return o, state_out
+
+
+def _rows(t: torch.Tensor, name: str):
+    """Device, dtype, rows and channels of a token-major tensor [..., channels]."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA/HIP tensor")
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    if t.dim() < 1 or t.numel() == 0:
+        raise ValueError(f"{name} must be [..., channels] and not empty")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.device, t.dtype, t.numel() // t.shape[-1], t.shape[-1]
+
+
+def ssm_gate_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                  groups: int = 1, eps: float = 1e-5, center: bool = False, gate_first: bool = False,
+                  y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Grouped norm of token rows with a SiLU gate (see ``ssm_gate_norm`` in include/ssm_scan.h): every row of
+    x [..., channels] in ``groups`` groups, RMS or (``center``) mean and variance; y = weight * norm(x) * silu(z), or
+    with ``gate_first`` weight * norm(x * silu(z)).
+
+    x, z: float32 or bfloat16; weight: [channels] float32 (None: ones); z None: no gate.  Returns y like x."""
+    device, dt, rows, c = _rows(x, "x")
+    if z is not None:
+        _need(z, "z", dt, device, x.shape)
+    if weight is not None:
+        _need(weight, "weight", torch.float32, device, (c,))
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need(y, "y", dt, device, x.shape)
+    lib = load_library()
+    with torch.cuda.device(device):
+        rc = lib.ssm_gate_norm(_ptr(x), _ptr(z), _ptr(weight), _ptr(y), rows, c, int(groups), float(eps),
+                               int(bool(center)), int(bool(gate_first)), SSM_F32 if dt == torch.float32 else SSM_BF16,
+                               _stream(device))
+    _check(rc)
+    return y
+
+
+def ssm_gate_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                      z: Optional[torch.Tensor] = None, groups: int = 1, eps: float = 1e-5, center: bool = False,
+                      gate_first: bool = False, want_dweight: bool = True):
+    """Gradients of ssm_gate_norm (see ``ssm_gate_norm_bwd`` in include/ssm_scan.h) for dy like x.  Returns
+    (dx, dweight [channels] float32 or None, dz or None)."""
+    device, dt, rows, c = _rows(x, "x")
+    _need(dy, "dy", dt, device, x.shape)
+    if z is not None:
+        _need(z, "z", dt, device, x.shape)
+    if weight is not None:
+        _need(weight, "weight", torch.float32, device, (c,))
+    dx = torch.empty_like(x)
+    dz = torch.empty_like(x) if z is not None else None
+    dw = torch.empty((c,), device=device, dtype=torch.float32) if want_dweight else None
+    lib = load_library()
+    code = SSM_F32 if dt == torch.float32 else SSM_BF16
+    with torch.cuda.device(device):
+        ws = _workspace(lib.ssm_gate_norm_workspace, device, rows, c, int(groups), code) if want_dweight else None
+        rc = lib.ssm_gate_norm_bwd(_ptr(x), _ptr(z), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dz), _ptr(dw), _ptr(ws),
+                                   _bytes(ws), rows, c, int(groups), float(eps), int(bool(center)),
+                                   int(bool(gate_first)), code, _stream(device))
+    _check(rc)
+    return dx, dw, dz
+
+
+def ssm_linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, act: str = "none", return_pre: bool = False,
+               out: Optional[torch.Tensor] = None):
+    """Linear layer on token rows with its epilogue (see ``ssm_linear`` in include/ssm_scan.h):
+    out = act(x W^T + bias) + residual.
+
+    x: [..., d_in], W: [d_out, d_in], bias: [d_out], residual: [..., d_out], all float32 or all bfloat16; act: "none",
+    "silu" or "gelu".  Returns out [..., d_out], with ``return_pre`` (out, pre), pre the value before act."""
+    device, dt, rows, k = _rows(x, "x")
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("W must be [d_out, d_in]")
+    m = W.shape[0]
+    shape = (*x.shape[:-1], m)
+    _need(W, "W", dt, device, (m, k))
+    if bias is not None:
+        _need(bias, "bias", dt, device, (m,))
+    if residual is not None:
+        _need(residual, "residual", dt, device, shape)
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {list(ACTS)}")
+    if out is None:
+        out = torch.empty(shape, device=device, dtype=dt)
+    else:
+        _need(out, "out", dt, device, shape)
+    pre = torch.empty(shape, device=device, dtype=dt) if return_pre else None
+    lib = load_library()
+    code = SSM_F32 if dt == torch.float32 else SSM_BF16
+    with torch.cuda.device(device):
+        ws = _workspace(lib.ssm_linear_workspace, device, rows, k, m, ACTS[act], code, 0)
+        rc = lib.ssm_linear(_ptr(x), _ptr(W), _ptr(bias), _ptr(residual), ACTS[act], _ptr(out), _ptr(pre), _ptr(ws),
+                            _bytes(ws), rows, k, m, code, _stream(device))
+    _check(rc)
+    return (out, pre) if return_pre else out
+
+
+def ssm_linear_bwd(x: torch.Tensor, W: torch.Tensor, dout: torch.Tensor, pre: Optional[torch.Tensor] = None,
+                   act: str = "none", want_dx: bool = True, want_dW: bool = True, want_dbias: bool = True):
+    """Gradients of ssm_linear (see ``ssm_linear_bwd`` in include/ssm_scan.h) for dout [..., d_out]; pre as ssm_linear
+    returned it (None with act "none").  Returns (dx, dW, dbias), None where not asked for."""
+    device, dt, rows, k = _rows(x, "x")
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("W must be [d_out, d_in]")
+    m = W.shape[0]
+    shape = (*x.shape[:-1], m)
+    _need(W, "W", dt, device, (m, k))
+    _need(dout, "dout", dt, device, shape)
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {list(ACTS)}")
+    if pre is not None:
+        _need(pre, "pre", dt, device, shape)
+    dx = torch.empty_like(x) if want_dx else None
+    dW = torch.empty_like(W) if want_dW else None
+    db = torch.empty((m,), device=device, dtype=dt) if want_dbias else None
+    lib = load_library()
+    code = SSM_F32 if dt == torch.float32 else SSM_BF16
+    with torch.cuda.device(device):
+        ws = _workspace(lib.ssm_linear_workspace, device, rows, k, m, ACTS[act], code, 1)
+        rc = lib.ssm_linear_bwd(_ptr(x), _ptr(W), _ptr(pre), ACTS[act], _ptr(dout), _ptr(dx), _ptr(dW), _ptr(db), _ptr(ws),
+                                _bytes(ws), rows, k, m, code, _stream(device))
+    _check(rc)
+    return dx, dW, db
 
 
 def affine_scan(a: torch.Tensor, b: torch.Tensor, return_a: bool = True,

@@ -8,6 +8,8 @@ marshalling only; every step runs in the library's kernels.
     y, last_state = selective_scan_conv(x, conv_w, conv_b, delta, A, B, C, D, z, ...)
     out = out_proj(y, W)          # the Linear after the gate, [b, L, d_model]
     o, last_state = head_scan(q, k, v, g=g)   # one decay per head, matrix state
+    y = gate_norm(x, weight, z, groups=heads)   # grouped norm of token rows with a SiLU gate
+    out = linear(y, W, bias, residual, act="silu")   # act(y W^T + bias) + residual
 
 Gradients flow to every tensor argument that requires them (dB and dC are
 computed in float32 and returned in the dtype of B and C).
@@ -18,10 +20,11 @@ from typing import Optional
 
 import torch
 
-from . import (ssm_head_scan_bwd, ssm_head_scan_fwd, ssm_out_proj, ssm_out_proj_bwd, ssm_scan_bwd, ssm_scan_bwd_conv,
+from . import (ssm_gate_norm, ssm_gate_norm_bwd, ssm_head_scan_bwd, ssm_head_scan_fwd, ssm_linear, ssm_linear_bwd,
+               ssm_out_proj, ssm_out_proj_bwd, ssm_scan_bwd, ssm_scan_bwd_conv,
                ssm_scan_fwd_conv, ssm_scan_fwd_states)
 
-__all__ = ["selective_scan", "selective_scan_conv", "out_proj", "head_scan"]
+__all__ = ["selective_scan", "selective_scan_conv", "out_proj", "head_scan", "gate_norm", "linear"]
 
 
 def _grad_or_zero(g, like):
@@ -136,3 +139,51 @@ def head_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[tor
     if g_head is not None and g_head.requires_grad:
         raise ValueError("g_head takes no gradient: expand a learned decay to g [b, L, n_heads]")
     return _HeadScan.apply(q, k, v, g, h0, g_head, lengths, scale)
+
+
+class _GateNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, z, groups, eps, center, gate_first):
+        ctx.save_for_backward(x, weight, z)
+        ctx.opts = dict(groups=groups, eps=eps, center=center, gate_first=gate_first)
+        return ssm_gate_norm(x, weight, z, **ctx.opts)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, z = ctx.saved_tensors
+        dx, dw, dz = ssm_gate_norm_bwd(x, dy.contiguous(), weight, z, want_dweight=ctx.needs_input_grad[1], **ctx.opts)
+        return dx, dw, dz, None, None, None, None
+
+
+def gate_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None, groups: int = 1,
+              eps: float = 1e-5, center: bool = False, gate_first: bool = False) -> torch.Tensor:
+    """Differentiable grouped norm of token rows [..., channels] with a SiLU gate."""
+    return _GateNorm.apply(x, weight, z, groups, eps, center, gate_first)
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, bias, residual, act):
+        # the value before act is kept only where its slope is asked for
+        keep = act != "none" and any(ctx.needs_input_grad[:3])
+        r = ssm_linear(x, W, bias, residual, act, return_pre=keep)
+        out, pre = r if keep else (r, None)
+        ctx.save_for_backward(x, W, pre)
+        ctx.act = act
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        x, W, pre = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dout = dout.contiguous()
+        dx = dW = db = None
+        if any(need[:3]):
+            dx, dW, db = ssm_linear_bwd(x, W, dout, pre, ctx.act, want_dx=need[0], want_dW=need[1], want_dbias=need[2])
+        return dx, dW, db, dout if need[3] else None, None
+
+
+def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None,
+           residual: Optional[torch.Tensor] = None, act: str = "none") -> torch.Tensor:
+    """Differentiable linear layer on token rows [..., d_in] with its epilogue: act(x W^T + bias) + residual."""
+    return _Linear.apply(x, W, bias, residual, act)

@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libssmscan.so")
 SOURCES = ["ssm_fwd.hip", "ssm_bwd.hip", "ssm_step.hip", "ssm_proj.hip", "affine_scan.hip", "noalloc.hip",
            "ssm_lpar.hip", "ssm_head.hip", "ssm_head_bf16.hip", "ssm_head_f32.hip",
-           "capi.cpp", "capi_head.cpp"]
+           "ssm_norm.hip", "ssm_linear.hip", "capi.cpp", "capi_head.cpp", "capi_layer.cpp"]
 FLAGS = ["-O3", "--offload-arch=gfx950", "-std=c++17", "-fPIC", "-ffp-contract=off",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wall", "-Wno-unused-command-line-argument"]

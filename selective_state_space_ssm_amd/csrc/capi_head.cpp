@@ -29,6 +29,7 @@ int check_head_sizes(int64_t batch, int64_t L, int64_t H, int64_t Hk, int64_t dk
   int64_t bh, n;
   if (!mul_ok(batch, H, &bh) || !mul_ok(bh, L, &n) || !mul_ok(n, ssm::kHeadMaxDim, &n) || n > (int64_t(1) << 58))
     return fail(SSM_EINVAL, "tensor sizes overflow");
+  if (L > (int64_t(1) << 30)) return fail(SSM_EUNSUPPORTED, "L=%lld > 2^30 is not supported", (long long)L);
   if (bh > 65535) return fail(SSM_EUNSUPPORTED, "batch * n_heads = %lld > 65535 is not supported", (long long)bh);
   return SSM_OK;
 }

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, co
                                                          const float* dlast, const float* rq, const float* rk,
                                                          int64_t ntile, HeadDev p, int64_t seg_len, void* dg) {
   __shared__ double sh[4];
-  const int64_t bh = blockIdx.y, k = blockIdx.x, b = bh / p.H, h = bh % p.H, ssize = p.rows * p.cols;
+  const int64_t bh = blockIdx.y, k = blockIdx.x, b = bh / p.H, h = bh % p.H, ssize = static_cast<int64_t>(p.rows) * p.cols;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int64_t len = p.L;
   if (p.lengths != nullptr) {
@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, co
   if (lane == 0) sh[wave] = x;
   __syncthreads();
   double carry = (sh[0] + sh[1]) + (sh[2] + sh[3]);
-  if (k + 1 < p.nseg && t1 < len) carry *= __builtin_amdgcn_exp2f(headk::decay_at<IO>(p, b, h, t1));
-  const int64_t nbh = p.batch * p.H;
+  if (k + 1 < p.nseg && t1 < len) carry *= __builtin_amdgcn_exp2f(headk::decay_at<IO>(p, static_cast<int>(b), static_cast<int>(h), static_cast<int>(t1)));
+  const int64_t nbh = static_cast<int64_t>(p.batch) * p.H;
   for (int64_t e = t1; e > t0; e -= 256) {
     const int64_t t = e - 1 - tid;  // thread 0 has the last token
     double v = 0;
@@ -108,7 +108,9 @@ __global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, co
     for (int w = 0; w < wave; ++w) before += sh[w];
     carry += (sh[0] + sh[1]) + (sh[2] + sh[3]);
     if (t >= t0) {
-      const float out = t < len ? static_cast<float>(before + v) : 0.f;
+      // nothing is decayed at the first token of a sequence that starts from zero
+      const bool none = t >= len || (t == 0 && p.h0 == nullptr);
+      const float out = none ? 0.f : static_cast<float>(before + v);
       IO::template st<1>(static_cast<typename IO::T*>(dg) + (b * p.L + t) * p.H + h, &out);
     }
   }
@@ -231,16 +233,18 @@ __global__ void __launch_bounds__(256) ssm_head_step_kernel(HeadStepDev p) {
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
-// 64-column tiles per workgroup for an operand pair: two where the state then
-// still fits the registers of two workgroups per CU.
-int nc_for(int64_t rows, int64_t cols) { return rows > 32 && rows <= 128 && cols > 64 ? 2 : 1; }
-int64_t tiles_for(int64_t rows, int64_t cols) { return cdiv(cols, 64 * nc_for(rows, cols)); }
+// Wavefronts per workgroup, each with 16 columns: eight where there are more
+// than 64 columns and every operand row is whole vectors.
+int nw_for(int64_t cols, bool vec) { return cols > 64 && vec ? 8 : 4; }
+int64_t tiles_for(int64_t cols, bool vec) { return cdiv(cols, 16 * nw_for(cols, vec)); }
 
 struct Plan {
   int64_t C, nch, cps, nseg;
+  bool vec;
 };
-Plan plan_of(int64_t batch, int64_t H, int64_t tiles, int64_t L, bool bf16, bool dg) {
+Plan plan_of(int64_t batch, int64_t H, int64_t tiles, int64_t L, bool bf16, bool dg, bool vec) {
   Plan p;
+  p.vec = vec;
   p.C = bf16 ? headk::HeadCfg<BF16>::C : headk::HeadCfg<F32>::C;
   p.nch = cdiv(L, p.C);
   int64_t want = kHeadSlots / (batch * H * tiles);
@@ -259,13 +263,19 @@ struct Operand {
   int rep;
 };
 
-hipError_t launch_pass(const HeadDev& p, bool bf16, int mode, hipStream_t st) {
-  const int nc = nc_for(p.rows, p.cols);
-  return bf16 ? launch_head_bf16(p, mode, nc, st) : launch_head_f32(p, mode, nc, st);
+hipError_t launch_pass(const HeadDev& p, bool bf16, int mode, bool vec, hipStream_t st) {
+  const int nw = nw_for(p.cols, vec);
+  return bf16 ? launch_head_bf16(p, mode, nw, vec, st) : launch_head_f32(p, mode, nw, vec, st);
 }
 
-bool vec16(const Operand& o, int64_t width, int64_t es) {
-  return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.b * es % 16 == 0 && o.t * es % 16 == 0 && width * es % 16 == 0;
+// Every row of every operand is whole, aligned 16-byte vectors.
+bool vec16(const void* p, int64_t b, int64_t t, int64_t es) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && b * es % 16 == 0 && t * es % 16 == 0;
+}
+bool all_vec(const HeadArgs& a, bool bf16) {
+  const int64_t es = bf16 ? 2 : 4;
+  return a.dk * es % 16 == 0 && a.dv * es % 16 == 0 && vec16(a.q, a.q_b, a.q_t, es) && vec16(a.k, a.k_b, a.k_t, es) &&
+         vec16(a.v, a.v_b, a.v_t, es);
 }
 
 // A pass' operands: x and y of width `rows`, z and the output of width `cols`.
@@ -275,23 +285,25 @@ HeadDev pass_of(const HeadArgs& a, const Plan& pl, const Operand& x, const Opera
   HeadDev d{};
   d.x = static_cast<const char*>(x.p); d.y = static_cast<const char*>(y.p); d.z = static_cast<const char*>(z.p);
   d.o = static_cast<char*>(o);
-  d.x_b = x.b; d.x_t = x.t; d.y_b = y.b; d.y_t = y.t; d.z_b = z.b; d.z_t = z.t;
+  d.x_b = x.b * es; d.y_b = y.b * es; d.z_b = z.b * es;
+  d.x_t = static_cast<uint32_t>(x.t * es); d.y_t = static_cast<uint32_t>(y.t * es); d.z_t = static_cast<uint32_t>(z.t * es);
   d.x_rep = x.rep; d.y_rep = y.rep; d.z_rep = z.rep;
   d.g = static_cast<const char*>(a.g); d.g_head = a.g_head; d.lengths = a.lengths;
-  d.batch = a.batch; d.H = a.H; d.L = a.L; d.rows = rows; d.cols = cols;
-  d.nch = pl.nch; d.cps = pl.cps; d.nseg = pl.nseg; d.ntile = tiles_for(rows, cols);
+  d.batch = static_cast<int>(a.batch); d.H = static_cast<int>(a.H); d.L = static_cast<int>(a.L);
+  d.rows = static_cast<int>(rows); d.cols = static_cast<int>(cols);
+  d.nch = static_cast<int>(pl.nch); d.cps = static_cast<int>(pl.cps); d.nseg = static_cast<int>(pl.nseg);
+  d.ntile = static_cast<int>(tiles_for(cols, pl.vec));
   d.ps = d.ss = d.us = 1.f;
-  d.vec_x = vec16(x, rows, es); d.vec_y = vec16(y, rows, es); d.vec_z = vec16(z, cols, es);
   d.vec_o = cols % 4 == 0;
   return d;
 }
 
 hipError_t launch_carry(const HeadDev& d, hipStream_t st) {
   if (d.nseg <= 2) return hipSuccess;
-  const int64_t ssize = d.rows * d.cols;
+  const int64_t ssize = static_cast<int64_t>(d.rows) * d.cols;
   hipLaunchKernelGGL(ssm_head_carry_kernel, dim3(static_cast<unsigned>(cdiv(ssize, 256)),
                                                  static_cast<unsigned>(d.batch * d.H)), dim3(256), 0, st, d.seg_state,
-                     d.seg_decay, d.nseg, d.nseg - 1, ssize, d.rev);
+                     d.seg_decay, static_cast<int64_t>(d.nseg), static_cast<int64_t>(d.nseg - 1), ssize, d.rev);
   return hipGetLastError();
 }
 
@@ -318,7 +330,7 @@ BwdSpace bwd_space(const HeadArgs& a, const Plan& pl) {
     at += up16(bytes);
     return r;
   };
-  const int64_t bh = a.batch * a.H, ss = a.dk * a.dv, nt = tiles_for(a.dv, a.dk);
+  const int64_t bh = a.batch * a.H, ss = a.dk * a.dv, nt = tiles_for(a.dk, false);  // the narrower tiles: enough for both
   if (pl.nseg > 1) {
     w.s = take(4 * bh * pl.nseg * ss);
     w.r = take(4 * bh * pl.nseg * ss);
@@ -335,10 +347,13 @@ BwdSpace bwd_space(const HeadArgs& a, const Plan& pl) {
   w.total = at;
   return w;
 }
-Plan fwd_plan(const HeadArgs& a, bool bf16) { return plan_of(a.batch, a.H, tiles_for(a.dk, a.dv), a.L, bf16, false); }
+// The segments go by the sizes alone (the workspace's size is asked for without the operands).
+Plan fwd_plan(const HeadArgs& a, bool bf16) {
+  return plan_of(a.batch, a.H, tiles_for(a.dv, true), a.L, bf16, false, all_vec(a, bf16));
+}
 Plan bwd_plan(const HeadArgs& a, bool bf16) {
-  const int64_t t1 = tiles_for(a.dk, a.dv), t2 = tiles_for(a.dv, a.dk);
-  return plan_of(a.batch, a.H, t1 < t2 ? t1 : t2, a.L, bf16, true);
+  const int64_t t1 = tiles_for(a.dv, true), t2 = tiles_for(a.dk, true);
+  return plan_of(a.batch, a.H, t1 < t2 ? t1 : t2, a.L, bf16, true, all_vec(a, bf16));
 }
 
 template <typename IO>
@@ -356,7 +371,7 @@ int64_t head_workspace_bytes(const HeadArgs& a, bool bf16, bool backward) {
 }
 
 int64_t head_workgroups(const HeadArgs& a, bool bf16) {
-  const int64_t t1 = tiles_for(a.dk, a.dv), t2 = tiles_for(a.dv, a.dk);
+  const int64_t t1 = tiles_for(a.dv, false), t2 = tiles_for(a.dk, false);
   return a.batch * a.H * (t1 > t2 ? t1 : t2) * bwd_plan(a, bf16).nseg;
 }
 
@@ -367,17 +382,17 @@ hipError_t launch_head_fwd(const HeadArgs& a, bool bf16, char* work, hipStream_t
   HeadDev d = pass_of(a, pl, {a.q, a.q_b, a.q_t, rep}, {a.k, a.k_b, a.k_t, rep}, {a.v, a.v_b, a.v_t, 1}, a.o, a.dk, a.dv,
                       bf16);
   d.ps = d.ss = a.scale;
-  d.s_r = a.dv; d.s_c = 1;
+  d.s_r = static_cast<int>(a.dv); d.s_c = 1;
   d.h0 = a.h0;
-  d.last = a.last; d.last_bh = a.dk * a.dv;
+  d.last = a.last;
   d.seg_state = reinterpret_cast<float*>(work + w.state);
   d.seg_decay = reinterpret_cast<float*>(work + w.decay);
   if (pl.nseg > 1) {
-    hipError_t e = launch_pass(d, bf16, headk::kState, st);
+    hipError_t e = launch_pass(d, bf16, headk::kState, pl.vec, st);
     if (e == hipSuccess) e = launch_carry(d, st);
     if (e != hipSuccess) return e;
   }
-  return launch_pass(d, bf16, headk::kOut, st);
+  return launch_pass(d, bf16, headk::kOut, pl.vec, st);
 }
 
 hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t st) {
@@ -385,6 +400,7 @@ hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t
   const BwdSpace w = bwd_space(a, pl);
   const int rep = static_cast<int>(a.H / a.Hk);
   const bool shared = rep > 1, dg = a.dg != nullptr;
+  const int64_t es = bf16 ? 2 : 4;
   const Operand q{a.q, a.q_b, a.q_t, rep}, k{a.k, a.k_b, a.k_t, rep}, v{a.v, a.v_b, a.v_t, 1};
   const Operand go{a.dout, a.L * a.H * a.dv, a.H * a.dv, 1};
   float* s_seg = reinterpret_cast<float*>(work + w.s);
@@ -397,47 +413,49 @@ hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t
 
   HeadDev dq = pass_of(a, pl, go, v, k, pq, a.dv, a.dk, bf16);
   dq.ps = dq.ss = a.scale;
-  dq.s_r = 1; dq.s_c = a.dv;
+  dq.s_r = 1; dq.s_c = static_cast<int>(a.dv);
   dq.h0 = a.h0;
   dq.seg_state = s_seg; dq.seg_decay = reinterpret_cast<float*>(work + w.sdec);
-  dq.last = dg ? s_last : nullptr; dq.last_bh = a.dk * a.dv;
+  dq.last = dg ? s_last : nullptr;
   dq.out_f32 = shared;
 
   HeadDev dv = pass_of(a, pl, k, q, go, a.dv_out, a.dk, a.dv, bf16);
   dv.ps = dv.us = a.scale;
-  dv.s_r = a.dv; dv.s_c = 1;
+  dv.s_r = static_cast<int>(a.dv); dv.s_c = 1;
   dv.rev = 1;
   dv.h0 = a.dlast;
   dv.seg_state = r_seg; dv.seg_decay = reinterpret_cast<float*>(work + w.rdec);
-  dv.last = a.dh0; dv.last_bh = a.dk * a.dv; dv.end_decay = 1;
+  dv.last = a.dh0; dv.end_decay = 1;
 
   HeadDev dk = pass_of(a, pl, v, go, q, pk, a.dv, a.dk, bf16);
   dk.ps = dk.us = a.scale;
-  dk.s_r = 1; dk.s_c = a.dv;
+  dk.s_r = 1; dk.s_c = static_cast<int>(a.dv);
   dk.rev = 1;
   dk.h0 = a.dlast;
   dk.seg_state = r_seg; dk.seg_decay = dv.seg_decay;
   dk.out_f32 = shared;
 
   if (dg) {
-    dq.dotv = static_cast<const char*>(a.q); dq.dot_b = a.q_b; dq.dot_t = a.q_t; dq.dot_rep = rep; dq.dot_out = rq;
-    dk.dotv = static_cast<const char*>(a.k); dk.dot_b = a.k_b; dk.dot_t = a.k_t; dk.dot_rep = rep; dk.dot_out = rk;
+    dq.dotv = static_cast<const char*>(a.q); dq.dot_b = a.q_b * es; dq.dot_t = static_cast<uint32_t>(a.q_t * es);
+    dq.dot_rep = rep; dq.dot_out = rq;
+    dk.dotv = static_cast<const char*>(a.k); dk.dot_b = a.k_b * es; dk.dot_t = static_cast<uint32_t>(a.k_t * es);
+    dk.dot_rep = rep; dk.dot_out = rk;
   }
   hipError_t e = hipSuccess;
   if (pl.nseg > 1) {
-    e = launch_pass(dq, bf16, headk::kState, st);
+    e = launch_pass(dq, bf16, headk::kState, pl.vec, st);
     if (e == hipSuccess) e = launch_carry(dq, st);
-    if (e == hipSuccess) e = launch_pass(dv, bf16, headk::kState, st);
+    if (e == hipSuccess) e = launch_pass(dv, bf16, headk::kState, pl.vec, st);
     if (e == hipSuccess) e = launch_carry(dv, st);
   }
-  if (e == hipSuccess) e = launch_pass(dq, bf16, headk::kOut, st);
-  if (e == hipSuccess) e = launch_pass(dk, bf16, headk::kOut, st);
-  if (e == hipSuccess) e = launch_pass(dv, bf16, headk::kOut, st);
+  if (e == hipSuccess) e = launch_pass(dq, bf16, headk::kOut, pl.vec, st);
+  if (e == hipSuccess) e = launch_pass(dk, bf16, headk::kOut, pl.vec, st);
+  if (e == hipSuccess) e = launch_pass(dv, bf16, headk::kOut, pl.vec, st);
   if (e != hipSuccess) return e;
   if (dg) {
     auto kern = bf16 ? ssm_head_dg_kernel<BF16> : ssm_head_dg_kernel<F32>;
     hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(pl.nseg), static_cast<unsigned>(a.batch * a.H)), dim3(256), 0, st,
-                       s_seg, r_seg, s_last, a.dlast, rq, rk, dq.ntile, dq, pl.cps * pl.C, a.dg);
+                       s_seg, r_seg, s_last, a.dlast, rq, rk, static_cast<int64_t>(dq.ntile), dq, pl.cps * pl.C, a.dg);
     e = hipGetLastError();
   }
   if (e == hipSuccess && shared) {

@@ -3,8 +3,8 @@
 
 namespace ssm {
 
-hipError_t launch_head_f32(const headk::HeadDev& p, int mode, int nc, hipStream_t st) {
-  return headk::launch_head_io<dev::F32>(p, mode, nc, st);
+hipError_t launch_head_f32(const headk::HeadDev& p, int mode, int nw, bool vec, hipStream_t st) {
+  return headk::launch_head_io<dev::F32>(p, mode, nw, vec, st);
 }
 
 }  // namespace ssm

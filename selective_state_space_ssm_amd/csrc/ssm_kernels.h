@@ -231,4 +231,50 @@ struct HeadStepArgs {
 };
 hipError_t launch_head_step(const HeadStepArgs& a, bool bf16, hipStream_t st);
 
+// Grouped norm of dense rows [rows][channels] with a SiLU gate (ssm_norm.hip)
+// and its gradients.
+struct NormArgs {
+  const void* x;
+  const void* z;        // nullable: no gate
+  const float* w;       // [channels], nullable (ones)
+  void* y;
+  const void* dy;       // backward only, with dx, dz and dw
+  void* dx;
+  void* dz;             // iff z
+  float* dw;            // nullable
+  int64_t rows, channels, groups;
+  float eps;
+  int center, gate_first;
+};
+constexpr int64_t kNormMaxGroup = 8192;  // channels per group
+int64_t norm_workspace_bytes(const NormArgs& a, bool bf16);
+int64_t norm_workgroups(const NormArgs& a, bool bf16);
+hipError_t launch_gate_norm(const NormArgs& a, bool bf16, bool backward, float* work, hipStream_t st);
+
+// out[c] = sum over k < count of part[k][c], in a fixed order
+hipError_t launch_column_sum(const float* part, int64_t count, int64_t cols, void* out, bool bf16, hipStream_t st);
+
+// Token-major linear layer (ssm_linear.hip): out = act(x W^T + bias) +
+// residual, x [rows][k], W [m][k], out, residual and pre (the value before
+// act) [rows][m]; its gradients for dout.
+constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;
+struct LinearArgs {
+  const void* x;
+  const void* w;
+  const void* bias;      // [m], nullable
+  const void* residual;  // nullable
+  void* out;
+  void* pre;             // forward: output, nullable; backward: input, required unless act is none
+  const void* dout;
+  void* dx;              // nullable
+  void* dw;              // nullable
+  void* dbias;           // nullable
+  int64_t rows, k, m;
+  int act;
+};
+int64_t linear_workspace_bytes(const LinearArgs& a, bool bf16, bool backward);
+int64_t linear_workgroups(const LinearArgs& a, bool bf16);
+hipError_t launch_linear(const LinearArgs& a, bool bf16, char* work, hipStream_t st);
+hipError_t launch_linear_bwd(const LinearArgs& a, bool bf16, char* work, hipStream_t st);
+
 }  // namespace ssm

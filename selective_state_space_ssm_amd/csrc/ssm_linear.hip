@@ -1,0 +1,532 @@
+// Linear layer on token rows with bias, activation and residual in its
+// epilogue, and its gradients, on the matrix cores:
+//
+//   pre = x W^T + bias,  out = act(pre) + residual       x [T][K], W [M][K]
+//   dpre = dout act'(pre)                                 (elementwise, with the column sums for dbias)
+//   dx = dpre W,   dW = dpre^T x,   dbias = sum_t dpre
+//
+// All three products are one kernel: out[r][c] = sum_k R[r][k] C[c][k], each
+// operand stored either with k contiguous or (template flags) with its rows
+// contiguous:
+//
+//            r      c      k      R             C
+//   out      token  m      k      x             W
+//   dx       token  k      m      dpre          W, rows contiguous
+//   dW       m      k      token  dpre, rows c. x, rows contiguous
+//
+// The c side is the first operand of the matrix instruction, so that a lane
+// holds four consecutive c of one r and the epilogue reads and writes them as
+// one vector.
+//
+// A sum over k with few output tiles (dW over all tokens; few rows) is split
+// over workgroups: float32 partials, added in a fixed order by a second launch
+// that then holds the epilogue.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ssm_device.h"
+#include "ssm_kernels.h"
+
+namespace ssm {
+namespace {
+
+using namespace dev;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr uint32_t kOOB = 0x80000000u;     // an offset past every resource
+constexpr uint32_t kRecords = 0x7fffffffu;  // resources are bounded by the offsets' own checks
+constexpr int64_t kCUs = 256;
+
+template <typename IO>
+struct LinCfg;
+template <>
+struct LinCfg<F32> {
+  static constexpr int ES = 4, E = 4;  // bytes per value, values per 16 bytes
+};
+template <>
+struct LinCfg<BF16> {
+  static constexpr int ES = 2, E = 8;
+};
+
+struct LinDev {
+  const char* c;
+  const char* r;
+  char* out;                 // [nr][nc], or float32 partials [nsplit][nr][nc]
+  int64_t nc, nr, K;
+  int64_t ldc, ldr;          // elements between rows (k contiguous) or between k (rows contiguous)
+  int64_t kpart, nsplit;     // k per split (a multiple of the step)
+  const char* bias;          // [nc], nullable
+  const char* residual;      // [nr][nc], nullable
+  char* pre;                 // [nr][nc], nullable
+  int act;
+};
+
+__device__ __forceinline__ float act_of(float p, int act) {
+  if (act == kActSilu) return p * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * p));
+  if (act == kActGelu) return 0.5f * p * erfcf(-0.70710678118654752f * p);  // erfc keeps the tail's digits
+  return p;
+}
+
+__device__ __forceinline__ float act_grad(float p, int act) {
+  if (act == kActSilu) {
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * p));
+    return s * __builtin_fmaf(p, 1.f - s, 1.f);
+  }
+  if (act == kActGelu)
+    return __builtin_fmaf(p, 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * kLog2e * p * p),
+                          0.5f * erfcf(-0.70710678118654752f * p));
+  return 1.f;
+}
+
+// Four values of row r from column c: bias, act, residual, rounding.  CNT of them exist.
+template <typename IO, int CNT>
+__device__ __forceinline__ void epilogue(const LinDev& p, int64_t r, int64_t c, float* v) {
+  using T = typename IO::T;
+  const int64_t at = r * p.nc + c;
+  float t[CNT];
+  if (p.bias != nullptr) {
+    IO::template ld<CNT>(reinterpret_cast<const T*>(p.bias) + c, t);
+#pragma unroll
+    for (int e = 0; e < CNT; ++e) v[e] += t[e];
+  }
+  if (p.pre != nullptr) IO::template st<CNT>(reinterpret_cast<T*>(p.pre) + at, v);
+  if (p.act != kActNone) {
+#pragma unroll
+    for (int e = 0; e < CNT; ++e) v[e] = act_of(v[e], p.act);
+  }
+  if (p.residual != nullptr) {
+    IO::template ld<CNT>(reinterpret_cast<const T*>(p.residual) + at, t);
+#pragma unroll
+    for (int e = 0; e < CNT; ++e) v[e] += t[e];
+  }
+  IO::template st<CNT>(reinterpret_cast<T*>(p.out) + at, v);
+}
+
+// ------------------------------------------------------------------------
+// Tiles staged through registers: any size, both types.  A workgroup of four
+// wavefronts (2 x 2) owns 32 TC columns x 32 TR rows and walks k in steps of
+// 128 bytes; LDS holds both operands with k contiguous (the rows-contiguous
+// ones are transposed on the way in), double buffered, 16-byte chunk q of row
+// r at q ^ swz(r).
+// ------------------------------------------------------------------------
+__device__ __forceinline__ int swz(int r) { return (r ^ (r >> 3)) & 7; }
+
+template <typename IO, int ROWS, bool TR, bool VEC>
+struct Stage {
+  using C = LinCfg<IO>;
+  static constexpr int E = C::E, ES = C::ES;
+  static constexpr int N = TR ? E : ROWS / 32;  // 16-byte registers per thread
+  uint4 reg[N];
+
+  // rows row0 .. of `base` (nrows in all), k from k0, krem of them exist
+  __device__ __forceinline__ void load(const char* base, int64_t ld, int64_t row0, int64_t nrows, int64_t k0, int krem,
+                                       int tid) {
+    if constexpr (!TR) {
+      const int q = tid & 7, r0 = tid >> 3;
+      const Rsrc rs = make_rsrc(base + (row0 * ld + k0) * ES, kRecords);
+      const uint32_t rb = static_cast<uint32_t>(ld * ES);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int r = r0 + 32 * i;
+        const bool rok = row0 + r < nrows;
+        const uint32_t off = static_cast<uint32_t>(r) * rb + q * 16;
+        fetch(rs, off, rok ? krem - q * E : 0, reg[i]);
+      }
+    } else {
+      constexpr int G = ROWS / E;  // row groups; 8 k groups
+      const int tg = tid % G, kg = tid / G;
+      const Rsrc rs = make_rsrc(base + (k0 * ld + row0) * ES, kRecords);
+      const uint32_t kb = static_cast<uint32_t>(ld * ES);
+      const int64_t left = nrows - row0 - tg * E;
+      const int rrem = kg < 8 ? (left > E ? E : static_cast<int>(left)) : 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int k = kg * E + i;
+        fetch(rs, static_cast<uint32_t>(k) * kb + tg * 16, k < krem ? rrem : 0, reg[i]);
+      }
+    }
+  }
+  // 16 bytes, the first `have` values of them
+  static __device__ __forceinline__ void fetch(Rsrc rs, uint32_t off, int have, uint4& o) {
+    if constexpr (VEC) {
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, have > 0 ? off : kOOB, 0, 0);
+      o = make_uint4(v.x, v.y, v.z, v.w);
+    } else {
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t oe = e < have ? off + e * ES : kOOB;
+        if constexpr (ES == 4) {
+          w[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, oe, 0, 0);
+        } else {
+          const uint32_t h = __builtin_amdgcn_raw_buffer_load_b16(rs, oe, 0, 0);
+          w[e >> 1] |= (e & 1) ? (h << 16) : h;
+        }
+      }
+      o = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __device__ __forceinline__ void store(uint4* tile, int tid) const {
+    if constexpr (!TR) {
+      const int q = tid & 7, r0 = tid >> 3;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int r = r0 + 32 * i;
+        tile[r * 8 + (q ^ swz(r))] = reg[i];
+      }
+    } else {
+      constexpr int G = ROWS / E;
+      const int tg = tid % G, kg = tid / G;
+      if (kg >= 8) return;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        uint32_t o[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          if constexpr (ES == 2) {
+            const uint32_t lo = reinterpret_cast<const uint32_t*>(&reg[2 * d])[j >> 1];
+            const uint32_t hi = reinterpret_cast<const uint32_t*>(&reg[2 * d + 1])[j >> 1];
+            o[d] = (j & 1) ? ((lo >> 16) | (hi & 0xffff0000u)) : ((lo & 0xffffu) | (hi << 16));
+          } else {
+            o[d] = reinterpret_cast<const uint32_t*>(&reg[d])[j];
+          }
+        }
+        const int r = tg * E + j;
+        tile[r * 8 + (kg ^ swz(r))] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+};
+
+template <typename IO, int TC, int TR, bool CTR, bool RTR, bool VEC, bool PART>
+__global__ void __launch_bounds__(256, 2) ssm_linear_tile_kernel(LinDev p) {
+  using C = LinCfg<IO>;
+  constexpr int E = C::E, ES = C::ES, BC = 32 * TC, BR = 32 * TR, BK = 8 * E;
+  extern __shared__ uint4 lds[];  // [2][BC + BR][8]
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wc = wave & 1, wr = wave >> 1;
+
+  const int64_t mc = (p.nc + BC - 1) / BC, mr = (p.nr + BR - 1) / BR;
+  // XCD-contiguous order, c tiles fastest: the workgroups of an XCD share rows of R
+  const int64_t G = gridDim.x, pid = blockIdx.x, q8 = G / 8, r8 = G % 8, xcd = pid % 8;
+  int64_t idx = xcd * q8 + (xcd < r8 ? xcd : r8) + pid / 8;
+  const int64_t c0 = idx % mc * BC;
+  idx /= mc;
+  const int64_t r0 = idx % mr * BR, split = idx / mr;
+  const int64_t kb = split * p.kpart, ke = kb + p.kpart < p.K ? kb + p.kpart : p.K;
+
+  Stage<IO, BC, CTR, VEC> sc;
+  Stage<IO, BR, RTR, VEC> sr;
+  auto load = [&](int64_t k0) {
+    const int krem = ke - k0 > BK ? BK : static_cast<int>(ke - k0);
+    sc.load(p.c, p.ldc, c0, p.nc, k0, krem, tid);
+    sr.load(p.r, p.ldr, r0, p.nr, k0, krem, tid);
+  };
+  f32x4 acc[TC][TR];
+#pragma unroll
+  for (int i = 0; i < TC; ++i)
+#pragma unroll
+    for (int j = 0; j < TR; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int64_t steps = (ke - kb + BK - 1) / BK;
+  if (steps > 0) {
+    load(kb);
+    sc.store(lds, tid);
+    sr.store(lds + BC * 8, tid);
+  }
+  __syncthreads();
+  for (int64_t s = 0; s < steps; ++s) {
+    const uint4* tc = lds + (s & 1) * (BC + BR) * 8 + wc * (BC / 2) * 8;
+    const uint4* tr = lds + (s & 1) * (BC + BR) * 8 + (BC + wr * (BR / 2)) * 8;
+    if (s + 1 < steps) load(kb + (s + 1) * BK);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 fc[TC], fr[TR];
+#pragma unroll
+      for (int i = 0; i < TC; ++i) fc[i] = tc[(16 * i + li) * 8 + ((4 * h + g) ^ swz(16 * i + li + wc * (BC / 2)))];
+#pragma unroll
+      for (int j = 0; j < TR; ++j) fr[j] = tr[(16 * j + li) * 8 + ((4 * h + g) ^ swz(16 * j + li + wr * (BR / 2)))];
+      if constexpr (ES == 2) {
+#pragma unroll
+        for (int i = 0; i < TC; ++i)
+#pragma unroll
+          for (int j = 0; j < TR; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fc[i]),
+                                                                __builtin_bit_cast(bf16x8, fr[j]), acc[i][j], 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int i = 0; i < TC; ++i)
+#pragma unroll
+            for (int j = 0; j < TR; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                  __uint_as_float(reinterpret_cast<const uint32_t*>(&fc[i])[e]),
+                  __uint_as_float(reinterpret_cast<const uint32_t*>(&fr[j])[e]), acc[i][j], 0, 0, 0);
+      }
+    }
+    if (s + 1 < steps) {
+      uint4* n = lds + ((s + 1) & 1) * (BC + BR) * 8;
+      sc.store(n, tid);
+      sr.store(n + BC * 8, tid);
+    }
+    __syncthreads();
+  }
+
+#pragma unroll
+  for (int i = 0; i < TC; ++i) {
+    const int64_t c = c0 + wc * (BC / 2) + 16 * i + 4 * g;
+#pragma unroll
+    for (int j = 0; j < TR; ++j) {
+      const int64_t r = r0 + wr * (BR / 2) + 16 * j + li;
+      if (r >= p.nr || c >= p.nc) continue;
+      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      if constexpr (PART) {
+        float* o = reinterpret_cast<float*>(p.out) + (split * p.nr + r) * p.nc + c;
+        if constexpr (VEC) {
+          F32::st<4>(o, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < p.nc) o[e] = v[e];
+        }
+      } else if constexpr (VEC) {
+        epilogue<IO, 4>(p, r, c, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < p.nc) epilogue<IO, 1>(p, r, c + e, v + e);
+      }
+    }
+  }
+}
+
+// Partials added in order, then the epilogue: CNT values per thread.
+template <typename IO, int CNT>
+__global__ void __launch_bounds__(256) ssm_linear_sum_kernel(const float* part, LinDev p) {
+  const int64_t total = p.nr * p.nc / CNT, stride = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += stride) {
+    const int64_t at = i * CNT;
+    float v[CNT], t[CNT];
+    F32::ld<CNT>(part + at, v);
+    for (int64_t s = 1; s < p.nsplit; ++s) {
+      F32::ld<CNT>(part + s * p.nr * p.nc + at, t);
+#pragma unroll
+      for (int e = 0; e < CNT; ++e) v[e] += t[e];
+    }
+    epilogue<IO, CNT>(p, at / p.nc, at % p.nc, v);
+  }
+}
+
+// dpre = dout act'(pre), and its column sums over this workgroup's rows:
+// thread (cv, rr) takes CNT columns of rows rr, rr + 8, ...
+template <typename IO, int CNT>
+__global__ void __launch_bounds__(256) ssm_linear_dpre_kernel(const void* dout, const void* pre, void* dpre, float* part,
+                                                             int64_t rows, int64_t m, int64_t per, int act) {
+  using T = typename IO::T;
+  __shared__ float sh[8][32 * CNT];
+  const int cv = threadIdx.x & 31, rr = threadIdx.x >> 5;
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + cv) * CNT;
+  const int64_t t0 = blockIdx.y * per, t1 = t0 + per < rows ? t0 + per : rows;
+  float s[CNT];
+#pragma unroll
+  for (int e = 0; e < CNT; ++e) s[e] = 0.f;
+  if (c < m) {
+    for (int64_t t = t0 + rr; t < t1; t += 8) {
+      float d[CNT], q[CNT];
+      IO::template ld<CNT>(static_cast<const T*>(dout) + t * m + c, d);
+      if (act != kActNone) {
+        IO::template ld<CNT>(static_cast<const T*>(pre) + t * m + c, q);
+#pragma unroll
+        for (int e = 0; e < CNT; ++e) d[e] *= act_grad(q[e], act);
+        IO::template st<CNT>(static_cast<T*>(dpre) + t * m + c, d);
+      }
+#pragma unroll
+      for (int e = 0; e < CNT; ++e) s[e] += d[e];
+    }
+  }
+  if (part == nullptr) return;
+#pragma unroll
+  for (int e = 0; e < CNT; ++e) sh[rr][cv * CNT + e] = s[e];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * CNT; i += 256) {
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 * CNT + i;
+    if (col < m) {
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v += sh[k][i];
+      part[blockIdx.y * m + col] = v;
+    }
+  }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+// One product's tile (32 t x 32 t) and split of k.  The largest tile that
+// still gives every CU a workgroup; below that the smallest, with k split
+// until the CUs have one each and a split keeps at least four steps.
+struct Tiling {
+  int t;
+  int64_t kpart, nsplit;
+};
+template <typename IO>
+Tiling tiling(int64_t nc, int64_t nr, int64_t K) {
+  constexpr int64_t BK = 8 * LinCfg<IO>::E;
+  Tiling w{2, 0, 1};
+  auto tiles = [&](int t) { return cdiv(nc, 32 * t) * cdiv(nr, 32 * t); };
+  if (tiles(4) >= kCUs) w.t = 4;
+  const int64_t steps = cdiv(K, BK);
+  int64_t split = w.t == 2 && tiles(2) < kCUs ? kCUs / tiles(2) : 1;
+  if (split > steps / 4) split = steps / 4;
+  if (split < 1) split = 1;
+  w.kpart = cdiv(steps, split) * BK;
+  w.nsplit = cdiv(K, w.kpart);
+  return w;
+}
+template <typename IO>
+int64_t part_bytes(int64_t nc, int64_t nr, int64_t K) {
+  const Tiling w = tiling<IO>(nc, nr, K);
+  return w.nsplit > 1 ? up16(4 * w.nsplit * nc * nr) : 0;
+}
+
+template <typename IO, int T, bool CTR, bool RTR, bool VEC, bool PART>
+hipError_t launch_tile_t(const LinDev& p, hipStream_t st) {
+  const int64_t wgs = cdiv(p.nc, 32 * T) * cdiv(p.nr, 32 * T) * p.nsplit;
+  constexpr size_t smem = size_t(2) * 2 * 32 * T * 128;
+  hipLaunchKernelGGL((ssm_linear_tile_kernel<IO, T, T, CTR, RTR, VEC, PART>), dim3(static_cast<unsigned>(wgs)), dim3(256),
+                     smem, st, p);
+  return hipGetLastError();
+}
+
+template <typename IO, bool CTR, bool RTR>
+hipError_t product(LinDev p, char* work, hipStream_t st) {
+  constexpr int64_t E = LinCfg<IO>::E;
+  const Tiling w = tiling<IO>(p.nc, p.nr, p.K);
+  p.kpart = w.kpart;
+  p.nsplit = w.nsplit;
+  // every 16-byte chunk of an operand whole and aligned, every four outputs of a row too
+  const bool vec = p.ldc % E == 0 && p.ldr % E == 0 && p.K % ((CTR && RTR) ? 1 : E) == 0 && p.nc % (CTR ? E : 4) == 0 &&
+                   p.nr % (RTR ? E : 1) == 0;
+  const LinDev whole = p;
+  if (w.nsplit > 1) {
+    p.out = work;
+    p.bias = p.residual = nullptr;
+    p.pre = nullptr;
+  }
+  auto run = [&](auto t, auto v, auto part) {
+    return launch_tile_t<IO, decltype(t)::value, CTR, RTR, decltype(v)::value, decltype(part)::value>(p, st);
+  };
+  using T4 = std::integral_constant<int, 4>;
+  using T2 = std::integral_constant<int, 2>;
+  using Y = std::true_type;
+  using N = std::false_type;
+  hipError_t e;
+  if (w.t == 4)
+    e = vec ? run(T4{}, Y{}, N{}) : run(T4{}, N{}, N{});
+  else if (w.nsplit > 1)
+    e = vec ? run(T2{}, Y{}, Y{}) : run(T2{}, N{}, Y{});
+  else
+    e = vec ? run(T2{}, Y{}, N{}) : run(T2{}, N{}, N{});
+  if (e != hipSuccess || w.nsplit == 1) return e;
+  const bool four = p.nc % 4 == 0;
+  const int64_t blocks = cdiv(p.nr * p.nc / (four ? 4 : 1), 256);
+  auto sum = four ? ssm_linear_sum_kernel<IO, 4> : ssm_linear_sum_kernel<IO, 1>;
+  hipLaunchKernelGGL(sum, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st,
+                     reinterpret_cast<const float*>(work), whole);
+  return hipGetLastError();
+}
+
+template <typename IO>
+hipError_t forward_io(const LinearArgs& a, char* work, hipStream_t st) {
+  LinDev p{};
+  p.c = static_cast<const char*>(a.w); p.r = static_cast<const char*>(a.x); p.out = static_cast<char*>(a.out);
+  p.nc = a.m; p.nr = a.rows; p.K = a.k; p.ldc = a.k; p.ldr = a.k;
+  p.bias = static_cast<const char*>(a.bias); p.residual = static_cast<const char*>(a.residual);
+  p.pre = static_cast<char*>(a.pre); p.act = a.act;
+  return product<IO, false, false>(p, work, st);
+}
+
+// Rows per workgroup of the dpre kernel: about 2048 workgroups, 64 rows at least.
+int64_t dpre_rows(const LinearArgs& a, int64_t cols_per) {
+  const int64_t n = cdiv(2048, cdiv(a.m, cols_per));
+  const int64_t per = cdiv(a.rows, n);
+  return per < 64 ? 64 : per;
+}
+
+struct BwdSpace {
+  int64_t dpre, colsum, part, total;
+};
+template <typename IO>
+BwdSpace bwd_space(const LinearArgs& a) {
+  BwdSpace w{};
+  int64_t at = 0;
+  if (a.act != kActNone) at += up16(a.rows * a.m * LinCfg<IO>::ES);
+  w.colsum = at;
+  const int64_t cnt = a.m % LinCfg<IO>::E == 0 ? LinCfg<IO>::E : 1;
+  if (a.dbias != nullptr) at += up16(4 * cdiv(a.rows, dpre_rows(a, 32 * cnt)) * a.m);
+  w.part = at;
+  const int64_t px = a.dx ? part_bytes<IO>(a.k, a.rows, a.m) : 0, pw = a.dw ? part_bytes<IO>(a.k, a.m, a.rows) : 0;
+  w.total = at + (px > pw ? px : pw);
+  return w;
+}
+
+template <typename IO>
+hipError_t backward_io(const LinearArgs& a, char* work, hipStream_t st) {
+  constexpr int E = LinCfg<IO>::E;
+  const BwdSpace w = bwd_space<IO>(a);
+  const void* dpre = a.act != kActNone ? static_cast<const void*>(work + w.dpre) : a.dout;
+  hipError_t e = hipSuccess;
+  if (a.act != kActNone || a.dbias != nullptr) {
+    const bool vec = a.m % E == 0;
+    const int64_t per = dpre_rows(a, 32 * (vec ? E : 1)), nblk = cdiv(a.rows, per);
+    float* part = a.dbias != nullptr ? reinterpret_cast<float*>(work + w.colsum) : nullptr;
+    auto kern = vec ? ssm_linear_dpre_kernel<IO, E> : ssm_linear_dpre_kernel<IO, 1>;
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(cdiv(a.m, 32 * (vec ? E : 1))), static_cast<unsigned>(nblk)),
+                       dim3(256), 0, st, a.dout, a.pre, static_cast<void*>(work + w.dpre), part, a.rows, a.m, per, a.act);
+    e = hipGetLastError();
+    if (e == hipSuccess && part != nullptr)
+      e = launch_column_sum(part, nblk, a.m, a.dbias, std::is_same<IO, BF16>::value, st);
+  }
+  if (e == hipSuccess && a.dx != nullptr) {
+    LinDev p{};
+    p.c = static_cast<const char*>(a.w); p.r = static_cast<const char*>(dpre); p.out = static_cast<char*>(a.dx);
+    p.nc = a.k; p.nr = a.rows; p.K = a.m; p.ldc = a.k; p.ldr = a.m;
+    e = product<IO, true, false>(p, work + w.part, st);
+  }
+  if (e == hipSuccess && a.dw != nullptr) {
+    LinDev p{};
+    p.c = static_cast<const char*>(a.x); p.r = static_cast<const char*>(dpre); p.out = static_cast<char*>(a.dw);
+    p.nc = a.k; p.nr = a.m; p.K = a.rows; p.ldc = a.k; p.ldr = a.m;
+    e = product<IO, true, true>(p, work + w.part, st);
+  }
+  return e;
+}
+
+}  // namespace
+
+int64_t linear_workspace_bytes(const LinearArgs& a, bool bf16, bool backward) {
+  if (!backward) return bf16 ? part_bytes<BF16>(a.m, a.rows, a.k) : part_bytes<F32>(a.m, a.rows, a.k);
+  return bf16 ? bwd_space<BF16>(a).total : bwd_space<F32>(a).total;
+}
+
+int64_t linear_workgroups(const LinearArgs& a, bool bf16) {
+  (void)bf16;
+  // the smallest tile, and no more than one split per CU where there are fewer tiles than CUs
+  const int64_t f = cdiv(a.m, 64) * cdiv(a.rows, 64), x = cdiv(a.k, 64) * cdiv(a.rows, 64);
+  return (f > x ? f : x) + kCUs + cdiv(a.k, 64) * cdiv(a.m, 64);
+}
+
+hipError_t launch_linear(const LinearArgs& a, bool bf16, char* work, hipStream_t st) {
+  return bf16 ? forward_io<BF16>(a, work, st) : forward_io<F32>(a, work, st);
+}
+
+hipError_t launch_linear_bwd(const LinearArgs& a, bool bf16, char* work, hipStream_t st) {
+  return bf16 ? backward_io<BF16>(a, work, st) : backward_io<F32>(a, work, st);
+}
+
+}  // namespace ssm

@@ -3,8 +3,7 @@
 Tolerances, element by element.  Let B be the result with every product taken in absolute value (the oracle run on
 |q|, |k|, |v|, |do|): any float32 sum of the same products is off by at most n 2^-24 B, n the additions in a row
 (products over d, a chunk of at most 64, two per chunk for the state, and a few roundings of decays and scales).
-bfloat16 adds half a step of the output, 2^-8 |result|, and of each score, 2^-8 B, and the state's second part,
-2^-16 B.  dg is a sum of dots of q with dq and k with dk before those are rounded, scores in two parts (2^-16 B each),
+bfloat16 adds half a step of the output, 2^-8 |result|, and what scores and the state lose in two parts, 2^-16 B each.  dg is a sum of dots of q with dq and k with dk before those are rounded, scores in two parts (2^-16 B each),
 from a segment's end (at most 1024 tokens) to the token, plus <R, S> there.
 """
 import numpy as np
@@ -68,7 +67,7 @@ def bounds(x, want, B, low):
     n = adds(x) * 2.0 ** -24
     tiny = 1e-30
     if low == torch.bfloat16:
-        return 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -16 + n) * 1.01 * B + tiny
+        return 2.0 ** -8 * np.abs(want) + (2 * 2.0 ** -16 + n) * 1.01 * B + tiny
     return n * B + tiny
 
 
