@@ -42,7 +42,13 @@ namespace {
 using namespace dev;
 using headk::HeadDev;
 
-constexpr int64_t kHeadSlots = 512;       // workgroups that fill the chip: two per CU
+// The length is split where there are fewer workgroups than CUs, into as many
+// segments as give every CU two.  A split costs a second pass over y and z for
+// the segments' states: 256 heads of 128 x 128 (8 x 2048 tokens, bfloat16) take
+// 168 us whole and 187 us in two segments; 16 heads over 65536 tokens 512 us in
+// 16 segments, 464 in 32, 524 in 48.
+constexpr int64_t kHeadCUs = 256;
+constexpr int64_t kHeadSlots = 512;
 constexpr int64_t kHeadMinSegment = 256;  // tokens
 constexpr int64_t kHeadMaxDgSegment = 1024;  // tokens that the running sum of dg covers
 
@@ -233,10 +239,10 @@ __global__ void __launch_bounds__(256) ssm_head_step_kernel(HeadStepDev p) {
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
-// Wavefronts per workgroup, each with 16 columns: eight where there are more
-// than 64 columns and every operand row is whole vectors.
-int nw_for(int64_t cols, bool vec) { return cols > 64 && vec ? 8 : 4; }
-int64_t tiles_for(int64_t cols, bool vec) { return cdiv(cols, 16 * nw_for(cols, vec)); }
+// Columns of a workgroup's tile: 128 where there are more than 64 and every
+// operand row is whole vectors, else 64.
+bool wide_for(int64_t cols, bool vec) { return cols > 64 && vec; }
+int64_t tiles_for(int64_t cols, bool vec) { return cdiv(cols, wide_for(cols, vec) ? 128 : 64); }
 
 struct Plan {
   int64_t C, nch, cps, nseg;
@@ -247,7 +253,8 @@ Plan plan_of(int64_t batch, int64_t H, int64_t tiles, int64_t L, bool bf16, bool
   p.vec = vec;
   p.C = bf16 ? headk::HeadCfg<BF16>::C : headk::HeadCfg<F32>::C;
   p.nch = cdiv(L, p.C);
-  int64_t want = kHeadSlots / (batch * H * tiles);
+  const int64_t wgs = batch * H * tiles;
+  int64_t want = wgs < kHeadCUs ? kHeadSlots / wgs : 1;
   const int64_t most = L / kHeadMinSegment;
   if (want > most) want = most;
   if (want < 1) want = 1;
@@ -264,8 +271,8 @@ struct Operand {
 };
 
 hipError_t launch_pass(const HeadDev& p, bool bf16, int mode, bool vec, hipStream_t st) {
-  const int nw = nw_for(p.cols, vec);
-  return bf16 ? launch_head_bf16(p, mode, nw, vec, st) : launch_head_f32(p, mode, nw, vec, st);
+  const bool wide = wide_for(p.cols, vec);
+  return bf16 ? launch_head_bf16(p, mode, wide, vec, st) : launch_head_f32(p, mode, wide, vec, st);
 }
 
 // Every row of every operand is whole, aligned 16-byte vectors.
@@ -294,7 +301,6 @@ HeadDev pass_of(const HeadArgs& a, const Plan& pl, const Operand& x, const Opera
   d.nch = static_cast<int>(pl.nch); d.cps = static_cast<int>(pl.cps); d.nseg = static_cast<int>(pl.nseg);
   d.ntile = static_cast<int>(tiles_for(cols, pl.vec));
   d.ps = d.ss = d.us = 1.f;
-  d.vec_o = cols % 4 == 0;
   return d;
 }
 
@@ -417,7 +423,6 @@ hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t
   dq.h0 = a.h0;
   dq.seg_state = s_seg; dq.seg_decay = reinterpret_cast<float*>(work + w.sdec);
   dq.last = dg ? s_last : nullptr;
-  dq.out_f32 = shared;
 
   HeadDev dv = pass_of(a, pl, k, q, go, a.dv_out, a.dk, a.dv, bf16);
   dv.ps = dv.us = a.scale;
@@ -433,9 +438,10 @@ hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t
   dk.rev = 1;
   dk.h0 = a.dlast;
   dk.seg_state = r_seg; dk.seg_decay = dv.seg_decay;
-  dk.out_f32 = shared;
 
-  if (dg) {
+  // the float32 parts of shared heads come with their dots, wanted or not
+  const int mode = shared && bf16 ? headk::kOutF32 : headk::kOut;
+  if (dg || mode == headk::kOutF32) {
     dq.dotv = static_cast<const char*>(a.q); dq.dot_b = a.q_b * es; dq.dot_t = static_cast<uint32_t>(a.q_t * es);
     dq.dot_rep = rep; dq.dot_out = rq;
     dk.dotv = static_cast<const char*>(a.k); dk.dot_b = a.k_b * es; dk.dot_t = static_cast<uint32_t>(a.k_t * es);
@@ -448,8 +454,8 @@ hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t
     if (e == hipSuccess) e = launch_pass(dv, bf16, headk::kState, pl.vec, st);
     if (e == hipSuccess) e = launch_carry(dv, st);
   }
-  if (e == hipSuccess) e = launch_pass(dq, bf16, headk::kOut, pl.vec, st);
-  if (e == hipSuccess) e = launch_pass(dk, bf16, headk::kOut, pl.vec, st);
+  if (e == hipSuccess) e = launch_pass(dq, bf16, mode, pl.vec, st);
+  if (e == hipSuccess) e = launch_pass(dk, bf16, mode, pl.vec, st);
   if (e == hipSuccess) e = launch_pass(dv, bf16, headk::kOut, pl.vec, st);
   if (e != hipSuccess) return e;
   if (dg) {

@@ -3,8 +3,8 @@
 
 namespace ssm {
 
-hipError_t launch_head_bf16(const headk::HeadDev& p, int mode, int nw, bool vec, hipStream_t st) {
-  return headk::launch_head_io<dev::BF16>(p, mode, nw, vec, st);
+hipError_t launch_head_bf16(const headk::HeadDev& p, int mode, bool wide, bool vec, hipStream_t st) {
+  return headk::launch_head_io<dev::BF16>(p, mode, wide, vec, st);
 }
 
 }  // namespace ssm

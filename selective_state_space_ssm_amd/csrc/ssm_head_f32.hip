@@ -3,8 +3,8 @@
 
 namespace ssm {
 
-hipError_t launch_head_f32(const headk::HeadDev& p, int mode, int nw, bool vec, hipStream_t st) {
-  return headk::launch_head_io<dev::F32>(p, mode, nw, vec, st);
+hipError_t launch_head_f32(const headk::HeadDev& p, int mode, bool wide, bool vec, hipStream_t st) {
+  return headk::launch_head_io<dev::F32>(p, mode, wide, vec, st);
 }
 
 }  // namespace ssm

@@ -15,13 +15,12 @@
 // gives every gradient (ssm_head.hip).
 //
 // Mapping.  A workgroup of NW wavefronts owns one (batch row, head), a tile of
-// 16 NW columns and one segment of the length; it walks its segment's chunks
-// with the state in accumulators.  Wavefront w owns all rows and the columns
-// [16 w, 16 w + 16) of the tile, so that the state never leaves its registers:
+// 16 NW NC columns and one segment of the length; it walks its segment's
+// chunks with the state in accumulators.  Wavefront w owns all rows and 16 NC
+// columns of the tile, so that the state never leaves its registers:
 // the accumulator layout of a 16 x 16 tile (lane l holds rows 4 (l / 16) .. + 3
 // of column l % 16) is also the layout in which a matrix instruction takes that
-// tile as an operand contracted over the rows, when the other operand is read
-// in the matching order of k.  Only the C x C score matrix is shared by the
+// tile as an operand contracted over the rows (see state_row).  Only the C x C score matrix is shared by the
 // wavefronts, through LDS.  The next chunk's tiles are loaded into registers
 // while the present one is worked on.
 //
@@ -63,13 +62,28 @@ struct HeadCfg<F32> {
   static constexpr int ES = 4, E = 4, KS = 16, C = 32;
 };
 
-// Position of 16-byte chunk c of row r in a row of N chunks: the 16 rows of an
-// operand read (one chunk each) fall on different banks.
-template <int N>
-__device__ __forceinline__ int swz(int r, int c) {
-  if constexpr (N >= 16) return c ^ (r & 15);
-  else if constexpr (N == 8) return c ^ ((r ^ (r >> 3)) & 7);
-  else return c ^ (((r >> 1) ^ (r >> 3)) & 3);
+// LDS tiles have rows of N 16-byte chunks; chunk c of row r sits at position
+// c ^ swz(r).  Both kinds of operand read then spread over the banks: the same
+// chunk of 16 rows, and (bfloat16) four chunks of four neighbouring rows or
+// (float32) four chunks of rows four apart.  swz goes by r % 16, so that an
+// address is a lane's base, XORed with a constant for the chunk and offset by
+// whole rows: for row 16 R + i and chunk c | j (j the lane's, on other bits),
+//   16 N (16 R + i) + 16 ((c | j) ^ swz(i)) = (base(i, j) ^ 16 c) + 256 N R.
+template <typename IO, int N>
+__device__ __forceinline__ constexpr int swz(int r) {
+  const int r0 = r & 1, r1 = (r >> 1) & 1, r2 = (r >> 2) & 1, r3 = (r >> 3) & 1;
+  if constexpr (HeadCfg<IO>::ES == 2) {
+    if constexpr (N >= 16) return r1 << 3 | r0 << 2 | (r1 ^ r3) << 1 | r2;
+    else if constexpr (N == 8) return r1 << 2 | r2 << 1 | (r0 ^ r3);
+    else return (r1 ^ r3) << 1 | r2;
+  } else {
+    if constexpr (N >= 16) return r & 15;
+    else return (r & 7) ^ r3;
+  }
+}
+template <typename IO, int N>
+__device__ __forceinline__ int lane_base(int i, int j) {
+  return 16 * (N * i + (j ^ swz<IO, N>(i)));
 }
 
 template <typename IO>
@@ -86,54 +100,78 @@ __device__ __forceinline__ f32x4 mma(const uint4& a, const uint4& b, f32x4 acc) 
   }
 }
 
-// 16 bytes of row r, k = KS s + E g ..
+// Row 16 R + li, k = KS s + E g .. (16 bytes); base = lane_base(li, g).
 template <int N>
-__device__ __forceinline__ uint4 frag_row(const char* tile, int r, int s, int g) {
-  return *reinterpret_cast<const uint4*>(tile + (r * N + swz<N>(r, 4 * s + g)) * 16);
+__device__ __forceinline__ uint4 frag_row(const char* tile, int base, int R, int s) {
+  return *reinterpret_cast<const uint4*>(tile + ((base ^ (64 * s)) + 256 * N * R));
 }
 
-// row r, k = 32 s + 4 g .. + 3 and 32 s + 16 + 4 g .. + 3 (bfloat16): the order
-// in which two 16-row accumulator tiles hold their rows
-template <int N>
-__device__ __forceinline__ uint4 frag_acc_order(const char* tile, int r, int s, int g) {
-  const int u0 = 8 * s + g, u1 = u0 + 4;
-  const uint2 a = *reinterpret_cast<const uint2*>(tile + (r * N + swz<N>(r, u0 >> 1)) * 16 + (u0 & 1) * 8);
-  const uint2 b = *reinterpret_cast<const uint2*>(tile + (r * N + swz<N>(r, u1 >> 1)) * 16 + (u1 & 1) * 8);
-  return make_uint4(a.x, a.y, b.x, b.y);
+// Rows of the state.  An operand read gives lane group g the k of E g .. of a
+// step; the accumulator tiles hold four rows a group each.  With float32 that
+// is the same; with bfloat16 the two tiles of a step hold rows 8 g .. + 3 and
+// 8 g + 4 .. + 7 of its 32, so that they are its operand as they stand.
+template <typename IO>
+__device__ __forceinline__ constexpr int state_row(int rt, int g, int v) {
+  return HeadCfg<IO>::ES == 2 ? 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + v : 16 * rt + 4 * g + v;
 }
 
-// column 16 ct + (lane & 15) of the tile, k = rows KS s + E g .. (transposed read)
+// Transposed reads: for k = rows KS s + E g .. of a tile, one column a lane.
+// frag_col: column 16 ct + li.  frag_state_col: the column that is row li of
+// accumulator tile rt (state_row).  bfloat16: the transposing read takes four
+// columns of four rows from every group of 16 lanes (rows 8 g + li / 4, then
+// those four further on), lane li % 4 naming the columns.
 template <typename IO, int N>
-__device__ __forceinline__ uint4 frag_col(const char* tile, int ct, int s, int lane) {
-  const int g = lane >> 4;
+__device__ __forceinline__ int col_base(int li, int g) {
   if constexpr (HeadCfg<IO>::ES == 2) {
-    const int i = lane & 15, r = 32 * s + 8 * g + (i >> 2), u = 4 * ct + (i & 3);
-    const char* p0 = tile + (r * N + swz<N>(r, u >> 1)) * 16 + (u & 1) * 8;
-    const char* p1 = tile + ((r + 4) * N + swz<N>(r + 4, u >> 1)) * 16 + (u & 1) * 8;
+    const int r = 8 * g + (li >> 2);
+    return 16 * (N * r + (((li & 3) >> 1) ^ swz<IO, N>(r))) + 8 * (li & 1);
+  } else {
+    return 16 * (N * 4 * g + ((li >> 2) ^ swz<IO, N>(4 * g))) + 4 * (li & 3);
+  }
+}
+template <typename IO, int N>
+__device__ __forceinline__ int state_col_base(int li, int g) {
+  if constexpr (HeadCfg<IO>::ES == 2) return lane_base<IO, N>(8 * g + (li >> 2), li & 3);
+  else return col_base<IO, N>(li, g);
+}
+// `flip`: 16-byte chunk that the constant part of the columns adds
+template <typename IO, int N>
+__device__ __forceinline__ uint4 frag_transposed(const char* tile, int base, int flip, int s) {
+  if constexpr (HeadCfg<IO>::ES == 2) {
+    const char* p0 = tile + ((base ^ (16 * flip)) + 16 * N * 32 * s);
+    const char* p1 = tile + ((base ^ (16 * (flip ^ swz<IO, N>(4)))) + 16 * N * (32 * s + 4));
     const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)p0));
     const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)p1));
     return make_uint4(a.x, a.y, b.x, b.y);
   } else {
-    const int c = 16 * ct + (lane & 15), r = 16 * s + 4 * g;
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      w[e] = *reinterpret_cast<const uint32_t*>(tile + ((r + e) * N + swz<N>(r + e, c >> 2)) * 16 + (c & 3) * 4);
+      w[e] = *reinterpret_cast<const uint32_t*>(tile + ((base ^ (16 * (flip ^ swz<IO, N>(e)))) + 16 * N * (16 * s + e)));
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
+template <typename IO, int N>
+__device__ __forceinline__ uint4 frag_col(const char* tile, int base, int ct, int s) {
+  return frag_transposed<IO, N>(tile, base, HeadCfg<IO>::ES == 2 ? 2 * ct : 4 * ct, s);
+}
+template <typename IO, int N>
+__device__ __forceinline__ uint4 frag_state_col(const char* tile, int base, int rt, int s) {
+  if constexpr (HeadCfg<IO>::ES == 2) return frag_transposed<IO, N>(tile, base + 8 * (rt & 1), 4 * (rt >> 1), s);
+  else return frag_transposed<IO, N>(tile, base, 4 * rt, s);
+}
 
-// The lane's place, opaque to the compiler: addresses and bounds derived from
-// it are worked out where they are used.  Derived from threadIdx they are all
-// loop invariants (or common to prologue and epilogue) and kept in registers
-// across the loop, which then spills (measured: 40 to 400 spilled registers).
+// A lane's place or base address, opaque to the compiler: what is derived from
+// it is worked out where it is used.  Derived from threadIdx, every LDS address
+// is a loop invariant (or common to prologue and epilogue) and is kept in a
+// register across the loop, which then spills (measured: 40 to 400 registers).
 __device__ __forceinline__ int opaque(int v) {
   asm volatile("" : "+v"(v));
   return v;
 }
 
-// 8 values as a sum of bfloat16 parts: hi takes the leading 8 bits; what is
-// left stays in v
+// 8 values as a sum of bfloat16 parts: returns the leading 8 bits; what is
+// left stays in v (exact).
 __device__ __forceinline__ uint4 take_bf16(float (&v)[8]) {
   uint32_t w[4];
 #pragma unroll
@@ -143,6 +181,36 @@ __device__ __forceinline__ uint4 take_bf16(float (&v)[8]) {
     v[2 * e + 1] -= bf_hi(w[e]);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A value that is the same in every lane, for buffer resources: the compiler
+// clamps such values in a vector instruction and then takes them for divergent
+// (a loop over the lanes round every access).
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+// n rows of ts bytes, n clamped to 0 .. most
+__device__ __forceinline__ uint32_t row_bytes(int n, int most, uint32_t ts) {
+  return static_cast<uint32_t>(uniform(n < 0 ? 0 : (n < most ? n : most))) * ts;
+}
+
+// Running sum over the wavefront's 64 lanes as a pair of floats (hi, lo): a
+// two-sum at every step of a scan on cross-lane operands; lanes that a step
+// does not reach add zero.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ void scan_step(float& hi, float& lo) {
+  const float ph = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(hi), CTRL, ROWS, 0xf, false));
+  const float pl = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(lo), CTRL, ROWS, 0xf, false));
+  const float s = ph + hi, bb = s - ph;
+  lo = (pl + lo) + ((ph - (s - bb)) + (hi - bb));
+  hi = s;
+}
+__device__ __forceinline__ void scan_pair(float& hi, float& lo) {
+  lo = 0.f;
+  scan_step<0x111, 0xf>(hi, lo);  // one lane up within a row of 16
+  scan_step<0x112, 0xf>(hi, lo);
+  scan_step<0x114, 0xf>(hi, lo);
+  scan_step<0x118, 0xf>(hi, lo);
+  scan_step<0x142, 0xa>(hi, lo);  // the row before's total to rows 1 and 3
+  scan_step<0x143, 0xc>(hi, lo);  // the lower half's to rows 2 and 3
 }
 
 struct HeadDev {
@@ -170,9 +238,7 @@ struct HeadDev {
   int nch, cps, nseg, ntile;   // chunks, chunks per segment, segments, column tiles
   float ps, ss, us;
   int rev;                     // time reversed; a token's decay then acts on the step after it
-  int out_f32;                 // o is float32 whatever the storage type
   int end_decay;               // the last state is decayed by the first token's g
-  int vec_o;                   // four outputs of a row are one aligned store
 };
 
 // NaN stays NaN; -inf becomes kMinLog2Decay
@@ -193,24 +259,36 @@ __device__ __forceinline__ float decay_at(const HeadDev& p, int b, int h, int t)
   return clamp_decay(v * kLog2e);
 }
 
-// MODE: kOut writes o (and the last state), kState only the segment's own end
-// state (from zero, or from the start state for the first segment) and decay.
-constexpr int kOut = 0, kState = 1;
+// MODE: kOut writes o (and the last state), kOutF32 writes it in float32
+// whatever the storage type (per-head parts of a shared head's gradient),
+// kState only the segment's own end state (from zero, or from the start state
+// for the first segment) and decay.
+constexpr int kOut = 0, kState = 1, kOutF32 = 2;
 
 // Bytes of LDS: y and z tiles, x tile, scores (bfloat16: hi and lo), the
 // chunk's decays, and the wavefronts' dots.
-template <typename IO, int ROWS, int NW, int MODE, bool DOT>
+template <typename IO, int ROWS, int NW, int NC, int MODE, bool DOT>
 constexpr size_t head_lds_bytes() {
   using K = HeadCfg<IO>;
-  constexpr size_t xy = size_t(K::C) * ROWS * K::ES, z = size_t(K::C) * 16 * NW * K::ES;
+  constexpr size_t xy = size_t(K::C) * ROWS * K::ES, z = size_t(K::C) * 16 * NW * NC * K::ES;
   constexpr size_t sc = size_t(K::C) * K::C * K::ES * (K::ES == 2 ? 2 : 1);
-  return xy + z + 4 * K::C * 4 + (MODE == kOut ? xy + sc : 0) + (DOT ? size_t(NW) * K::C * 4 : 0);
+  return xy + z + 4 * K::C * 4 + (MODE != kState ? xy + sc : 0) + (DOT ? size_t(NW) * K::C * 4 : 0);
 }
 
-template <typename IO, int ROWS, int NW, int MODE, bool DOT, bool VEC>
-__global__ void __launch_bounds__(64 * NW, 2) ssm_head_kernel(const HeadDev p) {
+// Wavefronts per SIMD the registers have to leave room for: what fits without spills.
+template <typename IO, int ROWS, int NW, bool DOT, bool VEC>
+constexpr int head_waves() {
+  if (!VEC || ROWS == 256) return 2;
+  if (ROWS == 128) return HeadCfg<IO>::ES == 2 && !DOT ? (NW == 8 ? 4 : 3) : 2;
+  return 4;
+}
+
+template <typename IO, int ROWS, int NW, int NC, int MODE, bool DOT, bool VEC>
+__global__ void __launch_bounds__(64 * NW, (head_waves<IO, ROWS, NW, DOT, VEC>())) ssm_head_kernel(const HeadDev p) {
   using K = HeadCfg<IO>;
-  constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
+  constexpr bool F32OUT = K::ES == 4 || MODE == kOutF32;
+  constexpr int OES = F32OUT ? 4 : 2;  // bytes per output
+  constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW * NC;
   constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;  // 16-byte chunks per LDS row
   constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
   // 16-byte chunks per thread and tile; a small tile leaves threads without one
@@ -232,13 +310,19 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_head_kernel(const HeadDev p) {
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  // XCD-contiguous order, column tiles fastest: tiles that share x and y share an L2
+  // Workgroups go to the 8 XCDs in turn.  The column tiles of a (batch row, head, segment), which share x and y, stay
+  // on one XCD and follow each other there; the heads and batch rows are dealt out in turn, so that rows of different
+  // lengths load the XCDs alike.
   int ct, seg, h, b;
   {
-    const uint32_t G = gridDim.x, pid = blockIdx.x, q8 = G / 8, r8 = G % 8, xcd = pid % 8;
-    uint32_t idx = xcd * q8 + (xcd < r8 ? xcd : r8) + pid / 8;
-    ct = idx % p.ntile;
-    idx /= p.ntile;
+    const uint32_t pid = blockIdx.x, nt = p.ntile, whole = gridDim.x / nt / 8 * 8 * nt;
+    uint32_t idx = pid / nt;
+    ct = pid % nt;
+    if (pid < whole) {
+      const uint32_t slot = pid / 8;
+      idx = slot / nt * 8 + pid % 8;
+      ct = slot % nt;
+    }
     const uint32_t nrun = MODE == kState ? p.nseg - 1 : p.nseg;
     seg = idx % nrun;
     idx /= nrun;
@@ -252,27 +336,27 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_head_kernel(const HeadDev p) {
     const int n = p.lengths[b];
     len = n < 0 ? 0 : (n < p.L ? n : p.L);
   }
-  const int col0 = ct * COLS, cw = col0 + wave * 16;
+  const int col0 = ct * COLS, cw = col0 + wave * 16 * NC;
   const int64_t bh = static_cast<int64_t>(b) * p.H + h, ssize = static_cast<int64_t>(p.rows) * p.cols;
 
-  // ---- the state: lane holds rows 16 rt + 4 g + v, column cw + li
-  f32x4 S[RT];
+  // ---- the state: lane holds rows state_row(rt, g, v), columns cw + 16 nc + li
+  f32x4 S[RT][NC];
   {
     const float* src = nullptr;
     if (seg == 0) {
       if (p.h0 != nullptr) src = p.h0 + bh * ssize;
-    } else if (MODE == kOut) {
+    } else if (MODE != kState) {
       src = p.seg_state + (bh * p.nseg + (p.rev ? pseg + 1 : pseg - 1)) * ssize;
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int r = 16 * rt + 4 * ((tid & 63) >> 4) + v, c = cw + (tid & 15);
-        S[rt][v] = src != nullptr && r < p.rows && c < p.cols ? src[r * p.s_r + c * p.s_c] : 0.f;
+      for (int i = 0; i < 4 * NC; ++i) {
+        const int nc = i / 4, v = i % 4, r = state_row<IO>(rt, (tid & 63) >> 4, v), c = cw + 16 * nc + (tid & 15);
+        S[rt][nc][v] = src != nullptr && r < p.rows && c < p.cols ? src[r * p.s_r + c * p.s_c] : 0.f;
       }
   }
-  if constexpr (MODE == kOut) {
+  if constexpr (MODE != kState) {
     // the score tiles above the diagonal that a product step covers are never written again
     for (int i = tid; i < (ES == 2 ? 2 : 1) * C * C * ES / 16; i += T)
       reinterpret_cast<uint4*>(tp)[i] = make_uint4(0, 0, 0, 0);
@@ -282,26 +366,24 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_head_kernel(const HeadDev p) {
   const char* const yb = p.y + b * p.y_b + static_cast<int64_t>(h / p.y_rep) * p.rows * ES;
   const char* const zb = p.z + b * p.z_b + static_cast<int64_t>(h / p.z_rep) * p.cols * ES;
 
-  // one [C][N 16-byte chunks] tile of tokens t0 .. (those below len; the rest zero) into registers: `width` values
-  // of a token from value w0 on
-  auto load_tile = [&](const char* base, uint32_t ts, int width, int w0, int t0, auto nchunk, uint4* reg, auto count) {
-    constexpr int N = decltype(nchunk)::value, CNT = decltype(count)::value;
-    const Rsrc r = make_rsrc(base + static_cast<int64_t>(t0) * ts, 0x7fffffffu);
-    const int live = len - t0;  // rows
-    const int me = opaque(threadIdx.x);
+  // Staging.  Thread t holds the 16-byte chunk t % N of rows t / N + i T / N of a [C][N chunks] tile, i counted
+  // backwards when the time is reversed, so that register i always goes to the same place after register i - 1.  A
+  // resource of its own for every i bounds the rows by the length: what is past it reads zero.
+  auto load_tile = [&](const char* base, uint32_t ts, uint32_t voff, int left, int t0, auto nchunk, uint4* reg,
+                       auto count) {
+    constexpr int N = decltype(nchunk)::value, CNT = decltype(count)::value, STEP = T / N;
 #pragma unroll
     for (int i = 0; i < CNT; ++i) {
-      const int id = me + T * i, row = id / N, c = w0 + id % N * E;
-      const uint32_t off = static_cast<uint32_t>(row) * ts + static_cast<uint32_t>(c * ES);
-      const int lim = row < live ? (C * N % T != 0 && row >= C ? 0 : width) : 0;
+      const int r0 = STEP * (p.rev ? CNT - 1 - i : i);
+      const Rsrc r = make_rsrc(base + static_cast<int64_t>(t0 + r0) * ts, row_bytes(len - t0 - r0, C, ts));
       if constexpr (VEC) {
-        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, c < lim ? off : kOOB, 0, 0);
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, left > 0 ? voff : kOOB, 0, 0);
         reg[i] = make_uint4(v.x, v.y, v.z, v.w);
       } else {
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const uint32_t oe = c + e < lim ? off + e * ES : kOOB;
+          const uint32_t oe = e < left ? voff + e * ES : kOOB;
           if constexpr (ES == 4) {
             w[e] = __builtin_amdgcn_raw_buffer_load_b32(r, oe, 0, 0);
           } else {
@@ -313,238 +395,311 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_head_kernel(const HeadDev p) {
       }
     }
   };
-  auto store_tile = [&](char* tile, auto nchunk, const uint4* reg, auto count) {
-    constexpr int N = decltype(nchunk)::value, CNT = decltype(count)::value;
-    const int me = opaque(threadIdx.x);
+  auto store_tile = [&](char* tile, int row, int ch, auto nchunk, const uint4* reg, auto count) {
+    constexpr int N = decltype(nchunk)::value, CNT = decltype(count)::value, STEP = T / N;
 #pragma unroll
     for (int i = 0; i < CNT; ++i) {
-      const int id = me + T * i, ph = id / N;
-      if (C * N % T != 0 && ph >= C) break;
-      const int row = p.rev ? C - 1 - ph : ph;
-      *reinterpret_cast<uint4*>(tile + (row * N + swz<N>(row, id % N)) * 16) = reg[i];
+      const int r = row + STEP * i;
+      *reinterpret_cast<uint4*>(tile + 16 * (N * r + (ch ^ swz<IO, N>(STEP % 16 == 0 ? row : r)))) = reg[i];
     }
   };
   using KN = std::integral_constant<int, NK>;
   using ZN = std::integral_constant<int, NZ>;
   using XC = std::integral_constant<int, LX>;
   using ZC = std::integral_constant<int, LZ>;
+  // this thread's chunk and first row of the x and y tiles and of the z tile; threads past a small tile have none
+  const int kr = tid / NK, kc = tid % NK, zr = tid / NZ, zc = tid % NZ;
+  const int left_k = C * NK % T == 0 || kr < C ? p.rows - kc * E : 0, left_z = p.cols - col0 - zc * E;
+  const uint32_t vx = kr * p.x_t + kc * 16, vy = kr * p.y_t + kc * 16, vz = zr * p.z_t + (col0 + zc * E) * ES;
 
   float seg_dec = 1.f;
   uint4 rx[LX], ry[LX], rz[LZ];
-  float rg = 0.f;
+  // The decay that acts on logical row `lane` of a chunk (reversed: that of the token after it), as stored; nothing
+  // past the length.  Asked for by every wavefront and first, so that no branch and no later load is waited for with
+  // it; scanned by the wavefront with the fewest score tiles, ahead of the barrier.
+  uint32_t raw_g = 0;
+  float rg = 0.f, rlo = 0.f;
+  const char* const gb = p.g != nullptr ? p.g + (static_cast<int64_t>(b) * p.L * p.H + h) * ES : p.y;
+  const uint32_t g_t = p.g != nullptr ? p.H * ES : 0;
+  const float fixed = p.g == nullptr && p.g_head != nullptr ? clamp_decay(p.g_head[h] * kLog2e) : 0.f;
+  auto scan_decay = [&](int pc) {
+    if (wave != NW - 1) return;
+    if (p.g != nullptr)
+      rg = clamp_decay((ES == 2 ? __uint_as_float(raw_g << 16) : __uint_as_float(raw_g)) * kLog2e);
+    else
+      rg = (tid & 63) < C && pc * C + (p.rev ? C - (tid & 63) : tid & 63) < len ? fixed : 0.f;
+    scan_pair(rg, rlo);
+  };
   auto load_chunk = [&](int pc) {
     const int t0 = pc * C;
-    if constexpr (MODE == kOut) load_tile(xb, p.x_t, p.rows, 0, t0, KN{}, rx, XC{});
-    load_tile(yb, p.y_t, p.rows, 0, t0, KN{}, ry, XC{});
-    load_tile(zb, p.z_t, p.cols, col0, t0, ZN{}, rz, ZC{});
-    if (wave == NW - 1) {
-      // the decay that acts on logical row `lane` of the chunk
-      rg = 0.f;
-      const int lane = tid & 63;
-      if (lane < C) {
-        const int t = p.rev ? t0 + C - lane : t0 + lane;  // reversed: the token after it
-        if (t < len) rg = decay_at<IO>(p, b, h, t);
+    {
+      const Rsrc r = make_rsrc(gb + static_cast<int64_t>(t0) * g_t, row_bytes(len - t0, C + 1, g_t));
+      const int lane = opaque(tid) & 63;
+      const uint32_t off = lane < C ? (p.rev ? C - lane : lane) * g_t : kOOB;
+      if constexpr (ES == 2) raw_g = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+      else raw_g = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+    }
+    if constexpr (MODE != kState) load_tile(xb, p.x_t, vx, left_k, t0, KN{}, rx, XC{});
+    load_tile(yb, p.y_t, vy, left_k, t0, KN{}, ry, XC{});
+    load_tile(zb, p.z_t, vz, left_z, t0, ZN{}, rz, ZC{});
+  };
+
+  // One chunk's outputs (physical chunk at t0; nothing is written with rows = 0), columns cw + 16 nc + 4 g + v
+  auto store_out = [&](const f32x4 (&O)[IB][NC], int t0, int rows, int li, int g) {
+    const int lr = p.rev ? 15 - li : li;  // the lane's token in its block of 16
+    const uint32_t ts = static_cast<uint32_t>(p.H * p.cols * OES);
+    const char* const ob = p.o + ((static_cast<int64_t>(b) * p.L + t0) * p.H + h) * p.cols * OES;
+#pragma unroll
+    for (int ib = 0; ib < IB; ++ib) {
+      const int r0 = 16 * (p.rev ? IB - 1 - ib : ib);
+      const Rsrc ro = make_rsrc(ob + static_cast<int64_t>(r0) * ts, row_bytes(rows - r0, 16, ts));
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) {
+        const int c = cw + 16 * nc + 4 * g;
+        const uint32_t off = lr * ts + static_cast<uint32_t>(c * OES);
+        const f32x4 v = O[ib][nc];
+        if constexpr (VEC) {
+          const uint32_t to = c < p.cols ? off : kOOB;
+          if constexpr (F32OUT) {
+            u32x4 w;
+            w.x = __float_as_uint(v[0]); w.y = __float_as_uint(v[1]);
+            w.z = __float_as_uint(v[2]); w.w = __float_as_uint(v[3]);
+            __builtin_amdgcn_raw_buffer_store_b128(w, ro, to, 0, 0);
+          } else {
+            u32x2 w;
+            w.x = BF16::cvt2(v[0], v[1]);
+            w.y = BF16::cvt2(v[2], v[3]);
+            __builtin_amdgcn_raw_buffer_store_b64(w, ro, to, 0, 0);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t to = c + e < p.cols ? off + e * OES : kOOB;
+            if constexpr (F32OUT)
+              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), ro, to, 0, 0);
+            else
+              __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(BF16::cvt(v[e])), ro, to, 0, 0);
+          }
+        }
       }
     }
   };
 
-  const int n = c1 - c0;
-  if (n > 0) load_chunk(p.rev ? c1 - 1 : c0);
+  // chunks wholly past the length leave the state alone (their rows are zeroed at the end): they come last forwards,
+  // first backwards
+  const int cl = (len + C - 1) / C, ce = c1 < cl ? c1 : cl, n = ce - c0;
+  if (n > 0) {
+    load_chunk(p.rev ? ce - 1 : c0);
+    scan_decay(p.rev ? ce - 1 : c0);
+    if constexpr (MODE != kState) {
+      // Loads and stores are counted together and in order.  With as many stores behind the first loads as the loop
+      // has behind its own (these write nothing), the wait for a chunk's loads leaves the stores behind them in
+      // flight on either way into the loop; without them it waits for every store to arrive.
+      const f32x4 none[IB][NC] = {};
+      store_out(none, 0, 0, tid & 15, (tid & 63) >> 4);
+    }
+  }
   for (int k = 0; k < n; ++k) {
-    const int pc = p.rev ? c1 - 1 - k : c0 + k, t0 = pc * C;
-    const int lane = opaque(tid) & 63, g = lane >> 4, li = lane & 15;
+    const int pc = p.rev ? ce - 1 - k : c0 + k, t0 = pc * C;
     __syncthreads();  // the chunk before is done with the tiles
-    if constexpr (MODE == kOut) store_tile(tx, KN{}, rx, XC{});
-    store_tile(ty, KN{}, ry, XC{});
-    store_tile(tz, ZN{}, rz, ZC{});
-    if (wave == NW - 1) {
-      // running sum over the chunk as a pair of floats (two-sum at every step)
-      const int lane = tid & 63;
-      float hi = rg, lo = 0.f;
-#pragma unroll
-      for (int d = 1; d < C; d *= 2) {
-        const float ph = __shfl_up(hi, d), pl = __shfl_up(lo, d);
-        if (lane >= d) {
-          const float s = ph + hi, bb = s - ph;
-          lo = (pl + lo) + ((ph - (s - bb)) + (hi - bb));
-          hi = s;
-        }
+    {
+      const int me = opaque(tid), rk = me / NK, rz0 = me / NZ;
+      const int kl = p.rev ? C - 1 - rk - (T / NK) * (LX - 1) : rk;   // logical row of register 0
+      const int zl = p.rev ? C - 1 - rz0 - (T / NZ) * (LZ - 1) : rz0;
+      if (C * NK % T == 0 || rk < C) {
+        if constexpr (MODE != kState) store_tile(tx, kl, me % NK, KN{}, rx, XC{});
+        store_tile(ty, kl, me % NK, KN{}, ry, XC{});
       }
-      const float eh = __shfl(hi, C - 1), el = __shfl(lo, C - 1);
+      store_tile(tz, zl, me % NZ, ZN{}, rz, ZC{});
+    }
+    if (wave == NW - 1) {
+      const float eh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(rg), C - 1));
+      const float el = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(rlo), C - 1));
+      const int lane = tid & 63;
       if (lane < C) {
-        ghi[lane] = hi;
-        glo[lane] = lo;
-        eg[lane] = p.ss * __builtin_amdgcn_exp2f(hi + lo);
-        we[lane] = p.us * __builtin_amdgcn_exp2f((eh - hi) + (el - lo));
+        ghi[lane] = rg;
+        glo[lane] = rlo;
+        eg[lane] = p.ss * __builtin_amdgcn_exp2f(rg + rlo);
+        we[lane] = p.us * __builtin_amdgcn_exp2f((eh - rg) + (el - rlo));
       }
     }
     __syncthreads();
     const float end_dec = __builtin_amdgcn_exp2f(ghi[C - 1] + glo[C - 1]);
     if constexpr (MODE == kState) seg_dec *= end_dec;
-    if (k + 1 < n) load_chunk(p.rev ? pc - 1 : pc + 1);
 
-    f32x4 O[IB];  // transposed: lane holds columns cw + 4 g + v of logical token 16 ib + li
-    if constexpr (MODE == kOut) {
+    const int lane = opaque(tid) & 63, g = lane >> 4, li = lane & 15;
+    f32x4 O[IB][NC];  // transposed: lane holds columns cw + 16 nc + 4 g + v of logical token 16 ib + li
+    if constexpr (MODE != kState) {
       // ---- scores, 16 x 16 tiles on and below the diagonal dealt to the wavefronts: lane holds j = 4 g + v of i = li
-#pragma unroll
-      for (int tile = 0; tile < IB * (IB + 1) / 2; ++tile) {
-        if (tile % NW != wave) continue;
-        int ib = 0, jb = tile;
-#pragma unroll
-        for (int q = 0; q < IB; ++q)
-          if (jb > ib) {
-            jb -= ib + 1;
-            ++ib;
-          }
+      const int rb = lane_base<IO, NK>(li, g);
+      for (int tile = wave; tile < IB * (IB + 1) / 2; tile += NW) {
+        const int ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6), jb = tile - ib * (ib + 1) / 2;
         const int i = 16 * ib + li, j0 = 16 * jb + 4 * g;
         f32x4 a = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < RS; ++s) a = mma<IO>(frag_row<NK>(ty, 16 * jb + li, s, g), frag_row<NK>(tx, i, s, g), a);
+        for (int s = 0; s < RS; ++s) a = mma<IO>(frag_row<NK>(ty, rb, jb, s), frag_row<NK>(tx, rb, ib, s), a);
         const float gi = ghi[i], gl = glo[i];
+        const float4 gj = *reinterpret_cast<const float4*>(ghi + j0), gk = *reinterpret_cast<const float4*>(glo + j0);
         float w[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const float d = __builtin_amdgcn_exp2f((gi - ghi[j0 + v]) + (gl - glo[j0 + v]));
+          const float d = __builtin_amdgcn_exp2f((gi - get(gj, v)) + (gl - get(gk, v)));
           w[v] = j0 + v <= i ? p.ps * d * a[v] : 0.f;
         }
         if constexpr (ES == 2) {
           const int u = 4 * jb + g;
-          const int at = (i * NP + swz<NP>(i, u >> 1)) * 16 + (u & 1) * 8;
+          const int to = (i * NP + ((u >> 1) ^ swz<IO, NP>(i))) * 16 + (u & 1) * 8;
           const uint2 hi2 = make_uint2(BF16::cvt2(w[0], w[1]), BF16::cvt2(w[2], w[3]));
-          *reinterpret_cast<uint2*>(tp + at) = hi2;
-          *reinterpret_cast<uint2*>(tpl + at) = make_uint2(BF16::cvt2(w[0] - bf_lo(hi2.x), w[1] - bf_hi(hi2.x)),
+          *reinterpret_cast<uint2*>(tp + to) = hi2;
+          *reinterpret_cast<uint2*>(tpl + to) = make_uint2(BF16::cvt2(w[0] - bf_lo(hi2.x), w[1] - bf_hi(hi2.x)),
                                                            BF16::cvt2(w[2] - bf_lo(hi2.y), w[3] - bf_hi(hi2.y)));
         } else {
-          *reinterpret_cast<float4*>(tp + (i * NP + swz<NP>(i, 4 * jb + g)) * 16) = make_float4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<float4*>(tp + (i * NP + ((4 * jb + g) ^ swz<IO, NP>(i))) * 16) = make_float4(w[0], w[1], w[2], w[3]);
         }
       }
       // ---- what the state before the chunk gives
 #pragma unroll
-      for (int ib = 0; ib < IB; ++ib) O[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int ib = 0; ib < IB; ++ib)
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) O[ib][nc] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int ab = opaque(rb);
 #pragma unroll
       for (int s = 0; s < RS; ++s) {
-        if constexpr (ES == 2) {
-          float v[8];
+        uint4 hi[NC], lo[NC];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = S[2 * s + (e >> 2)][e & 3];
-          const uint4 hi = take_bf16(v), lo = take_bf16(v);
+        for (int nc = 0; nc < NC; ++nc) {
+          if constexpr (ES == 2) {
+            float v[8];
 #pragma unroll
-          for (int ib = 0; ib < IB; ++ib) {
-            const uint4 fx = frag_acc_order<NK>(tx, 16 * ib + li, s, g);
-            O[ib] = mma<IO>(hi, fx, O[ib]);
-            O[ib] = mma<IO>(lo, fx, O[ib]);
+            for (int e = 0; e < 8; ++e) v[e] = S[2 * s + (e >> 2)][nc][e & 3];
+            hi[nc] = take_bf16(v);
+            lo[nc] = take_bf16(v);
+          } else {
+            hi[nc] = __builtin_bit_cast(uint4, S[s][nc]);
           }
-        } else {
+        }
 #pragma unroll
-          for (int ib = 0; ib < IB; ++ib)
-            O[ib] = mma<IO>(__builtin_bit_cast(uint4, S[s]), frag_row<NK>(tx, 16 * ib + li, s, g), O[ib]);
+        for (int ib = 0; ib < IB; ++ib) {
+          const uint4 fx = frag_row<NK>(tx, ab, ib, s);
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) {
+            O[ib][nc] = mma<IO>(hi[nc], fx, O[ib][nc]);
+            if constexpr (ES == 2) O[ib][nc] = mma<IO>(lo[nc], fx, O[ib][nc]);
+          }
         }
       }
 #pragma unroll
-      for (int ib = 0; ib < IB; ++ib) O[ib] *= eg[16 * ib + li];
+      for (int ib = 0; ib < IB; ++ib) {
+        const float e = eg[16 * ib + li];
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) O[ib][nc] *= e;
+      }
       __syncthreads();  // scores
     }
+    if (k + 1 < n) load_chunk(p.rev ? pc - 1 : pc + 1);
 
     // ---- z as an operand: column li, tokens KS js + E g ..
-    uint4 fz[JS];
+    uint4 fz[JS][NC];
+    const int zb0 = opaque(col_base<IO, NZ>(li, g));
 #pragma unroll
-    for (int js = 0; js < JS; ++js) fz[js] = frag_col<IO, NZ>(tz, wave, js, lane);
+    for (int js = 0; js < JS; ++js)
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) fz[js][nc] = frag_col<IO, NZ>(tz, zb0, wave * NC + nc, js);
 
-    if constexpr (MODE == kOut) {
+    if constexpr (MODE != kState) {
+      const int pb = opaque(lane_base<IO, NP>(li, g));
 #pragma unroll
       for (int ib = 0; ib < IB; ++ib)
 #pragma unroll
         for (int js = 0; js * KS < 16 * (ib + 1); ++js) {
-          O[ib] = mma<IO>(fz[js], frag_row<NP>(tp, 16 * ib + li, js, g), O[ib]);
-          if constexpr (ES == 2) O[ib] = mma<IO>(fz[js], frag_row<NP>(tpl, 16 * ib + li, js, g), O[ib]);
+          const uint4 fp = frag_row<NP>(tp, pb, ib, js);
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) O[ib][nc] = mma<IO>(fz[js][nc], fp, O[ib][nc]);
+          if constexpr (ES == 2) {
+            const uint4 fl = frag_row<NP>(tpl, pb, ib, js);
+#pragma unroll
+            for (int nc = 0; nc < NC; ++nc) O[ib][nc] = mma<IO>(fz[js][nc], fl, O[ib][nc]);
+          }
         }
     }
 
     // ---- the state after the chunk
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) S[rt] *= end_dec;
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int nc = 0; nc < NC; ++nc) S[rt][nc] *= end_dec;
+    const int yb0 = opaque(state_col_base<IO, NK>(li, g));
 #pragma unroll
     for (int js = 0; js < JS; ++js) {
       float w[E];
+      F32::ld<E>(we + KS * js + E * g, w);
+      constexpr int TERMS = ES == 2 ? 3 : 1;
+      uint4 hz[NC][TERMS];
 #pragma unroll
-      for (int e = 0; e < E; ++e) w[e] = we[KS * js + E * g + e];
-      if constexpr (ES == 2) {
-        float v[8];
-        const uint32_t* pw = reinterpret_cast<const uint32_t*>(&fz[js]);
+      for (int nc = 0; nc < NC; ++nc) {
+        if constexpr (ES == 2) {
+          float v[8];
+          const uint32_t* pw = reinterpret_cast<const uint32_t*>(&fz[js][nc]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = w[e] * (e & 1 ? bf_hi(pw[e >> 1]) : bf_lo(pw[e >> 1]));
-        const uint4 hi = take_bf16(v), mid = take_bf16(v), lo = take_bf16(v);
+          for (int e = 0; e < 8; ++e) v[e] = w[e] * (e & 1 ? bf_hi(pw[e >> 1]) : bf_lo(pw[e >> 1]));
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const uint4 fy = frag_col<IO, NK>(ty, rt, js, lane);
-          S[rt] = mma<IO>(fy, hi, S[rt]);
-          S[rt] = mma<IO>(fy, mid, S[rt]);
-          S[rt] = mma<IO>(fy, lo, S[rt]);
+          for (int q = 0; q < TERMS; ++q) hz[nc][q] = take_bf16(v);
+        } else {
+          const float* pf = reinterpret_cast<const float*>(&fz[js][nc]);
+          const float4 v = make_float4(w[0] * pf[0], w[1] * pf[1], w[2] * pf[2], w[3] * pf[3]);
+          hz[nc][0] = __builtin_bit_cast(uint4, v);
         }
-      } else {
-        const float* pf = reinterpret_cast<const float*>(&fz[js]);
-        const float4 v = make_float4(w[0] * pf[0], w[1] * pf[1], w[2] * pf[2], w[3] * pf[3]);
-        const uint4 hz = __builtin_bit_cast(uint4, v);
+      }
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) S[rt] = mma<IO>(frag_col<IO, NK>(ty, rt, js, lane), hz, S[rt]);
+      for (int rt = 0; rt < RT; ++rt) {
+        const uint4 fy = frag_state_col<IO, NK>(ty, yb0, rt, js);
+#pragma unroll
+        for (int q = 0; q < TERMS; ++q)
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) S[rt][nc] = mma<IO>(fy, hz[nc][q], S[rt][nc]);
       }
     }
 
+    if (k + 1 < n) scan_decay(p.rev ? pc - 1 : pc + 1);
+
     // ---- outputs, zero in rows past the length
-    if constexpr (MODE == kOut) {
-      const int oes = p.out_f32 ? 4 : ES;
-      const uint32_t ts = static_cast<uint32_t>(p.H * p.cols * oes);
-      const Rsrc ro = make_rsrc(p.o + ((static_cast<int64_t>(b) * p.L + t0) * p.H + h) * p.cols * oes, 0x7fffffffu);
-      const int c = cw + 4 * g;
+    if constexpr (MODE != kState) {
+      const int lr = p.rev ? 15 - li : li;  // the lane's token in physical block pb
+      if (t0 + C > len) {
 #pragma unroll
-      for (int ib = 0; ib < IB; ++ib) {
-        const int i = 16 * ib + li, ph = p.rev ? C - 1 - i : i;
-        const bool ok = t0 + ph < p.L, live = t0 + ph < len;
-        const f32x4 v = live ? O[ib] : f32x4{0.f, 0.f, 0.f, 0.f};
-        const uint32_t off = static_cast<uint32_t>(ph) * ts + static_cast<uint32_t>(c * oes);
-        if (p.vec_o) {
-          const uint32_t at = ok && c < p.cols ? off : kOOB;
-          if (ES == 4 || p.out_f32) {
-            u32x4 w;
-            w.x = __float_as_uint(v[0]); w.y = __float_as_uint(v[1]);
-            w.z = __float_as_uint(v[2]); w.w = __float_as_uint(v[3]);
-            __builtin_amdgcn_raw_buffer_store_b128(w, ro, at, 0, 0);
-          } else {
-            u32x2 w;
-            w.x = BF16::cvt2(v[0], v[1]);
-            w.y = BF16::cvt2(v[2], v[3]);
-            __builtin_amdgcn_raw_buffer_store_b64(w, ro, at, 0, 0);
-          }
-        } else {
+        for (int ib = 0; ib < IB; ++ib)
+          if (t0 + 16 * (p.rev ? IB - 1 - ib : ib) + lr >= len) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t at = ok && c + e < p.cols ? off + e * oes : kOOB;
-            if (ES == 4 || p.out_f32)
-              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), ro, at, 0, 0);
-            else
-              __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(BF16::cvt(v[e])), ro, at, 0, 0);
+            for (int nc = 0; nc < NC; ++nc) O[ib][nc] = f32x4{0.f, 0.f, 0.f, 0.f};
           }
-        }
-        if constexpr (DOT) {
+      }
+      if constexpr (DOT) {
+#pragma unroll
+        for (int ib = 0; ib < IB; ++ib) {
+          const int r0 = 16 * (p.rev ? IB - 1 - ib : ib);
+          const Rsrc rd = make_rsrc(p.dotv + b * p.dot_b + static_cast<int64_t>(t0 + r0) * p.dot_t +
+                                        static_cast<int64_t>(h / p.dot_rep) * p.cols * ES, row_bytes(len - t0 - r0, 16, p.dot_t));
           float dot = 0.f;
-          const Rsrc rd = make_rsrc(p.dotv + b * p.dot_b + static_cast<int64_t>(t0) * p.dot_t +
-                                        static_cast<int64_t>(h / p.dot_rep) * p.cols * ES, 0x7fffffffu);
-          const uint32_t doff = static_cast<uint32_t>(ph) * p.dot_t + static_cast<uint32_t>(c * ES);
-          float d[4];
-          if constexpr (VEC) {
-            BufOf<IO>::type::template ld<4>(rd, live && c < p.cols ? doff : kOOB, d);
-          } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              BufOf<IO>::type::template ld<1>(rd, live && c + e < p.cols ? doff + e * ES : kOOB, d + e);
+          for (int nc = 0; nc < NC; ++nc) {
+            const int c = cw + 16 * nc + 4 * g;
+            const uint32_t off = lr * p.dot_t + static_cast<uint32_t>(c * ES);
+            float d[4];
+            if constexpr (VEC) {
+              BufOf<IO>::type::template ld<4>(rd, c < p.cols ? off : kOOB, d);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) BufOf<IO>::type::template ld<1>(rd, c + e < p.cols ? off + e * ES : kOOB, d + e);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(d[e], O[ib][nc][e], dot);
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dot = __builtin_fmaf(d[e], v[e], dot);
           dot += __shfl_xor(dot, 16);
           dot += __shfl_xor(dot, 32);
-          if (g == 0) red[wave * C + i] = dot;
+          if (g == 0) red[wave * C + 16 * ib + li] = dot;
         }
       }
+      store_out(O, t0, p.L - t0, li, g);
       if constexpr (DOT) {
         __syncthreads();
         if (tid < C) {
@@ -555,6 +710,19 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_head_kernel(const HeadDev p) {
           if (t < p.L) p.dot_out[(static_cast<int64_t>(ct) * p.batch * p.H + bh) * p.L + t] = sum;
         }
       }
+    }
+  }
+
+  if constexpr (MODE != kState) {
+    // outputs (and dots) of the chunks past the length
+    const int t1 = c1 * C < p.L ? c1 * C : p.L;
+    for (int t = (ce > c0 ? ce : c0) * C + wave; t < t1; t += NW) {
+      char* const row = p.o + ((static_cast<int64_t>(b) * p.L + t) * p.H + h) * p.cols * OES;
+      for (int c = col0 + (tid & 63); c < col0 + COLS && c < p.cols; c += 64) {
+        if constexpr (F32OUT) reinterpret_cast<float*>(row)[c] = 0.f;
+        else reinterpret_cast<uint16_t*>(row)[c] = 0;
+      }
+      if (DOT && (tid & 63) == 0) p.dot_out[(static_cast<int64_t>(ct) * p.batch * p.H + bh) * p.L + t] = 0.f;
     }
   }
 
@@ -573,19 +741,19 @@ __global__ void __launch_bounds__(64 * NW, 2) ssm_head_kernel(const HeadDev p) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int r = 16 * rt + 4 * g + v, c = cw + li;
-        if (r < p.rows && c < p.cols) dst[r * p.s_r + c * p.s_c] = dec * S[rt][v];
+      for (int i = 0; i < 4 * NC; ++i) {
+        const int nc = i / 4, v = i % 4, r = state_row<IO>(rt, g, v), c = cw + 16 * nc + li;
+        if (r < p.rows && c < p.cols) dst[r * p.s_r + c * p.s_c] = dec * S[rt][nc][v];
       }
   }
 }
 
-template <typename IO, int ROWS, int NW, int MODE, bool DOT, bool VEC>
+template <typename IO, int ROWS, int NW, int NC, int MODE, bool DOT, bool VEC>
 hipError_t launch_head_t(const HeadDev& p, hipStream_t st) {
   const int64_t nrun = MODE == kState ? p.nseg - 1 : p.nseg;
   const int64_t wgs = nrun * p.ntile * p.H * p.batch;
-  constexpr size_t smem = head_lds_bytes<IO, ROWS, NW, MODE, DOT>();
-  auto kern = ssm_head_kernel<IO, ROWS, NW, MODE, DOT, VEC>;
+  constexpr size_t smem = head_lds_bytes<IO, ROWS, NW, NC, MODE, DOT>();
+  auto kern = ssm_head_kernel<IO, ROWS, NW, NC, MODE, DOT, VEC>;
   if (smem > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -595,34 +763,38 @@ hipError_t launch_head_t(const HeadDev& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-// ROWS: rows rounded up to 32, 64, 128 or 256.  Eight wavefronts (128 columns)
-// only where every operand row is whole 16-byte vectors.
+// ROWS: rows rounded up to 32, 64, 128 or 256.  `wide` is a tile of 128
+// columns: two 16-column tiles for each of four wavefronts, or with 256 rows,
+// whose state then fills the registers, eight wavefronts of one.
 template <typename IO, int MODE, bool DOT, int ROWS>
-hipError_t launch_head_r(const HeadDev& p, int nw, bool vec, hipStream_t st) {
-  if (!vec) return launch_head_t<IO, ROWS, 4, MODE, DOT, false>(p, st);
-  if (nw == 8) return launch_head_t<IO, ROWS, 8, MODE, DOT, true>(p, st);
-  return launch_head_t<IO, ROWS, 4, MODE, DOT, true>(p, st);
+hipError_t launch_head_r(const HeadDev& p, bool wide, bool vec, hipStream_t st) {
+  if (!vec) return launch_head_t<IO, ROWS, 4, 1, MODE, DOT, false>(p, st);
+  if (wide) return launch_head_t<IO, ROWS, 8, 1, MODE, DOT, true>(p, st);
+  return launch_head_t<IO, ROWS, 4, 1, MODE, DOT, true>(p, st);
 }
 
 template <typename IO, int MODE, bool DOT>
-hipError_t launch_head_m(const HeadDev& p, int nw, bool vec, hipStream_t st) {
-  if (p.rows <= 32) return launch_head_r<IO, MODE, DOT, 32>(p, nw, vec, st);
-  if (p.rows <= 64) return launch_head_r<IO, MODE, DOT, 64>(p, nw, vec, st);
-  if (p.rows <= 128) return launch_head_r<IO, MODE, DOT, 128>(p, nw, vec, st);
-  return launch_head_r<IO, MODE, DOT, 256>(p, nw, vec, st);
+hipError_t launch_head_m(const HeadDev& p, bool wide, bool vec, hipStream_t st) {
+  if (p.rows <= 32) return launch_head_r<IO, MODE, DOT, 32>(p, wide, vec, st);
+  if (p.rows <= 64) return launch_head_r<IO, MODE, DOT, 64>(p, wide, vec, st);
+  if (p.rows <= 128) return launch_head_r<IO, MODE, DOT, 128>(p, wide, vec, st);
+  return launch_head_r<IO, MODE, DOT, 256>(p, wide, vec, st);
 }
 
-// One pass: mode kOut (with the dot if p.dotv is set) or kState.
+// One pass: mode kOut (with the dot if p.dotv is set), kOutF32 (with the dot) or kState.
 template <typename IO>
-hipError_t launch_head_io(const HeadDev& p, int mode, int nw, bool vec, hipStream_t st) {
-  if (mode == kState) return launch_head_m<IO, kState, false>(p, nw, vec, st);
-  if (p.dotv != nullptr) return launch_head_m<IO, kOut, true>(p, nw, vec, st);
-  return launch_head_m<IO, kOut, false>(p, nw, vec, st);
+hipError_t launch_head_io(const HeadDev& p, int mode, bool wide, bool vec, hipStream_t st) {
+  if (mode == kState) return launch_head_m<IO, kState, false>(p, wide, vec, st);
+  if constexpr (HeadCfg<IO>::ES == 2) {
+    if (mode == kOutF32) return launch_head_m<IO, kOutF32, true>(p, wide, vec, st);
+  }
+  if (p.dotv != nullptr) return launch_head_m<IO, kOut, true>(p, wide, vec, st);
+  return launch_head_m<IO, kOut, false>(p, wide, vec, st);
 }
 
 }  // namespace headk
 
-hipError_t launch_head_bf16(const headk::HeadDev& p, int mode, int nw, bool vec, hipStream_t st);
-hipError_t launch_head_f32(const headk::HeadDev& p, int mode, int nw, bool vec, hipStream_t st);
+hipError_t launch_head_bf16(const headk::HeadDev& p, int mode, bool wide, bool vec, hipStream_t st);
+hipError_t launch_head_f32(const headk::HeadDev& p, int mode, bool wide, bool vec, hipStream_t st);
 
 }  // namespace ssm
