@@ -11,6 +11,7 @@ CPU fallback: if the library is missing or no GPU is present the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -643,6 +644,42 @@ def ssm_out_proj_bwd(y: torch.Tensor, W: torch.Tensor, dout: torch.Tensor, want_
     return dy, dW
 
 
+# The single-token calls are bound by the host: what follows keeps the cost of a call low (a plain int for a pointer,
+# no device context where the device is current already, sizes asked for once).
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(device, fn, *args):
+    """fn(*args, the device's current stream) with the device current; raises on a status."""
+    if torch.cuda.current_device() == device.index:
+        stream = (torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device.index))
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != SSM_OK:
+        _check(rc)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(name: str, *sizes) -> int:
+    """What a ``*_workspace`` query of the library says for a size (it goes by the sizes alone)."""
+    n = ctypes.c_int64()
+    _check(getattr(load_library(), name)(*sizes, ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(name: str, device, *sizes):
+    """(device memory of the size that a ``*_workspace`` query names, its bytes); torch's allocator keeps it in stream
+    order."""
+    n = _workspace_bytes(name, *sizes)
+    return (torch.empty(n, device=device, dtype=torch.uint8), n) if n else (None, 0)
+
+
 def _head_operand(t: torch.Tensor, name: str, dtype, device, shape):
     """[b, L, heads, d], dense over a token's row; the strides of tokens and batch rows are the caller's."""
     if not isinstance(t, torch.Tensor):
@@ -651,14 +688,15 @@ def _head_operand(t: torch.Tensor, name: str, dtype, device, shape):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    h, d = shape[-2:]
-    if (d > 1 and t.stride(-1) != 1) or (h > 1 and t.stride(-2) != d):
+    b, L, h, d = shape
+    sb, st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError(f"{name} must be dense over a token's heads (only the strides of batch rows and tokens are free)")
     # a stride over a size of one addresses nothing
-    token = t.stride(1) if shape[1] > 1 else h * d
-    return _ptr(t), t.stride(0) if shape[0] > 1 else shape[1] * token, token
+    token = st if L > 1 else h * d
+    return t.data_ptr(), sb if b > 1 else L * token, token
 
 
 def _head_sizes(q: torch.Tensor, v: torch.Tensor, name: str, dims: int):
@@ -678,17 +716,6 @@ def _head_decay(g, g_head, shape, heads, dtype, device):
         _need(g, "g", dtype, device, shape)
     if g_head is not None:
         _need(g_head, "g_head", torch.float32, device, (heads,))
-
-
-def _workspace(query, device, *sizes) -> Optional[torch.Tensor]:
-    """Device memory of the size that a ``*_workspace`` query names (torch's allocator keeps it in stream order)."""
-    n = ctypes.c_int64()
-    _check(query(*sizes, ctypes.byref(n)))
-    return torch.empty(n.value, device=device, dtype=torch.uint8) if n.value else None
-
-
-def _bytes(ws: Optional[torch.Tensor]) -> int:
-    return 0 if ws is None else ws.numel()
 
 
 def ssm_head_scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor] = None,
@@ -717,21 +744,18 @@ def ssm_head_scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Opti
     if lengths is not None:
         _need(lengths, "lengths", torch.int32, device, (b,))
     if o is None:
-        o = torch.empty((b, L, h, dv), device=device, dtype=dt)
+        o = torch.empty_like(v, memory_format=torch.contiguous_format)
     else:
         _need(o, "o", dt, device, (b, L, h, dv))
     if last_state is not None:
         _need(last_state, "last_state", torch.float32, device, (b, h, dk, dv))
     elif return_last_state:
         last_state = torch.empty((b, h, dk, dv), device=device, dtype=torch.float32)
-    lib = load_library()
-    sizes, code = (b, L, h, hk, dk, dv), SSM_F32 if dt == torch.float32 else SSM_BF16
-    with torch.cuda.device(device):
-        ws = _workspace(lib.ssm_head_scan_workspace, device, *sizes, code, 0)
-        rc = lib.ssm_head_scan_fwd(*ops[0], *ops[1], *ops[2], _ptr(g), _ptr(g_head), _ptr(h0), _ptr(lengths),
-                                   dk ** -0.5 if scale is None else float(scale), _ptr(o), _ptr(last_state), _ptr(ws),
-                                   _bytes(ws), *sizes, code, _stream(device))
-    _check(rc)
+    code = SSM_F32 if dt == torch.float32 else SSM_BF16
+    ws, nws = _workspace("ssm_head_scan_workspace", device, b, L, h, hk, dk, dv, code, 0)
+    _call(device, load_library().ssm_head_scan_fwd, *ops[0], *ops[1], *ops[2], _addr(g), _addr(g_head), _addr(h0),
+          _addr(lengths), dk ** -0.5 if scale is None else float(scale), o.data_ptr(), _addr(last_state), _addr(ws), nws,
+          b, L, h, hk, dk, dv, code)
     return o, last_state
 
 
@@ -763,15 +787,11 @@ def ssm_head_scan_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, do: tor
         "dg": torch.empty((b, L, h), device=device, dtype=dt) if want_dg and g is not None else None,
         "dh0": torch.empty((b, h, dk, dv), device=device, dtype=torch.float32) if want_dh0 else None,
     }
-    lib = load_library()
-    sizes, code = (b, L, h, hk, dk, dv), SSM_F32 if dt == torch.float32 else SSM_BF16
-    with torch.cuda.device(device):
-        ws = _workspace(lib.ssm_head_scan_workspace, device, *sizes, code, 1)
-        rc = lib.ssm_head_scan_bwd(*ops[0], *ops[1], *ops[2], _ptr(g), _ptr(g_head), _ptr(h0), _ptr(lengths),
-                                   dk ** -0.5 if scale is None else float(scale), _ptr(do), _ptr(dlast), _ptr(out["dq"]),
-                                   _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dh0"]), _ptr(ws),
-                                   _bytes(ws), *sizes, code, _stream(device))
-    _check(rc)
+    code = SSM_F32 if dt == torch.float32 else SSM_BF16
+    ws, nws = _workspace("ssm_head_scan_workspace", device, b, L, h, hk, dk, dv, code, 1)
+    _call(device, load_library().ssm_head_scan_bwd, *ops[0], *ops[1], *ops[2], _addr(g), _addr(g_head), _addr(h0),
+          _addr(lengths), dk ** -0.5 if scale is None else float(scale), do.data_ptr(), _addr(dlast),
+          *(_addr(t) for t in out.values()), _addr(ws), nws, b, L, h, hk, dk, dv, code)
     return out
 
 
@@ -799,15 +819,12 @@ def ssm_head_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torc
     else:
         _need(state_out, "state_out", torch.float32, device, (b, h, dk, dv))
     if o is None:
-        o = torch.empty((b, h, dv), device=device, dtype=dt)
+        o = torch.empty_like(v)
     else:
         _need(o, "o", dt, device, (b, h, dv))
-    lib = load_library()
-    with torch.cuda.device(device):
-        rc = lib.ssm_head_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(g_head), dk ** -0.5 if scale is None else float(scale),
-                               _ptr(state), _ptr(state_out), _ptr(o), b, h, hk, dk, dv,
-                               SSM_F32 if dt == torch.float32 else SSM_BF16, _stream(device))
-    _check(rc)
+    _call(device, load_library().ssm_head_step, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(g_head),
+          dk ** -0.5 if scale is None else float(scale), state.data_ptr(), state_out.data_ptr(), o.data_ptr(), b, h, hk,
+          dk, dv, SSM_F32 if dt == torch.float32 else SSM_BF16)
     return o, state_out
 
 
@@ -843,12 +860,8 @@ def ssm_gate_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, z: Opt
         y = torch.empty_like(x)
     else:
         _need(y, "y", dt, device, x.shape)
-    lib = load_library()
-    with torch.cuda.device(device):
-        rc = lib.ssm_gate_norm(_ptr(x), _ptr(z), _ptr(weight), _ptr(y), rows, c, int(groups), float(eps),
-                               int(bool(center)), int(bool(gate_first)), SSM_F32 if dt == torch.float32 else SSM_BF16,
-                               _stream(device))
-    _check(rc)
+    _call(device, load_library().ssm_gate_norm, x.data_ptr(), _addr(z), _addr(weight), y.data_ptr(), rows, c, int(groups),
+          float(eps), int(bool(center)), int(bool(gate_first)), SSM_F32 if dt == torch.float32 else SSM_BF16)
     return y
 
 
@@ -866,14 +879,11 @@ def ssm_gate_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: Optional[torch.
     dx = torch.empty_like(x)
     dz = torch.empty_like(x) if z is not None else None
     dw = torch.empty((c,), device=device, dtype=torch.float32) if want_dweight else None
-    lib = load_library()
     code = SSM_F32 if dt == torch.float32 else SSM_BF16
-    with torch.cuda.device(device):
-        ws = _workspace(lib.ssm_gate_norm_workspace, device, rows, c, int(groups), code) if want_dweight else None
-        rc = lib.ssm_gate_norm_bwd(_ptr(x), _ptr(z), _ptr(weight), _ptr(dy), _ptr(dx), _ptr(dz), _ptr(dw), _ptr(ws),
-                                   _bytes(ws), rows, c, int(groups), float(eps), int(bool(center)),
-                                   int(bool(gate_first)), code, _stream(device))
-    _check(rc)
+    ws, nws = _workspace("ssm_gate_norm_workspace", device, rows, c, int(groups), code) if want_dweight else (None, 0)
+    _call(device, load_library().ssm_gate_norm_bwd, x.data_ptr(), _addr(z), _addr(weight), dy.data_ptr(), dx.data_ptr(),
+          _addr(dz), _addr(dw), _addr(ws), nws, rows, c, int(groups), float(eps), int(bool(center)),
+          int(bool(gate_first)), code)
     return dx, dw, dz
 
 
@@ -902,13 +912,10 @@ def ssm_linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = 
     else:
         _need(out, "out", dt, device, shape)
     pre = torch.empty(shape, device=device, dtype=dt) if return_pre else None
-    lib = load_library()
     code = SSM_F32 if dt == torch.float32 else SSM_BF16
-    with torch.cuda.device(device):
-        ws = _workspace(lib.ssm_linear_workspace, device, rows, k, m, ACTS[act], code, 0)
-        rc = lib.ssm_linear(_ptr(x), _ptr(W), _ptr(bias), _ptr(residual), ACTS[act], _ptr(out), _ptr(pre), _ptr(ws),
-                            _bytes(ws), rows, k, m, code, _stream(device))
-    _check(rc)
+    ws, nws = _workspace("ssm_linear_workspace", device, rows, k, m, ACTS[act], code, 0)
+    _call(device, load_library().ssm_linear, x.data_ptr(), W.data_ptr(), _addr(bias), _addr(residual), ACTS[act],
+          out.data_ptr(), _addr(pre), _addr(ws), nws, rows, k, m, code)
     return (out, pre) if return_pre else out
 
 
@@ -930,13 +937,10 @@ def ssm_linear_bwd(x: torch.Tensor, W: torch.Tensor, dout: torch.Tensor, pre: Op
     dx = torch.empty_like(x) if want_dx else None
     dW = torch.empty_like(W) if want_dW else None
     db = torch.empty((m,), device=device, dtype=dt) if want_dbias else None
-    lib = load_library()
     code = SSM_F32 if dt == torch.float32 else SSM_BF16
-    with torch.cuda.device(device):
-        ws = _workspace(lib.ssm_linear_workspace, device, rows, k, m, ACTS[act], code, 1)
-        rc = lib.ssm_linear_bwd(_ptr(x), _ptr(W), _ptr(pre), ACTS[act], _ptr(dout), _ptr(dx), _ptr(dW), _ptr(db), _ptr(ws),
-                                _bytes(ws), rows, k, m, code, _stream(device))
-    _check(rc)
+    ws, nws = _workspace("ssm_linear_workspace", device, rows, k, m, ACTS[act], code, 1)
+    _call(device, load_library().ssm_linear_bwd, x.data_ptr(), W.data_ptr(), _addr(pre), ACTS[act], dout.data_ptr(),
+          _addr(dx), _addr(dW), _addr(db), _addr(ws), nws, rows, k, m, code)
     return dx, dW, db
 
 
