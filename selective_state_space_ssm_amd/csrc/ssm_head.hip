@@ -46,11 +46,18 @@ using headk::HeadDev;
 // segments as give every CU two.  A split costs a second pass over y and z for
 // the segments' states: 256 heads of 128 x 128 (8 x 2048 tokens, bfloat16) take
 // 168 us whole and 187 us in two segments; 16 heads over 65536 tokens 512 us in
-// 16 segments, 464 in 32, 524 in 48.
+// 16 segments, 464 in 32, 524 in 48.  The backward's three passes share the
+// segments' states: it is split for two workgroups per CU in any case (4 x 2048
+// tokens, 64 heads of 128 x 64: 815 us whole, 731 in two, 820 in three; float32,
+// 4 x 1999, 24 heads of 64: 538 whole, 384 in six).
 constexpr int64_t kHeadCUs = 256;
 constexpr int64_t kHeadSlots = 512;
 constexpr int64_t kHeadMinSegment = 256;  // tokens
-constexpr int64_t kHeadMaxDgSegment = 1024;  // tokens that the running sum of dg covers
+// Tokens that the running sum of dg covers: its terms are off by 2^-24 (float32)
+// or 2^-17 (bfloat16, where dg itself is rounded to 2^-8) of themselves, and the
+// sum's error grows like the root of their number.
+constexpr int64_t kHeadMaxDgSegmentF32 = 1024;
+constexpr int64_t kHeadMaxDgSegmentBf16 = 4096;
 
 // States carried over the segments, in order: state <- decay * (carried) + own.
 // Segment `first` holds its final state already.
@@ -122,17 +129,21 @@ __global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, co
   }
 }
 
-// out[t][hk][e] = sum over the heads that share hk of part[t][h][e]
-template <typename IO>
+// out[t][hk][e] = sum over the heads that share hk of part[t][h][e], V values a thread
+template <typename IO, int V>
 __global__ void __launch_bounds__(256) ssm_head_group_sum_kernel(const float* part, void* out, int64_t n, int64_t d,
                                                                 int64_t rep) {
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += stride) {
-    const float* src = part + (i / d) * rep * d + i % d;
-    float s = 0.f;
-    for (int64_t r = 0; r < rep; ++r) s += src[r * d];
-    IO::template st<1>(static_cast<typename IO::T*>(out) + i, &s);
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V;
+  if (i >= n) return;
+  const float* src = part + (i / d) * rep * d + i % d;
+  float s[V] = {}, x[V];
+#pragma unroll 8
+  for (int64_t r = 0; r < rep; ++r) {
+    F32::ld<V>(src + r * d, x);
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] += x[e];
   }
+  IO::template st<V>(static_cast<typename IO::T*>(out) + i, s);
 }
 
 // One token.  A workgroup owns one (batch row, head) and 32 columns of the
@@ -248,18 +259,19 @@ struct Plan {
   int64_t C, nch, cps, nseg;
   bool vec;
 };
-Plan plan_of(int64_t batch, int64_t H, int64_t tiles, int64_t L, bool bf16, bool dg, bool vec) {
+Plan plan_of(int64_t batch, int64_t H, int64_t tiles, int64_t L, bool bf16, bool backward, bool vec) {
   Plan p;
   p.vec = vec;
   p.C = bf16 ? headk::HeadCfg<BF16>::C : headk::HeadCfg<F32>::C;
   p.nch = cdiv(L, p.C);
   const int64_t wgs = batch * H * tiles;
-  int64_t want = wgs < kHeadCUs ? kHeadSlots / wgs : 1;
+  int64_t want = backward || wgs < kHeadCUs ? kHeadSlots / wgs : 1;
   const int64_t most = L / kHeadMinSegment;
   if (want > most) want = most;
   if (want < 1) want = 1;
   p.cps = cdiv(p.nch, want);
-  if (dg && p.cps * p.C > kHeadMaxDgSegment) p.cps = kHeadMaxDgSegment / p.C;
+  const int64_t span = bf16 ? kHeadMaxDgSegmentBf16 : kHeadMaxDgSegmentF32;
+  if (backward && p.cps * p.C > span) p.cps = span / p.C;
   p.nseg = cdiv(p.nch, p.cps);
   return p;
 }
@@ -364,9 +376,11 @@ Plan bwd_plan(const HeadArgs& a, bool bf16) {
 
 template <typename IO>
 hipError_t launch_group_sum(const float* part, void* out, const HeadArgs& a, hipStream_t st) {
-  const int64_t n = a.batch * a.L * a.Hk * a.dk, blocks = cdiv(n, 256);
-  hipLaunchKernelGGL(ssm_head_group_sum_kernel<IO>, dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)), dim3(256),
-                     0, st, part, out, n, a.dk, a.H / a.Hk);
+  const int64_t n = a.batch * a.L * a.Hk * a.dk;
+  const bool four = a.dk % 4 == 0;
+  auto kern = four ? ssm_head_group_sum_kernel<IO, 4> : ssm_head_group_sum_kernel<IO, 1>;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(cdiv(n, four ? 1024 : 256))), dim3(256), 0, st, part, out, n, a.dk,
+                     a.H / a.Hk);
   return hipGetLastError();
 }
 

@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "ssm_device.h"
+#include "ssm_dma.h"
 #include "ssm_kernels.h"
 
 namespace ssm {
@@ -65,9 +66,31 @@ struct LinDev {
   int act;
 };
 
+// erfc(x) with a relative error below 2e-7 for every x (so that gelu keeps its
+// digits in the tail): Chebyshev fit of log(erfc(x) / t) in t = 1 / (1 + x / 2),
+// x >= 0 (W. H. Press et al., Numerical Recipes, "Incomplete Gamma Function, Error
+// Function"), mirrored for x < 0.
+__device__ __forceinline__ float erfc_fit(float x) {
+  const float z = __builtin_fabsf(x), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, z, 1.f));
+  float s = 0.17087277f;
+  s = __builtin_fmaf(s, t, -0.82215223f);
+  s = __builtin_fmaf(s, t, 1.48851587f);
+  s = __builtin_fmaf(s, t, -1.13520398f);
+  s = __builtin_fmaf(s, t, 0.27886807f);
+  s = __builtin_fmaf(s, t, -0.18628806f);
+  s = __builtin_fmaf(s, t, 0.09678418f);
+  s = __builtin_fmaf(s, t, 0.37409196f);
+  s = __builtin_fmaf(s, t, 1.00002368f);
+  s = __builtin_fmaf(s, t, -1.26551223f);
+  // exp(-z^2 + s): z^2 as hi + lo, its rounding would be multiplied by the exponent
+  const float q = z * z, ql = __builtin_fmaf(z, z, -q);
+  const float e = t * __builtin_amdgcn_exp2f(kLog2e * (s - q)) * (1.f - ql);
+  return x >= 0.f ? e : 2.f - e;
+}
+
 __device__ __forceinline__ float act_of(float p, int act) {
   if (act == kActSilu) return p * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * p));
-  if (act == kActGelu) return 0.5f * p * erfcf(-0.70710678118654752f * p);  // erfc keeps the tail's digits
+  if (act == kActGelu) return 0.5f * p * erfc_fit(-0.70710678118654752f * p);
   return p;
 }
 
@@ -78,11 +101,11 @@ __device__ __forceinline__ float act_grad(float p, int act) {
   }
   if (act == kActGelu)
     return __builtin_fmaf(p, 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * kLog2e * p * p),
-                          0.5f * erfcf(-0.70710678118654752f * p));
+                          0.5f * erfc_fit(-0.70710678118654752f * p));
   return 1.f;
 }
 
-// Four values of row r from column c: bias, act, residual, rounding.  CNT of them exist.
+// CNT values of row r from column c on: bias, act, residual, rounding.
 template <typename IO, int CNT>
 __device__ __forceinline__ void epilogue(const LinDev& p, int64_t r, int64_t c, float* v) {
   using T = typename IO::T;
@@ -305,6 +328,253 @@ __global__ void __launch_bounds__(256, 2) ssm_linear_tile_kernel(LinDev p) {
   }
 }
 
+// ------------------------------------------------------------------------
+// bfloat16, whole 16-byte chunks, large products: 256 x 256 tiles whose
+// operands go from memory straight into LDS, four stages of 32 k, three of
+// them in flight.
+//
+// A stage holds each operand as it is stored: k contiguous as [256 rows][32 k]
+// (64-byte rows, chunk q of row r at q ^ ((r >> 1) & 3), read as they are), or
+// rows contiguous as [32 k][256 rows] (512-byte rows, chunk q of row k at
+// q ^ swz_kn(k), read with the transposing LDS read).  Both swizzles keep the
+// reads free of bank conflicts, and are applied by choosing which chunk a lane
+// fetches.
+// ------------------------------------------------------------------------
+constexpr int kStageK = 32;
+constexpr int kStages = 4;
+constexpr int kOperand = 256 * kStageK * 2;  // bytes of one operand's stage
+constexpr int kStage = 2 * kOperand;
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+
+__device__ __forceinline__ int swz_kn(int k) { return 2 * ((k & 3) | (((k >> 3) & 1) << 2)); }
+
+// One operand's share of the loads and reads of a workgroup of four wavefronts.
+template <bool TR>
+struct DmaSide {
+  uint32_t voff[4];  // byte offset of this lane's chunk in block `wave` + 4 i of a stage, kOOB outside the rows
+  int k[4];          // its first k in the stage
+  uint64_t addr;     // the next stage's start
+  uint64_t step;     // bytes to the one after
+  int frag[TR ? 8 : 1];
+
+  // rows row0 .. (nrows in all) from k0 on; the wavefront reads rows half * 128 .. of the tile
+  __device__ __forceinline__ void init(const char* base, int64_t ld, int64_t row0, int64_t nrows, int64_t k0, int wave,
+                                       int lane, int half) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = wave + 4 * i;  // 1 KB block
+      if constexpr (!TR) {
+        const int r = 16 * q + (lane >> 2), c = (lane & 3) ^ ((r >> 1) & 3);
+        k[i] = 8 * c;
+        voff[i] = row0 + r < nrows ? static_cast<uint32_t>(r * ld * 2 + 16 * c) : kOOB;
+      } else {
+        const int r = 2 * q + (lane >> 5), c = (lane & 31) ^ swz_kn(r);
+        k[i] = r;
+        voff[i] = row0 + 8 * c < nrows ? static_cast<uint32_t>(r * ld * 2 + 16 * c) : kOOB;
+      }
+    }
+    addr = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>((TR ? k0 * ld + row0 : row0 * ld + k0) * 2);
+    step = static_cast<uint64_t>(TR ? kStageK * ld * 2 : kStageK * 2);
+    if constexpr (!TR) {
+      frag[0] = (half * 128 + (lane & 15)) * 64 + 16 * ((lane >> 4) ^ (((lane & 15) >> 1) & 3));
+    } else {
+      const int kk = 8 * (lane >> 4) + ((lane & 15) >> 2);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        frag[j] = kk * 512 + 16 * (half * 16 + ((2 * j) ^ swz_kn(kk)) + ((lane >> 1) & 1)) + 8 * (lane & 1);
+    }
+  }
+  // i-th of the four loads of the next stage into LDS at `lds`; krem k of it exist (none: reads zeros)
+  __device__ __forceinline__ void load(uint32_t lds, int wave, int i, int krem) const {
+    const u32x4 d = dma_desc(reinterpret_cast<const void*>(addr), krem > 0 ? kRecords : 0u);
+    dma16(d, krem >= kStageK || k[i] < krem ? voff[i] : kOOB, lds + (wave + 4 * i) * 1024);
+  }
+  __device__ __forceinline__ uint4 read(const char* stage, int j) const {
+    if constexpr (!TR) {
+      return *reinterpret_cast<const uint4*>(stage + frag[0] + 1024 * j);
+    } else {
+      const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(stage + frag[j]));
+      const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(stage + frag[j] + 4 * 512));
+      const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
+      return make_uint4(l.x, l.y, h.x, h.y);
+    }
+  }
+};
+
+// How a tile leaves: float32 partials, rounded values, or through the epilogue.
+enum { kPart = 0, kPlain = 1, kFull = 2 };
+
+template <bool CTR, bool RTR, int OUT>
+__global__ void __launch_bounds__(256, 1) ssm_linear_dma_kernel(LinDev p) {
+  __shared__ __attribute__((aligned(1024))) char stg[kStages][kStage];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wc = wave & 1, wr = wave >> 1;
+  const int64_t mc = (p.nc + 255) / 256, mr = (p.nr + 255) / 256;
+  const int64_t G = gridDim.x, pid = blockIdx.x, q8 = G / 8, r8 = G % 8, xcd = pid % 8;
+  int64_t idx = xcd * q8 + (xcd < r8 ? xcd : r8) + pid / 8;
+  const int64_t c0 = idx % mc * 256;
+  idx /= mc;
+  const int64_t r0 = idx % mr * 256, split = idx / mr;
+  const int64_t kb = split * p.kpart, ke = kb + p.kpart < p.K ? kb + p.kpart : p.K;
+  const int64_t nsteps = (ke - kb + kStageK - 1) / kStageK;
+
+  DmaSide<CTR> sc;
+  DmaSide<RTR> sr;
+  sc.init(p.c, p.ldc, c0, p.nc, kb, wave, lane, wc);
+  sr.init(p.r, p.ldr, r0, p.nr, kb, wave, lane, wr);
+  int64_t left = ke - kb;  // k from the next stage on
+  // a stage past the end is still issued (its loads read zeros), so that one count serves every wait
+  auto issue = [&](auto KS) {
+    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)stg[decltype(KS)::value]));
+    const int krem = left > kStageK ? kStageK : static_cast<int>(left);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sc.load(base, wave, i, krem);
+      sr.load(base + kOperand, wave, i, krem);
+    }
+    if (left > 0) {
+      left -= kStageK;
+      sc.addr += sc.step;
+      sr.addr += sr.step;
+    }
+  };
+  struct Frag {
+    uint4 c[8], r[8];
+  };
+  auto read_c = [&](auto KS, Frag& f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.c[i] = sc.read(stg[decltype(KS)::value], i);
+  };
+  auto read_r = [&](auto KS, Frag& f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.r[j] = sr.read(stg[decltype(KS)::value] + kOperand, j);
+  };
+  f32x4 acc[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto products = [&](const Frag& f, auto I0) {  // columns' tiles I0, I0 + 1
+#pragma unroll
+    for (int i = decltype(I0)::value; i < decltype(I0)::value + 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.c[i]),
+                                                            __builtin_bit_cast(bf16x8, f.r[j]), acc[i][j], 0, 0, 0);
+  };
+
+  // Step s: wait until stage s + 1 has landed (8 loads a wavefront and stage: vmcnt(8) leaves stage s + 2 in flight)
+  // and this wavefront's reads of step s - 1 are done; barrier; then step s's products in four groups, with the refill
+  // of the stage read at step s - 1 and the reads of step s + 1's operands between them.
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
+  using S2 = std::integral_constant<int, 2>;
+  using S3 = std::integral_constant<int, 3>;
+  using S4 = std::integral_constant<int, 4>;
+  using S6 = std::integral_constant<int, 6>;
+  constexpr int kWait16 = 0 | (7 << 4) | (0 << 8) | (1 << 14);  // vmcnt(16) lgkmcnt(0)
+  constexpr int kWait8 = 8 | (7 << 4) | (0 << 8);               // vmcnt(8) lgkmcnt(0)
+  Frag F0, F1;
+  issue(S0{});
+  issue(S1{});
+  issue(S2{});
+  __builtin_amdgcn_s_waitcnt(kWait16);
+  asm volatile("s_barrier" ::: "memory");
+  read_c(S0{}, F0);
+  read_r(S0{}, F0);
+  auto step = [&](auto KR, auto KN, Frag& cur, Frag& nxt) {
+    __builtin_amdgcn_s_waitcnt(kWait8);
+    asm volatile("s_barrier" ::: "memory");
+    products(cur, S0{});
+    issue(KR);
+    products(cur, S2{});
+    read_c(KN, nxt);
+    products(cur, S4{});
+    read_r(KN, nxt);
+    products(cur, S6{});
+  };
+  for (int64_t s = 0; s < nsteps; s += 4) {
+    step(S3{}, S1{}, F0, F1);
+    if (s + 1 < nsteps) step(S0{}, S2{}, F1, F0);
+    if (s + 2 < nsteps) step(S1{}, S3{}, F0, F1);
+    if (s + 3 < nsteps) step(S2{}, S0{}, F1, F0);
+  }
+  // no load into LDS may still be in flight when the workgroup ends
+  __builtin_amdgcn_s_waitcnt(0);
+
+  if constexpr (OUT == kFull) {
+    // The epilogue reads and writes whole 128-byte runs of a row: every wavefront passes its 128 x 128 sums through
+    // its quarter of the LDS in two halves of 64 columns ([128 rows][16 chunks of 4 columns], chunk q of row r at
+    // q ^ (r & 15)).  Straight from the accumulators it is 64 copies of the epilogue's code (547 us for the forward of
+    // 16384 x 4096 -> 2048 with gelu and residual).
+    // The residuals of eight rows a lane are in flight together.
+    __syncthreads();
+    float4* own = reinterpret_cast<float4*>(&stg[0][0]) + wave * 128 * 16;
+    const int64_t rw = r0 + wr * 128, cwv = c0 + wc * 128, base = (rw * p.nc + cwv) * 2;
+    const Rsrc rres = make_rsrc(p.residual + base, kRecords), rout = make_rsrc(p.out + base, kRecords);
+    const Rsrc rpre = make_rsrc(p.pre + base, kRecords);
+    const uint32_t row_bytes = static_cast<uint32_t>(p.nc * 2);
+    const int rows = p.nr - rw > 128 ? 128 : static_cast<int>(p.nr - rw), lr = lane >> 3, lc = 8 * (lane & 7);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = 16 * j + (lane & 15);
+          const f32x4 v = acc[4 * half + i][j];
+          own[r * 16 + ((4 * i + (lane >> 4)) ^ (r & 15))] = make_float4(v[0], v[1], v[2], v[3]);
+        }
+      const bool cok = cwv + 64 * half + lc < p.nc;
+      float bias[8] = {};
+      if (p.bias != nullptr && cok) BF16::ld<8>(reinterpret_cast<const uint16_t*>(p.bias) + cwv + 64 * half + lc, bias);
+#pragma unroll 1
+      for (int k0 = 0; k0 < 128; k0 += 64) {
+        u32x4 res[8];
+        uint32_t off[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rl = k0 + 8 * k + lr;
+          off[k] = cok && rl < rows ? static_cast<uint32_t>(rl) * row_bytes + 2 * (64 * half + lc) : kOOB;
+          if (p.residual != nullptr) res[k] = __builtin_amdgcn_raw_buffer_load_b128(rres, off[k], 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rl = k0 + 8 * k + lr, q = 2 * (lane & 7);
+          const float4 x = own[rl * 16 + (q ^ (rl & 15))], y = own[rl * 16 + ((q + 1) ^ (rl & 15))];
+          float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += bias[e];
+          if (p.pre != nullptr) BufBF16::st<8>(rpre, off[k], v);
+          if (p.act != kActNone) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = act_of(v[e], p.act);
+          }
+          if (p.residual != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += e & 1 ? bf_hi(res[k][e >> 1]) : bf_lo(res[k][e >> 1]);
+          }
+          BufBF16::st<8>(rout, off[k], v);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t c = c0 + wc * 128 + 16 * i + 4 * (lane >> 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t r = r0 + wr * 128 + 16 * j + (lane & 15);
+        if (r >= p.nr || c >= p.nc) continue;
+        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        if constexpr (OUT == kPart) F32::st<4>(reinterpret_cast<float*>(p.out) + (split * p.nr + r) * p.nc + c, v);
+        else BF16::st<4>(reinterpret_cast<uint16_t*>(p.out) + r * p.nc + c, v);
+      }
+    }
+  }
+}
+
 // Partials added in order, then the epilogue: CNT values per thread.
 template <typename IO, int CNT>
 __global__ void __launch_bounds__(256) ssm_linear_sum_kernel(const float* part, LinDev p) {
@@ -319,6 +589,60 @@ __global__ void __launch_bounds__(256) ssm_linear_sum_kernel(const float* part, 
       for (int e = 0; e < CNT; ++e) v[e] += t[e];
     }
     epilogue<IO, CNT>(p, at / p.nc, at % p.nc, v);
+  }
+}
+
+// Few rows (up to 16): one launch whose traffic is W's.  A workgroup of eight
+// wavefronts owns 16 columns; wavefront w takes every eighth step of k, reads
+// both operands straight from memory (a lane reads 16 bytes of one row of W and
+// of x), and the eight partial 16 x 16 tiles meet in LDS.
+template <typename IO, bool VEC>
+__global__ void __launch_bounds__(512) ssm_linear_rows_kernel(LinDev p) {
+  using C = LinCfg<IO>;
+  constexpr int E = C::E, ES = C::ES, BK = 4 * E, DEPTH = 8;  // k per instruction (chunk of four lanes), steps in flight
+  __shared__ float part[8][16][17];
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const Rsrc rc = make_rsrc(p.c + c0 * p.ldc * ES, kRecords), rr = make_rsrc(p.r, kRecords);
+  const bool cok = c0 + li < p.nc, rok = li < p.nr;
+  const uint32_t cb = static_cast<uint32_t>(li * p.ldc * ES), rb = static_cast<uint32_t>(li * p.ldr * ES);
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  using Ld = Stage<IO, 64, false, VEC>;
+  for (int64_t k0 = wave * BK; k0 < p.K; k0 += 8 * BK * DEPTH) {
+    uint4 fc[DEPTH], fr[DEPTH];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      const int64_t k = k0 + d * 8 * BK + g * E, left = p.K - k;
+      const int have = left > E ? E : (left > 0 ? static_cast<int>(left) : 0);
+      Ld::fetch(rc, cb + static_cast<uint32_t>(k * ES), cok ? have : 0, fc[d]);
+      Ld::fetch(rr, rb + static_cast<uint32_t>(k * ES), rok ? have : 0, fr[d]);
+    }
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      if constexpr (ES == 2) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fc[d]), __builtin_bit_cast(bf16x8, fr[d]),
+                                                      acc, 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(reinterpret_cast<const uint32_t*>(&fc[d])[e]),
+                                                     __uint_as_float(reinterpret_cast<const uint32_t*>(&fr[d])[e]), acc, 0,
+                                                     0, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) part[wave][li][4 * g + v] = acc[v];
+  __syncthreads();
+  if (tid < 256) {
+    const int r = tid >> 4, c = tid & 15;
+    if (r < p.nr && c0 + c < p.nc) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v += part[w][r][c];
+      epilogue<IO, 1>(p, r, c0 + c, &v);
+    }
   }
 }
 
@@ -367,51 +691,71 @@ __global__ void __launch_bounds__(256) ssm_linear_dpre_kernel(const void* dout, 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
-// One product's tile (32 t x 32 t) and split of k.  The largest tile that
-// still gives every CU a workgroup; below that the smallest, with k split
-// until the CUs have one each and a split keeps at least four steps.
+// One product's tile (32 t x 32 t) and split of k.  bfloat16 with whole chunks
+// takes 256 x 256 tiles (t = 8) where they, with k in parts of at least 1024,
+// give three quarters of the CUs a workgroup; else the larger of 128 and 64
+// that gives every CU one, and below that 64 with k in parts of at least four
+// steps.
 struct Tiling {
   int t;
   int64_t kpart, nsplit;
 };
 template <typename IO>
-Tiling tiling(int64_t nc, int64_t nr, int64_t K) {
+Tiling tiling(int64_t nc, int64_t nr, int64_t K, bool vec) {
   constexpr int64_t BK = 8 * LinCfg<IO>::E;
   Tiling w{2, 0, 1};
   auto tiles = [&](int t) { return cdiv(nc, 32 * t) * cdiv(nr, 32 * t); };
-  if (tiles(4) >= kCUs) w.t = 4;
   const int64_t steps = cdiv(K, BK);
-  int64_t split = w.t == 2 && tiles(2) < kCUs ? kCUs / tiles(2) : 1;
-  if (split > steps / 4) split = steps / 4;
-  if (split < 1) split = 1;
+  int64_t split = 1;
+  if (std::is_same<IO, BF16>::value && vec) {
+    split = tiles(8) < kCUs ? kCUs / tiles(8) : 1;
+    if (split > K / 1024) split = K / 1024;
+    if (split < 1) split = 1;
+    if (4 * tiles(8) * split >= 3 * kCUs) w.t = 8;
+  }
+  if (w.t != 8) {
+    if (tiles(4) >= kCUs) w.t = 4;
+    split = w.t == 2 && tiles(2) < kCUs ? kCUs / tiles(2) : 1;
+    if (split > steps / 4) split = steps / 4;
+    if (split < 1) split = 1;
+  }
   w.kpart = cdiv(steps, split) * BK;
   w.nsplit = cdiv(K, w.kpart);
   return w;
 }
-template <typename IO>
+// Whole, aligned 16-byte chunks of both operands, and four outputs of a row together.
+template <typename IO, bool CTR, bool RTR>
+bool vec_of(int64_t nc, int64_t nr, int64_t K) {
+  constexpr int64_t E = LinCfg<IO>::E;
+  return (CTR && RTR ? true : K % E == 0) && nc % E == 0 && (RTR ? nr % E == 0 : true);
+}
+template <typename IO, bool CTR, bool RTR>
 int64_t part_bytes(int64_t nc, int64_t nr, int64_t K) {
-  const Tiling w = tiling<IO>(nc, nr, K);
+  const Tiling w = tiling<IO>(nc, nr, K, vec_of<IO, CTR, RTR>(nc, nr, K));
   return w.nsplit > 1 ? up16(4 * w.nsplit * nc * nr) : 0;
 }
 
 template <typename IO, int T, bool CTR, bool RTR, bool VEC, bool PART>
 hipError_t launch_tile_t(const LinDev& p, hipStream_t st) {
   const int64_t wgs = cdiv(p.nc, 32 * T) * cdiv(p.nr, 32 * T) * p.nsplit;
-  constexpr size_t smem = size_t(2) * 2 * 32 * T * 128;
-  hipLaunchKernelGGL((ssm_linear_tile_kernel<IO, T, T, CTR, RTR, VEC, PART>), dim3(static_cast<unsigned>(wgs)), dim3(256),
-                     smem, st, p);
+  if constexpr (T == 8) {
+    // the backward's products have no epilogue
+    constexpr int OUT = PART ? kPart : (CTR ? kPlain : kFull);
+    hipLaunchKernelGGL((ssm_linear_dma_kernel<CTR, RTR, OUT>), dim3(static_cast<unsigned>(wgs)), dim3(256), 0, st, p);
+  } else {
+    constexpr size_t smem = size_t(2) * 2 * 32 * T * 128;
+    hipLaunchKernelGGL((ssm_linear_tile_kernel<IO, T, T, CTR, RTR, VEC, PART>), dim3(static_cast<unsigned>(wgs)),
+                       dim3(256), smem, st, p);
+  }
   return hipGetLastError();
 }
 
 template <typename IO, bool CTR, bool RTR>
 hipError_t product(LinDev p, char* work, hipStream_t st) {
-  constexpr int64_t E = LinCfg<IO>::E;
-  const Tiling w = tiling<IO>(p.nc, p.nr, p.K);
+  const bool vec = vec_of<IO, CTR, RTR>(p.nc, p.nr, p.K);
+  const Tiling w = tiling<IO>(p.nc, p.nr, p.K, vec);
   p.kpart = w.kpart;
   p.nsplit = w.nsplit;
-  // every 16-byte chunk of an operand whole and aligned, every four outputs of a row too
-  const bool vec = p.ldc % E == 0 && p.ldr % E == 0 && p.K % ((CTR && RTR) ? 1 : E) == 0 && p.nc % (CTR ? E : 4) == 0 &&
-                   p.nr % (RTR ? E : 1) == 0;
   const LinDev whole = p;
   if (w.nsplit > 1) {
     p.out = work;
@@ -425,13 +769,19 @@ hipError_t product(LinDev p, char* work, hipStream_t st) {
   using T2 = std::integral_constant<int, 2>;
   using Y = std::true_type;
   using N = std::false_type;
-  hipError_t e;
-  if (w.t == 4)
+  hipError_t e = hipSuccess;
+  if (w.t == 8) {
+    if constexpr (std::is_same<IO, BF16>::value) {
+      using T8 = std::integral_constant<int, 8>;
+      e = w.nsplit > 1 ? run(T8{}, Y{}, Y{}) : run(T8{}, Y{}, N{});
+    }
+  } else if (w.t == 4) {
     e = vec ? run(T4{}, Y{}, N{}) : run(T4{}, N{}, N{});
-  else if (w.nsplit > 1)
+  } else if (w.nsplit > 1) {
     e = vec ? run(T2{}, Y{}, Y{}) : run(T2{}, N{}, Y{});
-  else
+  } else {
     e = vec ? run(T2{}, Y{}, N{}) : run(T2{}, N{}, N{});
+  }
   if (e != hipSuccess || w.nsplit == 1) return e;
   const bool four = p.nc % 4 == 0;
   const int64_t blocks = cdiv(p.nr * p.nc / (four ? 4 : 1), 256);
@@ -441,6 +791,9 @@ hipError_t product(LinDev p, char* work, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Rows of the one-launch kernel; W's row offsets are 32-bit there (16 rows of under 2^21 values).
+constexpr int64_t kFewRows = 16;
+
 template <typename IO>
 hipError_t forward_io(const LinearArgs& a, char* work, hipStream_t st) {
   LinDev p{};
@@ -448,6 +801,11 @@ hipError_t forward_io(const LinearArgs& a, char* work, hipStream_t st) {
   p.nc = a.m; p.nr = a.rows; p.K = a.k; p.ldc = a.k; p.ldr = a.k;
   p.bias = static_cast<const char*>(a.bias); p.residual = static_cast<const char*>(a.residual);
   p.pre = static_cast<char*>(a.pre); p.act = a.act;
+  if (a.rows <= kFewRows) {
+    auto kern = a.k % LinCfg<IO>::E == 0 ? ssm_linear_rows_kernel<IO, true> : ssm_linear_rows_kernel<IO, false>;
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(cdiv(a.m, 16))), dim3(512), 0, st, p);
+    return hipGetLastError();
+  }
   return product<IO, false, false>(p, work, st);
 }
 
@@ -470,7 +828,8 @@ BwdSpace bwd_space(const LinearArgs& a) {
   const int64_t cnt = a.m % LinCfg<IO>::E == 0 ? LinCfg<IO>::E : 1;
   if (a.dbias != nullptr) at += up16(4 * cdiv(a.rows, dpre_rows(a, 32 * cnt)) * a.m);
   w.part = at;
-  const int64_t px = a.dx ? part_bytes<IO>(a.k, a.rows, a.m) : 0, pw = a.dw ? part_bytes<IO>(a.k, a.m, a.rows) : 0;
+  const int64_t px = a.dx ? part_bytes<IO, true, false>(a.k, a.rows, a.m) : 0;
+  const int64_t pw = a.dw ? part_bytes<IO, true, true>(a.k, a.m, a.rows) : 0;
   w.total = at + (px > pw ? px : pw);
   return w;
 }
@@ -510,7 +869,8 @@ hipError_t backward_io(const LinearArgs& a, char* work, hipStream_t st) {
 }  // namespace
 
 int64_t linear_workspace_bytes(const LinearArgs& a, bool bf16, bool backward) {
-  if (!backward) return bf16 ? part_bytes<BF16>(a.m, a.rows, a.k) : part_bytes<F32>(a.m, a.rows, a.k);
+  if (!backward && a.rows <= kFewRows) return 0;
+  if (!backward) return bf16 ? part_bytes<BF16, false, false>(a.m, a.rows, a.k) : part_bytes<F32, false, false>(a.m, a.rows, a.k);
   return bf16 ? bwd_space<BF16>(a).total : bwd_space<F32>(a).total;
 }
 

@@ -16,8 +16,10 @@
 // output): a group's values stay in registers between the passes over them.
 // Token rows being dense, group u of the flattened rows * groups is the n
 // values from u n on.  LANES lanes share a group: the smallest power of two
-// that covers it with one 16-byte vector per lane, a wavefront with up to
-// kMaxVec vectors per lane, a workgroup of 256 beyond that.
+// that covers it with one 16-byte vector per lane, a wavefront with two, a
+// workgroup of 256 with up to eight beyond that (few registers a lane, so
+// that many wavefronts' loads are in flight).  In the forward small groups are
+// taken several at a time by the same lanes, for the same reason.
 //
 // dw is a sum over rows: every workgroup of the backward walks rows of one
 // group, keeps its sum in registers and leaves one float32 partial; a second
@@ -33,8 +35,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kMaxVec = 8;               // 16-byte vectors per lane
-constexpr int64_t kBwdWorkgroups = 2048;  // about eight workgroups per CU
+constexpr int64_t kBwdWorkgroups = 1024;  // four workgroups per CU
 
 enum { kNoGate = 0, kGateLast = 1, kGateFirst = 2 };
 
@@ -81,6 +82,19 @@ struct Group {
       }
     }
   }
+  // float32 values (16-byte aligned with VEC) at the same places
+  static __device__ __forceinline__ void load_f32(const float* p, int l, int64_t n, float* o) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int e = 0; e < CNT; e += 4) {
+        const float4 v = at(l, e) < n ? *reinterpret_cast<const float4*>(p + at(l, e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        o[e] = v.x; o[e + 1] = v.y; o[e + 2] = v.z; o[e + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < CNT; ++e) o[e] = at(l, e) < n ? p[at(l, e)] : 0.f;
+    }
+  }
   static __device__ __forceinline__ void store(void* base, int64_t off, int l, int64_t n, const float* o) {
     typename IO::T* p = static_cast<typename IO::T*>(base) + off;
     if constexpr (VEC) {
@@ -94,6 +108,10 @@ struct Group {
     }
   }
 };
+
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
+}
 
 // Sum over the group's lanes; every lane gets it.
 template <int LANES>
@@ -136,38 +154,45 @@ __device__ __forceinline__ float normalise(const NormDev& p, int l, float* u, co
   return r;
 }
 
-__device__ __forceinline__ float sigmoid(float z) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
-}
+// Groups that the same lanes take one after the other in the forward.
+template <int LANES, int NV>
+constexpr int norm_units() { return LANES < 256 ? 4 / NV : 1; }
 
 template <typename IO, int LANES, int NV, bool VEC, int GATE>
 __global__ void __launch_bounds__(256) ssm_gate_norm_kernel(NormDev p) {
   using Gr = Group<IO, LANES, NV, VEC>;
+  constexpr int U = norm_units<LANES, NV>(), PER = 256 / LANES;
   __shared__ float sh[4];
   const int l = threadIdx.x % LANES;
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
-  if (u >= p.rows * p.groups) return;  // with 256 lanes the grid is exact: no barrier is left behind
-  const int64_t off = u * p.n, wo = (u % p.groups) * p.n;
-  float x[Gr::CNT], s[Gr::CNT], w[Gr::CNT];
-  Gr::load(p.x, off, l, p.n, x);
-  if constexpr (GATE != kNoGate) {
-    Gr::load(p.z, off, l, p.n, s);
+  const int64_t total = p.rows * p.groups;
+  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * (PER * U) + threadIdx.x / LANES;
+  float x[U][Gr::CNT], s[U][Gr::CNT], w[Gr::CNT];
 #pragma unroll
-    for (int i = 0; i < Gr::CNT; ++i) s[i] *= sigmoid(s[i]);
+  for (int i = 0; i < U; ++i) {
+    const int64_t u = u0 + i * PER;
+    const int64_t n = u < total ? p.n : 0;  // nothing is read or written past the last group
+    Gr::load(p.x, u * p.n, l, n, x[i]);
+    if constexpr (GATE != kNoGate) Gr::load(p.z, u * p.n, l, n, s[i]);
   }
-  normalise<IO, LANES, NV, VEC, GATE>(p, l, x, s, sh);
-  if (p.w != nullptr) {
 #pragma unroll
-    for (int i = 0; i < Gr::CNT; ++i) {
-      w[i] = Gr::at(l, i) < p.n ? p.w[wo + Gr::at(l, i)] : 0.f;
-      x[i] *= w[i];
+  for (int i = 0; i < U; ++i) {
+    const int64_t u = u0 + i * PER, wo = (u % p.groups) * p.n;
+    if (p.w != nullptr) Gr::load_f32(p.w + wo, l, p.n, w);
+    if constexpr (GATE != kNoGate) {
+#pragma unroll
+      for (int e = 0; e < Gr::CNT; ++e) s[i][e] *= sigmoid(s[i][e]);
     }
-  }
-  if constexpr (GATE == kGateLast) {
+    normalise<IO, LANES, NV, VEC, GATE>(p, l, x[i], s[i], sh);
+    if (p.w != nullptr) {
 #pragma unroll
-    for (int i = 0; i < Gr::CNT; ++i) x[i] *= s[i];
+      for (int e = 0; e < Gr::CNT; ++e) x[i][e] *= w[e];
+    }
+    if constexpr (GATE == kGateLast) {
+#pragma unroll
+      for (int e = 0; e < Gr::CNT; ++e) x[i][e] *= s[i][e];
+    }
+    Gr::store(p.y, u * p.n, l, u < total ? p.n : 0, x[i]);
   }
-  Gr::store(p.y, off, l, p.n, x);
 }
 
 template <typename IO, int LANES, int NV, bool VEC, int GATE>
@@ -241,21 +266,23 @@ __global__ void __launch_bounds__(256) ssm_gate_norm_bwd_kernel(NormDev p) {
   }
 }
 
-// out[c] = sum over k of part[k][c], in order: 64 columns and 4 strands of k per workgroup
+// out[c] = sum over k of part[k][c], in order: 64 columns and 16 strands of k per workgroup
 template <typename IO>
-__global__ void __launch_bounds__(256) ssm_column_sum_kernel(const float* part, int64_t count, int64_t cols, void* out) {
-  __shared__ float sh[4][64];
+__global__ void __launch_bounds__(1024) ssm_column_sum_kernel(const float* part, int64_t count, int64_t cols, void* out) {
+  __shared__ float sh[16][64];
   const int lane = threadIdx.x & 63, strand = threadIdx.x >> 6;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
   float s = 0.f;
   if (c < cols) {
 #pragma unroll 8
-    for (int64_t k = strand; k < count; k += 4) s += part[k * cols + c];
+    for (int64_t k = strand; k < count; k += 16) s += part[k * cols + c];
   }
   sh[strand][lane] = s;
   __syncthreads();
   if (strand == 0 && c < cols) {
-    const float v = (sh[0][lane] + sh[1][lane]) + (sh[2][lane] + sh[3][lane]);
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += sh[i][lane];
     IO::template st<1>(static_cast<typename IO::T*>(out) + c, &v);
   }
 }
@@ -263,7 +290,8 @@ __global__ void __launch_bounds__(256) ssm_column_sum_kernel(const float* part, 
 template <typename IO, int LANES, int NV, bool VEC>
 hipError_t launch_norm_t(NormDev p, bool backward, int gate, hipStream_t st) {
   constexpr int PER = 256 / LANES;
-  const int64_t blocks = backward ? (p.groups + PER - 1) / PER * p.nsplit : (p.rows * p.groups + PER - 1) / PER;
+  constexpr int64_t fwd = PER * norm_units<LANES, NV>();
+  const int64_t blocks = backward ? (p.groups + PER - 1) / PER * p.nsplit : (p.rows * p.groups + fwd - 1) / fwd;
   auto run = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p);
     return hipGetLastError();
@@ -286,7 +314,7 @@ Shape shape_of(int64_t n, int64_t es) {
   const int64_t vecs = (n * es + 15) / 16;
   Shape s{8, 1};
   while (s.lanes < 64 && s.lanes < vecs) s.lanes *= 2;
-  if (s.lanes * kMaxVec < vecs) s.lanes = 256;
+  if (s.lanes * 2 < vecs) s.lanes = 256;
   while (static_cast<int64_t>(s.lanes) * s.nv < vecs) s.nv *= 2;
   return s;
 }
@@ -297,14 +325,12 @@ hipError_t launch_norm_v(const NormDev& p, Shape s, bool backward, int gate, hip
     if (s.lanes == 8) return launch_norm_t<IO, 8, 1, VEC>(p, backward, gate, st);
     if (s.lanes == 16) return launch_norm_t<IO, 16, 1, VEC>(p, backward, gate, st);
     if (s.lanes == 32) return launch_norm_t<IO, 32, 1, VEC>(p, backward, gate, st);
-    return launch_norm_t<IO, 64, 1, VEC>(p, backward, gate, st);
+    if (s.lanes == 64) return launch_norm_t<IO, 64, 1, VEC>(p, backward, gate, st);
+    return launch_norm_t<IO, 256, 1, VEC>(p, backward, gate, st);
   }
-  if (s.lanes == 64) {
-    if (s.nv == 2) return launch_norm_t<IO, 64, 2, VEC>(p, backward, gate, st);
-    if (s.nv == 4) return launch_norm_t<IO, 64, 4, VEC>(p, backward, gate, st);
-    return launch_norm_t<IO, 64, 8, VEC>(p, backward, gate, st);
-  }
-  if (s.nv <= 4) return launch_norm_t<IO, 256, 4, VEC>(p, backward, gate, st);
+  if (s.lanes == 64) return launch_norm_t<IO, 64, 2, VEC>(p, backward, gate, st);
+  if (s.nv == 2) return launch_norm_t<IO, 256, 2, VEC>(p, backward, gate, st);
+  if (s.nv == 4) return launch_norm_t<IO, 256, 4, VEC>(p, backward, gate, st);
   return launch_norm_t<IO, 256, 8, VEC>(p, backward, gate, st);
 }
 
@@ -329,7 +355,7 @@ int64_t norm_workgroups(const NormArgs& a, bool bf16) {
 
 hipError_t launch_column_sum(const float* part, int64_t count, int64_t cols, void* out, bool bf16, hipStream_t st) {
   auto kern = bf16 ? ssm_column_sum_kernel<BF16> : ssm_column_sum_kernel<F32>;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((cols + 63) / 64)), dim3(256), 0, st, part, count, cols, out);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((cols + 63) / 64)), dim3(1024), 0, st, part, count, cols, out);
   return hipGetLastError();
 }
 

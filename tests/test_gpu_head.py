@@ -4,7 +4,7 @@ Tolerances, element by element.  Let B be the result with every product taken in
 |q|, |k|, |v|, |do|): any float32 sum of the same products is off by at most n 2^-24 B, n the additions in a row
 (products over d, a chunk of at most 64, two per chunk for the state, and a few roundings of decays and scales).
 bfloat16 adds half a step of the output, 2^-8 |result|, and what scores and the state lose in two parts, 2^-16 B each.  dg is a sum of dots of q with dq and k with dk before those are rounded, scores in two parts (2^-16 B each),
-from a segment's end (at most 1024 tokens) to the token, plus <R, S> there.
+from a segment's end (at most 1024 tokens for float32, 4096 for bfloat16) to the token, plus <R, S> there.
 """
 import numpy as np
 import pytest
@@ -125,7 +125,8 @@ def test_backward(case, dtype, mode):
     ab1 = {**ab, "q": np.repeat(ab["q"], rep, 2), "k": np.repeat(ab["k"], rep, 2)}
     Bh = head.head_scan_bwd(do=np.abs(num(do)), dlast=None if dlast is None else np.abs(num(dlast)), **ab1)
     dots = (ab1["q"] * Bh["dq"]).sum(-1) + (ab1["k"] * Bh["dk"]).sum(-1)
-    span = np.stack([dots[:, t:(t // 1024 + 1) * 1024].sum(1) for t in range(L)], 1)
+    reach = 4096 if dtype == torch.bfloat16 else 1024
+    span = np.stack([dots[:, t:(t // reach + 1) * reach].sum(1) for t in range(L)], 1)
     each = adds(x) * 2.0 ** -24 + (2.0 ** -15 if dtype == torch.bfloat16 else 0)
     half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
     # <R, S> of a segment's end is at most B's dg there plus what it lost on the way, which `span` holds

@@ -255,3 +255,32 @@ def test_block_step_follows_prompt():
     # both sides are float32 chains: 2-norm within twice the chain's bound above
     assert float((got - whole).norm() / whole.norm()) <= 2 * 7 * 100 * U
     assert float((state - last).norm() / last.norm()) <= 2 * 7 * 100 * U
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_linear_large_tiles(act):
+    """Sizes that take the 256 x 256 tiles: ragged rows, columns and k tails in all three products, split sums in dW."""
+    rows, k, m = 3336, 1928, 3592
+    x, W, bias, res, dout = linear_case((rows, k, m), torch.bfloat16, seed=8)
+    out, pre = ssm.ssm_linear(x, W, bias, res, act, return_pre=True)
+    got = ssm.ssm_linear_bwd(x, W, dout, pre if act != "none" else None, act)
+    torch.cuda.synchronize(DEV)
+    # sampled rows and columns against the oracle: the tiles' corners and edges, and some inside
+    rs = np.unique(np.r_[0, 15, 16, 255, 256, 257, 1000, 2047, 2048, rows - 9, rows - 8, rows - 1])
+    cs = np.unique(np.r_[0, 63, 255, 256, 511, 1536, 1799, 1927])
+    half_ = half(torch.bfloat16)
+    X, Wn, D, P = num(x), num(W), num(dout), num(pre)
+    wo, wp = layer.linear(X[rs], Wn, num(bias), num(res)[rs], act)
+    E = (k + 16) * U * (np.abs(X[rs]) @ np.abs(Wn).T + np.abs(num(bias)))
+    close("pre", pre[rs], wp, half_ * np.abs(wp) + E)
+    close("out", out[rs], wo, half_ * np.abs(wo) + 1.13 * E + 16 * U * (1 + np.abs(wp)) ** 2
+          + 2 * U * (np.abs(wo) + np.abs(num(res)[rs])))
+    dp = D if act == "none" else D * layer.act(P, act)[1]
+    low = half_ if act != "none" else 0.0
+    ed = 64 * U * np.abs(D) * (1 + np.abs(P)) ** 2 * (act != "none")
+    wx = dp[rs] @ Wn
+    close("dx", got[0][rs], wx, half_ * np.abs(wx) + ((low + (m + 16) * U) * np.abs(dp[rs]) + 1.01 * ed[rs]) @ np.abs(Wn))
+    ww = dp.T @ X[:, cs]
+    close("dW", got[1][:, cs], ww, half_ * np.abs(ww) + ((low + (rows + 16) * U) * np.abs(dp) + 1.01 * ed).T @ np.abs(X[:, cs]))
+    wb = dp.sum(0)
+    close("dbias", got[2], wb, half_ * np.abs(wb) + ((rows + 16) * U * np.abs(dp) + 1.01 * ed).sum(0))
