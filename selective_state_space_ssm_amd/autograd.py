@@ -19,6 +19,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (ssm_gate_norm, ssm_gate_norm_bwd, ssm_head_scan_bwd, ssm_head_scan_fwd, ssm_linear, ssm_linear_bwd,
                ssm_out_proj, ssm_out_proj_bwd, ssm_scan_bwd, ssm_scan_bwd_conv,
@@ -123,6 +124,7 @@ class _HeadScan(torch.autograd.Function):
         return o, last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, dlast):
         q, k, v, g, h0, g_head, lengths = ctx.saved_tensors
         r = ssm_head_scan_bwd(q, k, v, v.new_zeros(v.shape) if do is None else do.contiguous(), g=g, g_head=g_head, h0=h0, lengths=lengths,
@@ -149,6 +151,7 @@ class _GateNorm(torch.autograd.Function):
         return ssm_gate_norm(x, weight, z, **ctx.opts)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, z = ctx.saved_tensors
         dx, dw, dz = ssm_gate_norm_bwd(x, dy.contiguous(), weight, z, want_dweight=ctx.needs_input_grad[1], **ctx.opts)
@@ -173,6 +176,7 @@ class _Linear(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         x, W, pre = ctx.saved_tensors
         need = ctx.needs_input_grad

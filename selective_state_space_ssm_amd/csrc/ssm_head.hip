@@ -121,8 +121,10 @@ __global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, co
     for (int w = 0; w < wave; ++w) before += sh[w];
     carry += (sh[0] + sh[1]) + (sh[2] + sh[3]);
     if (t >= t0) {
-      // nothing is decayed at the first token of a sequence that starts from zero
-      const bool none = t >= len || (t == 0 && p.h0 == nullptr);
+      // nothing is decayed at the first token of a sequence that starts from zero, or where the state starts anew
+      const bool none = t >= len || (t == 0 && p.h0 == nullptr) ||
+                        headk::decay_at<IO>(p, static_cast<int>(b), static_cast<int>(h), static_cast<int>(t)) ==
+                            headk::kMinLog2Decay;
       const float out = none ? 0.f : static_cast<float>(before + v);
       IO::template st<1>(static_cast<typename IO::T*>(dg) + (b * p.L + t) * p.H + h, &out);
     }

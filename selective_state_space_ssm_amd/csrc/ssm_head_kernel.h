@@ -35,6 +35,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ssm_device.h"
 #include "ssm_kernels.h"
 
@@ -754,10 +756,19 @@ hipError_t launch_head_t(const HeadDev& p, hipStream_t st) {
   const int64_t wgs = nrun * p.ntile * p.H * p.batch;
   constexpr size_t smem = head_lds_bytes<IO, ROWS, NW, NC, MODE, DOT>();
   auto kern = ssm_head_kernel<IO, ROWS, NW, NC, MODE, DOT, VEC>;
-  if (smem > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if constexpr (smem > 65536) {
+    // asked for once per device (the call costs as much as a launch)
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev > 63 || (allowed.load(std::memory_order_relaxed) & bit) == 0) {
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(smem));
+      if (e != hipSuccess) return e;
+      if (dev <= 63) allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
   }
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(wgs)), dim3(64 * NW), smem, st, p);
   return hipGetLastError();

@@ -646,11 +646,12 @@ __global__ void __launch_bounds__(512) ssm_linear_rows_kernel(LinDev p) {
   }
 }
 
-// dpre = dout act'(pre), and its column sums over this workgroup's rows:
-// thread (cv, rr) takes CNT columns of rows rr, rr + 8, ...
+// dpre = dout act'(pre), and its column sums over this workgroup's rows (into
+// dbias where it has them all): thread (cv, rr) takes CNT columns of rows rr,
+// rr + 8, ...
 template <typename IO, int CNT>
 __global__ void __launch_bounds__(256) ssm_linear_dpre_kernel(const void* dout, const void* pre, void* dpre, float* part,
-                                                             int64_t rows, int64_t m, int64_t per, int act) {
+                                                             void* dbias, int64_t rows, int64_t m, int64_t per, int act) {
   using T = typename IO::T;
   __shared__ float sh[8][32 * CNT];
   const int cv = threadIdx.x & 31, rr = threadIdx.x >> 5;
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(256) ssm_linear_dpre_kernel(const void* dout, 
       for (int e = 0; e < CNT; ++e) s[e] += d[e];
     }
   }
-  if (part == nullptr) return;
+  if (part == nullptr && dbias == nullptr) return;
 #pragma unroll
   for (int e = 0; e < CNT; ++e) sh[rr][cv * CNT + e] = s[e];
   __syncthreads();
@@ -683,7 +684,8 @@ __global__ void __launch_bounds__(256) ssm_linear_dpre_kernel(const void* dout, 
       float v = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) v += sh[k][i];
-      part[blockIdx.y * m + col] = v;
+      if (dbias != nullptr) IO::template st<1>(static_cast<T*>(dbias) + col, &v);
+      else part[blockIdx.y * m + col] = v;
     }
   }
 }
@@ -843,10 +845,12 @@ hipError_t backward_io(const LinearArgs& a, char* work, hipStream_t st) {
   if (a.act != kActNone || a.dbias != nullptr) {
     const bool vec = a.m % E == 0;
     const int64_t per = dpre_rows(a, 32 * (vec ? E : 1)), nblk = cdiv(a.rows, per);
-    float* part = a.dbias != nullptr ? reinterpret_cast<float*>(work + w.colsum) : nullptr;
+    float* part = a.dbias != nullptr && nblk > 1 ? reinterpret_cast<float*>(work + w.colsum) : nullptr;
+    void* dbias = nblk > 1 ? nullptr : a.dbias;
     auto kern = vec ? ssm_linear_dpre_kernel<IO, E> : ssm_linear_dpre_kernel<IO, 1>;
     hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(cdiv(a.m, 32 * (vec ? E : 1))), static_cast<unsigned>(nblk)),
-                       dim3(256), 0, st, a.dout, a.pre, static_cast<void*>(work + w.dpre), part, a.rows, a.m, per, a.act);
+                       dim3(256), 0, st, a.dout, a.pre, static_cast<void*>(work + w.dpre), part, dbias, a.rows, a.m,
+                       per, a.act);
     e = hipGetLastError();
     if (e == hipSuccess && part != nullptr)
       e = launch_column_sum(part, nblk, a.m, a.dbias, std::is_same<IO, BF16>::value, st);
