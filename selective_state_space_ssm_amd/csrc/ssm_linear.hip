@@ -723,10 +723,20 @@ int64_t up16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 int64_t up(int64_t n, int64_t to) { return cdiv(n, to) * to; }
 
-// One product's tile (32 t x 32 t) and split of k.  bfloat16 takes 256 x 256
-// tiles (t = 8) where they, with k in parts of at least 1024, give three
-// quarters of the CUs a workgroup; else the larger of 128 and 64 that gives
-// every CU one, and below that 64 with k in parts of at least four steps.
+// One product's tile (32 t x 32 t) and split of k.
+//   bfloat16 takes 256 x 256 tiles (t = 8) where they, with k in parts of at
+//   least 1024, give three quarters of the CUs a workgroup (products of 16384 x
+//   4096 x 2048: 287 to 360 us, 128 x 128 tiles 420 to 470).
+//   Else 128 x 128 where they, with k in parts of at least 16 steps, give as
+//   many (300 x 4096 -> 2048: bfloat16 25 us, float32 73; 64 x 64: 40 and 103;
+//   forward and gradients of 4099 x 768 -> 1536 in float32: 339, 64 x 64 where
+//   there are fewer tiles than CUs: 431).  k is split for one or for two
+//   workgroups a CU, whichever leaves a CU less to do, two where it is the same
+//   (1024 x 4096 -> 1024 in float32: 82 us, one: 89; 2048 x 768 -> 1536, where
+//   two do not come out even: 247, one: 215).
+//   Below that 64 x 64, k in parts of at least four steps, split for one
+//   workgroup a CU (64 x 4096 -> 2048: bfloat16 15.3 us, float32 22.7; for two:
+//   19.4 and 24.5).
 struct Tiling {
   int t;
   int64_t kpart, nsplit;
@@ -745,10 +755,14 @@ Tiling tiling(int64_t nc, int64_t nr, int64_t K) {
     if (4 * tiles(8) * split >= 3 * kCUs) w.t = 8;
   }
   if (w.t != 8) {
-    if (tiles(4) >= kCUs) w.t = 4;
-    split = w.t == 2 && tiles(2) < kCUs ? kCUs / tiles(2) : 1;
-    if (split > steps / 4) split = steps / 4;
-    if (split < 1) split = 1;
+    if (4 * tiles(4) * (steps >= 16 ? steps / 16 : 1) >= 3 * kCUs) w.t = 4;
+    const int64_t n = tiles(w.t), most = steps / (w.t == 4 ? 16 : 4);
+    auto parts = [&](int64_t wgs) {
+      const int64_t s = wgs / n < most ? wgs / n : most;
+      return s < 1 ? 1 : s;
+    };
+    const int64_t one = parts(kCUs), two = w.t == 4 ? parts(2 * kCUs) : one;
+    split = cdiv(n * two, kCUs) * one <= cdiv(n * one, kCUs) * two ? two : one;
   }
   w.kpart = cdiv(steps, split) * BK;
   w.nsplit = cdiv(K, w.kpart);
