@@ -602,21 +602,37 @@ __global__ void __launch_bounds__(256) ssm_linear_pack_kernel(PackDev p) {
 }
 
 // Few rows (up to 16): one launch whose traffic is W's.  A workgroup of eight
-// wavefronts owns 16 columns; wavefront w takes every eighth step of k, reads
+// wavefronts owns COLS columns; wavefront w takes every eighth run of DEPTH steps of k, reads
 // both operands straight from memory (a lane reads 16 bytes of one row of W and
 // of x), and the eight partial 16 x 16 tiles meet in LDS.
-template <typename IO, bool VEC>
+// COLS = 8 (up to 8 rows): lanes 8 to 15 of a group of 16 hold the same columns
+// and rows, one instruction's k further on, so that two diagonal quarters of
+// the tile are halves of the sum and there are twice the workgroups: where 16
+// columns give no more than every CU one, 8 x 4096 -> 2048 in bfloat16 takes 6.7
+// us with 8 columns and 9.0 with 16 (W alone at the rate of a large copy: 3.5;
+// the rest is the launch, one trip to memory and the sum through LDS).  With
+// more columns 16 are at that rate: 8 x 4096 -> 8192 14.9 us, 4.5 TB/s.
+template <typename IO, int COLS, bool VEC>
 __global__ void __launch_bounds__(512) ssm_linear_rows_kernel(LinDev p) {
   using C = LinCfg<IO>;
   constexpr int E = C::E, ES = C::ES, BK = 4 * E, DEPTH = 8;  // k per instruction (chunk of four lanes), steps in flight
+  using T = typename IO::T;
+  constexpr int STEP = BK * 16 / COLS;
   __shared__ float part[8][16][17];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int half = li / COLS, mine = li % COLS;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * COLS;
   const char* const cbase = p.c + c0 * p.ldc * ES;
   const Rsrc rc = make_rsrc(cbase, kRecords), rr = make_rsrc(p.r, kRecords);
-  const bool cok = c0 + li < p.nc, rok = li < p.nr;
-  const uint32_t cb = static_cast<uint32_t>(li * p.ldc * ES), rb = static_cast<uint32_t>(li * p.ldr * ES);
+  const bool cok = c0 + mine < p.nc, rok = mine < p.nr;
+  const uint32_t cb = static_cast<uint32_t>(mine * p.ldc * ES), rb = static_cast<uint32_t>(mine * p.ldr * ES);
+  // what the epilogue adds is on its way during the products
+  const int er = tid / COLS, ec = tid % COLS;
+  const bool eok = er < COLS && er < p.nr && c0 + ec < p.nc;
+  float bias = 0.f, res = 0.f;
+  if (eok && p.bias != nullptr) IO::template ld<1>(reinterpret_cast<const T*>(p.bias) + c0 + ec, &bias);
+  if (eok && p.residual != nullptr) IO::template ld<1>(reinterpret_cast<const T*>(p.residual) + er * p.nc + c0 + ec, &res);
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   // 16 bytes from p on, the first `have` values of them
   auto fetch = [&](Rsrc rs, const char* base, uint32_t off, int have) {
@@ -627,18 +643,18 @@ __global__ void __launch_bounds__(512) ssm_linear_rows_kernel(LinDev p) {
     } else if (have == E) {
       __builtin_memcpy(&o, base + off, 16);  // aligned to an element
     } else if (have > 0) {
-      typename IO::T v[E];
+      T v[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = e < have ? reinterpret_cast<const typename IO::T*>(base + off)[e] : typename IO::T(0);
+      for (int e = 0; e < E; ++e) v[e] = e < have ? reinterpret_cast<const T*>(base + off)[e] : T(0);
       __builtin_memcpy(&o, v, 16);
     }
     return o;
   };
-  for (int64_t k0 = wave * BK; k0 < p.K; k0 += 8 * BK * DEPTH) {
+  for (int64_t k0 = wave * STEP * DEPTH; k0 < p.K; k0 += 8 * STEP * DEPTH) {
     uint4 fc[DEPTH], fr[DEPTH];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      const int64_t k = k0 + d * 8 * BK + g * E, left = p.K - k;
+      const int64_t k = k0 + d * STEP + half * BK + g * E, left = p.K - k;
       const int have = left > E ? E : (left > 0 ? static_cast<int>(left) : 0);
       fc[d] = fetch(rc, cbase, cb + static_cast<uint32_t>(k * ES), cok ? have : 0);
       fr[d] = fetch(rr, p.r, rb + static_cast<uint32_t>(k * ES), rok ? have : 0);
@@ -660,14 +676,16 @@ __global__ void __launch_bounds__(512) ssm_linear_rows_kernel(LinDev p) {
 #pragma unroll
   for (int v = 0; v < 4; ++v) part[wave][li][4 * g + v] = acc[v];
   __syncthreads();
-  if (tid < 256) {
-    const int r = tid >> 4, c = tid & 15;
-    if (r < p.nr && c0 + c < p.nc) {
-      float v = 0.f;
+  if (eok) {
+    float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) v += part[w][r][c];
-      epilogue<IO, 1>(p, r, c0 + c, &v);
-    }
+    for (int w = 0; w < 8; ++w)
+      v += COLS == 16 ? part[w][er][ec] : part[w][er][ec] + part[w][8 + er][8 + ec];
+    v += bias;
+    const int64_t at = er * p.nc + c0 + ec;
+    if (p.pre != nullptr) IO::template st<1>(reinterpret_cast<T*>(p.pre) + at, &v);
+    v = act_of(v, p.act) + res;
+    IO::template st<1>(reinterpret_cast<T*>(p.out) + at, &v);
   }
 }
 
@@ -870,8 +888,10 @@ hipError_t forward_io(const LinearArgs& a, char* work, hipStream_t st) {
   p.bias = static_cast<const char*>(a.bias); p.residual = static_cast<const char*>(a.residual);
   p.pre = static_cast<char*>(a.pre); p.act = a.act;
   if (a.rows <= kFewRows) {
-    auto kern = a.k % LinCfg<IO>::E == 0 ? ssm_linear_rows_kernel<IO, true> : ssm_linear_rows_kernel<IO, false>;
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(cdiv(a.m, 16))), dim3(512), 0, st, p);
+    const bool vec = a.k % LinCfg<IO>::E == 0, few = a.rows <= 8 && cdiv(a.m, 16) <= kCUs;
+    auto kern = few ? (vec ? ssm_linear_rows_kernel<IO, 8, true> : ssm_linear_rows_kernel<IO, 8, false>)
+                    : (vec ? ssm_linear_rows_kernel<IO, 16, true> : ssm_linear_rows_kernel<IO, 16, false>);
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(cdiv(a.m, few ? 8 : 16))), dim3(512), 0, st, p);
     return hipGetLastError();
   }
   return product<IO, false, false>(p, work, st);
