@@ -752,6 +752,9 @@ int64_t up(int64_t n, int64_t to) { return cdiv(n, to) * to; }
 //   workgroups a CU, whichever leaves a CU less to do, two where it is the same
 //   (1024 x 4096 -> 1024 in float32: 82 us, one: 89; 2048 x 768 -> 1536, where
 //   two do not come out even: 247, one: 215).
+//   float32, which the matrix instructions bound, takes 96 x 96 where the last of
+//   them leave fewer CUs idle (4099 x 768 -> 1536: 107 us, 128 x 128: 118; 6000 x
+//   2048 -> 1024: 232, 265).
 //   Below that 64 x 64, k in parts of at least four steps, split for one
 //   workgroup a CU (64 x 4096 -> 2048: bfloat16 15.3 us, float32 22.7; for two:
 //   19.4 and 24.5).
@@ -774,13 +777,22 @@ Tiling tiling(int64_t nc, int64_t nr, int64_t K) {
   }
   if (w.t != 8) {
     if (4 * tiles(4) * (steps >= 16 ? steps / 16 : 1) >= 3 * kCUs) w.t = 4;
-    const int64_t n = tiles(w.t), most = steps / (w.t == 4 ? 16 : 4);
-    auto parts = [&](int64_t wgs) {
-      const int64_t s = wgs / n < most ? wgs / n : most;
+    auto parts = [&](int t, int64_t wgs, int64_t least) {
+      const int64_t s = wgs / tiles(t) < steps / least ? wgs / tiles(t) : steps / least;
       return s < 1 ? 1 : s;
     };
-    const int64_t one = parts(kCUs), two = w.t == 4 ? parts(2 * kCUs) : one;
-    split = cdiv(n * two, kCUs) * one <= cdiv(n * one, kCUs) * two ? two : one;
+    // what the fullest CU has to do, in 32 x 32 tiles times s
+    auto load = [&](int t, int64_t s) { return cdiv(tiles(t) * s, kCUs) * t * t; };
+    if (w.t == 4) {
+      const int64_t one = parts(4, kCUs, 16), two = parts(4, 2 * kCUs, 16);
+      split = load(4, two) * one <= load(4, one) * two ? two : one;
+      if (std::is_same<IO, F32>::value && load(3, 1) * split < load(4, split)) {
+        w.t = 3;
+        split = 1;
+      }
+    } else {
+      split = parts(2, kCUs, 4);
+    }
   }
   w.kpart = cdiv(steps, split) * BK;
   w.nsplit = cdiv(K, w.kpart);
@@ -867,7 +879,10 @@ hipError_t product(LinDev p, char* work, hipStream_t st) {
   if (q.w.t == 8) {
     if constexpr (std::is_same<IO, BF16>::value) e = run(std::integral_constant<int, 8>{});
   } else {
-    e = q.w.t == 4 ? run(std::integral_constant<int, 4>{}) : run(std::integral_constant<int, 2>{});
+    if constexpr (std::is_same<IO, F32>::value)
+      if (q.w.t == 3) e = run(std::integral_constant<int, 3>{});
+    if (q.w.t == 4) e = run(std::integral_constant<int, 4>{});
+    if (q.w.t == 2) e = run(std::integral_constant<int, 2>{});
   }
   if (e != hipSuccess || !q.part) return e;
   const bool four = p.nc % 4 == 0;
