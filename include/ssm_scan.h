@@ -416,8 +416,8 @@ int ssm_out_proj_bwd(const void *y, const void *W, const void *dout, void *dy, v
  *   d_key, d_value <= 256; batch * n_heads <= 65535; n_heads a multiple of
  *   n_qk_heads.
  * Rounding: sums, decays and the state are float32.  With SSM_BF16 the scores
- * q_i . k_j (decayed) are rounded to bfloat16 once and the state enters o's
- * product as a pair of bfloat16.  A non-finite k or v reaches every output of its
+ * q_i . k_j (decayed) and the state enter o's products as pairs of bfloat16
+ * (off by 2^-17 of themselves).  A non-finite k or v reaches every output of its
  * token's chunk (64 tokens, 32 for float32), those before it included.
  * Errors: SSM_EINVAL, SSM_EUNSUPPORTED, SSM_EHIP.  No memory is allocated.
  */
@@ -520,8 +520,9 @@ int ssm_gate_norm_workspace(int64_t rows, int64_t channels, int64_t groups, int 
  *   out  : [rows, d_out], dtype `dtype`, output.
  *   pre  : as out, output, nullable: the value before act, for ssm_linear_bwd.
  *   workspace : ssm_linear_workspace(..., backward = 0) bytes (may be 0).
- *   d_in, d_out < 2^21.  Any size is accepted; the fastest path needs d_in and
- *   d_out multiples of 8 (bfloat16) or 4 (float32).
+ *   d_in, d_out < 2^21, any sizes.  Where d_in is no multiple of 8 (bfloat16) or
+ *   4 (float32) the workspace holds padded copies of x and W, where d_out is
+ *   none, float32 sums (more than 16 rows; the backward likewise).
  * Sums are float32; the epilogue works on the unrounded sum.
  * Errors: SSM_EINVAL, SSM_EUNSUPPORTED, SSM_EHIP.
  */

@@ -32,6 +32,13 @@ def _grad_or_zero(g, like):
     return torch.zeros_like(like) if g is None else g.contiguous()
 
 
+def _dense(g):
+    """A gradient as the library takes it: contiguous and 16-byte aligned (that of a concatenation is a view of any
+    alignment)."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, u, delta, A, B, C, D, z, delta_bias, h0, delta_softplus, state_chunk):
@@ -127,8 +134,8 @@ class _HeadScan(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, do, dlast):
         q, k, v, g, h0, g_head, lengths = ctx.saved_tensors
-        r = ssm_head_scan_bwd(q, k, v, v.new_zeros(v.shape) if do is None else do.contiguous(), g=g, g_head=g_head, h0=h0, lengths=lengths,
-                              dlast=None if dlast is None else dlast.contiguous(), scale=ctx.scale,
+        r = ssm_head_scan_bwd(q, k, v, v.new_zeros(v.shape) if do is None else _dense(do), g=g, g_head=g_head, h0=h0,
+                              lengths=lengths, dlast=None if dlast is None else _dense(dlast), scale=ctx.scale,
                               want_dg=ctx.needs_input_grad[3], want_dh0=ctx.needs_input_grad[4])
         return r["dq"], r["dk"], r["dv"], r["dg"], r["dh0"], None, None, None
 
@@ -154,7 +161,7 @@ class _GateNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, weight, z = ctx.saved_tensors
-        dx, dw, dz = ssm_gate_norm_bwd(x, dy.contiguous(), weight, z, want_dweight=ctx.needs_input_grad[1], **ctx.opts)
+        dx, dw, dz = ssm_gate_norm_bwd(x, _dense(dy), weight, z, want_dweight=ctx.needs_input_grad[1], **ctx.opts)
         return dx, dw, dz, None, None, None, None
 
 
@@ -180,7 +187,7 @@ class _Linear(torch.autograd.Function):
     def backward(ctx, dout):
         x, W, pre = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dout = dout.contiguous()
+        dout = _dense(dout)
         dx = dW = db = None
         if any(need[:3]):
             dx, dW, db = ssm_linear_bwd(x, W, dout, pre, ctx.act, want_dx=need[0], want_dW=need[1], want_dbias=need[2])

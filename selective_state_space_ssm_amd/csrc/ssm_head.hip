@@ -131,7 +131,9 @@ __global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, co
   }
 }
 
-// out[t][hk][e] = sum over the heads that share hk of part[t][h][e], V values a thread
+// out[t][hk][e] = sum over the heads that share hk of part[t][h][e], V values a
+// thread.  The parts stay float32: 64 heads of 128 over 4 x 2048 tokens are 268 MB,
+// 58 us to read (4.6 TB/s).
 template <typename IO, int V>
 __global__ void __launch_bounds__(256) ssm_head_group_sum_kernel(const float* part, void* out, int64_t n, int64_t d,
                                                                 int64_t rep) {
@@ -151,7 +153,8 @@ __global__ void __launch_bounds__(256) ssm_head_group_sum_kernel(const float* pa
 // One token.  A workgroup owns one (batch row, head) and 32 columns of the
 // state: thread (rg, c) takes rows rg + 32 i, columns 4 c .. 4 c + 3.  Every
 // load is issued before the first store (the update may be in place); the
-// bound is the state's traffic, 8 bytes per value.
+// bound is the state's traffic, 8 bytes per value: 256 rows of 32 heads of 128 x
+// 128 take 192 us, 5.6 TB/s.
 struct HeadStepDev {
   const char* q;
   const char* k;

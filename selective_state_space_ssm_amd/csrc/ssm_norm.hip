@@ -21,6 +21,10 @@
 // that many wavefronts' loads are in flight).  In the forward small groups are
 // taken several at a time by the same lanes, for the same reason.
 //
+// Measured: 16384 x 4096 in 32 groups, bfloat16, 100 us (4.0 TB/s; one group at
+// a time 142); 8191 x 1536 in one group, float32, forward 24 us and backward
+// 44 (the backward with 64 lanes and eight vectors each: 124).
+//
 // dw is a sum over rows: every workgroup of the backward walks rows of one
 // group, keeps its sum in registers and leaves one float32 partial; a second
 // launch adds the partials in order (the same bits on every call).
