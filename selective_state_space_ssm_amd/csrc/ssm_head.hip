@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, co
 }
 
 // out[t][hk][e] = sum over the heads that share hk of part[t][h][e], V values a
-// thread.  The parts stay float32: 64 heads of 128 over 4 x 2048 tokens are 268 MB,
-// 58 us to read (4.6 TB/s).
+// thread.  The parts stay float32: 32 pairs of heads of 128 over 4 x 2048 tokens are
+// 134 MB, 30 us to read (4.4 TB/s).
 template <typename IO, int V>
 __global__ void __launch_bounds__(256) ssm_head_group_sum_kernel(const float* part, void* out, int64_t n, int64_t d,
                                                                 int64_t rep) {
@@ -379,13 +379,24 @@ Plan bwd_plan(const HeadArgs& a, bool bf16) {
   return plan_of(a.batch, a.H, t1 < t2 ? t1 : t2, a.L, bf16, true, all_vec(a, bf16));
 }
 
+// Heads whose parts of dq and dk a workgroup adds (kOutPair) where q and k are
+// shared: two if that leaves every CU a workgroup.  4 x 2048 tokens, 64 heads of
+// 128 x 64, bfloat16: the two passes 149 us each and their sums 30; one head a
+// workgroup 154 and 58.
+int64_t part_heads(const HeadArgs& a, const Plan& pl, bool bf16) {
+  return bf16 && pl.vec && a.dv <= headk::kPairRows && a.H / a.Hk % 2 == 0 &&
+                 a.batch * a.H / 2 * tiles_for(a.dk, true) * pl.nseg >= kHeadCUs
+             ? 2
+             : 1;
+}
+
 template <typename IO>
-hipError_t launch_group_sum(const float* part, void* out, const HeadArgs& a, hipStream_t st) {
+hipError_t launch_group_sum(const float* part, void* out, const HeadArgs& a, int64_t heads, hipStream_t st) {
   const int64_t n = a.batch * a.L * a.Hk * a.dk;
   const bool four = a.dk % 4 == 0;
   auto kern = four ? ssm_head_group_sum_kernel<IO, 4> : ssm_head_group_sum_kernel<IO, 1>;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(cdiv(n, four ? 1024 : 256))), dim3(256), 0, st, part, out, n, a.dk,
-                     a.H / a.Hk);
+                     a.H / a.Hk / heads);
   return hipGetLastError();
 }
 
@@ -459,8 +470,9 @@ hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t
   dk.seg_state = r_seg; dk.seg_decay = dv.seg_decay;
 
   // the float32 parts of shared heads come with their dots, wanted or not
-  const int mode = shared && bf16 ? headk::kOutF32 : headk::kOut;
-  if (dg || mode == headk::kOutF32) {
+  const int64_t heads = shared ? part_heads(a, pl, bf16) : 1;
+  const int mode = !shared || !bf16 ? headk::kOut : (heads == 2 ? headk::kOutPair : headk::kOutF32);
+  if (dg || mode != headk::kOut) {
     dq.dotv = static_cast<const char*>(a.q); dq.dot_b = a.q_b * es; dq.dot_t = static_cast<uint32_t>(a.q_t * es);
     dq.dot_rep = rep; dq.dot_out = rq;
     dk.dotv = static_cast<const char*>(a.k); dk.dot_b = a.k_b * es; dk.dot_t = static_cast<uint32_t>(a.k_t * es);
@@ -484,11 +496,11 @@ hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t
     e = hipGetLastError();
   }
   if (e == hipSuccess && shared) {
-    e = bf16 ? launch_group_sum<BF16>(static_cast<const float*>(pq), a.dq, a, st)
-             : launch_group_sum<F32>(static_cast<const float*>(pq), a.dq, a, st);
+    e = bf16 ? launch_group_sum<BF16>(static_cast<const float*>(pq), a.dq, a, heads, st)
+             : launch_group_sum<F32>(static_cast<const float*>(pq), a.dq, a, heads, st);
     if (e == hipSuccess)
-      e = bf16 ? launch_group_sum<BF16>(static_cast<const float*>(pk), a.dk_out, a, st)
-               : launch_group_sum<F32>(static_cast<const float*>(pk), a.dk_out, a, st);
+      e = bf16 ? launch_group_sum<BF16>(static_cast<const float*>(pk), a.dk_out, a, heads, st)
+               : launch_group_sum<F32>(static_cast<const float*>(pk), a.dk_out, a, heads, st);
   }
   return e;
 }

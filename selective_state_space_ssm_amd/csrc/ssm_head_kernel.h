@@ -277,8 +277,12 @@ __device__ __forceinline__ float decay_at(const HeadDev& p, int b, int h, int t)
 // MODE: kOut writes o (and the last state), kOutF32 writes it in float32
 // whatever the storage type (per-head parts of a shared head's gradient),
 // kState only the segment's own end state (from zero, or from the start state
-// for the first segment) and decay.
-constexpr int kOut = 0, kState = 1, kOutF32 = 2;
+// for the first segment) and decay.  kOutPair is kOutF32 with two neighbouring
+// heads, whose outputs it adds, in a workgroup of twice the wavefronts: half
+// the parts to write and to read again.
+constexpr int kOut = 0, kState = 1, kOutF32 = 2, kOutPair = 3;
+template <int MODE>
+constexpr int heads_of() { return MODE == kOutPair ? 2 : 1; }
 
 // Bytes of LDS: y and z tiles, x tile, scores (bfloat16: hi and lo), the
 // chunk's decays, and the wavefronts' dots.
@@ -289,6 +293,9 @@ constexpr size_t head_lds_bytes() {
   constexpr size_t sc = size_t(K::C) * K::C * K::ES * (K::ES == 2 ? 2 : 1);
   return xy + z + 4 * K::C * 4 + (MODE != kState ? xy + sc : 0) + (DOT ? size_t(NW) * K::C * 4 : 0);
 }
+// The outputs that the two heads of kOutPair exchange.
+template <typename IO, int NW, int NC, int MODE>
+constexpr size_t pair_lds_bytes() { return MODE == kOutPair ? size_t(HeadCfg<IO>::C) * 16 * NW * NC * 4 : 0; }
 
 // Wavefronts per SIMD the registers have to leave room for: what fits without spills.
 template <typename IO, int ROWS, int NW, bool DOT, bool VEC>
@@ -299,9 +306,11 @@ constexpr int head_waves() {
 }
 
 template <typename IO, int ROWS, int NW, int NC, int MODE, bool DOT, bool VEC>
-__global__ void __launch_bounds__(64 * NW, (head_waves<IO, ROWS, NW, DOT, VEC>())) ssm_head_kernel(const HeadDev p) {
+__global__ void __launch_bounds__((64 * NW * heads_of<MODE>()), (head_waves<IO, ROWS, NW, DOT, VEC>()))
+ssm_head_kernel(const HeadDev p) {
   using K = HeadCfg<IO>;
-  constexpr bool F32OUT = K::ES == 4 || MODE == kOutF32;
+  constexpr bool F32OUT = K::ES == 4 || MODE == kOutF32 || MODE == kOutPair;
+  constexpr int HEADS = heads_of<MODE>();
   constexpr int OES = F32OUT ? 4 : 2;  // bytes per output
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW * NC;
   constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;  // 16-byte chunks per LDS row
@@ -311,7 +320,9 @@ __global__ void __launch_bounds__(64 * NW, (head_waves<IO, ROWS, NW, DOT, VEC>()
   static_assert(LZ >= 1 && C * NZ % T == 0, "the z tile has the same share for every thread");
 
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  char* const ty = lds;
+  // with two heads the threads and all of LDS but the exchange are halved: below, everything is one head's
+  const int half = HEADS == 1 ? 0 : __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / T);
+  char* const ty = lds + half * static_cast<int>(head_lds_bytes<IO, ROWS, NW, NC, MODE, DOT>());
   char* const tz = ty + C * ROWS * ES;
   char* const tx = tz + C * COLS * ES;
   char* const tp = tx + C * ROWS * ES;
@@ -322,7 +333,7 @@ __global__ void __launch_bounds__(64 * NW, (head_waves<IO, ROWS, NW, DOT, VEC>()
   float* const we = eg + C;     // us e^{G_C - G_j}
   float* const red = we + C;    // [NW][C]
 
-  const int tid = threadIdx.x;
+  const int tid = static_cast<int>(threadIdx.x) - half * T;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   // Workgroups go to the 8 XCDs in turn.  The column tiles of a (batch row, head, segment), which share x and y, stay
@@ -341,8 +352,8 @@ __global__ void __launch_bounds__(64 * NW, (head_waves<IO, ROWS, NW, DOT, VEC>()
     const uint32_t nrun = MODE == kState ? p.nseg - 1 : p.nseg;
     seg = idx % nrun;
     idx /= nrun;
-    h = idx % p.H;
-    b = idx / p.H;
+    h = idx % (p.H / HEADS) * HEADS + half;
+    b = idx / (p.H / HEADS);
   }
   const int pseg = p.rev ? p.nseg - 1 - seg : seg;
   const int c0 = pseg * p.cps, c1 = c0 + p.cps < p.nch ? c0 + p.cps : p.nch;
@@ -459,20 +470,23 @@ __global__ void __launch_bounds__(64 * NW, (head_waves<IO, ROWS, NW, DOT, VEC>()
     load_tile(zb, p.z_t, vz, left_z, t0, ZN{}, rz, ZC{});
   };
 
-  // One chunk's outputs (physical chunk at t0; nothing is written with rows = 0), columns cw + 16 nc + 4 g + v
-  auto store_out = [&](const f32x4 (&O)[IB][NC], int t0, int rows, int li, int g) {
+  // One chunk's outputs (physical chunk at t0; nothing is written with rows = 0), columns cw + 16 nc + 4 g + v.  Of two
+  // heads each writes half of the blocks.
+  constexpr int OB = IB / HEADS;
+  const int oh = p.H / HEADS, ho = h / HEADS;
+  auto store_out = [&](const f32x4 (&O)[OB][NC], int t0, int rows, int li, int g) {
     const int lr = p.rev ? 15 - li : li;  // the lane's token in its block of 16
-    const uint32_t ts = static_cast<uint32_t>(p.H * p.cols * OES);
-    const char* const ob = p.o + ((static_cast<int64_t>(b) * p.L + t0) * p.H + h) * p.cols * OES;
+    const uint32_t ts = static_cast<uint32_t>(oh * p.cols * OES);
+    const char* const ob = p.o + ((static_cast<int64_t>(b) * p.L + t0) * oh + ho) * p.cols * OES;
 #pragma unroll
-    for (int ib = 0; ib < IB; ++ib) {
-      const int r0 = 16 * (p.rev ? IB - 1 - ib : ib);
+    for (int ob_ = 0; ob_ < OB; ++ob_) {
+      const int ib = half * OB + ob_, r0 = 16 * (p.rev ? IB - 1 - ib : ib);
       const Rsrc ro = make_rsrc(ob + static_cast<int64_t>(r0) * ts, row_bytes(rows - r0, 16, ts));
 #pragma unroll
       for (int nc = 0; nc < NC; ++nc) {
         const int c = cw + 16 * nc + 4 * g;
         const uint32_t off = lr * ts + static_cast<uint32_t>(c * OES);
-        const f32x4 v = O[ib][nc];
+        const f32x4 v = O[ob_][nc];
         if constexpr (VEC) {
           const uint32_t to = c < p.cols ? off : kOOB;
           if constexpr (F32OUT) {
@@ -510,7 +524,7 @@ __global__ void __launch_bounds__(64 * NW, (head_waves<IO, ROWS, NW, DOT, VEC>()
       // Loads and stores are counted together and in order.  With as many stores behind the first loads as the loop
       // has behind its own (these write nothing), the wait for a chunk's loads leaves the stores behind them in
       // flight on either way into the loop; without them it waits for every store to arrive.
-      const f32x4 none[IB][NC] = {};
+      const f32x4 none[OB][NC] = {};
       store_out(none, 0, 0, tid & 15, (tid & 63) >> 4);
     }
   }
@@ -714,9 +728,27 @@ __global__ void __launch_bounds__(64 * NW, (head_waves<IO, ROWS, NW, DOT, VEC>()
           if (g == 0) red[wave * C + 16 * ib + li] = dot;
         }
       }
-      store_out(O, t0, p.L - t0, li, g);
-      if constexpr (DOT) {
+      if constexpr (HEADS == 1) {
+        store_out(O, t0, p.L - t0, li, g);
+      } else {
+        f32x4* const ex = reinterpret_cast<f32x4*>(lds + 2 * head_lds_bytes<IO, ROWS, NW, NC, MODE, DOT>());
+        f32x4 mine[OB][NC];
+#pragma unroll
+        for (int ob = 0; ob < OB; ++ob)
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) {
+            ex[((half * OB + ob) * NC + nc) * T + tid] = half == 0 ? O[OB + ob][nc] : O[ob][nc];
+            mine[ob][nc] = half == 0 ? O[ob][nc] : O[OB + ob][nc];
+          }
         __syncthreads();
+#pragma unroll
+        for (int ob = 0; ob < OB; ++ob)
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) mine[ob][nc] += ex[(((1 - half) * OB + ob) * NC + nc) * T + tid];
+        store_out(mine, t0, p.L - t0, li, g);
+      }
+      if constexpr (DOT) {
+        if constexpr (HEADS == 1) __syncthreads();
         if (tid < C) {
           const int t = t0 + (p.rev ? C - 1 - tid : tid);
           float sum = 0.f;
@@ -732,8 +764,8 @@ __global__ void __launch_bounds__(64 * NW, (head_waves<IO, ROWS, NW, DOT, VEC>()
     // outputs (and dots) of the chunks past the length
     const int t1 = c1 * C < p.L ? c1 * C : p.L;
     for (int t = (ce > c0 ? ce : c0) * C + wave; t < t1; t += NW) {
-      char* const row = p.o + ((static_cast<int64_t>(b) * p.L + t) * p.H + h) * p.cols * OES;
-      for (int c = col0 + (tid & 63); c < col0 + COLS && c < p.cols; c += 64) {
+      char* const row = p.o + ((static_cast<int64_t>(b) * p.L + t) * oh + ho) * p.cols * OES;
+      for (int c = col0 + (tid & 63); half == 0 && c < col0 + COLS && c < p.cols; c += 64) {
         if constexpr (F32OUT) reinterpret_cast<float*>(row)[c] = 0.f;
         else reinterpret_cast<uint16_t*>(row)[c] = 0;
       }
@@ -766,8 +798,9 @@ __global__ void __launch_bounds__(64 * NW, (head_waves<IO, ROWS, NW, DOT, VEC>()
 template <typename IO, int ROWS, int NW, int NC, int MODE, bool DOT, bool VEC>
 hipError_t launch_head_t(const HeadDev& p, hipStream_t st) {
   const int64_t nrun = MODE == kState ? p.nseg - 1 : p.nseg;
-  const int64_t wgs = nrun * p.ntile * p.H * p.batch;
-  constexpr size_t smem = head_lds_bytes<IO, ROWS, NW, NC, MODE, DOT>();
+  constexpr int HEADS = heads_of<MODE>();
+  const int64_t wgs = nrun * p.ntile * (p.H / HEADS) * p.batch;
+  constexpr size_t smem = HEADS * head_lds_bytes<IO, ROWS, NW, NC, MODE, DOT>() + pair_lds_bytes<IO, NW, NC, MODE>();
   auto kern = ssm_head_kernel<IO, ROWS, NW, NC, MODE, DOT, VEC>;
   if constexpr (smem > 65536) {
     // asked for once per device (the call costs as much as a launch)
@@ -783,7 +816,7 @@ hipError_t launch_head_t(const HeadDev& p, hipStream_t st) {
       if (dev <= 63) allowed.fetch_or(bit, std::memory_order_relaxed);
     }
   }
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(wgs)), dim3(64 * NW), smem, st, p);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(wgs)), dim3(64 * NW * HEADS), smem, st, p);
   return hipGetLastError();
 }
 
@@ -804,12 +837,23 @@ hipError_t launch_head_m(const HeadDev& p, bool wide, bool vec, hipStream_t st) 
   return launch_head_r<IO, MODE, DOT, 256>(p, wide, vec, st);
 }
 
-// One pass: mode kOut (with the dot if p.dotv is set), kOutF32 (with the dot) or kState.
+// Whether kOutPair is there for a size: two heads' state and tiles have to fit the registers and LDS.
+constexpr int kPairRows = 64;
+
+// One pass: mode kOut (with the dot if p.dotv is set), kOutF32 and kOutPair (with the dot) or kState.
 template <typename IO>
 hipError_t launch_head_io(const HeadDev& p, int mode, bool wide, bool vec, hipStream_t st) {
   if (mode == kState) return launch_head_m<IO, kState, false>(p, wide, vec, st);
   if constexpr (HeadCfg<IO>::ES == 2) {
     if (mode == kOutF32) return launch_head_m<IO, kOutF32, true>(p, wide, vec, st);
+    if (mode == kOutPair) {
+      if (!vec || p.rows > kPairRows || p.H % 2 != 0) return hipErrorInvalidValue;
+      if (p.rows <= 32)
+        return wide ? launch_head_t<IO, 32, 8, 1, kOutPair, true, true>(p, st)
+                    : launch_head_t<IO, 32, 4, 1, kOutPair, true, true>(p, st);
+      return wide ? launch_head_t<IO, 64, 8, 1, kOutPair, true, true>(p, st)
+                  : launch_head_t<IO, 64, 4, 1, kOutPair, true, true>(p, st);
+    }
   }
   if (p.dotv != nullptr) return launch_head_m<IO, kOut, true>(p, wide, vec, st);
   return launch_head_m<IO, kOut, false>(p, wide, vec, st);
