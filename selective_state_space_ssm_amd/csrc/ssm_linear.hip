@@ -14,9 +14,9 @@
 //   dx       token  k      m      dpre          W, rows contiguous
 //   dW       m      k      token  dpre, rows c. x, rows contiguous
 //
-// 16384 x 4096 -> 2048 in bfloat16 with gelu and residual: 359 us forward (766
+// 16384 x 4096 -> 2048 in bfloat16 with gelu and residual: 316 us forward (870
 // TFLOP/s; the epilogue's 200 MB come after the products, nothing covers them),
-// dx 315, dW 277 (990), dpre 46.  8192 x 4096 -> 2048 in float32: 131 TFLOP/s.
+// dx 265, dW 238 (1155), dpre 47.  8192 x 4096 -> 2048 in float32: 131 TFLOP/s.
 // Both are bound by the matrix instructions and what stands between them.
 //
 // The c side is the first operand of the matrix instruction, so that a lane
@@ -370,10 +370,14 @@ struct DmaSide {
         frag[j] = kk * 512 + 16 * (half * 16 + ((2 * j) ^ swz_kn(kk)) + ((lane >> 1) & 1)) + 8 * (lane & 1);
     }
   }
-  // i-th of the four loads of the next stage into LDS at `lds`; krem k of it exist (none: reads zeros)
-  __device__ __forceinline__ void load(uint32_t lds, int wave, int i, int krem) const {
-    const u32x4 d = dma_desc(reinterpret_cast<const void*>(addr), krem > 0 ? kRecords : 0u);
-    dma16(d, krem >= kStageK || k[i] < krem ? voff[i] : kOOB, lds + (wave + 4 * i) * 1024);
+  // i-th of the four loads of the next stage into LDS at `lds`
+  __device__ __forceinline__ void load(uint32_t lds, int wave, int i) const {
+    dma16(dma_desc(reinterpret_cast<const void*>(addr), kRecords), voff[i], lds + (wave + 4 * i) * 1024);
+  }
+  // only krem k of the next stage exist, and none of those after it: what is past them reads zeros from here on
+  __device__ __forceinline__ void end(int krem) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) voff[i] = k[i] < krem ? voff[i] : kOOB;
   }
   __device__ __forceinline__ uint4 read(const char* stage, int j) const {
     if constexpr (!TR) {
@@ -410,19 +414,29 @@ __global__ void __launch_bounds__(256, 1) ssm_linear_dma_kernel(LinDev p) {
   sr.init(p.r, p.ldr, r0, p.nr, kb, wave, lane, wr);
   int64_t left = ke - kb;  // k from the next stage on
   // a stage past the end is still issued (its loads read zeros), so that one count serves every wait
+  auto before = [&]() {
+    if (left < kStageK) {
+      const int krem = left > 0 ? static_cast<int>(left) : 0;
+      sc.end(krem);
+      sr.end(krem);
+    }
+  };
+  auto next = [&]() {
+    left -= kStageK;
+    sc.addr += sc.step;
+    sr.addr += sr.step;
+  };
+  auto lds_of = [&](auto KS) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)stg[decltype(KS)::value]));
+  };
   auto issue = [&](auto KS) {
-    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)stg[decltype(KS)::value]));
-    const int krem = left > kStageK ? kStageK : static_cast<int>(left);
+    before();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      sc.load(base, wave, i, krem);
-      sr.load(base + kOperand, wave, i, krem);
+      sc.load(lds_of(KS), wave, i);
+      sr.load(lds_of(KS) + kOperand, wave, i);
     }
-    if (left > 0) {
-      left -= kStageK;
-      sc.addr += sc.step;
-      sr.addr += sr.step;
-    }
+    next();
   };
   struct Frag {
     uint4 c[8], r[8];
@@ -440,24 +454,16 @@ __global__ void __launch_bounds__(256, 1) ssm_linear_dma_kernel(LinDev p) {
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto products = [&](const Frag& f, auto I0) {  // columns' tiles I0, I0 + 1
-#pragma unroll
-    for (int i = decltype(I0)::value; i < decltype(I0)::value + 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.c[i]),
-                                                            __builtin_bit_cast(bf16x8, f.r[j]), acc[i][j], 0, 0, 0);
-  };
-
   // Step s: wait until stage s + 1 has landed (8 loads a wavefront and stage: vmcnt(8) leaves stage s + 2 in flight)
-  // and this wavefront's reads of step s - 1 are done; barrier; then step s's products in four groups, with the refill
-  // of the stage read at step s - 1 and the reads of step s + 1's operands between them.
+  // and this wavefront's reads of step s - 1 are done; barrier; then step s's 64 products.  What else the step issues,
+  // the reads of step s + 1's operands and the refill of the stage read at step s - 1, stands between the first 32 of
+  // them, so that it goes out while the matrix unit is busy and the reads have the other 32 to arrive: forward, dx and
+  // dW of 16384 x 4096 -> 2048 take 316, 265 and 238 us, in four blocks between groups of 16 products 365, 315 and 280,
+  // spread over 24 or all 32 pairs 320, 277 and 246.
   using S0 = std::integral_constant<int, 0>;
   using S1 = std::integral_constant<int, 1>;
   using S2 = std::integral_constant<int, 2>;
   using S3 = std::integral_constant<int, 3>;
-  using S4 = std::integral_constant<int, 4>;
-  using S6 = std::integral_constant<int, 6>;
   constexpr int kWait16 = 0 | (7 << 4) | (0 << 8) | (1 << 14);  // vmcnt(16) lgkmcnt(0)
   constexpr int kWait8 = 8 | (7 << 4) | (0 << 8);               // vmcnt(8) lgkmcnt(0)
   Frag F0, F1;
@@ -471,13 +477,28 @@ __global__ void __launch_bounds__(256, 1) ssm_linear_dma_kernel(LinDev p) {
   auto step = [&](auto KR, auto KN, Frag& cur, Frag& nxt) {
     __builtin_amdgcn_s_waitcnt(kWait8);
     asm volatile("s_barrier" ::: "memory");
-    products(cur, S0{});
-    issue(KR);
-    products(cur, S2{});
-    read_c(KN, nxt);
-    products(cur, S4{});
-    read_r(KN, nxt);
-    products(cur, S6{});
+    before();
+    const char* const from = stg[decltype(KN)::value];
+#pragma unroll
+    for (int t = 0; t < 32; ++t) {
+#pragma unroll
+      for (int m = 2 * t; m < 2 * t + 2; ++m)
+        acc[m / 8][m % 8] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, cur.c[m / 8]),
+                                                                    __builtin_bit_cast(bf16x8, cur.r[m % 8]),
+                                                                    acc[m / 8][m % 8], 0, 0, 0);
+      if (t < 16) {
+        const int u = t;
+        if (u < 8) nxt.c[u] = sc.read(from, u);
+        else nxt.r[u - 8] = sr.read(from + kOperand, u - 8);
+      }
+      if (t < 16 && t % 2 == 0) {
+        const int u = t / 2;
+        if (u < 4) sc.load(lds_of(KR), wave, u);
+        else sr.load(lds_of(KR) + kOperand, wave, u - 4);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    next();
   };
   for (int64_t s = 0; s < nsteps; s += 4) {
     step(S3{}, S1{}, F0, F1);
@@ -750,7 +771,7 @@ int64_t up(int64_t n, int64_t to) { return cdiv(n, to) * to; }
 // One product's tile (32 t x 32 t) and split of k.
 //   bfloat16 takes 256 x 256 tiles (t = 8) where they, with k in parts of at
 //   least 1024, give three quarters of the CUs a workgroup (products of 16384 x
-//   4096 x 2048: 287 to 360 us, 128 x 128 tiles 420 to 470).
+//   4096 x 2048: 238 to 316 us, 128 x 128 tiles 448 to 514).
 //   Else 128 x 128 where they, with k in parts of at least 16 steps, give as
 //   many (300 x 4096 -> 2048: bfloat16 25 us, float32 73; 64 x 64: 40 and 103;
 //   forward and gradients of 4099 x 768 -> 1536 in float32: 339, 64 x 64 where
