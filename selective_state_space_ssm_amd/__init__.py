@@ -127,6 +127,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _need(t: torch.Tensor, name: str, dtype, device, shape):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -651,11 +653,12 @@ def _addr(t: Optional[torch.Tensor]):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(device, fn, *args):
     """fn(*args, the device's current stream) with the device current; raises on a status."""
-    if torch.cuda.current_device() == device.index:
+    if _get_device() == device.index:
         stream = (torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device.index))
         rc = fn(*args, stream)
     else:
@@ -781,10 +784,10 @@ def ssm_head_scan_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, do: tor
     if lengths is not None:
         _need(lengths, "lengths", torch.int32, device, (b,))
     out = {
-        "dq": torch.empty((b, L, hk, dk), device=device, dtype=dt),
-        "dk": torch.empty((b, L, hk, dk), device=device, dtype=dt),
-        "dv": torch.empty((b, L, h, dv), device=device, dtype=dt),
-        "dg": torch.empty((b, L, h), device=device, dtype=dt) if want_dg and g is not None else None,
+        "dq": q.new_empty((b, L, hk, dk)),
+        "dk": q.new_empty((b, L, hk, dk)),
+        "dv": torch.empty_like(do),
+        "dg": torch.empty_like(g) if want_dg and g is not None else None,
         "dh0": torch.empty((b, h, dk, dv), device=device, dtype=torch.float32) if want_dh0 else None,
     }
     code = SSM_F32 if dt == torch.float32 else SSM_BF16
@@ -908,10 +911,10 @@ def ssm_linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = 
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}")
     if out is None:
-        out = torch.empty(shape, device=device, dtype=dt)
+        out = x.new_empty(shape)
     else:
         _need(out, "out", dt, device, shape)
-    pre = torch.empty(shape, device=device, dtype=dt) if return_pre else None
+    pre = torch.empty_like(out) if return_pre else None
     code = SSM_F32 if dt == torch.float32 else SSM_BF16
     ws, nws = _workspace("ssm_linear_workspace", device, rows, k, m, ACTS[act], code, 0)
     _call(device, load_library().ssm_linear, x.data_ptr(), W.data_ptr(), _addr(bias), _addr(residual), ACTS[act],
@@ -936,7 +939,7 @@ def ssm_linear_bwd(x: torch.Tensor, W: torch.Tensor, dout: torch.Tensor, pre: Op
         _need(pre, "pre", dt, device, shape)
     dx = torch.empty_like(x) if want_dx else None
     dW = torch.empty_like(W) if want_dW else None
-    db = torch.empty((m,), device=device, dtype=dt) if want_dbias else None
+    db = W.new_empty(m) if want_dbias else None
     code = SSM_F32 if dt == torch.float32 else SSM_BF16
     ws, nws = _workspace("ssm_linear_workspace", device, rows, k, m, ACTS[act], code, 1)
     _call(device, load_library().ssm_linear_bwd, x.data_ptr(), W.data_ptr(), _addr(pre), ACTS[act], dout.data_ptr(),
