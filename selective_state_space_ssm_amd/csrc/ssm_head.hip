@@ -32,6 +32,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "ssm_device.h"
 #include "ssm_head_kernel.h"
 #include "ssm_kernels.h"
@@ -50,9 +53,19 @@ using headk::HeadDev;
 // segments' states: it is split for two workgroups per CU in any case (4 x 2048
 // tokens, 64 heads of 128 x 64: 815 us whole, 731 in two, 820 in three; float32,
 // 4 x 1999, 24 heads of 64: 538 whole, 384 in six).
+// How short a segment may be: its states take two passes whatever its length,
+// and they are carried over the segments one after the other, so that the best
+// number of segments grows like the root of the length (4 heads, 8000 tokens:
+// bfloat16, 128 x 128, 49 us with the root's 42 segments, 56 with 31, 66 with
+// 125).  Below that 64 tokens: float32, 100 x 48, 300 tokens 32 us whole 51, 2757
+// tokens 40, in segments of 256 73 (forward and gradients 184, 283).  bfloat16
+// with more than 64 heads or fewer than six chunks is better off with 256
+// (128 heads, 500 tokens 46 us, in segments of 64 or 128 tokens 53; few heads:
+// 4, 500 tokens 28, 43).
 constexpr int64_t kHeadCUs = 256;
 constexpr int64_t kHeadSlots = 512;
-constexpr int64_t kHeadMinSegment = 256;  // tokens
+constexpr int64_t kHeadMinSegment = 64;       // tokens
+constexpr int64_t kHeadMinSegmentMany = 256;
 // Tokens that the running sum of dg covers: its terms are off by 2^-24 (float32)
 // or 2^-17 (bfloat16, where dg itself is rounded to 2^-8) of themselves, and the
 // sum's error grows like the root of their number.
@@ -271,7 +284,8 @@ Plan plan_of(int64_t batch, int64_t H, int64_t tiles, int64_t L, bool bf16, bool
   p.nch = cdiv(L, p.C);
   const int64_t wgs = batch * H * tiles;
   int64_t want = backward || wgs < kHeadCUs ? kHeadSlots / wgs : 1;
-  const int64_t most = L / kHeadMinSegment;
+  const int64_t least = bf16 && (want < 8 || p.nch < 6) ? kHeadMinSegmentMany : kHeadMinSegment;
+  const int64_t most = std::min(L / least, static_cast<int64_t>(std::sqrt(static_cast<double>(L)) / 1.5));
   if (want > most) want = most;
   if (want < 1) want = 1;
   p.cps = cdiv(p.nch, want);
