@@ -35,7 +35,7 @@
 // storage: float32 matrix instructions, nothing is rounded further.
 //
 // What bounds it.  8 x 2048 ragged tokens (five eighths of them there), 32
-// heads of 128 x 128, bfloat16: 160 us, 2.2 TB/s of q, k, v, o and the last
+// heads of 128 x 128, bfloat16: 156 us, 2.3 TB/s of q, k, v, o and the last
 // states; its loads and stores alone take 116 us, the scores 26.  A head's
 // chunks follow each other, 256 heads are one workgroup a CU, and a chunk's
 // 5 us are vector work (some 560 instructions a wavefront: decays, splits into
