@@ -1013,9 +1013,9 @@ int64_t linear_workspace_bytes(const LinearArgs& a, bool bf16, bool backward) {
 
 int64_t linear_workgroups(const LinearArgs& a, bool bf16) {
   (void)bf16;
-  // the smallest tile, and no more than one split per CU where there are fewer tiles than CUs
+  // the smallest tile; k is split where there are fewer tiles than CUs, for two workgroups a CU at most
   const int64_t f = cdiv(a.m, 64) * cdiv(a.rows, 64), x = cdiv(a.k, 64) * cdiv(a.rows, 64);
-  return (f > x ? f : x) + kCUs + cdiv(a.k, 64) * cdiv(a.m, 64);
+  return (f > x ? f : x) + 2 * kCUs + cdiv(a.k, 64) * cdiv(a.m, 64);
 }
 
 hipError_t launch_linear(const LinearArgs& a, bool bf16, char* work, hipStream_t st) {
