@@ -397,8 +397,9 @@ int ssm_out_proj_bwd(const void *y, const void *W, const void *dout, void *dy, v
  *   v    : [batch, L, n_heads, d_value], dtype `dtype`.
  *          Each of the three is dense over a token's row; *_token and *_batch
  *          are its strides in elements between tokens and batch rows (views of
- *          one projection's output), and its pointer needs the alignment of
- *          its type only (16-byte aligned rows are the fast path).
+ *          one projection's output; the stride over an L or a batch of one is
+ *          not looked at), and its pointer needs the alignment of its type only
+ *          (16-byte aligned rows are the fast path).
  *   g    : [batch, L, n_heads], dtype `dtype`: log decays, <= 0; -inf starts
  *          the head's state anew at that token (packed sequences).  Nullable.
  *   g_head : [n_heads] float32, a fixed log decay per head.  Nullable; at most

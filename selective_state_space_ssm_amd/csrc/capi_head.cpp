@@ -34,17 +34,19 @@ int check_head_sizes(int64_t batch, int64_t L, int64_t H, int64_t Hk, int64_t dk
   return SSM_OK;
 }
 
-// A token-strided operand [batch][L][heads * width]: its strides, and the bytes it spans.
-int check_strides(const char* name, int64_t b, int64_t t, int64_t batch, int64_t L, int64_t row, int64_t es,
+// A token-strided operand [batch][L][heads * width]: its strides, and the bytes it spans.  A stride over a size of one
+// addresses nothing, but the kernels bound their loads by tokens times stride: it is replaced by the dense one.
+int check_strides(const char* name, int64_t& b, int64_t& t, int64_t batch, int64_t L, int64_t row, int64_t es,
                   uint64_t* bytes) {
-  if (t < row && L > 1) return fail(SSM_EINVAL, "%s: a token stride of %lld is less than its row of %lld", name,
-                                    (long long)t, (long long)row);
+  if (L == 1) t = row;
+  if (t < row) return fail(SSM_EINVAL, "%s: a token stride of %lld is less than its row of %lld", name, (long long)t,
+                           (long long)row);
   // a chunk's rows are addressed with 32-bit byte offsets
-  if (t < 0 || t * es >= kLim31 / 128) return fail(SSM_EUNSUPPORTED, "%s: a token stride of %lld is too large", name,
-                                                   (long long)t);
+  if (t >= kLim31 / 128 / es) return fail(SSM_EUNSUPPORTED, "%s: a token stride of %lld is too large", name, (long long)t);
   int64_t span, bspan;
   if (!mul_ok(L - 1, t, &span)) return fail(SSM_EINVAL, "tensor sizes overflow");
   span += row;
+  if (batch == 1) b = L * t;
   if (batch > 1 && b < span) return fail(SSM_EINVAL, "%s: a batch stride of %lld is less than its %lld values", name,
                                          (long long)b, (long long)span);
   if (b < 0 || !mul_ok(batch - 1, b, &bspan) || !mul_ok(bspan + span, es, &bspan))
@@ -67,7 +69,7 @@ struct Spans {
   uint64_t q, k, v;
 };
 
-int check_operands(const ssm::HeadArgs& a, int64_t es, Spans* s) {
+int check_operands(ssm::HeadArgs& a, int64_t es, Spans* s) {
   for (const void* q : {a.q, a.k, a.v, a.g})
     if (q && reinterpret_cast<uintptr_t>(q) % es != 0) return fail(SSM_EINVAL, "q, k, v and g must be aligned to their type");
   if (int rc = check_strides("q", a.q_b, a.q_t, a.batch, a.L, a.Hk * a.dk, es, &s->q)) return rc;
