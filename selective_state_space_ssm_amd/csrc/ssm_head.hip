@@ -20,7 +20,7 @@
 // either recurrence gives dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t, a sum
 // from the end.  The dq and dk passes hand out those dots in float32; the
 // sum starts anew at every segment's end from <R, S> there, so that its
-// rounding does not grow with the length.
+// rounding does not grow with the length, and from zero where the state does.
 //
 // Long sequences with few heads are cut into segments: every segment's own
 // end state first (kState), then the states are carried over the segments
@@ -90,12 +90,15 @@ __global__ void __launch_bounds__(256) ssm_head_carry_kernel(float* state, const
   }
 }
 
-// dg of one segment: <R, S> at its end, then the sum of q . dq - k . dk from the end.
+// dg of one segment: <R, S> at its end, then the sum of q . dq - k . dk from the end.  Where the state starts anew
+// (a decay of -inf) dg is zero, and so is what the tokens before it take over: their sum is begun there, so that no
+// rounding of a packed sequence's dots enters those of the sequences before it.
 template <typename IO>
 __global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, const float* r_seg, const float* s_last,
                                                          const float* dlast, const float* rq, const float* rk,
                                                          int64_t ntile, HeadDev p, int64_t seg_len, void* dg) {
   __shared__ double sh[4];
+  __shared__ int sh_anew[4];
   const int64_t bh = blockIdx.y, k = blockIdx.x, b = bh / p.H, h = bh % p.H, ssize = static_cast<int64_t>(p.rows) * p.cols;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int64_t len = p.L;
@@ -104,6 +107,8 @@ __global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, co
     len = n < 0 ? 0 : (n < p.L ? n : p.L);
   }
   const int64_t t0 = k * seg_len, t1 = t0 + seg_len < p.L ? t0 + seg_len : p.L;
+  auto decay = [&](int64_t t) { return headk::decay_at<IO>(p, static_cast<int>(b), static_cast<int>(h), static_cast<int>(t)); };
+  auto starts = [&](int64_t t) { return t < len && decay(t) == headk::kMinLog2Decay; };
   const float* S = k + 1 < p.nseg ? s_seg + (bh * p.nseg + k) * ssize : s_last + bh * ssize;
   const float* R = k + 1 < p.nseg ? r_seg + (bh * p.nseg + k + 1) * ssize : (dlast ? dlast + bh * ssize : nullptr);
   double x = 0;
@@ -114,31 +119,39 @@ __global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, co
   if (lane == 0) sh[wave] = x;
   __syncthreads();
   double carry = (sh[0] + sh[1]) + (sh[2] + sh[3]);
-  if (k + 1 < p.nseg && t1 < len) carry *= __builtin_amdgcn_exp2f(headk::decay_at<IO>(p, static_cast<int>(b), static_cast<int>(h), static_cast<int>(t1)));
+  if (k + 1 < p.nseg && t1 < len) carry = starts(t1) ? 0. : carry * __builtin_amdgcn_exp2f(decay(t1));
   const int64_t nbh = static_cast<int64_t>(p.batch) * p.H;
   for (int64_t e = t1; e > t0; e -= 256) {
     const int64_t t = e - 1 - tid;  // thread 0 has the last token
     double v = 0;
-    if (t >= t0)
+    int anew = 0;  // the sum up to here begins at a token of these, not with what was carried
+    if (t >= t0) {
       for (int64_t c = 0; c < ntile; ++c)
         v += static_cast<double>(rq[(c * nbh + bh) * p.L + t]) - rk[(c * nbh + bh) * p.L + t];
+      anew = starts(t + 1);
+    }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
       const double o = __shfl_up(v, d);
-      if (lane >= d) v += o;
+      const int a = __shfl_up(anew, d);
+      if (lane >= d) {
+        if (!anew) v += o;
+        anew |= a;
+      }
     }
     __syncthreads();
-    if (lane == 63) sh[wave] = v;
+    if (lane == 63) {
+      sh[wave] = v;
+      sh_anew[wave] = anew;
+    }
     __syncthreads();
     double before = carry;
-    for (int w = 0; w < wave; ++w) before += sh[w];
-    carry += (sh[0] + sh[1]) + (sh[2] + sh[3]);
+    for (int w = 0; w < wave; ++w) before = sh_anew[w] ? sh[w] : before + sh[w];
+    for (int w = 0; w < 4; ++w) carry = sh_anew[w] ? sh[w] : carry + sh[w];
     if (t >= t0) {
       // nothing is decayed at the first token of a sequence that starts from zero, or where the state starts anew
-      const bool none = t >= len || (t == 0 && p.h0 == nullptr) ||
-                        headk::decay_at<IO>(p, static_cast<int>(b), static_cast<int>(h), static_cast<int>(t)) ==
-                            headk::kMinLog2Decay;
-      const float out = none ? 0.f : static_cast<float>(before + v);
+      const bool none = t >= len || (t == 0 && p.h0 == nullptr) || starts(t);
+      const float out = none ? 0.f : static_cast<float>(anew ? v : before + v);
       IO::template st<1>(static_cast<typename IO::T*>(dg) + (b * p.L + t) * p.H + h, &out);
     }
   }
