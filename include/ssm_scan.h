@@ -442,6 +442,11 @@ int ssm_head_scan_fwd(const void *q, int64_t q_batch, int64_t q_token, const voi
  *   dg    : [batch, L, n_heads], dtype `dtype`, output, nullable; needs g.
  *   dh0   : as h0, output, nullable.
  *   workspace : ssm_head_scan_workspace(..., backward = 1) bytes.
+ * dg is summed from the end, of q . dq - k . dk without the tokens' own pairs
+ * (they cancel), over at most 1024 tokens (float32; bfloat16 4096) and back to
+ * the last token before which the state started anew: its error goes by the
+ * size of those dots, so that a token that forgets everything between others
+ * that do not has theirs.
  * Every sum is taken in a fixed order: repeated calls give identical bits.
  * Other arguments and errors as ssm_head_scan_fwd.
  */

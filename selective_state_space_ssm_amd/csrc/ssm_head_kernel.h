@@ -249,7 +249,8 @@ struct HeadDev {
   int s_r, s_c;                // state strides of rows and columns
   float* seg_state;            // [b][H][nseg][rows cols]
   float* seg_decay;            // [b][H][nseg]
-  const char* dotv;            // [b][L][H / dot_rep][cols]: the dot of o_t with it goes to dot_out (DOT)
+  const char* dotv;            // [b][L][H / dot_rep][cols]: its dot with o_t, the token's own part of that left out,
+                               // goes to dot_out (DOT)
   int64_t dot_b;
   uint32_t dot_t;
   int dot_rep;
@@ -290,13 +291,13 @@ template <int MODE>
 constexpr int heads_of() { return MODE == kOutPair ? 2 : 1; }
 
 // Bytes of LDS: y and z tiles, x tile, scores (bfloat16: hi and lo), the
-// chunk's decays, and the wavefronts' dots.
+// chunk's decays, and (DOT) the tokens' own scores and the wavefronts' dots.
 template <typename IO, int ROWS, int NW, int NC, int MODE, bool DOT>
 constexpr size_t head_lds_bytes() {
   using K = HeadCfg<IO>;
   constexpr size_t xy = size_t(K::C) * ROWS * K::ES, z = size_t(K::C) * 16 * NW * NC * K::ES;
   constexpr size_t sc = size_t(K::C) * K::C * K::ES * (K::ES == 2 ? 2 : 1);
-  return xy + z + 4 * K::C * 4 + (MODE != kState ? xy + sc : 0) + (DOT ? size_t(NW) * K::C * 4 : 0);
+  return xy + z + 4 * K::C * 4 + (MODE != kState ? xy + sc : 0) + (DOT ? size_t(NW + 1) * K::C * 4 : 0);
 }
 // The outputs that the two heads of kOutPair exchange.
 template <typename IO, int NW, int NC, int MODE>
@@ -336,7 +337,8 @@ ssm_head_kernel(const HeadDev p) {
   float* const glo = ghi + C;
   float* const eg = glo + C;    // ss e^{G_i}
   float* const we = eg + C;     // us e^{G_C - G_j}
-  float* const red = we + C;    // [NW][C]
+  float* const own = we + C;    // scores of tokens with themselves
+  float* const red = own + C;   // [NW][C]
 
   const int tid = static_cast<int>(threadIdx.x) - half * T;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -578,7 +580,12 @@ ssm_head_kernel(const HeadDev p) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float d = __builtin_amdgcn_exp2f((gi - get(gj, v)) + (gl - get(gk, v)));
-          w[v] = j0 + v <= i ? p.ps * d * a[v] : 0.f;
+          w[v] = (DOT ? j0 + v < i : j0 + v <= i) ? p.ps * d * a[v] : 0.f;
+        }
+        if constexpr (DOT) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (j0 + v == i) own[i] = p.ps * a[v];
         }
         if constexpr (ES == 2) {
           const int u = 4 * jb + g;
@@ -731,6 +738,21 @@ ssm_head_kernel(const HeadDev p) {
           dot += __shfl_xor(dot, 16);
           dot += __shfl_xor(dot, 32);
           if (g == 0) red[wave * C + 16 * ib + li] = dot;
+        }
+        // what a token's own y and z give
+#pragma unroll
+        for (int ib = 0; ib < IB; ++ib) {
+          const int r = 16 * ib + li;
+          const float e = own[r];
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) {
+            const int c = 16 * (wave * NC + nc) + 4 * g;  // column in the tile
+            float zv[4];
+            IO::template ld<4>(reinterpret_cast<const typename IO::T*>(
+                                   tz + 16 * (NZ * r + (c / E ^ swz<IO, NZ>(li))) + c % E * ES), zv);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) O[ib][nc][v] = __builtin_fmaf(e, zv[v], O[ib][nc][v]);
+          }
         }
       }
       if constexpr (HEADS == 1) {
