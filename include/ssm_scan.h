@@ -400,8 +400,9 @@ int ssm_out_proj_bwd(const void *y, const void *W, const void *dout, void *dy, v
  *          one projection's output; the stride over an L or a batch of one is
  *          not looked at), and its pointer needs the alignment of its type only
  *          (16-byte aligned rows are the fast path).
- *   g    : [batch, L, n_heads], dtype `dtype`: log decays, <= 0; -inf starts
- *          the head's state anew at that token (packed sequences).  Nullable.
+ *   g    : [batch, L, n_heads], dtype `dtype`: log decays, <= 0; -inf (or
+ *          anything below -1387) starts the head's state anew at that token
+ *          (packed sequences).  Nullable.
  *   g_head : [n_heads] float32, a fixed log decay per head.  Nullable; at most
  *          one of g and g_head is given, neither means no decay.
  *   h0   : [batch, n_heads, d_key, d_value] float32 start state, nullable (zero).
@@ -418,8 +419,13 @@ int ssm_out_proj_bwd(const void *y, const void *W, const void *dout, void *dy, v
  *   n_qk_heads.
  * Rounding: sums, decays and the state are float32.  With SSM_BF16 the scores
  * q_i . k_j (decayed) and the state enter o's products as pairs of bfloat16
- * (off by 2^-17 of themselves).  A non-finite k or v reaches every output of its
- * token's chunk (64 tokens, 32 for float32), those before it included.
+ * (off by 2^-17 of themselves); one past bfloat16's largest value (3.39e38) counts
+ * as not finite there, and an infinite one gives NaN.
+ * Values that are not finite: a v reaches every output of its token's chunk (64
+ * tokens from a multiple of 64, float32: 32), those before it and those of other
+ * packed sequences in it included, a k its own sequence's later outputs.  Past its
+ * chunk neither goes further than the next token that starts the state anew:
+ * what a state held there is left out, whatever it is.
  * Errors: SSM_EINVAL, SSM_EUNSUPPORTED, SSM_EHIP.  No memory is allocated.
  */
 int ssm_head_scan_fwd(const void *q, int64_t q_batch, int64_t q_token, const void *k, int64_t k_batch, int64_t k_token,
@@ -447,6 +453,9 @@ int ssm_head_scan_fwd(const void *q, int64_t q_batch, int64_t q_token, const voi
  * the last token before which the state started anew: its error goes by the
  * size of those dots, so that a token that forgets everything between others
  * that do not has theirs.
+ * Values that are not finite: a k reaches every dq, a q every dk and a do every dv
+ * of its token's chunk, with dg of the tokens before them in their sequences;
+ * otherwise they stay within their sequence as in the forward.
  * Every sum is taken in a fixed order: repeated calls give identical bits.
  * Other arguments and errors as ssm_head_scan_fwd.
  */

@@ -75,8 +75,9 @@ constexpr int64_t kHeadMinSegmentMany = 256;
 constexpr int64_t kHeadMaxDgSegmentF32 = 1024;
 constexpr int64_t kHeadMaxDgSegmentBf16 = 4096;
 
-// States carried over the segments, in order: state <- decay * (carried) + own.
-// Segment `first` holds its final state already.
+// States carried over the segments, in order: state <- decay * (carried) + own,
+// or own alone where the state starts anew in the segment (a decay of -0; what
+// was carried may not be finite).  Segment `first` holds its final state already.
 __global__ void __launch_bounds__(256) ssm_head_carry_kernel(float* state, const float* decay, int64_t nseg, int64_t n,
                                                             int64_t ssize, int rev) {
   const int64_t bh = blockIdx.y, e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -88,7 +89,8 @@ __global__ void __launch_bounds__(256) ssm_head_carry_kernel(float* state, const
 #pragma unroll 4
   for (int64_t i = 1; i < n; ++i) {
     const int64_t at = first + i * step;
-    c = __builtin_fmaf(d[at], c, s[at * ssize]);
+    const float own = s[at * ssize], dec = d[at];
+    c = __float_as_uint(dec) == 0x80000000u ? own : __builtin_fmaf(dec, c, own);
     s[at * ssize] = c;
   }
 }
@@ -238,12 +240,18 @@ __global__ void __launch_bounds__(256) ssm_head_step_kernel(HeadStepDev p) {
     vv[e] = 0.f;
     if (c + e < p.dv) IO::template ld<1>(v + c + e, &vv[e]);
   }
-  float a = 1.f;
+  float a = 0.f;
   if (p.g != nullptr) {
     IO::template ld<1>(reinterpret_cast<const T*>(p.g) + bh, &a);
-    a = __builtin_amdgcn_exp2f(headk::clamp_decay(a * kLog2e));
   } else if (p.g_head != nullptr) {
-    a = __builtin_amdgcn_exp2f(headk::clamp_decay(p.g_head[h] * kLog2e));
+    a = p.g_head[h];
+  }
+  a = __builtin_amdgcn_exp2f(headk::clamp_decay(a * kLog2e));
+  if (a == 0.f) {  // what is forgotten may not be finite
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
   }
   float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

@@ -64,7 +64,7 @@ typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 
 constexpr uint32_t kOOB = 0x80000000u;  // an offset past every resource (sizes are < 2^31)
-constexpr float kMinLog2Decay = -2000.f;  // 2^-2000 is 0 in float32: a decay of -inf becomes this
+constexpr float kMinLog2Decay = -2000.f;  // 2^-2000 is 0 in float32: a decay of -inf becomes this, a start of the state
 
 template <typename IO>
 struct HeadCfg;
@@ -233,6 +233,18 @@ __device__ __forceinline__ void scan_pair(float& hi, float& lo) {
   scan_step<0x143, 0xc>(hi, lo);  // the lower half's to rows 2 and 3
 }
 
+// A decay times a value: where the decay is zero so is this, whatever the
+// value.  What a state held before it starts anew (g = -inf), and what tokens
+// before that gave, is gone, infinities and NaN too.  (Operands of a matrix
+// product cannot be left out that way: see `cut` for y.)  The instruction for it
+// has no builtin of its own: the intrinsic is named.
+extern "C" __device__ __attribute__((const)) float ssm_mul_legacy(float, float) __asm("llvm.amdgcn.fmul.legacy");
+__device__ __forceinline__ float times(float decay, float v) { return ssm_mul_legacy(decay, v); }
+__device__ __forceinline__ void scale(f32x4& v, float decay) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = times(decay, v[i]);
+}
+
 struct HeadDev {
   const char* x;
   const char* y;
@@ -248,7 +260,7 @@ struct HeadDev {
   float* last;                 // last state, nullable
   int s_r, s_c;                // state strides of rows and columns
   float* seg_state;            // [b][H][nseg][rows cols]
-  float* seg_decay;            // [b][H][nseg]
+  float* seg_decay;            // [b][H][nseg], -0 where nothing is left of the state before one of the chunks
   const char* dotv;            // [b][L][H / dot_rep][cols]: its dot with o_t, the token's own part of that left out,
                                // goes to dot_out (DOT)
   int64_t dot_b;
@@ -291,13 +303,14 @@ template <int MODE>
 constexpr int heads_of() { return MODE == kOutPair ? 2 : 1; }
 
 // Bytes of LDS: y and z tiles, x tile, scores (bfloat16: hi and lo), the
-// chunk's decays, and (DOT) the tokens' own scores and the wavefronts' dots.
+// chunk's decays and last start, and (DOT) the tokens' own scores and the
+// wavefronts' dots.
 template <typename IO, int ROWS, int NW, int NC, int MODE, bool DOT>
 constexpr size_t head_lds_bytes() {
   using K = HeadCfg<IO>;
   constexpr size_t xy = size_t(K::C) * ROWS * K::ES, z = size_t(K::C) * 16 * NW * NC * K::ES;
   constexpr size_t sc = size_t(K::C) * K::C * K::ES * (K::ES == 2 ? 2 : 1);
-  return xy + z + 4 * K::C * 4 + (MODE != kState ? xy + sc : 0) + (DOT ? size_t(NW + 1) * K::C * 4 : 0);
+  return xy + z + 4 * K::C * 4 + 16 + (MODE != kState ? xy + sc : 0) + (DOT ? size_t(NW + 1) * K::C * 4 : 0);
 }
 // The outputs that the two heads of kOutPair exchange.
 template <typename IO, int NW, int NC, int MODE>
@@ -337,7 +350,8 @@ ssm_head_kernel(const HeadDev p) {
   float* const glo = ghi + C;
   float* const eg = glo + C;    // ss e^{G_i}
   float* const we = eg + C;     // us e^{G_C - G_j}
-  float* const own = we + C;    // scores of tokens with themselves
+  int* const start = reinterpret_cast<int*>(we + C);  // the chunk's last token where the state starts anew (0: none)
+  float* const own = we + C + 4;  // scores of tokens with themselves
   float* const red = own + C;   // [NW][C]
 
   const int tid = static_cast<int>(threadIdx.x) - half * T;
@@ -452,6 +466,7 @@ ssm_head_kernel(const HeadDev p) {
   // it; scanned by the wavefront with the fewest score tiles, ahead of the barrier.
   uint32_t raw_g = 0;
   float rg = 0.f, rlo = 0.f;
+  int last_start = 0;
   const char* const gb = p.g != nullptr ? p.g + (static_cast<int64_t>(b) * p.L * p.H + h) * ES : p.y;
   const uint32_t g_t = p.g != nullptr ? p.H * ES : 0;
   const float fixed = p.g == nullptr && p.g_head != nullptr ? clamp_decay(p.g_head[h] * kLog2e) : 0.f;
@@ -461,6 +476,8 @@ ssm_head_kernel(const HeadDev p) {
       rg = clamp_decay((ES == 2 ? __uint_as_float(raw_g << 16) : __uint_as_float(raw_g)) * kLog2e);
     else
       rg = (tid & 63) < C && pc * C + (p.rev ? C - (tid & 63) : tid & 63) < len ? fixed : 0.f;
+    const uint64_t at = __builtin_amdgcn_ballot_w64(rg == kMinLog2Decay);
+    last_start = at != 0 ? 63 - __builtin_clzll(at) : 0;
     scan_pair(rg, rlo);
   };
   auto load_chunk = [&](int pc) {
@@ -558,10 +575,11 @@ ssm_head_kernel(const HeadDev p) {
         eg[lane] = p.ss * __builtin_amdgcn_exp2f(rg + rlo);
         we[lane] = p.us * __builtin_amdgcn_exp2f((eh - rg) + (el - rlo));
       }
+      if (lane == 0) *start = last_start;
     }
     __syncthreads();
     const float end_dec = __builtin_amdgcn_exp2f(ghi[C - 1] + glo[C - 1]);
-    if constexpr (MODE == kState) seg_dec *= end_dec;
+    if constexpr (MODE == kState) seg_dec = end_dec == 0.f ? -0.f : seg_dec * end_dec;
 
     const int lane = opaque(tid) & 63, g = lane >> 4, li = lane & 15;
     f32x4 O[IB][NC];  // transposed: lane holds columns cw + 16 nc + 4 g + v of logical token 16 ib + li
@@ -580,7 +598,7 @@ ssm_head_kernel(const HeadDev p) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float d = __builtin_amdgcn_exp2f((gi - get(gj, v)) + (gl - get(gk, v)));
-          w[v] = (DOT ? j0 + v < i : j0 + v <= i) ? p.ps * d * a[v] : 0.f;
+          w[v] = (DOT ? j0 + v < i : j0 + v <= i) ? times(p.ps * d, a[v]) : 0.f;
         }
         if constexpr (DOT) {
 #pragma unroll
@@ -633,9 +651,19 @@ ssm_head_kernel(const HeadDev p) {
       for (int ib = 0; ib < IB; ++ib) {
         const float e = eg[16 * ib + li];
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc) O[ib][nc] *= e;
+        for (int nc = 0; nc < NC; ++nc) scale(O[ib][nc], e);
       }
       __syncthreads();  // scores
+    }
+    const int from = uniform(*start);
+    bool cut = from > 0;  // in either head: the barriers are common
+    if constexpr (HEADS == 2)
+      cut |= uniform(start[(half ? -1 : 1) * static_cast<int>(head_lds_bytes<IO, ROWS, NW, NC, MODE, DOT>() / 4)]) > 0;
+    // What comes before the chunk's last start is left out of the state after it: y's rows here (they are done with
+    // but for that), z's by its decays of zero.
+    if (cut) {
+      for (int i = opaque(tid); i < from * NK; i += T) reinterpret_cast<uint4*>(ty)[i] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
     }
     if (k + 1 < n) load_chunk(p.rev ? pc - 1 : pc + 1);
 
@@ -668,7 +696,7 @@ ssm_head_kernel(const HeadDev p) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int nc = 0; nc < NC; ++nc) S[rt][nc] *= end_dec;
+      for (int nc = 0; nc < NC; ++nc) scale(S[rt][nc], end_dec);
     const int yb0 = opaque(state_col_base<IO, NK>(li, g));
 #pragma unroll
     for (int js = 0; js < JS; ++js) {
@@ -682,12 +710,12 @@ ssm_head_kernel(const HeadDev p) {
           float v[8];
           const uint32_t* pw = reinterpret_cast<const uint32_t*>(&fz[js][nc]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = w[e] * (e & 1 ? bf_hi(pw[e >> 1]) : bf_lo(pw[e >> 1]));
+          for (int e = 0; e < 8; ++e) v[e] = times(w[e], e & 1 ? bf_hi(pw[e >> 1]) : bf_lo(pw[e >> 1]));
 #pragma unroll
           for (int q = 0; q < TERMS; ++q) hz[nc][q] = take_bf16(v);
         } else {
           const float* pf = reinterpret_cast<const float*>(&fz[js][nc]);
-          const float4 v = make_float4(w[0] * pf[0], w[1] * pf[1], w[2] * pf[2], w[3] * pf[3]);
+          const float4 v = make_float4(times(w[0], pf[0]), times(w[1], pf[1]), times(w[2], pf[2]), times(w[3], pf[3]));
           hz[nc][0] = __builtin_bit_cast(uint4, v);
         }
       }
@@ -817,7 +845,7 @@ ssm_head_kernel(const HeadDev p) {
 #pragma unroll
       for (int i = 0; i < 4 * NC; ++i) {
         const int nc = i / 4, v = i % 4, r = state_row<IO>(rt, g, v), c = cw + 16 * nc + li;
-        if (r < p.rows && c < p.cols) dst[r * p.s_r + c * p.s_c] = dec * S[rt][nc][v];
+        if (r < p.rows && c < p.cols) dst[r * p.s_r + c * p.s_c] = times(dec, S[rt][nc][v]);
       }
   }
 }
