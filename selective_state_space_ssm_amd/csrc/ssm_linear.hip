@@ -66,6 +66,8 @@ struct LinCfg<BF16> {
   static constexpr int ES = 2, E = 8;
 };
 
+constexpr float kLog2eLo = 1.9259629911e-8f;  // log2(e) - kLog2e
+
 struct LinDev {
   const char* c;
   const char* r;
@@ -80,13 +82,29 @@ struct LinDev {
   int act;
 };
 
-// erfc(x) with a relative error below 2e-7 for every x (so that gelu keeps its
-// digits in the tail): Chebyshev fit of log(erfc(x) / t) in t = 1 / (1 + x / 2),
-// x >= 0 (W. H. Press et al., Numerical Recipes, "Incomplete Gamma Function, Error
-// Function"), mirrored for x < 0.
-__device__ __forceinline__ float erfc_fit(float x) {
-  // erfc(16) is far below the smallest float; further out z^2 is infinite and its lo part no number
-  const float z = __builtin_fminf(__builtin_fabsf(x), 16.f), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, z, 1.f));
+// exp(-p^2 / 2).  An absolute error of the exponent is a relative one of the
+// result, so that p^2 / 2 and its product with log2(e) are taken as hi + lo and
+// the lo parts applied to the result (the plain float32 form is off by 1e-5 at p =
+// -12).
+__device__ __forceinline__ float gauss(float p) {
+  const float h = 0.5f * p, q = h * p, ql = __builtin_fmaf(h, p, -q);
+  const float e = q * kLog2e, el = __builtin_fmaf(q, kLog2eLo, __builtin_fmaf(q, kLog2e, -e));
+  return __builtin_amdgcn_exp2f(-e) * (1.f - __builtin_fmaf(el, kLn2, ql));
+}
+
+// The normal distribution function, erfc(-p / sqrt 2) / 2, and exp(-p^2 / 2).
+// Relative error below 1e-6 for every p (so that gelu keeps its digits in the
+// tail): Chebyshev fit of log(erfc(z) exp(z^2) / t) in t = 1 / (1 + z / 2), z >= 0,
+// to 1.2e-7 (W. H. Press et al., Numerical Recipes, "Incomplete Gamma Function,
+// Error Function"), mirrored for p > 0; the rest are the roundings.
+// For bfloat16, rounded to 2^-8 next, the plain exponential does: below 2e-5 down
+// to p = -12 (forward of 16384 x 4096 -> 2048 with gelu and residual 270 us, with
+// the other 278; dpre 36 and 38).
+template <typename IO>
+__device__ __forceinline__ float normal_cdf(float p, float* g) {
+  // exp(-24^2 / 2) is far below the smallest float; further out p^2 is infinite and its lo part no number
+  const float a = __builtin_fminf(__builtin_fabsf(p), 24.f);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, 0.70710678118654752f * a, 1.f));
   float s = 0.17087277f;
   s = __builtin_fmaf(s, t, -0.82215223f);
   s = __builtin_fmaf(s, t, 1.48851587f);
@@ -97,26 +115,39 @@ __device__ __forceinline__ float erfc_fit(float x) {
   s = __builtin_fmaf(s, t, 0.37409196f);
   s = __builtin_fmaf(s, t, 1.00002368f);
   s = __builtin_fmaf(s, t, -1.26551223f);
-  // exp(-z^2 + s): z^2 as hi + lo, its rounding would be multiplied by the exponent
-  const float q = z * z, ql = __builtin_fmaf(z, z, -q);
-  const float e = t * __builtin_amdgcn_exp2f(kLog2e * (s - q)) * (1.f - ql);
-  return x >= 0.f ? e : 2.f - e;
+  float e;
+  if constexpr (std::is_same<IO, F32>::value) {
+    *g = gauss(a);
+    e = 0.5f * (t * __builtin_amdgcn_exp2f(kLog2e * s) * *g);
+  } else {
+    const float q = 0.5f * a * a;
+    *g = __builtin_amdgcn_exp2f(-kLog2e * q);
+    e = 0.5f * (t * __builtin_amdgcn_exp2f(kLog2e * (s - q)));
+  }
+  return p <= 0.f ? e : 1.f - e;
 }
 
+template <typename IO>
 __device__ __forceinline__ float act_of(float p, int act) {
   if (act == kActSilu) return p * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * p));
-  if (act == kActGelu) return 0.5f * p * erfc_fit(-0.70710678118654752f * p);
+  if (act == kActGelu) {
+    float g;
+    return p * normal_cdf<IO>(p, &g);
+  }
   return p;
 }
 
+template <typename IO>
 __device__ __forceinline__ float act_grad(float p, int act) {
   if (act == kActSilu) {
     const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * p));
     return s * __builtin_fmaf(p, 1.f - s, 1.f);
   }
-  if (act == kActGelu)
-    return __builtin_fmaf(p, 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * kLog2e * p * p),
-                          0.5f * erfc_fit(-0.70710678118654752f * p));
+  if (act == kActGelu) {
+    float g;
+    const float c = normal_cdf<IO>(p, &g);
+    return __builtin_fmaf(p, 0.3989422804014327f * g, c);
+  }
   return 1.f;
 }
 
@@ -134,7 +165,7 @@ __device__ __forceinline__ void epilogue(const LinDev& p, int64_t r, int64_t c, 
   if (p.pre != nullptr) IO::template st<CNT>(reinterpret_cast<T*>(p.pre) + at, v);
   if (p.act != kActNone) {
 #pragma unroll
-    for (int e = 0; e < CNT; ++e) v[e] = act_of(v[e], p.act);
+    for (int e = 0; e < CNT; ++e) v[e] = act_of<IO>(v[e], p.act);
   }
   if (p.residual != nullptr) {
     IO::template ld<CNT>(reinterpret_cast<const T*>(p.residual) + at, t);
@@ -555,7 +586,7 @@ __global__ void __launch_bounds__(256, 1) ssm_linear_dma_kernel(LinDev p) {
           if (p.pre != nullptr) BufBF16::st<8>(rpre, off[k], v);
           if (p.act != kActNone) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = act_of(v[e], p.act);
+            for (int e = 0; e < 8; ++e) v[e] = act_of<BF16>(v[e], p.act);
           }
           if (p.residual != nullptr) {
 #pragma unroll
@@ -711,7 +742,7 @@ __global__ void __launch_bounds__(512) ssm_linear_rows_kernel(LinDev p) {
     v += bias;
     const int64_t at = er * p.nc + c0 + ec;
     if (p.pre != nullptr) IO::template st<1>(reinterpret_cast<T*>(p.pre) + at, &v);
-    v = act_of(v, p.act) + res;
+    v = act_of<IO>(v, p.act) + res;
     IO::template st<1>(reinterpret_cast<T*>(p.out) + at, &v);
   }
 }
@@ -738,7 +769,7 @@ __global__ void __launch_bounds__(256) ssm_linear_dpre_kernel(const void* dout, 
       if (act != kActNone) {
         IO::template ld<CNT>(static_cast<const T*>(pre) + t * m + c, q);
 #pragma unroll
-        for (int e = 0; e < CNT; ++e) d[e] *= act_grad(q[e], act);
+        for (int e = 0; e < CNT; ++e) d[e] *= act_grad<IO>(q[e], act);
       }
       if (dpre != nullptr) IO::template st<CNT>(static_cast<T*>(dpre) + t * ld + c, d);
 #pragma unroll
