@@ -144,8 +144,8 @@ def head_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[tor
               g_head: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
               lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None):
     """Differentiable head scan: returns (o, last_state).  g_head is a constant (a fixed decay per head takes no
-    gradient); a learned one is expanded to g."""
-    if g_head is not None and g_head.requires_grad:
+    gradient); a learned one is expanded to g, where gradients are recorded at all."""
+    if g_head is not None and g_head.requires_grad and torch.is_grad_enabled():
         raise ValueError("g_head takes no gradient: expand a learned decay to g [b, L, n_heads]")
     return _HeadScan.apply(q, k, v, g, h0, g_head, lengths, scale)
 
