@@ -173,9 +173,7 @@ def gate_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, z: Optiona
 
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, W, bias, residual, act):
-        # the value before act is kept only where its slope is asked for
-        keep = act != "none" and any(ctx.needs_input_grad[:3])
+    def forward(ctx, x, W, bias, residual, act, keep):
         r = ssm_linear(x, W, bias, residual, act, return_pre=keep)
         out, pre = r if keep else (r, None)
         ctx.save_for_backward(x, W, pre)
@@ -191,10 +189,13 @@ class _Linear(torch.autograd.Function):
         dx = dW = db = None
         if any(need[:3]):
             dx, dW, db = ssm_linear_bwd(x, W, dout, pre, ctx.act, want_dx=need[0], want_dW=need[1], want_dbias=need[2])
-        return dx, dW, db, dout if need[3] else None, None
+        return dx, dW, db, dout if need[3] else None, None, None
 
 
 def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None,
            residual: Optional[torch.Tensor] = None, act: str = "none") -> torch.Tensor:
     """Differentiable linear layer on token rows [..., d_in] with its epilogue: act(x W^T + bias) + residual."""
-    return _Linear.apply(x, W, bias, residual, act)
+    # the value before act is kept only where its slope will be asked for (needs_input_grad says so under no_grad too)
+    keep = act != "none" and torch.is_grad_enabled() and any(
+        isinstance(t, torch.Tensor) and t.requires_grad for t in (x, W, bias))
+    return _Linear.apply(x, W, bias, residual, act, keep)
