@@ -31,6 +31,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ssm_device.h"
 #include "ssm_kernels.h"
 
@@ -335,7 +337,9 @@ hipError_t launch_norm_v(const NormDev& p, Shape s, bool backward, int gate, hip
   if (s.lanes == 64) return launch_norm_t<IO, 64, 2, VEC>(p, backward, gate, st);
   if (s.nv == 2) return launch_norm_t<IO, 256, 2, VEC>(p, backward, gate, st);
   if (s.nv == 4) return launch_norm_t<IO, 256, 4, VEC>(p, backward, gate, st);
-  return launch_norm_t<IO, 256, 8, VEC>(p, backward, gate, st);
+  // float32 only: 8192 values of bfloat16 are four vectors a lane
+  if constexpr (std::is_same<IO, F32>::value) return launch_norm_t<IO, 256, 8, VEC>(p, backward, gate, st);
+  return hipErrorInvalidValue;
 }
 
 int64_t bwd_splits(const NormArgs& a, int64_t es) {
