@@ -15,6 +15,8 @@ using namespace ssm::capi;
 namespace {
 
 constexpr int64_t kLim31 = int64_t(1) << 31;
+// a launch has fewer than 2^32 threads; 256 for every 64 columns of a head
+constexpr int64_t kMaxWorkgroups = int64_t(1) << 24;
 
 int check_head_sizes(int64_t batch, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, int dtype) {
   if (batch <= 0 || L <= 0 || H <= 0 || Hk <= 0 || dk <= 0 || dv <= 0)
@@ -122,7 +124,7 @@ int ssm_head_scan_fwd(const void* q, int64_t q_batch, int64_t q_token, const voi
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(SSM_EINVAL, "workspace of %lld bytes, %lld are needed", (long long)(workspace ? workspace_bytes : 0),
                 (long long)need);
-  if (ssm::head_workgroups(a, bf16) >= kLim31) return fail(SSM_EUNSUPPORTED, "too many workgroups for one launch");
+  if (ssm::head_workgroups(a, bf16, false) >= kMaxWorkgroups) return fail(SSM_EUNSUPPORTED, "too many workgroups for one launch");
   if (int rc = check_overlaps({range_of(q, s.q), range_of(k, s.k), range_of(v, s.v), range_of(g, nt * es),
                                range_of(g_head, uint64_t(n_heads) * 4), range_of(h0, nstate),
                                range_of(lengths, uint64_t(batch) * 4)},
@@ -164,7 +166,7 @@ int ssm_head_scan_bwd(const void* q, int64_t q_batch, int64_t q_token, const voi
   if (!workspace || workspace_bytes < need)
     return fail(SSM_EINVAL, "workspace of %lld bytes, %lld are needed", (long long)(workspace ? workspace_bytes : 0),
                 (long long)need);
-  if (ssm::head_workgroups(a, bf16) >= kLim31) return fail(SSM_EUNSUPPORTED, "too many workgroups for one launch");
+  if (ssm::head_workgroups(a, bf16, true) >= kMaxWorkgroups) return fail(SSM_EUNSUPPORTED, "too many workgroups for one launch");
   if (int rc = check_overlaps({range_of(q, s.q), range_of(k, s.k), range_of(v, s.v), range_of(g, nt * es),
                                range_of(g_head, uint64_t(n_heads) * 4), range_of(h0, nstate),
                                range_of(lengths, uint64_t(batch) * 4), range_of(dout, nv), range_of(dlast, nstate)},

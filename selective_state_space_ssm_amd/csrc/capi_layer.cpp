@@ -14,7 +14,8 @@ using namespace ssm::capi;
 
 namespace {
 
-constexpr int64_t kLim31 = int64_t(1) << 31;
+// a launch has fewer than 2^32 threads, here in workgroups of 256
+constexpr int64_t kMaxWorkgroups = int64_t(1) << 24;
 
 int check_norm(ssm::NormArgs* a, const void* x, const void* z, const float* weight, int64_t rows, int64_t channels,
                int64_t groups, float eps, int center, int gate_first, int dtype) {
@@ -36,7 +37,7 @@ int check_norm(ssm::NormArgs* a, const void* x, const void* z, const float* weig
   a->x = x; a->z = z; a->w = weight;
   a->rows = rows; a->channels = channels; a->groups = groups;
   a->eps = eps; a->center = center; a->gate_first = gate_first;
-  if (ssm::norm_workgroups(*a, dtype == SSM_BF16) >= kLim31)
+  if (ssm::norm_workgroups(*a, dtype == SSM_BF16) >= kMaxWorkgroups)
     return fail(SSM_EUNSUPPORTED, "too many workgroups for one launch");
   return SSM_OK;
 }
@@ -72,7 +73,7 @@ int check_linear(ssm::LinearArgs* a, int64_t rows, int64_t k, int64_t m, int act
     return fail(SSM_EUNSUPPORTED, "d_in=%lld and d_out=%lld must be under 2^21", (long long)k, (long long)m);
   if (rows > (int64_t(1) << 36)) return fail(SSM_EUNSUPPORTED, "rows=%lld is too large", (long long)rows);
   a->rows = rows; a->k = k; a->m = m; a->act = act;
-  if (ssm::linear_workgroups(*a, dtype == SSM_BF16) >= kLim31)
+  if (ssm::linear_workgroups(*a, dtype == SSM_BF16) >= kMaxWorkgroups)
     return fail(SSM_EUNSUPPORTED, "too many output tiles for one launch");
   return SSM_OK;
 }

@@ -67,6 +67,7 @@ using headk::HeadDev;
 // 4, 500 tokens 28, 43).
 constexpr int64_t kHeadCUs = 256;
 constexpr int64_t kHeadSlots = 512;
+constexpr int64_t kHeadSumWorkgroups = 8192;  // of the sums over shared heads, which go on from there
 constexpr int64_t kHeadMinSegment = 64;       // tokens
 constexpr int64_t kHeadMinSegmentMany = 256;
 // Tokens that the running sum of dg covers: its terms are off by 2^-24 (float32)
@@ -163,22 +164,22 @@ __global__ void __launch_bounds__(256) ssm_head_dg_kernel(const float* s_seg, co
 }
 
 // out[t][hk][e] = sum over the heads that share hk of part[t][h][e], V values a
-// thread.  The parts stay float32: 32 pairs of heads of 128 over 4 x 2048 tokens are
+// thread and turn.  The parts stay float32: 32 pairs of heads of 128 over 4 x 2048 tokens are
 // 134 MB, 30 us to read (4.4 TB/s).
 template <typename IO, int V>
 __global__ void __launch_bounds__(256) ssm_head_group_sum_kernel(const float* part, void* out, int64_t n, int64_t d,
                                                                 int64_t rep) {
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V;
-  if (i >= n) return;
-  const float* src = part + (i / d) * rep * d + i % d;
-  float s[V] = {}, x[V];
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V; i < n; i += static_cast<int64_t>(gridDim.x) * 256 * V) {
+    const float* src = part + (i / d) * rep * d + i % d;
+    float s[V] = {}, x[V];
 #pragma unroll 8
-  for (int64_t r = 0; r < rep; ++r) {
-    F32::ld<V>(src + r * d, x);
+    for (int64_t r = 0; r < rep; ++r) {
+      F32::ld<V>(src + r * d, x);
 #pragma unroll
-    for (int e = 0; e < V; ++e) s[e] += x[e];
+      for (int e = 0; e < V; ++e) s[e] += x[e];
+    }
+    IO::template st<V>(static_cast<typename IO::T*>(out) + i, s);
   }
-  IO::template st<V>(static_cast<typename IO::T*>(out) + i, s);
 }
 
 // One token.  A workgroup owns one (batch row, head) and 32 columns of the
@@ -433,8 +434,8 @@ hipError_t launch_group_sum(const float* part, void* out, const HeadArgs& a, int
   const int64_t n = a.batch * a.L * a.Hk * a.dk;
   const bool four = a.dk % 4 == 0;
   auto kern = four ? ssm_head_group_sum_kernel<IO, 4> : ssm_head_group_sum_kernel<IO, 1>;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(cdiv(n, four ? 1024 : 256))), dim3(256), 0, st, part, out, n, a.dk,
-                     a.H / a.Hk / heads);
+  const int64_t wgs = std::min(cdiv(n, four ? 1024 : 256), kHeadSumWorkgroups);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(wgs)), dim3(256), 0, st, part, out, n, a.dk, a.H / a.Hk / heads);
   return hipGetLastError();
 }
 
@@ -444,9 +445,11 @@ int64_t head_workspace_bytes(const HeadArgs& a, bool bf16, bool backward) {
   return backward ? bwd_space(a, bwd_plan(a, bf16)).total : fwd_space(a, fwd_plan(a, bf16)).total;
 }
 
-int64_t head_workgroups(const HeadArgs& a, bool bf16) {
-  const int64_t t1 = tiles_for(a.dv, false), t2 = tiles_for(a.dk, false);
-  return a.batch * a.H * (t1 > t2 ? t1 : t2) * bwd_plan(a, bf16).nseg;
+int64_t head_workgroups(const HeadArgs& a, bool bf16, bool backward) {
+  // a tile of 128 columns counts as two of 64
+  auto tiles = [](int64_t cols) { return std::max(tiles_for(cols, false), cols > 64 ? 2 * tiles_for(cols, true) : 1); };
+  return backward ? a.batch * a.H * std::max(tiles(a.dv), tiles(a.dk)) * bwd_plan(a, bf16).nseg
+                  : a.batch * a.H * tiles(a.dv) * fwd_plan(a, bf16).nseg;
 }
 
 hipError_t launch_head_fwd(const HeadArgs& a, bool bf16, char* work, hipStream_t st) {

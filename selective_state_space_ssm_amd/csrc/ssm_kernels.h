@@ -211,8 +211,8 @@ struct HeadArgs {
 };
 constexpr int64_t kHeadMaxDim = 256;
 int64_t head_workspace_bytes(const HeadArgs& a, bool bf16, bool backward);
-// workgroups of the largest launch
-int64_t head_workgroups(const HeadArgs& a, bool bf16);
+// workgroups of the largest launch, of 256 threads each
+int64_t head_workgroups(const HeadArgs& a, bool bf16, bool backward);
 hipError_t launch_head_fwd(const HeadArgs& a, bool bf16, char* work, hipStream_t st);
 hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t st);
 

@@ -1043,10 +1043,13 @@ int64_t linear_workspace_bytes(const LinearArgs& a, bool bf16, bool backward) {
 }
 
 int64_t linear_workgroups(const LinearArgs& a, bool bf16) {
-  (void)bf16;
-  // the smallest tile; k is split where there are fewer tiles than CUs, for two workgroups a CU at most
-  const int64_t f = cdiv(a.m, 64) * cdiv(a.rows, 64), x = cdiv(a.k, 64) * cdiv(a.rows, 64);
-  return (f > x ? f : x) + 2 * kCUs + cdiv(a.k, 64) * cdiv(a.m, 64);
+  auto count = [&](int64_t nc, int64_t nr, int64_t K) {
+    const Tiling w = bf16 ? tiling<BF16>(nc, nr, K) : tiling<F32>(nc, nr, K);
+    return cdiv(nc, 32 * w.t) * cdiv(nr, 32 * w.t) * w.nsplit;
+  };
+  const int64_t f = count(a.m, a.rows, a.k), x = count(a.k, a.rows, a.m), w = count(a.k, a.m, a.rows);
+  const int64_t most = f > x ? f : x;
+  return most > w ? most : w;
 }
 
 hipError_t launch_linear(const LinearArgs& a, bool bf16, char* work, hipStream_t st) {

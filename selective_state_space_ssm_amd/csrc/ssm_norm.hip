@@ -161,13 +161,12 @@ __device__ __forceinline__ float normalise(const NormDev& p, int l, float* u, co
 }
 
 // Groups that the same lanes take one after the other in the forward.
-template <int LANES, int NV>
-constexpr int norm_units() { return LANES < 256 ? 4 / NV : 1; }
+constexpr int norm_units(int lanes, int nv) { return lanes < 256 ? 4 / nv : 1; }
 
 template <typename IO, int LANES, int NV, bool VEC, int GATE>
 __global__ void __launch_bounds__(256) ssm_gate_norm_kernel(NormDev p) {
   using Gr = Group<IO, LANES, NV, VEC>;
-  constexpr int U = norm_units<LANES, NV>(), PER = 256 / LANES;
+  constexpr int U = norm_units(LANES, NV), PER = 256 / LANES;
   __shared__ float sh[4];
   const int l = threadIdx.x % LANES;
   const int64_t total = p.rows * p.groups;
@@ -296,7 +295,7 @@ __global__ void __launch_bounds__(1024) ssm_column_sum_kernel(const float* part,
 template <typename IO, int LANES, int NV, bool VEC>
 hipError_t launch_norm_t(NormDev p, bool backward, int gate, hipStream_t st) {
   constexpr int PER = 256 / LANES;
-  constexpr int64_t fwd = PER * norm_units<LANES, NV>();
+  constexpr int64_t fwd = PER * norm_units(LANES, NV);
   const int64_t blocks = backward ? (p.groups + PER - 1) / PER * p.nsplit : (p.rows * p.groups + fwd - 1) / fwd;
   auto run = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p);
@@ -357,8 +356,11 @@ int64_t norm_workspace_bytes(const NormArgs& a, bool bf16) {
 }
 
 int64_t norm_workgroups(const NormArgs& a, bool bf16) {
-  const Shape s = shape_of(a.channels / a.groups, bf16 ? 2 : 4);
-  return (a.rows * a.groups * s.lanes + 255) / 256;
+  const int64_t es = bf16 ? 2 : 4;
+  const Shape s = shape_of(a.channels / a.groups, es);
+  const int64_t per = 256 / s.lanes, fwd = per * norm_units(s.lanes, s.nv);
+  const int64_t f = (a.rows * a.groups + fwd - 1) / fwd, b = (a.groups + per - 1) / per * bwd_splits(a, es);
+  return f > b ? f : b;
 }
 
 hipError_t launch_column_sum(const float* part, int64_t count, int64_t cols, void* out, bool bf16, hipStream_t st) {
