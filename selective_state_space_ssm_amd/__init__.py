@@ -710,6 +710,8 @@ def _head_sizes(q: torch.Tensor, v: torch.Tensor, name: str, dims: int):
             "L, " if dims == 4 else ""))
     if q.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("q must be float32 or bfloat16")
+    if 0 in q.shape or 0 in v.shape:
+        raise SSMError(SSM_EINVAL, f"sizes must be positive (q {tuple(q.shape)}, v {tuple(v.shape)})")
 
 
 def _head_decay(g, g_head, shape, heads, dtype, device):

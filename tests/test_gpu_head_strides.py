@@ -45,3 +45,17 @@ def test_a_stride_over_a_size_of_one_means_nothing(b, L, token, batch, dtype, ba
     got = run(x, token, batch, backward)
     assert all(torch.equal(a, w) for a, w in zip(got, want))
     assert all(float(a.float().abs().min()) < 7 for a in got)
+
+
+def test_empty_sizes_are_refused_as_such():
+    """No token, no sequence, no key, no value: the library's own refusal, for every call."""
+    new = lambda *s: torch.zeros(*s, device=DEV)
+    for b, L, h, dk, dv in ((0, 3, 2, 4, 4), (1, 0, 2, 4, 4), (1, 3, 0, 4, 4), (1, 3, 2, 0, 4), (1, 3, 2, 4, 0)):
+        q, v = new(b, L, h, dk), new(b, L, h, dv)
+        with pytest.raises(ssm.SSMError, match="sizes must be positive"):
+            ssm.ssm_head_scan_fwd(q, q.clone(), v)
+        with pytest.raises(ssm.SSMError, match="sizes must be positive"):
+            ssm.ssm_head_scan_bwd(q, q.clone(), v, v.clone())
+        if L:
+            with pytest.raises(ssm.SSMError):
+                ssm.ssm_head_step(new(b, h, dk), new(b, h, dk), new(b, h, dv), new(b, h, dk, dv))
