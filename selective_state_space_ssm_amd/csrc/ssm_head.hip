@@ -50,21 +50,21 @@ using headk::HeadDev;
 
 // The length is split where there are fewer workgroups than CUs, into as many
 // segments as give every CU two.  A split costs a second pass over y and z for
-// the segments' states: 256 heads of 128 x 128 (8 x 2048 tokens, bfloat16) take
-// 168 us whole and 187 us in two segments; 16 heads over 65536 tokens 512 us in
-// 16 segments, 464 in 32, 524 in 48.  The backward's three passes share the
-// segments' states: it is split for two workgroups per CU in any case (4 x 2048
-// tokens, 64 heads of 128 x 64: 815 us whole, 731 in two, 820 in three; float32,
-// 4 x 1999, 24 heads of 64: 538 whole, 384 in six).
+// the segments' states: 256 heads of 128 x 128 (8 x 2048 ragged tokens, bfloat16)
+// take 151 us whole and 180 us in two segments; 16 heads over 65536 tokens 438 us
+// in 32 segments, 489 in 48.  The backward's three passes share the segments'
+// states: it is split for two workgroups per CU in any case (gradients of 4 x 2048
+// tokens, 64 heads of 128 x 64: 737 us whole, 551 in two, 672 in three; float32,
+// 4 x 1999, 24 heads of 64: 457 whole, 295 in five).
 // How short a segment may be: its states take two passes whatever its length,
 // and they are carried over the segments one after the other, so that the best
 // number of segments grows like the root of the length (4 heads, 8000 tokens:
-// bfloat16, 128 x 128, 49 us with the root's 42 segments, 56 with 31, 66 with
-// 125).  Below that 64 tokens: float32, 100 x 48, 300 tokens 32 us whole 51, 2757
-// tokens 40, in segments of 256 73 (forward and gradients 184, 283).  bfloat16
+// bfloat16, 128 x 128, 47 us with the root's 42 segments, 55 with 31, 66 with
+// 125).  Below that 64 tokens: float32, 100 x 48, 300 tokens 31 us, whole 51, 2757
+// tokens 40, in segments of 256 73 (their gradients 114, 213).  bfloat16
 // with more than 64 heads or fewer than six chunks is better off with 256
 // (128 heads, 500 tokens 46 us, in segments of 64 or 128 tokens 53; few heads:
-// 4, 500 tokens 28, 43).
+// 4, 500 tokens 27, 43).
 constexpr int64_t kHeadCUs = 256;
 constexpr int64_t kHeadSlots = 512;
 constexpr int64_t kHeadSumWorkgroups = 8192;  // of the sums over shared heads, which go on from there
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(256) ssm_head_group_sum_kernel(const float* pa
 // state: thread (rg, c) takes rows rg + 32 i, columns 4 c .. 4 c + 3.  Every
 // load is issued before the first store (the update may be in place); the
 // bound is the state's traffic, 8 bytes per value: 256 rows of 32 heads of 128 x
-// 128 take 192 us, 5.6 TB/s.
+// 128 take 191 us, 5.6 TB/s.
 struct HeadStepDev {
   const char* q;
   const char* k;
@@ -419,9 +419,9 @@ Plan bwd_plan(const HeadArgs& a, bool bf16) {
 }
 
 // Heads whose parts of dq and dk a workgroup adds (kOutPair) where q and k are
-// shared: two if that leaves every CU a workgroup.  4 x 2048 tokens, 64 heads of
-// 128 x 64, bfloat16: the two passes 149 us each and their sums 30; one head a
-// workgroup 154 and 58.
+// shared: two if that leaves every CU a workgroup.  Gradients of 4 x 2048 tokens,
+// 64 heads of 128 x 64, bfloat16: 551 us (the two passes 147 each, their sums 30),
+// one head a workgroup 619.
 int64_t part_heads(const HeadArgs& a, const Plan& pl, bool bf16) {
   return bf16 && pl.vec && a.dv <= headk::kPairRows && a.H / a.Hk % 2 == 0 &&
                  a.batch * a.H / 2 * tiles_for(a.dk, true) * pl.nseg >= kHeadCUs

@@ -24,8 +24,8 @@
 // score matrix is shared by the wavefronts, through LDS.  The next chunk's
 // tiles are loaded into registers while the present one is worked on.  Eight
 // wavefronts take 128 columns, four 64 or fewer: with four for 128 the state and
-// the tiles in flight do not fit the registers (522 us for the case below,
-// 255 with eight).
+// the tiles in flight do not fit the registers (twice the time in the case
+// below).
 //
 // Roundings.  bfloat16 storage: scores and the state enter their products as
 // hi + lo pairs of bfloat16 (error 2^-17), and the decayed z of the state's
@@ -34,9 +34,11 @@
 // pair of float32, since differences of it are exponentiated.  float32
 // storage: float32 matrix instructions, nothing is rounded further.
 //
-// What bounds it.  8 x 2048 ragged tokens (five eighths of them there), 32
-// heads of 128 x 128, bfloat16: 156 us, 2.3 TB/s of q, k, v, o and the last
-// states; its loads and stores alone take 116 us, the scores 26.  A head's
+// What bounds it.  8 x 2048 ragged tokens (some five eighths of them there), 32
+// heads of 128 x 128, bfloat16: 150 us where the longest row has 1630 tokens, 171
+// where it has 2029 (a row's workgroups walk it whole), 2.2 TB/s of q, k, v, o and
+// the last states; the loads and stores alone are three quarters of it, the
+// scores a sixth (each left out by itself).  A head's
 // chunks follow each other, 256 heads are one workgroup a CU, and a chunk's
 // 5 us are vector work (some 560 instructions a wavefront: decays, splits into
 // bfloat16 parts) and then matrix work (97 instructions of 16 cycles) between
@@ -82,8 +84,8 @@ struct HeadCfg<F32> {
 // lane, which go by 16 lanes, four chunks of 16 rows (a sixteen holds rows 0 to
 // 3 and 12 to 15 of one chunk and rows 4 to 11 of its neighbour: with a swizzle
 // made for 16 rows of one chunk every such read took half as long again, 9.1
-// instead of 3.0 million cycles of bank conflicts in the case above, 172 instead
-// of 167 us), and (bfloat16) two chunks of four rows from each of two eights;
+// instead of 3.0 million cycles of bank conflicts in the case above, 3 % of its
+// time), and (bfloat16) two chunks of four rows from each of two eights;
 // four half chunks of them, the state's update, are two to a bank at best.
 // (float32: four chunks of rows four apart.)  swz goes by r % 16, so that an
 // address is a lane's base, XORed with a constant for the chunk and offset by
@@ -316,7 +318,10 @@ constexpr size_t head_lds_bytes() {
 template <typename IO, int NW, int NC, int MODE>
 constexpr size_t pair_lds_bytes() { return MODE == kOutPair ? size_t(HeadCfg<IO>::C) * 16 * NW * NC * 4 : 0; }
 
-// Wavefronts per SIMD the registers have to leave room for: what fits without spills.
+// Wavefronts per SIMD the registers have to leave room for: what fits without
+// spills.  One size does not: float32, more than 128 rows, four wavefronts, 131 to
+// 156 registers of 256 and their traffic in the chunk loop (4 x 2048 tokens, 32
+// heads of 192 x 48: 456 us, bfloat16 188).
 template <typename IO, int ROWS, int NW, bool DOT, bool VEC>
 constexpr int head_waves() {
   if (!VEC || ROWS == 256) return 2;

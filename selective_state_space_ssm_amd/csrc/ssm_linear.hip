@@ -14,9 +14,9 @@
 //   dx       token  k      m      dpre          W, rows contiguous
 //   dW       m      k      token  dpre, rows c. x, rows contiguous
 //
-// 16384 x 4096 -> 2048 in bfloat16 with gelu and residual: 316 us forward (870
+// 16384 x 4096 -> 2048 in bfloat16 with gelu and residual: 289 us forward (950
 // TFLOP/s; the epilogue's 200 MB come after the products, nothing covers them),
-// dx 265, dW 238 (1155), dpre 47.  8192 x 4096 -> 2048 in float32: 131 TFLOP/s.
+// dx 237, dW 222 (1240), dpre 43.  8192 x 4096 -> 2048 in float32: 131 TFLOP/s.
 // Both are bound by the matrix instructions and what stands between them.
 //
 // The c side is the first operand of the matrix instruction, so that a lane
@@ -489,8 +489,8 @@ __global__ void __launch_bounds__(256, 1) ssm_linear_dma_kernel(LinDev p) {
   // and this wavefront's reads of step s - 1 are done; barrier; then step s's 64 products.  What else the step issues,
   // the reads of step s + 1's operands and the refill of the stage read at step s - 1, stands between the first 32 of
   // them, so that it goes out while the matrix unit is busy and the reads have the other 32 to arrive: forward, dx and
-  // dW of 16384 x 4096 -> 2048 take 316, 265 and 238 us, in four blocks between groups of 16 products 365, 315 and 280,
-  // spread over 24 or all 32 pairs 320, 277 and 246.
+  // dW of 16384 x 4096 -> 2048 take 0.87, 0.84 and 0.85 of the time that they took in four blocks between groups of 16
+  // products, spread over 24 or all 32 pairs 0.88, 0.88 and 0.88.
   using S0 = std::integral_constant<int, 0>;
   using S1 = std::integral_constant<int, 1>;
   using S2 = std::integral_constant<int, 2>;
@@ -543,8 +543,8 @@ __global__ void __launch_bounds__(256, 1) ssm_linear_dma_kernel(LinDev p) {
   if constexpr (OUT == kFull) {
     // The epilogue reads and writes whole 128-byte runs of a row: every wavefront passes its 128 x 128 sums through
     // its quarter of the LDS in two halves of 64 columns ([128 rows][16 chunks of 4 columns], chunk q of row r at
-    // q ^ (r & 15)).  Straight from the accumulators it is 64 copies of the epilogue's code (547 us for the forward of
-    // 16384 x 4096 -> 2048 with gelu and residual).
+    // q ^ (r & 15)).  Straight from the accumulators it is 64 copies of the epilogue's code (the forward of 16384 x
+    // 4096 -> 2048 with gelu and residual half as long again).
     // The residuals of eight rows a lane are in flight together.
     __syncthreads();
     float4* own = reinterpret_cast<float4*>(&stg[0][0]) + wave * 128 * 16;
@@ -802,7 +802,7 @@ int64_t up(int64_t n, int64_t to) { return cdiv(n, to) * to; }
 // One product's tile (32 t x 32 t) and split of k.
 //   bfloat16 takes 256 x 256 tiles (t = 8) where they, with k in parts of at
 //   least 1024, give three quarters of the CUs a workgroup (products of 16384 x
-//   4096 x 2048: 238 to 316 us, 128 x 128 tiles 448 to 514).
+//   4096 x 2048: 222 to 289 us, 128 x 128 tiles 1.6 to 1.9 times that).
 //   Else 128 x 128 where they, with k in parts of at least 16 steps, give as
 //   many (300 x 4096 -> 2048: bfloat16 25 us, float32 73; 64 x 64: 40 and 103;
 //   forward and gradients of 4099 x 768 -> 1536 in float32: 339, 64 x 64 where

@@ -19,11 +19,16 @@
 // that covers it with one 16-byte vector per lane, a wavefront with two, a
 // workgroup of 256 with up to eight beyond that (few registers a lane, so
 // that many wavefronts' loads are in flight).  In the forward small groups are
-// taken several at a time by the same lanes, for the same reason.
+// taken several at a time by the same lanes, for the same reason.  Groups that
+// are no whole vectors take single values in the same shapes.
 //
 // Measured: 16384 x 4096 in 32 groups, bfloat16, 100 us (4.0 TB/s; one group at
 // a time 142); 8191 x 1536 in one group, float32, forward 24 us and backward
-// 44 (the backward with 64 lanes and eight vectors each: 124).
+// 44 (the backward with 64 lanes and eight vectors each: 124).  Single values are
+// slower, 4096 rows of 5001 with the gate first 134 us in bfloat16 and 47 in
+// float32 (5000: 29 and 37), backward 318 and 125 (110 and 108); above 4096 of
+// them without a gate or with it last the forward's registers spill by the
+// thousand: 3.1 and 4.1 ms.
 //
 // dw is a sum over rows: every workgroup of the backward walks rows of one
 // group, keeps its sum in registers and leaves one float32 partial; a second
