@@ -452,9 +452,9 @@ int ssm_head_scan_fwd(const void *q, int64_t q_batch, int64_t q_token, const voi
  * (they cancel), over at most 1024 tokens (float32; bfloat16 4096) and back to
  * the last token before which the state started anew: its error goes by the
  * size of those dots, so that a token that forgets everything between others
- * that do not has theirs.  dq and dk take a token's own pair in float32 where dg
- * is asked for and otherwise as the scores' pairs of bfloat16 (n_qk_heads =
- * n_heads): their last bits may differ.
+ * that do not has theirs.  Where dg is asked for (and with shared q and k in
+ * bfloat16) a token's own pair is added to dq and dk after the other products:
+ * their last bits may differ from those of a call without dg.
  * Values that are not finite: a k reaches every dq, a q every dk and a do every dv
  * of its token's chunk, with dg of the tokens before them in their sequences;
  * otherwise they stay within their sequence as in the forward.
