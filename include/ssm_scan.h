@@ -490,6 +490,68 @@ int ssm_head_step(const void *q, const void *k, const void *v, const void *g, co
                   int64_t d_key, int64_t d_value, int dtype, void *stream);
 
 /*
+ * ssm_delta_scan_fwd -- the head scan with the gated delta rule: before a token's
+ * value is written under its key, what the state holds there is taken out,
+ *     S~_t = exp(g_t) S_{t-1},      r_t = v_t - S~_t^T k_t,
+ *     S_t  = S~_t + beta_t k_t r_t^T,   o_t = scale * S_t^T q_t.
+ * beta 1 and k of unit length replace the value under k; the recurrence is stable
+ * while beta |k|^2 is between 0 and 2 (keys are normalised in front of it, e.g. by
+ * ssm_gate_norm with a weight of d_key^-1/2).
+ *   beta : [batch, L, n_heads], dtype `dtype`, aligned to its type.  Nullable (ones).
+ *   workspace : device memory of ssm_delta_scan_workspace(..., backward = 0)
+ *          bytes, the caller's; calls that may run at the same time need one each.
+ * All other arguments, limits and errors as ssm_head_scan_fwd (no g_head: a fixed
+ * decay is expanded to g).
+ * Rounding: sums, decays, r and the state are float32.  With SSM_BF16 the state
+ * and what is added to it enter products as three parts of bfloat16 (all of a
+ * float32), the scores and the corrections among a chunk's tokens as two (off by
+ * 2^-17 of themselves).
+ * Values that are not finite reach every later result of their head in their
+ * batch row, and those of their chunk (64 tokens from a multiple of 64, float32:
+ * 32) before them; a decay of -inf does not hold them back within a chunk.
+ */
+int ssm_delta_scan_fwd(const void *q, int64_t q_batch, int64_t q_token, const void *k, int64_t k_batch, int64_t k_token,
+                       const void *v, int64_t v_batch, int64_t v_token, const void *g, const void *beta,
+                       const float *h0, const int32_t *lengths, float scale, void *o, float *last_state,
+                       void *workspace, int64_t workspace_bytes, int64_t batch, int64_t L, int64_t n_heads,
+                       int64_t n_qk_heads, int64_t d_key, int64_t d_value, int dtype, void *stream);
+
+/*
+ * ssm_delta_scan_bwd -- gradients of ssm_delta_scan_fwd for the loss
+ * sum(do * o) + sum(dlast * last_state).  With R_t = dLoss/dS_t, e_t = R_t^T k_t,
+ *     dv_t = beta_t e_t,   dbeta_t = e_t . r_t,   dq_t = scale S_t do_t,
+ *     dk_t = beta_t R_t r_t - S~_t dv_t,          dg_t = <R_t - k_t dv_t^T, S~_t>,
+ *     R_{t-1} = exp(g_t) (R_t - k_t dv_t^T) + scale q_{t-1} do_{t-1}^T  (R_L += dlast)
+ * dq and dk summed over the heads that share a q and k head.
+ *   dbeta : [batch, L, n_heads], dtype `dtype`, output, nullable; needs beta.
+ *   workspace : ssm_delta_scan_workspace(..., backward = 1) bytes: it holds the
+ *           state and its gradient at every chunk.
+ * dg of a chunk's tokens is a sum over the chunk from its end.  Every sum is taken
+ * in a fixed order: repeated calls give identical bits.
+ * Other arguments and errors as ssm_head_scan_bwd and ssm_delta_scan_fwd.
+ */
+int ssm_delta_scan_bwd(const void *q, int64_t q_batch, int64_t q_token, const void *k, int64_t k_batch, int64_t k_token,
+                       const void *v, int64_t v_batch, int64_t v_token, const void *g, const void *beta,
+                       const float *h0, const int32_t *lengths, float scale, const void *dout, const float *dlast,
+                       void *dq, void *dk, void *dv, void *dg, void *dbeta, float *dh0, void *workspace,
+                       int64_t workspace_bytes, int64_t batch, int64_t L, int64_t n_heads, int64_t n_qk_heads,
+                       int64_t d_key, int64_t d_value, int dtype, void *stream);
+
+/* Bytes of workspace ssm_delta_scan_fwd (backward = 0) or ssm_delta_scan_bwd (1) needs for a size (host only). */
+int ssm_delta_scan_workspace(int64_t batch, int64_t L, int64_t n_heads, int64_t n_qk_heads, int64_t d_key,
+                             int64_t d_value, int dtype, int backward, int64_t *bytes);
+
+/*
+ * ssm_delta_step -- one token of the delta scan for every sequence:
+ *     S~ = exp(g) S,   S <- S~ + beta k (v - S~^T k)^T,   o = scale * S^T q.
+ *   beta : [batch, n_heads], dtype `dtype`, nullable (ones).
+ * Other arguments, sizes and errors as ssm_head_step (no g_head).
+ */
+int ssm_delta_step(const void *q, const void *k, const void *v, const void *g, const void *beta, float scale,
+                   const float *state_in, float *state_out, void *o, int64_t batch, int64_t n_heads, int64_t n_qk_heads,
+                   int64_t d_key, int64_t d_value, int dtype, void *stream);
+
+/*
  * ssm_gate_norm -- grouped norm of token rows (channels last) with a SiLU gate,
  * what follows the head scan in its block.  Every row of `channels` values is
  * cut into `groups` groups; with n^ = (u - mu) / sqrt(mean((u - mu)^2) + eps)

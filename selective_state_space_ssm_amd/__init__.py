@@ -19,7 +19,9 @@ import torch
 
 __all__ = ["SSMError", "ssm_scan_fwd", "ssm_scan_fwd_states", "ssm_scan_fwd_conv", "ssm_scan_bwd",
            "ssm_scan_bwd_conv", "ssm_step", "ssm_step_conv", "ssm_out_proj", "ssm_out_proj_bwd", "ssm_head_scan_fwd",
-           "ssm_head_scan_bwd", "ssm_head_step", "ssm_gate_norm", "ssm_gate_norm_bwd", "ssm_linear", "ssm_linear_bwd", "affine_scan", "affine_scan_order", "plan_for", "library_path", "load_library", "PLANS", "ACTS"]
+           "ssm_head_scan_bwd", "ssm_head_step", "ssm_delta_scan_fwd", "ssm_delta_scan_bwd", "ssm_delta_step",
+           "ssm_gate_norm", "ssm_gate_norm_bwd", "ssm_linear", "ssm_linear_bwd", "affine_scan", "affine_scan_order",
+           "plan_for", "library_path", "load_library", "PLANS", "ACTS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libssmscan.so")
@@ -94,6 +96,14 @@ def load_library():
     lib.ssm_head_scan_workspace.restype = I
     lib.ssm_head_step.argtypes = [P, P, P, P, P, F, P, P, P] + [I64] * 5 + [I, P]
     lib.ssm_head_step.restype = I
+    lib.ssm_delta_scan_fwd.argtypes = strided + [P, P, P, P, F, P, P, P, I64] + [I64] * 6 + [I, P]
+    lib.ssm_delta_scan_fwd.restype = I
+    lib.ssm_delta_scan_bwd.argtypes = strided + [P, P, P, P, F, P, P, P, P, P, P, P, P, P, I64] + [I64] * 6 + [I, P]
+    lib.ssm_delta_scan_bwd.restype = I
+    lib.ssm_delta_scan_workspace.argtypes = [I64] * 6 + [I, I, ctypes.POINTER(I64)]
+    lib.ssm_delta_scan_workspace.restype = I
+    lib.ssm_delta_step.argtypes = [P, P, P, P, P, F, P, P, P] + [I64] * 5 + [I, P]
+    lib.ssm_delta_step.restype = I
     lib.ssm_gate_norm.argtypes = [P, P, P, P, I64, I64, I64, F, I, I, I, P]
     lib.ssm_gate_norm.restype = I
     lib.ssm_gate_norm_bwd.argtypes = [P] * 8 + [I64, I64, I64, I64, F, I, I, I, P]
@@ -828,6 +838,118 @@ def ssm_head_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, state: torc
     else:
         _need(o, "o", dt, device, (b, h, dv))
     _call(device, load_library().ssm_head_step, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(g_head),
+          dk ** -0.5 if scale is None else float(scale), state.data_ptr(), state_out.data_ptr(), o.data_ptr(), b, h, hk,
+          dk, dv, SSM_F32 if dt == torch.float32 else SSM_BF16)
+    return o, state_out
+
+
+def _delta_rates(g, beta, shape, dtype, device):
+    for t, n in ((g, "g"), (beta, "beta")):
+        if t is not None:
+            _need(t, n, dtype, device, shape)
+
+
+def ssm_delta_scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: Optional[torch.Tensor] = None,
+                       g: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                       lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                       return_last_state: bool = True, o: Optional[torch.Tensor] = None,
+                       last_state: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Scan with the gated delta rule and a matrix state, S~_t = e^{g_t} S_{t-1}, S_t = S~_t + beta_t k_t (v_t - S~_t^T
+    k_t)^T, o_t = scale S_t^T q_t (see ``ssm_delta_scan_fwd`` in include/ssm_scan.h).
+
+    beta: [b, L, n_heads] in the dtype of q (None: ones), everything else as in ``ssm_head_scan_fwd``.
+    Returns (o [b, L, n_heads, d_value], last_state float32 or None).
+    """
+    _head_sizes(q, v, "ssm_delta_scan_fwd", 4)
+    device, dt = q.device, q.dtype
+    b, L, hk, dk = q.shape
+    h, dv = v.shape[2:]
+    ops = [_head_operand(t, n, dt, device, s) for t, n, s in ((q, "q", (b, L, hk, dk)), (k, "k", (b, L, hk, dk)),
+                                                              (v, "v", (b, L, h, dv)))]
+    _delta_rates(g, beta, (b, L, h), dt, device)
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, device, (b, h, dk, dv))
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, device, (b,))
+    if o is None:
+        o = torch.empty_like(v, memory_format=torch.contiguous_format)
+    else:
+        _need(o, "o", dt, device, (b, L, h, dv))
+    if last_state is not None:
+        _need(last_state, "last_state", torch.float32, device, (b, h, dk, dv))
+    elif return_last_state:
+        last_state = torch.empty((b, h, dk, dv), device=device, dtype=torch.float32)
+    code = SSM_F32 if dt == torch.float32 else SSM_BF16
+    ws, nws = _workspace("ssm_delta_scan_workspace", device, b, L, h, hk, dk, dv, code, 0)
+    _call(device, load_library().ssm_delta_scan_fwd, *ops[0], *ops[1], *ops[2], _addr(g), _addr(beta), _addr(h0),
+          _addr(lengths), dk ** -0.5 if scale is None else float(scale), o.data_ptr(), _addr(last_state), _addr(ws), nws,
+          b, L, h, hk, dk, dv, code)
+    return o, last_state
+
+
+def ssm_delta_scan_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, do: torch.Tensor,
+                       beta: Optional[torch.Tensor] = None, g: Optional[torch.Tensor] = None,
+                       h0: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                       dlast: Optional[torch.Tensor] = None, scale: Optional[float] = None, want_dg: bool = True,
+                       want_dbeta: bool = True, want_dh0: bool = True) -> dict:
+    """Gradients of ssm_delta_scan_fwd (see ``ssm_delta_scan_bwd`` in include/ssm_scan.h) for do [b, L, n_heads,
+    d_value] (dense, dtype of v) and dlast (float32, or None).  Returns a dict with dq, dk, dv, dg and dbeta (dtype of
+    q; None without g or beta or when not asked for) and dh0 (float32, or None)."""
+    _head_sizes(q, v, "ssm_delta_scan_bwd", 4)
+    device, dt = q.device, q.dtype
+    b, L, hk, dk = q.shape
+    h, dv = v.shape[2:]
+    ops = [_head_operand(t, n, dt, device, s) for t, n, s in ((q, "q", (b, L, hk, dk)), (k, "k", (b, L, hk, dk)),
+                                                              (v, "v", (b, L, h, dv)))]
+    _need(do, "do", dt, device, (b, L, h, dv))
+    _delta_rates(g, beta, (b, L, h), dt, device)
+    for t, n in ((h0, "h0"), (dlast, "dlast")):
+        if t is not None:
+            _need(t, n, torch.float32, device, (b, h, dk, dv))
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, device, (b,))
+    out = {
+        "dq": q.new_empty((b, L, hk, dk)),
+        "dk": q.new_empty((b, L, hk, dk)),
+        "dv": torch.empty_like(do),
+        "dg": torch.empty_like(g) if want_dg and g is not None else None,
+        "dbeta": torch.empty_like(beta) if want_dbeta and beta is not None else None,
+        "dh0": torch.empty((b, h, dk, dv), device=device, dtype=torch.float32) if want_dh0 else None,
+    }
+    code = SSM_F32 if dt == torch.float32 else SSM_BF16
+    ws, nws = _workspace("ssm_delta_scan_workspace", device, b, L, h, hk, dk, dv, code, 1)
+    _call(device, load_library().ssm_delta_scan_bwd, *ops[0], *ops[1], *ops[2], _addr(g), _addr(beta), _addr(h0),
+          _addr(lengths), dk ** -0.5 if scale is None else float(scale), do.data_ptr(), _addr(dlast),
+          *(_addr(t) for t in out.values()), _addr(ws), nws, b, L, h, hk, dk, dv, code)
+    return out
+
+
+def ssm_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: Optional[torch.Tensor], state: torch.Tensor,
+                   g: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                   state_out: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None):
+    """One token of the delta scan (see ``ssm_delta_step`` in include/ssm_scan.h).
+
+    beta: [b, n_heads] in the dtype of q (None: ones), everything else as in ``ssm_head_step``.  The new state goes to
+    ``state_out`` (default: ``state`` itself, updated in place).  Returns (o [b, n_heads, d_value], state_out).
+    """
+    _head_sizes(q, v, "ssm_delta_step", 3)
+    device, dt = q.device, q.dtype
+    b, hk, dk = q.shape
+    h, dv = v.shape[1:]
+    _need(q, "q", dt, device, (b, hk, dk))
+    _need(k, "k", dt, device, (b, hk, dk))
+    _need(v, "v", dt, device, (b, h, dv))
+    _delta_rates(g, beta, (b, h), dt, device)
+    _need(state, "state", torch.float32, device, (b, h, dk, dv))
+    if state_out is None:
+        state_out = state
+    else:
+        _need(state_out, "state_out", torch.float32, device, (b, h, dk, dv))
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _need(o, "o", dt, device, (b, h, dv))
+    _call(device, load_library().ssm_delta_step, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(g), _addr(beta),
           dk ** -0.5 if scale is None else float(scale), state.data_ptr(), state_out.data_ptr(), o.data_ptr(), b, h, hk,
           dk, dv, SSM_F32 if dt == torch.float32 else SSM_BF16)
     return o, state_out

@@ -8,6 +8,7 @@ marshalling only; every step runs in the library's kernels.
     y, last_state = selective_scan_conv(x, conv_w, conv_b, delta, A, B, C, D, z, ...)
     out = out_proj(y, W)          # the Linear after the gate, [b, L, d_model]
     o, last_state = head_scan(q, k, v, g=g)   # one decay per head, matrix state
+    o, last_state = delta_scan(q, k, v, beta, g=g)   # the same with the gated delta rule
     y = gate_norm(x, weight, z, groups=heads)   # grouped norm of token rows with a SiLU gate
     out = linear(y, W, bias, residual, act="silu")   # act(y W^T + bias) + residual
 
@@ -21,11 +22,11 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (ssm_gate_norm, ssm_gate_norm_bwd, ssm_head_scan_bwd, ssm_head_scan_fwd, ssm_linear, ssm_linear_bwd,
+from . import (ssm_delta_scan_bwd, ssm_delta_scan_fwd, ssm_gate_norm, ssm_gate_norm_bwd, ssm_head_scan_bwd, ssm_head_scan_fwd, ssm_linear, ssm_linear_bwd,
                ssm_out_proj, ssm_out_proj_bwd, ssm_scan_bwd, ssm_scan_bwd_conv,
                ssm_scan_fwd_conv, ssm_scan_fwd_states)
 
-__all__ = ["selective_scan", "selective_scan_conv", "out_proj", "head_scan", "gate_norm", "linear"]
+__all__ = ["selective_scan", "selective_scan_conv", "out_proj", "head_scan", "delta_scan", "gate_norm", "linear"]
 
 
 def _grad_or_zero(g, like):
@@ -148,6 +149,33 @@ def head_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: Optional[tor
     if g_head is not None and g_head.requires_grad and torch.is_grad_enabled():
         raise ValueError("g_head takes no gradient: expand a learned decay to g [b, L, n_heads]")
     return _HeadScan.apply(q, k, v, g, h0, g_head, lengths, scale)
+
+
+class _DeltaScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, beta, g, h0, lengths, scale):
+        ctx.set_materialize_grads(False)
+        o, last = ssm_delta_scan_fwd(q, k, v, beta, g=g, h0=h0, lengths=lengths, scale=scale)
+        ctx.save_for_backward(q, k, v, beta, g, h0, lengths)
+        ctx.scale = scale
+        return o, last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do, dlast):
+        q, k, v, beta, g, h0, lengths = ctx.saved_tensors
+        r = ssm_delta_scan_bwd(q, k, v, v.new_zeros(v.shape) if do is None else _dense(do), beta, g=g, h0=h0,
+                               lengths=lengths, dlast=None if dlast is None else _dense(dlast), scale=ctx.scale,
+                               want_dbeta=ctx.needs_input_grad[3], want_dg=ctx.needs_input_grad[4],
+                               want_dh0=ctx.needs_input_grad[5])
+        return r["dq"], r["dk"], r["dv"], r["dbeta"], r["dg"], r["dh0"], None, None
+
+
+def delta_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: Optional[torch.Tensor] = None,
+               g: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+               lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None):
+    """Differentiable delta scan: returns (o, last_state)."""
+    return _DeltaScan.apply(q, k, v, beta, g, h0, lengths, scale)
 
 
 class _GateNorm(torch.autograd.Function):

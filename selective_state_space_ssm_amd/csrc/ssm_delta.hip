@@ -1,0 +1,441 @@
+// The delta scan: the head scan whose update takes out what the state holds
+// under the key first,
+//
+//   S~_t = e^{g_t} S_{t-1},  r_t = v_t - S~_t^T k_t,  S_t = S~_t + b_t k_t r_t^T,  o_t = scale S_t^T q_t,
+//
+// its gradients and its step for single tokens.  The chunk kernels and their
+// mathematics are in ssm_delta_kernel.h; here are the order of the passes, the
+// carry over segments of the length and the step.
+//
+//   forwards   M of all chunks | [segments' own ends and transitions, carry] | the walk with the outputs
+//   backwards  M | [segments] | the walk that keeps the states and r | [segments from the end] | the walk from the
+//              end that keeps R and e | all other gradients, all chunks at once | [sums over shared heads]
+//
+// The walk is a chain of chunks; where batch rows, heads and column tiles leave
+// CUs idle the length is cut into segments.  A segment makes A S + B of the state
+// S before it: B is the walk from zero, A the walk from the identity without v,
+// so that both come from the same kernel, and R before it is A^T R + B'.
+//
+// Page cited: [Mamba-2 page] "Mamba (part 2): parallel scan and
+// hardware-aware optimisation" (scwacadex.pages.dev, blog8_mamba_parallel_scan)
+// §4.3 on chunked recomputation, §7 on the constant-time step.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "ssm_delta_kernel.h"
+#include "ssm_device.h"
+#include "ssm_kernels.h"
+
+namespace ssm {
+namespace {
+
+using namespace dev;
+using deltak::DeltaDev;
+using deltak::DeltaGradDev;
+
+constexpr int64_t kDeltaSlots = 512;     // workgroups that a split length is to give
+constexpr int64_t kDeltaMinSegment = 8;  // chunks
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+bool wide_for(int64_t cols, bool vec) { return cols > 64 && vec; }
+int64_t tiles_for(int64_t cols, bool vec) { return cdiv(cols, wide_for(cols, vec) ? 128 : 64); }
+
+// States carried over the segments, in order, 16 columns a workgroup: state <- A carried + own, or A^T carried + own
+// from the end.  Float32 matrix instructions; the carried columns are in LDS.
+__global__ void __launch_bounds__(256) ssm_delta_carry_kernel(float* state, const float* trans, int64_t nseg, int rp, int cp,
+                                                              int rev) {
+  __shared__ float carried[256][17];
+  const int64_t bh = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15, wave = tid >> 6;
+  const int c = blockIdx.x * 16 + li, tiles = rp / 16;
+  const int64_t ws = static_cast<int64_t>(rp) * cp, ts = static_cast<int64_t>(rp) * rp;
+  float* const s = state + bh * nseg * ws;
+  const float* const m = trans + bh * nseg * ts;
+  const int64_t first = rev ? nseg - 1 : 0, step = rev ? -1 : 1;
+  for (int r = tid / 16; r < rp; r += 16) carried[r][tid % 16] = s[first * ws + static_cast<int64_t>(r) * cp + blockIdx.x * 16 + tid % 16];
+  __syncthreads();
+  for (int64_t i = 1; i < nseg - 1; ++i) {
+    const int64_t at = first + i * step;
+    const float* const a = m + at * ts;
+    float* const own = s + at * ws;
+    headk::f32x4 acc[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int rt = wave + 4 * t;
+      if (rt >= tiles) continue;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[t][v] = own[static_cast<int64_t>(16 * rt + 4 * g + v) * cp + c];
+    }
+    for (int k0 = 0; k0 < rp; k0 += 16) {
+      const float4 x = make_float4(carried[k0 + 4 * g][li], carried[k0 + 4 * g + 1][li], carried[k0 + 4 * g + 2][li],
+                                   carried[k0 + 4 * g + 3][li]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int rt = wave + 4 * t;
+        if (rt >= tiles) continue;
+        const int r = 16 * rt + li, k = k0 + 4 * g;
+        float4 f;
+        if (rev) f = make_float4(a[k * rp + r], a[(k + 1) * rp + r], a[(k + 2) * rp + r], a[(k + 3) * rp + r]);
+        else f = *reinterpret_cast<const float4*>(a + r * rp + k);
+        acc[t] = headk::mma<F32>(__builtin_bit_cast(uint4, f), __builtin_bit_cast(uint4, x), acc[t]);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int rt = wave + 4 * t;
+      if (rt >= tiles) continue;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int r = 16 * rt + 4 * g + v;
+        carried[r][li] = acc[t][v];
+        own[static_cast<int64_t>(r) * cp + c] = acc[t][v];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// One token.  A workgroup owns one (batch row, head) and 32 columns of the
+// state: thread (rg, c) takes rows rg + 32 i, columns 4 c .. 4 c + 3.  With
+// S~ = e^g S, both S~^T k and S~^T q come from one pass over the state's
+// registers, with q . k: o = scale (S~^T q + (q . k) u), u = b (v - S~^T k), so
+// that one exchange between the wavefronts serves both.  Every load is issued
+// before the first store (the update may be in place).
+struct DeltaStepDev {
+  const char* q;
+  const char* k;
+  const char* v;
+  const char* g;
+  const char* beta;
+  const float* in;
+  float* out;
+  char* o;
+  int64_t H, Hk, dk, dv, ntile;
+  float scale;
+};
+
+template <typename IO, int ROWS, bool VEC>
+__global__ void __launch_bounds__(256) ssm_delta_step_kernel(DeltaStepDev p) {
+  using T = typename IO::T;
+  constexpr int N = ROWS / 32;  // rows per thread
+  __shared__ float sh[4][2][32], shq[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t ct = blockIdx.x % p.ntile, bh = blockIdx.x / p.ntile, b = bh / p.H, h = bh % p.H;
+  const int64_t c = ct * 32 + 4 * (tid & 7);
+  const int rg = tid >> 3;
+  const T* q = reinterpret_cast<const T*>(p.q) + (b * p.Hk + h / (p.H / p.Hk)) * p.dk;
+  const T* k = reinterpret_cast<const T*>(p.k) + (b * p.Hk + h / (p.H / p.Hk)) * p.dk;
+  const T* v = reinterpret_cast<const T*>(p.v) + bh * p.dv;
+  float s[N][4], kk[N], qq[N], vv[4];
+  const int64_t base = bh * p.dk * p.dv + c;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t r = rg + 32 * i;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+    kk[i] = qq[i] = 0.f;
+    if (r < p.dk) {
+      if constexpr (VEC) {
+        if (c < p.dv) {
+          const headk::f32x4 x = __builtin_nontemporal_load(reinterpret_cast<const headk::f32x4*>(p.in + base + r * p.dv));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][e] = x[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < p.dv) s[i][e] = p.in[base + r * p.dv + e];
+      }
+      IO::template ld<1>(k + r, &kk[i]);
+      IO::template ld<1>(q + r, &qq[i]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    vv[e] = 0.f;
+    if (c + e < p.dv) IO::template ld<1>(v + c + e, &vv[e]);
+  }
+  float a = 0.f, bt = 1.f;
+  if (p.g != nullptr) IO::template ld<1>(reinterpret_cast<const T*>(p.g) + bh, &a);
+  if (p.beta != nullptr) IO::template ld<1>(reinterpret_cast<const T*>(p.beta) + bh, &bt);
+  a = __builtin_amdgcn_exp2f(headk::clamp_decay(a * kLog2e));
+  float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f}, qk = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    qk = __builtin_fmaf(qq[i], kk[i], qk);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s[i][e] = headk::times(a, s[i][e]);  // what is forgotten may not be finite
+      pk[e] = __builtin_fmaf(kk[i], s[i][e], pk[e]);
+      pq[e] = __builtin_fmaf(qq[i], s[i][e], pq[e]);
+    }
+  }
+  // over the wavefront's 8 row groups, then over the wavefronts
+#pragma unroll
+  for (int d = 8; d < 64; d *= 2) {
+    qk += __shfl_xor(qk, d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      pk[e] += __shfl_xor(pk[e], d);
+      pq[e] += __shfl_xor(pq[e], d);
+    }
+  }
+  if (lane < 8) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sh[wave][0][4 * lane + e] = pk[e];
+      sh[wave][1][4 * lane + e] = pq[e];
+    }
+    if (lane == 0) shq[wave] = qk;
+  }
+  __syncthreads();
+  float u[4], y[4];
+  qk = (shq[0] + shq[1]) + (shq[2] + shq[3]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int x = 4 * (tid & 7) + e;
+    u[e] = bt * (vv[e] - ((sh[0][0][x] + sh[1][0][x]) + (sh[2][0][x] + sh[3][0][x])));
+    y[e] = p.scale * __builtin_fmaf(qk, u[e], (sh[0][1][x] + sh[1][1][x]) + (sh[2][1][x] + sh[3][1][x]));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t r = rg + 32 * i;
+    if (r < p.dk) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] = __builtin_fmaf(kk[i], u[e], s[i][e]);
+      if constexpr (VEC) {
+        if (c < p.dv) {
+          const headk::f32x4 x = {s[i][0], s[i][1], s[i][2], s[i][3]};
+          __builtin_nontemporal_store(x, reinterpret_cast<headk::f32x4*>(p.out + base + r * p.dv));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < p.dv) p.out[base + r * p.dv + e] = s[i][e];
+      }
+    }
+  }
+  if (rg == 0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < p.dv) IO::template st<1>(reinterpret_cast<T*>(p.o) + bh * p.dv + c + e, &y[e]);
+  }
+}
+
+struct Plan {
+  int64_t C, nch, cps, nseg, rp, cp;
+};
+Plan plan_of(const DeltaArgs& a, bool bf16) {
+  Plan p;
+  p.C = bf16 ? headk::HeadCfg<BF16>::C : headk::HeadCfg<F32>::C;
+  p.nch = cdiv(a.L, p.C);
+  p.rp = up(a.dk, 16);
+  p.cp = up(a.dv, deltak::kSlab);
+  const int64_t wgs = a.batch * a.H * tiles_for(a.dv, true);
+  int64_t want = std::min(kDeltaSlots / wgs, p.nch / kDeltaMinSegment);
+  if (want < 3) want = 1;  // a split costs a walk of its own, twice as wide
+  p.cps = cdiv(p.nch, want);
+  p.nseg = cdiv(p.nch, p.cps);
+  return p;
+}
+
+// Every row of every operand is whole, aligned 16-byte vectors.
+bool vec16(const void* p, int64_t b, int64_t t, int64_t es) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && b * es % 16 == 0 && t * es % 16 == 0;
+}
+bool all_vec(const DeltaArgs& a, bool bf16) {
+  const int64_t es = bf16 ? 2 : 4;
+  return a.dk * es % 16 == 0 && a.dv * es % 16 == 0 && vec16(a.q, a.q_b, a.q_t, es) && vec16(a.k, a.k_b, a.k_t, es) &&
+         vec16(a.v, a.v_b, a.v_t, es);
+}
+
+int64_t m_bytes(const DeltaArgs& a, const Plan& pl, bool bf16) {
+  return a.batch * a.H * pl.nch * pl.C * pl.C * 4;  // two parts of 2 bytes, or one of 4
+}
+
+// Heads whose parts of dq and dk a workgroup adds: all that share a key head, unless that leaves CUs idle.
+int64_t grad_heads(const DeltaArgs& a, const Plan& pl) {
+  const int64_t rep = a.H / a.Hk;
+  int64_t n = rep;
+  while (n > 1 && a.batch * (a.H / n) * pl.nch < kDeltaSlots) {
+    --n;
+    while (rep % n != 0) --n;
+  }
+  return n;
+}
+
+// Where the workspace's parts are, in bytes from its start.
+struct Space {
+  int64_t m, ss, rs, trans, s0, r1, r, e, pq, pk, total;
+};
+Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
+  Space w{};
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t r = at;
+    at += up(bytes, 16);
+    return r;
+  };
+  const int64_t bh = a.batch * a.H;
+  w.m = take(m_bytes(a, pl, bf16));
+  if (pl.nseg > 1) {
+    w.ss = take(4 * bh * pl.nseg * pl.rp * pl.cp);
+    w.trans = take(4 * bh * pl.nseg * pl.rp * pl.rp);
+    if (backward) w.rs = take(4 * bh * pl.nseg * pl.rp * pl.cp);
+  }
+  if (backward) {
+    w.s0 = take(4 * bh * pl.nch * pl.rp * pl.cp);
+    w.r1 = take(4 * bh * pl.nch * pl.rp * pl.cp);
+    w.r = take(4 * bh * pl.nch * pl.C * pl.cp);
+    w.e = take(4 * bh * pl.nch * pl.C * pl.cp);
+    const int64_t hn = grad_heads(a, pl);
+    if (hn < a.H / a.Hk) {
+      w.pq = take(4 * bh / hn * a.L * a.dk);
+      w.pk = take(4 * bh / hn * a.L * a.dk);
+    }
+  }
+  w.total = at;
+  return w;
+}
+
+DeltaDev dev_of(const DeltaArgs& a, const Plan& pl, const Space& w, char* work, bool bf16, bool vec) {
+  const int64_t es = bf16 ? 2 : 4;
+  DeltaDev d{};
+  d.q = static_cast<const char*>(a.q); d.k = static_cast<const char*>(a.k); d.v = static_cast<const char*>(a.v);
+  d.o = static_cast<char*>(a.o);
+  d.q_b = a.q_b * es; d.k_b = a.k_b * es; d.v_b = a.v_b * es;
+  d.q_t = static_cast<uint32_t>(a.q_t * es); d.k_t = static_cast<uint32_t>(a.k_t * es); d.v_t = static_cast<uint32_t>(a.v_t * es);
+  d.rep = static_cast<int>(a.H / a.Hk);
+  d.g = static_cast<const char*>(a.g); d.beta = static_cast<const char*>(a.beta); d.lengths = a.lengths;
+  d.h0 = a.h0; d.last = a.last;
+  d.m = work + w.m;
+  d.seg_state = reinterpret_cast<float*>(work + w.ss);
+  d.seg_trans = reinterpret_cast<float*>(work + w.trans);
+  d.states = reinterpret_cast<float*>(work + w.s0);
+  d.res = reinterpret_cast<float*>(work + w.r);
+  d.batch = static_cast<int>(a.batch); d.H = static_cast<int>(a.H); d.L = static_cast<int>(a.L);
+  d.rows = static_cast<int>(a.dk); d.cols = static_cast<int>(a.dv);
+  d.rp = static_cast<int>(pl.rp); d.cp = static_cast<int>(pl.cp);
+  d.nch = static_cast<int>(pl.nch); d.cps = static_cast<int>(pl.cps); d.nseg = static_cast<int>(pl.nseg);
+  d.nvt = d.ntile = static_cast<int>(tiles_for(a.dv, vec));
+  d.scale = a.scale;
+  return d;
+}
+
+hipError_t launch_pass(const DeltaDev& d, bool bf16, int pass, bool vec, hipStream_t st) {
+  const bool wide = wide_for(d.cols, vec);
+  return bf16 ? launch_delta_bf16(d, pass, wide, vec, st) : launch_delta_f32(d, pass, wide, vec, st);
+}
+
+hipError_t launch_carry(const DeltaDev& d, int rev, hipStream_t st) {
+  if (d.nseg <= 2) return hipSuccess;
+  hipLaunchKernelGGL(ssm_delta_carry_kernel, dim3(static_cast<unsigned>(d.cp / 16), static_cast<unsigned>(d.batch * d.H)),
+                     dim3(256), 0, st, d.seg_state, d.seg_trans, static_cast<int64_t>(d.nseg), d.rp, d.cp, rev);
+  return hipGetLastError();
+}
+
+// M of all chunks, and the states at the segments' ends
+hipError_t launch_start(const DeltaDev& d, bool bf16, bool vec, hipStream_t st) {
+  hipError_t e = launch_pass(d, bf16, deltak::kPassPrep, vec, st);
+  if (e != hipSuccess || d.nseg == 1) return e;
+  DeltaDev s = d;
+  s.ntile = d.nvt + static_cast<int>(cdiv(d.rp, wide_for(d.cols, vec) ? 128 : 64));
+  e = launch_pass(s, bf16, deltak::kPassSeg, vec, st);
+  return e == hipSuccess ? launch_carry(d, 0, st) : e;
+}
+
+}  // namespace
+
+int64_t delta_workspace_bytes(const DeltaArgs& a, bool bf16, bool backward) {
+  return space_of(a, plan_of(a, bf16), bf16, backward).total;
+}
+
+int64_t delta_workgroups(const DeltaArgs& a, bool bf16, bool backward) {
+  const Plan pl = plan_of(a, bf16);
+  const int64_t bh = a.batch * a.H, tiles = cdiv(a.dv, 64) + cdiv(pl.rp, 64);
+  return std::max(2 * bh * pl.nch, 2 * bh * tiles * pl.nseg);  // the larger workgroups have 512 threads
+}
+
+hipError_t launch_delta_fwd(const DeltaArgs& a, bool bf16, char* work, hipStream_t st) {
+  const Plan pl = plan_of(a, bf16);
+  const bool vec = all_vec(a, bf16);
+  const DeltaDev d = dev_of(a, pl, space_of(a, pl, bf16, false), work, bf16, vec);
+  const hipError_t e = launch_start(d, bf16, vec, st);
+  return e == hipSuccess ? launch_pass(d, bf16, deltak::kPassOut, vec, st) : e;
+}
+
+hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream_t st) {
+  const Plan pl = plan_of(a, bf16);
+  const bool vec = all_vec(a, bf16);
+  const Space w = space_of(a, pl, bf16, true);
+  const int64_t es = bf16 ? 2 : 4;
+  DeltaDev d = dev_of(a, pl, w, work, bf16, vec);
+  d.last = nullptr;
+  hipError_t e = launch_start(d, bf16, vec, st);
+  if (e == hipSuccess) e = launch_pass(d, bf16, deltak::kPassStates, vec, st);
+  if (e != hipSuccess) return e;
+
+  DeltaDev r = d;
+  r.v = static_cast<const char*>(a.dout);
+  r.v_b = a.L * a.H * a.dv * es;
+  r.v_t = static_cast<uint32_t>(a.H * a.dv * es);
+  r.h0 = a.dlast;
+  r.last = a.dh0;
+  r.seg_state = reinterpret_cast<float*>(work + w.rs);
+  r.states = reinterpret_cast<float*>(work + w.r1);
+  r.res = reinterpret_cast<float*>(work + w.e);
+  if (pl.nseg > 1) {
+    e = launch_pass(r, bf16, deltak::kPassRevSeg, vec, st);
+    if (e == hipSuccess) e = launch_carry(r, 1, st);
+    if (e != hipSuccess) return e;
+  }
+  e = launch_pass(r, bf16, deltak::kPassRev, vec, st);
+  if (e != hipSuccess) return e;
+
+  const int64_t rep = a.H / a.Hk, hn = grad_heads(a, pl);
+  DeltaGradDev gd{};
+  gd.f = d;
+  gd.f.v = r.v; gd.f.v_b = r.v_b; gd.f.v_t = r.v_t;
+  gd.r1 = r.states; gd.e = r.res;
+  gd.hn = static_cast<int>(hn);
+  gd.parts = hn < rep;
+  gd.dq = gd.parts ? work + w.pq : static_cast<char*>(a.dq);
+  gd.dk = gd.parts ? work + w.pk : static_cast<char*>(a.dk_out);
+  gd.dv = static_cast<char*>(a.dv_out);
+  gd.dg = static_cast<char*>(a.dg);
+  gd.db = static_cast<char*>(a.dbeta);
+  e = bf16 ? launch_delta_grad_bf16(gd, vec, st) : launch_delta_grad_f32(gd, vec, st);
+  if (e != hipSuccess || !gd.parts) return e;
+  e = launch_head_group_sum(reinterpret_cast<const float*>(gd.dq), a.dq, a, hn, bf16, st);
+  return e == hipSuccess ? launch_head_group_sum(reinterpret_cast<const float*>(gd.dk), a.dk_out, a, hn, bf16, st) : e;
+}
+
+namespace {
+
+template <typename IO, bool VEC>
+auto step_kernel(int64_t dk) {
+  return dk <= 64 ? ssm_delta_step_kernel<IO, 64, VEC> : dk <= 128 ? ssm_delta_step_kernel<IO, 128, VEC>
+                                                                   : ssm_delta_step_kernel<IO, 256, VEC>;
+}
+
+}  // namespace
+
+hipError_t launch_delta_step(const DeltaStepArgs& a, bool bf16, hipStream_t st) {
+  DeltaStepDev d{};
+  d.q = static_cast<const char*>(a.q); d.k = static_cast<const char*>(a.k); d.v = static_cast<const char*>(a.v);
+  d.g = static_cast<const char*>(a.g); d.beta = static_cast<const char*>(a.beta);
+  d.in = a.state_in; d.out = a.state_out; d.o = static_cast<char*>(a.o);
+  d.H = a.H; d.Hk = a.Hk; d.dk = a.dk; d.dv = a.dv; d.ntile = cdiv(a.dv, 32); d.scale = a.scale;
+  const bool vec = a.dv % 4 == 0;
+  auto kern = bf16 ? (vec ? step_kernel<BF16, true>(a.dk) : step_kernel<BF16, false>(a.dk))
+                   : (vec ? step_kernel<F32, true>(a.dk) : step_kernel<F32, false>(a.dk));
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(a.batch * a.H * d.ntile)), dim3(256), 0, st, d);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

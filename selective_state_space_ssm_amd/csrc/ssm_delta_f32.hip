@@ -1,0 +1,10 @@
+// The delta scan's walks over the length for float32 storage.
+#include "ssm_delta_kernel.h"
+
+namespace ssm {
+
+hipError_t launch_delta_f32(const deltak::DeltaDev& p, int pass, bool wide, bool vec, hipStream_t st) {
+  return deltak::launch_pass_io<dev::F32>(p, pass, wide, vec, st);
+}
+
+}  // namespace ssm

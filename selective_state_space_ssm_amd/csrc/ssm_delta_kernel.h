@@ -1,0 +1,1472 @@
+// The delta scan's chunk kernels: a linear recurrence with one decay per head
+// and a matrix state that first takes out what it holds under the key, computed
+// chunk by chunk on the matrix cores (gfx950).
+//
+//   S~_t = e^{g_t} S_{t-1},  r_t = v_t - S~_t^T k_t,  S_t = S~_t + b_t k_t r_t^T
+//   o_t = scale S_t^T q_t                          S [rows = d_key][cols = d_value]
+//
+// For a chunk of C tokens with the running decay G_i, the state S_0 before it,
+// D_ij = e^{G_i - G_j}, N = the part of (D . K K^T) below the diagonal and
+// P = scale (D . Q K^T) on and below it:
+//
+//   x = V - e^G (K S_0),   r = x - M (b x),   M = N (I + diag(b) N)^-1
+//   o = scale e^G (Q S_0) + P (b r)
+//   S_C = e^{G_C} S_0 + K^T (e^{G_C - G} b r)
+//
+// Backwards, with R_C = dLoss/dS_C and e_t = R_t^T k_t (so that dv = b e):
+//
+//   y = P^T dO + e^{G_C - G} (K R_C),   e = y - M^T (b y)
+//   R_0 = e^{G_C} R_C + Q^T (scale e^G dO) - K^T (e^G b e)
+//
+// M needs neither the state nor b on its outside (b = 0 divides nothing) and is
+// the same in both directions: ssm_delta_prep_kernel makes it for all chunks at
+// once, and what is left of a chunk in the walk over the length is products.
+// With S_0 and R_C of every chunk kept, and r and e, the other gradients are
+// again all chunks at once (ssm_delta_grad_kernel):
+//
+//   dP = dO (b r)^T,  dN = -(b e)(b r)^T, each times D below the diagonal
+//   dq = scale e^G (dO S_0^T) + dP K
+//   dk = e^{G_C - G} (b r) R_C^T + dP^T Q + dN^T K - e^G (b e) S_0^T + dN K
+//   db = e . r,   dg: see there
+//
+// The kernels' tiles, swizzles and operand layouts are those of the head scan's
+// chunk kernel: a wavefront owns 16 columns of the state and all rows, in
+// accumulators, and an accumulator tile is an operand contracted over its rows
+// as it stands (state_row), so that x, r and the state pass from product to
+// product without leaving the wavefront.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "ssm_device.h"
+#include "ssm_head_kernel.h"
+#include "ssm_kernels.h"
+
+namespace ssm {
+namespace deltak {
+
+using namespace headk;
+
+constexpr int kSlab = 64;  // columns of d_value that the gradient kernel takes at a time; padded widths go by it
+
+struct DeltaDev {
+  const char* q;
+  const char* k;
+  const char* v;               // backwards dO
+  char* o;
+  int64_t q_b, k_b, v_b;       // byte strides of batch rows
+  uint32_t q_t, k_t, v_t;      // byte strides of tokens
+  int rep;                     // head h reads head h / rep of q and k
+  const char* g;               // [b][L][H], nullable
+  const char* beta;            // [b][L][H], nullable (ones)
+  const int32_t* lengths;      // [b], nullable
+  const float* h0;             // state at the first token (backwards: after the last), nullable
+  float* last;                 // state after the last token (backwards: at the first), nullable
+  char* m;                     // -M of every chunk, [b][H][nch][parts][C][C]
+  float* seg_state;            // [b][H][nseg][rp][cp]
+  float* seg_trans;            // [b][H][nseg][rp][rp]: what a segment makes of the state before it
+  float* states;               // [b][H][nch][rp][cp]: the state before (backwards: after) every chunk
+  float* res;                  // [b][H][nch][C][cp]: r, backwards e
+  int batch, H, L, rows, cols;
+  int rp, cp;                  // rows and columns of states in the workspace: multiples of 16 and of kSlab
+  int nch, cps, nseg;          // chunks, chunks per segment, segments
+  int ntile, nvt;              // column tiles, those of the state (the others: of the transition)
+  float scale;
+};
+
+// Parts that a float32 value enters a product in (bfloat16 storage): the state
+// and what is added to it in three, which is exact to float32; the corrections
+// M (b x), whose operands are both such values, and all that ends in a bfloat16
+// result in two (2^-17 of themselves).
+template <typename IO>
+struct DeltaCfg {
+  static constexpr int STATE = HeadCfg<IO>::ES == 2 ? 3 : 1;
+  static constexpr int PAIR = HeadCfg<IO>::ES == 2 ? 2 : 1;
+};
+
+// E values (one operand register of a lane) as N parts
+template <typename IO, int N>
+__device__ __forceinline__ void split(float* v, uint4* out) {
+  if constexpr (HeadCfg<IO>::ES == 2) {
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = v[e];
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = take_bf16(w);
+  } else {
+    static_assert(N == 1, "float32 is one part");
+    out[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+}
+// storage values of one operand register as float32
+template <typename IO>
+__device__ __forceinline__ void unpack(const uint4& r, float* v) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+  for (int e = 0; e < HeadCfg<IO>::E; ++e) {
+    if constexpr (HeadCfg<IO>::ES == 2) v[e] = e & 1 ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
+    else v[e] = __uint_as_float(w[e]);
+  }
+}
+
+// The row that is row li of accumulator tile rt (state_row), k = KS s + E g ..
+template <typename IO, int N>
+__device__ __forceinline__ int state_row_base(int li, int g) {
+  return HeadCfg<IO>::ES == 2 ? lane_base<IO, N>(8 * (li >> 2) + (li & 3), g) : lane_base<IO, N>(li, g);
+}
+template <typename IO, int N>
+__device__ __forceinline__ uint4 frag_state_row(const char* tile, int base, int rt, int s) {
+  if constexpr (HeadCfg<IO>::ES == 2) {
+    const int up = rt & 1;
+    return *reinterpret_cast<const uint4*>(tile + ((base ^ (64 * s) ^ (up ? 16 * swz<IO, N>(4) : 0)) +
+                                                   16 * N * (32 * (rt >> 1) + 4 * up)));
+  } else {
+    return frag_row<N>(tile, base, rt, s);
+  }
+}
+
+// Accumulator tile and register of value e of operand step s
+template <typename IO>
+__device__ __forceinline__ constexpr int tile_of(int s, int e) { return s * (HeadCfg<IO>::E / 4) + (e >> 2); }
+
+// 16 bytes at byte offset off of a row bounded by the resource; `left` values of the row remain there
+template <typename IO, bool VEC>
+__device__ __forceinline__ uint4 load16(Rsrc r, uint32_t off, int left) {
+  constexpr int E = HeadCfg<IO>::E, ES = HeadCfg<IO>::ES;
+  if constexpr (VEC) {
+    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, left > 0 ? off : kOOB, 0, 0);
+    return make_uint4(v.x, v.y, v.z, v.w);
+  } else {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const uint32_t oe = e < left ? off + e * ES : kOOB;
+      if constexpr (ES == 4) {
+        w[e] = __builtin_amdgcn_raw_buffer_load_b32(r, oe, 0, 0);
+      } else {
+        const uint32_t hv = __builtin_amdgcn_raw_buffer_load_b16(r, oe, 0, 0);
+        w[e >> 1] |= (e & 1) ? (hv << 16) : hv;
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// A tile of C tokens, N chunks of 16 bytes each, dealt to T threads: thread t
+// has chunk t % N of rows t / N + i T / N.
+template <typename IO, int N, int T>
+struct Tile {
+  static constexpr int C = HeadCfg<IO>::C, CNT = (C * N + T - 1) / T, STEP = T / N;
+  template <bool VEC>
+  static __device__ __forceinline__ void load(const char* base, uint32_t ts, int t0, int len, int width, int tid, uint4* reg) {
+    const int row = tid / N, c = tid % N;
+    const int left = C * N % T == 0 || row < C ? width - c * HeadCfg<IO>::E : 0;
+    const uint32_t off = row * ts + c * 16;
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) {
+      const int r0 = STEP * i;
+      const Rsrc r = make_rsrc(base + static_cast<int64_t>(t0 + r0) * ts, row_bytes(len - t0 - r0, C, ts));
+      reg[i] = load16<IO, VEC>(r, off, left);
+    }
+  }
+  static __device__ __forceinline__ void store(char* tile, int tid, const uint4* reg) {
+    const int row = tid / N, c = tid % N;
+    if (C * N % T != 0 && row >= C) return;
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) {
+      const int r = row + STEP * i;
+      *reinterpret_cast<uint4*>(tile + 16 * (N * r + (c ^ swz<IO, N>(r)))) = reg[i];
+    }
+  }
+};
+
+// A chunk's decays and b, one token a lane of one wavefront: asked for, then scanned and written
+// to LDS.  A token past the length has neither decay nor b.
+template <typename IO>
+struct Rates {
+  static constexpr int C = HeadCfg<IO>::C, ES = HeadCfg<IO>::ES;
+  uint32_t raw_g = 0, raw_b = 0;
+  static __device__ __forceinline__ uint32_t one(const char* p, const DeltaDev& d, int b, int h, int t0, int len, int lane) {
+    const uint32_t ts = d.H * ES;
+    const Rsrc r = make_rsrc(p + ((static_cast<int64_t>(b) * d.L + t0) * d.H + h) * ES, row_bytes(len - t0, C, ts));
+    const uint32_t off = lane < C ? lane * ts : kOOB;
+    if constexpr (ES == 2) return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    else return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+  }
+  __device__ __forceinline__ void load(const DeltaDev& d, int b, int h, int t0, int len, int lane) {
+    if (d.g != nullptr) raw_g = one(d.g, d, b, h, t0, len, lane);
+    if (d.beta != nullptr) raw_b = one(d.beta, d, b, h, t0, len, lane);
+  }
+  static __device__ __forceinline__ float value(uint32_t raw) { return __uint_as_float(ES == 2 ? raw << 16 : raw); }
+  // G as a pair of floats (log2 units), lanes past C hold the chunk's sum
+  __device__ __forceinline__ void scan(float& hi, float& lo) const {
+    hi = clamp_decay(value(raw_g) * kLog2e);
+    scan_pair(hi, lo);
+  }
+  __device__ __forceinline__ float beta(const DeltaDev& d, int t0, int len, int lane) const {
+    return d.beta != nullptr ? value(raw_b) : (t0 + lane < len ? 1.f : 0.f);
+  }
+};
+
+__device__ __forceinline__ int length_of(const DeltaDev& p, int b) {
+  if (p.lengths == nullptr) return p.L;
+  const int n = p.lengths[b];
+  return n < 0 ? 0 : (n < p.L ? n : p.L);
+}
+
+// ---------------------------------------------------------------- M of every chunk
+
+template <typename IO, int ROWS>
+constexpr size_t prep_lds_bytes() {
+  using K = HeadCfg<IO>;
+  return size_t(K::C) * ROWS * K::ES + size_t(K::C) * (K::C + 4) * 4 + size_t(K::C / 16) * 16 * 20 * 4 + 3 * K::C * 4;
+}
+
+// One (batch row, head, chunk) a workgroup of four wavefronts.  N on the matrix
+// cores; the 16 x 16 blocks on the diagonal of I + N diag(b) inverted by
+// substitution, a column a lane; then, a block column a wavefront, by block rows
+//   M_IK = (I + N_II b_I)^-1 (N_IK - sum_{K <= J < I} N_IJ b_J M_JK)
+// in float32 matrix instructions, the tiles M_JK staying in registers.
+// (Substitution, not powers of N b: keys alike make those grow past float32
+// where the inverse does not.)
+template <typename IO, int ROWS, bool VEC>
+__global__ void __launch_bounds__(256) ssm_delta_prep_kernel(const DeltaDev p) {
+  using K = HeadCfg<IO>;
+  constexpr int ES = K::ES, E = K::E, C = K::C, T = 256, IB = C / 16, NK = ROWS * ES / 16, RS = ROWS / K::KS;
+  constexpr int LD = C + 4;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char* const ty = lds;
+  float* const n = reinterpret_cast<float*>(ty + C * ROWS * ES);  // [C][LD]
+  float* const inv = n + C * LD;                                  // [IB][16][20]
+  float* const ghi = inv + IB * 16 * 20;
+  float* const glo = ghi + C;
+  float* const bt = glo + C;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pc = blockIdx.x % p.nch, bh = blockIdx.x / p.nch, h = bh % p.H, b = bh / p.H, t0 = pc * C;
+  const int len = length_of(p, b);
+  if (t0 >= len) return;
+
+  uint4 ry[Tile<IO, NK, T>::CNT];
+  Rates<IO> rates;
+  if (wave == 3) rates.load(p, b, h, t0, len, lane);
+  Tile<IO, NK, T>::template load<VEC>(p.k + b * p.k_b + static_cast<int64_t>(h / p.rep) * p.rows * ES, p.k_t, t0, len, p.rows,
+                                      tid, ry);
+  if (wave == 3) {
+    float hi, lo;
+    rates.scan(hi, lo);
+    if (lane < C) {
+      ghi[lane] = hi;
+      glo[lane] = lo;
+      bt[lane] = rates.beta(p, t0, len, lane);
+    }
+  }
+  Tile<IO, NK, T>::store(ty, tid, ry);
+  __syncthreads();
+
+  const int rb = lane_base<IO, NK>(li, g);
+  for (int tile = wave; tile < IB * (IB + 1) / 2; tile += 4) {
+    const int ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6), jb = tile - ib * (ib + 1) / 2;
+    const int i = 16 * ib + li, j0 = 16 * jb + 4 * g;
+    f32x4 a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < RS; ++s) a = mma<IO>(frag_row<NK>(ty, rb, jb, s), frag_row<NK>(ty, rb, ib, s), a);
+    const float gi = ghi[i], gl = glo[i];
+    float4 w;
+    float* pw = reinterpret_cast<float*>(&w);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const float d = __builtin_amdgcn_exp2f((gi - ghi[j0 + v]) + (gl - glo[j0 + v]));
+      pw[v] = j0 + v < i ? times(d, a[v]) : 0.f;
+    }
+    *reinterpret_cast<float4*>(n + i * LD + j0) = w;
+  }
+  __syncthreads();
+
+  if (wave < IB) {
+    // column li of the inverse; the four lane groups work alike and write four rows each
+    float t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s = i == li ? 1.f : 0.f;
+#pragma unroll
+      for (int k = 0; k < i; ++k) s = __builtin_fmaf(-n[(16 * wave + i) * LD + 16 * wave + k] * bt[16 * wave + k], t[k], s);
+      t[i] = s;
+      if ((i >> 2) == g) inv[(wave * 16 + i) * 20 + li] = s;
+    }
+  }
+  __syncthreads();
+
+  f32x4 M[IB];
+  if (wave < IB) {
+#pragma unroll
+    for (int I = 0; I < IB; ++I) {
+      M[I] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (I < wave) continue;
+      f32x4 a;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) a[v] = n[(16 * I + 4 * g + v) * LD + 16 * wave + li];
+#pragma unroll
+      for (int J = 0; J < I; ++J) {
+        if (J < wave) continue;
+        const float4 nn = *reinterpret_cast<const float4*>(n + (16 * I + li) * LD + 16 * J + 4 * g);
+        const float4 bb = *reinterpret_cast<const float4*>(bt + 16 * J + 4 * g);
+        const float4 f = make_float4(-nn.x * bb.x, -nn.y * bb.y, -nn.z * bb.z, -nn.w * bb.w);
+        a = mma<F32>(__builtin_bit_cast(uint4, f), __builtin_bit_cast(uint4, M[J]), a);
+      }
+      const float4 f = *reinterpret_cast<const float4*>(inv + (I * 16 + li) * 20 + 4 * g);
+      M[I] = mma<F32>(__builtin_bit_cast(uint4, f), __builtin_bit_cast(uint4, a), M[I]);
+    }
+  }
+  __syncthreads();
+  if (wave < IB) {
+#pragma unroll
+    for (int I = 0; I < IB; ++I)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) n[(16 * I + 4 * g + v) * LD + 16 * wave + li] = -M[I][v];
+  }
+  __syncthreads();
+  constexpr int PARTS = DeltaCfg<IO>::PAIR;
+  char* const dst = p.m + (static_cast<int64_t>(bh) * p.nch + pc) * (PARTS * C * C * ES);
+  for (int i = tid; i < C * C / E; i += T) {
+    const int r = i / (C / E), c = i % (C / E) * E;
+    float v[E];
+    F32::ld<E>(n + r * LD + c, v);
+    uint4 w[PARTS];
+    split<IO, PARTS>(v, w);
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) *reinterpret_cast<uint4*>(dst + q * C * C * ES + 16 * i) = w[q];
+  }
+}
+
+// ---------------------------------------------------------------- the walk over the length, forwards
+
+// kOut writes o (and the last state); kSeg a segment's own end state (from zero,
+// or from the start state for the first segment) and, in the tiles past nvt, what
+// it makes of the state before it (the walk from the identity without v); kStates
+// the state before every chunk and r.
+constexpr int kDeltaOut = 0, kDeltaSeg = 1, kDeltaStates = 2;
+
+template <typename IO, int ROWS, int NW, bool QUERY>
+constexpr size_t delta_lds_bytes() {
+  using K = HeadCfg<IO>;
+  constexpr size_t xy = size_t(K::C) * ROWS * K::ES, z = size_t(K::C) * 16 * NW * K::ES;
+  constexpr size_t sq = size_t(K::C) * K::C * K::ES * DeltaCfg<IO>::PAIR;
+  return xy + z + sq + 6 * K::C * 4 + (QUERY ? xy + sq : 0);
+}
+
+// Workgroups are dealt to the XCDs as the head scan's: the column tiles of a (batch row, head, segment) follow each
+// other on one XCD.
+__device__ __forceinline__ void place(const DeltaDev& p, int nrun, int& ct, int& seg, int& h, int& b) {
+  const uint32_t pid = blockIdx.x, nt = p.ntile, whole = gridDim.x / nt / 8 * 8 * nt;
+  uint32_t idx = pid / nt;
+  ct = pid % nt;
+  if (pid < whole) {
+    const uint32_t slot = pid / 8;
+    idx = slot / nt * 8 + pid % 8;
+    ct = slot % nt;
+  }
+  seg = idx % nrun;
+  idx /= nrun;
+  h = idx % p.H;
+  b = idx / p.H;
+}
+
+template <typename IO, int RT>
+__device__ __forceinline__ void load_state(const float* src, int rows, int cols, int ld, int c, int g, f32x4 (&S)[RT]) {
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int r = state_row<IO>(rt, g, v);
+      S[rt][v] = src != nullptr && r < rows && c < cols ? src[r * ld + c] : 0.f;
+    }
+}
+template <typename IO, int RT>
+__device__ __forceinline__ void store_state(float* dst, int rows, int cols, int ld, int c, int g, const f32x4 (&S)[RT]) {
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int r = state_row<IO>(rt, g, v);
+      if (r < rows && c < cols) dst[r * ld + c] = S[rt][v];
+    }
+}
+// r or e of a chunk: rows of cp floats, all C of them
+template <typename IO, int TB>
+__device__ __forceinline__ void store_res(float* dst, int cp, int c, int g, const f32x4 (&X)[TB]) {
+  if (c >= cp) return;
+#pragma unroll
+  for (int rt = 0; rt < TB; ++rt)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) dst[state_row<IO>(rt, g, v) * cp + c] = X[rt][v];
+}
+
+template <typename IO, int ROWS, int NW, int MODE, bool VEC>
+__global__ void __launch_bounds__((64 * NW), (NW == 8 || ROWS == 256 ? 2 : 3))
+ssm_delta_kernel(const DeltaDev p) {
+  using K = HeadCfg<IO>;
+  constexpr bool QUERY = MODE == kDeltaOut;
+  constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
+  constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
+  constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
+  constexpr int PS = DeltaCfg<IO>::STATE, PP = DeltaCfg<IO>::PAIR;
+  constexpr int MB = PP * C * C * ES, LM = (MB / 16 + T - 1) / T;  // bytes of a chunk's M, 16-byte chunks a thread
+  using TK = Tile<IO, NK, T>;
+  using TZ = Tile<IO, NZ, T>;
+
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char* const ty = lds;
+  char* const tz = ty + C * ROWS * ES;
+  char* const tm = tz + C * COLS * ES;
+  float* const ghi = reinterpret_cast<float*>(tm + MB);
+  float* const glo = ghi + C;
+  float* const ek = glo + C;  // e^{G_i}
+  float* const we = ek + C;   // e^{G_C - G_i}
+  float* const bt = we + C;   // b
+  float* const eo = bt + C;   // scale e^{G_i}
+  char* const tx = reinterpret_cast<char*>(eo + C);
+  char* const tp = tx + C * ROWS * ES;
+
+  const int tid = static_cast<int>(threadIdx.x);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int ct, seg, h, b;
+  place(p, MODE == kDeltaSeg ? p.nseg - 1 : p.nseg, ct, seg, h, b);
+  const bool trans = MODE == kDeltaSeg && ct >= p.nvt;
+  if (trans) {
+    if (seg == 0) return;  // its state before is the start state
+    ct -= p.nvt;
+  }
+  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nch ? c0 + p.cps : p.nch;
+  const int len = length_of(p, b);
+  const int col0 = ct * COLS, cw = col0 + wave * 16;
+  const int64_t bh = static_cast<int64_t>(b) * p.H + h, wsize = static_cast<int64_t>(p.rp) * p.cp;
+
+  f32x4 S[RT];
+  {
+    const int g = (tid & 63) >> 4, c = cw + (tid & 15);
+    if (trans) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) S[rt][v] = state_row<IO>(rt, g, v) == c ? 1.f : 0.f;
+    } else if (seg == 0) {
+      load_state<IO, RT>(p.h0 != nullptr ? p.h0 + bh * p.rows * p.cols : nullptr, p.rows, p.cols, p.cols, c, g, S);
+    } else {
+      load_state<IO, RT>(MODE == kDeltaSeg ? nullptr : p.seg_state + (bh * p.nseg + seg - 1) * wsize, p.rp, p.cp, p.cp, c, g, S);
+    }
+  }
+  if constexpr (QUERY) {
+    // the score tiles above the diagonal that a product step covers are never written again
+    for (int i = tid; i < MB / 16; i += T) reinterpret_cast<uint4*>(tp)[i] = make_uint4(0, 0, 0, 0);
+  }
+
+  const char* const xb = p.q + b * p.q_b + static_cast<int64_t>(h / p.rep) * p.rows * ES;
+  const char* const yb = p.k + b * p.k_b + static_cast<int64_t>(h / p.rep) * p.rows * ES;
+  const char* const zb = p.v + b * p.v_b + (static_cast<int64_t>(h) * p.cols + col0) * ES;
+  const char* const mb = p.m + bh * p.nch * MB;
+
+  uint4 rx[TK::CNT], ry[TK::CNT], rz[TZ::CNT], rm[LM];
+  Rates<IO> rates;
+  auto load_chunk = [&](int pc) {
+    const int t0 = pc * C, me = opaque(tid);
+    rates.load(p, b, h, t0, len, me & 63);
+    TK::template load<VEC>(yb, p.k_t, t0, len, p.rows, me, ry);
+#pragma unroll
+    for (int i = 0; i < LM; ++i)
+      if (MB / 16 % T == 0 || me < MB / 16)
+        rm[i] = *reinterpret_cast<const uint4*>(mb + static_cast<int64_t>(pc) * MB + 16 * (me + i * T));
+    if (!trans) TZ::template load<VEC>(zb, p.v_t, t0, len, p.cols - col0, me, rz);
+    if constexpr (QUERY) TK::template load<VEC>(xb, p.q_t, t0, len, p.rows, me, rx);
+  };
+
+  const int cl = (len + C - 1) / C, ce = c1 < cl ? c1 : cl, nc = ce - c0;
+  if (nc > 0) load_chunk(c0);
+  for (int kk = 0; kk < nc; ++kk) {
+    const int pc = c0 + kk, t0 = pc * C;
+    __syncthreads();  // the chunk before is done with the tiles
+    {
+      const int me = opaque(tid);
+      TK::store(ty, me, ry);
+      if (!trans) TZ::store(tz, me, rz);
+      if constexpr (QUERY) TK::store(tx, me, rx);
+#pragma unroll
+      for (int i = 0; i < LM; ++i) {
+        const int at = me + i * T, r = at / NP;  // rows of both parts follow each other
+        if (MB / 16 % T == 0 || at < MB / 16) *reinterpret_cast<uint4*>(tm + 16 * (NP * r + (at % NP ^ swz<IO, NP>(r)))) = rm[i];
+      }
+    }
+    if (wave == NW - 1) {
+      float hi, lo;
+      rates.scan(hi, lo);
+      const float eh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hi), C - 1));
+      const float el = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lo), C - 1));
+      const int lane = tid & 63;
+      if (lane < C) {
+        const float e = __builtin_amdgcn_exp2f(hi + lo);
+        ghi[lane] = hi;
+        glo[lane] = lo;
+        ek[lane] = e;
+        eo[lane] = p.scale * e;
+        we[lane] = __builtin_amdgcn_exp2f((eh - hi) + (el - lo));
+        bt[lane] = rates.beta(p, t0, len, lane);
+      }
+    }
+    __syncthreads();
+    const float end_dec = ek[C - 1];
+    const int lane = opaque(tid) & 63, g = lane >> 4, li = lane & 15;
+    if (kk + 1 < nc) load_chunk(pc + 1);
+
+    if constexpr (MODE == kDeltaStates)
+      store_state<IO, RT>(p.states + (bh * p.nch + pc) * wsize, p.rp, p.cp, p.cp, cw + li, g, S);
+
+    if constexpr (QUERY) {
+      // ---- scores, 16 x 16 tiles on and below the diagonal dealt to the wavefronts: lane holds j = 4 g + v of i = li
+      const int rb = lane_base<IO, NK>(li, g);
+      for (int tile = wave; tile < IB * (IB + 1) / 2; tile += NW) {
+        const int ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6), jb = tile - ib * (ib + 1) / 2;
+        const int i = 16 * ib + li, j0 = 16 * jb + 4 * g;
+        f32x4 a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < RS; ++s) a = mma<IO>(frag_row<NK>(ty, rb, jb, s), frag_row<NK>(tx, rb, ib, s), a);
+        const float gi = ghi[i], gl = glo[i];
+        const float4 gj = *reinterpret_cast<const float4*>(ghi + j0), gk = *reinterpret_cast<const float4*>(glo + j0);
+        float w[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float d = __builtin_amdgcn_exp2f((gi - get(gj, v)) + (gl - get(gk, v)));
+          w[v] = j0 + v <= i ? times(p.scale * d, a[v]) : 0.f;
+        }
+        if constexpr (ES == 2) {
+          const int u = 4 * jb + g;
+          const int to = (i * NP + ((u >> 1) ^ swz<IO, NP>(i))) * 16 + (u & 1) * 8;
+          const uint2 hi2 = make_uint2(BF16::cvt2(w[0], w[1]), BF16::cvt2(w[2], w[3]));
+          *reinterpret_cast<uint2*>(tp + to) = hi2;
+          *reinterpret_cast<uint2*>(tp + C * C * ES + to) =
+              make_uint2(BF16::cvt2(w[0] - bf_lo(hi2.x), w[1] - bf_hi(hi2.x)),
+                         BF16::cvt2(w[2] - bf_lo(hi2.y), w[3] - bf_hi(hi2.y)));
+        } else {
+          *reinterpret_cast<float4*>(tp + (i * NP + ((4 * jb + g) ^ swz<IO, NP>(i))) * 16) = make_float4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+
+    // ---- what the state before the chunk gives: X = K S (rows are tokens, by state_row), O = Q S (transposed)
+    f32x4 X[IB], O[IB];
+#pragma unroll
+    for (int i = 0; i < IB; ++i) X[i] = O[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    {
+      const int sb = opaque(state_row_base<IO, NK>(li, g)), qb = opaque(lane_base<IO, NK>(li, g));
+#pragma unroll
+      for (int s = 0; s < RS; ++s) {
+        float v[E];
+        uint4 sp[PS];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = S[tile_of<IO>(s, e)][e & 3];
+        split<IO, PS>(v, sp);
+#pragma unroll
+        for (int i = 0; i < IB; ++i) {
+          const uint4 fk = frag_state_row<IO, NK>(ty, sb, i, s);
+#pragma unroll
+          for (int q = 0; q < PS; ++q) X[i] = mma<IO>(fk, sp[q], X[i]);
+          if constexpr (QUERY) {
+            const uint4 fq = frag_row<NK>(tx, qb, i, s);
+#pragma unroll
+            for (int q = 0; q < PP; ++q) O[i] = mma<IO>(sp[q], fq, O[i]);
+          }
+        }
+      }
+    }
+    // ---- x, then r = x - M (b x)
+    uint4 bx[JS][PP];
+    const int zb0 = opaque(col_base<IO, NZ>(li, g));
+#pragma unroll
+    for (int js = 0; js < JS; ++js) {
+      float e[E], bb[E], v[E] = {};
+      F32::ld<E>(ek + KS * js + E * g, e);
+      F32::ld<E>(bt + KS * js + E * g, bb);
+      if (!trans) unpack<IO>(frag_col<IO, NZ>(tz, zb0, wave, js), v);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int t = tile_of<IO>(js, i);
+        v[i] -= times(e[i], X[t][i & 3]);
+        X[t][i & 3] = v[i];
+        v[i] *= bb[i];
+      }
+      split<IO, PP>(v, bx[js]);
+    }
+    const int mb0 = opaque(state_row_base<IO, NP>(li, g));
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+      for (int js = 0; js * KS < 16 * (i + 1); ++js) {
+        const uint4 fm = frag_state_row<IO, NP>(tm, mb0, i, js);
+#pragma unroll
+        for (int q = 0; q < PP; ++q) X[i] = mma<IO>(fm, bx[js][q], X[i]);
+        if constexpr (PP == 2) X[i] = mma<IO>(frag_state_row<IO, NP>(tm + C * C * ES, mb0, i, js), bx[js][0], X[i]);
+      }
+    if constexpr (MODE == kDeltaStates)
+      store_res<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp, p.cp, cw + li, g, X);
+
+    // ---- u = b r as an operand of o, e^{G_C - G} u as one of the state's update
+    uint4 fu[JS][PP], fw[JS][PS];
+#pragma unroll
+    for (int js = 0; js < JS; ++js) {
+      float bb[E], w[E], v[E];
+      F32::ld<E>(bt + KS * js + E * g, bb);
+      F32::ld<E>(we + KS * js + E * g, w);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        v[i] = bb[i] * X[tile_of<IO>(js, i)][i & 3];
+        w[i] = times(w[i], v[i]);
+      }
+      if constexpr (QUERY) split<IO, PP>(v, fu[js]);
+      split<IO, PS>(w, fw[js]);
+    }
+    if constexpr (QUERY) {
+#pragma unroll
+      for (int ib = 0; ib < IB; ++ib) scale(O[ib], eo[16 * ib + li]);
+      __syncthreads();  // scores
+      const int pb = opaque(lane_base<IO, NP>(li, g));
+#pragma unroll
+      for (int ib = 0; ib < IB; ++ib)
+#pragma unroll
+        for (int js = 0; js * KS < 16 * (ib + 1); ++js) {
+          const uint4 fp = frag_row<NP>(tp, pb, ib, js);
+#pragma unroll
+          for (int q = 0; q < PP; ++q) O[ib] = mma<IO>(fu[js][q], fp, O[ib]);
+          if constexpr (PP == 2) O[ib] = mma<IO>(fu[js][0], frag_row<NP>(tp + C * C * ES, pb, ib, js), O[ib]);
+        }
+    }
+    // ---- the state after the chunk
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) scale(S[rt], end_dec);
+    const int yb0 = opaque(state_col_base<IO, NK>(li, g));
+#pragma unroll
+    for (int js = 0; js < JS; ++js)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const uint4 fy = frag_state_col<IO, NK>(ty, yb0, rt, js);
+#pragma unroll
+        for (int q = 0; q < PS; ++q) S[rt] = mma<IO>(fy, fw[js][q], S[rt]);
+      }
+
+    // ---- outputs, zero in rows past the length: lane holds columns cw + 4 g + v of token 16 ib + li
+    if constexpr (QUERY) {
+      const uint32_t ts = static_cast<uint32_t>(p.H * p.cols * ES);
+      const char* const ob = p.o + ((static_cast<int64_t>(b) * p.L + t0) * p.H + h) * p.cols * ES;
+      const int c = cw + 4 * g;
+#pragma unroll
+      for (int ib = 0; ib < IB; ++ib) {
+        const Rsrc ro = make_rsrc(ob + static_cast<int64_t>(16 * ib) * ts, row_bytes(p.L - t0 - 16 * ib, 16, ts));
+        if (t0 + 16 * ib + li >= len) O[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const float w[4] = {O[ib][0], O[ib][1], O[ib][2], O[ib][3]};
+        const uint32_t off = li * ts + static_cast<uint32_t>(c * ES);
+        if constexpr (VEC) {
+          BufOf<IO>::type::template st<4>(ro, c < p.cols ? off : kOOB, w);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) BufOf<IO>::type::template st<1>(ro, c + e < p.cols ? off + e * ES : kOOB, w + e);
+        }
+      }
+    }
+  }
+
+  if constexpr (QUERY) {
+    // outputs of the chunks past the length
+    const int t1 = c1 * C < p.L ? c1 * C : p.L;
+    for (int t = (ce > c0 ? ce : c0) * C + wave; t < t1; t += NW) {
+      char* const row = p.o + ((static_cast<int64_t>(b) * p.L + t) * p.H + h) * p.cols * ES;
+      for (int c = col0 + (tid & 63); c < col0 + COLS && c < p.cols; c += 64) {
+        if constexpr (ES == 4) reinterpret_cast<float*>(row)[c] = 0.f;
+        else reinterpret_cast<uint16_t*>(row)[c] = 0;
+      }
+    }
+  }
+  const int g = (tid & 63) >> 4, c = cw + (tid & 15);
+  if constexpr (MODE == kDeltaSeg) {
+    if (trans) store_state<IO, RT>(p.seg_trans + (bh * p.nseg + seg) * p.rp * p.rp, p.rp, p.rp, p.rp, c, g, S);
+    else store_state<IO, RT>(p.seg_state + (bh * p.nseg + seg) * wsize, p.rp, p.cp, p.cp, c, g, S);
+  } else if (p.last != nullptr && seg == p.nseg - 1) {
+    store_state<IO, RT>(p.last + bh * p.rows * p.cols, p.rows, p.cols, p.cols, c, g, S);
+  }
+}
+
+// ---------------------------------------------------------------- the walk over the length, backwards
+
+template <typename IO, int ROWS, int NW>
+constexpr size_t delta_rev_lds_bytes() { return delta_lds_bytes<IO, ROWS, NW, true>(); }
+
+// v is dO, h0 dlast, last dh0.  SEG: a segment's own R at its first token, from zero (the last segment: from dlast);
+// else R after every chunk and e are written.
+template <typename IO, int ROWS, int NW, bool SEG, bool VEC>
+__global__ void __launch_bounds__((64 * NW), (NW == 8 || ROWS == 256 ? 2 : 3))
+ssm_delta_rev_kernel(const DeltaDev p) {
+  using K = HeadCfg<IO>;
+  constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
+  constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
+  constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
+  constexpr int PS = DeltaCfg<IO>::STATE, PP = DeltaCfg<IO>::PAIR;
+  constexpr int MB = PP * C * C * ES, LM = (MB / 16 + T - 1) / T;
+  using TK = Tile<IO, NK, T>;
+  using TZ = Tile<IO, NZ, T>;
+
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char* const ty = lds;
+  char* const tz = ty + C * ROWS * ES;
+  char* const tm = tz + C * COLS * ES;
+  float* const ghi = reinterpret_cast<float*>(tm + MB);
+  float* const glo = ghi + C;
+  float* const ek = glo + C;
+  float* const we = ek + C;
+  float* const bt = we + C;
+  float* const eo = bt + C;
+  char* const tx = reinterpret_cast<char*>(eo + C);
+  char* const tp = tx + C * ROWS * ES;  // P^T: rows are the keys' tokens
+
+  const int tid = static_cast<int>(threadIdx.x);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int ct, seg, h, b;
+  place(p, SEG ? p.nseg - 1 : p.nseg, ct, seg, h, b);
+  if constexpr (SEG) ++seg;
+  const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nch ? c0 + p.cps : p.nch;
+  const int len = length_of(p, b);
+  const int col0 = ct * COLS, cw = col0 + wave * 16;
+  const int64_t bh = static_cast<int64_t>(b) * p.H + h, wsize = static_cast<int64_t>(p.rp) * p.cp;
+
+  f32x4 R[RT];
+  {
+    const int g = (tid & 63) >> 4, c = cw + (tid & 15);
+    if (seg == p.nseg - 1)
+      load_state<IO, RT>(p.h0 != nullptr ? p.h0 + bh * p.rows * p.cols : nullptr, p.rows, p.cols, p.cols, c, g, R);
+    else
+      load_state<IO, RT>(SEG ? nullptr : p.seg_state + (bh * p.nseg + seg + 1) * wsize, p.rp, p.cp, p.cp, c, g, R);
+  }
+  for (int i = tid; i < MB / 16; i += T) reinterpret_cast<uint4*>(tp)[i] = make_uint4(0, 0, 0, 0);
+
+  const char* const xb = p.q + b * p.q_b + static_cast<int64_t>(h / p.rep) * p.rows * ES;
+  const char* const yb = p.k + b * p.k_b + static_cast<int64_t>(h / p.rep) * p.rows * ES;
+  const char* const zb = p.v + b * p.v_b + (static_cast<int64_t>(h) * p.cols + col0) * ES;
+  const char* const mb = p.m + bh * p.nch * MB;
+
+  uint4 rx[TK::CNT], ry[TK::CNT], rz[TZ::CNT], rm[LM];
+  Rates<IO> rates;
+  auto load_chunk = [&](int pc) {
+    const int t0 = pc * C, me = opaque(tid);
+    rates.load(p, b, h, t0, len, me & 63);
+    TK::template load<VEC>(yb, p.k_t, t0, len, p.rows, me, ry);
+    TK::template load<VEC>(xb, p.q_t, t0, len, p.rows, me, rx);
+#pragma unroll
+    for (int i = 0; i < LM; ++i)
+      if (MB / 16 % T == 0 || me < MB / 16)
+        rm[i] = *reinterpret_cast<const uint4*>(mb + static_cast<int64_t>(pc) * MB + 16 * (me + i * T));
+    TZ::template load<VEC>(zb, p.v_t, t0, len, p.cols - col0, me, rz);
+  };
+
+  const int cl = (len + C - 1) / C, ce = c1 < cl ? c1 : cl, nc = ce - c0;
+  if (nc > 0) load_chunk(ce - 1);
+  for (int kk = 0; kk < nc; ++kk) {
+    const int pc = ce - 1 - kk, t0 = pc * C;
+    __syncthreads();
+    {
+      const int me = opaque(tid);
+      TK::store(ty, me, ry);
+      TK::store(tx, me, rx);
+      TZ::store(tz, me, rz);
+#pragma unroll
+      for (int i = 0; i < LM; ++i) {
+        const int at = me + i * T, r = at / NP;
+        if (MB / 16 % T == 0 || at < MB / 16) *reinterpret_cast<uint4*>(tm + 16 * (NP * r + (at % NP ^ swz<IO, NP>(r)))) = rm[i];
+      }
+    }
+    if (wave == NW - 1) {
+      float hi, lo;
+      rates.scan(hi, lo);
+      const float eh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hi), C - 1));
+      const float el = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lo), C - 1));
+      const int lane = tid & 63;
+      if (lane < C) {
+        const float e = __builtin_amdgcn_exp2f(hi + lo);
+        ghi[lane] = hi;
+        glo[lane] = lo;
+        ek[lane] = e;
+        eo[lane] = p.scale * e;
+        we[lane] = __builtin_amdgcn_exp2f((eh - hi) + (el - lo));
+        bt[lane] = rates.beta(p, t0, len, lane);
+      }
+    }
+    __syncthreads();
+    const float end_dec = ek[C - 1];
+    const int lane = opaque(tid) & 63, g = lane >> 4, li = lane & 15;
+    if (kk + 1 < nc) load_chunk(pc - 1);
+    if constexpr (!SEG) store_state<IO, RT>(p.states + (bh * p.nch + pc) * wsize, p.rp, p.cp, p.cp, cw + li, g, R);
+
+    // ---- scores transposed: lane holds i = 4 g + v of j = li
+    {
+      const int rb = lane_base<IO, NK>(li, g);
+      for (int tile = wave; tile < IB * (IB + 1) / 2; tile += NW) {
+        const int ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6), jb = tile - ib * (ib + 1) / 2;
+        const int j = 16 * jb + li, i0 = 16 * ib + 4 * g;
+        f32x4 a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < RS; ++s) a = mma<IO>(frag_row<NK>(tx, rb, ib, s), frag_row<NK>(ty, rb, jb, s), a);
+        const float gj = ghi[j], gl = glo[j];
+        const float4 gi = *reinterpret_cast<const float4*>(ghi + i0), gk = *reinterpret_cast<const float4*>(glo + i0);
+        float w[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float d = __builtin_amdgcn_exp2f((get(gi, v) - gj) + (get(gk, v) - gl));
+          w[v] = i0 + v >= j ? times(p.scale * d, a[v]) : 0.f;
+        }
+        if constexpr (ES == 2) {
+          const int u = 4 * ib + g;
+          const int to = (j * NP + ((u >> 1) ^ swz<IO, NP>(j))) * 16 + (u & 1) * 8;
+          const uint2 hi2 = make_uint2(BF16::cvt2(w[0], w[1]), BF16::cvt2(w[2], w[3]));
+          *reinterpret_cast<uint2*>(tp + to) = hi2;
+          *reinterpret_cast<uint2*>(tp + C * C * ES + to) =
+              make_uint2(BF16::cvt2(w[0] - bf_lo(hi2.x), w[1] - bf_hi(hi2.x)),
+                         BF16::cvt2(w[2] - bf_lo(hi2.y), w[3] - bf_hi(hi2.y)));
+        } else {
+          *reinterpret_cast<float4*>(tp + (j * NP + ((4 * ib + g) ^ swz<IO, NP>(j))) * 16) = make_float4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+
+    // ---- X = K R (rows are tokens)
+    f32x4 X[IB];
+#pragma unroll
+    for (int i = 0; i < IB; ++i) X[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    {
+      const int sb = opaque(state_row_base<IO, NK>(li, g));
+#pragma unroll
+      for (int s = 0; s < RS; ++s) {
+        float v[E];
+        uint4 sp[PS];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = R[tile_of<IO>(s, e)][e & 3];
+        split<IO, PS>(v, sp);
+#pragma unroll
+        for (int i = 0; i < IB; ++i) {
+          const uint4 fk = frag_state_row<IO, NK>(ty, sb, i, s);
+#pragma unroll
+          for (int q = 0; q < PS; ++q) X[i] = mma<IO>(fk, sp[q], X[i]);
+        }
+      }
+    }
+    // ---- y = P^T dO + e^{G_C - G} X
+    uint4 fz[JS];
+    const int zb0 = opaque(col_base<IO, NZ>(li, g));
+#pragma unroll
+    for (int js = 0; js < JS; ++js) {
+      float w[E];
+      F32::ld<E>(we + KS * js + E * g, w);
+      fz[js] = frag_col<IO, NZ>(tz, zb0, wave, js);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int t = tile_of<IO>(js, i);
+        X[t][i & 3] = times(w[i], X[t][i & 3]);
+      }
+    }
+    __syncthreads();  // scores
+    const int mb0 = opaque(state_row_base<IO, NP>(li, g));
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+      for (int js = 0; js < JS; ++js) {
+        if (KS * (js + 1) <= 16 * i) continue;  // above the diagonal of the transposed
+        X[i] = mma<IO>(frag_state_row<IO, NP>(tp, mb0, i, js), fz[js], X[i]);
+        if constexpr (PP == 2) X[i] = mma<IO>(frag_state_row<IO, NP>(tp + C * C * ES, mb0, i, js), fz[js], X[i]);
+      }
+    // ---- e = y - M^T (b y)
+    uint4 by[JS][PP];
+#pragma unroll
+    for (int js = 0; js < JS; ++js) {
+      float bb[E];
+      F32::ld<E>(bt + KS * js + E * g, bb);
+#pragma unroll
+      for (int i = 0; i < E; ++i) bb[i] *= X[tile_of<IO>(js, i)][i & 3];
+      split<IO, PP>(bb, by[js]);
+    }
+    const int mc0 = opaque(state_col_base<IO, NP>(li, g));
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+      for (int js = 0; js < JS; ++js) {
+        if (KS * (js + 1) <= 16 * i) continue;
+        const uint4 fm = frag_state_col<IO, NP>(tm, mc0, i, js);
+#pragma unroll
+        for (int q = 0; q < PP; ++q) X[i] = mma<IO>(fm, by[js][q], X[i]);
+        if constexpr (PP == 2) X[i] = mma<IO>(frag_state_col<IO, NP>(tm + C * C * ES, mc0, i, js), by[js][0], X[i]);
+      }
+    if constexpr (!SEG) store_res<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp, p.cp, cw + li, g, X);
+
+    // ---- the state before the chunk
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) scale(R[rt], end_dec);
+    const int yb0 = opaque(state_col_base<IO, NK>(li, g));
+#pragma unroll
+    for (int js = 0; js < JS; ++js) {
+      float e[E], bb[E], v[E], w[E];
+      F32::ld<E>(ek + KS * js + E * g, e);
+      F32::ld<E>(bt + KS * js + E * g, bb);
+      unpack<IO>(fz[js], v);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        w[i] = -times(e[i], bb[i] * X[tile_of<IO>(js, i)][i & 3]);
+        v[i] = times(p.scale * e[i], v[i]);
+      }
+      uint4 fo[PS], fe[PS];
+      split<IO, PS>(v, fo);
+      split<IO, PS>(w, fe);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const uint4 fx = frag_state_col<IO, NK>(tx, yb0, rt, js), fy = frag_state_col<IO, NK>(ty, yb0, rt, js);
+#pragma unroll
+        for (int q = 0; q < PS; ++q) {
+          R[rt] = mma<IO>(fx, fo[q], R[rt]);
+          R[rt] = mma<IO>(fy, fe[q], R[rt]);
+        }
+      }
+    }
+  }
+
+  const int g = (tid & 63) >> 4, c = cw + (tid & 15);
+  if constexpr (SEG) store_state<IO, RT>(p.seg_state + (bh * p.nseg + seg) * wsize, p.rp, p.cp, p.cp, c, g, R);
+  else if (p.last != nullptr && seg == 0) store_state<IO, RT>(p.last + bh * p.rows * p.cols, p.rows, p.cols, p.cols, c, g, R);
+}
+
+// ---------------------------------------------------------------- the gradients, all chunks at once
+
+struct DeltaGradDev {
+  DeltaDev f;                  // q, k, rates, sizes; v is dO; states S_0, res r
+  const float* r1;             // [b][H][nch][rp][cp]: R after every chunk
+  const float* e;              // [b][H][nch][C][cp]
+  char* dq;                    // [b][L][H / hn][rows]; float32 parts with `parts`
+  char* dk;
+  char* dv;                    // [b][L][H][cols]
+  char* dg;                    // [b][L][H], nullable
+  char* db;                    // [b][L][H], nullable
+  int hn;                      // heads of a group that a workgroup adds up
+  int parts;
+};
+
+template <typename IO, int ROWS, int NW>
+constexpr size_t grad_lds_bytes() {
+  using K = HeadCfg<IO>;
+  constexpr size_t slab = size_t(K::C) * kSlab * K::ES * (1 + 2 * DeltaCfg<IO>::PAIR);
+  constexpr size_t sc = size_t(2) * K::C * K::C * K::ES * DeltaCfg<IO>::PAIR;
+  return 2 * size_t(K::C) * ROWS * K::ES + (slab > sc ? slab : sc) + (size_t(2) * NW + 7) * K::C * 4 + NW * 4;
+}
+
+// dg_t = <dLoss/dS~_t, S~_t> telescopes within the chunk:
+//   dg_t = sum_{i >= t} (q_i . dq_i - k_i . dk^+_i + k_i . dk^-_i) + e^{G_C} <R_C, S_0> + sum_i k_i . w_i R_C u_i
+// with dk^+ the key's gradient as what is written (first three terms of dk above), dk^- as what is taken out (the
+// last two), each without a token's own pair scale (q . k)(do . u), which is in both and cancels.  Where the state
+// starts anew (a decay of -inf) dg is zero and the sum of the tokens before begins there.
+template <typename IO, int ROWS, int NW, bool VEC>
+__global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const DeltaGradDev d) {
+  using K = HeadCfg<IO>;
+  const DeltaDev& p = d.f;
+  constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW;
+  constexpr int NK = ROWS * ES / 16, NS = kSlab * ES / 16, NP = C * ES / 16;
+  constexpr int IB = C / 16, JS = C / KS, SS = kSlab / KS, CT = ROWS / 16 / NW;
+  constexpr int PP = DeltaCfg<IO>::PAIR, SB = C * kSlab * ES, PB = C * C * ES;
+  constexpr int TILES = IB * (IB + 1) / 2, MINE = (2 * TILES + NW - 1) / NW;
+  constexpr int TASKS = C * NS / T;  // staging tasks a thread, rows tid / NS + i T / NS
+  static_assert(C * NS % T == 0 && CT >= 1, "shares are even");
+  using TK = Tile<IO, NK, T>;
+
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  char* const tx = lds;
+  char* const ty = tx + C * ROWS * ES;
+  char* const slab = ty + C * ROWS * ES;  // dO, b r, b e; then the scores dP and dN
+  constexpr size_t kSlabBytes = SB * (1 + 2 * PP) > 2 * PB * PP ? SB * (1 + 2 * PP) : 2 * PB * PP;
+  char* const tdo = slab;
+  char* const tu = slab + SB;
+  char* const te = tu + PP * SB;
+  char* const tp = slab;
+  char* const tn = slab + PP * PB;
+  float* const ghi = reinterpret_cast<float*>(slab + kSlabBytes);
+  float* const glo = ghi + C;
+  float* const ek = glo + C;
+  float* const we = ek + C;
+  float* const bt = we + C;
+  float* const own = bt + C;    // scale do . u of a token's own
+  int* const anew = reinterpret_cast<int*>(own + C);  // the state starts anew at the token
+  float* const red = own + 2 * C;   // [NW][C]
+  float* const redc = red + NW * C;
+  float* const rs = redc + NW * C;  // [NW]
+
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int groups = p.H / d.hn;
+  const int pc = blockIdx.x % p.nch, bg = blockIdx.x / p.nch, hg = bg % groups, b = bg / groups, t0 = pc * C;
+  const int len = length_of(p, b);
+  const int oes = d.parts ? 4 : ES;
+  const uint32_t ots = static_cast<uint32_t>(groups * p.rows * oes), vts = p.H * p.cols * ES;
+  const int64_t row0 = static_cast<int64_t>(b) * p.L + t0;
+
+  f32x4 DQ[CT][IB], DK[CT][IB];
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int i = 0; i < IB; ++i) DQ[c][i] = DK[c][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  if (t0 < len) {
+    const int hk = hg * d.hn / p.rep;
+    {
+      uint4 rx[TK::CNT], ry[TK::CNT];
+      TK::template load<VEC>(p.q + b * p.q_b + static_cast<int64_t>(hk) * p.rows * ES, p.q_t, t0, len, p.rows, tid, rx);
+      TK::template load<VEC>(p.k + b * p.k_b + static_cast<int64_t>(hk) * p.rows * ES, p.k_t, t0, len, p.rows, tid, ry);
+      TK::store(tx, tid, rx);
+      TK::store(ty, tid, ry);
+    }
+    for (int hh = 0; hh < d.hn; ++hh) {
+      const int h = hg * d.hn + hh;
+      const int64_t bh = static_cast<int64_t>(b) * p.H + h, chunk = bh * p.nch + pc;
+      const float* const s0 = p.states + chunk * p.rp * p.cp;
+      const float* const r1 = d.r1 + chunk * p.rp * p.cp;
+      const uint32_t wbytes = static_cast<uint32_t>(p.rp * p.cp * 4);
+      const Rsrc rs0 = make_rsrc(s0, wbytes), rr1 = make_rsrc(r1, wbytes);
+      __syncthreads();  // the head before is done with the LDS
+      if (wave == NW - 1) {
+        Rates<IO> rates;
+        rates.load(p, b, h, t0, len, lane);
+        float hi, lo;
+        rates.scan(hi, lo);
+        const float eh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hi), C - 1));
+        const float el = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lo), C - 1));
+        if (lane < C) {
+          ghi[lane] = hi;
+          glo[lane] = lo;
+          ek[lane] = __builtin_amdgcn_exp2f(hi + lo);
+          we[lane] = __builtin_amdgcn_exp2f((eh - hi) + (el - lo));
+          bt[lane] = rates.beta(p, t0, len, lane);
+          anew[lane] = clamp_decay(Rates<IO>::value(rates.raw_g) * kLog2e) == kMinLog2Decay;
+        }
+      }
+      __syncthreads();
+
+      f32x4 dq[CT][IB], ur[CT][IB], vs[CT][IB], sc[MINE];
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int i = 0; i < IB; ++i) dq[c][i] = ur[c][i] = vs[c][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) sc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      float dot_rs = 0.f, dot_b[TASKS] = {};
+
+      for (int v0 = 0; v0 < p.cols; v0 += kSlab) {
+        // ---- dO, b r and b e of 64 columns, as parts; dv and the sums of db on the way
+#pragma unroll
+        for (int i = 0; i < TASKS; ++i) {
+          const int r = tid / NS + i * (T / NS), c = tid % NS, col = v0 + c * E;
+          const Rsrc rdo = make_rsrc(p.v + b * p.v_b + static_cast<int64_t>(t0) * p.v_t + static_cast<int64_t>(h) * p.cols * ES,
+                                     row_bytes(len - t0, C, p.v_t));
+          const uint4 fo = load16<IO, VEC>(rdo, r * p.v_t + col * ES, p.cols - col);
+          const int64_t at = (chunk * C + r) * p.cp + col;
+          float x[E], y[E], bb = bt[r];
+          F32::ld<E>(p.res + at, x);
+          F32::ld<E>(d.e + at, y);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            dot_b[i] = __builtin_fmaf(x[e], y[e], dot_b[i]);
+            x[e] *= bb;
+            y[e] *= bb;
+          }
+          if (t0 + r < p.L) {
+            const Rsrc rdv = make_rsrc(d.dv + row0 * vts + static_cast<int64_t>(h) * p.cols * ES, row_bytes(p.L - t0, C, vts));
+            const uint32_t off = r * vts + col * ES;
+            if constexpr (VEC) {
+              BufOf<IO>::type::template st<E>(rdv, col < p.cols ? off : kOOB, y);
+            } else {
+#pragma unroll
+              for (int e = 0; e < E; ++e) BufOf<IO>::type::template st<1>(rdv, col + e < p.cols ? off + e * ES : kOOB, y + e);
+            }
+          }
+          uint4 w[PP];
+          const int to = 16 * (NS * r + (c ^ swz<IO, NS>(r)));
+          *reinterpret_cast<uint4*>(tdo + to) = fo;
+          split<IO, PP>(x, w);
+#pragma unroll
+          for (int q = 0; q < PP; ++q) *reinterpret_cast<uint4*>(tu + q * SB + to) = w[q];
+          split<IO, PP>(y, w);
+#pragma unroll
+          for (int q = 0; q < PP; ++q) *reinterpret_cast<uint4*>(te + q * SB + to) = w[q];
+        }
+        __syncthreads();
+        const int fb = lane_base<IO, NS>(li, g);
+#pragma unroll
+        for (int s = 0; s < SS; ++s) {
+          uint4 fs[CT][PP], fr[CT][PP];
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            const uint32_t off = static_cast<uint32_t>(((wave * CT + c) * 16 + li) * p.cp + v0 + KS * s + E * g) * 4;
+            float x[E], y[E];
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+              BufF32::ld<4>(rs0, off + 4 * e, x + e);
+              BufF32::ld<4>(rr1, off + 4 * e, y + e);
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) dot_rs = __builtin_fmaf(x[e], y[e], dot_rs);
+            split<IO, PP>(x, fs[c]);
+            split<IO, PP>(y, fr[c]);
+          }
+#pragma unroll
+          for (int ib = 0; ib < IB; ++ib) {
+            uint4 fo = frag_row<NS>(tdo, fb, ib, s), fu[PP], fe[PP];
+#pragma unroll
+            for (int q = 0; q < PP; ++q) {
+              fu[q] = frag_row<NS>(tu + q * SB, fb, ib, s);
+              fe[q] = frag_row<NS>(te + q * SB, fb, ib, s);
+            }
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+#pragma unroll
+              for (int q = 0; q < PP; ++q) {
+                dq[c][ib] = mma<IO>(fs[c][q], fo, dq[c][ib]);
+                ur[c][ib] = mma<IO>(fr[c][q], fu[0], ur[c][ib]);
+                vs[c][ib] = mma<IO>(fs[c][q], fe[0], vs[c][ib]);
+              }
+              if constexpr (PP == 2) {
+                ur[c][ib] = mma<IO>(fr[c][0], fu[1], ur[c][ib]);
+                vs[c][ib] = mma<IO>(fs[c][0], fe[1], vs[c][ib]);
+              }
+            }
+          }
+          // tiles of dP, then of dN, dealt to the wavefronts: lane holds j = 4 g + v of i = li
+#pragma unroll
+          for (int m = 0; m < MINE; ++m) {
+            const int job = wave + m * NW, tile = job < TILES ? job : job - TILES;
+            if (job >= 2 * TILES) break;
+            const int ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6), jb = tile - ib * (ib + 1) / 2;
+            const char* const x = job < TILES ? tdo : te;
+            const uint4 fx = frag_row<NS>(x, fb, ib, s);
+#pragma unroll
+            for (int q = 0; q < PP; ++q) sc[m] = mma<IO>(frag_row<NS>(tu + q * SB, fb, jb, s), fx, sc[m]);
+            if (PP == 2 && job >= TILES) sc[m] = mma<IO>(frag_row<NS>(tu, fb, jb, s), frag_row<NS>(te + SB, fb, ib, s), sc[m]);
+          }
+        }
+        __syncthreads();
+      }
+
+      // ---- the scores' gradients to LDS, below the diagonal
+      for (int i = tid; i < 2 * PP * PB / 16; i += T) reinterpret_cast<uint4*>(slab)[i] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+#pragma unroll
+      for (int m = 0; m < MINE; ++m) {
+        const int job = wave + m * NW, tile = job < TILES ? job : job - TILES;
+        if (job >= 2 * TILES) break;
+        const int ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6), jb = tile - ib * (ib + 1) / 2;
+        const int i = 16 * ib + li, j0 = 16 * jb + 4 * g;
+        const float by = job < TILES ? p.scale : -1.f;
+        float w[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float dd = __builtin_amdgcn_exp2f((ghi[i] - ghi[j0 + v]) + (glo[i] - glo[j0 + v]));
+          w[v] = j0 + v < i ? times(by * dd, sc[m][v]) : 0.f;
+          if (job < TILES && j0 + v == i) own[i] = p.scale * sc[m][v];
+        }
+        char* const to = job < TILES ? tp : tn;
+        if constexpr (ES == 2) {
+          const int u = 4 * jb + g, at = (i * NP + ((u >> 1) ^ swz<IO, NP>(i))) * 16 + (u & 1) * 8;
+          const uint2 hi2 = make_uint2(BF16::cvt2(w[0], w[1]), BF16::cvt2(w[2], w[3]));
+          *reinterpret_cast<uint2*>(to + at) = hi2;
+          *reinterpret_cast<uint2*>(to + PB + at) = make_uint2(BF16::cvt2(w[0] - bf_lo(hi2.x), w[1] - bf_hi(hi2.x)),
+                                                               BF16::cvt2(w[2] - bf_lo(hi2.y), w[3] - bf_hi(hi2.y)));
+        } else {
+          *reinterpret_cast<float4*>(to + (i * NP + ((4 * jb + g) ^ swz<IO, NP>(i))) * 16) = make_float4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      // <R_C, S_0> of the wavefront
+#pragma unroll
+      for (int x = 1; x < 64; x *= 2) dot_rs += __shfl_xor(dot_rs, x);
+      if (lane == 0) rs[wave] = dot_rs;
+      // db: the NS lanes of a row
+      if (d.db != nullptr) {
+#pragma unroll
+        for (int i = 0; i < TASKS; ++i) {
+          float x = dot_b[i];
+#pragma unroll
+          for (int s = 1; s < NS; s *= 2) x += __shfl_xor(x, s);
+          const int r = tid / NS + i * (T / NS);
+          if (tid % NS == 0 && t0 + r < p.L) {
+            IO::template st<1>(reinterpret_cast<typename IO::T*>(d.db) + (row0 + r) * p.H + h, &x);
+          }
+        }
+      }
+      // ---- the state's parts scaled: lane holds rows (d_key) 16 (wave CT + c) + 4 g + v of token 16 ib + li
+      auto values = [&](const char* tile, int c, int ib, float* v) {
+        const int r = 16 * ib + li, col = 16 * (wave * CT + c) + 4 * g;
+        IO::template ld<4>(reinterpret_cast<const typename IO::T*>(
+                               tile + 16 * (NK * r + (col / E ^ swz<IO, NK>(li))) + col % E * ES), v);
+      };
+#pragma unroll
+      for (int ib = 0; ib < IB; ++ib) {
+        const float fe = ek[16 * ib + li], fw = we[16 * ib + li];
+        float dot = 0.f;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          scale(dq[c][ib], p.scale * fe);
+          scale(vs[c][ib], -fe);
+          scale(ur[c][ib], fw);
+          float kv[4];
+          values(ty, c, ib, kv);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) dot = __builtin_fmaf(kv[v], ur[c][ib][v], dot);
+        }
+        dot += __shfl_xor(dot, 16);
+        dot += __shfl_xor(dot, 32);
+        if (g == 0) redc[wave * C + 16 * ib + li] = dot;
+      }
+      __syncthreads();  // scores
+      // ---- what the chunk's tokens give each other
+      const int pb = lane_base<IO, NP>(li, g), pcb = col_base<IO, NP>(li, g), kb = col_base<IO, NK>(li, g);
+#pragma unroll
+      for (int js = 0; js < JS; ++js) {
+        uint4 fk[CT], fq[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          fk[c] = frag_col<IO, NK>(ty, kb, wave * CT + c, js);
+          fq[c] = frag_col<IO, NK>(tx, kb, wave * CT + c, js);
+        }
+#pragma unroll
+        for (int ib = 0; ib < IB; ++ib) {
+          if (js * KS < 16 * (ib + 1)) {
+#pragma unroll
+            for (int q = 0; q < PP; ++q) {
+              const uint4 fp = frag_row<NP>(tp + q * PB, pb, ib, js), fn = frag_row<NP>(tn + q * PB, pb, ib, js);
+#pragma unroll
+              for (int c = 0; c < CT; ++c) {
+                dq[c][ib] = mma<IO>(fk[c], fp, dq[c][ib]);
+                vs[c][ib] = mma<IO>(fk[c], fn, vs[c][ib]);
+              }
+            }
+          }
+          if (KS * (js + 1) > 16 * ib) {
+#pragma unroll
+            for (int q = 0; q < PP; ++q) {
+              const uint4 fp = frag_col<IO, NP>(tp + q * PB, pcb, ib, js), fn = frag_col<IO, NP>(tn + q * PB, pcb, ib, js);
+#pragma unroll
+              for (int c = 0; c < CT; ++c) {
+                ur[c][ib] = mma<IO>(fq[c], fp, ur[c][ib]);
+                ur[c][ib] = mma<IO>(fk[c], fn, ur[c][ib]);
+              }
+            }
+          }
+        }
+      }
+      // ---- the dots for dg, then a token's own pair
+#pragma unroll
+      for (int ib = 0; ib < IB; ++ib) {
+        float dot = 0.f;
+        const float o = own[16 * ib + li];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          float qv[4], kv[4];
+          values(tx, c, ib, qv);
+          values(ty, c, ib, kv);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            dot = __builtin_fmaf(qv[v], dq[c][ib][v], dot);
+            dot = __builtin_fmaf(kv[v], vs[c][ib][v] - ur[c][ib][v], dot);
+            DQ[c][ib][v] += __builtin_fmaf(o, kv[v], dq[c][ib][v]);
+            DK[c][ib][v] += __builtin_fmaf(o, qv[v], ur[c][ib][v] + vs[c][ib][v]);
+          }
+        }
+        dot += __shfl_xor(dot, 16);
+        dot += __shfl_xor(dot, 32);
+        if (g == 0) red[wave * C + 16 * ib + li] = dot;
+      }
+      if (d.dg != nullptr) {
+        __syncthreads();
+        if (wave == 0) {
+          double v = 0, tail = 0, edge = 0;
+          int cut = 0;
+          if (lane < C) {
+            for (int w = 0; w < NW; ++w) {
+              v += red[w * C + lane];
+              tail += redc[w * C + lane];
+            }
+            cut = lane + 1 < C ? anew[lane + 1] : 0;
+          }
+          for (int w = 0; w < NW; ++w) edge += rs[w];
+#pragma unroll
+          for (int x = 1; x < 64; x *= 2) tail += __shfl_xor(tail, x);
+          if (lane == C - 1) v += tail + times(ek[C - 1], static_cast<float>(edge));
+          // sums from the end; lane l takes over those further on unless the state starts anew between
+#pragma unroll
+          for (int x = 1; x < 64; x *= 2) {
+            const double o = __shfl_down(v, x);
+            const int a = __shfl_down(cut, x);
+            if (lane + x < 64) {
+              if (!cut) v += o;
+              cut |= a;
+            }
+          }
+          const int t = t0 + lane;
+          if (lane < C && t < p.L) {
+            const bool none = t >= len || (t == 0 && p.h0 == nullptr) || anew[lane];
+            const float out = none ? 0.f : static_cast<float>(v);
+            IO::template st<1>(reinterpret_cast<typename IO::T*>(d.dg) + (row0 + lane) * p.H + h, &out);
+          }
+        }
+      }
+    }
+  } else {
+    // nothing of the chunk exists
+    for (int r = wave; r < C && t0 + r < p.L; r += NW) {
+      for (int hh = 0; hh < d.hn; ++hh) {
+        const int64_t at = (row0 + r) * p.H + hg * d.hn + hh;
+        const float z = 0.f;
+        for (int c = lane; c < p.cols; c += 64) IO::template st<1>(reinterpret_cast<typename IO::T*>(d.dv) + at * p.cols + c, &z);
+        if (lane == 0 && d.dg != nullptr) IO::template st<1>(reinterpret_cast<typename IO::T*>(d.dg) + at, &z);
+        if (lane == 0 && d.db != nullptr) IO::template st<1>(reinterpret_cast<typename IO::T*>(d.db) + at, &z);
+      }
+    }
+  }
+
+  // ---- dq and dk
+  const int64_t out0 = row0 * ots + static_cast<int64_t>(hg) * p.rows * oes;
+#pragma unroll
+  for (int ib = 0; ib < IB; ++ib) {
+    const uint32_t nb = row_bytes(p.L - t0 - 16 * ib, 16, ots);
+    const Rsrc rq = make_rsrc(d.dq + out0 + static_cast<int64_t>(16 * ib) * ots, nb);
+    const Rsrc rk = make_rsrc(d.dk + out0 + static_cast<int64_t>(16 * ib) * ots, nb);
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      const int col = 16 * (wave * CT + c) + 4 * g;
+      const uint32_t off = li * ots + col * oes;
+      const float vq[4] = {DQ[c][ib][0], DQ[c][ib][1], DQ[c][ib][2], DQ[c][ib][3]};
+      const float vk[4] = {DK[c][ib][0], DK[c][ib][1], DK[c][ib][2], DK[c][ib][3]};
+      if (VEC && !d.parts) {
+        BufOf<IO>::type::template st<4>(rq, col < p.rows ? off : kOOB, vq);
+        BufOf<IO>::type::template st<4>(rk, col < p.rows ? off : kOOB, vk);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t oe = col + e < p.rows ? off + e * oes : kOOB;
+          if (d.parts) {
+            BufF32::st<1>(rq, oe, vq + e);
+            BufF32::st<1>(rk, oe, vk + e);
+          } else {
+            BufOf<IO>::type::template st<1>(rq, oe, vq + e);
+            BufOf<IO>::type::template st<1>(rk, oe, vk + e);
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- launches
+
+// More than 64 KB of LDS is asked for once per device and kernel (the call costs as much as a launch).
+template <typename Kern>
+hipError_t allow_lds(Kern kern, size_t smem, std::atomic<uint64_t>& allowed) {
+  if (smem <= 65536) return hipSuccess;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev > 63 || (allowed.load(std::memory_order_relaxed) & bit) == 0) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            static_cast<int>(smem));
+    if (e == hipSuccess && dev <= 63) allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return e;
+}
+
+template <typename IO, int ROWS, bool VEC>
+hipError_t launch_prep_t(const DeltaDev& p, hipStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
+  constexpr size_t smem = prep_lds_bytes<IO, ROWS>();
+  auto kern = ssm_delta_prep_kernel<IO, ROWS, VEC>;
+  if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.batch * p.H * p.nch)), dim3(256), smem, st, p);
+  return hipGetLastError();
+}
+
+template <typename IO, int ROWS, int NW, int MODE, bool VEC>
+hipError_t launch_walk_t(const DeltaDev& p, hipStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
+  constexpr size_t smem = delta_lds_bytes<IO, ROWS, NW, MODE == kDeltaOut>();
+  const int64_t nrun = MODE == kDeltaSeg ? p.nseg - 1 : p.nseg;
+  auto kern = ssm_delta_kernel<IO, ROWS, NW, MODE, VEC>;
+  if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(nrun * p.ntile * p.H * p.batch)), dim3(64 * NW), smem, st, p);
+  return hipGetLastError();
+}
+
+template <typename IO, int ROWS, int NW, bool SEG, bool VEC>
+hipError_t launch_rev_t(const DeltaDev& p, hipStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
+  constexpr size_t smem = delta_rev_lds_bytes<IO, ROWS, NW>();
+  const int64_t nrun = SEG ? p.nseg - 1 : p.nseg;
+  auto kern = ssm_delta_rev_kernel<IO, ROWS, NW, SEG, VEC>;
+  if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(nrun * p.ntile * p.H * p.batch)), dim3(64 * NW), smem, st, p);
+  return hipGetLastError();
+}
+
+template <typename IO, int ROWS, bool VEC>
+hipError_t launch_grad_t(const DeltaGradDev& d, hipStream_t st) {
+  constexpr int NW = ROWS == 64 ? 4 : 8;
+  static std::atomic<uint64_t> allowed{0};
+  constexpr size_t smem = grad_lds_bytes<IO, ROWS, NW>();
+  auto kern = ssm_delta_grad_kernel<IO, ROWS, NW, VEC>;
+  if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
+  const int64_t wgs = static_cast<int64_t>(d.f.batch) * (d.f.H / d.hn) * d.f.nch;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(wgs)), dim3(64 * NW), smem, st, d);
+  return hipGetLastError();
+}
+
+// `wide` is a tile of 128 columns, eight wavefronts of 16, else 64 and four.
+enum { kPassPrep, kPassOut, kPassSeg, kPassStates, kPassRevSeg, kPassRev };
+
+template <typename IO, int ROWS, bool VEC>
+hipError_t launch_pass_r(const DeltaDev& p, int pass, bool wide, hipStream_t st) {
+  if (pass == kPassPrep) return launch_prep_t<IO, ROWS, VEC>(p, st);
+  if constexpr (VEC) {
+    if (wide) {
+      if (pass == kPassOut) return launch_walk_t<IO, ROWS, 8, kDeltaOut, VEC>(p, st);
+      if (pass == kPassSeg) return launch_walk_t<IO, ROWS, 8, kDeltaSeg, VEC>(p, st);
+      if (pass == kPassStates) return launch_walk_t<IO, ROWS, 8, kDeltaStates, VEC>(p, st);
+      if (pass == kPassRevSeg) return launch_rev_t<IO, ROWS, 8, true, VEC>(p, st);
+      return launch_rev_t<IO, ROWS, 8, false, VEC>(p, st);
+    }
+  }
+  if (pass == kPassOut) return launch_walk_t<IO, ROWS, 4, kDeltaOut, VEC>(p, st);
+  if (pass == kPassSeg) return launch_walk_t<IO, ROWS, 4, kDeltaSeg, VEC>(p, st);
+  if (pass == kPassStates) return launch_walk_t<IO, ROWS, 4, kDeltaStates, VEC>(p, st);
+  if (pass == kPassRevSeg) return launch_rev_t<IO, ROWS, 4, true, VEC>(p, st);
+  return launch_rev_t<IO, ROWS, 4, false, VEC>(p, st);
+}
+
+template <typename IO>
+hipError_t launch_pass_io(const DeltaDev& p, int pass, bool wide, bool vec, hipStream_t st) {
+  if (p.rows <= 64) return vec ? launch_pass_r<IO, 64, true>(p, pass, wide, st) : launch_pass_r<IO, 64, false>(p, pass, wide, st);
+  if (p.rows <= 128) return vec ? launch_pass_r<IO, 128, true>(p, pass, wide, st) : launch_pass_r<IO, 128, false>(p, pass, wide, st);
+  return vec ? launch_pass_r<IO, 256, true>(p, pass, wide, st) : launch_pass_r<IO, 256, false>(p, pass, wide, st);
+}
+
+template <typename IO>
+hipError_t launch_grad_io(const DeltaGradDev& d, bool vec, hipStream_t st) {
+  if (d.f.rows <= 64) return vec ? launch_grad_t<IO, 64, true>(d, st) : launch_grad_t<IO, 64, false>(d, st);
+  if (d.f.rows <= 128) return vec ? launch_grad_t<IO, 128, true>(d, st) : launch_grad_t<IO, 128, false>(d, st);
+  return vec ? launch_grad_t<IO, 256, true>(d, st) : launch_grad_t<IO, 256, false>(d, st);
+}
+
+}  // namespace deltak
+
+// One pass; ROWS is d_key rounded up to 64, 128 or 256 (one source file per type and forwards or backwards).
+hipError_t launch_delta_bf16(const deltak::DeltaDev& p, int pass, bool wide, bool vec, hipStream_t st);
+hipError_t launch_delta_f32(const deltak::DeltaDev& p, int pass, bool wide, bool vec, hipStream_t st);
+hipError_t launch_delta_grad_bf16(const deltak::DeltaGradDev& d, bool vec, hipStream_t st);
+hipError_t launch_delta_grad_f32(const deltak::DeltaGradDev& d, bool vec, hipStream_t st);
+
+}  // namespace ssm

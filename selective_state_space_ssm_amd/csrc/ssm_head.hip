@@ -429,17 +429,17 @@ int64_t part_heads(const HeadArgs& a, const Plan& pl, bool bf16) {
              : 1;
 }
 
-template <typename IO>
-hipError_t launch_group_sum(const float* part, void* out, const HeadArgs& a, int64_t heads, hipStream_t st) {
+}  // namespace
+
+hipError_t launch_head_group_sum(const float* part, void* out, const HeadArgs& a, int64_t heads, bool bf16, hipStream_t st) {
   const int64_t n = a.batch * a.L * a.Hk * a.dk;
   const bool four = a.dk % 4 == 0;
-  auto kern = four ? ssm_head_group_sum_kernel<IO, 4> : ssm_head_group_sum_kernel<IO, 1>;
+  auto kern = bf16 ? (four ? ssm_head_group_sum_kernel<BF16, 4> : ssm_head_group_sum_kernel<BF16, 1>)
+                   : (four ? ssm_head_group_sum_kernel<F32, 4> : ssm_head_group_sum_kernel<F32, 1>);
   const int64_t wgs = std::min(cdiv(n, four ? 1024 : 256), kHeadSumWorkgroups);
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(wgs)), dim3(256), 0, st, part, out, n, a.dk, a.H / a.Hk / heads);
   return hipGetLastError();
 }
-
-}  // namespace
 
 int64_t head_workspace_bytes(const HeadArgs& a, bool bf16, bool backward) {
   return backward ? bwd_space(a, bwd_plan(a, bf16)).total : fwd_space(a, fwd_plan(a, bf16)).total;
@@ -537,11 +537,8 @@ hipError_t launch_head_bwd(const HeadArgs& a, bool bf16, char* work, hipStream_t
     e = hipGetLastError();
   }
   if (e == hipSuccess && shared) {
-    e = bf16 ? launch_group_sum<BF16>(static_cast<const float*>(pq), a.dq, a, heads, st)
-             : launch_group_sum<F32>(static_cast<const float*>(pq), a.dq, a, heads, st);
-    if (e == hipSuccess)
-      e = bf16 ? launch_group_sum<BF16>(static_cast<const float*>(pk), a.dk_out, a, heads, st)
-               : launch_group_sum<F32>(static_cast<const float*>(pk), a.dk_out, a, heads, st);
+    e = launch_head_group_sum(static_cast<const float*>(pq), a.dq, a, heads, bf16, st);
+    if (e == hipSuccess) e = launch_head_group_sum(static_cast<const float*>(pk), a.dk_out, a, heads, bf16, st);
   }
   return e;
 }

@@ -231,6 +231,27 @@ struct HeadStepArgs {
 };
 hipError_t launch_head_step(const HeadStepArgs& a, bool bf16, hipStream_t st);
 
+// dq or dk of shared heads: out[t][hk][e] = sum of the parts of the heads that share hk, `heads` of them a part
+hipError_t launch_head_group_sum(const float* part, void* out, const HeadArgs& a, int64_t heads, bool bf16, hipStream_t st);
+
+// Delta scan (ssm_delta.hip): S~_t = e^{g_t} S_{t-1}, r_t = v_t - S~_t^T k_t,
+// S_t = S~_t + beta_t k_t r_t^T, o_t = scale S_t^T q_t.  Operands as the head
+// scan's; g_head is not used.
+struct DeltaArgs : HeadArgs {
+  const void* beta;        // [batch][L][H], nullable (ones)
+  void* dbeta;             // [batch][L][H], nullable
+};
+int64_t delta_workspace_bytes(const DeltaArgs& a, bool bf16, bool backward);
+// workgroups of the largest launch, of 256 threads each
+int64_t delta_workgroups(const DeltaArgs& a, bool bf16, bool backward);
+hipError_t launch_delta_fwd(const DeltaArgs& a, bool bf16, char* work, hipStream_t st);
+hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream_t st);
+
+struct DeltaStepArgs : HeadStepArgs {
+  const void* beta;        // nullable (ones)
+};
+hipError_t launch_delta_step(const DeltaStepArgs& a, bool bf16, hipStream_t st);
+
 // Grouped norm of dense rows [rows][channels] with a SiLU gate (ssm_norm.hip)
 // and its gradients.
 struct NormArgs {
