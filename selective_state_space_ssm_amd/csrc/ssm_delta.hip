@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 #include "ssm_delta_kernel.h"
 #include "ssm_device.h"
@@ -34,6 +35,7 @@ namespace {
 
 using namespace dev;
 using deltak::DeltaDev;
+using headk::f32x4;
 using deltak::DeltaGradDev;
 
 constexpr int64_t kDeltaSlots = 512;     // workgroups that a split length is to give
@@ -41,59 +43,72 @@ constexpr int64_t kDeltaMinSegment = 8;  // chunks
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
-bool wide_for(int64_t cols, bool vec) { return cols > 64 && vec; }
+bool wide_for(int64_t cols, bool vec) { static const char* e = getenv("DW"); return e && cols > 64 && vec; }
 int64_t tiles_for(int64_t cols, bool vec) { return cdiv(cols, wide_for(cols, vec) ? 128 : 64); }
 
 // States carried over the segments, in order, 16 columns a workgroup: state <- A carried + own, or A^T carried + own
-// from the end.  Float32 matrix instructions; the carried columns are in LDS.
-__global__ void __launch_bounds__(256) ssm_delta_carry_kernel(float* state, const float* trans, int64_t nseg, int rp, int cp,
-                                                              int rev) {
-  __shared__ float carried[256][17];
+// from the end.  Float32 matrix instructions; the carried columns are in LDS.  A segment's part of A (16 RT rows a
+// wavefront) is asked for while the segment before is worked on: each operand takes its successor once it is used.
+template <int RT, bool REV>
+__global__ void __launch_bounds__(512) ssm_delta_carry_kernel(float* state, const float* trans, int nseg, int rp, int cp) {
+  constexpr int KT = 8 * RT;  // operand steps of 16 rows: rp / 16 of them
+  __shared__ float carried[128 * RT][17];
   const int64_t bh = blockIdx.y;
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = blockIdx.x * 16 + li, tiles = rp / 16;
   const int64_t ws = static_cast<int64_t>(rp) * cp, ts = static_cast<int64_t>(rp) * rp;
   float* const s = state + bh * nseg * ws;
   const float* const m = trans + bh * nseg * ts;
-  const int64_t first = rev ? nseg - 1 : 0, step = rev ? -1 : 1;
-  for (int r = tid / 16; r < rp; r += 16) carried[r][tid % 16] = s[first * ws + static_cast<int64_t>(r) * cp + blockIdx.x * 16 + tid % 16];
-  __syncthreads();
-  for (int64_t i = 1; i < nseg - 1; ++i) {
-    const int64_t at = first + i * step;
+  const int first = REV ? nseg - 1 : 0, step = REV ? -1 : 1;
+  float4 f[RT][KT];
+  f32x4 acc[RT];
+  auto load_a = [&](int at, int t, int k) {
     const float* const a = m + at * ts;
+    const int r = 16 * (wave + 8 * t) + li, k0 = 16 * k + 4 * g;
+    if (wave + 8 * t >= tiles || k >= tiles) return;
+    if (REV) f[t][k] = make_float4(a[k0 * rp + r], a[(k0 + 1) * rp + r], a[(k0 + 2) * rp + r], a[(k0 + 3) * rp + r]);
+    else f[t][k] = *reinterpret_cast<const float4*>(a + r * rp + k0);
+  };
+  for (int i = tid; i < rp * 16; i += 512) carried[i / 16][i % 16] = s[first * ws + static_cast<int64_t>(i / 16) * cp + blockIdx.x * 16 + i % 16];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int k = 0; k < KT; ++k) load_a(first + step, t, k);
+  __syncthreads();
+  for (int i = 1; i < nseg - 1; ++i) {
+    const int at = first + i * step, next = i + 2 < nseg ? at + step : at;
     float* const own = s + at * ws;
-    headk::f32x4 acc[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int rt = wave + 4 * t;
-      if (rt >= tiles) continue;
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) acc[t][v] = own[static_cast<int64_t>(16 * rt + 4 * g + v) * cp + c];
-    }
-    for (int k0 = 0; k0 < rp; k0 += 16) {
-      const float4 x = make_float4(carried[k0 + 4 * g][li], carried[k0 + 4 * g + 1][li], carried[k0 + 4 * g + 2][li],
-                                   carried[k0 + 4 * g + 3][li]);
+      for (int v = 0; v < 4; ++v)
+        acc[t][v] = wave + 8 * t < tiles ? own[static_cast<int64_t>(16 * (wave + 8 * t) + 4 * g + v) * cp + c] : 0.f;
+    f32x4 sum[RT][2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int rt = wave + 4 * t;
-        if (rt >= tiles) continue;
-        const int r = 16 * rt + li, k = k0 + 4 * g;
-        float4 f;
-        if (rev) f = make_float4(a[k * rp + r], a[(k + 1) * rp + r], a[(k + 2) * rp + r], a[(k + 3) * rp + r]);
-        else f = *reinterpret_cast<const float4*>(a + r * rp + k);
-        acc[t] = headk::mma<F32>(__builtin_bit_cast(uint4, f), __builtin_bit_cast(uint4, x), acc[t]);
+    for (int t = 0; t < RT; ++t) sum[t][0] = sum[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      if (k >= tiles) continue;
+      const float4 x = make_float4(carried[16 * k + 4 * g][li], carried[16 * k + 4 * g + 1][li], carried[16 * k + 4 * g + 2][li],
+                                   carried[16 * k + 4 * g + 3][li]);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        if (wave + 8 * t < tiles)
+          sum[t][k & 1] = headk::mma<F32>(__builtin_bit_cast(uint4, f[t][k]), __builtin_bit_cast(uint4, x), sum[t][k & 1]);
+        load_a(next, t, k);
       }
     }
     __syncthreads();
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int rt = wave + 4 * t;
-      if (rt >= tiles) continue;
+    for (int t = 0; t < RT; ++t) {
+      if (wave + 8 * t >= tiles) continue;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int r = 16 * rt + 4 * g + v;
-        carried[r][li] = acc[t][v];
-        own[static_cast<int64_t>(r) * cp + c] = acc[t][v];
+        const int r = 16 * (wave + 8 * t) + 4 * g + v;
+        const float x = acc[t][v] + (sum[t][0][v] + sum[t][1][v]);
+        carried[r][li] = x;
+        own[static_cast<int64_t>(r) * cp + c] = x;
       }
     }
     __syncthreads();
@@ -238,7 +253,7 @@ Plan plan_of(const DeltaArgs& a, bool bf16) {
   p.cp = up(a.dv, deltak::kSlab);
   const int64_t wgs = a.batch * a.H * tiles_for(a.dv, true);
   int64_t want = std::min(kDeltaSlots / wgs, p.nch / kDeltaMinSegment);
-  if (want < 3) want = 1;  // a split costs a walk of its own, twice as wide
+  if (want < 6) want = 1;  // a split costs a walk of its own, twice as wide
   p.cps = cdiv(p.nch, want);
   p.nseg = cdiv(p.nch, p.cps);
   return p;
@@ -254,7 +269,8 @@ bool all_vec(const DeltaArgs& a, bool bf16) {
          vec16(a.v, a.v_b, a.v_t, es);
 }
 
-int64_t m_bytes(const DeltaArgs& a, const Plan& pl, bool bf16) {
+// M or P of every chunk
+int64_t square_bytes(const DeltaArgs& a, const Plan& pl) {
   return a.batch * a.H * pl.nch * pl.C * pl.C * 4;  // two parts of 2 bytes, or one of 4
 }
 
@@ -271,9 +287,9 @@ int64_t grad_heads(const DeltaArgs& a, const Plan& pl) {
 
 // Where the workspace's parts are, in bytes from its start.
 struct Space {
-  int64_t m, ss, rs, trans, s0, r1, r, e, pq, pk, total;
+  int64_t m, s, rates, ss, rs, trans, s0, r1, r, e, pq, pk, total;
 };
-Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
+Space space_of(const DeltaArgs& a, const Plan& pl, bool backward) {
   Space w{};
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -282,7 +298,9 @@ Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
     return r;
   };
   const int64_t bh = a.batch * a.H;
-  w.m = take(m_bytes(a, pl, bf16));
+  w.m = take(square_bytes(a, pl));
+  w.s = take(square_bytes(a, pl));
+  w.rates = take(bh * pl.nch * pl.C * deltak::kRates * 4);
   if (pl.nseg > 1) {
     w.ss = take(4 * bh * pl.nseg * pl.rp * pl.cp);
     w.trans = take(4 * bh * pl.nseg * pl.rp * pl.rp);
@@ -314,6 +332,8 @@ DeltaDev dev_of(const DeltaArgs& a, const Plan& pl, const Space& w, char* work, 
   d.g = static_cast<const char*>(a.g); d.beta = static_cast<const char*>(a.beta); d.lengths = a.lengths;
   d.h0 = a.h0; d.last = a.last;
   d.m = work + w.m;
+  d.s = work + w.s;
+  d.rates = reinterpret_cast<float*>(work + w.rates);
   d.seg_state = reinterpret_cast<float*>(work + w.ss);
   d.seg_trans = reinterpret_cast<float*>(work + w.trans);
   d.states = reinterpret_cast<float*>(work + w.s0);
@@ -332,27 +352,29 @@ hipError_t launch_pass(const DeltaDev& d, bool bf16, int pass, bool vec, hipStre
   return bf16 ? launch_delta_bf16(d, pass, wide, vec, st) : launch_delta_f32(d, pass, wide, vec, st);
 }
 
-hipError_t launch_carry(const DeltaDev& d, int rev, hipStream_t st) {
+hipError_t launch_carry(const DeltaDev& d, bool rev, hipStream_t st) {
   if (d.nseg <= 2) return hipSuccess;
-  hipLaunchKernelGGL(ssm_delta_carry_kernel, dim3(static_cast<unsigned>(d.cp / 16), static_cast<unsigned>(d.batch * d.H)),
-                     dim3(256), 0, st, d.seg_state, d.seg_trans, static_cast<int64_t>(d.nseg), d.rp, d.cp, rev);
+  auto kern = d.rp <= 128 ? (rev ? ssm_delta_carry_kernel<1, true> : ssm_delta_carry_kernel<1, false>)
+                          : (rev ? ssm_delta_carry_kernel<2, true> : ssm_delta_carry_kernel<2, false>);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(d.cp / 16), static_cast<unsigned>(d.batch * d.H)), dim3(512), 0, st,
+                     d.seg_state, d.seg_trans, d.nseg, d.rp, d.cp);
   return hipGetLastError();
 }
 
-// M of all chunks, and the states at the segments' ends
+// M, P and the decays of all chunks, and the states at the segments' ends
 hipError_t launch_start(const DeltaDev& d, bool bf16, bool vec, hipStream_t st) {
   hipError_t e = launch_pass(d, bf16, deltak::kPassPrep, vec, st);
   if (e != hipSuccess || d.nseg == 1) return e;
   DeltaDev s = d;
   s.ntile = d.nvt + static_cast<int>(cdiv(d.rp, wide_for(d.cols, vec) ? 128 : 64));
   e = launch_pass(s, bf16, deltak::kPassSeg, vec, st);
-  return e == hipSuccess ? launch_carry(d, 0, st) : e;
+  return e == hipSuccess ? launch_carry(d, false, st) : e;
 }
 
 }  // namespace
 
 int64_t delta_workspace_bytes(const DeltaArgs& a, bool bf16, bool backward) {
-  return space_of(a, plan_of(a, bf16), bf16, backward).total;
+  return space_of(a, plan_of(a, bf16), backward).total;
 }
 
 int64_t delta_workgroups(const DeltaArgs& a, bool bf16, bool backward) {
@@ -364,7 +386,7 @@ int64_t delta_workgroups(const DeltaArgs& a, bool bf16, bool backward) {
 hipError_t launch_delta_fwd(const DeltaArgs& a, bool bf16, char* work, hipStream_t st) {
   const Plan pl = plan_of(a, bf16);
   const bool vec = all_vec(a, bf16);
-  const DeltaDev d = dev_of(a, pl, space_of(a, pl, bf16, false), work, bf16, vec);
+  const DeltaDev d = dev_of(a, pl, space_of(a, pl, false), work, bf16, vec);
   const hipError_t e = launch_start(d, bf16, vec, st);
   return e == hipSuccess ? launch_pass(d, bf16, deltak::kPassOut, vec, st) : e;
 }
@@ -372,7 +394,7 @@ hipError_t launch_delta_fwd(const DeltaArgs& a, bool bf16, char* work, hipStream
 hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream_t st) {
   const Plan pl = plan_of(a, bf16);
   const bool vec = all_vec(a, bf16);
-  const Space w = space_of(a, pl, bf16, true);
+  const Space w = space_of(a, pl, true);
   const int64_t es = bf16 ? 2 : 4;
   DeltaDev d = dev_of(a, pl, w, work, bf16, vec);
   d.last = nullptr;
@@ -391,7 +413,7 @@ hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   r.res = reinterpret_cast<float*>(work + w.e);
   if (pl.nseg > 1) {
     e = launch_pass(r, bf16, deltak::kPassRevSeg, vec, st);
-    if (e == hipSuccess) e = launch_carry(r, 1, st);
+    if (e == hipSuccess) e = launch_carry(r, true, st);
     if (e != hipSuccess) return e;
   }
   e = launch_pass(r, bf16, deltak::kPassRev, vec, st);

@@ -19,8 +19,9 @@
 //   R_0 = e^{G_C} R_C + Q^T (scale e^G dO) - K^T (e^G b e)
 //
 // M needs neither the state nor b on its outside (b = 0 divides nothing) and is
-// the same in both directions: ssm_delta_prep_kernel makes it for all chunks at
-// once, and what is left of a chunk in the walk over the length is products.
+// the same in both directions: ssm_delta_prep_kernel makes it, P and the decays
+// for all chunks at once, and what is left of a chunk in the walk over the
+// length is products.
 // With S_0 and R_C of every chunk kept, and r and e, the other gradients are
 // again all chunks at once (ssm_delta_grad_kernel):
 //
@@ -66,6 +67,8 @@ struct DeltaDev {
   const float* h0;             // state at the first token (backwards: after the last), nullable
   float* last;                 // state after the last token (backwards: at the first), nullable
   char* m;                     // -M of every chunk, [b][H][nch][parts][C][C]
+  char* s;                     // P of every chunk, as m
+  float* rates;                // [b][H][nch][kRates][C]
   float* seg_state;            // [b][H][nseg][rp][cp]
   float* seg_trans;            // [b][H][nseg][rp][rp]: what a segment makes of the state before it
   float* states;               // [b][H][nch][rp][cp]: the state before (backwards: after) every chunk
@@ -128,6 +131,16 @@ __device__ __forceinline__ uint4 frag_state_row(const char* tile, int base, int 
   }
 }
 
+// The order of what lies between two scheduling barriers: N matrix instructions with V vector instructions after each
+template <int N, int V>
+__device__ __forceinline__ void mix() {
+  if constexpr (N > 0) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
+    mix<N - 1, V>();
+  }
+}
+
 // Accumulator tile and register of value e of operand step s
 template <typename IO>
 __device__ __forceinline__ constexpr int tile_of(int s, int e) { return s * (HeadCfg<IO>::E / 4) + (e >> 2); }
@@ -165,12 +178,9 @@ struct Tile {
     const int row = tid / N, c = tid % N;
     const int left = C * N % T == 0 || row < C ? width - c * HeadCfg<IO>::E : 0;
     const uint32_t off = row * ts + c * 16;
+    const Rsrc r = make_rsrc(base + static_cast<int64_t>(t0) * ts, row_bytes(len - t0, C, ts));
 #pragma unroll
-    for (int i = 0; i < CNT; ++i) {
-      const int r0 = STEP * i;
-      const Rsrc r = make_rsrc(base + static_cast<int64_t>(t0 + r0) * ts, row_bytes(len - t0 - r0, C, ts));
-      reg[i] = load16<IO, VEC>(r, off, left);
-    }
+    for (int i = 0; i < CNT; ++i) reg[i] = load16<IO, VEC>(r, off + STEP * i * ts, left);
   }
   static __device__ __forceinline__ void store(char* tile, int tid, const uint4* reg) {
     const int row = tid / N, c = tid % N;
@@ -178,13 +188,58 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < CNT; ++i) {
       const int r = row + STEP * i;
-      *reinterpret_cast<uint4*>(tile + 16 * (N * r + (c ^ swz<IO, N>(r)))) = reg[i];
+      *reinterpret_cast<uint4*>(tile + 16 * (N * r + (c ^ swz<IO, N>(STEP % 16 == 0 ? row : r)))) = reg[i];
     }
   }
 };
 
-// A chunk's decays and b, one token a lane of one wavefront: asked for, then scanned and written
-// to LDS.  A token past the length has neither decay nor b.
+// BYTES as they stand, dealt to T threads
+template <int BYTES, int T>
+struct Flat {
+  static constexpr int CNT = (BYTES / 16 + T - 1) / T;
+  static __device__ __forceinline__ void load(const char* base, int tid, uint4* reg) {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) {
+      const int at = tid + i * T;
+      reg[i] = make_uint4(0, 0, 0, 0);
+      if (at < BYTES / 16) reg[i] = reinterpret_cast<const uint4*>(base)[at];
+    }
+  }
+  static __device__ __forceinline__ void store(char* to, int tid, const uint4* reg) {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i)
+      if (tid + i * T < BYTES / 16) reinterpret_cast<uint4*>(to)[tid + i * T] = reg[i];
+  }
+};
+
+// A chunk's M or P, all parts: BYTES of 16-byte chunks, rows of N of them, dealt to T threads
+template <typename IO, int BYTES, int N, int T>
+struct TileM {
+  static constexpr int CNT = (BYTES / 16 + T - 1) / T;
+  static __device__ __forceinline__ void load(const char* base, int tid, uint4* reg) {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) {
+      const int at = tid + i * T;
+      reg[i] = make_uint4(0, 0, 0, 0);
+      if (BYTES / 16 % T == 0 || at < BYTES / 16) reg[i] = *reinterpret_cast<const uint4*>(base + 16 * at);
+    }
+  }
+  static __device__ __forceinline__ void store(char* tile, int tid, const uint4* reg) {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) {
+      const int at = tid + i * T, r = at / N;
+      if (BYTES / 16 % T == 0 || at < BYTES / 16)
+        *reinterpret_cast<uint4*>(tile + 16 * (N * r + (at % N ^ swz<IO, N>(T / N % 16 == 0 ? tid / N : r)))) = reg[i];
+    }
+  }
+};
+
+// What is kept of a chunk's decays and b, a row of C floats each: G_i as a pair (log2 units), e^{G_i}, e^{G_C - G_i},
+// b_i, and 1 where the state starts anew.
+enum { kGHi, kGLo, kEk, kWe, kBeta, kAnew, kRates };
+
+// A chunk's decays and b, one token a lane of one wavefront: asked for, then scanned.  A token past the length has
+// neither decay nor b.
 template <typename IO>
 struct Rates {
   static constexpr int C = HeadCfg<IO>::C, ES = HeadCfg<IO>::ES;
@@ -219,89 +274,149 @@ __device__ __forceinline__ int length_of(const DeltaDev& p, int b) {
 
 // ---------------------------------------------------------------- M of every chunk
 
-template <typename IO, int ROWS>
+template <typename IO, int ROWS, bool QUERY>
 constexpr size_t prep_lds_bytes() {
   using K = HeadCfg<IO>;
-  return size_t(K::C) * ROWS * K::ES + size_t(K::C) * (K::C + 4) * 4 + size_t(K::C / 16) * 16 * 20 * 4 + 3 * K::C * 4;
+  constexpr size_t tiles = (QUERY ? 2 : 1) * size_t(K::C) * ROWS * K::ES;
+  constexpr size_t square = size_t(K::C) * (K::C + 4) * 4 + size_t(K::C / 16) * 16 * 20 * 4;
+  return kRates * K::C * 4 + (tiles > square ? tiles : square);
 }
 
-// One (batch row, head, chunk) a workgroup of four wavefronts.  N on the matrix
-// cores; the 16 x 16 blocks on the diagonal of I + N diag(b) inverted by
-// substitution, a column a lane; then, a block column a wavefront, by block rows
+// Score tiles, 16 x 16 on and below the diagonal, dealt to wavefronts
+template <int IB>
+__device__ __forceinline__ void score_tile(int tile, int& ib, int& jb) {
+  ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6);
+  jb = tile - ib * (ib + 1) / 2;
+}
+
+// A float32 matrix [C][LD] in LDS to global memory as parts, whole and coalesced
+template <typename IO, int LD, int T>
+__device__ __forceinline__ void store_parts(const float* n, char* dst, int tid) {
+  using K = HeadCfg<IO>;
+  constexpr int PARTS = DeltaCfg<IO>::PAIR, C = K::C, E = K::E;
+  for (int i = tid; i < C * C / E; i += T) {
+    const int r = i / (C / E), c = i % (C / E) * E;
+    float v[E];
+    F32::ld<E>(n + r * LD + c, v);
+    uint4 w[PARTS];
+    split<IO, PARTS>(v, w);
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q) *reinterpret_cast<uint4*>(dst + q * C * C * K::ES + 16 * i) = w[q];
+  }
+}
+
+// One (batch row, head, chunk) a workgroup of four wavefronts.  N (and P) on the
+// matrix cores; the 16 x 16 blocks on the diagonal of I + N diag(b) inverted by
+// substitution, all of them by one wavefront, a block a group of 16 lanes and a
+// column a lane; then, a block column a wavefront, by block rows
 //   M_IK = (I + N_II b_I)^-1 (N_IK - sum_{K <= J < I} N_IJ b_J M_JK)
 // in float32 matrix instructions, the tiles M_JK staying in registers.
 // (Substitution, not powers of N b: keys alike make those grow past float32
 // where the inverse does not.)
-template <typename IO, int ROWS, bool VEC>
+template <typename IO, int ROWS, bool QUERY, bool VEC>
 __global__ void __launch_bounds__(256) ssm_delta_prep_kernel(const DeltaDev p) {
   using K = HeadCfg<IO>;
-  constexpr int ES = K::ES, E = K::E, C = K::C, T = 256, IB = C / 16, NK = ROWS * ES / 16, RS = ROWS / K::KS;
-  constexpr int LD = C + 4;
+  constexpr int ES = K::ES, C = K::C, T = 256, IB = C / 16, NK = ROWS * ES / 16, RS = ROWS / K::KS;
+  constexpr int LD = C + 4, TILES = IB * (IB + 1) / 2, MINE = (TILES + 3) / 4, MB = DeltaCfg<IO>::PAIR * C * C * ES;
+  using TK = Tile<IO, NK, T>;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  char* const ty = lds;
-  float* const n = reinterpret_cast<float*>(ty + C * ROWS * ES);  // [C][LD]
-  float* const inv = n + C * LD;                                  // [IB][16][20]
-  float* const ghi = inv + IB * 16 * 20;
-  float* const glo = ghi + C;
-  float* const bt = glo + C;
+  float* const rt = reinterpret_cast<float*>(lds);  // [kRates][C]
+  char* const ty = reinterpret_cast<char*>(rt + kRates * C);
+  char* const tx = ty + C * ROWS * ES;
+  // in the place of the tiles once the scores are there: with half the LDS twice the workgroups share a CU
+  float* const n = reinterpret_cast<float*>(ty);    // [C][LD]: N, then M, then P
+  float* const inv = n + C * LD;                    // [IB][16][20]
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int pc = blockIdx.x % p.nch, bh = blockIdx.x / p.nch, h = bh % p.H, b = bh / p.H, t0 = pc * C;
   const int len = length_of(p, b);
   if (t0 >= len) return;
+  const int64_t chunk = static_cast<int64_t>(bh) * p.nch + pc;
 
-  uint4 ry[Tile<IO, NK, T>::CNT];
+  uint4 ry[TK::CNT], rx[QUERY ? TK::CNT : 1];
   Rates<IO> rates;
   if (wave == 3) rates.load(p, b, h, t0, len, lane);
-  Tile<IO, NK, T>::template load<VEC>(p.k + b * p.k_b + static_cast<int64_t>(h / p.rep) * p.rows * ES, p.k_t, t0, len, p.rows,
-                                      tid, ry);
+  TK::template load<VEC>(p.k + b * p.k_b + static_cast<int64_t>(h / p.rep) * p.rows * ES, p.k_t, t0, len, p.rows, tid, ry);
+  if constexpr (QUERY)
+    TK::template load<VEC>(p.q + b * p.q_b + static_cast<int64_t>(h / p.rep) * p.rows * ES, p.q_t, t0, len, p.rows, tid, rx);
   if (wave == 3) {
     float hi, lo;
     rates.scan(hi, lo);
+    const float eh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hi), C - 1));
+    const float el = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lo), C - 1));
     if (lane < C) {
-      ghi[lane] = hi;
-      glo[lane] = lo;
-      bt[lane] = rates.beta(p, t0, len, lane);
+      rt[kGHi * C + lane] = hi;
+      rt[kGLo * C + lane] = lo;
+      rt[kEk * C + lane] = __builtin_amdgcn_exp2f(hi + lo);
+      rt[kWe * C + lane] = __builtin_amdgcn_exp2f((eh - hi) + (el - lo));
+      rt[kBeta * C + lane] = rates.beta(p, t0, len, lane);
+      rt[kAnew * C + lane] = clamp_decay(Rates<IO>::value(rates.raw_g) * kLog2e) == kMinLog2Decay ? 1.f : 0.f;
     }
   }
-  Tile<IO, NK, T>::store(ty, tid, ry);
+  TK::store(ty, tid, ry);
+  if constexpr (QUERY) TK::store(tx, tid, rx);
   __syncthreads();
+  if (tid < kRates * C / 4)
+    reinterpret_cast<float4*>(p.rates + chunk * kRates * C)[tid] = reinterpret_cast<const float4*>(rt)[tid];
 
+  // lane holds j = 4 g + v of i = li
   const int rb = lane_base<IO, NK>(li, g);
-  for (int tile = wave; tile < IB * (IB + 1) / 2; tile += 4) {
-    const int ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6), jb = tile - ib * (ib + 1) / 2;
-    const int i = 16 * ib + li, j0 = 16 * jb + 4 * g;
-    f32x4 a = {0.f, 0.f, 0.f, 0.f};
+  f32x4 sc[MINE], sq[MINE];
 #pragma unroll
-    for (int s = 0; s < RS; ++s) a = mma<IO>(frag_row<NK>(ty, rb, jb, s), frag_row<NK>(ty, rb, ib, s), a);
-    const float gi = ghi[i], gl = glo[i];
-    float4 w;
-    float* pw = reinterpret_cast<float*>(&w);
+  for (int m = 0; m < MINE; ++m) {
+    const int tile = wave + 4 * m;
+    sc[m] = sq[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (tile >= TILES) continue;
+    int ib, jb;
+    score_tile<IB>(tile, ib, jb);
+    const int i = 16 * ib + li, j0 = 16 * jb + 4 * g;
+    f32x4 a = {0.f, 0.f, 0.f, 0.f}, c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+      const uint4 fy = frag_row<NK>(ty, rb, jb, s);
+      a = mma<IO>(fy, frag_row<NK>(ty, rb, ib, s), a);
+      if constexpr (QUERY) c = mma<IO>(fy, frag_row<NK>(tx, rb, ib, s), c);
+    }
+    const float gi = rt[kGHi * C + i], gl = rt[kGLo * C + i];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const float d = __builtin_amdgcn_exp2f((gi - ghi[j0 + v]) + (gl - glo[j0 + v]));
-      pw[v] = j0 + v < i ? times(d, a[v]) : 0.f;
+      const float d = __builtin_amdgcn_exp2f((gi - rt[kGHi * C + j0 + v]) + (gl - rt[kGLo * C + j0 + v]));
+      sc[m][v] = j0 + v < i ? times(d, a[v]) : 0.f;
+      if constexpr (QUERY) sq[m][v] = j0 + v <= i ? times(p.scale * d, c[v]) : 0.f;
     }
-    *reinterpret_cast<float4*>(n + i * LD + j0) = w;
   }
+  auto put_scores = [&](const f32x4 (&x)[MINE]) {
+#pragma unroll
+    for (int m = 0; m < MINE; ++m) {
+      const int tile = wave + 4 * m;
+      if (tile >= TILES) continue;
+      int ib, jb;
+      score_tile<IB>(tile, ib, jb);
+      *reinterpret_cast<f32x4*>(n + (16 * ib + li) * LD + 16 * jb + 4 * g) = x[m];
+    }
+  };
+  __syncthreads();
+  put_scores(sc);
   __syncthreads();
 
-  if (wave < IB) {
-    // column li of the inverse; the four lane groups work alike and write four rows each
+  if (wave == 0 && g < IB) {
+    // column li of block g's inverse, each value times its row's b as it is needed further down
+    const float* const nb = n + 16 * g * LD + 16 * g;
     float t[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float s = i == li ? 1.f : 0.f;
 #pragma unroll
-      for (int k = 0; k < i; ++k) s = __builtin_fmaf(-n[(16 * wave + i) * LD + 16 * wave + k] * bt[16 * wave + k], t[k], s);
-      t[i] = s;
-      if ((i >> 2) == g) inv[(wave * 16 + i) * 20 + li] = s;
+      for (int k = 0; k < i; ++k) s = __builtin_fmaf(-nb[i * LD + k], t[k], s);
+      inv[(g * 16 + i) * 20 + li] = s;
+      t[i] = s * rt[kBeta * C + 16 * g + i];
     }
   }
   __syncthreads();
 
   f32x4 M[IB];
   if (wave < IB) {
+    f32x4 mb[IB];  // -b M
 #pragma unroll
     for (int I = 0; I < IB; ++I) {
       M[I] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -312,13 +427,13 @@ __global__ void __launch_bounds__(256) ssm_delta_prep_kernel(const DeltaDev p) {
 #pragma unroll
       for (int J = 0; J < I; ++J) {
         if (J < wave) continue;
-        const float4 nn = *reinterpret_cast<const float4*>(n + (16 * I + li) * LD + 16 * J + 4 * g);
-        const float4 bb = *reinterpret_cast<const float4*>(bt + 16 * J + 4 * g);
-        const float4 f = make_float4(-nn.x * bb.x, -nn.y * bb.y, -nn.z * bb.z, -nn.w * bb.w);
-        a = mma<F32>(__builtin_bit_cast(uint4, f), __builtin_bit_cast(uint4, M[J]), a);
+        const float4 f = *reinterpret_cast<const float4*>(n + (16 * I + li) * LD + 16 * J + 4 * g);
+        a = mma<F32>(__builtin_bit_cast(uint4, f), __builtin_bit_cast(uint4, mb[J]), a);
       }
       const float4 f = *reinterpret_cast<const float4*>(inv + (I * 16 + li) * 20 + 4 * g);
       M[I] = mma<F32>(__builtin_bit_cast(uint4, f), __builtin_bit_cast(uint4, a), M[I]);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) mb[I][v] = -rt[kBeta * C + 16 * I + 4 * g + v] * M[I][v];
     }
   }
   __syncthreads();
@@ -329,16 +444,12 @@ __global__ void __launch_bounds__(256) ssm_delta_prep_kernel(const DeltaDev p) {
       for (int v = 0; v < 4; ++v) n[(16 * I + 4 * g + v) * LD + 16 * wave + li] = -M[I][v];
   }
   __syncthreads();
-  constexpr int PARTS = DeltaCfg<IO>::PAIR;
-  char* const dst = p.m + (static_cast<int64_t>(bh) * p.nch + pc) * (PARTS * C * C * ES);
-  for (int i = tid; i < C * C / E; i += T) {
-    const int r = i / (C / E), c = i % (C / E) * E;
-    float v[E];
-    F32::ld<E>(n + r * LD + c, v);
-    uint4 w[PARTS];
-    split<IO, PARTS>(v, w);
-#pragma unroll
-    for (int q = 0; q < PARTS; ++q) *reinterpret_cast<uint4*>(dst + q * C * C * ES + 16 * i) = w[q];
+  store_parts<IO, LD, T>(n, p.m + chunk * MB, tid);
+  if constexpr (QUERY) {
+    __syncthreads();
+    put_scores(sq);  // above the diagonal -M holds zeros, and so does P
+    __syncthreads();
+    store_parts<IO, LD, T>(n, p.s + chunk * MB, tid);
   }
 }
 
@@ -355,7 +466,7 @@ constexpr size_t delta_lds_bytes() {
   using K = HeadCfg<IO>;
   constexpr size_t xy = size_t(K::C) * ROWS * K::ES, z = size_t(K::C) * 16 * NW * K::ES;
   constexpr size_t sq = size_t(K::C) * K::C * K::ES * DeltaCfg<IO>::PAIR;
-  return xy + z + sq + 6 * K::C * 4 + (QUERY ? xy + sq : 0);
+  return xy + z + sq + kRates * K::C * 4 + (QUERY ? xy + sq : 0);
 }
 
 // Workgroups are dealt to the XCDs as the head scan's: the column tiles of a (batch row, head, segment) follow each
@@ -395,18 +506,22 @@ __device__ __forceinline__ void store_state(float* dst, int rows, int cols, int 
       if (r < rows && c < cols) dst[r * ld + c] = S[rt][v];
     }
 }
-// r or e of a chunk: rows of cp floats, all C of them
-template <typename IO, int TB>
-__device__ __forceinline__ void store_res(float* dst, int cp, int c, int g, const f32x4 (&X)[TB]) {
-  if (c >= cp) return;
+// Accumulator tiles to `rows` rows of cp floats in the workspace (a resource, which bounds the rows; none of it with
+// rows = 0), by instructions whose number does not depend on the sizes: loads and stores are counted together and in
+// order, and the wait for the next chunk's loads can leave these in flight only if their number is known.
+template <typename IO, int N>
+__device__ __forceinline__ void keep(float* dst, int rows, int cp, int c, int g, const f32x4 (&X)[N]) {
+  const Rsrc r = make_rsrc(dst, static_cast<uint32_t>(rows * cp * 4));
+  const uint32_t off = c < cp ? c * 4 : kOOB;
 #pragma unroll
-  for (int rt = 0; rt < TB; ++rt)
+  for (int rt = 0; rt < N; ++rt)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) dst[state_row<IO>(rt, g, v) * cp + c] = X[rt][v];
+    for (int v = 0; v < 4; ++v)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(X[rt][v]), r, off + state_row<IO>(rt, g, v) * cp * 4, 0, 0);
 }
 
 template <typename IO, int ROWS, int NW, int MODE, bool VEC>
-__global__ void __launch_bounds__((64 * NW), (NW == 8 || ROWS == 256 ? 2 : 3))
+__global__ void __launch_bounds__((64 * NW), 2)
 ssm_delta_kernel(const DeltaDev p) {
   using K = HeadCfg<IO>;
   constexpr bool QUERY = MODE == kDeltaOut;
@@ -414,21 +529,21 @@ ssm_delta_kernel(const DeltaDev p) {
   constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
   constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
   constexpr int PS = DeltaCfg<IO>::STATE, PP = DeltaCfg<IO>::PAIR;
-  constexpr int MB = PP * C * C * ES, LM = (MB / 16 + T - 1) / T;  // bytes of a chunk's M, 16-byte chunks a thread
+  constexpr int MB = PP * C * C * ES;  // bytes of a chunk's M
   using TK = Tile<IO, NK, T>;
   using TZ = Tile<IO, NZ, T>;
+  using TM = TileM<IO, MB, NP, T>;
+  using TR = Flat<kRates * C * 4, T>;
 
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char* const ty = lds;
   char* const tz = ty + C * ROWS * ES;
   char* const tm = tz + C * COLS * ES;
-  float* const ghi = reinterpret_cast<float*>(tm + MB);
-  float* const glo = ghi + C;
-  float* const ek = glo + C;  // e^{G_i}
-  float* const we = ek + C;   // e^{G_C - G_i}
-  float* const bt = we + C;   // b
-  float* const eo = bt + C;   // scale e^{G_i}
-  char* const tx = reinterpret_cast<char*>(eo + C);
+  float* const rt = reinterpret_cast<float*>(tm + MB);  // [kRates][C]
+  const float* const ek = rt + kEk * C;
+  const float* const we = rt + kWe * C;
+  const float* const bt = rt + kBeta * C;
+  char* const tx = reinterpret_cast<char*>(rt + kRates * C);
   char* const tp = tx + C * ROWS * ES;
 
   const int tid = static_cast<int>(threadIdx.x);
@@ -459,60 +574,72 @@ ssm_delta_kernel(const DeltaDev p) {
       load_state<IO, RT>(MODE == kDeltaSeg ? nullptr : p.seg_state + (bh * p.nseg + seg - 1) * wsize, p.rp, p.cp, p.cp, c, g, S);
     }
   }
-  if constexpr (QUERY) {
-    // the score tiles above the diagonal that a product step covers are never written again
-    for (int i = tid; i < MB / 16; i += T) reinterpret_cast<uint4*>(tp)[i] = make_uint4(0, 0, 0, 0);
-  }
-
   const char* const xb = p.q + b * p.q_b + static_cast<int64_t>(h / p.rep) * p.rows * ES;
   const char* const yb = p.k + b * p.k_b + static_cast<int64_t>(h / p.rep) * p.rows * ES;
   const char* const zb = p.v + b * p.v_b + (static_cast<int64_t>(h) * p.cols + col0) * ES;
-  const char* const mb = p.m + bh * p.nch * MB;
 
-  uint4 rx[TK::CNT], ry[TK::CNT], rz[TZ::CNT], rm[LM];
-  Rates<IO> rates;
+  uint4 rx[TK::CNT], ry[TK::CNT], rz[TZ::CNT], rm[TM::CNT], rp[TM::CNT], rr[TR::CNT];
   auto load_chunk = [&](int pc) {
-    const int t0 = pc * C, me = opaque(tid);
-    rates.load(p, b, h, t0, len, me & 63);
+    const int t0 = pc * C, me = ROWS == 256 || !VEC ? opaque(tid) : tid;
+    const int64_t chunk = bh * p.nch + pc;
     TK::template load<VEC>(yb, p.k_t, t0, len, p.rows, me, ry);
-#pragma unroll
-    for (int i = 0; i < LM; ++i)
-      if (MB / 16 % T == 0 || me < MB / 16)
-        rm[i] = *reinterpret_cast<const uint4*>(mb + static_cast<int64_t>(pc) * MB + 16 * (me + i * T));
+    TR::load(reinterpret_cast<const char*>(p.rates + chunk * kRates * C), me, rr);
     if (!trans) TZ::template load<VEC>(zb, p.v_t, t0, len, p.cols - col0, me, rz);
-    if constexpr (QUERY) TK::template load<VEC>(xb, p.q_t, t0, len, p.rows, me, rx);
+    TM::load(p.m + chunk * MB, me, rm);
+  };
+  // these are asked for half a chunk later: with them the registers do not hold the products' operands
+  auto load_queries = [&](int pc) {
+    const int t0 = pc * C, me = ROWS == 256 || !VEC ? opaque(tid) : tid;
+    TK::template load<VEC>(xb, p.q_t, t0, len, p.rows, me, rx);
+    TM::load(p.s + (bh * p.nch + pc) * MB, me, rp);
+  };
+
+  // A chunk's outputs: lane holds columns cw + 4 g + v of token 16 ib + li; nothing is written with rows = 0.
+  auto store_out = [&](const f32x4 (&O)[IB], int t0, int rows, int li, int g) {
+    const uint32_t ts = static_cast<uint32_t>(p.H * p.cols * ES);
+    const char* const ob = p.o + ((static_cast<int64_t>(b) * p.L + t0) * p.H + h) * p.cols * ES;
+    const Rsrc ro = make_rsrc(ob, row_bytes(rows, C, ts));
+    const int c = cw + 4 * g;
+    const uint32_t off = li * ts + static_cast<uint32_t>(c * ES);
+#pragma unroll
+    for (int ib = 0; ib < IB; ++ib) {
+      const float w[4] = {O[ib][0], O[ib][1], O[ib][2], O[ib][3]};
+      const uint32_t at = off + 16 * ib * ts;
+      if constexpr (VEC) {
+        BufOf<IO>::type::template st<4>(ro, c < p.cols ? at : kOOB, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) BufOf<IO>::type::template st<1>(ro, c + e < p.cols ? at + e * ES : kOOB, w + e);
+      }
+    }
   };
 
   const int cl = (len + C - 1) / C, ce = c1 < cl ? c1 : cl, nc = ce - c0;
-  if (nc > 0) load_chunk(c0);
+  if (nc > 0) {
+    load_chunk(c0);
+    if constexpr (QUERY) load_queries(c0);
+    // as many stores behind the first loads as the loop has behind its own (see keep)
+    const f32x4 none[RT > IB ? RT : IB] = {};
+    const int li = tid & 15, g = (tid & 63) >> 4;
+    if constexpr (QUERY) {
+      store_out(reinterpret_cast<const f32x4(&)[IB]>(none), 0, 0, li, g);
+    } else if constexpr (MODE == kDeltaStates) {
+      keep<IO, RT>(p.states, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
+      keep<IO, IB>(p.res, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
+    }
+  }
   for (int kk = 0; kk < nc; ++kk) {
     const int pc = c0 + kk, t0 = pc * C;
     __syncthreads();  // the chunk before is done with the tiles
     {
-      const int me = opaque(tid);
+      const int me = ROWS == 256 || !VEC ? opaque(tid) : tid;
       TK::store(ty, me, ry);
       if (!trans) TZ::store(tz, me, rz);
-      if constexpr (QUERY) TK::store(tx, me, rx);
-#pragma unroll
-      for (int i = 0; i < LM; ++i) {
-        const int at = me + i * T, r = at / NP;  // rows of both parts follow each other
-        if (MB / 16 % T == 0 || at < MB / 16) *reinterpret_cast<uint4*>(tm + 16 * (NP * r + (at % NP ^ swz<IO, NP>(r)))) = rm[i];
-      }
-    }
-    if (wave == NW - 1) {
-      float hi, lo;
-      rates.scan(hi, lo);
-      const float eh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hi), C - 1));
-      const float el = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lo), C - 1));
-      const int lane = tid & 63;
-      if (lane < C) {
-        const float e = __builtin_amdgcn_exp2f(hi + lo);
-        ghi[lane] = hi;
-        glo[lane] = lo;
-        ek[lane] = e;
-        eo[lane] = p.scale * e;
-        we[lane] = __builtin_amdgcn_exp2f((eh - hi) + (el - lo));
-        bt[lane] = rates.beta(p, t0, len, lane);
+      TM::store(tm, me, rm);
+      TR::store(reinterpret_cast<char*>(rt), me, rr);
+      if constexpr (QUERY) {
+        TK::store(tx, me, rx);
+        TM::store(tp, me, rp);
       }
     }
     __syncthreads();
@@ -521,157 +648,176 @@ ssm_delta_kernel(const DeltaDev p) {
     if (kk + 1 < nc) load_chunk(pc + 1);
 
     if constexpr (MODE == kDeltaStates)
-      store_state<IO, RT>(p.states + (bh * p.nch + pc) * wsize, p.rp, p.cp, p.cp, cw + li, g, S);
+      keep<IO, RT>(p.states + (bh * p.nch + pc) * wsize, p.rp, p.cp, cw + li, g, S);
 
-    if constexpr (QUERY) {
-      // ---- scores, 16 x 16 tiles on and below the diagonal dealt to the wavefronts: lane holds j = 4 g + v of i = li
-      const int rb = lane_base<IO, NK>(li, g);
-      for (int tile = wave; tile < IB * (IB + 1) / 2; tile += NW) {
-        const int ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6), jb = tile - ib * (ib + 1) / 2;
-        const int i = 16 * ib + li, j0 = 16 * jb + 4 * g;
-        f32x4 a = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < RS; ++s) a = mma<IO>(frag_row<NK>(ty, rb, jb, s), frag_row<NK>(tx, rb, ib, s), a);
-        const float gi = ghi[i], gl = glo[i];
-        const float4 gj = *reinterpret_cast<const float4*>(ghi + j0), gk = *reinterpret_cast<const float4*>(glo + j0);
-        float w[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float d = __builtin_amdgcn_exp2f((gi - get(gj, v)) + (gl - get(gk, v)));
-          w[v] = j0 + v <= i ? times(p.scale * d, a[v]) : 0.f;
-        }
-        if constexpr (ES == 2) {
-          const int u = 4 * jb + g;
-          const int to = (i * NP + ((u >> 1) ^ swz<IO, NP>(i))) * 16 + (u & 1) * 8;
-          const uint2 hi2 = make_uint2(BF16::cvt2(w[0], w[1]), BF16::cvt2(w[2], w[3]));
-          *reinterpret_cast<uint2*>(tp + to) = hi2;
-          *reinterpret_cast<uint2*>(tp + C * C * ES + to) =
-              make_uint2(BF16::cvt2(w[0] - bf_lo(hi2.x), w[1] - bf_hi(hi2.x)),
-                         BF16::cvt2(w[2] - bf_lo(hi2.y), w[3] - bf_hi(hi2.y)));
-        } else {
-          *reinterpret_cast<float4*>(tp + (i * NP + ((4 * jb + g) ^ swz<IO, NP>(i))) * 16) = make_float4(w[0], w[1], w[2], w[3]);
-        }
-      }
-    }
-
-    // ---- what the state before the chunk gives: X = K S (rows are tokens, by state_row), O = Q S (transposed)
+    // ---- what the state before the chunk gives: X = K S (rows are tokens, by state_row), O = Q S (transposed).  The
+    // operands of step s + 1 are read and split under the matrix instructions of step s.
     f32x4 X[IB], O[IB];
 #pragma unroll
     for (int i = 0; i < IB; ++i) X[i] = O[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    uint4 fz[JS];
+    float e[JS][E];
     {
-      const int sb = opaque(state_row_base<IO, NK>(li, g)), qb = opaque(lane_base<IO, NK>(li, g));
+      const int sb = state_row_base<IO, NK>(li, g), qb = lane_base<IO, NK>(li, g), zb0 = col_base<IO, NZ>(li, g);
+      uint4 fk[IB], fq[QUERY ? IB : 1], sp[2][PS];
+      auto read_keys = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < IB; ++i) fk[i] = frag_state_row<IO, NK>(ty, sb, i, s);
+      };
+      auto parts = [&](int s) {
+        float v[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = S[tile_of<IO>(s, i)][i & 3];
+        split<IO, PS>(v, sp[s & 1]);
+      };
+      read_keys(0);
+      parts(0);
 #pragma unroll
       for (int s = 0; s < RS; ++s) {
-        float v[E];
-        uint4 sp[PS];
+        if constexpr (QUERY) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = S[tile_of<IO>(s, e)][e & 3];
-        split<IO, PS>(v, sp);
+          for (int i = 0; i < IB; ++i) fq[i] = frag_row<NK>(tx, qb, i, s);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + 1 < RS) parts(s + 1);
 #pragma unroll
-        for (int i = 0; i < IB; ++i) {
-          const uint4 fk = frag_state_row<IO, NK>(ty, sb, i, s);
+        for (int q = 0; q < PS; ++q)
 #pragma unroll
-          for (int q = 0; q < PS; ++q) X[i] = mma<IO>(fk, sp[q], X[i]);
-          if constexpr (QUERY) {
-            const uint4 fq = frag_row<NK>(tx, qb, i, s);
+          for (int i = 0; i < IB; ++i) X[i] = mma<IO>(fk[i], sp[s & 1][q], X[i]);
+        mix<IB * PS, 4>();
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + 1 < RS) {
+          read_keys(s + 1);
+        } else {
 #pragma unroll
-            for (int q = 0; q < PP; ++q) O[i] = mma<IO>(sp[q], fq, O[i]);
+          for (int js = 0; js < JS; ++js) {
+            if (!trans) fz[js] = frag_col<IO, NZ>(tz, zb0, wave, js);
+            F32::ld<E>(ek + KS * js + E * g, e[js]);
           }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (QUERY) {
+#pragma unroll
+          for (int q = 0; q < PP; ++q)
+#pragma unroll
+            for (int i = 0; i < IB; ++i) O[i] = mma<IO>(sp[s & 1][q], fq[i], O[i]);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
     // ---- x, then r = x - M (b x)
-    uint4 bx[JS][PP];
-    const int zb0 = opaque(col_base<IO, NZ>(li, g));
+    constexpr int LOW = IB == 2 ? 3 : 6;  // operand steps on and below the diagonal
+    uint4 bx[JS][PS], fm[LOW];
+    const int mb0 = state_row_base<IO, NP>(li, g);
+#pragma unroll
+    for (int i = 0, n = 0; i < IB; ++i)
+#pragma unroll
+      for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) fm[n] = frag_state_row<IO, NP>(tm, mb0, i, js);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int js = 0; js < JS; ++js) {
-      float e[E], bb[E], v[E] = {};
-      F32::ld<E>(ek + KS * js + E * g, e);
+      float v[E] = {}, bb[E];
       F32::ld<E>(bt + KS * js + E * g, bb);
-      if (!trans) unpack<IO>(frag_col<IO, NZ>(tz, zb0, wave, js), v);
+      if (!trans) unpack<IO>(fz[js], v);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const int t = tile_of<IO>(js, i);
-        v[i] -= times(e[i], X[t][i & 3]);
+        v[i] -= times(e[js][i], X[t][i & 3]);
         X[t][i & 3] = v[i];
         v[i] *= bb[i];
       }
-      split<IO, PP>(v, bx[js]);
+      split<IO, PS>(v, bx[js]);
     }
-    const int mb0 = opaque(state_row_base<IO, NP>(li, g));
+    uint4 fl[LOW];
+    if constexpr (PP == 2) {
 #pragma unroll
-    for (int i = 0; i < IB; ++i)
+      for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
-      for (int js = 0; js * KS < 16 * (i + 1); ++js) {
-        const uint4 fm = frag_state_row<IO, NP>(tm, mb0, i, js);
+        for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) fl[n] = frag_state_row<IO, NP>(tm + C * C * ES, mb0, i, js);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int q = 0; q < PP; ++q) X[i] = mma<IO>(fm, bx[js][q], X[i]);
-        if constexpr (PP == 2) X[i] = mma<IO>(frag_state_row<IO, NP>(tm + C * C * ES, mb0, i, js), bx[js][0], X[i]);
-      }
+    for (int rt = 0; rt < RT; ++rt) scale(S[rt], end_dec);
+    if constexpr (QUERY) {
+#pragma unroll
+      for (int ib = 0; ib < IB; ++ib) scale(O[ib], p.scale * ek[16 * ib + li]);
+    }
+#pragma unroll
+    for (int q = 0; q < PS + (PP == 2 ? 2 : 0); ++q)
+#pragma unroll
+      for (int i = 0, n = 0; i < IB; ++i)
+#pragma unroll
+        for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n)
+          X[i] = q < PS ? mma<IO>(fm[n], bx[js][q], X[i]) : mma<IO>(fl[n], bx[js][q - PS], X[i]);
+    mix<LOW * (PS + (PP == 2 ? 2 : 0)), 2>();
+    __builtin_amdgcn_sched_barrier(0);
+    if (QUERY && kk + 1 < nc) load_queries(pc + 1);
+    const int pb = lane_base<IO, NP>(li, g);
+    if constexpr (QUERY) {
+#pragma unroll
+      for (int i = 0, n = 0; i < IB; ++i)
+#pragma unroll
+        for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) fm[n] = frag_row<NP>(tp, pb, i, js);
+    }
+    __builtin_amdgcn_sched_barrier(0);
     if constexpr (MODE == kDeltaStates)
-      store_res<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp, p.cp, cw + li, g, X);
+      keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp, C, p.cp, cw + li, g, X);
 
     // ---- u = b r as an operand of o, e^{G_C - G} u as one of the state's update
+    const int yb0 = state_col_base<IO, NK>(li, g);
     uint4 fu[JS][PP], fw[JS][PS];
 #pragma unroll
     for (int js = 0; js < JS; ++js) {
-      float bb[E], w[E], v[E];
-      F32::ld<E>(bt + KS * js + E * g, bb);
+      float v[E], w[E];
       F32::ld<E>(we + KS * js + E * g, w);
+      F32::ld<E>(bt + KS * js + E * g, v);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        v[i] = bb[i] * X[tile_of<IO>(js, i)][i & 3];
+        v[i] *= X[tile_of<IO>(js, i)][i & 3];
         w[i] = times(w[i], v[i]);
       }
       if constexpr (QUERY) split<IO, PP>(v, fu[js]);
       split<IO, PS>(w, fw[js]);
     }
+    uint4 fy[2][JS];
+#pragma unroll
+    for (int js = 0; js < JS; ++js) fy[0][js] = frag_state_col<IO, NK>(ty, yb0, 0, js);
     if constexpr (QUERY) {
+      if constexpr (PP == 2) {
 #pragma unroll
-      for (int ib = 0; ib < IB; ++ib) scale(O[ib], eo[16 * ib + li]);
-      __syncthreads();  // scores
-      const int pb = opaque(lane_base<IO, NP>(li, g));
+        for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
-      for (int ib = 0; ib < IB; ++ib)
+          for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) fl[n] = frag_row<NP>(tp + C * C * ES, pb, i, js);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int js = 0; js * KS < 16 * (ib + 1); ++js) {
-          const uint4 fp = frag_row<NP>(tp, pb, ib, js);
+      for (int q = 0; q < 2 * PP - 1; ++q)
 #pragma unroll
-          for (int q = 0; q < PP; ++q) O[ib] = mma<IO>(fu[js][q], fp, O[ib]);
-          if constexpr (PP == 2) O[ib] = mma<IO>(fu[js][0], frag_row<NP>(tp + C * C * ES, pb, ib, js), O[ib]);
-        }
+        for (int i = 0, n = 0; i < IB; ++i)
+#pragma unroll
+          for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n)
+            O[i] = q < PP ? mma<IO>(fu[js][q], fm[n], O[i]) : mma<IO>(fu[js][0], fl[n], O[i]);
     }
     // ---- the state after the chunk
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) scale(S[rt], end_dec);
-    const int yb0 = opaque(state_col_base<IO, NK>(li, g));
+    for (int rt = 0; rt < RT; ++rt) {
+      if (rt + 1 < RT) {
 #pragma unroll
-    for (int js = 0; js < JS; ++js)
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const uint4 fy = frag_state_col<IO, NK>(ty, yb0, rt, js);
-#pragma unroll
-        for (int q = 0; q < PS; ++q) S[rt] = mma<IO>(fy, fw[js][q], S[rt]);
+        for (int js = 0; js < JS; ++js) fy[(rt + 1) & 1][js] = frag_state_col<IO, NK>(ty, yb0, rt + 1, js);
       }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int js = 0; js < JS; ++js)
+#pragma unroll
+        for (int q = 0; q < PS; ++q) S[rt] = mma<IO>(fy[rt & 1][js], fw[js][q], S[rt]);
+    }
 
-    // ---- outputs, zero in rows past the length: lane holds columns cw + 4 g + v of token 16 ib + li
+    // ---- outputs, zero in rows past the length
     if constexpr (QUERY) {
-      const uint32_t ts = static_cast<uint32_t>(p.H * p.cols * ES);
-      const char* const ob = p.o + ((static_cast<int64_t>(b) * p.L + t0) * p.H + h) * p.cols * ES;
-      const int c = cw + 4 * g;
 #pragma unroll
-      for (int ib = 0; ib < IB; ++ib) {
-        const Rsrc ro = make_rsrc(ob + static_cast<int64_t>(16 * ib) * ts, row_bytes(p.L - t0 - 16 * ib, 16, ts));
+      for (int ib = 0; ib < IB; ++ib)
         if (t0 + 16 * ib + li >= len) O[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const float w[4] = {O[ib][0], O[ib][1], O[ib][2], O[ib][3]};
-        const uint32_t off = li * ts + static_cast<uint32_t>(c * ES);
-        if constexpr (VEC) {
-          BufOf<IO>::type::template st<4>(ro, c < p.cols ? off : kOOB, w);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) BufOf<IO>::type::template st<1>(ro, c + e < p.cols ? off + e * ES : kOOB, w + e);
-        }
-      }
+      store_out(O, t0, p.L - t0, li, g);
     }
   }
 
@@ -703,29 +849,29 @@ constexpr size_t delta_rev_lds_bytes() { return delta_lds_bytes<IO, ROWS, NW, tr
 // v is dO, h0 dlast, last dh0.  SEG: a segment's own R at its first token, from zero (the last segment: from dlast);
 // else R after every chunk and e are written.
 template <typename IO, int ROWS, int NW, bool SEG, bool VEC>
-__global__ void __launch_bounds__((64 * NW), (NW == 8 || ROWS == 256 ? 2 : 3))
+__global__ void __launch_bounds__((64 * NW), 2)
 ssm_delta_rev_kernel(const DeltaDev p) {
   using K = HeadCfg<IO>;
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
   constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
   constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
   constexpr int PS = DeltaCfg<IO>::STATE, PP = DeltaCfg<IO>::PAIR;
-  constexpr int MB = PP * C * C * ES, LM = (MB / 16 + T - 1) / T;
+  constexpr int MB = PP * C * C * ES;
   using TK = Tile<IO, NK, T>;
   using TZ = Tile<IO, NZ, T>;
+  using TM = TileM<IO, MB, NP, T>;
+  using TR = Flat<kRates * C * 4, T>;
 
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char* const ty = lds;
   char* const tz = ty + C * ROWS * ES;
   char* const tm = tz + C * COLS * ES;
-  float* const ghi = reinterpret_cast<float*>(tm + MB);
-  float* const glo = ghi + C;
-  float* const ek = glo + C;
-  float* const we = ek + C;
-  float* const bt = we + C;
-  float* const eo = bt + C;
-  char* const tx = reinterpret_cast<char*>(eo + C);
-  char* const tp = tx + C * ROWS * ES;  // P^T: rows are the keys' tokens
+  float* const rt = reinterpret_cast<float*>(tm + MB);  // [kRates][C]
+  const float* const ek = rt + kEk * C;
+  const float* const we = rt + kWe * C;
+  const float* const bt = rt + kBeta * C;
+  char* const tx = reinterpret_cast<char*>(rt + kRates * C);
+  char* const tp = tx + C * ROWS * ES;
 
   const int tid = static_cast<int>(threadIdx.x);
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -745,95 +891,51 @@ ssm_delta_rev_kernel(const DeltaDev p) {
     else
       load_state<IO, RT>(SEG ? nullptr : p.seg_state + (bh * p.nseg + seg + 1) * wsize, p.rp, p.cp, p.cp, c, g, R);
   }
-  for (int i = tid; i < MB / 16; i += T) reinterpret_cast<uint4*>(tp)[i] = make_uint4(0, 0, 0, 0);
 
   const char* const xb = p.q + b * p.q_b + static_cast<int64_t>(h / p.rep) * p.rows * ES;
   const char* const yb = p.k + b * p.k_b + static_cast<int64_t>(h / p.rep) * p.rows * ES;
   const char* const zb = p.v + b * p.v_b + (static_cast<int64_t>(h) * p.cols + col0) * ES;
-  const char* const mb = p.m + bh * p.nch * MB;
 
-  uint4 rx[TK::CNT], ry[TK::CNT], rz[TZ::CNT], rm[LM];
-  Rates<IO> rates;
+  uint4 rx[TK::CNT], ry[TK::CNT], rz[TZ::CNT], rm[TM::CNT], rp[TM::CNT], rr[TR::CNT];
   auto load_chunk = [&](int pc) {
-    const int t0 = pc * C, me = opaque(tid);
-    rates.load(p, b, h, t0, len, me & 63);
+    const int t0 = pc * C, me = ROWS == 256 || !VEC ? opaque(tid) : tid;
+    const int64_t chunk = bh * p.nch + pc;
     TK::template load<VEC>(yb, p.k_t, t0, len, p.rows, me, ry);
-    TK::template load<VEC>(xb, p.q_t, t0, len, p.rows, me, rx);
-#pragma unroll
-    for (int i = 0; i < LM; ++i)
-      if (MB / 16 % T == 0 || me < MB / 16)
-        rm[i] = *reinterpret_cast<const uint4*>(mb + static_cast<int64_t>(pc) * MB + 16 * (me + i * T));
+    TR::load(reinterpret_cast<const char*>(p.rates + chunk * kRates * C), me, rr);
+    TM::load(p.s + chunk * MB, me, rp);
     TZ::template load<VEC>(zb, p.v_t, t0, len, p.cols - col0, me, rz);
+    TM::load(p.m + chunk * MB, me, rm);
+    TK::template load<VEC>(xb, p.q_t, t0, len, p.rows, me, rx);
   };
 
   const int cl = (len + C - 1) / C, ce = c1 < cl ? c1 : cl, nc = ce - c0;
-  if (nc > 0) load_chunk(ce - 1);
+  if (nc > 0) {
+    load_chunk(ce - 1);
+    if constexpr (!SEG) {
+      // as many stores behind the first loads as the loop has behind its own (see keep)
+      const f32x4 none[RT > IB ? RT : IB] = {};
+      const int li = tid & 15, g = (tid & 63) >> 4;
+      keep<IO, RT>(p.states, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
+      keep<IO, IB>(p.res, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
+    }
+  }
   for (int kk = 0; kk < nc; ++kk) {
     const int pc = ce - 1 - kk, t0 = pc * C;
     __syncthreads();
     {
-      const int me = opaque(tid);
+      const int me = ROWS == 256 || !VEC ? opaque(tid) : tid;
       TK::store(ty, me, ry);
       TK::store(tx, me, rx);
       TZ::store(tz, me, rz);
-#pragma unroll
-      for (int i = 0; i < LM; ++i) {
-        const int at = me + i * T, r = at / NP;
-        if (MB / 16 % T == 0 || at < MB / 16) *reinterpret_cast<uint4*>(tm + 16 * (NP * r + (at % NP ^ swz<IO, NP>(r)))) = rm[i];
-      }
-    }
-    if (wave == NW - 1) {
-      float hi, lo;
-      rates.scan(hi, lo);
-      const float eh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hi), C - 1));
-      const float el = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lo), C - 1));
-      const int lane = tid & 63;
-      if (lane < C) {
-        const float e = __builtin_amdgcn_exp2f(hi + lo);
-        ghi[lane] = hi;
-        glo[lane] = lo;
-        ek[lane] = e;
-        eo[lane] = p.scale * e;
-        we[lane] = __builtin_amdgcn_exp2f((eh - hi) + (el - lo));
-        bt[lane] = rates.beta(p, t0, len, lane);
-      }
+      TM::store(tm, me, rm);
+      TM::store(tp, me, rp);
+      TR::store(reinterpret_cast<char*>(rt), me, rr);
     }
     __syncthreads();
     const float end_dec = ek[C - 1];
     const int lane = opaque(tid) & 63, g = lane >> 4, li = lane & 15;
     if (kk + 1 < nc) load_chunk(pc - 1);
-    if constexpr (!SEG) store_state<IO, RT>(p.states + (bh * p.nch + pc) * wsize, p.rp, p.cp, p.cp, cw + li, g, R);
-
-    // ---- scores transposed: lane holds i = 4 g + v of j = li
-    {
-      const int rb = lane_base<IO, NK>(li, g);
-      for (int tile = wave; tile < IB * (IB + 1) / 2; tile += NW) {
-        const int ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6), jb = tile - ib * (ib + 1) / 2;
-        const int j = 16 * jb + li, i0 = 16 * ib + 4 * g;
-        f32x4 a = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < RS; ++s) a = mma<IO>(frag_row<NK>(tx, rb, ib, s), frag_row<NK>(ty, rb, jb, s), a);
-        const float gj = ghi[j], gl = glo[j];
-        const float4 gi = *reinterpret_cast<const float4*>(ghi + i0), gk = *reinterpret_cast<const float4*>(glo + i0);
-        float w[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float d = __builtin_amdgcn_exp2f((get(gi, v) - gj) + (get(gk, v) - gl));
-          w[v] = i0 + v >= j ? times(p.scale * d, a[v]) : 0.f;
-        }
-        if constexpr (ES == 2) {
-          const int u = 4 * ib + g;
-          const int to = (j * NP + ((u >> 1) ^ swz<IO, NP>(j))) * 16 + (u & 1) * 8;
-          const uint2 hi2 = make_uint2(BF16::cvt2(w[0], w[1]), BF16::cvt2(w[2], w[3]));
-          *reinterpret_cast<uint2*>(tp + to) = hi2;
-          *reinterpret_cast<uint2*>(tp + C * C * ES + to) =
-              make_uint2(BF16::cvt2(w[0] - bf_lo(hi2.x), w[1] - bf_hi(hi2.x)),
-                         BF16::cvt2(w[2] - bf_lo(hi2.y), w[3] - bf_hi(hi2.y)));
-        } else {
-          *reinterpret_cast<float4*>(tp + (j * NP + ((4 * ib + g) ^ swz<IO, NP>(j))) * 16) = make_float4(w[0], w[1], w[2], w[3]);
-        }
-      }
-    }
+    if constexpr (!SEG) keep<IO, RT>(p.states + (bh * p.nch + pc) * wsize, p.rp, p.cp, cw + li, g, R);
 
     // ---- X = K R (rows are tokens)
     f32x4 X[IB];
@@ -870,27 +972,25 @@ ssm_delta_rev_kernel(const DeltaDev p) {
         X[t][i & 3] = times(w[i], X[t][i & 3]);
       }
     }
-    __syncthreads();  // scores
-    const int mb0 = opaque(state_row_base<IO, NP>(li, g));
+    const int mc0 = opaque(state_col_base<IO, NP>(li, g));
 #pragma unroll
     for (int i = 0; i < IB; ++i)
 #pragma unroll
       for (int js = 0; js < JS; ++js) {
         if (KS * (js + 1) <= 16 * i) continue;  // above the diagonal of the transposed
-        X[i] = mma<IO>(frag_state_row<IO, NP>(tp, mb0, i, js), fz[js], X[i]);
-        if constexpr (PP == 2) X[i] = mma<IO>(frag_state_row<IO, NP>(tp + C * C * ES, mb0, i, js), fz[js], X[i]);
+        X[i] = mma<IO>(frag_state_col<IO, NP>(tp, mc0, i, js), fz[js], X[i]);
+        if constexpr (PP == 2) X[i] = mma<IO>(frag_state_col<IO, NP>(tp + C * C * ES, mc0, i, js), fz[js], X[i]);
       }
     // ---- e = y - M^T (b y)
-    uint4 by[JS][PP];
+    uint4 by[JS][PS];
 #pragma unroll
     for (int js = 0; js < JS; ++js) {
       float bb[E];
       F32::ld<E>(bt + KS * js + E * g, bb);
 #pragma unroll
       for (int i = 0; i < E; ++i) bb[i] *= X[tile_of<IO>(js, i)][i & 3];
-      split<IO, PP>(bb, by[js]);
+      split<IO, PS>(bb, by[js]);
     }
-    const int mc0 = opaque(state_col_base<IO, NP>(li, g));
 #pragma unroll
     for (int i = 0; i < IB; ++i)
 #pragma unroll
@@ -898,10 +998,14 @@ ssm_delta_rev_kernel(const DeltaDev p) {
         if (KS * (js + 1) <= 16 * i) continue;
         const uint4 fm = frag_state_col<IO, NP>(tm, mc0, i, js);
 #pragma unroll
-        for (int q = 0; q < PP; ++q) X[i] = mma<IO>(fm, by[js][q], X[i]);
-        if constexpr (PP == 2) X[i] = mma<IO>(frag_state_col<IO, NP>(tm + C * C * ES, mc0, i, js), by[js][0], X[i]);
+        for (int q = 0; q < PS; ++q) X[i] = mma<IO>(fm, by[js][q], X[i]);
+        if constexpr (PP == 2) {
+          const uint4 fl = frag_state_col<IO, NP>(tm + C * C * ES, mc0, i, js);
+          X[i] = mma<IO>(fl, by[js][0], X[i]);
+          X[i] = mma<IO>(fl, by[js][1], X[i]);
+        }
       }
-    if constexpr (!SEG) store_res<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp, p.cp, cw + li, g, X);
+    if constexpr (!SEG) keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp, C, p.cp, cw + li, g, X);
 
     // ---- the state before the chunk
 #pragma unroll
@@ -989,14 +1093,15 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
   char* const te = tu + PP * SB;
   char* const tp = slab;
   char* const tn = slab + PP * PB;
-  float* const ghi = reinterpret_cast<float*>(slab + kSlabBytes);
-  float* const glo = ghi + C;
-  float* const ek = glo + C;
-  float* const we = ek + C;
-  float* const bt = we + C;
-  float* const own = bt + C;    // scale do . u of a token's own
-  int* const anew = reinterpret_cast<int*>(own + C);  // the state starts anew at the token
-  float* const red = own + 2 * C;   // [NW][C]
+  float* const rt = reinterpret_cast<float*>(slab + kSlabBytes);  // [kRates][C]
+  const float* const ghi = rt + kGHi * C;
+  const float* const glo = rt + kGLo * C;
+  const float* const ek = rt + kEk * C;
+  const float* const we = rt + kWe * C;
+  const float* const bt = rt + kBeta * C;
+  const float* const anew = rt + kAnew * C;
+  float* const own = rt + kRates * C;  // scale do . u of a token's own
+  float* const red = own + C;       // [NW][C]
   float* const redc = red + NW * C;
   float* const rs = redc + NW * C;  // [NW]
 
@@ -1032,22 +1137,8 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
       const uint32_t wbytes = static_cast<uint32_t>(p.rp * p.cp * 4);
       const Rsrc rs0 = make_rsrc(s0, wbytes), rr1 = make_rsrc(r1, wbytes);
       __syncthreads();  // the head before is done with the LDS
-      if (wave == NW - 1) {
-        Rates<IO> rates;
-        rates.load(p, b, h, t0, len, lane);
-        float hi, lo;
-        rates.scan(hi, lo);
-        const float eh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hi), C - 1));
-        const float el = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lo), C - 1));
-        if (lane < C) {
-          ghi[lane] = hi;
-          glo[lane] = lo;
-          ek[lane] = __builtin_amdgcn_exp2f(hi + lo);
-          we[lane] = __builtin_amdgcn_exp2f((eh - hi) + (el - lo));
-          bt[lane] = rates.beta(p, t0, len, lane);
-          anew[lane] = clamp_decay(Rates<IO>::value(rates.raw_g) * kLog2e) == kMinLog2Decay;
-        }
-      }
+      if (tid < kRates * C / 4)
+        reinterpret_cast<float4*>(rt)[tid] = reinterpret_cast<const float4*>(p.rates + chunk * kRates * C)[tid];
       __syncthreads();
 
       f32x4 dq[CT][IB], ur[CT][IB], vs[CT][IB], sc[MINE];
@@ -1292,7 +1383,7 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
               v += red[w * C + lane];
               tail += redc[w * C + lane];
             }
-            cut = lane + 1 < C ? anew[lane + 1] : 0;
+            cut = lane + 1 < C && anew[lane + 1] != 0.f;
           }
           for (int w = 0; w < NW; ++w) edge += rs[w];
 #pragma unroll
@@ -1310,7 +1401,7 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
           }
           const int t = t0 + lane;
           if (lane < C && t < p.L) {
-            const bool none = t >= len || (t == 0 && p.h0 == nullptr) || anew[lane];
+            const bool none = t >= len || (t == 0 && p.h0 == nullptr) || anew[lane] != 0.f;
             const float out = none ? 0.f : static_cast<float>(v);
             IO::template st<1>(reinterpret_cast<typename IO::T*>(d.dg) + (row0 + lane) * p.H + h, &out);
           }
@@ -1384,8 +1475,8 @@ hipError_t allow_lds(Kern kern, size_t smem, std::atomic<uint64_t>& allowed) {
 template <typename IO, int ROWS, bool VEC>
 hipError_t launch_prep_t(const DeltaDev& p, hipStream_t st) {
   static std::atomic<uint64_t> allowed{0};
-  constexpr size_t smem = prep_lds_bytes<IO, ROWS>();
-  auto kern = ssm_delta_prep_kernel<IO, ROWS, VEC>;
+  constexpr size_t smem = prep_lds_bytes<IO, ROWS, true>();
+  auto kern = ssm_delta_prep_kernel<IO, ROWS, true, VEC>;
   if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.batch * p.H * p.nch)), dim3(256), smem, st, p);
   return hipGetLastError();
