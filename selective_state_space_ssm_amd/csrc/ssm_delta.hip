@@ -47,66 +47,58 @@ bool wide_for(int64_t cols, bool vec) { static const char* e = getenv("DW"); ret
 int64_t tiles_for(int64_t cols, bool vec) { return cdiv(cols, wide_for(cols, vec) ? 128 : 64); }
 
 // States carried over the segments, in order, 16 columns a workgroup: state <- A carried + own, or A^T carried + own
-// from the end.  Float32 matrix instructions; the carried columns are in LDS.  A segment's part of A (16 RT rows a
-// wavefront) is asked for while the segment before is worked on: each operand takes its successor once it is used.
-template <int RT, bool REV>
-__global__ void __launch_bounds__(512) ssm_delta_carry_kernel(float* state, const float* trans, int nseg, int rp, int cp) {
-  constexpr int KT = 8 * RT;  // operand steps of 16 rows: rp / 16 of them
-  __shared__ float carried[128 * RT][17];
+// from the end.  Float32 matrix instructions, 16 rows a wavefront; the carried columns are in LDS.  A segment's rows of
+// A are asked for while the segment before is worked on: each operand takes its successor once it is used.
+template <int NW, bool REV>
+__global__ void __launch_bounds__(64 * NW) ssm_delta_carry_kernel(float* state, const float* trans, int nseg, int rp, int cp) {
+  __shared__ float carried[16 * NW][17];
   const int64_t bh = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c = blockIdx.x * 16 + li, tiles = rp / 16;
+  const int c = blockIdx.x * 16 + li, tiles = rp / 16, row = 16 * wave;
   const int64_t ws = static_cast<int64_t>(rp) * cp, ts = static_cast<int64_t>(rp) * rp;
   float* const s = state + bh * nseg * ws;
   const float* const m = trans + bh * nseg * ts;
   const int first = REV ? nseg - 1 : 0, step = REV ? -1 : 1;
-  float4 f[RT][KT];
-  f32x4 acc[RT];
-  auto load_a = [&](int at, int t, int k) {
-    const float* const a = m + at * ts;
-    const int r = 16 * (wave + 8 * t) + li, k0 = 16 * k + 4 * g;
-    if (wave + 8 * t >= tiles || k >= tiles) return;
-    if (REV) f[t][k] = make_float4(a[k0 * rp + r], a[(k0 + 1) * rp + r], a[(k0 + 2) * rp + r], a[(k0 + 3) * rp + r]);
-    else f[t][k] = *reinterpret_cast<const float4*>(a + r * rp + k0);
+  const bool mine = wave < tiles;
+  float4 f[NW];  // operand steps of 16 of A's columns
+  auto load_a = [&](int at, int k) {
+    if (!mine || k >= tiles) return;
+    const Rsrc a = make_rsrc(m + at * ts, static_cast<uint32_t>(4 * ts));
+    float* const o = reinterpret_cast<float*>(&f[k]);
+    if constexpr (REV) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) BufF32::ld<1>(a, 4 * ((4 * g + e) * rp + row + li) + 64 * k * rp, o + e);
+    } else {
+      BufF32::ld<4>(a, 4 * ((row + li) * rp + 4 * g) + 64 * k, o);
+    }
   };
-  for (int i = tid; i < rp * 16; i += 512) carried[i / 16][i % 16] = s[first * ws + static_cast<int64_t>(i / 16) * cp + blockIdx.x * 16 + i % 16];
+  for (int i = tid; i < rp * 16; i += 64 * NW)
+    carried[i / 16][i % 16] = s[first * ws + static_cast<int64_t>(i / 16) * cp + blockIdx.x * 16 + i % 16];
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int k = 0; k < KT; ++k) load_a(first + step, t, k);
+  for (int k = 0; k < NW; ++k) load_a(first + step, k);
   __syncthreads();
   for (int i = 1; i < nseg - 1; ++i) {
     const int at = first + i * step, next = i + 2 < nseg ? at + step : at;
     float* const own = s + at * ws;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f}, sum[2] = {acc, acc};
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int v = 0; v < 4; ++v)
+      if (mine) acc[v] = own[static_cast<int64_t>(row + 4 * g + v) * cp + c];
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        acc[t][v] = wave + 8 * t < tiles ? own[static_cast<int64_t>(16 * (wave + 8 * t) + 4 * g + v) * cp + c] : 0.f;
-    f32x4 sum[RT][2];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) sum[t][0] = sum[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
+    for (int k = 0; k < NW; ++k) {
       if (k >= tiles) continue;
       const float4 x = make_float4(carried[16 * k + 4 * g][li], carried[16 * k + 4 * g + 1][li], carried[16 * k + 4 * g + 2][li],
                                    carried[16 * k + 4 * g + 3][li]);
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        if (wave + 8 * t < tiles)
-          sum[t][k & 1] = headk::mma<F32>(__builtin_bit_cast(uint4, f[t][k]), __builtin_bit_cast(uint4, x), sum[t][k & 1]);
-        load_a(next, t, k);
-      }
+      if (mine) sum[k & 1] = headk::mma<F32>(__builtin_bit_cast(uint4, f[k]), __builtin_bit_cast(uint4, x), sum[k & 1]);
+      load_a(next, k);
     }
     __syncthreads();
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      if (wave + 8 * t >= tiles) continue;
+    if (mine) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int r = 16 * (wave + 8 * t) + 4 * g + v;
-        const float x = acc[t][v] + (sum[t][0][v] + sum[t][1][v]);
+        const int r = row + 4 * g + v;
+        const float x = acc[v] + (sum[0][v] + sum[1][v]);
         carried[r][li] = x;
         own[static_cast<int64_t>(r) * cp + c] = x;
       }
@@ -277,7 +269,7 @@ int64_t square_bytes(const DeltaArgs& a, const Plan& pl) {
 // Heads whose parts of dq and dk a workgroup adds: all that share a key head, unless that leaves CUs idle.
 int64_t grad_heads(const DeltaArgs& a, const Plan& pl) {
   const int64_t rep = a.H / a.Hk;
-  int64_t n = rep;
+  int64_t n = a.dk > 128 ? 1 : rep;  // kGradOneHead
   while (n > 1 && a.batch * (a.H / n) * pl.nch < kDeltaSlots) {
     --n;
     while (rep % n != 0) --n;
@@ -354,10 +346,11 @@ hipError_t launch_pass(const DeltaDev& d, bool bf16, int pass, bool vec, hipStre
 
 hipError_t launch_carry(const DeltaDev& d, bool rev, hipStream_t st) {
   if (d.nseg <= 2) return hipSuccess;
-  auto kern = d.rp <= 128 ? (rev ? ssm_delta_carry_kernel<1, true> : ssm_delta_carry_kernel<1, false>)
-                          : (rev ? ssm_delta_carry_kernel<2, true> : ssm_delta_carry_kernel<2, false>);
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(d.cp / 16), static_cast<unsigned>(d.batch * d.H)), dim3(512), 0, st,
-                     d.seg_state, d.seg_trans, d.nseg, d.rp, d.cp);
+  const bool wide = d.rp > 128;
+  auto kern = wide ? (rev ? ssm_delta_carry_kernel<16, true> : ssm_delta_carry_kernel<16, false>)
+                   : (rev ? ssm_delta_carry_kernel<8, true> : ssm_delta_carry_kernel<8, false>);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(d.cp / 16), static_cast<unsigned>(d.batch * d.H)), dim3(wide ? 1024 : 512),
+                     0, st, d.seg_state, d.seg_trans, d.nseg, d.rp, d.cp);
   return hipGetLastError();
 }
 

@@ -1044,6 +1044,9 @@ ssm_delta_rev_kernel(const DeltaDev p) {
 
 // ---------------------------------------------------------------- the gradients, all chunks at once
 
+// From this width on the sums over heads do not fit the registers: a workgroup then has one head.
+constexpr int kGradOneHead = 256;
+
 struct DeltaGradDev {
   DeltaDev f;                  // q, k, rates, sizes; v is dO; states S_0, res r
   const float* r1;             // [b][H][nch][rp][cp]: R after every chunk
@@ -1057,12 +1060,15 @@ struct DeltaGradDev {
   int parts;
 };
 
+// Slabs in LDS: two where they fit, so that the next one is written while one is worked on.
+template <int ROWS>
+constexpr int grad_buffers() { return ROWS == 256 ? 1 : 2; }
 template <typename IO, int ROWS, int NW>
 constexpr size_t grad_lds_bytes() {
   using K = HeadCfg<IO>;
   constexpr size_t slab = size_t(K::C) * kSlab * K::ES * (1 + 2 * DeltaCfg<IO>::PAIR);
   constexpr size_t sc = size_t(2) * K::C * K::C * K::ES * DeltaCfg<IO>::PAIR;
-  return 2 * size_t(K::C) * ROWS * K::ES + (slab > sc ? slab : sc) + (size_t(2) * NW + 7) * K::C * 4 + NW * 4;
+  return 2 * size_t(K::C) * ROWS * K::ES + grad_buffers<ROWS>() * slab + sc + (size_t(2) * NW + kRates + 1) * K::C * 4 + NW * 4;
 }
 
 // dg_t = <dLoss/dS~_t, S~_t> telescopes within the chunk:
@@ -1076,24 +1082,21 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
   const DeltaDev& p = d.f;
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW;
   constexpr int NK = ROWS * ES / 16, NS = kSlab * ES / 16, NP = C * ES / 16;
-  constexpr int IB = C / 16, JS = C / KS, SS = kSlab / KS, CT = ROWS / 16 / NW;
-  constexpr int PP = DeltaCfg<IO>::PAIR, SB = C * kSlab * ES, PB = C * C * ES;
+  constexpr int IB = C / 16, JS = C / KS, SS = kSlab / KS, CT = ROWS / 16 / NW, NBUF = grad_buffers<ROWS>();
+  constexpr int PP = DeltaCfg<IO>::PAIR, SB = C * kSlab * ES, PB = C * C * ES, SLAB = SB * (1 + 2 * PP);
   constexpr int TILES = IB * (IB + 1) / 2, MINE = (2 * TILES + NW - 1) / NW;
   constexpr int TASKS = C * NS / T;  // staging tasks a thread, rows tid / NS + i T / NS
+  constexpr bool MULTI = ROWS < kGradOneHead;
   static_assert(C * NS % T == 0 && CT >= 1, "shares are even");
   using TK = Tile<IO, NK, T>;
 
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char* const tx = lds;
   char* const ty = tx + C * ROWS * ES;
-  char* const slab = ty + C * ROWS * ES;  // dO, b r, b e; then the scores dP and dN
-  constexpr size_t kSlabBytes = SB * (1 + 2 * PP) > 2 * PB * PP ? SB * (1 + 2 * PP) : 2 * PB * PP;
-  char* const tdo = slab;
-  char* const tu = slab + SB;
-  char* const te = tu + PP * SB;
-  char* const tp = slab;
-  char* const tn = slab + PP * PB;
-  float* const rt = reinterpret_cast<float*>(slab + kSlabBytes);  // [kRates][C]
+  char* const slabs = ty + C * ROWS * ES;  // each dO, b r, b e of kSlab columns
+  char* const tp = slabs + NBUF * SLAB;    // dP, then dN
+  char* const tn = tp + PP * PB;
+  float* const rt = reinterpret_cast<float*>(tn + PP * PB);  // [kRates][C]
   const float* const ghi = rt + kGHi * C;
   const float* const glo = rt + kGLo * C;
   const float* const ek = rt + kEk * C;
@@ -1114,34 +1117,71 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
   const uint32_t ots = static_cast<uint32_t>(groups * p.rows * oes), vts = p.H * p.cols * ES;
   const int64_t row0 = static_cast<int64_t>(b) * p.L + t0;
 
-  f32x4 DQ[CT][IB], DK[CT][IB];
+  // the head's, and the sums over the heads that share a key head (one head: none)
+  f32x4 dq[CT][IB], ur[CT][IB], DQ[MULTI ? CT : 1][IB], DK[MULTI ? CT : 1][IB];
 #pragma unroll
   for (int c = 0; c < CT; ++c)
 #pragma unroll
-    for (int i = 0; i < IB; ++i) DQ[c][i] = DK[c][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < IB; ++i) {
+      dq[c][i] = ur[c][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (MULTI) DQ[c][i] = DK[c][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 
   if (t0 < len) {
-    const int hk = hg * d.hn / p.rep;
+    const int hk = hg * d.hn / p.rep, nslab = p.cp / kSlab;
+    const uint32_t wbytes = static_cast<uint32_t>(p.rp * p.cp * 4), rbytes = static_cast<uint32_t>(C * p.cp * 4);
+    // What a thread has in flight: its part of a slab's dO, r and e, and the operands S_0 and R_C of its wavefront.
+    uint4 go[TASKS];
+    float gr[TASKS][E], ge[TASKS][E], s0[CT][E], r1[CT][E];
+    auto load_slab = [&](int h, int v0) {
+      const int64_t chunk = (static_cast<int64_t>(b) * p.H + h) * p.nch + pc;
+      const Rsrc rdo = make_rsrc(p.v + b * p.v_b + static_cast<int64_t>(t0) * p.v_t + static_cast<int64_t>(h) * p.cols * ES,
+                                 row_bytes(len - t0, C, p.v_t));
+      const Rsrc rr = make_rsrc(p.res + chunk * C * p.cp, rbytes), re = make_rsrc(d.e + chunk * C * p.cp, rbytes);
+#pragma unroll
+      for (int i = 0; i < TASKS; ++i) {
+        const int me = opaque(tid), r = me / NS + i * (T / NS), col = v0 + me % NS * E;
+        go[i] = load16<IO, VEC>(rdo, r * p.v_t + col * ES, p.cols - col);
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          BufF32::ld<4>(rr, (r * p.cp + col + e) * 4, &gr[i][e]);
+          BufF32::ld<4>(re, (r * p.cp + col + e) * 4, &ge[i][e]);
+        }
+      }
+    };
+    auto load_states = [&](int h, int v0) {
+      const int64_t chunk = (static_cast<int64_t>(b) * p.H + h) * p.nch + pc;
+      const Rsrc rs0 = make_rsrc(p.states + chunk * p.rp * p.cp, wbytes), rr1 = make_rsrc(d.r1 + chunk * p.rp * p.cp, wbytes);
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const uint32_t off = static_cast<uint32_t>(((wave * CT + c) * 16 + li) * p.cp + v0 + E * g) * 4;
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          BufF32::ld<4>(rs0, off + 4 * e, &s0[c][e]);
+          BufF32::ld<4>(rr1, off + 4 * e, &r1[c][e]);
+        }
+      }
+    };
     {
       uint4 rx[TK::CNT], ry[TK::CNT];
       TK::template load<VEC>(p.q + b * p.q_b + static_cast<int64_t>(hk) * p.rows * ES, p.q_t, t0, len, p.rows, tid, rx);
       TK::template load<VEC>(p.k + b * p.k_b + static_cast<int64_t>(hk) * p.rows * ES, p.k_t, t0, len, p.rows, tid, ry);
+      load_slab(hg * d.hn, 0);
+      load_states(hg * d.hn, 0);
       TK::store(tx, tid, rx);
       TK::store(ty, tid, ry);
     }
+    // the score tiles above the diagonal that a product step covers are never written again
+    for (int i = tid; i < 2 * PP * PB / 16; i += T) reinterpret_cast<uint4*>(tp)[i] = make_uint4(0, 0, 0, 0);
     for (int hh = 0; hh < d.hn; ++hh) {
       const int h = hg * d.hn + hh;
       const int64_t bh = static_cast<int64_t>(b) * p.H + h, chunk = bh * p.nch + pc;
-      const float* const s0 = p.states + chunk * p.rp * p.cp;
-      const float* const r1 = d.r1 + chunk * p.rp * p.cp;
-      const uint32_t wbytes = static_cast<uint32_t>(p.rp * p.cp * 4);
-      const Rsrc rs0 = make_rsrc(s0, wbytes), rr1 = make_rsrc(r1, wbytes);
-      __syncthreads();  // the head before is done with the LDS
+      __syncthreads();  // the head before is done with the rates
       if (tid < kRates * C / 4)
         reinterpret_cast<float4*>(rt)[tid] = reinterpret_cast<const float4*>(p.rates + chunk * kRates * C)[tid];
       __syncthreads();
 
-      f32x4 dq[CT][IB], ur[CT][IB], vs[CT][IB], sc[MINE];
+      f32x4 vs[CT][IB], sc[MINE];
 #pragma unroll
       for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -1150,65 +1190,60 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
       for (int i = 0; i < MINE; ++i) sc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
       float dot_rs = 0.f, dot_b[TASKS] = {};
 
-      for (int v0 = 0; v0 < p.cols; v0 += kSlab) {
+      for (int v = 0; v < nslab; ++v) {
+        const int v0 = v * kSlab;
+        char* const tdo = slabs + v % NBUF * SLAB;
+        char* const tu = tdo + SB;
+        char* const te = tu + PP * SB;
+        if (NBUF == 1 && v > 0) __syncthreads();  // the slab before is done with
         // ---- dO, b r and b e of 64 columns, as parts; dv and the sums of db on the way
+        const Rsrc rdv = make_rsrc(d.dv + row0 * vts + static_cast<int64_t>(h) * p.cols * ES, row_bytes(p.L - t0, C, vts));
 #pragma unroll
         for (int i = 0; i < TASKS; ++i) {
-          const int r = tid / NS + i * (T / NS), c = tid % NS, col = v0 + c * E;
-          const Rsrc rdo = make_rsrc(p.v + b * p.v_b + static_cast<int64_t>(t0) * p.v_t + static_cast<int64_t>(h) * p.cols * ES,
-                                     row_bytes(len - t0, C, p.v_t));
-          const uint4 fo = load16<IO, VEC>(rdo, r * p.v_t + col * ES, p.cols - col);
-          const int64_t at = (chunk * C + r) * p.cp + col;
-          float x[E], y[E], bb = bt[r];
-          F32::ld<E>(p.res + at, x);
-          F32::ld<E>(d.e + at, y);
+          const int me = opaque(tid), r = me / NS + i * (T / NS), c = me % NS, col = v0 + c * E;
+          const float bb = bt[r];
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            dot_b[i] = __builtin_fmaf(x[e], y[e], dot_b[i]);
-            x[e] *= bb;
-            y[e] *= bb;
+            dot_b[i] = __builtin_fmaf(gr[i][e], ge[i][e], dot_b[i]);
+            gr[i][e] *= bb;
+            ge[i][e] *= bb;
           }
-          if (t0 + r < p.L) {
-            const Rsrc rdv = make_rsrc(d.dv + row0 * vts + static_cast<int64_t>(h) * p.cols * ES, row_bytes(p.L - t0, C, vts));
-            const uint32_t off = r * vts + col * ES;
-            if constexpr (VEC) {
-              BufOf<IO>::type::template st<E>(rdv, col < p.cols ? off : kOOB, y);
-            } else {
+          const uint32_t off = r * vts + col * ES;
+          if constexpr (VEC) {
+            BufOf<IO>::type::template st<E>(rdv, col < p.cols ? off : kOOB, ge[i]);
+          } else {
 #pragma unroll
-              for (int e = 0; e < E; ++e) BufOf<IO>::type::template st<1>(rdv, col + e < p.cols ? off + e * ES : kOOB, y + e);
-            }
+            for (int e = 0; e < E; ++e) BufOf<IO>::type::template st<1>(rdv, col + e < p.cols ? off + e * ES : kOOB, &ge[i][e]);
           }
           uint4 w[PP];
           const int to = 16 * (NS * r + (c ^ swz<IO, NS>(r)));
-          *reinterpret_cast<uint4*>(tdo + to) = fo;
-          split<IO, PP>(x, w);
+          *reinterpret_cast<uint4*>(tdo + to) = go[i];
+          split<IO, PP>(gr[i], w);
 #pragma unroll
           for (int q = 0; q < PP; ++q) *reinterpret_cast<uint4*>(tu + q * SB + to) = w[q];
-          split<IO, PP>(y, w);
+          split<IO, PP>(ge[i], w);
 #pragma unroll
           for (int q = 0; q < PP; ++q) *reinterpret_cast<uint4*>(te + q * SB + to) = w[q];
         }
         __syncthreads();
-        const int fb = lane_base<IO, NS>(li, g);
+        if (v + 1 < nslab) load_slab(h, v0 + kSlab);
+        else if (hh + 1 < d.hn) load_slab(h + 1, 0);
+        const int fb = opaque(lane_base<IO, NS>(li, g));
 #pragma unroll
         for (int s = 0; s < SS; ++s) {
           uint4 fs[CT][PP], fr[CT][PP];
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
-            const uint32_t off = static_cast<uint32_t>(((wave * CT + c) * 16 + li) * p.cp + v0 + KS * s + E * g) * 4;
-            float x[E], y[E];
 #pragma unroll
-            for (int e = 0; e < E; e += 4) {
-              BufF32::ld<4>(rs0, off + 4 * e, x + e);
-              BufF32::ld<4>(rr1, off + 4 * e, y + e);
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) dot_rs = __builtin_fmaf(x[e], y[e], dot_rs);
-            split<IO, PP>(x, fs[c]);
-            split<IO, PP>(y, fr[c]);
+            for (int e = 0; e < E; ++e) dot_rs = __builtin_fmaf(s0[c][e], r1[c][e], dot_rs);
+            split<IO, PP>(s0[c], fs[c]);
+            split<IO, PP>(r1[c], fr[c]);
           }
+          if (s + 1 < SS || v + 1 < nslab) load_states(h, v0 + KS * (s + 1));
+          else if (hh + 1 < d.hn) load_states(h + 1, 0);
 #pragma unroll
           for (int ib = 0; ib < IB; ++ib) {
+            __builtin_amdgcn_sched_barrier(0);
             uint4 fo = frag_row<NS>(tdo, fb, ib, s), fu[PP], fe[PP];
 #pragma unroll
             for (int q = 0; q < PP; ++q) {
@@ -1232,28 +1267,31 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
           // tiles of dP, then of dN, dealt to the wavefronts: lane holds j = 4 g + v of i = li
 #pragma unroll
           for (int m = 0; m < MINE; ++m) {
-            const int job = wave + m * NW, tile = job < TILES ? job : job - TILES;
-            if (job >= 2 * TILES) break;
-            const int ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6), jb = tile - ib * (ib + 1) / 2;
-            const char* const x = job < TILES ? tdo : te;
-            const uint4 fx = frag_row<NS>(x, fb, ib, s);
-#pragma unroll
-            for (int q = 0; q < PP; ++q) sc[m] = mma<IO>(frag_row<NS>(tu + q * SB, fb, jb, s), fx, sc[m]);
-            if (PP == 2 && job >= TILES) sc[m] = mma<IO>(frag_row<NS>(tu, fb, jb, s), frag_row<NS>(te + SB, fb, ib, s), sc[m]);
+            __builtin_amdgcn_sched_barrier(0);
+            const int job = wave + m * NW;
+            if (job >= 2 * TILES) continue;
+            int ib, jb;
+            score_tile<IB>(job < TILES ? job : job - TILES, ib, jb);
+            const uint4 fx = frag_row<NS>(job < TILES ? tdo : te, fb, ib, s);
+            const uint4 fu = frag_row<NS>(tu, fb, jb, s);
+            sc[m] = mma<IO>(fu, fx, sc[m]);
+            if constexpr (PP == 2) {
+              sc[m] = mma<IO>(frag_row<NS>(tu + SB, fb, jb, s), fx, sc[m]);
+              if (job >= TILES) sc[m] = mma<IO>(fu, frag_row<NS>(te + SB, fb, ib, s), sc[m]);
+            }
           }
         }
-        __syncthreads();
       }
 
       // ---- the scores' gradients to LDS, below the diagonal
-      for (int i = tid; i < 2 * PP * PB / 16; i += T) reinterpret_cast<uint4*>(slab)[i] = make_uint4(0, 0, 0, 0);
-      __syncthreads();
 #pragma unroll
       for (int m = 0; m < MINE; ++m) {
-        const int job = wave + m * NW, tile = job < TILES ? job : job - TILES;
-        if (job >= 2 * TILES) break;
-        const int ib = (tile >= 1) + (IB > 2 && tile >= 3) + (IB > 2 && tile >= 6), jb = tile - ib * (ib + 1) / 2;
-        const int i = 16 * ib + li, j0 = 16 * jb + 4 * g;
+        __builtin_amdgcn_sched_barrier(0);
+        const int job = wave + m * NW;
+        if (job >= 2 * TILES) continue;
+        int ib, jb;
+        score_tile<IB>(job < TILES ? job : job - TILES, ib, jb);
+        const int me = opaque(lane), g = me >> 4, i = 16 * ib + (me & 15), j0 = 16 * jb + 4 * g;
         const float by = job < TILES ? p.scale : -1.f;
         float w[4];
 #pragma unroll
@@ -1292,12 +1330,13 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
       }
       // ---- the state's parts scaled: lane holds rows (d_key) 16 (wave CT + c) + 4 g + v of token 16 ib + li
       auto values = [&](const char* tile, int c, int ib, float* v) {
-        const int r = 16 * ib + li, col = 16 * (wave * CT + c) + 4 * g;
+        const int me = opaque(lane), r = 16 * ib + (me & 15), col = 16 * (wave * CT + c) + 4 * (me >> 4);
         IO::template ld<4>(reinterpret_cast<const typename IO::T*>(
-                               tile + 16 * (NK * r + (col / E ^ swz<IO, NK>(li))) + col % E * ES), v);
+                               tile + 16 * (NK * r + (col / E ^ swz<IO, NK>(r))) + col % E * ES), v);
       };
 #pragma unroll
       for (int ib = 0; ib < IB; ++ib) {
+        __builtin_amdgcn_sched_barrier(0);
         const float fe = ek[16 * ib + li], fw = we[16 * ib + li];
         float dot = 0.f;
 #pragma unroll
@@ -1316,7 +1355,8 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
       }
       __syncthreads();  // scores
       // ---- what the chunk's tokens give each other
-      const int pb = lane_base<IO, NP>(li, g), pcb = col_base<IO, NP>(li, g), kb = col_base<IO, NK>(li, g);
+      const int pb = opaque(lane_base<IO, NP>(li, g)), pcb = opaque(col_base<IO, NP>(li, g));
+      const int kb = opaque(col_base<IO, NK>(li, g));
 #pragma unroll
       for (int js = 0; js < JS; ++js) {
         uint4 fk[CT], fq[CT];
@@ -1327,6 +1367,7 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
         }
 #pragma unroll
         for (int ib = 0; ib < IB; ++ib) {
+          __builtin_amdgcn_sched_barrier(0);
           if (js * KS < 16 * (ib + 1)) {
 #pragma unroll
             for (int q = 0; q < PP; ++q) {
@@ -1354,6 +1395,7 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
       // ---- the dots for dg, then a token's own pair
 #pragma unroll
       for (int ib = 0; ib < IB; ++ib) {
+        __builtin_amdgcn_sched_barrier(0);
         float dot = 0.f;
         const float o = own[16 * ib + li];
 #pragma unroll
@@ -1365,8 +1407,12 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
           for (int v = 0; v < 4; ++v) {
             dot = __builtin_fmaf(qv[v], dq[c][ib][v], dot);
             dot = __builtin_fmaf(kv[v], vs[c][ib][v] - ur[c][ib][v], dot);
-            DQ[c][ib][v] += __builtin_fmaf(o, kv[v], dq[c][ib][v]);
-            DK[c][ib][v] += __builtin_fmaf(o, qv[v], ur[c][ib][v] + vs[c][ib][v]);
+            dq[c][ib][v] = __builtin_fmaf(o, kv[v], dq[c][ib][v]);
+            ur[c][ib][v] = __builtin_fmaf(o, qv[v], ur[c][ib][v] + vs[c][ib][v]);
+            if (MULTI) {
+              DQ[c][ib][v] += dq[c][ib][v];
+              DK[c][ib][v] += ur[c][ib][v];
+            }
           }
         }
         dot += __shfl_xor(dot, 16);
@@ -1432,8 +1478,8 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
     for (int c = 0; c < CT; ++c) {
       const int col = 16 * (wave * CT + c) + 4 * g;
       const uint32_t off = li * ots + col * oes;
-      const float vq[4] = {DQ[c][ib][0], DQ[c][ib][1], DQ[c][ib][2], DQ[c][ib][3]};
-      const float vk[4] = {DK[c][ib][0], DK[c][ib][1], DK[c][ib][2], DK[c][ib][3]};
+      const f32x4 xq = MULTI ? DQ[MULTI ? c : 0][ib] : dq[c][ib], xk = MULTI ? DK[MULTI ? c : 0][ib] : ur[c][ib];
+      const float vq[4] = {xq[0], xq[1], xq[2], xq[3]}, vk[4] = {xk[0], xk[1], xk[2], xk[3]};
       if (VEC && !d.parts) {
         BufOf<IO>::type::template st<4>(rq, col < p.rows ? off : kOOB, vq);
         BufOf<IO>::type::template st<4>(rk, col < p.rows ? off : kOOB, vk);
