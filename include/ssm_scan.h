@@ -584,6 +584,57 @@ int ssm_gate_norm_bwd(const void *x, const void *z, const float *weight, const v
 /* Bytes of workspace ssm_gate_norm_bwd needs for a size (host only). */
 int ssm_gate_norm_workspace(int64_t rows, int64_t channels, int64_t groups, int dtype, int64_t *bytes);
 
+/*
+ * ssm_add_norm -- root-mean-square norm of token rows (channels last) with the
+ * residual's addition in front of it, what stands before a block:
+ *     h = x + residual,   y = weight * h / sqrt(mean(h^2) + eps)
+ *   x    : [rows, channels], dtype `dtype`.
+ *   residual, h : [rows, channels], dtype `residual_dtype` (SSM_F32, or that of
+ *          x).  residual nullable (h = x); h nullable (not written), equal to
+ *          residual (updated in place) or disjoint from it.
+ *   weight : [channels] float32, nullable (ones).
+ *   y    : [rows, channels], dtype `dtype`, output.
+ *   channels <= 8192, any number (a multiple of 8 is the fast path); eps >= 0.
+ * The norm acts on h as it is stored.  Arithmetic is float32, each result rounded
+ * once.  All pointers 16-byte aligned.
+ * Errors: SSM_EINVAL, SSM_EUNSUPPORTED, SSM_EHIP.
+ */
+int ssm_add_norm(const void *x, const void *residual, const float *weight, void *y, void *h, int64_t rows,
+                 int64_t channels, float eps, int dtype, int residual_dtype, void *stream);
+
+/*
+ * ssm_add_norm_e4m3 -- ssm_add_norm with y in 8 bits and its scales, for a
+ * projection that takes such rows: every group of `group` channels has
+ *     scale = max |y| / 448,   y = scale * (e4m3 value)
+ *   y    : [rows, channels], one byte each (e4m3 without infinities, largest
+ *          value 448), y / scale rounded to nearest even.
+ *   scale : [rows, channels / group] float32, group 32, 64 or 128 and a divisor
+ *          of channels, or group 0: [rows], a whole row.
+ * A group of zeros has scale 0 and values 0; one with a value that is no number
+ * has neither a scale nor values that are.
+ */
+int ssm_add_norm_e4m3(const void *x, const void *residual, const float *weight, void *y, float *scale, int64_t group,
+                      void *h, int64_t rows, int64_t channels, float eps, int dtype, int residual_dtype, void *stream);
+
+/*
+ * ssm_add_norm_bwd -- gradients of ssm_add_norm for dy and dh, the gradient of h
+ * from what h goes on to (nullable, zero).  With p = dy weight and
+ * n = 1 / sqrt(mean(h^2) + eps), taken again from h,
+ *     dx = dresidual = dh + n (p - h n mean(p h n)),   dweight = sum of dy h n.
+ *   h    : as ssm_add_norm wrote it.
+ *   dx   : dtype `dtype`, dresidual, dh: dtype `residual_dtype`; the two outputs
+ *          are the same values in their types, each nullable (not computed).
+ *   dweight : [channels] float32, nullable: a sum over the rows in a fixed order.
+ *   workspace : ssm_add_norm_workspace bytes (not needed without dweight).
+ * Other arguments and errors as ssm_add_norm.
+ */
+int ssm_add_norm_bwd(const void *h, const float *weight, const void *dy, const void *dh, void *dx, void *dresidual,
+                     float *dweight, void *workspace, int64_t workspace_bytes, int64_t rows, int64_t channels, float eps,
+                     int dtype, int residual_dtype, void *stream);
+
+/* Bytes of workspace ssm_add_norm_bwd needs for a size (host only). */
+int ssm_add_norm_workspace(int64_t rows, int64_t channels, int64_t *bytes);
+
 /* Activations of ssm_linear. */
 #define SSM_ACT_NONE 0
 #define SSM_ACT_SILU 1

@@ -73,3 +73,19 @@ def linear_bwd(x, W, dout, pre=None, kind="none"):
     dpre = dout if kind == "none" else dout * act(_arr(pre), kind)[1]
     d2 = dpre.reshape(-1, W.shape[0])
     return dpre @ W, d2.T @ x.reshape(-1, W.shape[1]), d2.sum(0), dpre
+
+
+def add_norm(h, weight=None, eps=1e-5):
+    """y of the norm that acts on h = x + residual as it is stored."""
+    h = _arr(h)
+    n = h / np.sqrt((h * h).mean(-1, keepdims=True) + eps)
+    return n if weight is None else n * _arr(weight)
+
+
+def add_norm_bwd(h, dy, weight=None, dh=None, eps=1e-5):
+    """(dx = dresidual, dweight)."""
+    h, dy = _arr(h), _arr(dy)
+    p = dy if weight is None else dy * _arr(weight)
+    r = 1 / np.sqrt((h * h).mean(-1, keepdims=True) + eps)
+    d = r * (p - h * r * (p * h * r).mean(-1, keepdims=True))
+    return d if dh is None else d + _arr(dh), (dy * h * r).reshape(-1, h.shape[-1]).sum(0)

@@ -20,8 +20,8 @@ import torch
 __all__ = ["SSMError", "ssm_scan_fwd", "ssm_scan_fwd_states", "ssm_scan_fwd_conv", "ssm_scan_bwd",
            "ssm_scan_bwd_conv", "ssm_step", "ssm_step_conv", "ssm_out_proj", "ssm_out_proj_bwd", "ssm_head_scan_fwd",
            "ssm_head_scan_bwd", "ssm_head_step", "ssm_delta_scan_fwd", "ssm_delta_scan_bwd", "ssm_delta_step",
-           "ssm_gate_norm", "ssm_gate_norm_bwd", "ssm_linear", "ssm_linear_bwd", "affine_scan", "affine_scan_order",
-           "plan_for", "library_path", "load_library", "PLANS", "ACTS"]
+           "ssm_gate_norm", "ssm_gate_norm_bwd", "ssm_add_norm", "ssm_add_norm_e4m3", "ssm_add_norm_bwd", "ssm_linear", "ssm_linear_bwd",
+           "affine_scan", "affine_scan_order", "plan_for", "library_path", "load_library", "PLANS", "ACTS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libssmscan.so")
@@ -110,6 +110,14 @@ def load_library():
     lib.ssm_gate_norm_bwd.restype = I
     lib.ssm_gate_norm_workspace.argtypes = [I64, I64, I64, I, ctypes.POINTER(I64)]
     lib.ssm_gate_norm_workspace.restype = I
+    lib.ssm_add_norm.argtypes = [P] * 5 + [I64, I64, F, I, I, P]
+    lib.ssm_add_norm.restype = I
+    lib.ssm_add_norm_e4m3.argtypes = [P] * 5 + [I64, P, I64, I64, F, I, I, P]
+    lib.ssm_add_norm_e4m3.restype = I
+    lib.ssm_add_norm_bwd.argtypes = [P] * 8 + [I64, I64, I64, F, I, I, P]
+    lib.ssm_add_norm_bwd.restype = I
+    lib.ssm_add_norm_workspace.argtypes = [I64, I64, ctypes.POINTER(I64)]
+    lib.ssm_add_norm_workspace.restype = I
     lib.ssm_linear.argtypes = [P, P, P, P, I, P, P, P, I64, I64, I64, I64, I, P]
     lib.ssm_linear.restype = I
     lib.ssm_linear_bwd.argtypes = [P, P, P, I, P, P, P, P, P, I64, I64, I64, I64, I, P]
@@ -1012,6 +1020,82 @@ def ssm_gate_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: Optional[torch.
           _addr(dz), _addr(dw), _addr(ws), nws, rows, c, int(groups), float(eps), int(bool(center)),
           int(bool(gate_first)), code)
     return dx, dw, dz
+
+
+def _add_norm_args(x, residual, weight, residual_dtype, h):
+    device, dt, rows, c = _rows(x, "x")
+    rt = residual.dtype if isinstance(residual, torch.Tensor) else residual_dtype or dt
+    if rt != torch.float32 and rt != dt:
+        raise TypeError(f"the residual must be float32 or of the dtype of x, got {rt}")
+    if residual is not None:
+        _need(residual, "residual", rt, device, x.shape)
+    if weight is not None:
+        _need(weight, "weight", torch.float32, device, (c,))
+    if h is None:
+        h = torch.empty_like(x, dtype=rt)
+    else:
+        _need(h, "h", rt, device, x.shape)
+    return device, rows, c, h, SSM_F32 if dt == torch.float32 else SSM_BF16, SSM_F32 if rt == torch.float32 else SSM_BF16
+
+
+def ssm_add_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                 eps: float = 1e-5, residual_dtype: Optional[torch.dtype] = None, y: Optional[torch.Tensor] = None,
+                 h: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Root-mean-square norm of token rows with the residual's addition (see ``ssm_add_norm`` in include/ssm_scan.h):
+    h = x + residual, y = weight * h / sqrt(mean(h^2) + eps).
+
+    x: [..., channels] float32 or bfloat16; residual: like x, float32 or of its dtype (None: h = x, in
+    ``residual_dtype``); weight: [channels] float32 (None: ones).  ``h`` may be residual itself (updated in place).
+    Returns (y like x, h in the residual's dtype)."""
+    device, rows, c, h, code, rcode = _add_norm_args(x, residual, weight, residual_dtype, h)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need(y, "y", x.dtype, device, x.shape)
+    _call(device, load_library().ssm_add_norm, x.data_ptr(), _addr(residual), _addr(weight), y.data_ptr(), h.data_ptr(),
+          rows, c, float(eps), code, rcode)
+    return y, h
+
+
+def ssm_add_norm_e4m3(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                      group: int = 0, eps: float = 1e-5, residual_dtype: Optional[torch.dtype] = None,
+                      h: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """ssm_add_norm with y in 8 bits (see ``ssm_add_norm_e4m3`` in include/ssm_scan.h).
+
+    group: channels that share a scale, 32, 64 or 128, or 0 for a whole row.  Returns (y [..., channels]
+    float8_e4m3fn, scale [..., channels / group] float32, h); y * scale are the normed values."""
+    device, rows, c, h, code, rcode = _add_norm_args(x, residual, weight, residual_dtype, h)
+    y = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    scale = torch.empty((*x.shape[:-1], c // group if group else 1), device=device, dtype=torch.float32)
+    _call(device, load_library().ssm_add_norm_e4m3, x.data_ptr(), _addr(residual), _addr(weight), y.data_ptr(),
+          scale.data_ptr(), int(group), h.data_ptr(), rows, c, float(eps), code, rcode)
+    return y, scale, h
+
+
+def ssm_add_norm_bwd(h: torch.Tensor, dy: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                     dh: Optional[torch.Tensor] = None, eps: float = 1e-5, want_dx: bool = True,
+                     want_dresidual: bool = True, want_dweight: bool = True):
+    """Gradients of ssm_add_norm (see ``ssm_add_norm_bwd`` in include/ssm_scan.h) for dy like its y and dh like its h
+    (None: zero).  Returns (dx, dresidual, dweight float32), None where not asked for; where the residual has the dtype
+    of x, dresidual is dx itself."""
+    device, dt, rows, c = _rows(dy, "dy")
+    rt = h.dtype if isinstance(h, torch.Tensor) else None
+    if rt != torch.float32 and rt != dt:
+        raise TypeError("h must be float32 or of the dtype of dy")
+    _need(h, "h", rt, device, dy.shape)
+    if dh is not None:
+        _need(dh, "dh", rt, device, dy.shape)
+    if weight is not None:
+        _need(weight, "weight", torch.float32, device, (c,))
+    same = rt == dt
+    dx = torch.empty_like(dy) if want_dx or (same and want_dresidual) else None
+    dres = torch.empty_like(h) if want_dresidual and not same else None
+    dw = torch.empty((c,), device=device, dtype=torch.float32) if want_dweight else None
+    code, rcode = (SSM_F32 if t == torch.float32 else SSM_BF16 for t in (dt, rt))
+    ws, nws = _workspace("ssm_add_norm_workspace", device, rows, c) if want_dweight else (None, 0)
+    _call(device, load_library().ssm_add_norm_bwd, h.data_ptr(), _addr(weight), dy.data_ptr(), _addr(dh), _addr(dx),
+          _addr(dres), _addr(dw), _addr(ws), nws, rows, c, float(eps), code, rcode)
+    return dx if want_dx else None, (dx if same else dres) if want_dresidual else None, dw
 
 
 def ssm_linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None,

@@ -10,6 +10,7 @@ marshalling only; every step runs in the library's kernels.
     o, last_state = head_scan(q, k, v, g=g)   # one decay per head, matrix state
     o, last_state = delta_scan(q, k, v, beta, g=g)   # the same with the gated delta rule
     y = gate_norm(x, weight, z, groups=heads)   # grouped norm of token rows with a SiLU gate
+    y, h = add_norm(x, residual, weight)   # h = x + residual, its root-mean-square norm
     out = linear(y, W, bias, residual, act="silu")   # act(y W^T + bias) + residual
 
 Gradients flow to every tensor argument that requires them (dB and dC are
@@ -22,11 +23,12 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (ssm_delta_scan_bwd, ssm_delta_scan_fwd, ssm_gate_norm, ssm_gate_norm_bwd, ssm_head_scan_bwd, ssm_head_scan_fwd, ssm_linear, ssm_linear_bwd,
+from . import (ssm_add_norm, ssm_add_norm_bwd, ssm_delta_scan_bwd, ssm_delta_scan_fwd, ssm_gate_norm, ssm_gate_norm_bwd, ssm_head_scan_bwd, ssm_head_scan_fwd, ssm_linear, ssm_linear_bwd,
                ssm_out_proj, ssm_out_proj_bwd, ssm_scan_bwd, ssm_scan_bwd_conv,
                ssm_scan_fwd_conv, ssm_scan_fwd_states)
 
-__all__ = ["selective_scan", "selective_scan_conv", "out_proj", "head_scan", "delta_scan", "gate_norm", "linear"]
+__all__ = ["selective_scan", "selective_scan_conv", "out_proj", "head_scan", "delta_scan", "gate_norm", "add_norm",
+           "linear"]
 
 
 def _grad_or_zero(g, like):
@@ -197,6 +199,34 @@ def gate_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, z: Optiona
               eps: float = 1e-5, center: bool = False, gate_first: bool = False) -> torch.Tensor:
     """Differentiable grouped norm of token rows [..., channels] with a SiLU gate."""
     return _GateNorm.apply(x, weight, z, groups, eps, center, gate_first)
+
+
+class _AddNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps, residual_dtype):
+        ctx.set_materialize_grads(False)
+        y, h = ssm_add_norm(x, residual, weight, eps=eps, residual_dtype=residual_dtype)
+        ctx.save_for_backward(h, weight)
+        ctx.eps, ctx.dtype = eps, x.dtype
+        return y, h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh):
+        h, weight = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        # where y is not used dy is zero and so is what it gives
+        dy = h.new_zeros(h.shape, dtype=ctx.dtype) if dy is None else _dense(dy)
+        dx, dres, dw = ssm_add_norm_bwd(h, dy, weight, None if dh is None else _dense(dh), eps=ctx.eps, want_dx=need[0],
+                                        want_dresidual=need[1], want_dweight=need[2])
+        return dx, dres, dw, None, None
+
+
+def add_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+             eps: float = 1e-5, residual_dtype: Optional[torch.dtype] = None):
+    """Differentiable norm of token rows with the residual's addition: returns (y, h).  The gradients of x and of a
+    residual of its dtype are one tensor."""
+    return _AddNorm.apply(x, residual, weight, eps, residual_dtype)
 
 
 class _Linear(torch.autograd.Function):

@@ -1,4 +1,4 @@
-// Host side of the gated norm's and the linear layer's entry points
+// Host side of the norms' and the linear layer's entry points
 // (include/ssm_scan.h): argument checks, all before any HIP call, and launches.
 #include <hip/hip_runtime.h>
 
@@ -78,6 +78,49 @@ int check_linear(ssm::LinearArgs* a, int64_t rows, int64_t k, int64_t m, int act
   return SSM_OK;
 }
 
+int check_add_norm(int64_t rows, int64_t channels, float eps, int dtype, int residual_dtype) {
+  if (rows <= 0 || channels <= 0)
+    return fail(SSM_EINVAL, "sizes must be positive (rows=%lld channels=%lld)", (long long)rows, (long long)channels);
+  if (dtype != SSM_F32 && dtype != SSM_BF16) return fail(SSM_EUNSUPPORTED, "dtype %d is not supported", dtype);
+  if (residual_dtype != SSM_F32 && residual_dtype != dtype)
+    return fail(SSM_EUNSUPPORTED, "residual_dtype %d is not supported: float32 or that of x", residual_dtype);
+  if (channels > ssm::kAddNormMax)
+    return fail(SSM_EUNSUPPORTED, "%lld channels, at most %lld are supported", (long long)channels, (long long)ssm::kAddNormMax);
+  if (!(eps >= 0) || !std::isfinite(eps)) return fail(SSM_EINVAL, "eps must be finite and not negative");
+  int64_t n;
+  if (!mul_ok(rows, channels, &n) || n > (int64_t(1) << 58)) return fail(SSM_EINVAL, "tensor sizes overflow");
+  if (ssm::add_norm_workgroups(rows, channels) >= kMaxWorkgroups)
+    return fail(SSM_EUNSUPPORTED, "too many workgroups for one launch");
+  return SSM_OK;
+}
+
+// scale: the 8-bit form
+int add_norm(const void* x, const void* residual, const float* weight, void* y, float* scale, int64_t group, void* h,
+             int64_t rows, int64_t channels, float eps, int dtype, int residual_dtype, void* stream) {
+  g_err.clear();
+  if (!x || !y) return fail(SSM_EINVAL, "x and y must not be NULL");
+  if (int rc = check_add_norm(rows, channels, eps, dtype, residual_dtype)) return rc;
+  if (scale && group != 0 && group != 32 && group != 64 && group != 128)
+    return fail(SSM_EUNSUPPORTED, "group=%lld is not supported: 0 (a whole row), 32, 64 or 128", (long long)group);
+  if (scale && group != 0 && channels % group != 0)
+    return fail(SSM_EINVAL, "channels=%lld must be a multiple of group=%lld", (long long)channels, (long long)group);
+  const uint64_t n = uint64_t(rows) * channels, nx = n * (dtype == SSM_BF16 ? 2 : 4), nr = n * (residual_dtype == SSM_BF16 ? 2 : 4);
+  const uint64_t ns = uint64_t(rows) * (group != 0 ? channels / group : 1) * 4;
+  const Range rr = range_of(residual, nr), rh = range_of(h, nr);
+  if (residual != h && overlap(rr, rh)) return fail(SSM_EINVAL, "h must equal residual or be disjoint from it");
+  const Range other = residual == h ? range_of(nullptr, 0) : rr;
+  if (int rc = check_ranges({range_of(x, nx), other, range_of(weight, uint64_t(channels) * 4)},
+                            {range_of(y, scale ? n : nx), rh, range_of(scale, ns)}))
+    return rc;
+  ssm::AddNormArgs a{};
+  a.x = x; a.residual = residual; a.w = weight; a.y = y; a.h = h; a.scale = scale;
+  a.rows = rows; a.n = channels; a.group = group; a.eps = eps;
+  const hipError_t e = ssm::launch_add_norm(a, dtype == SSM_BF16, residual_dtype == SSM_F32, scale != nullptr,
+                                            static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "add norm launch");
+  return SSM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -126,6 +169,49 @@ int ssm_gate_norm_bwd(const void* x, const void* z, const float* weight, const v
   const hipError_t e = ssm::launch_gate_norm(a, dtype == SSM_BF16, true, static_cast<float*>(workspace),
                                              static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "gated norm backward launch");
+  return SSM_OK;
+}
+
+int ssm_add_norm(const void* x, const void* residual, const float* weight, void* y, void* h, int64_t rows,
+                 int64_t channels, float eps, int dtype, int residual_dtype, void* stream) {
+  return add_norm(x, residual, weight, y, nullptr, 0, h, rows, channels, eps, dtype, residual_dtype, stream);
+}
+
+int ssm_add_norm_e4m3(const void* x, const void* residual, const float* weight, void* y, float* scale, int64_t group,
+                      void* h, int64_t rows, int64_t channels, float eps, int dtype, int residual_dtype, void* stream) {
+  g_err.clear();
+  if (!scale) return fail(SSM_EINVAL, "scale must not be NULL");
+  return add_norm(x, residual, weight, y, scale, group, h, rows, channels, eps, dtype, residual_dtype, stream);
+}
+
+int ssm_add_norm_workspace(int64_t rows, int64_t channels, int64_t* bytes) {
+  g_err.clear();
+  if (!bytes) return fail(SSM_EINVAL, "bytes must not be NULL");
+  if (int rc = check_add_norm(rows, channels, 0.f, SSM_F32, SSM_F32)) return rc;
+  *bytes = ssm::add_norm_workspace_bytes(rows, channels);
+  return SSM_OK;
+}
+
+int ssm_add_norm_bwd(const void* h, const float* weight, const void* dy, const void* dh, void* dx, void* dresidual,
+                     float* dweight, void* workspace, int64_t workspace_bytes, int64_t rows, int64_t channels, float eps,
+                     int dtype, int residual_dtype, void* stream) {
+  g_err.clear();
+  if (!h || !dy) return fail(SSM_EINVAL, "h and dy must not be NULL");
+  if (!dx && !dresidual && !dweight) return fail(SSM_EINVAL, "at least one of dx, dresidual and dweight must be given");
+  if (int rc = check_add_norm(rows, channels, eps, dtype, residual_dtype)) return rc;
+  const int64_t need = dweight ? ssm::add_norm_workspace_bytes(rows, channels) : 0;
+  if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
+  const uint64_t n = uint64_t(rows) * channels, nx = n * (dtype == SSM_BF16 ? 2 : 4), nr = n * (residual_dtype == SSM_BF16 ? 2 : 4);
+  const uint64_t nw = uint64_t(channels) * 4;
+  if (int rc = check_ranges({range_of(h, nr), range_of(weight, nw), range_of(dy, nx), range_of(dh, nr)},
+                            {range_of(dx, nx), range_of(dresidual, nr), range_of(dweight, nw), range_of(workspace, uint64_t(need))}))
+    return rc;
+  ssm::AddNormArgs a{};
+  a.h = const_cast<void*>(h); a.w = weight; a.dy = dy; a.dh = dh; a.dx = dx; a.dres = dresidual; a.dw = dweight;
+  a.rows = rows; a.n = channels; a.eps = eps;
+  const hipError_t e = ssm::launch_add_norm_bwd(a, dtype == SSM_BF16, residual_dtype == SSM_F32, static_cast<float*>(workspace),
+                                                static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "add norm backward launch");
   return SSM_OK;
 }
 

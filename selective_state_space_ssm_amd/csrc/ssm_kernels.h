@@ -272,6 +272,28 @@ int64_t norm_workspace_bytes(const NormArgs& a, bool bf16);
 int64_t norm_workgroups(const NormArgs& a, bool bf16);
 hipError_t launch_gate_norm(const NormArgs& a, bool bf16, bool backward, float* work, hipStream_t st);
 
+// Root-mean-square norm of dense rows [rows][n] with the residual's addition (ssm_addnorm.hip) and its gradients.
+struct AddNormArgs {
+  const void* x;
+  const void* residual;  // nullable
+  const float* w;        // [n], nullable (ones)
+  void* y;               // type of x, or e4m3
+  void* h;               // type of the residual, nullable; backward: input
+  float* scale;          // e4m3: [rows][n / group], group 0: [rows]
+  const void* dy;        // backward only, with what follows
+  const void* dh;        // nullable
+  void* dx;              // type of x, nullable
+  void* dres;            // type of the residual, nullable
+  float* dw;             // nullable
+  int64_t rows, n, group;
+  float eps;
+};
+constexpr int64_t kAddNormMax = 8192;  // channels
+int64_t add_norm_workspace_bytes(int64_t rows, int64_t n);
+int64_t add_norm_workgroups(int64_t rows, int64_t n);
+hipError_t launch_add_norm(const AddNormArgs& a, bool bf16, bool res32, bool out8, hipStream_t st);
+hipError_t launch_add_norm_bwd(const AddNormArgs& a, bool bf16, bool res32, float* work, hipStream_t st);
+
 // out[c] = sum over k < count of part[k][c], in a fixed order
 hipError_t launch_column_sum(const float* part, int64_t count, int64_t cols, void* out, bool bf16, hipStream_t st);
 
