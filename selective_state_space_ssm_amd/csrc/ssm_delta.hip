@@ -24,7 +24,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 
 #include "ssm_delta_kernel.h"
 #include "ssm_device.h"
@@ -43,8 +42,10 @@ constexpr int64_t kDeltaMinSegment = 8;  // chunks
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
-bool wide_for(int64_t cols, bool vec) { static const char* e = getenv("DW"); return e && cols > 64 && vec; }
-int64_t tiles_for(int64_t cols, bool vec) { return cdiv(cols, wide_for(cols, vec) ? 128 : 64); }
+// Columns of a workgroup's tile: 128 past 128 keys, where there are more than 64 and every operand row is whole vectors,
+// else 64.
+bool wide_for(int64_t rows, int64_t cols, bool vec) { return rows > 128 && cols > 64 && vec; }
+int64_t tiles_for(int64_t rows, int64_t cols, bool vec) { return cdiv(cols, wide_for(rows, cols, vec) ? 128 : 64); }
 
 // States carried over the segments, in order, 16 columns a workgroup: state <- A carried + own, or A^T carried + own
 // from the end.  Float32 matrix instructions, 16 rows a wavefront; the carried columns are in LDS.  A segment's rows of
@@ -243,7 +244,7 @@ Plan plan_of(const DeltaArgs& a, bool bf16) {
   p.nch = cdiv(a.L, p.C);
   p.rp = up(a.dk, 16);
   p.cp = up(a.dv, deltak::kSlab);
-  const int64_t wgs = a.batch * a.H * tiles_for(a.dv, true);
+  const int64_t wgs = a.batch * a.H * tiles_for(a.dk, a.dv, true);
   int64_t want = std::min(kDeltaSlots / wgs, p.nch / kDeltaMinSegment);
   if (want < 6) want = 1;  // a split costs a walk of its own, twice as wide
   p.cps = cdiv(p.nch, want);
@@ -334,13 +335,13 @@ DeltaDev dev_of(const DeltaArgs& a, const Plan& pl, const Space& w, char* work, 
   d.rows = static_cast<int>(a.dk); d.cols = static_cast<int>(a.dv);
   d.rp = static_cast<int>(pl.rp); d.cp = static_cast<int>(pl.cp);
   d.nch = static_cast<int>(pl.nch); d.cps = static_cast<int>(pl.cps); d.nseg = static_cast<int>(pl.nseg);
-  d.nvt = d.ntile = static_cast<int>(tiles_for(a.dv, vec));
+  d.nvt = d.ntile = static_cast<int>(tiles_for(a.dk, a.dv, vec));
   d.scale = a.scale;
   return d;
 }
 
 hipError_t launch_pass(const DeltaDev& d, bool bf16, int pass, bool vec, hipStream_t st) {
-  const bool wide = wide_for(d.cols, vec);
+  const bool wide = wide_for(d.rows, d.cols, vec);
   return bf16 ? launch_delta_bf16(d, pass, wide, vec, st) : launch_delta_f32(d, pass, wide, vec, st);
 }
 
@@ -359,7 +360,7 @@ hipError_t launch_start(const DeltaDev& d, bool bf16, bool vec, hipStream_t st) 
   hipError_t e = launch_pass(d, bf16, deltak::kPassPrep, vec, st);
   if (e != hipSuccess || d.nseg == 1) return e;
   DeltaDev s = d;
-  s.ntile = d.nvt + static_cast<int>(cdiv(d.rp, wide_for(d.cols, vec) ? 128 : 64));
+  s.ntile = d.nvt + static_cast<int>(cdiv(d.rp, wide_for(d.rows, d.cols, vec) ? 128 : 64));
   e = launch_pass(s, bf16, deltak::kPassSeg, vec, st);
   return e == hipSuccess ? launch_carry(d, false, st) : e;
 }

@@ -765,9 +765,8 @@ ssm_delta_kernel(const DeltaDev p) {
 
     // ---- u = b r as an operand of o, e^{G_C - G} u as one of the state's update
     const int yb0 = state_col_base<IO, NK>(li, g);
-    uint4 fu[JS][PP], fw[JS][PS];
-#pragma unroll
-    for (int js = 0; js < JS; ++js) {
+    uint4 fu[JS][PP], fw[2][PS];
+    auto update_parts = [&](int js) {
       float v[E], w[E];
       F32::ld<E>(we + KS * js + E * g, w);
       F32::ld<E>(bt + KS * js + E * g, v);
@@ -777,12 +776,12 @@ ssm_delta_kernel(const DeltaDev p) {
         w[i] = times(w[i], v[i]);
       }
       if constexpr (QUERY) split<IO, PP>(v, fu[js]);
-      split<IO, PS>(w, fw[js]);
-    }
-    uint4 fy[2][JS];
-#pragma unroll
-    for (int js = 0; js < JS; ++js) fy[0][js] = frag_state_col<IO, NK>(ty, yb0, 0, js);
+      split<IO, PS>(w, fw[js & 1]);
+    };
+    update_parts(0);
     if constexpr (QUERY) {
+#pragma unroll
+      for (int js = 1; js < JS; ++js) update_parts(js);
       if constexpr (PP == 2) {
 #pragma unroll
         for (int i = 0, n = 0; i < IB; ++i)
@@ -798,18 +797,28 @@ ssm_delta_kernel(const DeltaDev p) {
           for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n)
             O[i] = q < PP ? mma<IO>(fu[js][q], fm[n], O[i]) : mma<IO>(fu[js][0], fl[n], O[i]);
     }
-    // ---- the state after the chunk
+    // ---- the state after the chunk; under its products the next operand
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      if (rt + 1 < RT) {
+    for (int js = 0; js < JS; ++js) {
+      constexpr int GR = ROWS == 256 ? 2 : 4;  // rows' operands read together
+      uint4 fy[2][GR];
 #pragma unroll
-        for (int js = 0; js < JS; ++js) fy[(rt + 1) & 1][js] = frag_state_col<IO, NK>(ty, yb0, rt + 1, js);
+      for (int i = 0; i < GR; ++i) fy[0][i] = frag_state_col<IO, NK>(ty, yb0, i, js);
+#pragma unroll
+      for (int r = 0; r < RT / GR; ++r) {
+        if (r + 1 < RT / GR) {
+#pragma unroll
+          for (int i = 0; i < GR; ++i) fy[(r + 1) & 1][i] = frag_state_col<IO, NK>(ty, yb0, GR * (r + 1) + i, js);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (!QUERY && r == 0 && js + 1 < JS) update_parts(js + 1);
+#pragma unroll
+        for (int q = 0; q < PS; ++q)
+#pragma unroll
+          for (int i = 0; i < GR; ++i) S[GR * r + i] = mma<IO>(fy[r & 1][i], fw[js & 1][q], S[GR * r + i]);
+        mix<GR * PS, 6>();
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int js = 0; js < JS; ++js)
-#pragma unroll
-        for (int q = 0; q < PS; ++q) S[rt] = mma<IO>(fy[rt & 1][js], fw[js][q], S[rt]);
     }
 
     // ---- outputs, zero in rows past the length
@@ -898,19 +907,24 @@ ssm_delta_rev_kernel(const DeltaDev p) {
 
   uint4 rx[TK::CNT], ry[TK::CNT], rz[TZ::CNT], rm[TM::CNT], rp[TM::CNT], rr[TR::CNT];
   auto load_chunk = [&](int pc) {
-    const int t0 = pc * C, me = ROWS == 256 || !VEC ? opaque(tid) : tid;
+    const int t0 = pc * C, me = ROWS >= 128 || !VEC ? opaque(tid) : tid;
     const int64_t chunk = bh * p.nch + pc;
     TK::template load<VEC>(yb, p.k_t, t0, len, p.rows, me, ry);
     TR::load(reinterpret_cast<const char*>(p.rates + chunk * kRates * C), me, rr);
     TM::load(p.s + chunk * MB, me, rp);
     TZ::template load<VEC>(zb, p.v_t, t0, len, p.cols - col0, me, rz);
-    TM::load(p.m + chunk * MB, me, rm);
+  };
+  // these are asked for half a chunk later: with them the registers do not hold the products' operands
+  auto load_late = [&](int pc) {
+    const int t0 = pc * C, me = ROWS >= 128 || !VEC ? opaque(tid) : tid;
+    TM::load(p.m + (bh * p.nch + pc) * MB, me, rm);
     TK::template load<VEC>(xb, p.q_t, t0, len, p.rows, me, rx);
   };
 
   const int cl = (len + C - 1) / C, ce = c1 < cl ? c1 : cl, nc = ce - c0;
   if (nc > 0) {
     load_chunk(ce - 1);
+    load_late(ce - 1);
     if constexpr (!SEG) {
       // as many stores behind the first loads as the loop has behind its own (see keep)
       const f32x4 none[RT > IB ? RT : IB] = {};
@@ -923,7 +937,7 @@ ssm_delta_rev_kernel(const DeltaDev p) {
     const int pc = ce - 1 - kk, t0 = pc * C;
     __syncthreads();
     {
-      const int me = ROWS == 256 || !VEC ? opaque(tid) : tid;
+      const int me = ROWS >= 128 || !VEC ? opaque(tid) : tid;
       TK::store(ty, me, ry);
       TK::store(tx, me, rx);
       TZ::store(tz, me, rz);
@@ -937,102 +951,145 @@ ssm_delta_rev_kernel(const DeltaDev p) {
     if (kk + 1 < nc) load_chunk(pc - 1);
     if constexpr (!SEG) keep<IO, RT>(p.states + (bh * p.nch + pc) * wsize, p.rp, p.cp, cw + li, g, R);
 
-    // ---- X = K R (rows are tokens)
-    f32x4 X[IB];
+    // ---- X = K R (rows are tokens); the operands of step s + 1 are read and split under the matrix instructions of step s
+    constexpr int LOW = IB == 2 ? 3 : 6;  // operand steps on and below the diagonal
+    f32x4 X[IB], Y[IB];
 #pragma unroll
-    for (int i = 0; i < IB; ++i) X[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < IB; ++i) X[i] = Y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    uint4 fz[JS], ft[LOW], fl[LOW];
+    const int mc0 = state_col_base<IO, NP>(li, g);
+    // columns of a square matrix, its rows as the contraction: what lies below the diagonal of the transposed
+    auto read_square = [&](const char* tile, uint4 (&f)[LOW]) {
+#pragma unroll
+      for (int i = 0, n = 0; i < IB; ++i)
+#pragma unroll
+        for (int js = 0; js < JS; ++js)
+          if (KS * (js + 1) > 16 * i) f[n++] = frag_state_col<IO, NP>(tile, mc0, i, js);
+    };
+    auto times_square = [&](const uint4 (&f)[LOW], const uint4 (&by)[JS], f32x4 (&acc)[IB]) {
+#pragma unroll
+      for (int i = 0, n = 0; i < IB; ++i)
+#pragma unroll
+        for (int js = 0; js < JS; ++js)
+          if (KS * (js + 1) > 16 * i) acc[i] = mma<IO>(f[n++], by[js], acc[i]);
+    };
     {
-      const int sb = opaque(state_row_base<IO, NK>(li, g));
+      const int sb = state_row_base<IO, NK>(li, g), zb0 = col_base<IO, NZ>(li, g);
+      constexpr int NB = ROWS == 256 ? 1 : 2;  // what fits the registers
+      uint4 fk[NB][IB], sp[2][PS];
+      auto read_keys = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < IB; ++i) fk[s % NB][i] = frag_state_row<IO, NK>(ty, sb, i, s);
+      };
+      auto parts = [&](int s) {
+        float v[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = R[tile_of<IO>(s, i)][i & 3];
+        split<IO, PS>(v, sp[s & 1]);
+      };
+      if (NB == 2) read_keys(0);
+      parts(0);
 #pragma unroll
       for (int s = 0; s < RS; ++s) {
-        float v[E];
-        uint4 sp[PS];
+        if (NB == 1) read_keys(s);
+        if (s + 1 < RS) {
+          if (NB == 2) read_keys(s + 1);
+        } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = R[tile_of<IO>(s, e)][e & 3];
-        split<IO, PS>(v, sp);
-#pragma unroll
-        for (int i = 0; i < IB; ++i) {
-          const uint4 fk = frag_state_row<IO, NK>(ty, sb, i, s);
-#pragma unroll
-          for (int q = 0; q < PS; ++q) X[i] = mma<IO>(fk, sp[q], X[i]);
+          for (int js = 0; js < JS; ++js) fz[js] = frag_col<IO, NZ>(tz, zb0, wave, js);
+          read_square(tp, ft);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + 1 < RS) parts(s + 1);
+#pragma unroll
+        for (int q = 0; q < PS; ++q)
+#pragma unroll
+          for (int i = 0; i < IB; ++i) X[i] = mma<IO>(fk[s % NB][i], sp[s & 1][q], X[i]);
+        mix<IB * PS, 4>();
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     // ---- y = P^T dO + e^{G_C - G} X
-    uint4 fz[JS];
-    const int zb0 = opaque(col_base<IO, NZ>(li, g));
+    if constexpr (PP == 2) read_square(tp + C * C * ES, fl);
+    __builtin_amdgcn_sched_barrier(0);
+    times_square(ft, fz, Y);
+    if constexpr (PP == 2) times_square(fl, fz, Y);
+    read_square(tm, ft);
+    if constexpr (PP == 2) read_square(tm + C * C * ES, fl);
+    __builtin_amdgcn_sched_barrier(0);
+    // ---- e = y - M^T (b y)
+    uint4 by[PS][JS];
 #pragma unroll
     for (int js = 0; js < JS; ++js) {
-      float w[E];
+      float w[E], bb[E];
+      uint4 f[PS];
       F32::ld<E>(we + KS * js + E * g, w);
-      fz[js] = frag_col<IO, NZ>(tz, zb0, wave, js);
+      F32::ld<E>(bt + KS * js + E * g, bb);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         const int t = tile_of<IO>(js, i);
-        X[t][i & 3] = times(w[i], X[t][i & 3]);
+        X[t][i & 3] = Y[t][i & 3] + times(w[i], X[t][i & 3]);
+        bb[i] *= X[t][i & 3];
       }
+      split<IO, PS>(bb, f);
+#pragma unroll
+      for (int q = 0; q < PS; ++q) by[q][js] = f[q];
     }
-    const int mc0 = opaque(state_col_base<IO, NP>(li, g));
+    __builtin_amdgcn_sched_barrier(0);
+    // What the state before the chunk is made of, one operand after the other: scale e^G dO (with Q's rows), then
+    // -e^G b e (with K's); each is split under the products of the one before, the first under those of M.
+    uint4 fw[2][PS];
+    auto parts = [&](int n) {
+      const int js = n % JS;
+      float e[E], v[E];
+      F32::ld<E>(ek + KS * js + E * g, e);
+      if (n < JS) {
+        unpack<IO>(fz[js], v);
 #pragma unroll
-    for (int i = 0; i < IB; ++i)
+        for (int i = 0; i < E; ++i) v[i] = times(p.scale * e[i], v[i]);
+      } else {
+        F32::ld<E>(bt + KS * js + E * g, v);
 #pragma unroll
-      for (int js = 0; js < JS; ++js) {
-        if (KS * (js + 1) <= 16 * i) continue;  // above the diagonal of the transposed
-        X[i] = mma<IO>(frag_state_col<IO, NP>(tp, mc0, i, js), fz[js], X[i]);
-        if constexpr (PP == 2) X[i] = mma<IO>(frag_state_col<IO, NP>(tp + C * C * ES, mc0, i, js), fz[js], X[i]);
+        for (int i = 0; i < E; ++i) v[i] = -times(e[i], v[i] * X[tile_of<IO>(js, i)][i & 3]);
       }
-    // ---- e = y - M^T (b y)
-    uint4 by[JS][PS];
-#pragma unroll
-    for (int js = 0; js < JS; ++js) {
-      float bb[E];
-      F32::ld<E>(bt + KS * js + E * g, bb);
-#pragma unroll
-      for (int i = 0; i < E; ++i) bb[i] *= X[tile_of<IO>(js, i)][i & 3];
-      split<IO, PS>(bb, by[js]);
-    }
-#pragma unroll
-    for (int i = 0; i < IB; ++i)
-#pragma unroll
-      for (int js = 0; js < JS; ++js) {
-        if (KS * (js + 1) <= 16 * i) continue;
-        const uint4 fm = frag_state_col<IO, NP>(tm, mc0, i, js);
-#pragma unroll
-        for (int q = 0; q < PS; ++q) X[i] = mma<IO>(fm, by[js][q], X[i]);
-        if constexpr (PP == 2) {
-          const uint4 fl = frag_state_col<IO, NP>(tm + C * C * ES, mc0, i, js);
-          X[i] = mma<IO>(fl, by[js][0], X[i]);
-          X[i] = mma<IO>(fl, by[js][1], X[i]);
-        }
-      }
-    if constexpr (!SEG) keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp, C, p.cp, cw + li, g, X);
-
-    // ---- the state before the chunk
+      split<IO, PS>(v, fw[n & 1]);
+    };
+    parts(0);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) scale(R[rt], end_dec);
-    const int yb0 = opaque(state_col_base<IO, NK>(li, g));
 #pragma unroll
-    for (int js = 0; js < JS; ++js) {
-      float e[E], bb[E], v[E], w[E];
-      F32::ld<E>(ek + KS * js + E * g, e);
-      F32::ld<E>(bt + KS * js + E * g, bb);
-      unpack<IO>(fz[js], v);
+    for (int q = 0; q < PS; ++q) times_square(ft, by[q], X);
+    if constexpr (PP == 2) {
+      times_square(fl, by[0], X);
+      times_square(fl, by[1], X);
+    }
+    mix<LOW * (PS + (PP == 2 ? 2 : 0)), 3>();
+    __builtin_amdgcn_sched_barrier(0);
+    if (kk + 1 < nc) load_late(pc - 1);
+    if constexpr (!SEG) keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp, C, p.cp, cw + li, g, X);
+
+    const int yb0 = state_col_base<IO, NK>(li, g);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        w[i] = -times(e[i], bb[i] * X[tile_of<IO>(js, i)][i & 3]);
-        v[i] = times(p.scale * e[i], v[i]);
-      }
-      uint4 fo[PS], fe[PS];
-      split<IO, PS>(v, fo);
-      split<IO, PS>(w, fe);
+    for (int n = 0; n < 2 * JS; ++n) {
+      const char* const tile = n < JS ? tx : ty;
+      constexpr int GR = ROWS == 256 ? 2 : 4;  // rows' operands read together
+      uint4 fx[2][GR];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const uint4 fx = frag_state_col<IO, NK>(tx, yb0, rt, js), fy = frag_state_col<IO, NK>(ty, yb0, rt, js);
+      for (int i = 0; i < GR; ++i) fx[0][i] = frag_state_col<IO, NK>(tile, yb0, i, n % JS);
 #pragma unroll
-        for (int q = 0; q < PS; ++q) {
-          R[rt] = mma<IO>(fx, fo[q], R[rt]);
-          R[rt] = mma<IO>(fy, fe[q], R[rt]);
+      for (int r = 0; r < RT / GR; ++r) {
+        if (r + 1 < RT / GR) {
+#pragma unroll
+          for (int i = 0; i < GR; ++i) fx[(r + 1) & 1][i] = frag_state_col<IO, NK>(tile, yb0, GR * (r + 1) + i, n % JS);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (r == 0 && n + 1 < 2 * JS) parts(n + 1);
+#pragma unroll
+        for (int q = 0; q < PS; ++q)
+#pragma unroll
+          for (int i = 0; i < GR; ++i) R[GR * r + i] = mma<IO>(fx[r & 1][i], fw[n & 1][q], R[GR * r + i]);
+        mix<GR * PS, 5>();
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -1562,13 +1619,15 @@ hipError_t launch_grad_t(const DeltaGradDev& d, hipStream_t st) {
   return hipGetLastError();
 }
 
-// `wide` is a tile of 128 columns, eight wavefronts of 16, else 64 and four.
+// Four wavefronts of 16 columns: with eight for 128 the prompts below take as long and the training's 256 walks of 4 x
+// 2048 tokens, 32 heads of 128 x 128, half as long again.  `wide` is eight: past 128 keys LDS holds one workgroup a CU
+// either way.
 enum { kPassPrep, kPassOut, kPassSeg, kPassStates, kPassRevSeg, kPassRev };
 
 template <typename IO, int ROWS, bool VEC>
 hipError_t launch_pass_r(const DeltaDev& p, int pass, bool wide, hipStream_t st) {
   if (pass == kPassPrep) return launch_prep_t<IO, ROWS, VEC>(p, st);
-  if constexpr (VEC) {
+  if constexpr (VEC && ROWS == 256) {
     if (wide) {
       if (pass == kPassOut) return launch_walk_t<IO, ROWS, 8, kDeltaOut, VEC>(p, st);
       if (pass == kPassSeg) return launch_walk_t<IO, ROWS, 8, kDeltaSeg, VEC>(p, st);
