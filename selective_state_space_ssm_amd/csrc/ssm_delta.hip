@@ -8,8 +8,9 @@
 // carry over segments of the length and the step.
 //
 //   forwards   M of all chunks | [segments' own ends and transitions, carry] | the walk with the outputs
-//   backwards  M | [segments] | the walk that keeps the states and r | [segments from the end] | the walk from the
-//              end that keeps R and e | all other gradients, all chunks at once | [sums over shared heads]
+//   backwards  M, P | [segments, from the start and from the end, carries] | the walk that keeps the states and r beside
+//              the one from the end that keeps R and e | all other gradients, all chunks at once | [sums over shared
+//              heads]
 //
 // The walk is a chain of chunks; where batch rows, heads and column tiles leave
 // CUs idle the length is cut into segments.  A segment makes A S + B of the state
@@ -340,9 +341,9 @@ DeltaDev dev_of(const DeltaArgs& a, const Plan& pl, const Space& w, char* work, 
   return d;
 }
 
-hipError_t launch_pass(const DeltaDev& d, bool bf16, int pass, bool vec, hipStream_t st) {
+hipError_t launch_pass(const DeltaDev& d, const DeltaDev& r, bool bf16, int pass, bool vec, hipStream_t st) {
   const bool wide = wide_for(d.rows, d.cols, vec);
-  return bf16 ? launch_delta_bf16(d, pass, wide, vec, st) : launch_delta_f32(d, pass, wide, vec, st);
+  return bf16 ? launch_delta_bf16(d, r, pass, wide, vec, st) : launch_delta_f32(d, r, pass, wide, vec, st);
 }
 
 hipError_t launch_carry(const DeltaDev& d, bool rev, hipStream_t st) {
@@ -355,14 +356,10 @@ hipError_t launch_carry(const DeltaDev& d, bool rev, hipStream_t st) {
   return hipGetLastError();
 }
 
-// M, P and the decays of all chunks, and the states at the segments' ends
-hipError_t launch_start(const DeltaDev& d, bool bf16, bool vec, hipStream_t st) {
-  hipError_t e = launch_pass(d, bf16, deltak::kPassPrep, vec, st);
-  if (e != hipSuccess || d.nseg == 1) return e;
-  DeltaDev s = d;
-  s.ntile = d.nvt + static_cast<int>(cdiv(d.rp, wide_for(d.rows, d.cols, vec) ? 128 : 64));
-  e = launch_pass(s, bf16, deltak::kPassSeg, vec, st);
-  return e == hipSuccess ? launch_carry(d, false, st) : e;
+// with the tiles of the transitions
+DeltaDev with_transitions(DeltaDev d, bool vec) {
+  d.ntile = d.nvt + static_cast<int>(cdiv(d.rp, wide_for(d.rows, d.cols, vec) ? 128 : 64));
+  return d;
 }
 
 }  // namespace
@@ -374,15 +371,19 @@ int64_t delta_workspace_bytes(const DeltaArgs& a, bool bf16, bool backward) {
 int64_t delta_workgroups(const DeltaArgs& a, bool bf16, bool backward) {
   const Plan pl = plan_of(a, bf16);
   const int64_t bh = a.batch * a.H, tiles = cdiv(a.dv, 64) + cdiv(pl.rp, 64);
-  return std::max(2 * bh * pl.nch, 2 * bh * tiles * pl.nseg);  // the larger workgroups have 512 threads
+  return std::max(2 * bh * pl.nch, 4 * bh * tiles * pl.nseg);  // the larger workgroups have 512 threads
 }
 
 hipError_t launch_delta_fwd(const DeltaArgs& a, bool bf16, char* work, hipStream_t st) {
   const Plan pl = plan_of(a, bf16);
   const bool vec = all_vec(a, bf16);
   const DeltaDev d = dev_of(a, pl, space_of(a, pl, false), work, bf16, vec);
-  const hipError_t e = launch_start(d, bf16, vec, st);
-  return e == hipSuccess ? launch_pass(d, bf16, deltak::kPassOut, vec, st) : e;
+  hipError_t e = launch_pass(d, d, bf16, deltak::kPassPrep, vec, st);
+  if (e == hipSuccess && pl.nseg > 1) {
+    e = launch_pass(with_transitions(d, vec), d, bf16, deltak::kPassSeg, vec, st);
+    if (e == hipSuccess) e = launch_carry(d, false, st);
+  }
+  return e == hipSuccess ? launch_pass(d, d, bf16, deltak::kPassOut, vec, st) : e;
 }
 
 hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream_t st) {
@@ -392,10 +393,6 @@ hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   const int64_t es = bf16 ? 2 : 4;
   DeltaDev d = dev_of(a, pl, w, work, bf16, vec);
   d.last = nullptr;
-  hipError_t e = launch_start(d, bf16, vec, st);
-  if (e == hipSuccess) e = launch_pass(d, bf16, deltak::kPassStates, vec, st);
-  if (e != hipSuccess) return e;
-
   DeltaDev r = d;
   r.v = static_cast<const char*>(a.dout);
   r.v_b = a.L * a.H * a.dv * es;
@@ -405,12 +402,13 @@ hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   r.seg_state = reinterpret_cast<float*>(work + w.rs);
   r.states = reinterpret_cast<float*>(work + w.r1);
   r.res = reinterpret_cast<float*>(work + w.e);
-  if (pl.nseg > 1) {
-    e = launch_pass(r, bf16, deltak::kPassRevSeg, vec, st);
+  hipError_t e = launch_pass(d, d, bf16, deltak::kPassPrep, vec, st);
+  if (e == hipSuccess && pl.nseg > 1) {
+    e = launch_pass(with_transitions(d, vec), r, bf16, deltak::kPassBothSeg, vec, st);
+    if (e == hipSuccess) e = launch_carry(d, false, st);
     if (e == hipSuccess) e = launch_carry(r, true, st);
-    if (e != hipSuccess) return e;
   }
-  e = launch_pass(r, bf16, deltak::kPassRev, vec, st);
+  if (e == hipSuccess) e = launch_pass(d, r, bf16, deltak::kPassBoth, vec, st);
   if (e != hipSuccess) return e;
 
   const int64_t rep = a.H / a.Hk, hn = grad_heads(a, pl);

@@ -471,8 +471,8 @@ constexpr size_t delta_lds_bytes() {
 
 // Workgroups are dealt to the XCDs as the head scan's: the column tiles of a (batch row, head, segment) follow each
 // other on one XCD.
-__device__ __forceinline__ void place(const DeltaDev& p, int nrun, int& ct, int& seg, int& h, int& b) {
-  const uint32_t pid = blockIdx.x, nt = p.ntile, whole = gridDim.x / nt / 8 * 8 * nt;
+__device__ __forceinline__ void place(const DeltaDev& p, uint32_t pid, int nrun, int& ct, int& seg, int& h, int& b) {
+  const uint32_t nt = p.ntile, whole = static_cast<uint32_t>(nrun) * p.H * p.batch / 8 * 8 * nt;
   uint32_t idx = pid / nt;
   ct = pid % nt;
   if (pid < whole) {
@@ -521,8 +521,7 @@ __device__ __forceinline__ void keep(float* dst, int rows, int cp, int c, int g,
 }
 
 template <typename IO, int ROWS, int NW, int MODE, bool VEC>
-__global__ void __launch_bounds__((64 * NW), 2)
-ssm_delta_kernel(const DeltaDev p) {
+__device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char* lds) {
   using K = HeadCfg<IO>;
   constexpr bool QUERY = MODE == kDeltaOut;
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
@@ -535,7 +534,6 @@ ssm_delta_kernel(const DeltaDev p) {
   using TM = TileM<IO, MB, NP, T>;
   using TR = Flat<kRates * C * 4, T>;
 
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   char* const ty = lds;
   char* const tz = ty + C * ROWS * ES;
   char* const tm = tz + C * COLS * ES;
@@ -549,7 +547,7 @@ ssm_delta_kernel(const DeltaDev p) {
   const int tid = static_cast<int>(threadIdx.x);
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int ct, seg, h, b;
-  place(p, MODE == kDeltaSeg ? p.nseg - 1 : p.nseg, ct, seg, h, b);
+  place(p, pid, MODE == kDeltaSeg ? p.nseg - 1 : p.nseg, ct, seg, h, b);
   const bool trans = MODE == kDeltaSeg && ct >= p.nvt;
   if (trans) {
     if (seg == 0) return;  // its state before is the start state
@@ -850,16 +848,18 @@ ssm_delta_kernel(const DeltaDev p) {
   }
 }
 
-// ---------------------------------------------------------------- the walk over the length, backwards
+template <typename IO, int ROWS, int NW, int MODE, bool VEC>
+__global__ void __launch_bounds__((64 * NW), 2) ssm_delta_kernel(const DeltaDev p) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  delta_walk<IO, ROWS, NW, MODE, VEC>(p, blockIdx.x, lds);
+}
 
-template <typename IO, int ROWS, int NW>
-constexpr size_t delta_rev_lds_bytes() { return delta_lds_bytes<IO, ROWS, NW, true>(); }
+// ---------------------------------------------------------------- the walk over the length, backwards
 
 // v is dO, h0 dlast, last dh0.  SEG: a segment's own R at its first token, from zero (the last segment: from dlast);
 // else R after every chunk and e are written.
 template <typename IO, int ROWS, int NW, bool SEG, bool VEC>
-__global__ void __launch_bounds__((64 * NW), 2)
-ssm_delta_rev_kernel(const DeltaDev p) {
+__device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid, char* lds) {
   using K = HeadCfg<IO>;
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
   constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
@@ -871,7 +871,6 @@ ssm_delta_rev_kernel(const DeltaDev p) {
   using TM = TileM<IO, MB, NP, T>;
   using TR = Flat<kRates * C * 4, T>;
 
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   char* const ty = lds;
   char* const tz = ty + C * ROWS * ES;
   char* const tm = tz + C * COLS * ES;
@@ -885,7 +884,7 @@ ssm_delta_rev_kernel(const DeltaDev p) {
   const int tid = static_cast<int>(threadIdx.x);
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int ct, seg, h, b;
-  place(p, SEG ? p.nseg - 1 : p.nseg, ct, seg, h, b);
+  place(p, pid, SEG ? p.nseg - 1 : p.nseg, ct, seg, h, b);
   if constexpr (SEG) ++seg;
   const int c0 = seg * p.cps, c1 = c0 + p.cps < p.nch ? c0 + p.cps : p.nch;
   const int len = length_of(p, b);
@@ -1097,6 +1096,15 @@ ssm_delta_rev_kernel(const DeltaDev p) {
   const int g = (tid & 63) >> 4, c = cw + (tid & 15);
   if constexpr (SEG) store_state<IO, RT>(p.seg_state + (bh * p.nseg + seg) * wsize, p.rp, p.cp, p.cp, c, g, R);
   else if (p.last != nullptr && seg == 0) store_state<IO, RT>(p.last + bh * p.rows * p.cols, p.rows, p.cols, p.cols, c, g, R);
+}
+
+// The backward's two walks need nothing of each other: the first half of the workgroups walks forwards, the second half
+// backwards, so that the stores of one lie under the products of the other.  SEG: the segments' own ends.
+template <typename IO, int ROWS, int NW, bool SEG, bool VEC>
+__global__ void __launch_bounds__((64 * NW), 2) ssm_delta_both_kernel(const DeltaDev p, const DeltaDev r, uint32_t first) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  if (blockIdx.x < first) delta_walk<IO, ROWS, NW, SEG ? kDeltaSeg : kDeltaStates, VEC>(p, blockIdx.x, lds);
+  else delta_walk_back<IO, ROWS, NW, SEG, VEC>(r, blockIdx.x - first, lds);
 }
 
 // ---------------------------------------------------------------- the gradients, all chunks at once
@@ -1597,13 +1605,14 @@ hipError_t launch_walk_t(const DeltaDev& p, hipStream_t st) {
 }
 
 template <typename IO, int ROWS, int NW, bool SEG, bool VEC>
-hipError_t launch_rev_t(const DeltaDev& p, hipStream_t st) {
+hipError_t launch_both_t(const DeltaDev& p, const DeltaDev& r, hipStream_t st) {
   static std::atomic<uint64_t> allowed{0};
-  constexpr size_t smem = delta_rev_lds_bytes<IO, ROWS, NW>();
-  const int64_t nrun = SEG ? p.nseg - 1 : p.nseg;
-  auto kern = ssm_delta_rev_kernel<IO, ROWS, NW, SEG, VEC>;
+  constexpr size_t smem = delta_lds_bytes<IO, ROWS, NW, true>();
+  const int64_t runs = (SEG ? p.nseg - 1 : p.nseg) * static_cast<int64_t>(p.H) * p.batch;
+  auto kern = ssm_delta_both_kernel<IO, ROWS, NW, SEG, VEC>;
   if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(nrun * p.ntile * p.H * p.batch)), dim3(64 * NW), smem, st, p);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(runs * (p.ntile + r.ntile))), dim3(64 * NW), smem, st, p, r,
+                     static_cast<uint32_t>(runs * p.ntile));
   return hipGetLastError();
 }
 
@@ -1622,32 +1631,30 @@ hipError_t launch_grad_t(const DeltaGradDev& d, hipStream_t st) {
 // Four wavefronts of 16 columns: with eight for 128 the prompts below take as long and the training's 256 walks of 4 x
 // 2048 tokens, 32 heads of 128 x 128, half as long again.  `wide` is eight: past 128 keys LDS holds one workgroup a CU
 // either way.
-enum { kPassPrep, kPassOut, kPassSeg, kPassStates, kPassRevSeg, kPassRev };
+enum { kPassPrep, kPassOut, kPassSeg, kPassBoth, kPassBothSeg };
+
+template <typename IO, int ROWS, int NW, bool VEC>
+hipError_t launch_pass_n(const DeltaDev& p, const DeltaDev& r, int pass, hipStream_t st) {
+  if (pass == kPassOut) return launch_walk_t<IO, ROWS, NW, kDeltaOut, VEC>(p, st);
+  if (pass == kPassSeg) return launch_walk_t<IO, ROWS, NW, kDeltaSeg, VEC>(p, st);
+  if (pass == kPassBoth) return launch_both_t<IO, ROWS, NW, false, VEC>(p, r, st);
+  return launch_both_t<IO, ROWS, NW, true, VEC>(p, r, st);
+}
 
 template <typename IO, int ROWS, bool VEC>
-hipError_t launch_pass_r(const DeltaDev& p, int pass, bool wide, hipStream_t st) {
+hipError_t launch_pass_r(const DeltaDev& p, const DeltaDev& r, int pass, bool wide, hipStream_t st) {
   if (pass == kPassPrep) return launch_prep_t<IO, ROWS, VEC>(p, st);
-  if constexpr (VEC && ROWS == 256) {
-    if (wide) {
-      if (pass == kPassOut) return launch_walk_t<IO, ROWS, 8, kDeltaOut, VEC>(p, st);
-      if (pass == kPassSeg) return launch_walk_t<IO, ROWS, 8, kDeltaSeg, VEC>(p, st);
-      if (pass == kPassStates) return launch_walk_t<IO, ROWS, 8, kDeltaStates, VEC>(p, st);
-      if (pass == kPassRevSeg) return launch_rev_t<IO, ROWS, 8, true, VEC>(p, st);
-      return launch_rev_t<IO, ROWS, 8, false, VEC>(p, st);
-    }
-  }
-  if (pass == kPassOut) return launch_walk_t<IO, ROWS, 4, kDeltaOut, VEC>(p, st);
-  if (pass == kPassSeg) return launch_walk_t<IO, ROWS, 4, kDeltaSeg, VEC>(p, st);
-  if (pass == kPassStates) return launch_walk_t<IO, ROWS, 4, kDeltaStates, VEC>(p, st);
-  if (pass == kPassRevSeg) return launch_rev_t<IO, ROWS, 4, true, VEC>(p, st);
-  return launch_rev_t<IO, ROWS, 4, false, VEC>(p, st);
+  if constexpr (VEC && ROWS == 256)
+    if (wide) return launch_pass_n<IO, ROWS, 8, VEC>(p, r, pass, st);
+  return launch_pass_n<IO, ROWS, 4, VEC>(p, r, pass, st);
 }
 
 template <typename IO>
-hipError_t launch_pass_io(const DeltaDev& p, int pass, bool wide, bool vec, hipStream_t st) {
-  if (p.rows <= 64) return vec ? launch_pass_r<IO, 64, true>(p, pass, wide, st) : launch_pass_r<IO, 64, false>(p, pass, wide, st);
-  if (p.rows <= 128) return vec ? launch_pass_r<IO, 128, true>(p, pass, wide, st) : launch_pass_r<IO, 128, false>(p, pass, wide, st);
-  return vec ? launch_pass_r<IO, 256, true>(p, pass, wide, st) : launch_pass_r<IO, 256, false>(p, pass, wide, st);
+hipError_t launch_pass_io(const DeltaDev& p, const DeltaDev& r, int pass, bool wide, bool vec, hipStream_t st) {
+  if (p.rows <= 64) return vec ? launch_pass_r<IO, 64, true>(p, r, pass, wide, st) : launch_pass_r<IO, 64, false>(p, r, pass, wide, st);
+  if (p.rows <= 128)
+    return vec ? launch_pass_r<IO, 128, true>(p, r, pass, wide, st) : launch_pass_r<IO, 128, false>(p, r, pass, wide, st);
+  return vec ? launch_pass_r<IO, 256, true>(p, r, pass, wide, st) : launch_pass_r<IO, 256, false>(p, r, pass, wide, st);
 }
 
 template <typename IO>
@@ -1659,9 +1666,9 @@ hipError_t launch_grad_io(const DeltaGradDev& d, bool vec, hipStream_t st) {
 
 }  // namespace deltak
 
-// One pass; ROWS is d_key rounded up to 64, 128 or 256 (one source file per type and forwards or backwards).
-hipError_t launch_delta_bf16(const deltak::DeltaDev& p, int pass, bool wide, bool vec, hipStream_t st);
-hipError_t launch_delta_f32(const deltak::DeltaDev& p, int pass, bool wide, bool vec, hipStream_t st);
+// One pass (r: the walk backwards, where the pass has one); ROWS is d_key rounded up to 64, 128 or 256.
+hipError_t launch_delta_bf16(const deltak::DeltaDev& p, const deltak::DeltaDev& r, int pass, bool wide, bool vec, hipStream_t st);
+hipError_t launch_delta_f32(const deltak::DeltaDev& p, const deltak::DeltaDev& r, int pass, bool wide, bool vec, hipStream_t st);
 hipError_t launch_delta_grad_bf16(const deltak::DeltaGradDev& d, bool vec, hipStream_t st);
 hipError_t launch_delta_grad_f32(const deltak::DeltaGradDev& d, bool vec, hipStream_t st);
 
