@@ -129,49 +129,44 @@ struct DeltaStepDev {
 };
 
 template <typename IO, int ROWS, bool VEC>
-__global__ void __launch_bounds__(256) ssm_delta_step_kernel(DeltaStepDev p) {
-  using T = typename IO::T;
-  constexpr int N = ROWS / 32;  // rows per thread
+__global__ void __launch_bounds__(256, (ROWS == 256 || !VEC ? 4 : 8)) ssm_delta_step_kernel(DeltaStepDev p) {
+  using B = typename BufOf<IO>::type;
+  constexpr int N = ROWS / 32, ES = sizeof(typename IO::T);  // rows per thread
+  constexpr uint32_t kOOB = headk::kOOB;
   __shared__ float sh[4][2][32], shq[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int dk = static_cast<int>(p.dk), dv = static_cast<int>(p.dv);
   const int64_t ct = blockIdx.x % p.ntile, bh = blockIdx.x / p.ntile, b = bh / p.H, h = bh % p.H;
-  const int64_t c = ct * 32 + 4 * (tid & 7);
-  const int rg = tid >> 3;
-  const T* q = reinterpret_cast<const T*>(p.q) + (b * p.Hk + h / (p.H / p.Hk)) * p.dk;
-  const T* k = reinterpret_cast<const T*>(p.k) + (b * p.Hk + h / (p.H / p.Hk)) * p.dk;
-  const T* v = reinterpret_cast<const T*>(p.v) + bh * p.dv;
+  const int64_t hk = b * p.Hk + h / (p.H / p.Hk);
+  const int c = static_cast<int>(ct) * 32 + 4 * (tid & 7), rg = tid >> 3;
+  // resources bound the rows: nothing past them is read (it is zero) or written
+  const Rsrc rin = make_rsrc(p.in + bh * p.dk * p.dv, static_cast<uint32_t>(dk * dv * 4));
+  const Rsrc rq = make_rsrc(p.q + hk * p.dk * ES, static_cast<uint32_t>(dk * ES));
+  const Rsrc rk = make_rsrc(p.k + hk * p.dk * ES, static_cast<uint32_t>(dk * ES));
+  const Rsrc rv = make_rsrc(p.v + bh * p.dv * ES, static_cast<uint32_t>(dv * ES));
+  const uint32_t off = static_cast<uint32_t>(rg * dv + c) * 4, step = static_cast<uint32_t>(32 * dv) * 4;
   float s[N][4], kk[N], qq[N], vv[4];
-  const int64_t base = bh * p.dk * p.dv + c;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int64_t r = rg + 32 * i;
+    if constexpr (VEC) {
+      const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rin, c < dv ? off + i * step : kOOB, 0, kCacheNT);
+      s[i][0] = __uint_as_float(x.x); s[i][1] = __uint_as_float(x.y);
+      s[i][2] = __uint_as_float(x.z); s[i][3] = __uint_as_float(x.w);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
-    kk[i] = qq[i] = 0.f;
-    if (r < p.dk) {
-      if constexpr (VEC) {
-        if (c < p.dv) {
-          const headk::f32x4 x = __builtin_nontemporal_load(reinterpret_cast<const headk::f32x4*>(p.in + base + r * p.dv));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][e] = x[e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c + e < p.dv) s[i][e] = p.in[base + r * p.dv + e];
-      }
-      IO::template ld<1>(k + r, &kk[i]);
-      IO::template ld<1>(q + r, &qq[i]);
+      for (int e = 0; e < 4; ++e) BufF32::ld<1>(rin, c + e < dv ? off + i * step + 4 * e : kOOB, &s[i][e]);
     }
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    vv[e] = 0.f;
-    if (c + e < p.dv) IO::template ld<1>(v + c + e, &vv[e]);
+  for (int i = 0; i < N; ++i) {
+    B::template ld<1>(rk, (rg + 32 * i) * ES, &kk[i]);
+    B::template ld<1>(rq, (rg + 32 * i) * ES, &qq[i]);
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) B::template ld<1>(rv, (c + e) * ES, &vv[e]);
   float a = 0.f, bt = 1.f;
-  if (p.g != nullptr) IO::template ld<1>(reinterpret_cast<const T*>(p.g) + bh, &a);
-  if (p.beta != nullptr) IO::template ld<1>(reinterpret_cast<const T*>(p.beta) + bh, &bt);
+  if (p.g != nullptr) IO::template ld<1>(reinterpret_cast<const typename IO::T*>(p.g) + bh, &a);
+  if (p.beta != nullptr) IO::template ld<1>(reinterpret_cast<const typename IO::T*>(p.beta) + bh, &bt);
   a = __builtin_amdgcn_exp2f(headk::clamp_decay(a * kLog2e));
   float pk[4] = {0.f, 0.f, 0.f, 0.f}, pq[4] = {0.f, 0.f, 0.f, 0.f}, qk = 0.f;
 #pragma unroll
@@ -211,28 +206,25 @@ __global__ void __launch_bounds__(256) ssm_delta_step_kernel(DeltaStepDev p) {
     u[e] = bt * (vv[e] - ((sh[0][0][x] + sh[1][0][x]) + (sh[2][0][x] + sh[3][0][x])));
     y[e] = p.scale * __builtin_fmaf(qk, u[e], (sh[0][1][x] + sh[1][1][x]) + (sh[2][1][x] + sh[3][1][x]));
   }
+  const Rsrc rout = make_rsrc(p.out + bh * p.dk * p.dv, static_cast<uint32_t>(dk * dv * 4));
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int64_t r = rg + 32 * i;
-    if (r < p.dk) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[i][e] = __builtin_fmaf(kk[i], u[e], s[i][e]);
-      if constexpr (VEC) {
-        if (c < p.dv) {
-          const headk::f32x4 x = {s[i][0], s[i][1], s[i][2], s[i][3]};
-          __builtin_nontemporal_store(x, reinterpret_cast<headk::f32x4*>(p.out + base + r * p.dv));
-        }
-      } else {
+    for (int e = 0; e < 4; ++e) s[i][e] = __builtin_fmaf(kk[i], u[e], s[i][e]);
+    if constexpr (VEC) {
+      u32x4 x;
+      x.x = __float_as_uint(s[i][0]); x.y = __float_as_uint(s[i][1]);
+      x.z = __float_as_uint(s[i][2]); x.w = __float_as_uint(s[i][3]);
+      __builtin_amdgcn_raw_buffer_store_b128(x, rout, c < dv ? off + i * step : kOOB, 0, kCacheNT);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c + e < p.dv) p.out[base + r * p.dv + e] = s[i][e];
-      }
+      for (int e = 0; e < 4; ++e) BufF32::st<1>(rout, c + e < dv ? off + i * step + 4 * e : kOOB, &s[i][e]);
     }
   }
   if (rg == 0) {
+    const Rsrc ro = make_rsrc(p.o + bh * p.dv * ES, static_cast<uint32_t>(dv * ES));
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (c + e < p.dv) IO::template st<1>(reinterpret_cast<T*>(p.o) + bh * p.dv + c + e, &y[e]);
+    for (int e = 0; e < 4; ++e) B::template st<1>(ro, (c + e) * ES, &y[e]);
   }
 }
 
