@@ -91,13 +91,14 @@ def delta_step(q, k, v, state, g=None, beta=None, scale=1.0):
 
 
 def delta_scan_errors(q, k, v, do=None, g=None, beta=None, h0=None, lengths=None, scale=1.0, dlast=None, step=2.0 ** -24,
-                      pair=0.0, chunk=64):
+                      pair=0.0, kept=0.0, chunk=64):
     """What each result may be off by before it is rounded to its own type, by the results' names: a bound on the
     2-norm over d_key or d_value of a token's vector (o, dq, dk, dv), on a number (dg, dbeta) or on the norm of a
     state (last, dh0).
 
     ``step``: the error of a sum relative to the product of its vectors' norms.  ``pair``: that of a product of values
-    held in two parts.  A token's write k r^T is off by |k| (step + pair) times what r is made of, |v| + |k| |S|; these
+    held in two parts.  ``kept``: that of the states, r and e as the gradients of q, k, v, g and beta find them (what
+    goes on from token to token does not pass through them).  A token's write k r^T is off by |k| (step + pair) times what r is made of, |v| + |k| |S|; these
     errors of different tokens are independent and are decayed with the state, so their squares add up."""
     Q, K, V, a, bt, live, rep = _prepare(q, k, v, g, beta, lengths)
     b, L, h, _ = Q.shape
@@ -126,8 +127,9 @@ def delta_scan_errors(q, k, v, do=None, g=None, beta=None, h0=None, lengths=None
         ER[:, t] = np.sqrt(after ** 2 + (both * made) ** 2 + (st * Rn[:, t]) ** 2)
     Ee = kn * (ER[:, :L] + both * Rn)
     S0, E0 = a * Sn[:, :L], a * ES[:, :L]
-    out["dv"] = bt * Ee
-    out["dbeta"] = Ee * rn + en * Er + both * en * rn
+    out["dv"] = bt * (Ee + kept * en)
+    out["dbeta"] = Ee * rn + en * Er + (both + 2 * kept) * en * rn
+    both = both + 2 * kept  # two of them in a product
     eq = scale * don * (ES[:, 1:] + both * (Sn[:, 1:] + kn * bt * rn))
     ek = (bt * (ER[:, :L] * rn + Rn * Er + both * Rn * rn) + bt * (E0 * en + S0 * Ee + both * S0 * en))
     heads = lambda x: x.reshape(b, L, h // rep, rep).sum(3)

@@ -273,9 +273,9 @@ int64_t grad_heads(const DeltaArgs& a, const Plan& pl) {
 
 // Where the workspace's parts are, in bytes from its start.
 struct Space {
-  int64_t m, s, rates, ss, rs, trans, s0, r1, r, e, pq, pk, total;
+  int64_t m, s, rates, ss, rs, trans, s0, r1, r, e, s0_by, r1_by, r_by, e_by, pq, pk, total;
 };
-Space space_of(const DeltaArgs& a, const Plan& pl, bool backward) {
+Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
   Space w{};
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -293,10 +293,12 @@ Space space_of(const DeltaArgs& a, const Plan& pl, bool backward) {
     if (backward) w.rs = take(4 * bh * pl.nseg * pl.rp * pl.cp);
   }
   if (backward) {
-    w.s0 = take(4 * bh * pl.nch * pl.rp * pl.cp);
-    w.r1 = take(4 * bh * pl.nch * pl.rp * pl.cp);
-    w.r = take(4 * bh * pl.nch * pl.C * pl.cp);
-    w.e = take(4 * bh * pl.nch * pl.C * pl.cp);
+    const int64_t kept = bf16 ? 2 : 4;
+    w.s0 = take(kept * bh * pl.nch * pl.rp * pl.cp);
+    w.r1 = take(kept * bh * pl.nch * pl.rp * pl.cp);
+    w.r = take(kept * bh * pl.nch * pl.C * pl.cp);
+    w.e = take(kept * bh * pl.nch * pl.C * pl.cp);
+    for (int64_t* by : {&w.s0_by, &w.r1_by, &w.r_by, &w.e_by}) *by = take(bf16 ? 4 * bh * pl.nch * pl.cp / 16 : 0);
     const int64_t hn = grad_heads(a, pl);
     if (hn < a.H / a.Hk) {
       w.pq = take(4 * bh / hn * a.L * a.dk);
@@ -322,8 +324,10 @@ DeltaDev dev_of(const DeltaArgs& a, const Plan& pl, const Space& w, char* work, 
   d.rates = reinterpret_cast<float*>(work + w.rates);
   d.seg_state = reinterpret_cast<float*>(work + w.ss);
   d.seg_trans = reinterpret_cast<float*>(work + w.trans);
-  d.states = reinterpret_cast<float*>(work + w.s0);
-  d.res = reinterpret_cast<float*>(work + w.r);
+  d.states = work + w.s0;
+  d.res = work + w.r;
+  d.states_by = reinterpret_cast<float*>(work + w.s0_by);
+  d.res_by = reinterpret_cast<float*>(work + w.r_by);
   d.batch = static_cast<int>(a.batch); d.H = static_cast<int>(a.H); d.L = static_cast<int>(a.L);
   d.rows = static_cast<int>(a.dk); d.cols = static_cast<int>(a.dv);
   d.rp = static_cast<int>(pl.rp); d.cp = static_cast<int>(pl.cp);
@@ -357,7 +361,7 @@ DeltaDev with_transitions(DeltaDev d, bool vec) {
 }  // namespace
 
 int64_t delta_workspace_bytes(const DeltaArgs& a, bool bf16, bool backward) {
-  return space_of(a, plan_of(a, bf16), backward).total;
+  return space_of(a, plan_of(a, bf16), bf16, backward).total;
 }
 
 int64_t delta_workgroups(const DeltaArgs& a, bool bf16, bool backward) {
@@ -369,7 +373,7 @@ int64_t delta_workgroups(const DeltaArgs& a, bool bf16, bool backward) {
 hipError_t launch_delta_fwd(const DeltaArgs& a, bool bf16, char* work, hipStream_t st) {
   const Plan pl = plan_of(a, bf16);
   const bool vec = all_vec(a, bf16);
-  const DeltaDev d = dev_of(a, pl, space_of(a, pl, false), work, bf16, vec);
+  const DeltaDev d = dev_of(a, pl, space_of(a, pl, bf16, false), work, bf16, vec);
   hipError_t e = launch_pass(d, d, bf16, deltak::kPassPrep, vec, st);
   if (e == hipSuccess && pl.nseg > 1) {
     e = launch_pass(with_transitions(d, vec), d, bf16, deltak::kPassSeg, vec, st);
@@ -381,7 +385,7 @@ hipError_t launch_delta_fwd(const DeltaArgs& a, bool bf16, char* work, hipStream
 hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream_t st) {
   const Plan pl = plan_of(a, bf16);
   const bool vec = all_vec(a, bf16);
-  const Space w = space_of(a, pl, true);
+  const Space w = space_of(a, pl, bf16, true);
   const int64_t es = bf16 ? 2 : 4;
   DeltaDev d = dev_of(a, pl, w, work, bf16, vec);
   d.last = nullptr;
@@ -392,8 +396,10 @@ hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   r.h0 = a.dlast;
   r.last = a.dh0;
   r.seg_state = reinterpret_cast<float*>(work + w.rs);
-  r.states = reinterpret_cast<float*>(work + w.r1);
-  r.res = reinterpret_cast<float*>(work + w.e);
+  r.states = work + w.r1;
+  r.res = work + w.e;
+  r.states_by = reinterpret_cast<float*>(work + w.r1_by);
+  r.res_by = reinterpret_cast<float*>(work + w.e_by);
   hipError_t e = launch_pass(d, d, bf16, deltak::kPassPrep, vec, st);
   if (e == hipSuccess && pl.nseg > 1) {
     e = launch_pass(with_transitions(d, vec), r, bf16, deltak::kPassBothSeg, vec, st);
@@ -408,6 +414,7 @@ hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   gd.f = d;
   gd.f.v = r.v; gd.f.v_b = r.v_b; gd.f.v_t = r.v_t;
   gd.r1 = r.states; gd.e = r.res;
+  gd.r1_by = r.states_by; gd.e_by = r.res_by;
   gd.hn = static_cast<int>(hn);
   gd.parts = hn < rep;
   gd.dq = gd.parts ? work + w.pq : static_cast<char*>(a.dq);

@@ -71,8 +71,10 @@ struct DeltaDev {
   float* rates;                // [b][H][nch][kRates][C]
   float* seg_state;            // [b][H][nseg][rp][cp]
   float* seg_trans;            // [b][H][nseg][rp][rp]: what a segment makes of the state before it
-  float* states;               // [b][H][nch][rp][cp]: the state before (backwards: after) every chunk
-  float* res;                  // [b][H][nch][C][cp]: r, backwards e
+  char* states;                // [b][H][nch][rp][cp]: the state before (backwards: after) every chunk (see keep)
+  char* res;                   // [b][H][nch][C][cp]: r, backwards e, likewise
+  float* states_by;            // [b][H][nch][cp / 16]: what they are to be multiplied with (bfloat16 storage)
+  float* res_by;
   int batch, H, L, rows, cols;
   int rp, cp;                  // rows and columns of states in the workspace: multiples of 16 and of kSlab
   int nch, cps, nseg;          // chunks, chunks per segment, segments
@@ -506,18 +508,68 @@ __device__ __forceinline__ void store_state(float* dst, int rows, int cols, int 
       if (r < rows && c < cols) dst[r * ld + c] = S[rt][v];
     }
 }
-// Accumulator tiles to `rows` rows of cp floats in the workspace (a resource, which bounds the rows; none of it with
+// What the walks leave for the gradients: float32, or with bfloat16 storage float16 of the values over a power of two
+// that a wavefront's 16 columns share and that takes the largest of them to 2^14 .. 2^15.  Off by 2^-11 of a value at
+// most, where the gradients they end in are rounded to 2^-8: a walk writes and the gradients read half the bytes.
+template <typename IO>
+constexpr int kept_size() { return HeadCfg<IO>::ES; }
+
+// Accumulator tiles to `rows` rows of cp values in the workspace (a resource, which bounds the rows; none of it with
 // rows = 0), by instructions whose number does not depend on the sizes: loads and stores are counted together and in
-// order, and the wait for the next chunk's loads can leave these in flight only if their number is known.
+// order, and the wait for the next chunk's loads can leave these in flight only if their number is known.  by: the
+// chunk's cp / 16 factors.
 template <typename IO, int N>
-__device__ __forceinline__ void keep(float* dst, int rows, int cp, int c, int g, const f32x4 (&X)[N]) {
-  const Rsrc r = make_rsrc(dst, static_cast<uint32_t>(rows * cp * 4));
-  const uint32_t off = c < cp ? c * 4 : kOOB;
+__device__ __forceinline__ void keep(char* dst, float* by, int rows, int cp, int c, int g, const f32x4 (&X)[N]) {
+  constexpr int KB = kept_size<IO>();
+  const Rsrc r = make_rsrc(dst, static_cast<uint32_t>(rows * cp * KB));
+  const uint32_t off = c < cp ? c * KB : kOOB;
+  float f = 1.f;
+  if constexpr (KB == 2) {
+    float m = 0.f;
+#pragma unroll
+    for (int rt = 0; rt < N; ++rt)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) m = __builtin_fmaxf(m, __builtin_fabsf(X[rt][v]));
+    auto take = [&](auto ctrl, auto mask) {
+      constexpr int CTRL = decltype(ctrl)::value, ROWS = decltype(mask)::value;
+      m = __builtin_fmaxf(m, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m), CTRL, ROWS, 0xf, false)));
+    };
+    using std::integral_constant;
+    take(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // up within a row of 16, then over the rows
+    take(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+    take(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+    take(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+    take(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
+    take(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
+    // the exponent of the largest, at least that whose factor back is no denormal
+    int e = (__builtin_amdgcn_readlane(__float_as_int(m), 63) >> 23) & 255;
+    e = e < 15 ? 15 : e;
+    f = __int_as_float((268 - e) << 23);
+    const Rsrc rb = make_rsrc(by, rows > 0 ? static_cast<uint32_t>(cp / 16 * 4) : 0u);
+    __builtin_amdgcn_raw_buffer_store_b32(static_cast<uint32_t>(e - 14) << 23, rb, (c & 15) == 0 && g == 0 ? c / 16 * 4 : kOOB, 0, 0);
+  }
 #pragma unroll
   for (int rt = 0; rt < N; ++rt)
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(X[rt][v]), r, off + state_row<IO>(rt, g, v) * cp * 4, 0, 0);
+    for (int v = 0; v < 4; ++v) {
+      const uint32_t to = off + state_row<IO>(rt, g, v) * cp * KB;
+      if constexpr (KB == 2)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<_Float16>(X[rt][v] * f)), r, to, 0, 0);
+      else
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(X[rt][v]), r, to, 0, 0);
+    }
+}
+// The E kept values of 16 bytes and their factor
+template <typename IO>
+__device__ __forceinline__ void widen(const uint4& r, float by, float* v) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+  for (int e = 0; e < HeadCfg<IO>::E; ++e) {
+    if constexpr (HeadCfg<IO>::ES == 2)
+      v[e] = by * static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu)));
+    else
+      v[e] = __uint_as_float(w[e]);
+  }
 }
 
 template <typename IO, int ROWS, int NW, int MODE, bool VEC>
@@ -622,8 +674,8 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     if constexpr (QUERY) {
       store_out(reinterpret_cast<const f32x4(&)[IB]>(none), 0, 0, li, g);
     } else if constexpr (MODE == kDeltaStates) {
-      keep<IO, RT>(p.states, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
-      keep<IO, IB>(p.res, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
+      keep<IO, RT>(p.states, p.states_by, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
+      keep<IO, IB>(p.res, p.res_by, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
     }
   }
   for (int kk = 0; kk < nc; ++kk) {
@@ -646,7 +698,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     if (kk + 1 < nc) load_chunk(pc + 1);
 
     if constexpr (MODE == kDeltaStates)
-      keep<IO, RT>(p.states + (bh * p.nch + pc) * wsize, p.rp, p.cp, cw + li, g, S);
+      keep<IO, RT>(p.states + (bh * p.nch + pc) * wsize * kept_size<IO>(), p.states_by + (bh * p.nch + pc) * (p.cp / 16), p.rp, p.cp, cw + li, g, S);
 
     // ---- what the state before the chunk gives: X = K S (rows are tokens, by state_row), O = Q S (transposed).  The
     // operands of step s + 1 are read and split under the matrix instructions of step s.
@@ -759,7 +811,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (MODE == kDeltaStates)
-      keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp, C, p.cp, cw + li, g, X);
+      keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp * kept_size<IO>(), p.res_by + (bh * p.nch + pc) * (p.cp / 16), C, p.cp, cw + li, g, X);
 
     // ---- u = b r as an operand of o, e^{G_C - G} u as one of the state's update
     const int yb0 = state_col_base<IO, NK>(li, g);
@@ -928,8 +980,8 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
       // as many stores behind the first loads as the loop has behind its own (see keep)
       const f32x4 none[RT > IB ? RT : IB] = {};
       const int li = tid & 15, g = (tid & 63) >> 4;
-      keep<IO, RT>(p.states, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
-      keep<IO, IB>(p.res, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
+      keep<IO, RT>(p.states, p.states_by, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
+      keep<IO, IB>(p.res, p.res_by, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
     }
   }
   for (int kk = 0; kk < nc; ++kk) {
@@ -948,7 +1000,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     const float end_dec = ek[C - 1];
     const int lane = opaque(tid) & 63, g = lane >> 4, li = lane & 15;
     if (kk + 1 < nc) load_chunk(pc - 1);
-    if constexpr (!SEG) keep<IO, RT>(p.states + (bh * p.nch + pc) * wsize, p.rp, p.cp, cw + li, g, R);
+    if constexpr (!SEG) keep<IO, RT>(p.states + (bh * p.nch + pc) * wsize * kept_size<IO>(), p.states_by + (bh * p.nch + pc) * (p.cp / 16), p.rp, p.cp, cw + li, g, R);
 
     // ---- X = K R (rows are tokens); the operands of step s + 1 are read and split under the matrix instructions of step s
     constexpr int LOW = IB == 2 ? 3 : 6;  // operand steps on and below the diagonal
@@ -1065,7 +1117,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     mix<LOW * (PS + (PP == 2 ? 2 : 0)), 3>();
     __builtin_amdgcn_sched_barrier(0);
     if (kk + 1 < nc) load_late(pc - 1);
-    if constexpr (!SEG) keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp, C, p.cp, cw + li, g, X);
+    if constexpr (!SEG) keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp * kept_size<IO>(), p.res_by + (bh * p.nch + pc) * (p.cp / 16), C, p.cp, cw + li, g, X);
 
     const int yb0 = state_col_base<IO, NK>(li, g);
 #pragma unroll
@@ -1114,8 +1166,10 @@ constexpr int kGradOneHead = 256;
 
 struct DeltaGradDev {
   DeltaDev f;                  // q, k, rates, sizes; v is dO; states S_0, res r
-  const float* r1;             // [b][H][nch][rp][cp]: R after every chunk
-  const float* e;              // [b][H][nch][C][cp]
+  const char* r1;              // [b][H][nch][rp][cp]: R after every chunk
+  const char* e;               // [b][H][nch][C][cp]
+  const float* r1_by;          // their factors
+  const float* e_by;
   char* dq;                    // [b][L][H / hn][rows]; float32 parts with `parts`
   char* dk;
   char* dv;                    // [b][L][H][cols]
@@ -1136,6 +1190,28 @@ constexpr size_t grad_lds_bytes() {
   return 2 * size_t(K::C) * ROWS * K::ES + grad_buffers<ROWS>() * slab + sc + (size_t(2) * NW + kRates + 1) * K::C * 4 + NW * 4;
 }
 
+// Running sum from the last lane as a pair of floats (scan_pair's, the other way round)
+__device__ __forceinline__ void scan_back(float& hi, float& lo) {
+  lo = 0.f;
+  scan_step<0x101, 0xf>(hi, lo);  // one lane down within a row of 16
+  scan_step<0x102, 0xf>(hi, lo);
+  scan_step<0x104, 0xf>(hi, lo);
+  scan_step<0x108, 0xf>(hi, lo);
+  const int row = (threadIdx.x & 63) >> 4;
+  float h = 0.f, l = 0.f;  // what the rows further on hold together
+#pragma unroll
+  for (int r = 3; r > 0; --r) {
+    const float th = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hi), 16 * r));
+    const float tl = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lo), 16 * r));
+    const float s = h + (row < r ? th : 0.f), bb = s - h;
+    l += ((h - (s - bb)) + ((row < r ? th : 0.f) - bb)) + (row < r ? tl : 0.f);
+    h = s;
+  }
+  const float s = h + hi, bb = s - h;
+  lo = (l + lo) + ((h - (s - bb)) + (hi - bb));
+  hi = s;
+}
+
 // dg_t = <dLoss/dS~_t, S~_t> telescopes within the chunk:
 //   dg_t = sum_{i >= t} (q_i . dq_i - k_i . dk^+_i + k_i . dk^-_i) + e^{G_C} <R_C, S_0> + sum_i k_i . w_i R_C u_i
 // with dk^+ the key's gradient as what is written (first three terms of dk above), dk^- as what is taken out (the
@@ -1152,8 +1228,9 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
   constexpr int TILES = IB * (IB + 1) / 2, MINE = (2 * TILES + NW - 1) / NW;
   constexpr int TASKS = C * NS / T;  // staging tasks a thread, rows tid / NS + i T / NS
   constexpr bool MULTI = ROWS < kGradOneHead;
-  static_assert(C * NS % T == 0 && CT >= 1, "shares are even");
+  static_assert(C * NS % T == 0 && CT >= 1 && SS % 2 == 0, "shares are even");
   using TK = Tile<IO, NK, T>;
+  using TR = Flat<kRates * C * 4, T>;
 
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char* const tx = lds;
@@ -1193,46 +1270,62 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
     }
 
   if (t0 < len) {
-    const int hk = hg * d.hn / p.rep, nslab = p.cp / kSlab;
-    const uint32_t wbytes = static_cast<uint32_t>(p.rp * p.cp * 4), rbytes = static_cast<uint32_t>(C * p.cp * 4);
-    // What a thread has in flight: its part of a slab's dO, r and e, and the operands S_0 and R_C of its wavefront.
-    uint4 go[TASKS];
-    float gr[TASKS][E], ge[TASKS][E], s0[CT][E], r1[CT][E];
-    auto load_slab = [&](int h, int v0) {
-      const int64_t chunk = (static_cast<int64_t>(b) * p.H + h) * p.nch + pc;
-      const Rsrc rdo = make_rsrc(p.v + b * p.v_b + static_cast<int64_t>(t0) * p.v_t + static_cast<int64_t>(h) * p.cols * ES,
+    constexpr int KB = kept_size<IO>();
+    const int hk = hg * d.hn / p.rep, nslab = p.cp / kSlab, steps = nslab * SS;
+    const uint32_t wbytes = static_cast<uint32_t>(p.rp * p.cp * KB), rbytes = static_cast<uint32_t>(C * p.cp * KB);
+    const uint32_t bybytes = static_cast<uint32_t>(p.cp / 16 * 4);
+    const int64_t chunk0 = (static_cast<int64_t>(b) * p.H + hg * d.hn) * p.nch + pc;  // of head hh: hh nch further
+    // What a thread has in flight: its part of a slab's dO, r and e, and the operands S_0 and R_C of its wavefront for
+    // the next two steps.
+    uint4 go[TASKS], gr[TASKS], ge[TASKS], s0[2][CT], r1[2][CT], rr[TR::CNT];
+    float gr_by[TASKS], ge_by[TASKS], s0_by[2], r1_by[2];
+    auto factor = [&](const float* by, int64_t chunk, int col) {
+      if constexpr (KB == 4) return 1.f;
+      const Rsrc r = make_rsrc(by + chunk * (p.cp / 16), bybytes);
+      return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, col / 16 * 4, 0, 0));
+    };
+    auto load_slab = [&](int hh, int v0) {
+      const int64_t chunk = chunk0 + static_cast<int64_t>(hh) * p.nch;
+      const Rsrc rdo = make_rsrc(p.v + b * p.v_b + static_cast<int64_t>(t0) * p.v_t + static_cast<int64_t>(hg * d.hn + hh) * p.cols * ES,
                                  row_bytes(len - t0, C, p.v_t));
-      const Rsrc rr = make_rsrc(p.res + chunk * C * p.cp, rbytes), re = make_rsrc(d.e + chunk * C * p.cp, rbytes);
+      const Rsrc rres = make_rsrc(p.res + chunk * rbytes, rbytes), re = make_rsrc(d.e + chunk * rbytes, rbytes);
 #pragma unroll
       for (int i = 0; i < TASKS; ++i) {
         const int me = opaque(tid), r = me / NS + i * (T / NS), col = v0 + me % NS * E;
         go[i] = load16<IO, VEC>(rdo, r * p.v_t + col * ES, p.cols - col);
-#pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          BufF32::ld<4>(rr, (r * p.cp + col + e) * 4, &gr[i][e]);
-          BufF32::ld<4>(re, (r * p.cp + col + e) * 4, &ge[i][e]);
-        }
+        gr[i] = load16<IO, true>(rres, (r * p.cp + col) * KB, 1);
+        ge[i] = load16<IO, true>(re, (r * p.cp + col) * KB, 1);
+        gr_by[i] = factor(p.res_by, chunk, col);
+        ge_by[i] = factor(d.e_by, chunk, col);
       }
     };
-    auto load_states = [&](int h, int v0) {
-      const int64_t chunk = (static_cast<int64_t>(b) * p.H + h) * p.nch + pc;
-      const Rsrc rs0 = make_rsrc(p.states + chunk * p.rp * p.cp, wbytes), rr1 = make_rsrc(d.r1 + chunk * p.rp * p.cp, wbytes);
+    // step n of head hh, of the next head where this one has none
+    auto load_states = [&](int hh, int n, int to) {
+      if (n >= steps) {
+        n -= steps;
+        ++hh;
+      }
+      if (n >= steps || hh >= d.hn) return;
+      const int64_t chunk = chunk0 + static_cast<int64_t>(hh) * p.nch;
+      const Rsrc rs0 = make_rsrc(p.states + chunk * wbytes, wbytes), rr1 = make_rsrc(d.r1 + chunk * wbytes, wbytes);
+      const int me = opaque(lane), col = KS * n + E * (me >> 4);
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        const uint32_t off = static_cast<uint32_t>(((wave * CT + c) * 16 + li) * p.cp + v0 + E * g) * 4;
-#pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          BufF32::ld<4>(rs0, off + 4 * e, &s0[c][e]);
-          BufF32::ld<4>(rr1, off + 4 * e, &r1[c][e]);
-        }
+        const uint32_t off = static_cast<uint32_t>(((wave * CT + c) * 16 + (me & 15)) * p.cp + col) * KB;
+        s0[to][c] = load16<IO, true>(rs0, off, 1);
+        r1[to][c] = load16<IO, true>(rr1, off, 1);
       }
+      s0_by[to] = factor(p.states_by, chunk, col);
+      r1_by[to] = factor(d.r1_by, chunk, col);
     };
     {
       uint4 rx[TK::CNT], ry[TK::CNT];
       TK::template load<VEC>(p.q + b * p.q_b + static_cast<int64_t>(hk) * p.rows * ES, p.q_t, t0, len, p.rows, tid, rx);
       TK::template load<VEC>(p.k + b * p.k_b + static_cast<int64_t>(hk) * p.rows * ES, p.k_t, t0, len, p.rows, tid, ry);
-      load_slab(hg * d.hn, 0);
-      load_states(hg * d.hn, 0);
+      TR::load(reinterpret_cast<const char*>(p.rates + chunk0 * kRates * C), tid, rr);
+      load_slab(0, 0);
+      load_states(0, 0, 0);
+      load_states(0, 1, 1);
       TK::store(tx, tid, rx);
       TK::store(ty, tid, ry);
     }
@@ -1240,11 +1333,10 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
     for (int i = tid; i < 2 * PP * PB / 16; i += T) reinterpret_cast<uint4*>(tp)[i] = make_uint4(0, 0, 0, 0);
     for (int hh = 0; hh < d.hn; ++hh) {
       const int h = hg * d.hn + hh;
-      const int64_t bh = static_cast<int64_t>(b) * p.H + h, chunk = bh * p.nch + pc;
       __syncthreads();  // the head before is done with the rates
-      if (tid < kRates * C / 4)
-        reinterpret_cast<float4*>(rt)[tid] = reinterpret_cast<const float4*>(p.rates + chunk * kRates * C)[tid];
+      TR::store(reinterpret_cast<char*>(rt), tid, rr);
       __syncthreads();
+      if (hh + 1 < d.hn) TR::load(reinterpret_cast<const char*>(p.rates + (chunk0 + (hh + 1) * static_cast<int64_t>(p.nch)) * kRates * C), tid, rr);
 
       f32x4 vs[CT][IB], sc[MINE];
 #pragma unroll
@@ -1267,45 +1359,50 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
         for (int i = 0; i < TASKS; ++i) {
           const int me = opaque(tid), r = me / NS + i * (T / NS), c = me % NS, col = v0 + c * E;
           const float bb = bt[r];
+          float x[E], y[E];
+          widen<IO>(gr[i], gr_by[i], x);
+          widen<IO>(ge[i], ge_by[i], y);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            dot_b[i] = __builtin_fmaf(gr[i][e], ge[i][e], dot_b[i]);
-            gr[i][e] *= bb;
-            ge[i][e] *= bb;
+            dot_b[i] = __builtin_fmaf(x[e], y[e], dot_b[i]);
+            x[e] *= bb;
+            y[e] *= bb;
           }
           const uint32_t off = r * vts + col * ES;
           if constexpr (VEC) {
-            BufOf<IO>::type::template st<E>(rdv, col < p.cols ? off : kOOB, ge[i]);
+            BufOf<IO>::type::template st<E>(rdv, col < p.cols ? off : kOOB, y);
           } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) BufOf<IO>::type::template st<1>(rdv, col + e < p.cols ? off + e * ES : kOOB, &ge[i][e]);
+            for (int e = 0; e < E; ++e) BufOf<IO>::type::template st<1>(rdv, col + e < p.cols ? off + e * ES : kOOB, y + e);
           }
           uint4 w[PP];
           const int to = 16 * (NS * r + (c ^ swz<IO, NS>(r)));
           *reinterpret_cast<uint4*>(tdo + to) = go[i];
-          split<IO, PP>(gr[i], w);
+          split<IO, PP>(x, w);
 #pragma unroll
           for (int q = 0; q < PP; ++q) *reinterpret_cast<uint4*>(tu + q * SB + to) = w[q];
-          split<IO, PP>(ge[i], w);
+          split<IO, PP>(y, w);
 #pragma unroll
           for (int q = 0; q < PP; ++q) *reinterpret_cast<uint4*>(te + q * SB + to) = w[q];
         }
         __syncthreads();
-        if (v + 1 < nslab) load_slab(h, v0 + kSlab);
-        else if (hh + 1 < d.hn) load_slab(h + 1, 0);
+        if (v + 1 < nslab) load_slab(hh, v0 + kSlab);
+        else if (hh + 1 < d.hn) load_slab(hh + 1, 0);
         const int fb = opaque(lane_base<IO, NS>(li, g));
 #pragma unroll
         for (int s = 0; s < SS; ++s) {
           uint4 fs[CT][PP], fr[CT][PP];
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
+            float x[E], y[E];
+            widen<IO>(s0[s & 1][c], s0_by[s & 1], x);
+            widen<IO>(r1[s & 1][c], r1_by[s & 1], y);
 #pragma unroll
-            for (int e = 0; e < E; ++e) dot_rs = __builtin_fmaf(s0[c][e], r1[c][e], dot_rs);
-            split<IO, PP>(s0[c], fs[c]);
-            split<IO, PP>(r1[c], fr[c]);
+            for (int e = 0; e < E; ++e) dot_rs = __builtin_fmaf(x[e], y[e], dot_rs);
+            split<IO, PP>(x, fs[c]);
+            split<IO, PP>(y, fr[c]);
           }
-          if (s + 1 < SS || v + 1 < nslab) load_states(h, v0 + KS * (s + 1));
-          else if (hh + 1 < d.hn) load_states(h + 1, 0);
+          load_states(hh, v * SS + s + 2, s & 1);
 #pragma unroll
           for (int ib = 0; ib < IB; ++ib) {
             __builtin_amdgcn_sched_barrier(0);
@@ -1487,33 +1584,41 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
       if (d.dg != nullptr) {
         __syncthreads();
         if (wave == 0) {
-          double v = 0, tail = 0, edge = 0;
+          float v = 0.f, end = 0.f, edge = 0.f;
           int cut = 0;
           if (lane < C) {
             for (int w = 0; w < NW; ++w) {
               v += red[w * C + lane];
-              tail += redc[w * C + lane];
+              end += redc[w * C + lane];
             }
             cut = lane + 1 < C && anew[lane + 1] != 0.f;
           }
           for (int w = 0; w < NW; ++w) edge += rs[w];
+          float lo, end_lo;
+          scan_back(end, end_lo);  // lane 0 has the sum
+          end = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(end), 0)) +
+                __int_as_float(__builtin_amdgcn_readlane(__float_as_int(end_lo), 0));
+          if (lane == C - 1) v += end + times(ek[C - 1], edge);
+          // sums from the end
+          if (__builtin_amdgcn_ballot_w64(cut) == 0) {
+            scan_back(v, lo);
+            v += lo;
+          } else {
+            // lane l takes over those further on unless the state starts anew between
 #pragma unroll
-          for (int x = 1; x < 64; x *= 2) tail += __shfl_xor(tail, x);
-          if (lane == C - 1) v += tail + times(ek[C - 1], static_cast<float>(edge));
-          // sums from the end; lane l takes over those further on unless the state starts anew between
-#pragma unroll
-          for (int x = 1; x < 64; x *= 2) {
-            const double o = __shfl_down(v, x);
-            const int a = __shfl_down(cut, x);
-            if (lane + x < 64) {
-              if (!cut) v += o;
-              cut |= a;
+            for (int x = 1; x < 64; x *= 2) {
+              const float o = __shfl_down(v, x);
+              const int a = __shfl_down(cut, x);
+              if (lane + x < 64) {
+                if (!cut) v += o;
+                cut |= a;
+              }
             }
           }
           const int t = t0 + lane;
           if (lane < C && t < p.L) {
             const bool none = t >= len || (t == 0 && p.h0 == nullptr) || anew[lane] != 0.f;
-            const float out = none ? 0.f : static_cast<float>(v);
+            const float out = none ? 0.f : v;
             IO::template st<1>(reinterpret_cast<typename IO::T*>(d.dg) + (row0 + lane) * p.H + h, &out);
           }
         }

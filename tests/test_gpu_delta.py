@@ -5,7 +5,8 @@ a float32 sum of n products is off by at most 6 sqrt(n) 2^-24 of the product of 
 rounding error analysis, N. J. Higham and T. Mary, SIAM J. Sci. Comput. 41, 2019, with 6 standard deviations), n the
 additions in a row (d_key, d_value, a chunk's 64 tokens twice, some roundings of decays and scales).  bfloat16 storage
 adds 2^-16 for products of values in two parts, times 1 + |M|, since what is corrected among a chunk's tokens is M times
-as large; and half a step of the result, 2^-8 of it (float32: 2^-24, in the sums).
+as large; half a step of float16, 2^-11, for the states, r and e that the gradients are made of; and half a step of the
+result, 2^-8 of it (float32: 2^-24, in the sums).
 """
 import numpy as np
 import pytest
@@ -78,6 +79,7 @@ def errors(x, dtype, do=None, dlast=None):
                                    dlast=None if dlast is None else dlast.double().cpu().numpy(),
                                    step=6 * np.sqrt(dk + dv + 2 * 64 + 32) * 2.0 ** -24,
                                    pair=2.0 ** -16 * kappa(y, dtype) if dtype == torch.bfloat16 else 0.0,
+                                   kept=2.0 ** -11 if dtype == torch.bfloat16 else 0.0,
                                    chunk=64 if dtype == torch.bfloat16 else 32)
 
 
