@@ -256,8 +256,8 @@ bool all_vec(const DeltaArgs& a, bool bf16) {
 }
 
 // M or P of every chunk
-int64_t square_bytes(const DeltaArgs& a, const Plan& pl) {
-  return a.batch * a.H * pl.nch * pl.C * pl.C * 4;  // two parts of 2 bytes, or one of 4
+int64_t square_bytes(const DeltaArgs& a, const Plan& pl, bool bf16) {
+  return a.batch * a.H * pl.nch * (bf16 ? deltak::Square<BF16>::BYTES : deltak::Square<F32>::BYTES);
 }
 
 // Heads whose parts of dq and dk a workgroup adds: all that share a key head, unless that leaves CUs idle.
@@ -284,8 +284,8 @@ Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
     return r;
   };
   const int64_t bh = a.batch * a.H;
-  w.m = take(square_bytes(a, pl));
-  w.s = take(square_bytes(a, pl));
+  w.m = take(square_bytes(a, pl, bf16));
+  w.s = take(square_bytes(a, pl, bf16));
   w.rates = take(bh * pl.nch * pl.C * deltak::kRates * 4);
   if (pl.nseg > 1) {
     w.ss = take(4 * bh * pl.nseg * pl.rp * pl.cp);
@@ -374,6 +374,7 @@ hipError_t launch_delta_fwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   const Plan pl = plan_of(a, bf16);
   const bool vec = all_vec(a, bf16);
   const DeltaDev d = dev_of(a, pl, space_of(a, pl, bf16, false), work, bf16, vec);
+  if (pl.nch == 1 && d.ntile == 1) return launch_pass(d, d, bf16, deltak::kPassOne, vec, st);
   hipError_t e = launch_pass(d, d, bf16, deltak::kPassPrep, vec, st);
   if (e == hipSuccess && pl.nseg > 1) {
     e = launch_pass(with_transitions(d, vec), d, bf16, deltak::kPassSeg, vec, st);

@@ -214,25 +214,51 @@ struct Flat {
   }
 };
 
-// A chunk's M or P, all parts: BYTES of 16-byte chunks, rows of N of them, dealt to T threads
-template <typename IO, int BYTES, int N, int T>
+// A chunk's M or P in the workspace: of a [C][C] matrix the 16-byte chunks of the 16 x 16 blocks on and below the
+// diagonal, block row by block row (five eighths of it for 64 tokens), a part after the other.
+template <typename IO>
+struct Square {
+  using K = HeadCfg<IO>;
+  static constexpr int PER = 16 / K::E, IB = K::C / 16, CHUNKS = 8 * PER * IB * (IB + 1), PARTS = DeltaCfg<IO>::PAIR;
+  static constexpr int BYTES = 16 * CHUNKS * PARTS, LDS = PARTS * K::C * K::C * K::ES;
+  static __device__ __forceinline__ void place(int i, int& row, int& c) {
+    const int rb = (i >= 16 * PER) + (IB > 2 && i >= 48 * PER) + (IB > 2 && i >= 96 * PER), at = i - 8 * PER * rb * (rb + 1);
+    row = 16 * rb + at / (PER * (rb + 1));
+    c = at % (PER * (rb + 1));
+  }
+};
+
+// The same dealt to T threads for LDS tiles of whole rows; where a thread's chunks go there is worked out once.
+template <typename IO, int T>
 struct TileM {
-  static constexpr int CNT = (BYTES / 16 + T - 1) / T;
-  static __device__ __forceinline__ void load(const char* base, int tid, uint4* reg) {
+  using S = Square<IO>;
+  static constexpr int N = HeadCfg<IO>::C / HeadCfg<IO>::E, CNT = (S::CHUNKS * S::PARTS + T - 1) / T;
+  int to[CNT];
+  __device__ __forceinline__ explicit TileM(int tid) {
 #pragma unroll
     for (int i = 0; i < CNT; ++i) {
-      const int at = tid + i * T;
-      reg[i] = make_uint4(0, 0, 0, 0);
-      if (BYTES / 16 % T == 0 || at < BYTES / 16) reg[i] = *reinterpret_cast<const uint4*>(base + 16 * at);
+      const int at = tid + i * T, part = at / S::CHUNKS;
+      int row, c;
+      S::place(at % S::CHUNKS, row, c);
+      to[i] = part < S::PARTS ? 16 * (N * (HeadCfg<IO>::C * part + row) + (c ^ swz<IO, N>(row))) : -1;
     }
   }
-  static __device__ __forceinline__ void store(char* tile, int tid, const uint4* reg) {
+  static __device__ __forceinline__ void load(const char* base, int tid, uint4* reg) {
+    const Rsrc r = make_rsrc(base, S::BYTES);
 #pragma unroll
     for (int i = 0; i < CNT; ++i) {
-      const int at = tid + i * T, r = at / N;
-      if (BYTES / 16 % T == 0 || at < BYTES / 16)
-        *reinterpret_cast<uint4*>(tile + 16 * (N * r + (at % N ^ swz<IO, N>(T / N % 16 == 0 ? tid / N : r)))) = reg[i];
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, 16 * (tid + i * T), 0, 0);
+      reg[i] = make_uint4(v.x, v.y, v.z, v.w);
     }
+  }
+  __device__ __forceinline__ void store(char* tile, const uint4* reg) const {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i)
+      if (S::CHUNKS * S::PARTS % T == 0 || to[i] >= 0) *reinterpret_cast<uint4*>(tile + to[i]) = reg[i];
+  }
+  // what lies above the blocks is never written again
+  static __device__ __forceinline__ void clear(char* tile, int tid) {
+    for (int i = tid; i < S::LDS / 16; i += T) reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
   }
 };
 
@@ -291,19 +317,20 @@ __device__ __forceinline__ void score_tile(int tile, int& ib, int& jb) {
   jb = tile - ib * (ib + 1) / 2;
 }
 
-// A float32 matrix [C][LD] in LDS to global memory as parts, whole and coalesced
+// A float32 matrix [C][LD] in LDS to global memory as parts
 template <typename IO, int LD, int T>
 __device__ __forceinline__ void store_parts(const float* n, char* dst, int tid) {
-  using K = HeadCfg<IO>;
-  constexpr int PARTS = DeltaCfg<IO>::PAIR, C = K::C, E = K::E;
-  for (int i = tid; i < C * C / E; i += T) {
-    const int r = i / (C / E), c = i % (C / E) * E;
+  using S = Square<IO>;
+  constexpr int E = HeadCfg<IO>::E;
+  for (int i = tid; i < S::CHUNKS; i += T) {
+    int r, c;
+    S::place(i, r, c);
     float v[E];
-    F32::ld<E>(n + r * LD + c, v);
-    uint4 w[PARTS];
-    split<IO, PARTS>(v, w);
+    F32::ld<E>(n + r * LD + c * E, v);
+    uint4 w[S::PARTS];
+    split<IO, S::PARTS>(v, w);
 #pragma unroll
-    for (int q = 0; q < PARTS; ++q) *reinterpret_cast<uint4*>(dst + q * C * C * K::ES + 16 * i) = w[q];
+    for (int q = 0; q < S::PARTS; ++q) *reinterpret_cast<uint4*>(dst + 16 * (q * S::CHUNKS + i)) = w[q];
   }
 }
 
@@ -316,12 +343,11 @@ __device__ __forceinline__ void store_parts(const float* n, char* dst, int tid) 
 // (Substitution, not powers of N b: keys alike make those grow past float32
 // where the inverse does not.)
 template <typename IO, int ROWS, bool QUERY, bool VEC>
-__global__ void __launch_bounds__(256) ssm_delta_prep_kernel(const DeltaDev p) {
+__device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char* lds) {
   using K = HeadCfg<IO>;
   constexpr int ES = K::ES, C = K::C, T = 256, IB = C / 16, NK = ROWS * ES / 16, RS = ROWS / K::KS;
-  constexpr int LD = C + 4, TILES = IB * (IB + 1) / 2, MINE = (TILES + 3) / 4, MB = DeltaCfg<IO>::PAIR * C * C * ES;
+  constexpr int LD = C + 4, TILES = IB * (IB + 1) / 2, MINE = (TILES + 3) / 4, MB = Square<IO>::BYTES;
   using TK = Tile<IO, NK, T>;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   float* const rt = reinterpret_cast<float*>(lds);  // [kRates][C]
   char* const ty = reinterpret_cast<char*>(rt + kRates * C);
   char* const tx = ty + C * ROWS * ES;
@@ -330,7 +356,7 @@ __global__ void __launch_bounds__(256) ssm_delta_prep_kernel(const DeltaDev p) {
   float* const inv = n + C * LD;                    // [IB][16][20]
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int pc = blockIdx.x % p.nch, bh = blockIdx.x / p.nch, h = bh % p.H, b = bh / p.H, t0 = pc * C;
+  const int pc = pid % p.nch, bh = pid / p.nch, h = bh % p.H, b = bh / p.H, t0 = pc * C;
   const int len = length_of(p, b);
   if (t0 >= len) return;
   const int64_t chunk = static_cast<int64_t>(bh) * p.nch + pc;
@@ -453,6 +479,12 @@ __global__ void __launch_bounds__(256) ssm_delta_prep_kernel(const DeltaDev p) {
     __syncthreads();
     store_parts<IO, LD, T>(n, p.s + chunk * MB, tid);
   }
+}
+
+template <typename IO, int ROWS, bool VEC>
+__global__ void __launch_bounds__(256) ssm_delta_prep_kernel(const DeltaDev p) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  delta_prep<IO, ROWS, true, VEC>(p, blockIdx.x, lds);
 }
 
 // ---------------------------------------------------------------- the walk over the length, forwards
@@ -580,16 +612,16 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
   constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
   constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
   constexpr int PS = DeltaCfg<IO>::STATE, PP = DeltaCfg<IO>::PAIR;
-  constexpr int MB = PP * C * C * ES;  // bytes of a chunk's M
+  constexpr int MB = Square<IO>::BYTES, ML = Square<IO>::LDS;  // bytes of a chunk's M, and in LDS
   using TK = Tile<IO, NK, T>;
   using TZ = Tile<IO, NZ, T>;
-  using TM = TileM<IO, MB, NP, T>;
+  using TM = TileM<IO, T>;
   using TR = Flat<kRates * C * 4, T>;
 
   char* const ty = lds;
   char* const tz = ty + C * ROWS * ES;
   char* const tm = tz + C * COLS * ES;
-  float* const rt = reinterpret_cast<float*>(tm + MB);  // [kRates][C]
+  float* const rt = reinterpret_cast<float*>(tm + ML);  // [kRates][C]
   const float* const ek = rt + kEk * C;
   const float* const we = rt + kWe * C;
   const float* const bt = rt + kBeta * C;
@@ -628,6 +660,9 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
   const char* const yb = p.k + b * p.k_b + static_cast<int64_t>(h / p.rep) * p.rows * ES;
   const char* const zb = p.v + b * p.v_b + (static_cast<int64_t>(h) * p.cols + col0) * ES;
 
+  const TM square(tid);
+  TM::clear(tm, tid);
+  if constexpr (QUERY) TM::clear(tp, tid);
   uint4 rx[TK::CNT], ry[TK::CNT], rz[TZ::CNT], rm[TM::CNT], rp[TM::CNT], rr[TR::CNT];
   auto load_chunk = [&](int pc) {
     const int t0 = pc * C, me = ROWS == 256 || !VEC ? opaque(tid) : tid;
@@ -685,11 +720,11 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
       const int me = ROWS == 256 || !VEC ? opaque(tid) : tid;
       TK::store(ty, me, ry);
       if (!trans) TZ::store(tz, me, rz);
-      TM::store(tm, me, rm);
+      square.store(tm, rm);
       TR::store(reinterpret_cast<char*>(rt), me, rr);
       if constexpr (QUERY) {
         TK::store(tx, me, rx);
-        TM::store(tp, me, rp);
+        square.store(tp, rp);
       }
     }
     __syncthreads();
@@ -906,6 +941,18 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_kernel(const DeltaDev 
   delta_walk<IO, ROWS, NW, MODE, VEC>(p, blockIdx.x, lds);
 }
 
+// One chunk and one column tile: a launch for both (17 tokens, 4 heads of 32 x 32: SSM_ONE).
+template <typename IO, int ROWS, bool VEC>
+__global__ void __launch_bounds__(256, 2) ssm_delta_one_kernel(const DeltaDev p) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  // the walk's workgroup of a (batch row, head) makes that one's M
+  int ct, seg, h, b;
+  place(p, blockIdx.x, 1, ct, seg, h, b);
+  delta_prep<IO, ROWS, true, VEC>(p, b * p.H + h, lds);
+  __syncthreads();  // what it wrote, the walk reads back
+  delta_walk<IO, ROWS, 4, kDeltaOut, VEC>(p, blockIdx.x, lds);
+}
+
 // ---------------------------------------------------------------- the walk over the length, backwards
 
 // v is dO, h0 dlast, last dh0.  SEG: a segment's own R at its first token, from zero (the last segment: from dlast);
@@ -917,16 +964,16 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
   constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
   constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
   constexpr int PS = DeltaCfg<IO>::STATE, PP = DeltaCfg<IO>::PAIR;
-  constexpr int MB = PP * C * C * ES;
+  constexpr int MB = Square<IO>::BYTES, ML = Square<IO>::LDS;
   using TK = Tile<IO, NK, T>;
   using TZ = Tile<IO, NZ, T>;
-  using TM = TileM<IO, MB, NP, T>;
+  using TM = TileM<IO, T>;
   using TR = Flat<kRates * C * 4, T>;
 
   char* const ty = lds;
   char* const tz = ty + C * ROWS * ES;
   char* const tm = tz + C * COLS * ES;
-  float* const rt = reinterpret_cast<float*>(tm + MB);  // [kRates][C]
+  float* const rt = reinterpret_cast<float*>(tm + ML);  // [kRates][C]
   const float* const ek = rt + kEk * C;
   const float* const we = rt + kWe * C;
   const float* const bt = rt + kBeta * C;
@@ -956,6 +1003,9 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
   const char* const yb = p.k + b * p.k_b + static_cast<int64_t>(h / p.rep) * p.rows * ES;
   const char* const zb = p.v + b * p.v_b + (static_cast<int64_t>(h) * p.cols + col0) * ES;
 
+  const TM square(tid);
+  TM::clear(tm, tid);
+  TM::clear(tp, tid);
   uint4 rx[TK::CNT], ry[TK::CNT], rz[TZ::CNT], rm[TM::CNT], rp[TM::CNT], rr[TR::CNT];
   auto load_chunk = [&](int pc) {
     const int t0 = pc * C, me = ROWS >= 128 || !VEC ? opaque(tid) : tid;
@@ -992,8 +1042,8 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
       TK::store(ty, me, ry);
       TK::store(tx, me, rx);
       TZ::store(tz, me, rz);
-      TM::store(tm, me, rm);
-      TM::store(tp, me, rp);
+      square.store(tm, rm);
+      square.store(tp, rp);
       TR::store(reinterpret_cast<char*>(rt), me, rr);
     }
     __syncthreads();
@@ -1692,9 +1742,20 @@ template <typename IO, int ROWS, bool VEC>
 hipError_t launch_prep_t(const DeltaDev& p, hipStream_t st) {
   static std::atomic<uint64_t> allowed{0};
   constexpr size_t smem = prep_lds_bytes<IO, ROWS, true>();
-  auto kern = ssm_delta_prep_kernel<IO, ROWS, true, VEC>;
+  auto kern = ssm_delta_prep_kernel<IO, ROWS, VEC>;
   if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.batch * p.H * p.nch)), dim3(256), smem, st, p);
+  return hipGetLastError();
+}
+
+template <typename IO, int ROWS, bool VEC>
+hipError_t launch_one_t(const DeltaDev& p, hipStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
+  constexpr size_t prep = prep_lds_bytes<IO, ROWS, true>(), walk = delta_lds_bytes<IO, ROWS, 4, true>();
+  constexpr size_t smem = prep > walk ? prep : walk;
+  auto kern = ssm_delta_one_kernel<IO, ROWS, VEC>;
+  if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.H * p.batch)), dim3(256), smem, st, p);
   return hipGetLastError();
 }
 
@@ -1736,7 +1797,7 @@ hipError_t launch_grad_t(const DeltaGradDev& d, hipStream_t st) {
 // Four wavefronts of 16 columns: with eight for 128 the prompts below take as long and the training's 256 walks of 4 x
 // 2048 tokens, 32 heads of 128 x 128, half as long again.  `wide` is eight: past 128 keys LDS holds one workgroup a CU
 // either way.
-enum { kPassPrep, kPassOut, kPassSeg, kPassBoth, kPassBothSeg };
+enum { kPassPrep, kPassOne, kPassOut, kPassSeg, kPassBoth, kPassBothSeg };
 
 template <typename IO, int ROWS, int NW, bool VEC>
 hipError_t launch_pass_n(const DeltaDev& p, const DeltaDev& r, int pass, hipStream_t st) {
@@ -1749,6 +1810,7 @@ hipError_t launch_pass_n(const DeltaDev& p, const DeltaDev& r, int pass, hipStre
 template <typename IO, int ROWS, bool VEC>
 hipError_t launch_pass_r(const DeltaDev& p, const DeltaDev& r, int pass, bool wide, hipStream_t st) {
   if (pass == kPassPrep) return launch_prep_t<IO, ROWS, VEC>(p, st);
+  if (pass == kPassOne) return launch_one_t<IO, ROWS, VEC>(p, st);
   if constexpr (VEC && ROWS == 256)
     if (wide) return launch_pass_n<IO, ROWS, 8, VEC>(p, r, pass, st);
   return launch_pass_n<IO, ROWS, 4, VEC>(p, r, pass, st);
