@@ -38,8 +38,9 @@ using deltak::DeltaDev;
 using headk::f32x4;
 using deltak::DeltaGradDev;
 
-constexpr int64_t kDeltaSlots = 512;     // workgroups that a split length is to give
-constexpr int64_t kDeltaMinSegment = 8;  // chunks
+constexpr int64_t kDeltaCUs = 256;
+constexpr int64_t kDeltaMinSegment = 3;   // chunks
+constexpr int64_t kDeltaMaxSegments = 64;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
@@ -237,9 +238,24 @@ Plan plan_of(const DeltaArgs& a, bool bf16) {
   p.nch = cdiv(a.L, p.C);
   p.rp = up(a.dk, 16);
   p.cp = up(a.dv, deltak::kSlab);
-  const int64_t wgs = a.batch * a.H * tiles_for(a.dk, a.dv, true);
-  int64_t want = std::min(kDeltaSlots / wgs, p.nch / kDeltaMinSegment);
-  if (want < 6) want = 1;  // a split costs a walk of its own, twice as wide
+  // The number of segments that the model below finds shortest, in chunks of a workgroup alone on its CU (4.2 us,
+  // bfloat16, 128 x 128): two workgroups a CU take 1.75 of that (float32: 2, the matrix instructions bound it), the segments' own walk 0.8, with the transitions' tiles
+  // beside the state's in all but the first, a step of the carry 0.8, two more launches 3.  16 heads of 128 x 128 over
+  // 32768 tokens: 589 us in 16 segments, 605 in 8, whole some 2.2 ms; 128 heads of 128 x 128 over 2048 tokens are better
+  // off whole.  A tenth has to be gained.
+  const int64_t tv = tiles_for(a.dk, a.dv, true), tt = cdiv(p.rp, wide_for(a.dk, a.dv, true) ? 128 : 64), bh = a.batch * a.H;
+  const double pair = bf16 ? 1.75 : 2.;
+  auto rate = [pair](double wgs) { return wgs <= kDeltaCUs ? 1. : std::max(pair, wgs * pair / (2 * kDeltaCUs)); };
+  double best = 0.9 * p.nch * rate(bh * tv);
+  int64_t want = 1;
+  for (int64_t n = 2; n <= kDeltaMaxSegments && n * kDeltaMinSegment <= p.nch; ++n) {
+    const double own = bh * ((n - 1) * tv + (n - 2) * tt);
+    const double t = cdiv(p.nch, n) * (0.8 * rate(own) + rate(bh * n * tv)) + 0.8 * (n - 2) + 3;
+    if (t < best) {
+      best = t;
+      want = n;
+    }
+  }
   p.cps = cdiv(p.nch, want);
   p.nseg = cdiv(p.nch, p.cps);
   return p;
@@ -264,7 +280,7 @@ int64_t square_bytes(const DeltaArgs& a, const Plan& pl, bool bf16) {
 int64_t grad_heads(const DeltaArgs& a, const Plan& pl) {
   const int64_t rep = a.H / a.Hk;
   int64_t n = a.dk > 128 ? 1 : rep;  // kGradOneHead
-  while (n > 1 && a.batch * (a.H / n) * pl.nch < kDeltaSlots) {
+  while (n > 1 && a.batch * (a.H / n) * pl.nch < 2 * kDeltaCUs) {
     --n;
     while (rep % n != 0) --n;
   }

@@ -83,9 +83,12 @@ struct DeltaDev {
 };
 
 // Parts that a float32 value enters a product in (bfloat16 storage): the state
-// and what is added to it in three, which is exact to float32; the corrections
-// M (b x), whose operands are both such values, and all that ends in a bfloat16
-// result in two (2^-17 of themselves).
+// and what is added to it in three, which is exact to float32, and of M (b x),
+// where both are such values, the five products that matter (with three the
+// last state is off by 1.2e-6, with five by 7e-7, 32768 tokens); all that ends in
+// a bfloat16 result in two (2^-17 of themselves), and so what a segment hands
+// to the next (the walk that finds it takes 264 instead of 330 us there, the
+// last state stays where it was).
 template <typename IO>
 struct DeltaCfg {
   static constexpr int STATE = HeadCfg<IO>::ES == 2 ? 3 : 1;
@@ -611,7 +614,8 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
   constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
   constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
-  constexpr int PS = DeltaCfg<IO>::STATE, PP = DeltaCfg<IO>::PAIR;
+  constexpr int PP = DeltaCfg<IO>::PAIR, PS = MODE == kDeltaSeg ? PP : DeltaCfg<IO>::STATE;
+  constexpr int PL = PP == 2 ? PS - 1 : 0;  // parts of b x that meet M's second part
   constexpr int MB = Square<IO>::BYTES, ML = Square<IO>::LDS;  // bytes of a chunk's M, and in LDS
   using TK = Tile<IO, NK, T>;
   using TZ = Tile<IO, NZ, T>;
@@ -828,13 +832,13 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
       for (int ib = 0; ib < IB; ++ib) scale(O[ib], p.scale * ek[16 * ib + li]);
     }
 #pragma unroll
-    for (int q = 0; q < PS + (PP == 2 ? 2 : 0); ++q)
+    for (int q = 0; q < PS + PL; ++q)
 #pragma unroll
       for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
         for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n)
           X[i] = q < PS ? mma<IO>(fm[n], bx[js][q], X[i]) : mma<IO>(fl[n], bx[js][q - PS], X[i]);
-    mix<LOW * (PS + (PP == 2 ? 2 : 0)), 2>();
+    mix<LOW * (PS + PL), 2>();
     __builtin_amdgcn_sched_barrier(0);
     if (QUERY && kk + 1 < nc) load_queries(pc + 1);
     const int pb = lane_base<IO, NP>(li, g);
@@ -963,7 +967,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
   constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
   constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
-  constexpr int PS = DeltaCfg<IO>::STATE, PP = DeltaCfg<IO>::PAIR;
+  constexpr int PP = DeltaCfg<IO>::PAIR, PS = SEG ? PP : DeltaCfg<IO>::STATE;
   constexpr int MB = Square<IO>::BYTES, ML = Square<IO>::LDS;
   using TK = Tile<IO, NK, T>;
   using TZ = Tile<IO, NZ, T>;
