@@ -239,10 +239,10 @@ Plan plan_of(const DeltaArgs& a, bool bf16) {
   p.rp = up(a.dk, 16);
   p.cp = up(a.dv, deltak::kSlab);
   // The number of segments that the model below finds shortest, in chunks of a workgroup alone on its CU (4.2 us,
-  // bfloat16, 128 x 128): two workgroups a CU take 1.75 of that (float32: 2, the matrix instructions bound it), the segments' own walk 0.8, with the transitions' tiles
-  // beside the state's in all but the first, a step of the carry 0.8, two more launches 3.  16 heads of 128 x 128 over
-  // 32768 tokens: 589 us in 16 segments, 605 in 8, whole some 2.2 ms; 128 heads of 128 x 128 over 2048 tokens are better
-  // off whole.  A tenth has to be gained.
+  // bfloat16, 128 x 128): two workgroups a CU take 1.75 of that (float32: 2, the matrix instructions bound it), the
+  // segments' own walk 0.8, with the transitions' tiles beside the state's in all but the first, a step of the carry
+  // 0.8, two more launches 3.  16 heads of 128 x 128 over 32768 tokens: 582 us in 16 segments, 605 in 8, whole some
+  // 2.2 ms; 128 heads of 128 x 128 over 2048 tokens are better off whole.  A tenth has to be gained.
   const int64_t tv = tiles_for(a.dk, a.dv, true), tt = cdiv(p.rp, wide_for(a.dk, a.dv, true) ? 128 : 64), bh = a.batch * a.H;
   const double pair = bf16 ? 1.75 : 2.;
   auto rate = [pair](double wgs) { return wgs <= kDeltaCUs ? 1. : std::max(pair, wgs * pair / (2 * kDeltaCUs)); };
@@ -390,7 +390,8 @@ hipError_t launch_delta_fwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   const Plan pl = plan_of(a, bf16);
   const bool vec = all_vec(a, bf16);
   const DeltaDev d = dev_of(a, pl, space_of(a, pl, bf16, false), work, bf16, vec);
-  if (pl.nch == 1 && d.ntile == 1) return launch_pass(d, d, bf16, deltak::kPassOne, vec, st);
+  if (pl.nch == 1 && d.ntile == 1 && !wide_for(d.rows, d.cols, vec))  // that kernel's tile has 64 columns
+    return launch_pass(d, d, bf16, deltak::kPassOne, vec, st);
   hipError_t e = launch_pass(d, d, bf16, deltak::kPassPrep, vec, st);
   if (e == hipSuccess && pl.nseg > 1) {
     e = launch_pass(with_transitions(d, vec), d, bf16, deltak::kPassSeg, vec, st);
@@ -406,6 +407,7 @@ hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   const int64_t es = bf16 ? 2 : 4;
   DeltaDev d = dev_of(a, pl, w, work, bf16, vec);
   d.last = nullptr;
+  d.back = 1;
   DeltaDev r = d;
   r.v = static_cast<const char*>(a.dout);
   r.v_b = a.L * a.H * a.dv * es;

@@ -79,21 +79,76 @@ struct DeltaDev {
   int rp, cp;                  // rows and columns of states in the workspace: multiples of 16 and of kSlab
   int nch, cps, nseg;          // chunks, chunks per segment, segments
   int ntile, nvt;              // column tiles, those of the state (the others: of the transition)
+  int back;                    // P is for the walk backwards
   float scale;
 };
 
 // Parts that a float32 value enters a product in (bfloat16 storage): the state
-// and what is added to it in three, which is exact to float32, and of M (b x),
-// where both are such values, the five products that matter (with three the
-// last state is off by 1.2e-6, with five by 7e-7, 32768 tokens); all that ends in
-// a bfloat16 result in two (2^-17 of themselves), and so what a segment hands
-// to the next (the walk that finds it takes 264 instead of 330 us there, the
-// last state stays where it was).
+// and what is added to it in three, which is exact to float32; what ends in a
+// bfloat16 result in two (2^-17 of themselves).  M (b x), where both are such
+// values, is made of float16 parts instead, two of each over powers of two (see
+// Halves): exact to 2^-22 with three products of the four, where two bfloat16
+// parts of M leave the state off by 2^-18 of what the chunk's tokens give each
+// other (1114 tokens, keys of 16: the last state 1.4e-6, so 1.5e-7), and a third part, six
+// products, does not fit LDS beside a second workgroup.
 template <typename IO>
 struct DeltaCfg {
   static constexpr int STATE = HeadCfg<IO>::ES == 2 ? 3 : 1;
   static constexpr int PAIR = HeadCfg<IO>::ES == 2 ? 2 : 1;
 };
+
+// Float32 values as two float16 parts over a power of two that takes the largest of them to 2^14 .. 2^15: the parts
+// together are off by 2^-24 of a value, or by 2^-39 of the largest.
+typedef _Float16 half2 __attribute__((ext_vector_type(2)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+struct Halves {
+  float to, back;  // the power of two and its inverse
+  // of values whose largest magnitude is m: its exponent, at least that whose factor back is no denormal
+  __device__ __forceinline__ explicit Halves(float m) {
+    uint32_t e = __float_as_uint(m) & 0x7f800000u;
+    e = e < 15u << 23 ? 15u << 23 : e;
+    to = __uint_as_float((268u << 23) - e);
+    back = __uint_as_float(e - (14u << 23));
+  }
+  // v (times the power of two) as parts
+  static __device__ __forceinline__ void split(const float* v, uint4* out) {
+    uint32_t* const hi = reinterpret_cast<uint32_t*>(&out[0]);
+    uint32_t* const lo = reinterpret_cast<uint32_t*>(&out[1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const half2 h = {static_cast<_Float16>(v[2 * i]), static_cast<_Float16>(v[2 * i + 1])};
+      const half2 l = {static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h.x), -1.f, v[2 * i])),
+                       static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h.y), -1.f, v[2 * i + 1]))};
+      hi[i] = __builtin_bit_cast(uint32_t, h);
+      lo[i] = __builtin_bit_cast(uint32_t, l);
+    }
+  }
+  static __device__ __forceinline__ f32x4 mma(const uint4& a, const uint4& b, f32x4 acc) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), acc, 0, 0, 0);
+  }
+};
+// The largest of a column's values, one of an accumulator's: over the lanes li, li + 16, ..
+__device__ __forceinline__ float column_max(float m) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+  m = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  a = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+  return __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+// The largest of a wavefront's values that are not negative, in every lane
+__device__ __forceinline__ float wave_max(float m) {
+  auto take = [&](auto ctrl, auto mask) {
+    constexpr int CTRL = decltype(ctrl)::value, ROWS = decltype(mask)::value;
+    m = __builtin_fmaxf(m, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m), CTRL, ROWS, 0xf, false)));
+  };
+  using std::integral_constant;
+  take(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // up within a row of 16, then over the rows
+  take(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+  take(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+  take(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+  take(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
+  take(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(m), 63));
+}
 
 // E values (one operand register of a lane) as N parts
 template <typename IO, int N>
@@ -266,8 +321,9 @@ struct TileM {
 };
 
 // What is kept of a chunk's decays and b, a row of C floats each: G_i as a pair (log2 units), e^{G_i}, e^{G_C - G_i},
-// b_i, and 1 where the state starts anew.
-enum { kGHi, kGLo, kEk, kWe, kBeta, kAnew, kRates };
+// b_i, 1 where the state starts anew, and what the values of M and (backwards) of P are to be multiplied with, the first
+// two of the last row.
+enum { kGHi, kGLo, kEk, kWe, kBeta, kAnew, kBy, kRates };
 
 // A chunk's decays and b, one token a lane of one wavefront: asked for, then scanned.  A token past the length has
 // neither decay nor b.
@@ -305,10 +361,10 @@ __device__ __forceinline__ int length_of(const DeltaDev& p, int b) {
 
 // ---------------------------------------------------------------- M of every chunk
 
-template <typename IO, int ROWS, bool QUERY>
+template <typename IO, int ROWS>
 constexpr size_t prep_lds_bytes() {
   using K = HeadCfg<IO>;
-  constexpr size_t tiles = (QUERY ? 2 : 1) * size_t(K::C) * ROWS * K::ES;
+  constexpr size_t tiles = 2 * size_t(K::C) * ROWS * K::ES;
   constexpr size_t square = size_t(K::C) * (K::C + 4) * 4 + size_t(K::C / 16) * 16 * 20 * 4;
   return kRates * K::C * 4 + (tiles > square ? tiles : square);
 }
@@ -320,9 +376,9 @@ __device__ __forceinline__ void score_tile(int tile, int& ib, int& jb) {
   jb = tile - ib * (ib + 1) / 2;
 }
 
-// A float32 matrix [C][LD] in LDS to global memory as parts
-template <typename IO, int LD, int T>
-__device__ __forceinline__ void store_parts(const float* n, char* dst, int tid) {
+// A float32 matrix [C][LD] in LDS to global memory as parts; HALF: times `by` as parts of float16 (see Halves)
+template <typename IO, int LD, int T, bool HALF>
+__device__ __forceinline__ void store_parts(const float* n, char* dst, int tid, float by) {
   using S = Square<IO>;
   constexpr int E = HeadCfg<IO>::E;
   for (int i = tid; i < S::CHUNKS; i += T) {
@@ -331,13 +387,19 @@ __device__ __forceinline__ void store_parts(const float* n, char* dst, int tid) 
     float v[E];
     F32::ld<E>(n + r * LD + c * E, v);
     uint4 w[S::PARTS];
-    split<IO, S::PARTS>(v, w);
+    if constexpr (HALF) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] *= by;
+      Halves::split(v, w);
+    } else {
+      split<IO, S::PARTS>(v, w);
+    }
 #pragma unroll
     for (int q = 0; q < S::PARTS; ++q) *reinterpret_cast<uint4*>(dst + 16 * (q * S::CHUNKS + i)) = w[q];
   }
 }
 
-// One (batch row, head, chunk) a workgroup of four wavefronts.  N (and P) on the
+// One (batch row, head, chunk) a workgroup of four wavefronts.  N and P on the
 // matrix cores; the 16 x 16 blocks on the diagonal of I + N diag(b) inverted by
 // substitution, all of them by one wavefront, a block a group of 16 lanes and a
 // column a lane; then, a block column a wavefront, by block rows
@@ -345,11 +407,12 @@ __device__ __forceinline__ void store_parts(const float* n, char* dst, int tid) 
 // in float32 matrix instructions, the tiles M_JK staying in registers.
 // (Substitution, not powers of N b: keys alike make those grow past float32
 // where the inverse does not.)
-template <typename IO, int ROWS, bool QUERY, bool VEC>
+template <typename IO, int ROWS, bool VEC>
 __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char* lds) {
   using K = HeadCfg<IO>;
   constexpr int ES = K::ES, C = K::C, T = 256, IB = C / 16, NK = ROWS * ES / 16, RS = ROWS / K::KS;
   constexpr int LD = C + 4, TILES = IB * (IB + 1) / 2, MINE = (TILES + 3) / 4, MB = Square<IO>::BYTES;
+  constexpr bool HALF = ES == 2;
   using TK = Tile<IO, NK, T>;
   float* const rt = reinterpret_cast<float*>(lds);  // [kRates][C]
   char* const ty = reinterpret_cast<char*>(rt + kRates * C);
@@ -364,12 +427,11 @@ __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char
   if (t0 >= len) return;
   const int64_t chunk = static_cast<int64_t>(bh) * p.nch + pc;
 
-  uint4 ry[TK::CNT], rx[QUERY ? TK::CNT : 1];
+  uint4 ry[TK::CNT], rx[TK::CNT];
   Rates<IO> rates;
   if (wave == 3) rates.load(p, b, h, t0, len, lane);
   TK::template load<VEC>(p.k + b * p.k_b + static_cast<int64_t>(h / p.rep) * p.rows * ES, p.k_t, t0, len, p.rows, tid, ry);
-  if constexpr (QUERY)
-    TK::template load<VEC>(p.q + b * p.q_b + static_cast<int64_t>(h / p.rep) * p.rows * ES, p.q_t, t0, len, p.rows, tid, rx);
+  TK::template load<VEC>(p.q + b * p.q_b + static_cast<int64_t>(h / p.rep) * p.rows * ES, p.q_t, t0, len, p.rows, tid, rx);
   if (wave == 3) {
     float hi, lo;
     rates.scan(hi, lo);
@@ -385,9 +447,9 @@ __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char
     }
   }
   TK::store(ty, tid, ry);
-  if constexpr (QUERY) TK::store(tx, tid, rx);
+  TK::store(tx, tid, rx);
   __syncthreads();
-  if (tid < kRates * C / 4)
+  if (tid < kBy * C / 4)
     reinterpret_cast<float4*>(p.rates + chunk * kRates * C)[tid] = reinterpret_cast<const float4*>(rt)[tid];
 
   // lane holds j = 4 g + v of i = li
@@ -406,14 +468,14 @@ __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char
     for (int s = 0; s < RS; ++s) {
       const uint4 fy = frag_row<NK>(ty, rb, jb, s);
       a = mma<IO>(fy, frag_row<NK>(ty, rb, ib, s), a);
-      if constexpr (QUERY) c = mma<IO>(fy, frag_row<NK>(tx, rb, ib, s), c);
+      c = mma<IO>(fy, frag_row<NK>(tx, rb, ib, s), c);
     }
     const float gi = rt[kGHi * C + i], gl = rt[kGLo * C + i];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const float d = __builtin_amdgcn_exp2f((gi - rt[kGHi * C + j0 + v]) + (gl - rt[kGLo * C + j0 + v]));
       sc[m][v] = j0 + v < i ? times(d, a[v]) : 0.f;
-      if constexpr (QUERY) sq[m][v] = j0 + v <= i ? times(p.scale * d, c[v]) : 0.f;
+      sq[m][v] = j0 + v <= i ? times(p.scale * d, c[v]) : 0.f;
     }
   }
   auto put_scores = [&](const f32x4 (&x)[MINE]) {
@@ -469,25 +531,53 @@ __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char
   }
   __syncthreads();
   if (wave < IB) {
+    float most = 0.f;
 #pragma unroll
     for (int I = 0; I < IB; ++I)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) n[(16 * I + 4 * g + v) * LD + 16 * wave + li] = -M[I][v];
+      for (int v = 0; v < 4; ++v) {
+        n[(16 * I + 4 * g + v) * LD + 16 * wave + li] = -M[I][v];
+        if constexpr (HALF) most = __builtin_fmaxf(most, __builtin_fabsf(M[I][v]));
+      }
+    if constexpr (HALF) {
+      most = wave_max(most);
+      if (lane == 0) inv[wave] = most;
+    }
   }
   __syncthreads();
-  store_parts<IO, LD, T>(n, p.m + chunk * MB, tid);
-  if constexpr (QUERY) {
-    __syncthreads();
-    put_scores(sq);  // above the diagonal -M holds zeros, and so does P
-    __syncthreads();
-    store_parts<IO, LD, T>(n, p.s + chunk * MB, tid);
+  // the factor of the four wavefronts' largest value, left for the walk
+  auto factor = [&](const float* most, int at) {
+    const Halves h(__builtin_fmaxf(__builtin_fmaxf(most[0], most[1]), __builtin_fmaxf(most[2], most[3])));
+    if (tid == 0) p.rates[(chunk * kRates + kBy) * C + at] = h.back;
+    return h.to;
+  };
+  float by = 1.f;
+  if constexpr (HALF) by = factor(inv, 0);
+  store_parts<IO, LD, T, HALF>(n, p.m + chunk * MB, tid, by);
+  __syncthreads();
+  put_scores(sq);  // above the diagonal -M holds zeros, and so does P
+  if constexpr (HALF) {
+    float most = 0.f;
+#pragma unroll
+    for (int m = 0; m < MINE; ++m)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) most = __builtin_fmaxf(most, __builtin_fabsf(sq[m][v]));
+    most = wave_max(most);
+    if (lane == 0) inv[4 + wave] = most;
+  }
+  __syncthreads();
+  if (HALF && p.back) {
+    by = factor(inv + 4, 1);
+    store_parts<IO, LD, T, HALF>(n, p.s + chunk * MB, tid, by);
+  } else {
+    store_parts<IO, LD, T, false>(n, p.s + chunk * MB, tid, 1.f);
   }
 }
 
 template <typename IO, int ROWS, bool VEC>
 __global__ void __launch_bounds__(256) ssm_delta_prep_kernel(const DeltaDev p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  delta_prep<IO, ROWS, true, VEC>(p, blockIdx.x, lds);
+  delta_prep<IO, ROWS, VEC>(p, blockIdx.x, lds);
 }
 
 // ---------------------------------------------------------------- the walk over the length, forwards
@@ -565,23 +655,10 @@ __device__ __forceinline__ void keep(char* dst, float* by, int rows, int cp, int
     for (int rt = 0; rt < N; ++rt)
 #pragma unroll
       for (int v = 0; v < 4; ++v) m = __builtin_fmaxf(m, __builtin_fabsf(X[rt][v]));
-    auto take = [&](auto ctrl, auto mask) {
-      constexpr int CTRL = decltype(ctrl)::value, ROWS = decltype(mask)::value;
-      m = __builtin_fmaxf(m, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m), CTRL, ROWS, 0xf, false)));
-    };
-    using std::integral_constant;
-    take(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // up within a row of 16, then over the rows
-    take(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
-    take(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
-    take(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
-    take(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
-    take(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
-    // the exponent of the largest, at least that whose factor back is no denormal
-    int e = (__builtin_amdgcn_readlane(__float_as_int(m), 63) >> 23) & 255;
-    e = e < 15 ? 15 : e;
-    f = __int_as_float((268 - e) << 23);
+    const Halves h(wave_max(m));
+    f = h.to;
     const Rsrc rb = make_rsrc(by, rows > 0 ? static_cast<uint32_t>(cp / 16 * 4) : 0u);
-    __builtin_amdgcn_raw_buffer_store_b32(static_cast<uint32_t>(e - 14) << 23, rb, (c & 15) == 0 && g == 0 ? c / 16 * 4 : kOOB, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h.back), rb, (c & 15) == 0 && g == 0 ? c / 16 * 4 : kOOB, 0, 0);
   }
 #pragma unroll
   for (int rt = 0; rt < N; ++rt)
@@ -614,8 +691,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
   constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
   constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
-  constexpr int PP = DeltaCfg<IO>::PAIR, PS = MODE == kDeltaSeg ? PP : DeltaCfg<IO>::STATE;
-  constexpr int PL = PP == 2 ? PS - 1 : 0;  // parts of b x that meet M's second part
+  constexpr int PP = DeltaCfg<IO>::PAIR, PS = DeltaCfg<IO>::STATE;
   constexpr int MB = Square<IO>::BYTES, ML = Square<IO>::LDS;  // bytes of a chunk's M, and in LDS
   using TK = Tile<IO, NK, T>;
   using TZ = Tile<IO, NZ, T>;
@@ -796,26 +872,43 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     }
     // ---- x, then r = x - M (b x)
     constexpr int LOW = IB == 2 ? 3 : 6;  // operand steps on and below the diagonal
-    uint4 bx[JS][PS], fm[LOW];
+    uint4 bx[JS][PP], fm[LOW];
+    float back = 1.f;
     const int mb0 = state_row_base<IO, NP>(li, g);
 #pragma unroll
     for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
       for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) fm[n] = frag_state_row<IO, NP>(tm, mb0, i, js);
     __builtin_amdgcn_sched_barrier(0);
+    {
+      float w[JS][E], most = 0.f;
 #pragma unroll
-    for (int js = 0; js < JS; ++js) {
-      float v[E] = {}, bb[E];
-      F32::ld<E>(bt + KS * js + E * g, bb);
-      if (!trans) unpack<IO>(fz[js], v);
+      for (int js = 0; js < JS; ++js) {
+        float v[E] = {}, bb[E];
+        F32::ld<E>(bt + KS * js + E * g, bb);
+        if (!trans) unpack<IO>(fz[js], v);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int t = tile_of<IO>(js, i);
-        v[i] -= times(e[js][i], X[t][i & 3]);
-        X[t][i & 3] = v[i];
-        v[i] *= bb[i];
+        for (int i = 0; i < E; ++i) {
+          const int t = tile_of<IO>(js, i);
+          v[i] -= times(e[js][i], X[t][i & 3]);
+          X[t][i & 3] = v[i];
+          w[js][i] = bb[i] * v[i];
+          most = __builtin_fmaxf(most, __builtin_fabsf(w[js][i]));
+        }
       }
-      split<IO, PS>(v, bx[js]);
+      if constexpr (PP == 2) {
+        const Halves by(column_max(most));
+        back = by.back * rt[kBy * C];
+#pragma unroll
+        for (int js = 0; js < JS; ++js) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) w[js][i] *= by.to;
+          Halves::split(w[js], bx[js]);
+        }
+      } else {
+#pragma unroll
+        for (int js = 0; js < JS; ++js) split<IO, 1>(w[js], bx[js]);
+      }
     }
     uint4 fl[LOW];
     if constexpr (PP == 2) {
@@ -831,15 +924,29 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
 #pragma unroll
       for (int ib = 0; ib < IB; ++ib) scale(O[ib], p.scale * ek[16 * ib + li]);
     }
+    if constexpr (PP == 2) {
+      f32x4 Y[IB] = {};
 #pragma unroll
-    for (int q = 0; q < PS + PL; ++q)
+      for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int i = 0, n = 0; i < IB; ++i)
+#pragma unroll
+          for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n)
+            Y[i] = q < 2 ? Halves::mma(fm[n], bx[js][1 - q], Y[i]) : Halves::mma(fl[n], bx[js][0], Y[i]);
+      mix<LOW * 3, 3>();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) X[i][v] = __builtin_fmaf(Y[i][v], back, X[i][v]);
+    } else {
 #pragma unroll
       for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
-        for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n)
-          X[i] = q < PS ? mma<IO>(fm[n], bx[js][q], X[i]) : mma<IO>(fl[n], bx[js][q - PS], X[i]);
-    mix<LOW * (PS + PL), 2>();
-    __builtin_amdgcn_sched_barrier(0);
+        for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) X[i] = mma<IO>(fm[n], bx[js][0], X[i]);
+      mix<LOW, 2>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
     if (QUERY && kk + 1 < nc) load_queries(pc + 1);
     const int pb = lane_base<IO, NP>(li, g);
     if constexpr (QUERY) {
@@ -945,14 +1052,14 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_kernel(const DeltaDev 
   delta_walk<IO, ROWS, NW, MODE, VEC>(p, blockIdx.x, lds);
 }
 
-// One chunk and one column tile: a launch for both (17 tokens, 4 heads of 32 x 32: SSM_ONE).
+// One chunk and one column tile: a launch for both (17 tokens, 4 heads of 32 x 32: 12.7 us, two launches 15.6).
 template <typename IO, int ROWS, bool VEC>
 __global__ void __launch_bounds__(256, 2) ssm_delta_one_kernel(const DeltaDev p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   // the walk's workgroup of a (batch row, head) makes that one's M
   int ct, seg, h, b;
   place(p, blockIdx.x, 1, ct, seg, h, b);
-  delta_prep<IO, ROWS, true, VEC>(p, b * p.H + h, lds);
+  delta_prep<IO, ROWS, VEC>(p, b * p.H + h, lds);
   __syncthreads();  // what it wrote, the walk reads back
   delta_walk<IO, ROWS, 4, kDeltaOut, VEC>(p, blockIdx.x, lds);
 }
@@ -967,7 +1074,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
   constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
   constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
-  constexpr int PP = DeltaCfg<IO>::PAIR, PS = SEG ? PP : DeltaCfg<IO>::STATE;
+  constexpr int PP = DeltaCfg<IO>::PAIR, PS = DeltaCfg<IO>::STATE;
   constexpr int MB = Square<IO>::BYTES, ML = Square<IO>::LDS;
   using TK = Tile<IO, NK, T>;
   using TZ = Tile<IO, NZ, T>;
@@ -1071,12 +1178,12 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
         for (int js = 0; js < JS; ++js)
           if (KS * (js + 1) > 16 * i) f[n++] = frag_state_col<IO, NP>(tile, mc0, i, js);
     };
-    auto times_square = [&](const uint4 (&f)[LOW], const uint4 (&by)[JS], f32x4 (&acc)[IB]) {
+    auto times_square = [&](const uint4 (&f)[LOW], const uint4 (&by)[JS], f32x4 (&acc)[IB], auto&& add) {
 #pragma unroll
       for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
         for (int js = 0; js < JS; ++js)
-          if (KS * (js + 1) > 16 * i) acc[i] = mma<IO>(f[n++], by[js], acc[i]);
+          if (KS * (js + 1) > 16 * i) acc[i] = add(f[n++], by[js], acc[i]);
     };
     {
       const int sb = state_row_base<IO, NK>(li, g), zb0 = col_base<IO, NZ>(li, g);
@@ -1117,28 +1224,71 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     // ---- y = P^T dO + e^{G_C - G} X
     if constexpr (PP == 2) read_square(tp + C * C * ES, fl);
     __builtin_amdgcn_sched_barrier(0);
-    times_square(ft, fz, Y);
-    if constexpr (PP == 2) times_square(fl, fz, Y);
+    auto half = [](const uint4& a, const uint4& b, f32x4 acc) { return Halves::mma(a, b, acc); };
+    float yb = 1.f;
+    if constexpr (PP == 2) {
+      // dO as float16 over a power of two: exact but for what is below 2^-32 of the column's largest
+      uint4 fo[JS];
+      float d[JS][E], most = 0.f;
+#pragma unroll
+      for (int js = 0; js < JS; ++js) {
+        unpack<IO>(fz[js], d[js]);
+#pragma unroll
+        for (int i = 0; i < E; ++i) most = __builtin_fmaxf(most, __builtin_fabsf(d[js][i]));
+      }
+      const Halves h(column_max(most));
+      yb = h.back * rt[kBy * C + 1];
+#pragma unroll
+      for (int js = 0; js < JS; ++js) {
+        uint32_t* const f = reinterpret_cast<uint32_t*>(&fo[js]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const half2 x = {static_cast<_Float16>(d[js][2 * i] * h.to), static_cast<_Float16>(d[js][2 * i + 1] * h.to)};
+          f[i] = __builtin_bit_cast(uint32_t, x);
+        }
+      }
+      times_square(ft, fo, Y, half);
+      times_square(fl, fo, Y, half);
+    } else {
+      times_square(ft, fz, Y, mma<IO>);
+    }
     read_square(tm, ft);
     if constexpr (PP == 2) read_square(tm + C * C * ES, fl);
     __builtin_amdgcn_sched_barrier(0);
     // ---- e = y - M^T (b y)
-    uint4 by[PS][JS];
+    uint4 by[PP][JS];
+    float back = 1.f;
+    {
+      float bb[JS][E], most = 0.f;
 #pragma unroll
-    for (int js = 0; js < JS; ++js) {
-      float w[E], bb[E];
-      uint4 f[PS];
-      F32::ld<E>(we + KS * js + E * g, w);
-      F32::ld<E>(bt + KS * js + E * g, bb);
+      for (int js = 0; js < JS; ++js) {
+        float w[E];
+        F32::ld<E>(we + KS * js + E * g, w);
+        F32::ld<E>(bt + KS * js + E * g, bb[js]);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int t = tile_of<IO>(js, i);
-        X[t][i & 3] = Y[t][i & 3] + times(w[i], X[t][i & 3]);
-        bb[i] *= X[t][i & 3];
+        for (int i = 0; i < E; ++i) {
+          const int t = tile_of<IO>(js, i);
+          X[t][i & 3] = __builtin_fmaf(Y[t][i & 3], yb, times(w[i], X[t][i & 3]));
+          bb[js][i] *= X[t][i & 3];
+          most = __builtin_fmaxf(most, __builtin_fabsf(bb[js][i]));
+        }
       }
-      split<IO, PS>(bb, f);
+      if constexpr (PP == 2) {
+        const Halves h(column_max(most));
+        back = h.back * rt[kBy * C];
 #pragma unroll
-      for (int q = 0; q < PS; ++q) by[q][js] = f[q];
+        for (int js = 0; js < JS; ++js) {
+          uint4 f[2];
+#pragma unroll
+          for (int i = 0; i < E; ++i) bb[js][i] *= h.to;
+          Halves::split(bb[js], f);
+          by[0][js] = f[0];
+          by[1][js] = f[1];
+        }
+      } else {
+#pragma unroll
+        for (int js = 0; js < JS; ++js) split<IO, 1>(bb[js], &by[0][js]);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     // What the state before the chunk is made of, one operand after the other: scale e^G dO (with Q's rows), then
@@ -1162,14 +1312,23 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     parts(0);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) scale(R[rt], end_dec);
-#pragma unroll
-    for (int q = 0; q < PS; ++q) times_square(ft, by[q], X);
     if constexpr (PP == 2) {
-      times_square(fl, by[0], X);
-      times_square(fl, by[1], X);
+#pragma unroll
+      for (int i = 0; i < IB; ++i) Y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      times_square(ft, by[1], Y, half);
+      times_square(fl, by[0], Y, half);
+      times_square(ft, by[0], Y, half);
+      mix<LOW * 3, 3>();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) X[i][v] = __builtin_fmaf(Y[i][v], back, X[i][v]);
+    } else {
+      times_square(ft, by[0], X, mma<IO>);
+      mix<LOW, 3>();
+      __builtin_amdgcn_sched_barrier(0);
     }
-    mix<LOW * (PS + (PP == 2 ? 2 : 0)), 3>();
-    __builtin_amdgcn_sched_barrier(0);
     if (kk + 1 < nc) load_late(pc - 1);
     if constexpr (!SEG) keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp * kept_size<IO>(), p.res_by + (bh * p.nch + pc) * (p.cp / 16), C, p.cp, cw + li, g, X);
 
@@ -1745,7 +1904,7 @@ hipError_t allow_lds(Kern kern, size_t smem, std::atomic<uint64_t>& allowed) {
 template <typename IO, int ROWS, bool VEC>
 hipError_t launch_prep_t(const DeltaDev& p, hipStream_t st) {
   static std::atomic<uint64_t> allowed{0};
-  constexpr size_t smem = prep_lds_bytes<IO, ROWS, true>();
+  constexpr size_t smem = prep_lds_bytes<IO, ROWS>();
   auto kern = ssm_delta_prep_kernel<IO, ROWS, VEC>;
   if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.batch * p.H * p.nch)), dim3(256), smem, st, p);
@@ -1755,7 +1914,7 @@ hipError_t launch_prep_t(const DeltaDev& p, hipStream_t st) {
 template <typename IO, int ROWS, bool VEC>
 hipError_t launch_one_t(const DeltaDev& p, hipStream_t st) {
   static std::atomic<uint64_t> allowed{0};
-  constexpr size_t prep = prep_lds_bytes<IO, ROWS, true>(), walk = delta_lds_bytes<IO, ROWS, 4, true>();
+  constexpr size_t prep = prep_lds_bytes<IO, ROWS>(), walk = delta_lds_bytes<IO, ROWS, 4, true>();
   constexpr size_t smem = prep > walk ? prep : walk;
   auto kern = ssm_delta_one_kernel<IO, ROWS, VEC>;
   if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;

@@ -60,6 +60,33 @@ def test_rows_without_tokens(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("dk", [16, 64, 65, 128, 136, 256])
+def test_few_tokens_of_every_width(dk, dtype):
+    """One chunk and two; column tiles of 64 and of 128, whole and not."""
+    for L, dv in ((1, 64), (5, 72), (17, 100), (31, 128), (40, 136), (53, 256), (65, 128), (53, 192)):
+        x, do, dlast = make(2, L, 2, 1, dk, dv, dtype, seed=dk + dv)
+        torch.full((1 << 24,), float("nan"), device=DEV)  # what the outputs' memory may have held
+        against_oracle(x, do, dlast, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_states_are_kept_to_float32(dtype):
+    """Few keys, many tokens, no decay: a token's update of the last state and of dh0 is a few float32 operations, each
+    off by 2^-24 at most of the values it works on, and those of different tokens are independent: twice the square
+    root of the tokens' number, with either storage type."""
+    for case in ((2, 1114, 16, 16, 16, 64), (1, 2000, 2, 2, 48, 64)):
+        x, do, dlast = make(*case, dtype, seed=case[1], g=False)
+        r = both(x, do, dlast)
+        y = f64(x)
+        _, last = delta.delta_scan(**y)
+        want = delta.delta_scan_bwd(**y, do=do.double().cpu().numpy(), dlast=dlast.double().cpu().numpy())
+        most = 2 * 2.0 ** -24 * case[1] ** 0.5
+        for got, w in ((r["last"], last), (r["dh0"], want["dh0"])):
+            off = np.linalg.norm(got.double().cpu().numpy() - w) / np.linalg.norm(w)
+            assert off <= most, (off, most)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 @pytest.mark.parametrize("size", [(3, 140, 4, 2, 64, 64), (3, 1300, 2, 1, 32, 96)], ids=["", "segments"])
 def test_what_lies_past_a_length_is_not_read(size, dtype):
     x, do, dlast = make(*size, dtype, seed=2)
