@@ -55,10 +55,10 @@ int64_t tiles_for(int64_t rows, int64_t cols, bool vec) { return cdiv(cols, wide
 template <int NW, bool REV>
 __global__ void __launch_bounds__(64 * NW) ssm_delta_carry_kernel(float* state, const float* trans, int nseg, int rp, int cp) {
   __shared__ float carried[16 * NW][17];
-  const int64_t bh = blockIdx.y;
+  const int64_t bh = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c = blockIdx.x * 16 + li, tiles = rp / 16, row = 16 * wave;
+  const int c = blockIdx.y * 16 + li, tiles = rp / 16, row = 16 * wave;
   const int64_t ws = static_cast<int64_t>(rp) * cp, ts = static_cast<int64_t>(rp) * rp;
   float* const s = state + bh * nseg * ws;
   const float* const m = trans + bh * nseg * ts;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(64 * NW) ssm_delta_carry_kernel(float* state, 
     }
   };
   for (int i = tid; i < rp * 16; i += 64 * NW)
-    carried[i / 16][i % 16] = s[first * ws + static_cast<int64_t>(i / 16) * cp + blockIdx.x * 16 + i % 16];
+    carried[i / 16][i % 16] = s[first * ws + static_cast<int64_t>(i / 16) * cp + blockIdx.y * 16 + i % 16];
 #pragma unroll
   for (int k = 0; k < NW; ++k) load_a(first + step, k);
   __syncthreads();
@@ -363,7 +363,7 @@ hipError_t launch_carry(const DeltaDev& d, bool rev, hipStream_t st) {
   const bool wide = d.rp > 128;
   auto kern = wide ? (rev ? ssm_delta_carry_kernel<16, true> : ssm_delta_carry_kernel<16, false>)
                    : (rev ? ssm_delta_carry_kernel<8, true> : ssm_delta_carry_kernel<8, false>);
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(d.cp / 16), static_cast<unsigned>(d.batch * d.H)), dim3(wide ? 1024 : 512),
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(d.batch * d.H), static_cast<unsigned>(d.cp / 16)), dim3(wide ? 1024 : 512),
                      0, st, d.seg_state, d.seg_trans, d.nseg, d.rp, d.cp);
   return hipGetLastError();
 }
