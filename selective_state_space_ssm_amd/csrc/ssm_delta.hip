@@ -289,7 +289,7 @@ int64_t grad_heads(const DeltaArgs& a, const Plan& pl) {
 
 // Where the workspace's parts are, in bytes from its start.
 struct Space {
-  int64_t m, s, rates, ss, rs, trans, s0, r1, r, e, s0_by, r1_by, r_by, e_by, pq, pk, total;
+  int64_t m, s, rates, ss, rs, trans, s0, r1, r, e, s0_by, r1_by, r_by, e_by, do_by, pq, pk, total;
 };
 Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
   Space w{};
@@ -314,7 +314,7 @@ Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
     w.r1 = take(kept * bh * pl.nch * pl.rp * pl.cp);
     w.r = take(kept * bh * pl.nch * pl.C * pl.cp);
     w.e = take(kept * bh * pl.nch * pl.C * pl.cp);
-    for (int64_t* by : {&w.s0_by, &w.r1_by, &w.r_by, &w.e_by}) *by = take(bf16 ? 4 * bh * pl.nch * pl.cp / 16 : 0);
+    for (int64_t* by : {&w.s0_by, &w.r1_by, &w.r_by, &w.e_by, &w.do_by}) *by = take(bf16 ? 4 * bh * pl.nch * pl.cp / 16 : 0);
     const int64_t hn = grad_heads(a, pl);
     if (hn < a.H / a.Hk) {
       w.pq = take(4 * bh / hn * a.L * a.dk);
@@ -419,6 +419,7 @@ hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   r.res = work + w.e;
   r.states_by = reinterpret_cast<float*>(work + w.r1_by);
   r.res_by = reinterpret_cast<float*>(work + w.e_by);
+  r.in_by = reinterpret_cast<float*>(work + w.do_by);
   hipError_t e = launch_pass(d, d, bf16, deltak::kPassPrep, vec, st);
   if (e == hipSuccess && pl.nseg > 1) {
     e = launch_pass(with_transitions(d, vec), r, bf16, deltak::kPassBothSeg, vec, st);
@@ -433,7 +434,7 @@ hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   gd.f = d;
   gd.f.v = r.v; gd.f.v_b = r.v_b; gd.f.v_t = r.v_t;
   gd.r1 = r.states; gd.e = r.res;
-  gd.r1_by = r.states_by; gd.e_by = r.res_by;
+  gd.r1_by = r.states_by; gd.e_by = r.res_by; gd.do_by = r.in_by;
   gd.hn = static_cast<int>(hn);
   gd.parts = hn < rep;
   gd.dq = gd.parts ? work + w.pq : static_cast<char*>(a.dq);

@@ -75,6 +75,7 @@ struct DeltaDev {
   char* res;                   // [b][H][nch][C][cp]: r, backwards e, likewise
   float* states_by;            // [b][H][nch][cp / 16]: what they are to be multiplied with (bfloat16 storage)
   float* res_by;
+  float* in_by;                // backwards, of dO's columns
   int batch, H, L, rows, cols;
   int rp, cp;                  // rows and columns of states in the workspace: multiples of 16 and of kSlab
   int nch, cps, nseg;          // chunks, chunks per segment, segments
@@ -122,6 +123,17 @@ struct Halves {
       hi[i] = __builtin_bit_cast(uint32_t, h);
       lo[i] = __builtin_bit_cast(uint32_t, l);
     }
+  }
+  // one part, for what is rounded no further (2^-11 of a value)
+  static __device__ __forceinline__ uint4 one(const float* v, float by) {
+    uint4 out;
+    uint32_t* const w = reinterpret_cast<uint32_t*>(&out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const half2 h = {static_cast<_Float16>(v[2 * i] * by), static_cast<_Float16>(v[2 * i + 1] * by)};
+      w[i] = __builtin_bit_cast(uint32_t, h);
+    }
+    return out;
   }
   static __device__ __forceinline__ f32x4 mma(const uint4& a, const uint4& b, f32x4 acc) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), acc, 0, 0, 0);
@@ -639,6 +651,12 @@ __device__ __forceinline__ void store_state(float* dst, int rows, int cols, int 
 template <typename IO>
 constexpr int kept_size() { return HeadCfg<IO>::ES; }
 
+// A factor of the columns c .. c + 15 of a wavefront beside the chunk's others; nothing is written with rows = 0.
+__device__ __forceinline__ void keep_factor(float* by, int rows, int cp, int c, int g, float f) {
+  const Rsrc r = make_rsrc(by, rows > 0 ? static_cast<uint32_t>(cp / 16 * 4) : 0u);
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), r, (c & 15) == 0 && g == 0 ? c / 16 * 4 : kOOB, 0, 0);
+}
+
 // Accumulator tiles to `rows` rows of cp values in the workspace (a resource, which bounds the rows; none of it with
 // rows = 0), by instructions whose number does not depend on the sizes: loads and stores are counted together and in
 // order, and the wait for the next chunk's loads can leave these in flight only if their number is known.  by: the
@@ -657,8 +675,7 @@ __device__ __forceinline__ void keep(char* dst, float* by, int rows, int cp, int
       for (int v = 0; v < 4; ++v) m = __builtin_fmaxf(m, __builtin_fabsf(X[rt][v]));
     const Halves h(wave_max(m));
     f = h.to;
-    const Rsrc rb = make_rsrc(by, rows > 0 ? static_cast<uint32_t>(cp / 16 * 4) : 0u);
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h.back), rb, (c & 15) == 0 && g == 0 ? c / 16 * 4 : kOOB, 0, 0);
+    keep_factor(by, rows, cp, c, g, h.back);
   }
 #pragma unroll
   for (int rt = 0; rt < N; ++rt)
@@ -1142,6 +1159,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
       const f32x4 none[RT > IB ? RT : IB] = {};
       const int li = tid & 15, g = (tid & 63) >> 4;
       keep<IO, RT>(p.states, p.states_by, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
+      if constexpr (PP == 2) keep_factor(p.in_by, 0, p.cp, cw + li, g, 1.f);
       keep<IO, IB>(p.res, p.res_by, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
     }
   }
@@ -1225,7 +1243,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     if constexpr (PP == 2) read_square(tp + C * C * ES, fl);
     __builtin_amdgcn_sched_barrier(0);
     auto half = [](const uint4& a, const uint4& b, f32x4 acc) { return Halves::mma(a, b, acc); };
-    float yb = 1.f;
+    float yb = 1.f, ob = 1.f;
     if constexpr (PP == 2) {
       // dO as float16 over a power of two: exact but for what is below 2^-32 of the column's largest
       uint4 fo[JS];
@@ -1239,14 +1257,8 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
       const Halves h(column_max(most));
       yb = h.back * rt[kBy * C + 1];
 #pragma unroll
-      for (int js = 0; js < JS; ++js) {
-        uint32_t* const f = reinterpret_cast<uint32_t*>(&fo[js]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const half2 x = {static_cast<_Float16>(d[js][2 * i] * h.to), static_cast<_Float16>(d[js][2 * i + 1] * h.to)};
-          f[i] = __builtin_bit_cast(uint32_t, x);
-        }
-      }
+      for (int js = 0; js < JS; ++js) fo[js] = Halves::one(d[js], h.to);
+      if constexpr (!SEG) ob = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, Halves(wave_max(most)).back)));
       times_square(ft, fo, Y, half);
       times_square(fl, fo, Y, half);
     } else {
@@ -1331,6 +1343,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     }
     if (kk + 1 < nc) load_late(pc - 1);
     if constexpr (!SEG) keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp * kept_size<IO>(), p.res_by + (bh * p.nch + pc) * (p.cp / 16), C, p.cp, cw + li, g, X);
+    if constexpr (!SEG && PP == 2) keep_factor(p.in_by + (bh * p.nch + pc) * (p.cp / 16), 1, p.cp, cw + li, g, ob);
 
     const int yb0 = state_col_base<IO, NK>(li, g);
 #pragma unroll
@@ -1383,6 +1396,7 @@ struct DeltaGradDev {
   const char* e;               // [b][H][nch][C][cp]
   const float* r1_by;          // their factors
   const float* e_by;
+  const float* do_by;
   char* dq;                    // [b][L][H / hn][rows]; float32 parts with `parts`
   char* dk;
   char* dv;                    // [b][L][H][cols]
@@ -1394,11 +1408,11 @@ struct DeltaGradDev {
 
 // Slabs in LDS: two where they fit, so that the next one is written while one is worked on.
 template <int ROWS>
-constexpr int grad_buffers() { return ROWS == 256 ? 1 : 2; }
+constexpr int grad_buffers() { return ROWS == 128 ? 2 : 1; }
 template <typename IO, int ROWS, int NW>
 constexpr size_t grad_lds_bytes() {
   using K = HeadCfg<IO>;
-  constexpr size_t slab = size_t(K::C) * kSlab * K::ES * (1 + 2 * DeltaCfg<IO>::PAIR);
+  constexpr size_t slab = size_t(K::C) * kSlab * K::ES * 3;
   constexpr size_t sc = size_t(2) * K::C * K::C * K::ES * DeltaCfg<IO>::PAIR;
   return 2 * size_t(K::C) * ROWS * K::ES + grad_buffers<ROWS>() * slab + sc + (size_t(2) * NW + kRates + 1) * K::C * 4 + NW * 4;
 }
@@ -1437,7 +1451,8 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW;
   constexpr int NK = ROWS * ES / 16, NS = kSlab * ES / 16, NP = C * ES / 16;
   constexpr int IB = C / 16, JS = C / KS, SS = kSlab / KS, CT = ROWS / 16 / NW, NBUF = grad_buffers<ROWS>();
-  constexpr int PP = DeltaCfg<IO>::PAIR, SB = C * kSlab * ES, PB = C * C * ES, SLAB = SB * (1 + 2 * PP);
+  constexpr int PP = DeltaCfg<IO>::PAIR, SB = C * kSlab * ES, PB = C * C * ES, SLAB = 3 * SB;
+  constexpr bool HALF = ES == 2;
   constexpr int TILES = IB * (IB + 1) / 2, MINE = (2 * TILES + NW - 1) / NW;
   constexpr int TASKS = C * NS / T;  // staging tasks a thread, rows tid / NS + i T / NS
   constexpr bool MULTI = ROWS < kGradOneHead;
@@ -1491,7 +1506,7 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
     // What a thread has in flight: its part of a slab's dO, r and e, and the operands S_0 and R_C of its wavefront for
     // the next two steps.
     uint4 go[TASKS], gr[TASKS], ge[TASKS], s0[2][CT], r1[2][CT], rr[TR::CNT];
-    float gr_by[TASKS], ge_by[TASKS], s0_by[2], r1_by[2];
+    float gr_by[TASKS], ge_by[TASKS], s0_by[2], r1_by[2], most[5] = {};
     auto factor = [&](const float* by, int64_t chunk, int col) {
       if constexpr (KB == 4) return 1.f;
       const Rsrc r = make_rsrc(by + chunk * (p.cp / 16), bybytes);
@@ -1511,6 +1526,15 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
         gr_by[i] = factor(p.res_by, chunk, col);
         ge_by[i] = factor(d.e_by, chunk, col);
       }
+    };
+    // a head's factors, those of 16 columns a lane
+    auto load_factors = [&](int hh) {
+      const int64_t chunk = chunk0 + static_cast<int64_t>(hh) * p.nch;
+      most[0] = factor(p.states_by, chunk, 16 * lane);
+      most[1] = factor(d.r1_by, chunk, 16 * lane);
+      most[2] = factor(p.res_by, chunk, 16 * lane);
+      most[3] = factor(d.e_by, chunk, 16 * lane);
+      most[4] = factor(d.do_by, chunk, 16 * lane);
     };
     // step n of head hh, of the next head where this one has none
     auto load_states = [&](int hh, int n, int to) {
@@ -1536,6 +1560,7 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
       TK::template load<VEC>(p.q + b * p.q_b + static_cast<int64_t>(hk) * p.rows * ES, p.q_t, t0, len, p.rows, tid, rx);
       TK::template load<VEC>(p.k + b * p.k_b + static_cast<int64_t>(hk) * p.rows * ES, p.k_t, t0, len, p.rows, tid, ry);
       TR::load(reinterpret_cast<const char*>(p.rates + chunk0 * kRates * C), tid, rr);
+      if constexpr (HALF) load_factors(0);
       load_slab(0, 0);
       load_states(0, 0, 0);
       load_states(0, 1, 1);
@@ -1551,6 +1576,17 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
       __syncthreads();
       if (hh + 1 < d.hn) TR::load(reinterpret_cast<const char*>(p.rates + (chunk0 + (hh + 1) * static_cast<int64_t>(p.nch)) * kRates * C), tid, rr);
 
+      // float16 operands: over the largest of all columns' powers of two, b's at least 1
+      float sb = 1.f, rb = 1.f, ub = 1.f, eb = 1.f, ob = 1.f, si = 1.f, ri = 1.f, ui = 1.f, ei = 1.f, oi = 1.f;
+      if constexpr (HALF) {
+        auto inverse = [](float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); };
+        const float bm = wave_max(__builtin_fabsf(lane < C ? bt[lane] : 0.f));
+        const float bb = __uint_as_float(bm < 1.f ? 127u << 23 : (__float_as_uint(bm) & 0x7f800000u) + (1u << 23));
+        sb = wave_max(most[0]); rb = wave_max(most[1]); ub = wave_max(most[2]) * bb; eb = wave_max(most[3]) * bb;
+        ob = wave_max(most[4]);
+        si = inverse(sb); ri = inverse(rb); ui = inverse(ub); ei = inverse(eb); oi = inverse(ob);
+        if (hh + 1 < d.hn) load_factors(hh + 1);
+      }
       f32x4 vs[CT][IB], sc[MINE];
 #pragma unroll
       for (int c = 0; c < CT; ++c)
@@ -1564,7 +1600,7 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
         const int v0 = v * kSlab;
         char* const tdo = slabs + v % NBUF * SLAB;
         char* const tu = tdo + SB;
-        char* const te = tu + PP * SB;
+        char* const te = tu + SB;
         if (NBUF == 1 && v > 0) __syncthreads();  // the slab before is done with
         // ---- dO, b r and b e of 64 columns, as parts; dv and the sums of db on the way
         const Rsrc rdv = make_rsrc(d.dv + row0 * vts + static_cast<int64_t>(h) * p.cols * ES, row_bytes(p.L - t0, C, vts));
@@ -1588,15 +1624,17 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
 #pragma unroll
             for (int e = 0; e < E; ++e) BufOf<IO>::type::template st<1>(rdv, col + e < p.cols ? off + e * ES : kOOB, y + e);
           }
-          uint4 w[PP];
           const int to = 16 * (NS * r + (c ^ swz<IO, NS>(r)));
-          *reinterpret_cast<uint4*>(tdo + to) = go[i];
-          split<IO, PP>(x, w);
-#pragma unroll
-          for (int q = 0; q < PP; ++q) *reinterpret_cast<uint4*>(tu + q * SB + to) = w[q];
-          split<IO, PP>(y, w);
-#pragma unroll
-          for (int q = 0; q < PP; ++q) *reinterpret_cast<uint4*>(te + q * SB + to) = w[q];
+          if constexpr (HALF) {
+            *reinterpret_cast<uint4*>(tu + to) = Halves::one(x, ui);
+            *reinterpret_cast<uint4*>(te + to) = Halves::one(y, ei);
+            unpack<IO>(go[i], x);
+            *reinterpret_cast<uint4*>(tdo + to) = Halves::one(x, oi);
+          } else {
+            *reinterpret_cast<uint4*>(tdo + to) = go[i];
+            *reinterpret_cast<float4*>(tu + to) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(te + to) = make_float4(y[0], y[1], y[2], y[3]);
+          }
         }
         __syncthreads();
         if (v + 1 < nslab) load_slab(hh, v0 + kSlab);
@@ -1604,39 +1642,36 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
         const int fb = opaque(lane_base<IO, NS>(li, g));
 #pragma unroll
         for (int s = 0; s < SS; ++s) {
-          uint4 fs[CT][PP], fr[CT][PP];
+          uint4 fs[CT], fr[CT];
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
+            fs[c] = s0[s & 1][c];
+            fr[c] = r1[s & 1][c];
+            if constexpr (HALF) {
+              const _Float16 x = static_cast<_Float16>(s0_by[s & 1] * si), y = static_cast<_Float16>(r1_by[s & 1] * ri);
+              fs[c] = __builtin_bit_cast(uint4, __builtin_bit_cast(half8, fs[c]) * x);
+              fr[c] = __builtin_bit_cast(uint4, __builtin_bit_cast(half8, fr[c]) * y);
+            }
             float x[E], y[E];
-            widen<IO>(s0[s & 1][c], s0_by[s & 1], x);
-            widen<IO>(r1[s & 1][c], r1_by[s & 1], y);
+            widen<IO>(fs[c], 1.f, x);
+            widen<IO>(fr[c], 1.f, y);
 #pragma unroll
             for (int e = 0; e < E; ++e) dot_rs = __builtin_fmaf(x[e], y[e], dot_rs);
-            split<IO, PP>(x, fs[c]);
-            split<IO, PP>(y, fr[c]);
           }
           load_states(hh, v * SS + s + 2, s & 1);
+          auto add = [](const uint4& a, const uint4& b, f32x4 acc) {
+            if constexpr (HALF) return Halves::mma(a, b, acc);
+            else return mma<IO>(a, b, acc);
+          };
 #pragma unroll
           for (int ib = 0; ib < IB; ++ib) {
             __builtin_amdgcn_sched_barrier(0);
-            uint4 fo = frag_row<NS>(tdo, fb, ib, s), fu[PP], fe[PP];
-#pragma unroll
-            for (int q = 0; q < PP; ++q) {
-              fu[q] = frag_row<NS>(tu + q * SB, fb, ib, s);
-              fe[q] = frag_row<NS>(te + q * SB, fb, ib, s);
-            }
+            const uint4 fo = frag_row<NS>(tdo, fb, ib, s), fu = frag_row<NS>(tu, fb, ib, s), fe = frag_row<NS>(te, fb, ib, s);
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
-#pragma unroll
-              for (int q = 0; q < PP; ++q) {
-                dq[c][ib] = mma<IO>(fs[c][q], fo, dq[c][ib]);
-                ur[c][ib] = mma<IO>(fr[c][q], fu[0], ur[c][ib]);
-                vs[c][ib] = mma<IO>(fs[c][q], fe[0], vs[c][ib]);
-              }
-              if constexpr (PP == 2) {
-                ur[c][ib] = mma<IO>(fr[c][0], fu[1], ur[c][ib]);
-                vs[c][ib] = mma<IO>(fs[c][0], fe[1], vs[c][ib]);
-              }
+              dq[c][ib] = add(fs[c], fo, dq[c][ib]);
+              ur[c][ib] = add(fr[c], fu, ur[c][ib]);
+              vs[c][ib] = add(fs[c], fe, vs[c][ib]);
             }
           }
           // tiles of dP, then of dN, dealt to the wavefronts: lane holds j = 4 g + v of i = li
@@ -1647,13 +1682,7 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
             if (job >= 2 * TILES) continue;
             int ib, jb;
             score_tile<IB>(job < TILES ? job : job - TILES, ib, jb);
-            const uint4 fx = frag_row<NS>(job < TILES ? tdo : te, fb, ib, s);
-            const uint4 fu = frag_row<NS>(tu, fb, jb, s);
-            sc[m] = mma<IO>(fu, fx, sc[m]);
-            if constexpr (PP == 2) {
-              sc[m] = mma<IO>(frag_row<NS>(tu + SB, fb, jb, s), fx, sc[m]);
-              if (job >= TILES) sc[m] = mma<IO>(fu, frag_row<NS>(te + SB, fb, ib, s), sc[m]);
-            }
+            sc[m] = add(frag_row<NS>(tu, fb, jb, s), frag_row<NS>(job < TILES ? tdo : te, fb, ib, s), sc[m]);
           }
         }
       }
@@ -1667,13 +1696,13 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
         int ib, jb;
         score_tile<IB>(job < TILES ? job : job - TILES, ib, jb);
         const int me = opaque(lane), g = me >> 4, i = 16 * ib + (me & 15), j0 = 16 * jb + 4 * g;
-        const float by = job < TILES ? p.scale : -1.f;
+        const float by = (job < TILES ? p.scale * ob : -eb) * ub;
         float w[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float dd = __builtin_amdgcn_exp2f((ghi[i] - ghi[j0 + v]) + (glo[i] - glo[j0 + v]));
           w[v] = j0 + v < i ? times(by * dd, sc[m][v]) : 0.f;
-          if (job < TILES && j0 + v == i) own[i] = p.scale * sc[m][v];
+          if (job < TILES && j0 + v == i) own[i] = by * sc[m][v];
         }
         char* const to = job < TILES ? tp : tn;
         if constexpr (ES == 2) {
@@ -1689,7 +1718,7 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
       // <R_C, S_0> of the wavefront
 #pragma unroll
       for (int x = 1; x < 64; x *= 2) dot_rs += __shfl_xor(dot_rs, x);
-      if (lane == 0) rs[wave] = dot_rs;
+      if (lane == 0) rs[wave] = dot_rs * sb * rb;
       // db: the NS lanes of a row
       if (d.db != nullptr) {
 #pragma unroll
@@ -1716,9 +1745,9 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-          scale(dq[c][ib], p.scale * fe);
-          scale(vs[c][ib], -fe);
-          scale(ur[c][ib], fw);
+          scale(dq[c][ib], p.scale * fe * (sb * ob));
+          scale(vs[c][ib], -fe * (sb * eb));
+          scale(ur[c][ib], fw * (rb * ub));
           float kv[4];
           values(ty, c, ib, kv);
 #pragma unroll
