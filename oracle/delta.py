@@ -129,7 +129,7 @@ def delta_scan_errors(q, k, v, do=None, g=None, beta=None, h0=None, lengths=None
     S0, E0 = a * Sn[:, :L], a * ES[:, :L]
     out["dv"] = bt * (Ee + kept * en)
     out["dbeta"] = Ee * rn + en * Er + (both + 2 * kept) * en * rn
-    both = both + 2 * kept  # two of them in a product
+    both = both + 4 * kept  # two of them in a product, r and e once more after their product with beta
     eq = scale * don * (ES[:, 1:] + both * (Sn[:, 1:] + kn * bt * rn))
     ek = (bt * (ER[:, :L] * rn + Rn * Er + both * Rn * rn) + bt * (E0 * en + S0 * Ee + both * S0 * en))
     heads = lambda x: x.reshape(b, L, h // rep, rep).sum(3)

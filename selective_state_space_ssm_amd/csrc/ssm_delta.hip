@@ -276,10 +276,11 @@ int64_t square_bytes(const DeltaArgs& a, const Plan& pl, bool bf16) {
   return a.batch * a.H * pl.nch * (bf16 ? deltak::Square<BF16>::BYTES : deltak::Square<F32>::BYTES);
 }
 
-// Heads whose parts of dq and dk a workgroup adds: all that share a key head, unless that leaves CUs idle.
+// Heads whose parts of dq and dk a workgroup adds: all that share a key head, unless that leaves CUs idle, and one past
+// 128 keys, where the sums do not fit the registers.
 int64_t grad_heads(const DeltaArgs& a, const Plan& pl) {
   const int64_t rep = a.H / a.Hk;
-  int64_t n = a.dk > 128 ? 1 : rep;  // kGradOneHead
+  int64_t n = a.dk > 128 ? 1 : rep;
   while (n > 1 && a.batch * (a.H / n) * pl.nch < 2 * kDeltaCUs) {
     --n;
     while (rep % n != 0) --n;

@@ -1387,8 +1387,6 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_both_kernel(const Delt
 
 // ---------------------------------------------------------------- the gradients, all chunks at once
 
-// From this width on the sums over heads do not fit the registers: a workgroup then has one head.
-constexpr int kGradOneHead = 256;
 
 struct DeltaGradDev {
   DeltaDev f;                  // q, k, rates, sizes; v is dO; states S_0, res r
@@ -1406,15 +1404,13 @@ struct DeltaGradDev {
   int parts;
 };
 
-// Slabs in LDS: two where they fit, so that the next one is written while one is worked on.
-template <int ROWS>
-constexpr int grad_buffers() { return ROWS == 128 ? 2 : 1; }
+// The scores' gradients take the place of the slab once it is done with.
 template <typename IO, int ROWS, int NW>
 constexpr size_t grad_lds_bytes() {
   using K = HeadCfg<IO>;
   constexpr size_t slab = size_t(K::C) * kSlab * K::ES * 3;
   constexpr size_t sc = size_t(2) * K::C * K::C * K::ES * DeltaCfg<IO>::PAIR;
-  return 2 * size_t(K::C) * ROWS * K::ES + grad_buffers<ROWS>() * slab + sc + (size_t(2) * NW + kRates + 1) * K::C * 4 + NW * 4;
+  return 2 * size_t(K::C) * ROWS * K::ES + (slab > sc ? slab : sc) + (size_t(2) * NW + kRates + 1) * K::C * 4 + NW * 4;
 }
 
 // Running sum from the last lane as a pair of floats (scan_pair's, the other way round)
@@ -1444,18 +1440,26 @@ __device__ __forceinline__ void scan_back(float& hi, float& lo) {
 // with dk^+ the key's gradient as what is written (first three terms of dk above), dk^- as what is taken out (the
 // last two), each without a token's own pair scale (q . k)(do . u), which is in both and cancels.  Where the state
 // starts anew (a decay of -inf) dg is zero and the sum of the tokens before begins there.
-template <typename IO, int ROWS, int NW, bool VEC>
-__global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const DeltaGradDev d) {
+//
+// MULTI adds up the d.hn heads of a key head in the workgroup: 4 x 2048 tokens, 32 heads of 128 x 128 on 8 key heads,
+// bfloat16, 558 us for the whole backward, 641 with key heads of their own (more loads and stores of keys' gradients).
+// A workgroup is on its CU alone in bfloat16 (its registers), two or three in float32 with one head, where that many fit
+// with few spills (4 x 2048 tokens, 32 heads of 64 x 64: the backward 490 us, with the registers of two 516; bfloat16
+// 304 with two, 422 with three).
+template <typename IO, int ROWS, int NW, bool MULTI>
+constexpr int grad_waves() { return HeadCfg<IO>::ES == 4 && !MULTI ? (ROWS == 128 ? 4 : ROWS == 64 ? 3 : 2) : 2; }
+
+template <typename IO, int ROWS, int NW, bool MULTI, bool VEC>
+__global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())) ssm_delta_grad_kernel(const DeltaGradDev d) {
   using K = HeadCfg<IO>;
   const DeltaDev& p = d.f;
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW;
   constexpr int NK = ROWS * ES / 16, NS = kSlab * ES / 16, NP = C * ES / 16;
-  constexpr int IB = C / 16, JS = C / KS, SS = kSlab / KS, CT = ROWS / 16 / NW, NBUF = grad_buffers<ROWS>();
-  constexpr int PP = DeltaCfg<IO>::PAIR, SB = C * kSlab * ES, PB = C * C * ES, SLAB = 3 * SB;
+  constexpr int IB = C / 16, JS = C / KS, SS = kSlab / KS, CT = ROWS / 16 / NW;
+  constexpr int PP = DeltaCfg<IO>::PAIR, SB = C * kSlab * ES, PB = C * C * ES, GAP = KS == 32 ? IB / 2 : 0;  // tiles above the diagonal that a product step covers
   constexpr bool HALF = ES == 2;
   constexpr int TILES = IB * (IB + 1) / 2, MINE = (2 * TILES + NW - 1) / NW;
   constexpr int TASKS = C * NS / T;  // staging tasks a thread, rows tid / NS + i T / NS
-  constexpr bool MULTI = ROWS < kGradOneHead;
   static_assert(C * NS % T == 0 && CT >= 1 && SS % 2 == 0, "shares are even");
   using TK = Tile<IO, NK, T>;
   using TR = Flat<kRates * C * 4, T>;
@@ -1463,10 +1467,12 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
   extern __shared__ __attribute__((aligned(16))) char lds[];
   char* const tx = lds;
   char* const ty = tx + C * ROWS * ES;
-  char* const slabs = ty + C * ROWS * ES;  // each dO, b r, b e of kSlab columns
-  char* const tp = slabs + NBUF * SLAB;    // dP, then dN
+  char* const tdo = ty + C * ROWS * ES;  // dO, b r, b e of kSlab columns
+  char* const tu = tdo + SB;
+  char* const te = tu + SB;
+  char* const tp = tdo;                  // in their place dP, then dN
   char* const tn = tp + PP * PB;
-  float* const rt = reinterpret_cast<float*>(tn + PP * PB);  // [kRates][C]
+  float* const rt = reinterpret_cast<float*>(tdo + (3 * SB > 2 * PP * PB ? 3 * SB : 2 * PP * PB));  // [kRates][C]
   const float* const ghi = rt + kGHi * C;
   const float* const glo = rt + kGLo * C;
   const float* const ek = rt + kEk * C;
@@ -1567,8 +1573,6 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
       TK::store(tx, tid, rx);
       TK::store(ty, tid, ry);
     }
-    // the score tiles above the diagonal that a product step covers are never written again
-    for (int i = tid; i < 2 * PP * PB / 16; i += T) reinterpret_cast<uint4*>(tp)[i] = make_uint4(0, 0, 0, 0);
     for (int hh = 0; hh < d.hn; ++hh) {
       const int h = hg * d.hn + hh;
       __syncthreads();  // the head before is done with the rates
@@ -1598,10 +1602,7 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
 
       for (int v = 0; v < nslab; ++v) {
         const int v0 = v * kSlab;
-        char* const tdo = slabs + v % NBUF * SLAB;
-        char* const tu = tdo + SB;
-        char* const te = tu + SB;
-        if (NBUF == 1 && v > 0) __syncthreads();  // the slab before is done with
+        if (v > 0) __syncthreads();  // the slab before is done with
         // ---- dO, b r and b e of 64 columns, as parts; dv and the sums of db on the way
         const Rsrc rdv = make_rsrc(d.dv + row0 * vts + static_cast<int64_t>(h) * p.cols * ES, row_bytes(p.L - t0, C, vts));
 #pragma unroll
@@ -1687,7 +1688,13 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_grad_kernel(const Delt
         }
       }
 
-      // ---- the scores' gradients to LDS, below the diagonal
+      // ---- the scores' gradients to LDS, below the diagonal, and zeros in the tiles above it that a product step covers
+      __syncthreads();
+      for (int i = tid; i < 2 * PP * GAP * 16 * (16 / E); i += T) {
+        const int part = i / (GAP * 16 * (16 / E)), at = i % (GAP * 16 * (16 / E)), r = at / (16 / E), c = at % (16 / E);
+        const int row = (r / 16) * 32 + r % 16, col = ((r / 16) * 32 + 16) / E + c;
+        *reinterpret_cast<uint4*>(tp + part * PB + 16 * (NP * row + (col ^ swz<IO, NP>(row)))) = make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
       for (int m = 0; m < MINE; ++m) {
         __builtin_amdgcn_sched_barrier(0);
@@ -1974,16 +1981,23 @@ hipError_t launch_both_t(const DeltaDev& p, const DeltaDev& r, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename IO, int ROWS, bool VEC>
+template <typename IO, int ROWS, int NW, bool MULTI, bool VEC>
 hipError_t launch_grad_t(const DeltaGradDev& d, hipStream_t st) {
-  constexpr int NW = ROWS == 64 ? 4 : 8;
   static std::atomic<uint64_t> allowed{0};
   constexpr size_t smem = grad_lds_bytes<IO, ROWS, NW>();
-  auto kern = ssm_delta_grad_kernel<IO, ROWS, NW, VEC>;
+  auto kern = ssm_delta_grad_kernel<IO, ROWS, NW, MULTI, VEC>;
   if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
   const int64_t wgs = static_cast<int64_t>(d.f.batch) * (d.f.H / d.hn) * d.f.nch;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(wgs)), dim3(64 * NW), smem, st, d);
   return hipGetLastError();
+}
+
+template <typename IO, bool VEC>
+hipError_t launch_grad_v(const DeltaGradDev& d, hipStream_t st) {
+  if (d.hn > 1) return d.f.rows <= 64 ? launch_grad_t<IO, 64, 4, true, VEC>(d, st) : launch_grad_t<IO, 128, 8, true, VEC>(d, st);
+  return d.f.rows <= 64    ? launch_grad_t<IO, 64, 4, false, VEC>(d, st)
+         : d.f.rows <= 128 ? launch_grad_t<IO, 128, 8, false, VEC>(d, st)
+                           : launch_grad_t<IO, 256, 8, false, VEC>(d, st);
 }
 
 // Four wavefronts of 16 columns: with eight for 128 the prompts below take as long and the training's 256 walks of 4 x
@@ -2018,9 +2032,7 @@ hipError_t launch_pass_io(const DeltaDev& p, const DeltaDev& r, int pass, bool w
 
 template <typename IO>
 hipError_t launch_grad_io(const DeltaGradDev& d, bool vec, hipStream_t st) {
-  if (d.f.rows <= 64) return vec ? launch_grad_t<IO, 64, true>(d, st) : launch_grad_t<IO, 64, false>(d, st);
-  if (d.f.rows <= 128) return vec ? launch_grad_t<IO, 128, true>(d, st) : launch_grad_t<IO, 128, false>(d, st);
-  return vec ? launch_grad_t<IO, 256, true>(d, st) : launch_grad_t<IO, 256, false>(d, st);
+  return vec ? launch_grad_v<IO, true>(d, st) : launch_grad_v<IO, false>(d, st);
 }
 
 }  // namespace deltak
