@@ -504,8 +504,9 @@ int ssm_head_step(const void *q, const void *k, const void *v, const void *g, co
  * decay is expanded to g).
  * Rounding: sums, decays, r and the state are float32.  With SSM_BF16 the state
  * and what is added to it enter products as three parts of bfloat16 (all of a
- * float32), the scores and the corrections among a chunk's tokens as two (off by
- * 2^-17 of themselves).
+ * float32), the corrections among a chunk's tokens as two of float16 over a power
+ * of two for each column (off by 2^-22 of themselves, or 2^-39 of the chunk's
+ * largest in that column), and what ends in o as two of bfloat16 (2^-17).
  * Values that are not finite reach every later result of their head in their
  * batch row, and those of their chunk (64 tokens from a multiple of 64, float32:
  * 32) before them; a decay of -inf does not hold them back within a chunk.
@@ -528,6 +529,10 @@ int ssm_delta_scan_fwd(const void *q, int64_t q_batch, int64_t q_token, const vo
  *           state and its gradient at every chunk.
  * dg of a chunk's tokens is a sum over the chunk from its end.  Every sum is taken
  * in a fixed order: repeated calls give identical bits.
+ * Rounding: R, and with it dh0, as the state.  With SSM_BF16 dq, dk, dv, dg and
+ * dbeta, which are rounded to 2^-8, take the states, r and e as float16 (2^-11)
+ * over a power of two that 16 columns share.  With values that are not finite no
+ * gradient of their head in their batch row is defined.
  * Other arguments and errors as ssm_head_scan_bwd and ssm_delta_scan_fwd.
  */
 int ssm_delta_scan_bwd(const void *q, int64_t q_batch, int64_t q_token, const void *k, int64_t k_batch, int64_t k_token,

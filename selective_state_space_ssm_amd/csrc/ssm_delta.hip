@@ -44,10 +44,14 @@ constexpr int64_t kDeltaMaxSegments = 64;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
-// Columns of a workgroup's tile: 128 past 128 keys, where there are more than 64 and every operand row is whole vectors,
-// else 64.
-bool wide_for(int64_t rows, int64_t cols, bool vec) { return rows > 128 && cols > 64 && vec; }
-int64_t tiles_for(int64_t rows, int64_t cols, bool vec) { return cdiv(cols, wide_for(rows, cols, vec) ? 128 : 64); }
+// Columns of a workgroup's tile: 128 in bfloat16 past 128 keys, where there are more than 64 and every operand row is
+// whole vectors (LDS then holds one workgroup a CU either way; 4 x 2048 tokens, 32 heads of 192 x 128, forward and
+// backward 376 and 1389 us, with tiles of 64 455 and 1897; 2 x 2048, 16 heads of 256 x 256 250 and 887, 324 and 953),
+// else 64 (float32, the latter 544 and 1249, with 128 596 and 1811; the former 629 and 2373, 993 and 2223).
+bool wide_for(int64_t rows, int64_t cols, bool vec, bool bf16) { return bf16 && rows > 128 && cols > 64 && vec; }
+int64_t tiles_for(int64_t rows, int64_t cols, bool vec, bool bf16) {
+  return cdiv(cols, wide_for(rows, cols, vec, bf16) ? 128 : 64);
+}
 
 // States carried over the segments, in order, 16 columns a workgroup: state <- A carried + own, or A^T carried + own
 // from the end.  Float32 matrix instructions, 16 rows a wavefront; the carried columns are in LDS.  A segment's rows of
@@ -243,7 +247,7 @@ Plan plan_of(const DeltaArgs& a, bool bf16) {
   // segments' own walk 0.8, with the transitions' tiles beside the state's in all but the first, a step of the carry
   // 0.8, two more launches 3.  16 heads of 128 x 128 over 32768 tokens: 582 us in 16 segments, 605 in 8, whole some
   // 2.2 ms; 128 heads of 128 x 128 over 2048 tokens are better off whole.  A tenth has to be gained.
-  const int64_t tv = tiles_for(a.dk, a.dv, true), tt = cdiv(p.rp, wide_for(a.dk, a.dv, true) ? 128 : 64), bh = a.batch * a.H;
+  const int64_t tv = tiles_for(a.dk, a.dv, true, bf16), tt = cdiv(p.rp, wide_for(a.dk, a.dv, true, bf16) ? 128 : 64), bh = a.batch * a.H;
   const double pair = bf16 ? 1.75 : 2.;
   auto rate = [pair](double wgs) { return wgs <= kDeltaCUs ? 1. : std::max(pair, wgs * pair / (2 * kDeltaCUs)); };
   double best = 0.9 * p.nch * rate(bh * tv);
@@ -276,8 +280,10 @@ int64_t square_bytes(const DeltaArgs& a, const Plan& pl, bool bf16) {
   return a.batch * a.H * pl.nch * (bf16 ? deltak::Square<BF16>::BYTES : deltak::Square<F32>::BYTES);
 }
 
-// Heads whose parts of dq and dk a workgroup adds: all that share a key head, unless that leaves CUs idle, and one past
-// 128 keys, where the sums do not fit the registers.
+// Heads whose parts of dq and dk a workgroup adds: all that share a key head, unless that leaves CUs idle (4 x 2048
+// tokens, 32 heads of 128 x 128 on 16 key heads, bfloat16: backward 583 us, with parts for every head 778; 2048 tokens,
+// 16 heads of 64 x 64 on one: 105 us, with all in a workgroup 262), and one past 128 keys, where the sums do not fit the
+// registers.
 int64_t grad_heads(const DeltaArgs& a, const Plan& pl) {
   const int64_t rep = a.H / a.Hk;
   int64_t n = a.dk > 128 ? 1 : rep;
@@ -349,14 +355,13 @@ DeltaDev dev_of(const DeltaArgs& a, const Plan& pl, const Space& w, char* work, 
   d.rows = static_cast<int>(a.dk); d.cols = static_cast<int>(a.dv);
   d.rp = static_cast<int>(pl.rp); d.cp = static_cast<int>(pl.cp);
   d.nch = static_cast<int>(pl.nch); d.cps = static_cast<int>(pl.cps); d.nseg = static_cast<int>(pl.nseg);
-  d.nvt = d.ntile = static_cast<int>(tiles_for(a.dk, a.dv, vec));
+  d.nvt = d.ntile = static_cast<int>(tiles_for(a.dk, a.dv, vec, bf16));
   d.scale = a.scale;
   return d;
 }
 
 hipError_t launch_pass(const DeltaDev& d, const DeltaDev& r, bool bf16, int pass, bool vec, hipStream_t st) {
-  const bool wide = wide_for(d.rows, d.cols, vec);
-  return bf16 ? launch_delta_bf16(d, r, pass, wide, vec, st) : launch_delta_f32(d, r, pass, wide, vec, st);
+  return bf16 ? launch_delta_bf16(d, r, pass, wide_for(d.rows, d.cols, vec, true), vec, st) : launch_delta_f32(d, r, pass, vec, st);
 }
 
 hipError_t launch_carry(const DeltaDev& d, bool rev, hipStream_t st) {
@@ -370,8 +375,8 @@ hipError_t launch_carry(const DeltaDev& d, bool rev, hipStream_t st) {
 }
 
 // with the tiles of the transitions
-DeltaDev with_transitions(DeltaDev d, bool vec) {
-  d.ntile = d.nvt + static_cast<int>(cdiv(d.rp, wide_for(d.rows, d.cols, vec) ? 128 : 64));
+DeltaDev with_transitions(DeltaDev d, bool vec, bool bf16) {
+  d.ntile = d.nvt + static_cast<int>(cdiv(d.rp, wide_for(d.rows, d.cols, vec, bf16) ? 128 : 64));
   return d;
 }
 
@@ -391,11 +396,11 @@ hipError_t launch_delta_fwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   const Plan pl = plan_of(a, bf16);
   const bool vec = all_vec(a, bf16);
   const DeltaDev d = dev_of(a, pl, space_of(a, pl, bf16, false), work, bf16, vec);
-  if (pl.nch == 1 && d.ntile == 1 && !wide_for(d.rows, d.cols, vec))  // that kernel's tile has 64 columns
+  if (pl.nch == 1 && d.ntile == 1 && !wide_for(d.rows, d.cols, vec, bf16))  // that kernel's tile has 64 columns
     return launch_pass(d, d, bf16, deltak::kPassOne, vec, st);
   hipError_t e = launch_pass(d, d, bf16, deltak::kPassPrep, vec, st);
   if (e == hipSuccess && pl.nseg > 1) {
-    e = launch_pass(with_transitions(d, vec), d, bf16, deltak::kPassSeg, vec, st);
+    e = launch_pass(with_transitions(d, vec, bf16), d, bf16, deltak::kPassSeg, vec, st);
     if (e == hipSuccess) e = launch_carry(d, false, st);
   }
   return e == hipSuccess ? launch_pass(d, d, bf16, deltak::kPassOut, vec, st) : e;
@@ -423,7 +428,7 @@ hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   r.in_by = reinterpret_cast<float*>(work + w.do_by);
   hipError_t e = launch_pass(d, d, bf16, deltak::kPassPrep, vec, st);
   if (e == hipSuccess && pl.nseg > 1) {
-    e = launch_pass(with_transitions(d, vec), r, bf16, deltak::kPassBothSeg, vec, st);
+    e = launch_pass(with_transitions(d, vec, bf16), r, bf16, deltak::kPassBothSeg, vec, st);
     if (e == hipSuccess) e = launch_carry(d, false, st);
     if (e == hipSuccess) e = launch_carry(r, true, st);
   }

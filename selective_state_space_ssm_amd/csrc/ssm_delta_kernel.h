@@ -419,6 +419,10 @@ __device__ __forceinline__ void store_parts(const float* n, char* dst, int tid, 
 // in float32 matrix instructions, the tiles M_JK staying in registers.
 // (Substitution, not powers of N b: keys alike make those grow past float32
 // where the inverse does not.)
+// A chunk needs nothing of the others, and a workgroup's steps wait for each
+// other: what counts is how many share a CU, hence the scores in the place of the
+// tiles.  It reads k and q and writes five eighths of M and P: 8 x 2048 ragged
+// tokens, 32 heads of 128, bfloat16, 76 us, 4 x 2048 tokens 45.
 template <typename IO, int ROWS, bool VEC>
 __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char* lds) {
   using K = HeadCfg<IO>;
@@ -701,6 +705,12 @@ __device__ __forceinline__ void widen(const uint4& r, float by, float* v) {
   }
 }
 
+// A chunk at a time, a workgroup for a (batch row, head, segment) and 16 NW columns of d_value: its chunks follow each
+// other, and every wavefront's products too (S into x, x into r, r into S), so that a chunk takes what its longest chain
+// takes.  The next chunk's operands are under way meanwhile, those of a product are read and split under the product
+// before.  Two workgroups share a CU (80 KB of LDS, 256 registers): alone a chunk takes 4.2 us, two 7.3 (128 x 128,
+// bfloat16), of which the vector unit is busy for 39 %, the matrix unit for 30 % and 18 % are waits.  8 x 2048 ragged
+// tokens, 32 heads of 128 x 128, bfloat16: 179 us.
 template <typename IO, int ROWS, int NW, int MODE, bool VEC>
 __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char* lds) {
   using K = HeadCfg<IO>;
@@ -1377,7 +1387,9 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
 }
 
 // The backward's two walks need nothing of each other: the first half of the workgroups walks forwards, the second half
-// backwards, so that the stores of one lie under the products of the other.  SEG: the segments' own ends.
+// backwards, so that the stores of one lie under the products of the other (forward and backward of 4 x 2048 tokens, 32
+// heads of 128 x 128, bfloat16, 903 us for 983 with a launch each; of 4 x 1999 ragged tokens, 24 heads of 64, float32, 571
+// for 706).  Now 283 and 214 of it.  SEG: the segments' own ends.
 template <typename IO, int ROWS, int NW, bool SEG, bool VEC>
 __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_both_kernel(const DeltaDev p, const DeltaDev r, uint32_t first) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -1386,7 +1398,6 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_both_kernel(const Delt
 }
 
 // ---------------------------------------------------------------- the gradients, all chunks at once
-
 
 struct DeltaGradDev {
   DeltaDev f;                  // q, k, rates, sizes; v is dO; states S_0, res r
@@ -1441,6 +1452,10 @@ __device__ __forceinline__ void scan_back(float& hi, float& lo) {
 // last two), each without a token's own pair scale (q . k)(do . u), which is in both and cancels.  Where the state
 // starts anew (a decay of -inf) dg is zero and the sum of the tokens before begins there.
 //
+// In bfloat16 the states, r and e are operands as they are kept, float16 over powers of two, brought to the largest of a
+// chunk's (the products of several columns add up), and dO beside them: 277 us, in two bfloat16 parts each 321 (4 x 2048
+// tokens, 32 heads of 128 x 128 on 16 key heads; 2.4 TB/s).  Bound by its loads: 32 KB of states a step, two steps ahead
+// are all that the registers hold.
 // MULTI adds up the d.hn heads of a key head in the workgroup: 4 x 2048 tokens, 32 heads of 128 x 128 on 8 key heads,
 // bfloat16, 558 us for the whole backward, 641 with key heads of their own (more loads and stores of keys' gradients).
 // A workgroup is on its CU alone in bfloat16 (its registers), two or three in float32 with one head, where that many fit
@@ -2000,9 +2015,9 @@ hipError_t launch_grad_v(const DeltaGradDev& d, hipStream_t st) {
                            : launch_grad_t<IO, 256, 8, false, VEC>(d, st);
 }
 
-// Four wavefronts of 16 columns: with eight for 128 the prompts below take as long and the training's 256 walks of 4 x
-// 2048 tokens, 32 heads of 128 x 128, half as long again.  `wide` is eight: past 128 keys LDS holds one workgroup a CU
-// either way.
+// Four wavefronts of 16 columns: with eight for 128 the prompts of 8 x 2048 ragged tokens take as long and the training's
+// 256 walks of 4 x 2048 tokens, 32 heads of 128 x 128, half as long again.  `wide` is eight, see
+// wide_for.
 enum { kPassPrep, kPassOne, kPassOut, kPassSeg, kPassBoth, kPassBothSeg };
 
 template <typename IO, int ROWS, int NW, bool VEC>
@@ -2017,7 +2032,7 @@ template <typename IO, int ROWS, bool VEC>
 hipError_t launch_pass_r(const DeltaDev& p, const DeltaDev& r, int pass, bool wide, hipStream_t st) {
   if (pass == kPassPrep) return launch_prep_t<IO, ROWS, VEC>(p, st);
   if (pass == kPassOne) return launch_one_t<IO, ROWS, VEC>(p, st);
-  if constexpr (VEC && ROWS == 256)
+  if constexpr (VEC && ROWS == 256 && HeadCfg<IO>::ES == 2)
     if (wide) return launch_pass_n<IO, ROWS, 8, VEC>(p, r, pass, st);
   return launch_pass_n<IO, ROWS, 4, VEC>(p, r, pass, st);
 }
@@ -2039,7 +2054,7 @@ hipError_t launch_grad_io(const DeltaGradDev& d, bool vec, hipStream_t st) {
 
 // One pass (r: the walk backwards, where the pass has one); ROWS is d_key rounded up to 64, 128 or 256.
 hipError_t launch_delta_bf16(const deltak::DeltaDev& p, const deltak::DeltaDev& r, int pass, bool wide, bool vec, hipStream_t st);
-hipError_t launch_delta_f32(const deltak::DeltaDev& p, const deltak::DeltaDev& r, int pass, bool wide, bool vec, hipStream_t st);
+hipError_t launch_delta_f32(const deltak::DeltaDev& p, const deltak::DeltaDev& r, int pass, bool vec, hipStream_t st);
 hipError_t launch_delta_grad_bf16(const deltak::DeltaGradDev& d, bool vec, hipStream_t st);
 hipError_t launch_delta_grad_f32(const deltak::DeltaGradDev& d, bool vec, hipStream_t st);
 
