@@ -296,7 +296,7 @@ int64_t grad_heads(const DeltaArgs& a, const Plan& pl) {
 
 // Where the workspace's parts are, in bytes from its start.
 struct Space {
-  int64_t m, s, rates, ss, rs, trans, s0, r1, r, e, s0_by, r1_by, r_by, e_by, do_by, pq, pk, total;
+  int64_t m, s, rates, ss, rs, trans, kept, pq, pk, total;
 };
 Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
   Space w{};
@@ -316,12 +316,8 @@ Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
     if (backward) w.rs = take(4 * bh * pl.nseg * pl.rp * pl.cp);
   }
   if (backward) {
-    const int64_t kept = bf16 ? 2 : 4;
-    w.s0 = take(kept * bh * pl.nch * pl.rp * pl.cp);
-    w.r1 = take(kept * bh * pl.nch * pl.rp * pl.cp);
-    w.r = take(kept * bh * pl.nch * pl.C * pl.cp);
-    w.e = take(kept * bh * pl.nch * pl.C * pl.cp);
-    for (int64_t* by : {&w.s0_by, &w.r1_by, &w.r_by, &w.e_by, &w.do_by}) *by = take(bf16 ? 4 * bh * pl.nch * pl.cp / 16 : 0);
+    const int rp = static_cast<int>(pl.rp), cp = static_cast<int>(pl.cp);
+    w.kept = take(bh * pl.nch * (bf16 ? deltak::Kept<BF16>(rp, cp).bytes() : deltak::Kept<F32>(rp, cp).bytes()));
     const int64_t hn = grad_heads(a, pl);
     if (hn < a.H / a.Hk) {
       w.pq = take(4 * bh / hn * a.L * a.dk);
@@ -347,10 +343,7 @@ DeltaDev dev_of(const DeltaArgs& a, const Plan& pl, const Space& w, char* work, 
   d.rates = reinterpret_cast<float*>(work + w.rates);
   d.seg_state = reinterpret_cast<float*>(work + w.ss);
   d.seg_trans = reinterpret_cast<float*>(work + w.trans);
-  d.states = work + w.s0;
-  d.res = work + w.r;
-  d.states_by = reinterpret_cast<float*>(work + w.s0_by);
-  d.res_by = reinterpret_cast<float*>(work + w.r_by);
+  d.kept = work + w.kept;
   d.batch = static_cast<int>(a.batch); d.H = static_cast<int>(a.H); d.L = static_cast<int>(a.L);
   d.rows = static_cast<int>(a.dk); d.cols = static_cast<int>(a.dv);
   d.rp = static_cast<int>(pl.rp); d.cp = static_cast<int>(pl.cp);
@@ -421,11 +414,6 @@ hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   r.h0 = a.dlast;
   r.last = a.dh0;
   r.seg_state = reinterpret_cast<float*>(work + w.rs);
-  r.states = work + w.r1;
-  r.res = work + w.e;
-  r.states_by = reinterpret_cast<float*>(work + w.r1_by);
-  r.res_by = reinterpret_cast<float*>(work + w.e_by);
-  r.in_by = reinterpret_cast<float*>(work + w.do_by);
   hipError_t e = launch_pass(d, d, bf16, deltak::kPassPrep, vec, st);
   if (e == hipSuccess && pl.nseg > 1) {
     e = launch_pass(with_transitions(d, vec, bf16), r, bf16, deltak::kPassBothSeg, vec, st);
@@ -439,8 +427,6 @@ hipError_t launch_delta_bwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   DeltaGradDev gd{};
   gd.f = d;
   gd.f.v = r.v; gd.f.v_b = r.v_b; gd.f.v_t = r.v_t;
-  gd.r1 = r.states; gd.e = r.res;
-  gd.r1_by = r.states_by; gd.e_by = r.res_by; gd.do_by = r.in_by;
   gd.hn = static_cast<int>(hn);
   gd.parts = hn < rep;
   gd.dq = gd.parts ? work + w.pq : static_cast<char*>(a.dq);

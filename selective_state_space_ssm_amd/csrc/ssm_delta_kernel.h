@@ -71,11 +71,7 @@ struct DeltaDev {
   float* rates;                // [b][H][nch][kRates][C]
   float* seg_state;            // [b][H][nseg][rp][cp]
   float* seg_trans;            // [b][H][nseg][rp][rp]: what a segment makes of the state before it
-  char* states;                // [b][H][nch][rp][cp]: the state before (backwards: after) every chunk (see keep)
-  char* res;                   // [b][H][nch][C][cp]: r, backwards e, likewise
-  float* states_by;            // [b][H][nch][cp / 16]: what they are to be multiplied with (bfloat16 storage)
-  float* res_by;
-  float* in_by;                // backwards, of dO's columns
+  char* kept;                  // [b][H][nch] records of what the walks leave for the gradients (see Kept)
   int batch, H, L, rows, cols;
   int rp, cp;                  // rows and columns of states in the workspace: multiples of 16 and of kSlab
   int nch, cps, nseg;          // chunks, chunks per segment, segments
@@ -655,8 +651,22 @@ __device__ __forceinline__ void store_state(float* dst, int rows, int cols, int 
 template <typename IO>
 constexpr int kept_size() { return HeadCfg<IO>::ES; }
 
+// A chunk's record, one piece of memory so that one resource reaches all of it: S_0, R_C ([rp][cp] each), r, e ([C][cp])
+// and, in bfloat16, the factors of S_0, R_C, r, e and dO for every 16 columns.
+template <typename IO>
+struct Kept {
+  static constexpr int FACTORS = kept_size<IO>() == 2 ? 5 : 0;
+  uint32_t w, t, f;  // bytes of a state, of tokens' rows, of factors
+  __host__ __device__ __forceinline__ Kept(int rp, int cp)
+      : w(rp * cp * kept_size<IO>()), t(HeadCfg<IO>::C * cp * kept_size<IO>()), f(cp / 16 * 4) {}
+  __host__ __device__ __forceinline__ uint32_t state(int back) const { return back * w; }
+  __host__ __device__ __forceinline__ uint32_t rows(int back) const { return 2 * w + back * t; }
+  __host__ __device__ __forceinline__ uint32_t by(int i) const { return 2 * w + 2 * t + i * f; }
+  __host__ __device__ __forceinline__ uint32_t bytes() const { return (by(FACTORS) + 255) / 256 * 256; }  // whole cache lines
+};
+
 // A factor of the columns c .. c + 15 of a wavefront beside the chunk's others; nothing is written with rows = 0.
-__device__ __forceinline__ void keep_factor(float* by, int rows, int cp, int c, int g, float f) {
+__device__ __forceinline__ void keep_factor(char* by, int rows, int cp, int c, int g, float f) {
   const Rsrc r = make_rsrc(by, rows > 0 ? static_cast<uint32_t>(cp / 16 * 4) : 0u);
   __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), r, (c & 15) == 0 && g == 0 ? c / 16 * 4 : kOOB, 0, 0);
 }
@@ -666,7 +676,7 @@ __device__ __forceinline__ void keep_factor(float* by, int rows, int cp, int c, 
 // order, and the wait for the next chunk's loads can leave these in flight only if their number is known.  by: the
 // chunk's cp / 16 factors.
 template <typename IO, int N>
-__device__ __forceinline__ void keep(char* dst, float* by, int rows, int cp, int c, int g, const f32x4 (&X)[N]) {
+__device__ __forceinline__ void keep(char* dst, char* by, int rows, int cp, int c, int g, const f32x4 (&X)[N]) {
   constexpr int KB = kept_size<IO>();
   const Rsrc r = make_rsrc(dst, static_cast<uint32_t>(rows * cp * KB));
   const uint32_t off = c < cp ? c * KB : kOOB;
@@ -806,6 +816,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     }
   };
 
+  const Kept<IO> kept(p.rp, p.cp);
   const int cl = (len + C - 1) / C, ce = c1 < cl ? c1 : cl, nc = ce - c0;
   if (nc > 0) {
     load_chunk(c0);
@@ -816,12 +827,13 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     if constexpr (QUERY) {
       store_out(reinterpret_cast<const f32x4(&)[IB]>(none), 0, 0, li, g);
     } else if constexpr (MODE == kDeltaStates) {
-      keep<IO, RT>(p.states, p.states_by, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
-      keep<IO, IB>(p.res, p.res_by, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
+      keep<IO, RT>(p.kept, p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
+      keep<IO, IB>(p.kept, p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
     }
   }
   for (int kk = 0; kk < nc; ++kk) {
     const int pc = c0 + kk, t0 = pc * C;
+    char* const record = p.kept + (bh * p.nch + pc) * static_cast<int64_t>(kept.bytes());
     __syncthreads();  // the chunk before is done with the tiles
     {
       const int me = ROWS == 256 || !VEC ? opaque(tid) : tid;
@@ -840,7 +852,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     if (kk + 1 < nc) load_chunk(pc + 1);
 
     if constexpr (MODE == kDeltaStates)
-      keep<IO, RT>(p.states + (bh * p.nch + pc) * wsize * kept_size<IO>(), p.states_by + (bh * p.nch + pc) * (p.cp / 16), p.rp, p.cp, cw + li, g, S);
+      keep<IO, RT>(record + kept.state(0), record + kept.by(0), p.rp, p.cp, cw + li, g, S);
 
     // ---- what the state before the chunk gives: X = K S (rows are tokens, by state_row), O = Q S (transposed).  The
     // operands of step s + 1 are read and split under the matrix instructions of step s.
@@ -984,7 +996,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (MODE == kDeltaStates)
-      keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp * kept_size<IO>(), p.res_by + (bh * p.nch + pc) * (p.cp / 16), C, p.cp, cw + li, g, X);
+      keep<IO, IB>(record + kept.rows(0), record + kept.by(2), C, p.cp, cw + li, g, X);
 
     // ---- u = b r as an operand of o, e^{G_C - G} u as one of the state's update
     const int yb0 = state_col_base<IO, NK>(li, g);
@@ -1160,6 +1172,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     TK::template load<VEC>(xb, p.q_t, t0, len, p.rows, me, rx);
   };
 
+  const Kept<IO> kept(p.rp, p.cp);
   const int cl = (len + C - 1) / C, ce = c1 < cl ? c1 : cl, nc = ce - c0;
   if (nc > 0) {
     load_chunk(ce - 1);
@@ -1168,13 +1181,14 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
       // as many stores behind the first loads as the loop has behind its own (see keep)
       const f32x4 none[RT > IB ? RT : IB] = {};
       const int li = tid & 15, g = (tid & 63) >> 4;
-      keep<IO, RT>(p.states, p.states_by, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
-      if constexpr (PP == 2) keep_factor(p.in_by, 0, p.cp, cw + li, g, 1.f);
-      keep<IO, IB>(p.res, p.res_by, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
+      keep<IO, RT>(p.kept, p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
+      if constexpr (PP == 2) keep_factor(p.kept, 0, p.cp, cw + li, g, 1.f);
+      keep<IO, IB>(p.kept, p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
     }
   }
   for (int kk = 0; kk < nc; ++kk) {
     const int pc = ce - 1 - kk, t0 = pc * C;
+    char* const record = p.kept + (bh * p.nch + pc) * static_cast<int64_t>(kept.bytes());
     __syncthreads();
     {
       const int me = ROWS >= 128 || !VEC ? opaque(tid) : tid;
@@ -1189,7 +1203,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     const float end_dec = ek[C - 1];
     const int lane = opaque(tid) & 63, g = lane >> 4, li = lane & 15;
     if (kk + 1 < nc) load_chunk(pc - 1);
-    if constexpr (!SEG) keep<IO, RT>(p.states + (bh * p.nch + pc) * wsize * kept_size<IO>(), p.states_by + (bh * p.nch + pc) * (p.cp / 16), p.rp, p.cp, cw + li, g, R);
+    if constexpr (!SEG) keep<IO, RT>(record + kept.state(1), record + kept.by(1), p.rp, p.cp, cw + li, g, R);
 
     // ---- X = K R (rows are tokens); the operands of step s + 1 are read and split under the matrix instructions of step s
     constexpr int LOW = IB == 2 ? 3 : 6;  // operand steps on and below the diagonal
@@ -1352,8 +1366,8 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
       __builtin_amdgcn_sched_barrier(0);
     }
     if (kk + 1 < nc) load_late(pc - 1);
-    if constexpr (!SEG) keep<IO, IB>(p.res + (bh * p.nch + pc) * C * p.cp * kept_size<IO>(), p.res_by + (bh * p.nch + pc) * (p.cp / 16), C, p.cp, cw + li, g, X);
-    if constexpr (!SEG && PP == 2) keep_factor(p.in_by + (bh * p.nch + pc) * (p.cp / 16), 1, p.cp, cw + li, g, ob);
+    if constexpr (!SEG) keep<IO, IB>(record + kept.rows(1), record + kept.by(3), C, p.cp, cw + li, g, X);
+    if constexpr (!SEG && PP == 2) keep_factor(record + kept.by(4), 1, p.cp, cw + li, g, ob);
 
     const int yb0 = state_col_base<IO, NK>(li, g);
 #pragma unroll
@@ -1400,12 +1414,7 @@ __global__ void __launch_bounds__((64 * NW), 2) ssm_delta_both_kernel(const Delt
 // ---------------------------------------------------------------- the gradients, all chunks at once
 
 struct DeltaGradDev {
-  DeltaDev f;                  // q, k, rates, sizes; v is dO; states S_0, res r
-  const char* r1;              // [b][H][nch][rp][cp]: R after every chunk
-  const char* e;               // [b][H][nch][C][cp]
-  const float* r1_by;          // their factors
-  const float* e_by;
-  const float* do_by;
+  DeltaDev f;                  // q, k, rates, kept, sizes; v is dO
   char* dq;                    // [b][L][H / hn][rows]; float32 parts with `parts`
   char* dk;
   char* dv;                    // [b][L][H][cols]
@@ -1521,41 +1530,42 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
   if (t0 < len) {
     constexpr int KB = kept_size<IO>();
     const int hk = hg * d.hn / p.rep, nslab = p.cp / kSlab, steps = nslab * SS;
-    const uint32_t wbytes = static_cast<uint32_t>(p.rp * p.cp * KB), rbytes = static_cast<uint32_t>(C * p.cp * KB);
-    const uint32_t bybytes = static_cast<uint32_t>(p.cp / 16 * 4);
+    const Kept<IO> kept(p.rp, p.cp);
     const int64_t chunk0 = (static_cast<int64_t>(b) * p.H + hg * d.hn) * p.nch + pc;  // of head hh: hh nch further
     // What a thread has in flight: its part of a slab's dO, r and e, and the operands S_0 and R_C of its wavefront for
     // the next two steps.
     uint4 go[TASKS], gr[TASKS], ge[TASKS], s0[2][CT], r1[2][CT], rr[TR::CNT];
     float gr_by[TASKS], ge_by[TASKS], s0_by[2], r1_by[2], most[5] = {};
-    auto factor = [&](const float* by, int64_t chunk, int col) {
-      if constexpr (KB == 4) return 1.f;
-      const Rsrc r = make_rsrc(by + chunk * (p.cp / 16), bybytes);
-      return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, col / 16 * 4, 0, 0));
+    auto record = [&](int hh) {
+      return make_rsrc(p.kept + (chunk0 + static_cast<int64_t>(hh) * p.nch) * kept.bytes(), kept.bytes());
+    };
+    auto values_at = [](Rsrc r, uint32_t off, uint32_t part) {
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off, part, 0);
+      return make_uint4(v.x, v.y, v.z, v.w);
+    };
+    auto factor_at = [](Rsrc r, uint32_t off, uint32_t part) {
+      return __uint_as_float(HALF ? __builtin_amdgcn_raw_buffer_load_b32(r, off, part, 0) : 0x3f800000u);
     };
     auto load_slab = [&](int hh, int v0) {
-      const int64_t chunk = chunk0 + static_cast<int64_t>(hh) * p.nch;
+      const Rsrc rec = record(hh);
       const Rsrc rdo = make_rsrc(p.v + b * p.v_b + static_cast<int64_t>(t0) * p.v_t + static_cast<int64_t>(hg * d.hn + hh) * p.cols * ES,
                                  row_bytes(len - t0, C, p.v_t));
-      const Rsrc rres = make_rsrc(p.res + chunk * rbytes, rbytes), re = make_rsrc(d.e + chunk * rbytes, rbytes);
 #pragma unroll
       for (int i = 0; i < TASKS; ++i) {
         const int me = opaque(tid), r = me / NS + i * (T / NS), col = v0 + me % NS * E;
         go[i] = load16<IO, VEC>(rdo, r * p.v_t + col * ES, p.cols - col);
-        gr[i] = load16<IO, true>(rres, (r * p.cp + col) * KB, 1);
-        ge[i] = load16<IO, true>(re, (r * p.cp + col) * KB, 1);
-        gr_by[i] = factor(p.res_by, chunk, col);
-        ge_by[i] = factor(d.e_by, chunk, col);
+        gr[i] = values_at(rec, (r * p.cp + col) * KB, kept.rows(0));
+        ge[i] = values_at(rec, (r * p.cp + col) * KB, kept.rows(1));
+        gr_by[i] = factor_at(rec, col / 16 * 4, kept.by(2));
+        ge_by[i] = factor_at(rec, col / 16 * 4, kept.by(3));
       }
     };
     // a head's factors, those of 16 columns a lane
     auto load_factors = [&](int hh) {
-      const int64_t chunk = chunk0 + static_cast<int64_t>(hh) * p.nch;
-      most[0] = factor(p.states_by, chunk, 16 * lane);
-      most[1] = factor(d.r1_by, chunk, 16 * lane);
-      most[2] = factor(p.res_by, chunk, 16 * lane);
-      most[3] = factor(d.e_by, chunk, 16 * lane);
-      most[4] = factor(d.do_by, chunk, 16 * lane);
+      const Rsrc rec = record(hh);
+      const uint32_t off = 16 * lane < p.cp ? 4 * lane : kOOB;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) most[i] = factor_at(rec, off, kept.by(i));
     };
     // step n of head hh, of the next head where this one has none
     auto load_states = [&](int hh, int n, int to) {
@@ -1564,17 +1574,17 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
         ++hh;
       }
       if (n >= steps || hh >= d.hn) return;
-      const int64_t chunk = chunk0 + static_cast<int64_t>(hh) * p.nch;
-      const Rsrc rs0 = make_rsrc(p.states + chunk * wbytes, wbytes), rr1 = make_rsrc(d.r1 + chunk * wbytes, wbytes);
+      const Rsrc rec = record(hh);
       const int me = opaque(lane), col = KS * n + E * (me >> 4);
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        const uint32_t off = static_cast<uint32_t>(((wave * CT + c) * 16 + (me & 15)) * p.cp + col) * KB;
-        s0[to][c] = load16<IO, true>(rs0, off, 1);
-        r1[to][c] = load16<IO, true>(rr1, off, 1);
+        const int row = (wave * CT + c) * 16;
+        const uint32_t off = row < p.rp ? static_cast<uint32_t>((row + (me & 15)) * p.cp + col) * KB : kOOB;
+        s0[to][c] = values_at(rec, off, kept.state(0));
+        r1[to][c] = values_at(rec, off, kept.state(1));
       }
-      s0_by[to] = factor(p.states_by, chunk, col);
-      r1_by[to] = factor(d.r1_by, chunk, col);
+      s0_by[to] = factor_at(rec, col / 16 * 4, kept.by(0));
+      r1_by[to] = factor_at(rec, col / 16 * 4, kept.by(1));
     };
     {
       uint4 rx[TK::CNT], ry[TK::CNT];
