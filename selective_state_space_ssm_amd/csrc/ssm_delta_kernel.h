@@ -1689,27 +1689,41 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
             if constexpr (HALF) return Halves::mma(a, b, acc);
             else return mma<IO>(a, b, acc);
           };
-#pragma unroll
-          for (int ib = 0; ib < IB; ++ib) {
-            __builtin_amdgcn_sched_barrier(0);
-            const uint4 fo = frag_row<NS>(tdo, fb, ib, s), fu = frag_row<NS>(tu, fb, ib, s), fe = frag_row<NS>(te, fb, ib, s);
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-              dq[c][ib] = add(fs[c], fo, dq[c][ib]);
-              ur[c][ib] = add(fr[c], fu, ur[c][ib]);
-              vs[c][ib] = add(fs[c], fe, vs[c][ib]);
-            }
-          }
+          // the next block's operands are read before the present one's products
+          uint4 fo[2], fu[2], fe[2], fx[MINE], fy[MINE];
+          auto read = [&](int ib) {
+            fo[ib & 1] = frag_row<NS>(tdo, fb, ib, s);
+            fu[ib & 1] = frag_row<NS>(tu, fb, ib, s);
+            fe[ib & 1] = frag_row<NS>(te, fb, ib, s);
+          };
           // tiles of dP, then of dN, dealt to the wavefronts: lane holds j = 4 g + v of i = li
-#pragma unroll
-          for (int m = 0; m < MINE; ++m) {
-            __builtin_amdgcn_sched_barrier(0);
-            const int job = wave + m * NW;
-            if (job >= 2 * TILES) continue;
+          auto read_scores = [&](int m) {
+            const int job = wave + m * NW < 2 * TILES ? wave + m * NW : 0;
             int ib, jb;
             score_tile<IB>(job < TILES ? job : job - TILES, ib, jb);
-            sc[m] = add(frag_row<NS>(tu, fb, jb, s), frag_row<NS>(job < TILES ? tdo : te, fb, ib, s), sc[m]);
+            fx[m] = frag_row<NS>(tu, fb, jb, s);
+            fy[m] = frag_row<NS>(job < TILES ? tdo : te, fb, ib, s);
+          };
+          read(0);
+#pragma unroll
+          for (int ib = 0; ib < IB; ++ib) {
+            if (ib + 1 < IB) {
+              read(ib + 1);
+            } else {
+#pragma unroll
+              for (int m = 0; m < MINE; ++m) read_scores(m);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+              dq[c][ib] = add(fs[c], fo[ib & 1], dq[c][ib]);
+              ur[c][ib] = add(fr[c], fu[ib & 1], ur[c][ib]);
+              vs[c][ib] = add(fs[c], fe[ib & 1], vs[c][ib]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
+#pragma unroll
+          for (int m = 0; m < MINE; ++m) sc[m] = add(fx[m], fy[m], sc[m]);
         }
       }
 
@@ -1803,7 +1817,6 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
         }
 #pragma unroll
         for (int ib = 0; ib < IB; ++ib) {
-          __builtin_amdgcn_sched_barrier(0);
           if (js * KS < 16 * (ib + 1)) {
 #pragma unroll
             for (int q = 0; q < PP; ++q) {
