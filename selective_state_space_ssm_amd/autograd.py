@@ -15,6 +15,11 @@ marshalling only; every step runs in the library's kernels.
 
 Gradients flow to every tensor argument that requires them (dB and dC are
 computed in float32 and returned in the dtype of B and C).
+
+A backward pass may be captured into a HIP graph.  torch's own rule for it:
+no graph of the same leaves that was recorded outside the capture may still be
+alive then (its accumulation nodes belong to the other stream, and waiting for
+them ends the capture and the process); drop such outputs first.
 """
 from __future__ import annotations
 
@@ -23,8 +28,9 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (ssm_add_norm, ssm_add_norm_bwd, ssm_delta_scan_bwd, ssm_delta_scan_fwd, ssm_gate_norm, ssm_gate_norm_bwd, ssm_head_scan_bwd, ssm_head_scan_fwd, ssm_linear, ssm_linear_bwd,
-               ssm_out_proj, ssm_out_proj_bwd, ssm_scan_bwd, ssm_scan_bwd_conv,
+from . import (ssm_add_norm, ssm_add_norm_bwd, ssm_delta_scan_bwd, ssm_delta_scan_fwd, ssm_gate_norm,
+               ssm_gate_norm_bwd, ssm_head_scan_bwd, ssm_head_scan_fwd, ssm_linear, ssm_linear_bwd, ssm_out_proj,
+               ssm_out_proj_bwd, ssm_scan_bwd, ssm_scan_bwd_conv,
                ssm_scan_fwd_conv, ssm_scan_fwd_states)
 
 __all__ = ["selective_scan", "selective_scan_conv", "out_proj", "head_scan", "delta_scan", "gate_norm", "add_norm",

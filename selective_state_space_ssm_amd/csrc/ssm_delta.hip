@@ -55,7 +55,9 @@ int64_t tiles_for(int64_t rows, int64_t cols, bool vec, bool bf16) {
 
 // States carried over the segments, in order, 16 columns a workgroup: state <- A carried + own, or A^T carried + own
 // from the end.  Float32 matrix instructions, 16 rows a wavefront; the carried columns are in LDS.  A segment's rows of
-// A are asked for while the segment before is worked on: each operand takes its successor once it is used.
+// A are asked for while the segment before is worked on: each operand takes its successor once it is used.  The column
+// tiles of a head are a multiple of the heads apart, so that with 8 or more heads they share an XCD's L2 for A.  16 heads
+// of 128 x 128 in 16 segments: 47 us, 3.4 a segment, from load to load.
 template <int NW, bool REV>
 __global__ void __launch_bounds__(64 * NW) ssm_delta_carry_kernel(float* state, const float* trans, int nseg, int rp, int cp) {
   __shared__ float carried[16 * NW][17];
@@ -119,7 +121,10 @@ __global__ void __launch_bounds__(64 * NW) ssm_delta_carry_kernel(float* state, 
 // S~ = e^g S, both S~^T k and S~^T q come from one pass over the state's
 // registers, with q . k: o = scale (S~^T q + (q . k) u), u = b (v - S~^T k), so
 // that one exchange between the wavefronts serves both.  Every load is issued
-// before the first store (the update may be in place).
+// before the first store (the update may be in place).  Bound by the state's
+// traffic: 256 sequences, 32 heads of 128 x 128 196 us, 5.5 TB/s, past what a
+// copy reaches (4.9); eight workgroups a CU, whose registers allow it up to 128
+// rows (with four 222 us).
 struct DeltaStepDev {
   const char* q;
   const char* k;
@@ -245,8 +250,8 @@ Plan plan_of(const DeltaArgs& a, bool bf16) {
   // The number of segments that the model below finds shortest, in chunks of a workgroup alone on its CU (4.2 us,
   // bfloat16, 128 x 128): two workgroups a CU take 1.75 of that (float32: 2, the matrix instructions bound it), the
   // segments' own walk 0.8, with the transitions' tiles beside the state's in all but the first, a step of the carry
-  // 0.8, two more launches 3.  16 heads of 128 x 128 over 32768 tokens: 582 us in 16 segments, 605 in 8, whole some
-  // 2.2 ms; 128 heads of 128 x 128 over 2048 tokens are better off whole.  A tenth has to be gained.
+  // 0.8, two more launches 3.  16 heads of 128 x 128 over 32768 tokens: 634 us in 16 segments, 637 in 8, 712 in 24,
+  // whole some 2.2 ms; 128 heads of 128 x 128 over 2048 tokens are better off whole.  A tenth has to be gained.
   const int64_t tv = tiles_for(a.dk, a.dv, true, bf16), tt = cdiv(p.rp, wide_for(a.dk, a.dv, true, bf16) ? 128 : 64), bh = a.batch * a.H;
   const double pair = bf16 ? 1.75 : 2.;
   auto rate = [pair](double wgs) { return wgs <= kDeltaCUs ? 1. : std::max(pair, wgs * pair / (2 * kDeltaCUs)); };

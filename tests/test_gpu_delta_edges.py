@@ -412,3 +412,45 @@ def test_gradients_of_any_layout():
     c = torch.autograd.grad([y, h], [r, z], [w, w], retain_graph=True)
     d = torch.autograd.grad([y, h], [r, z], [w.clone(), w.clone()])
     assert all(torch.equal(u, v) for u, v in zip(c, d))
+
+
+def test_a_gradient_shared_by_two_leaves_is_not_shared_memory():
+    """x and a residual of its dtype have one gradient; what is done to one leaf's does not reach the other's."""
+    x, r = (torch.randn(3, 5, 64, device=DEV, requires_grad=True) for _ in range(2))
+    y, h = ag.add_norm(x, r)
+    (y.sum() + h.square().sum()).backward()
+    assert torch.equal(x.grad, r.grad)
+    kept = r.grad.clone()
+    x.grad.zero_()
+    assert torch.equal(r.grad, kept)
+
+
+def test_a_captured_training_step():
+    """Forward and backward of the layer captured, replayed with other inputs between eager steps on other leaves."""
+    t, sizes = _inputs(torch.bfloat16, 21, L=200)
+    leaves = {n: v.clone().requires_grad_() for n, v in t.items() if n != "wk"}
+    leaves["wk"] = t["wk"]
+    names = [n for n in leaves if n != "wk"]
+
+    def step(a):
+        out = _layer(a, sizes)
+        return torch.autograd.grad([s.float().square().sum() for s in out], [a[n] for n in names])
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(leaves)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize(DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(leaves)
+    for i in range(3):
+        with torch.no_grad():
+            leaves["x"].mul_(0.5)
+            leaves["W"].mul_(-1)
+        graph.replay()
+        torch.cuda.synchronize(DEV)
+        want = step({n: v.detach().clone().requires_grad_(n != "wk") for n, v in leaves.items()})
+        for n, a, b in zip(names, got, want):
+            assert float((a.float() - b.float()).norm()) <= 2.0 ** -7 * float(b.float().norm()), (i, n)
