@@ -719,8 +719,9 @@ __device__ __forceinline__ void widen(const uint4& r, float by, float* v) {
 // other, and every wavefront's products too (S into x, x into r, r into S), so that a chunk takes what its longest chain
 // takes.  The next chunk's operands are under way meanwhile, those of a product are read and split under the product
 // before.  Two workgroups share a CU (80 KB of LDS, 256 registers): alone a chunk takes 4.2 us, two 7.3 (128 x 128,
-// bfloat16), of which the vector unit is busy for 39 %, the matrix unit for 30 % and 18 % are waits.  8 x 2048 ragged
-// tokens, 32 heads of 128 x 128, bfloat16: 179 us.
+// bfloat16), of which the vector unit is busy for 39 %, the matrix unit for 30 % and 18 % are waits.  A wavefront's
+// priority falls from product to product of a chunk, so that two on a SIMD are in different ones: 8 x 2048 ragged tokens,
+// 32 heads of 128 x 128, bfloat16, 163 us, all alike 175 (rising priorities 174; backwards no order gains anything).
 template <typename IO, int ROWS, int NW, int MODE, bool VEC>
 __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char* lds) {
   using K = HeadCfg<IO>;
@@ -854,6 +855,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     if constexpr (MODE == kDeltaStates)
       keep<IO, RT>(record + kept.state(0), record + kept.by(0), p.rp, p.cp, cw + li, g, S);
 
+    __builtin_amdgcn_s_setprio(3);
     // ---- what the state before the chunk gives: X = K S (rows are tokens, by state_row), O = Q S (transposed).  The
     // operands of step s + 1 are read and split under the matrix instructions of step s.
     f32x4 X[IB], O[IB];
@@ -909,6 +911,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
         }
       }
     }
+    __builtin_amdgcn_s_setprio(2);
     // ---- x, then r = x - M (b x)
     constexpr int LOW = IB == 2 ? 3 : 6;  // operand steps on and below the diagonal
     uint4 bx[JS][PP], fm[LOW];
@@ -998,6 +1001,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     if constexpr (MODE == kDeltaStates)
       keep<IO, IB>(record + kept.rows(0), record + kept.by(2), C, p.cp, cw + li, g, X);
 
+    __builtin_amdgcn_s_setprio(1);
     // ---- u = b r as an operand of o, e^{G_C - G} u as one of the state's update
     const int yb0 = state_col_base<IO, NK>(li, g);
     uint4 fu[JS][PP], fw[2][PS];
@@ -1032,6 +1036,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
           for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n)
             O[i] = q < PP ? mma<IO>(fu[js][q], fm[n], O[i]) : mma<IO>(fu[js][0], fl[n], O[i]);
     }
+    __builtin_amdgcn_s_setprio(0);
     // ---- the state after the chunk; under its products the next operand
 #pragma unroll
     for (int js = 0; js < JS; ++js) {
