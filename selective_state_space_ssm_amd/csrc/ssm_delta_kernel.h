@@ -418,7 +418,8 @@ __device__ __forceinline__ void store_parts(const float* n, char* dst, int tid, 
 // A chunk needs nothing of the others, and a workgroup's steps wait for each
 // other: what counts is how many share a CU, hence the scores in the place of the
 // tiles.  It reads k and q and writes five eighths of M and P: 8 x 2048 ragged
-// tokens, 32 heads of 128, bfloat16, 76 us, 4 x 2048 tokens 45.
+// tokens, 32 heads of 128, bfloat16, 60 us (chunks of a head one after the other,
+// each its own rows apart: 84), 4 x 2048 tokens 48.
 template <typename IO, int ROWS, bool VEC>
 __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char* lds) {
   using K = HeadCfg<IO>;
@@ -434,7 +435,7 @@ __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char
   float* const inv = n + C * LD;                    // [IB][16][20]
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int pc = pid % p.nch, bh = pid / p.nch, h = bh % p.H, b = bh / p.H, t0 = pc * C;
+  const int h = pid % p.H, pc = pid / p.H % p.nch, b = pid / p.H / p.nch, bh = b * p.H + h, t0 = pc * C;
   const int len = length_of(p, b);
   if (t0 >= len) return;
   const int64_t chunk = static_cast<int64_t>(bh) * p.nch + pc;
@@ -589,7 +590,10 @@ __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char
 template <typename IO, int ROWS, bool VEC>
 __global__ void __launch_bounds__(256) ssm_delta_prep_kernel(const DeltaDev p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  delta_prep<IO, ROWS, VEC>(p, blockIdx.x, lds);
+  // Heads follow each other, so that workgroups of one time read neighbouring parts of the same tokens' rows, eighths of
+  // them on an XCD each, where they share a key head's lines.
+  const uint32_t per = p.H / 8, slot = blockIdx.x / 8;
+  delta_prep<IO, ROWS, VEC>(p, p.H % 8 != 0 ? blockIdx.x : slot / per * p.H + blockIdx.x % 8 * per + slot % per, lds);
 }
 
 // ---------------------------------------------------------------- the walk over the length, forwards
