@@ -99,12 +99,15 @@ def delta_scan_errors(q, k, v, do=None, g=None, beta=None, h0=None, lengths=None
     ``step``: the error of a sum relative to the product of its vectors' norms.  ``pair``: that of a product of values
     held in two parts.  ``kept``: that of the states, r and e as the gradients of q, k, v, g and beta find them (what
     goes on from token to token does not pass through them).  A token's write k r^T is off by |k| (step + pair) times what r is made of, |v| + |k| |S|; these
-    errors of different tokens are independent and are decayed with the state, so their squares add up."""
+    errors of different tokens are independent and are decayed with the state, so their squares add up.  A token takes
+    a state's error to |I - beta k k^T| = max(1, |1 - beta |k|^2|) of itself at most."""
     Q, K, V, a, bt, live, rep = _prepare(q, k, v, g, beta, lengths)
     b, L, h, _ = Q.shape
     S, r = _forward(Q, K, V, a, bt, h0)
+    sign, bt = bt, np.abs(bt)
     n2 = lambda x: np.sqrt((x * x).sum(-1))
     qn, kn, vn, rn = n2(Q), n2(K), n2(V), n2(r)
+    amp = np.maximum(1.0, np.abs(1.0 - sign * kn ** 2))
     Sn = np.sqrt((S * S).sum((-1, -2))).transpose(1, 0, 2)  # [b, L + 1, h]
     st, both = step, step + pair
     ES = np.zeros((b, L + 1, h))
@@ -112,18 +115,19 @@ def delta_scan_errors(q, k, v, do=None, g=None, beta=None, h0=None, lengths=None
     for t in range(L):
         made = both * (vn[:, t] + kn[:, t] * a[:, t] * Sn[:, t])
         Er[:, t] = np.sqrt(made ** 2 + (kn[:, t] * a[:, t] * ES[:, t]) ** 2)
-        ES[:, t + 1] = np.sqrt((a[:, t] * ES[:, t]) ** 2 + (bt[:, t] * kn[:, t] * made) ** 2 + (st * Sn[:, t + 1]) ** 2)
+        ES[:, t + 1] = np.sqrt((amp[:, t] * a[:, t] * ES[:, t]) ** 2 + (bt[:, t] * kn[:, t] * made) ** 2 +
+                               (st * Sn[:, t + 1]) ** 2)
     out = {"o": scale * qn * (ES[:, 1:] + both * (Sn[:, 1:] + kn * bt * rn)), "last": ES[:, -1] + st * Sn[:, -1]}
     if do is None:
         return out
     DO = np.where(live[..., None, None], _arr(do), 0.0)
-    dq, dk, dv, dg, db, R, Rn = _backward(Q, K, V, DO, a, bt, S, r, scale, dlast)
+    dq, dk, dv, dg, db, R, Rn = _backward(Q, K, V, DO, a, sign, S, r, scale, dlast)
     don, en = n2(DO), Rn * kn
     # R~ at a token is R there less what it passed to v
     ER = np.zeros((b, L + 1, h))
     for t in reversed(range(L)):
         made = scale * qn[:, t] * don[:, t] + bt[:, t] * kn[:, t] ** 2 * Rn[:, t]
-        after = ER[:, t + 1] * (a[:, t + 1] if t + 1 < L else 1.0)
+        after = ER[:, t + 1] * (a[:, t + 1] * amp[:, t + 1] if t + 1 < L else 1.0)
         ER[:, t] = np.sqrt(after ** 2 + (both * made) ** 2 + (st * Rn[:, t]) ** 2)
     Ee = kn * (ER[:, :L] + both * Rn)
     S0, E0 = a * Sn[:, :L], a * ES[:, :L]

@@ -199,6 +199,18 @@ def test_large_and_small_values(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("by", [2.0 ** -6, 2.0 ** 6], ids=["small", "large"])
+@pytest.mark.parametrize("case", [(2, 150, 4, 2, 64, 64), (1, 1500, 2, 1, 128, 40)], ids=["", "segments"])
+def test_keys_and_beta_far_from_one(case, by, dtype):
+    """Keys of any length while beta |k|^2 stays below 2: beta past 1000 and below 2^-12, of either sign; queries too."""
+    x, do, dlast = make(*case, dtype, seed=13)
+    x["k"], x["q"] = x["k"] * by, x["q"] * by ** -3
+    x["beta"] = x["beta"] * by ** -2
+    x["beta"][:, 3::7] *= -0.25
+    against_oracle(x, do, dlast, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 def test_views_give_the_bits_of_copies(dtype):
     b, L, h, d = 3, 70, 2, 64
     r = torch.Generator().manual_seed(5)
