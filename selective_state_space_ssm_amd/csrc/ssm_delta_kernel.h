@@ -1539,7 +1539,7 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
 
   if (t0 < len) {
     constexpr int KB = kept_size<IO>();
-    const int hk = hg * d.hn / p.rep, nslab = p.cp / kSlab, steps = nslab * SS;
+    const int hk = hg * d.hn / p.rep, nslab = p.cp / kSlab;
     const Kept<IO> kept(p.rp, p.cp);
     const int64_t chunk0 = (static_cast<int64_t>(b) * p.H + hg * d.hn) * p.nch + pc;  // of head hh: hh nch further
     // What a thread has in flight: its part of a slab's dO, r and e, and the operands S_0 and R_C of its wavefront for
@@ -1556,8 +1556,7 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
     auto factor_at = [](Rsrc r, uint32_t off, uint32_t part) {
       return __uint_as_float(HALF ? __builtin_amdgcn_raw_buffer_load_b32(r, off, part, 0) : 0x3f800000u);
     };
-    auto load_slab = [&](int hh, int v0) {
-      const Rsrc rec = record(hh);
+    auto load_slab = [&](Rsrc rec, int hh, int v0) {
       const Rsrc rdo = make_rsrc(p.v + b * p.v_b + static_cast<int64_t>(t0) * p.v_t + static_cast<int64_t>(hg * d.hn + hh) * p.cols * ES,
                                  row_bytes(len - t0, C, p.v_t));
 #pragma unroll
@@ -1577,14 +1576,8 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
 #pragma unroll
       for (int i = 0; i < 5; ++i) most[i] = factor_at(rec, off, kept.by(i));
     };
-    // step n of head hh, of the next head where this one has none
-    auto load_states = [&](int hh, int n, int to) {
-      if (n >= steps) {
-        n -= steps;
-        ++hh;
-      }
-      if (n >= steps || hh >= d.hn) return;
-      const Rsrc rec = record(hh);
+    // step n of a head
+    auto load_states = [&](Rsrc rec, int n, int to) {
       const int me = opaque(lane), col = KS * n + E * (me >> 4);
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
@@ -1602,9 +1595,9 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
       TK::template load<VEC>(p.k + b * p.k_b + static_cast<int64_t>(hk) * p.rows * ES, p.k_t, t0, len, p.rows, tid, ry);
       TR::load(reinterpret_cast<const char*>(p.rates + chunk0 * kRates * C), tid, rr);
       if constexpr (HALF) load_factors(0);
-      load_slab(0, 0);
-      load_states(0, 0, 0);
-      load_states(0, 1, 1);
+      load_slab(record(0), 0, 0);
+      load_states(record(0), 0, 0);
+      load_states(record(0), 1, 1);
       TK::store(tx, tid, rx);
       TK::store(ty, tid, ry);
     }
@@ -1673,8 +1666,11 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
           }
         }
         __syncthreads();
-        if (v + 1 < nslab) load_slab(hh, v0 + kSlab);
-        else if (hh + 1 < d.hn) load_slab(hh + 1, 0);
+        // the next slab is this head's or the next one's
+        const bool more = v + 1 < nslab, any = more || hh + 1 < d.hn;
+        const int hn = more ? hh : hh + 1, vn = more ? v + 1 : 0;
+        const Rsrc rec = record(hn);
+        if (any) load_slab(rec, hn, vn * kSlab);
         const int fb = opaque(lane_base<IO, NS>(li, g));
 #pragma unroll
         for (int s = 0; s < SS; ++s) {
@@ -1694,7 +1690,8 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
 #pragma unroll
             for (int e = 0; e < E; ++e) dot_rs = __builtin_fmaf(x[e], y[e], dot_rs);
           }
-          load_states(hh, v * SS + s + 2, s & 1);
+          if (s + 2 < SS) load_states(record(hh), v * SS + s + 2, s & 1);
+          else if (any) load_states(rec, vn * SS + s + 2 - SS, s & 1);
           auto add = [](const uint4& a, const uint4& b, f32x4 acc) {
             if constexpr (HALF) return Halves::mma(a, b, acc);
             else return mma<IO>(a, b, acc);
