@@ -1196,7 +1196,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     }
   }
   for (int kk = 0; kk < nc; ++kk) {
-    const int pc = ce - 1 - kk, t0 = pc * C;
+    const int pc = ce - 1 - kk;
     char* const record = p.kept + (bh * p.nch + pc) * static_cast<int64_t>(kept.bytes());
     __syncthreads();
     {
@@ -1736,10 +1736,12 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
 
       // ---- the scores' gradients to LDS, below the diagonal, and zeros in the tiles above it that a product step covers
       __syncthreads();
-      for (int i = tid; i < 2 * PP * GAP * 16 * (16 / E); i += T) {
-        const int part = i / (GAP * 16 * (16 / E)), at = i % (GAP * 16 * (16 / E)), r = at / (16 / E), c = at % (16 / E);
-        const int row = (r / 16) * 32 + r % 16, col = ((r / 16) * 32 + 16) / E + c;
-        *reinterpret_cast<uint4*>(tp + part * PB + 16 * (NP * row + (col ^ swz<IO, NP>(row)))) = make_uint4(0, 0, 0, 0);
+      if constexpr (GAP > 0) {
+        for (int i = tid; i < 2 * PP * GAP * 16 * (16 / E); i += T) {
+          const int part = i / (GAP * 16 * (16 / E)), at = i % (GAP * 16 * (16 / E)), r = at / (16 / E), c = at % (16 / E);
+          const int row = (r / 16) * 32 + r % 16, col = ((r / 16) * 32 + 16) / E + c;
+          *reinterpret_cast<uint4*>(tp + part * PB + 16 * (NP * row + (col ^ swz<IO, NP>(row)))) = make_uint4(0, 0, 0, 0);
+        }
       }
 #pragma unroll
       for (int m = 0; m < MINE; ++m) {
