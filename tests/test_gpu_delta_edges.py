@@ -199,6 +199,16 @@ def test_large_and_small_values(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("b", [2, 33, 64, 65])
+def test_many_ragged_rows(b, dtype):
+    """Rows in the order of their lengths, equal ones among them; more rows than a wavefront has lanes."""
+    x, do, dlast = make(b, 100, 5, 5, 16, 16, dtype, seed=b)
+    r = torch.Generator().manual_seed(b)
+    x["lengths"] = torch.randint(0, 8, (b,), generator=r).mul(15).to(torch.int32).to(DEV)
+    against_oracle(x, do, dlast, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 @pytest.mark.parametrize("by", [2.0 ** -6, 2.0 ** 6], ids=["small", "large"])
 @pytest.mark.parametrize("case", [(2, 150, 4, 2, 64, 64), (1, 1500, 2, 1, 128, 40)], ids=["", "segments"])
 def test_keys_and_beta_far_from_one(case, by, dtype):
