@@ -250,8 +250,8 @@ Plan plan_of(const DeltaArgs& a, bool bf16) {
   // The number of segments that the model below finds shortest, in chunks of a workgroup alone on its CU (4.2 us,
   // bfloat16, 128 x 128): two workgroups a CU take 1.75 of that (float32: 2, the matrix instructions bound it), the
   // segments' own walk 0.8, with the transitions' tiles beside the state's in all but the first, a step of the carry
-  // 0.8, two more launches 3.  16 heads of 128 x 128 over 32768 tokens: 634 us in 16 segments, 637 in 8, 712 in 24,
-  // whole some 2.2 ms; 128 heads of 128 x 128 over 2048 tokens are better off whole.  A tenth has to be gained.
+  // 0.8, two more launches 3.  16 heads of 128 x 128 over 32768 tokens: 634 us in 16 segments (605 since), 637 in 8, 712
+  // in 24, whole some 2.2 ms; 128 heads of 128 x 128 over 2048 tokens are better off whole.  A tenth has to be gained.
   const int64_t tv = tiles_for(a.dk, a.dv, true, bf16), tt = cdiv(p.rp, wide_for(a.dk, a.dv, true, bf16) ? 128 : 64), bh = a.batch * a.H;
   const double pair = bf16 ? 1.75 : 2.;
   auto rate = [pair](double wgs) { return wgs <= kDeltaCUs ? 1. : std::max(pair, wgs * pair / (2 * kDeltaCUs)); };

@@ -1489,7 +1489,7 @@ __device__ __forceinline__ void scan_back(float& hi, float& lo) {
 // starts anew (a decay of -inf) dg is zero and the sum of the tokens before begins there.
 //
 // In bfloat16 the states, r and e are operands as they are kept, float16 over powers of two, brought to the largest of a
-// chunk's (the products of several columns add up), and dO beside them: 265 us, in two bfloat16 parts each 321 (4 x 2048
+// chunk's (the products of several columns add up), and dO beside them: 260 us, in two bfloat16 parts each 321 (4 x 2048
 // tokens, 32 heads of 128 x 128 on 16 key heads, which is 2.6 TB/s).  A workgroup a CU, so that nothing covers what it
 // waits for at its start (68 us of these) and between its barriers; loads are two steps of states and a slab ahead.
 //
