@@ -509,7 +509,8 @@ int ssm_head_step(const void *q, const void *k, const void *v, const void *g, co
  * largest in that column), and what ends in o as two of bfloat16 (2^-17).
  * Values that are not finite reach every later result of their head in their
  * batch row, and those of their chunk (64 tokens from a multiple of 64, float32:
- * 32) before them; a decay of -inf does not hold them back within a chunk.
+ * 32) before them, until the state starts anew at a chunk's first token (a decay
+ * of -inf there; within a chunk it does not hold them back).
  */
 int ssm_delta_scan_fwd(const void *q, int64_t q_batch, int64_t q_token, const void *k, int64_t k_batch, int64_t k_token,
                        const void *v, int64_t v_batch, int64_t v_token, const void *g, const void *beta,
@@ -532,7 +533,8 @@ int ssm_delta_scan_fwd(const void *q, int64_t q_batch, int64_t q_token, const vo
  * Rounding: R, and with it dh0, as the state.  With SSM_BF16 dq, dk, dv, dg and
  * dbeta, which are rounded to 2^-8, take the states, r and e as float16 (2^-11)
  * over a power of two that 16 columns share.  With values that are not finite no
- * gradient of their head in their batch row is defined.
+ * gradient of their head is defined between the starts at chunks' first tokens
+ * that are around them.
  * Other arguments and errors as ssm_head_scan_bwd and ssm_delta_scan_fwd.
  */
 int ssm_delta_scan_bwd(const void *q, int64_t q_batch, int64_t q_token, const void *k, int64_t k_batch, int64_t k_token,

@@ -40,7 +40,7 @@ using deltak::DeltaGradDev;
 
 constexpr int64_t kDeltaCUs = 256;
 constexpr int64_t kDeltaMinSegment = 3;   // chunks
-constexpr int64_t kDeltaMaxSegments = 64;
+constexpr int64_t kDeltaMaxSegments = 64;  // the carry's wavefronts hold something of each in a lane
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
@@ -57,9 +57,11 @@ int64_t tiles_for(int64_t rows, int64_t cols, bool vec, bool bf16) {
 // from the end.  Float32 matrix instructions, 16 rows a wavefront; the carried columns are in LDS.  A segment's rows of
 // A are asked for while the segment before is worked on: each operand takes its successor once it is used.  The column
 // tiles of a head are a multiple of the heads apart, so that with 8 or more heads they share an XCD's L2 for A.  16 heads
-// of 128 x 128 in 16 segments: 47 us, 3.4 a segment, from load to load.
+// of 128 x 128 in 16 segments: 49 us, 3.5 a segment, from load to load.  A segment in which the state starts anew, or which
+// has no tokens, takes no product (see kSegWhole).
 template <int NW, bool REV>
-__global__ void __launch_bounds__(64 * NW) ssm_delta_carry_kernel(float* state, const float* trans, int nseg, int rp, int cp) {
+__global__ void __launch_bounds__(64 * NW) ssm_delta_carry_kernel(float* state, const float* trans, const int* kinds, int nseg,
+                                                                  int rp, int cp) {
   __shared__ float carried[16 * NW][17];
   const int64_t bh = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
@@ -70,6 +72,7 @@ __global__ void __launch_bounds__(64 * NW) ssm_delta_carry_kernel(float* state, 
   const float* const m = trans + bh * nseg * ts;
   const int first = REV ? nseg - 1 : 0, step = REV ? -1 : 1;
   const bool mine = wave < tiles;
+  const int kind_of_lane = lane < nseg ? kinds[bh * nseg + lane] : 0;  // of segment `lane`
   float4 f[NW];  // operand steps of 16 of A's columns
   auto load_a = [&](int at, int k) {
     if (!mine || k >= tiles) return;
@@ -90,6 +93,7 @@ __global__ void __launch_bounds__(64 * NW) ssm_delta_carry_kernel(float* state, 
   for (int i = 1; i < nseg - 1; ++i) {
     const int at = first + i * step, next = i + 2 < nseg ? at + step : at;
     float* const own = s + at * ws;
+    const int kind = __builtin_amdgcn_readlane(kind_of_lane, at);
     f32x4 acc = {0.f, 0.f, 0.f, 0.f}, sum[2] = {acc, acc};
 #pragma unroll
     for (int v = 0; v < 4; ++v)
@@ -107,7 +111,9 @@ __global__ void __launch_bounds__(64 * NW) ssm_delta_carry_kernel(float* state, 
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int r = row + 4 * g + v;
-        const float x = acc[v] + (sum[0][v] + sum[1][v]);
+        float x = acc[v] + (sum[0][v] + sum[1][v]);
+        if (kind == deltak::kSegAnew) x = acc[v];
+        else if (kind == deltak::kSegEmpty) x = carried[r][li];
         carried[r][li] = x;
         own[static_cast<int64_t>(r) * cp + c] = x;
       }
@@ -301,7 +307,7 @@ int64_t grad_heads(const DeltaArgs& a, const Plan& pl) {
 
 // Where the workspace's parts are, in bytes from its start.
 struct Space {
-  int64_t m, s, rates, ss, rs, trans, kept, pq, pk, total;
+  int64_t m, s, rates, ss, rs, trans, kind, kept, pq, pk, total;
 };
 Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
   Space w{};
@@ -318,6 +324,7 @@ Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
   if (pl.nseg > 1) {
     w.ss = take(4 * bh * pl.nseg * pl.rp * pl.cp);
     w.trans = take(4 * bh * pl.nseg * pl.rp * pl.rp);
+    w.kind = take(4 * bh * pl.nseg);
     if (backward) w.rs = take(4 * bh * pl.nseg * pl.rp * pl.cp);
   }
   if (backward) {
@@ -348,6 +355,7 @@ DeltaDev dev_of(const DeltaArgs& a, const Plan& pl, const Space& w, char* work, 
   d.rates = reinterpret_cast<float*>(work + w.rates);
   d.seg_state = reinterpret_cast<float*>(work + w.ss);
   d.seg_trans = reinterpret_cast<float*>(work + w.trans);
+  d.seg_kind = reinterpret_cast<int*>(work + w.kind);
   d.kept = work + w.kept;
   d.batch = static_cast<int>(a.batch); d.H = static_cast<int>(a.H); d.L = static_cast<int>(a.L);
   d.rows = static_cast<int>(a.dk); d.cols = static_cast<int>(a.dv);
@@ -368,7 +376,7 @@ hipError_t launch_carry(const DeltaDev& d, bool rev, hipStream_t st) {
   auto kern = wide ? (rev ? ssm_delta_carry_kernel<16, true> : ssm_delta_carry_kernel<16, false>)
                    : (rev ? ssm_delta_carry_kernel<8, true> : ssm_delta_carry_kernel<8, false>);
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(d.batch * d.H), static_cast<unsigned>(d.cp / 16)), dim3(wide ? 1024 : 512),
-                     0, st, d.seg_state, d.seg_trans, d.nseg, d.rp, d.cp);
+                     0, st, d.seg_state, d.seg_trans, d.seg_kind, d.nseg, d.rp, d.cp);
   return hipGetLastError();
 }
 

@@ -72,6 +72,7 @@ struct DeltaDev {
   float* rates;                // [b][H][nch][kRates][C]
   float* seg_state;            // [b][H][nseg][rp][cp]
   float* seg_trans;            // [b][H][nseg][rp][rp]: what a segment makes of the state before it
+  int* seg_kind;               // [b][H][nseg]: see kSegWhole
   char* kept;                  // [b][H][nch] records of what the walks leave for the gradients (see Kept)
   int batch, H, L, rows, cols;
   int rp, cp;                  // rows and columns of states in the workspace: multiples of 16 and of kSlab
@@ -605,6 +606,11 @@ __global__ void __launch_bounds__(256) ssm_delta_prep_kernel(const DeltaDev p) {
 // the state before every chunk and r.
 constexpr int kDeltaOut = 0, kDeltaSeg = 1, kDeltaStates = 2;
 
+// What a segment leaves of the state before it: what its transition makes of it; nothing, since the state starts anew in
+// it; all, since it has no tokens.  A product with that transition of zeros or ones would not be that where the state is
+// not finite.
+constexpr int kSegWhole = 0, kSegAnew = 1, kSegEmpty = 2;
+
 template <typename IO, int ROWS, int NW, bool QUERY>
 constexpr size_t delta_lds_bytes() {
   using K = HeadCfg<IO>;
@@ -841,6 +847,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
 
   const Kept<IO> kept(p.rp, p.cp);
   const int cl = (len + C - 1) / C, ce = c1 < cl ? c1 : cl, nc = ce - c0;
+  int kind = nc > 0 ? kSegWhole : kSegEmpty;
   if (nc > 0) {
     load_chunk(c0);
     if constexpr (QUERY) load_queries(c0);
@@ -873,6 +880,8 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     const float end_dec = ek[C - 1];
     const int lane = opaque(tid) & 63, g = lane >> 4, li = lane & 15;
     if (kk + 1 < nc) load_chunk(pc + 1);
+    if constexpr (MODE == kDeltaSeg)
+      if (trans && end_dec == 0.f && __builtin_amdgcn_ballot_w64(lane < C && rt[kAnew * C + lane % C] != 0.f) != 0) kind = kSegAnew;
 
     if constexpr (MODE == kDeltaStates)
       keep<IO, RT>(record + kept.state(0), record + kept.by(0), p.rp, p.cp, cw + li, g, S);
@@ -1105,8 +1114,12 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
   }
   const int g = (tid & 63) >> 4, c = cw + (tid & 15);
   if constexpr (MODE == kDeltaSeg) {
-    if (trans) store_state<IO, RT>(p.seg_trans + (bh * p.nseg + seg) * p.rp * p.rp, p.rp, p.rp, p.rp, c, g, S);
-    else store_state<IO, RT>(p.seg_state + (bh * p.nseg + seg) * wsize, p.rp, p.cp, p.cp, c, g, S);
+    if (trans) {
+      store_state<IO, RT>(p.seg_trans + (bh * p.nseg + seg) * p.rp * p.rp, p.rp, p.rp, p.rp, c, g, S);
+      if (ct == 0 && tid == 0) p.seg_kind[bh * p.nseg + seg] = kind;
+    } else {
+      store_state<IO, RT>(p.seg_state + (bh * p.nseg + seg) * wsize, p.rp, p.cp, p.cp, c, g, S);
+    }
   } else if (p.last != nullptr && seg == p.nseg - 1) {
     store_state<IO, RT>(p.last + bh * p.rows * p.cols, p.rows, p.cols, p.cols, c, g, S);
   }
