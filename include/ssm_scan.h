@@ -530,11 +530,10 @@ int ssm_delta_scan_fwd(const void *q, int64_t q_batch, int64_t q_token, const vo
  *           state and its gradient at every chunk.
  * dg of a chunk's tokens is a sum over the chunk from its end.  Every sum is taken
  * in a fixed order: repeated calls give identical bits.
- * Rounding: R, and with it dh0, as the state.  With SSM_BF16 dq, dk, dv, dg and
- * dbeta, which are rounded to 2^-8, take the states, r and e as float16 (2^-11)
- * over a power of two that 16 columns share.  With values that are not finite no
- * gradient of their head is defined between the starts at chunks' first tokens
- * that are around them.
+ * Rounding: R, and with it dh0, as the state.  With SSM_BF16 the states, R, r and
+ * e enter the products that dq, dk, dv, dg and dbeta are made of as two parts of
+ * bfloat16 (2^-17).  With values that are not finite no gradient of their head is
+ * defined between the starts at chunks' first tokens that are around them.
  * Other arguments and errors as ssm_head_scan_bwd and ssm_delta_scan_fwd.
  */
 int ssm_delta_scan_bwd(const void *q, int64_t q_batch, int64_t q_token, const void *k, int64_t k_batch, int64_t k_token,

@@ -148,3 +148,37 @@ def delta_scan_errors(q, k, v, do=None, g=None, beta=None, h0=None, lengths=None
     out["dg"] = total.reshape(b, -1, h)[:, :L]
     out["dh0"] = ER[:, 0] + st * Rn[:, 0] if L else 0.0
     return out
+
+
+def delta_scan_spread(q, k, v, do, g=None, beta=None, h0=None, lengths=None, scale=1.0, dlast=None, chunk=64):
+    """Root of the sum of the squares of the products that each gradient's numbers are sums of: roundings of their factors
+    that are independent of each other add up to so much of the roundings' size.  dq, dk: [b, L, h, d_key], of the heads by
+    themselves; dv; dg, dbeta: [b, L, h].  dg as a sum over the rest of a chunk of a token's products with q and k, and
+    over the chunk's end of <R, S>."""
+    Q, K, V, a, bt, live, _ = _prepare(q, k, v, g, beta, lengths)
+    DO = np.where(live[..., None, None], _arr(do), 0.0)
+    b, L, h, _ = Q.shape
+    S, r = _forward(Q, K, V, a, bt, h0)
+    R = np.zeros_like(S[0]) if dlast is None else _arr(dlast).copy()
+    out = {"dq": np.zeros_like(Q), "dk": np.zeros_like(K), "dv": np.zeros_like(V), "dg": np.zeros((b, L, h)),
+           "dbeta": np.zeros((b, L, h))}
+    over = lambda x, m: np.matmul(x[:, :, None, :] ** 2, m * m)[:, :, 0]   # sum over rows of x_i^2 m_ij^2
+    along = lambda m, x: np.matmul(m * m, x[..., None] ** 2)[..., 0]       # over columns
+    total = np.zeros((b, h))
+    for t in reversed(range(L)):
+        if t == L - 1 or t % chunk == chunk - 1:
+            total = (R * R * S[t + 1] ** 2).sum((-1, -2))
+        R = R + scale * Q[:, t, :, :, None] * DO[:, t, :, None, :]
+        s = a[:, t, :, None, None] * S[t]
+        e = np.matmul(K[:, t, :, None, :], R)[:, :, 0]
+        n = bt[:, t, :, None]
+        dv = n * e
+        dq = scale ** 2 * along(S[t + 1], DO[:, t])
+        dk = along(R, n * r[:, t]), along(s, dv)
+        e2, r2 = over(K[:, t], R), V[:, t] ** 2 + over(K[:, t], s)
+        out["dq"][:, t], out["dk"][:, t], out["dv"][:, t] = np.sqrt(dq), np.sqrt(dk[0] + dk[1]), n * np.sqrt(e2)
+        out["dbeta"][:, t] = np.sqrt((e2 * r[:, t] ** 2 + e ** 2 * r2).sum(-1))
+        total = total + (Q[:, t] ** 2 * dq + K[:, t] ** 2 * (dk[0] + dk[1])).sum(-1)
+        out["dg"][:, t] = np.sqrt(total)
+        R = a[:, t, :, None, None] * (R - K[:, t, :, :, None] * dv[:, :, None, :])
+    return out

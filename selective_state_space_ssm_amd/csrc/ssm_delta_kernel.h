@@ -673,74 +673,32 @@ __device__ __forceinline__ void store_state(float* dst, int rows, int cols, int 
       if (r < rows && c < cols) dst[r * ld + c] = S[rt][v];
     }
 }
-// What the walks leave for the gradients: float32, or with bfloat16 storage float16 of the values over a power of two
-// that a wavefront's 16 columns share and that takes the largest of them to 2^14 .. 2^15.  Off by 2^-11 of a value at
-// most, where the gradients they end in are rounded to 2^-8: a walk writes and the gradients read half the bytes.
-template <typename IO>
-constexpr int kept_size() { return HeadCfg<IO>::ES; }
 
-// A chunk's record, one piece of memory so that one resource reaches all of it: S_0, R_C ([rp][cp] each), r, e ([C][cp])
-// and, in bfloat16, the factors of S_0, R_C, r, e and dO for every 16 columns.
+// What the walks leave of a chunk for the gradients, one piece of memory so that one resource reaches all of it: S_0, R_C
+// ([rp][cp] each), r, e ([C][cp]), float32 as they hold them.  (Float16 over powers of two moves half the bytes; dg, a sum
+// of many products that cancel, is then off by 3e-3 of its norm where its own rounding is 1.7e-3, and an e far below the
+// largest of its chunk is lost.)
 template <typename IO>
 struct Kept {
-  static constexpr int FACTORS = kept_size<IO>() == 2 ? 5 : 0;
-  uint32_t w, t, f;  // bytes of a state, of tokens' rows, of factors
-  __host__ __device__ __forceinline__ Kept(int rp, int cp)
-      : w(rp * cp * kept_size<IO>()), t(HeadCfg<IO>::C * cp * kept_size<IO>()), f(cp / 16 * 4) {}
+  uint32_t w, t;  // bytes of a state, of tokens' rows
+  __host__ __device__ __forceinline__ Kept(int rp, int cp) : w(rp * cp * 4), t(HeadCfg<IO>::C * cp * 4) {}
   __host__ __device__ __forceinline__ uint32_t state(int back) const { return back * w; }
   __host__ __device__ __forceinline__ uint32_t rows(int back) const { return 2 * w + back * t; }
-  __host__ __device__ __forceinline__ uint32_t by(int i) const { return 2 * w + 2 * t + i * f; }
-  __host__ __device__ __forceinline__ uint32_t bytes() const { return (by(FACTORS) + 255) / 256 * 256; }  // whole cache lines
+  __host__ __device__ __forceinline__ uint32_t bytes() const { return 2 * (w + t); }
 };
 
-// A factor of the columns c .. c + 15 of a wavefront beside the chunk's others; nothing is written with rows = 0.
-__device__ __forceinline__ void keep_factor(char* by, int rows, int cp, int c, int g, float f) {
-  const Rsrc r = make_rsrc(by, rows > 0 ? static_cast<uint32_t>(cp / 16 * 4) : 0u);
-  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f), r, (c & 15) == 0 && g == 0 ? c / 16 * 4 : kOOB, 0, 0);
-}
-
-// Accumulator tiles to `rows` rows of cp values in the workspace (a resource, which bounds the rows; none of it with
+// Accumulator tiles to `rows` rows of cp floats in the workspace (a resource, which bounds the rows; none of it with
 // rows = 0), by instructions whose number does not depend on the sizes: loads and stores are counted together and in
-// order, and the wait for the next chunk's loads can leave these in flight only if their number is known.  by: the
-// chunk's cp / 16 factors.
+// order, and the wait for the next chunk's loads can leave these in flight only if their number is known.
 template <typename IO, int N>
-__device__ __forceinline__ void keep(char* dst, char* by, int rows, int cp, int c, int g, const f32x4 (&X)[N]) {
-  constexpr int KB = kept_size<IO>();
-  const Rsrc r = make_rsrc(dst, static_cast<uint32_t>(rows * cp * KB));
-  const uint32_t off = c < cp ? c * KB : kOOB;
-  float f = 1.f;
-  if constexpr (KB == 2) {
-    float m = 0.f;
-#pragma unroll
-    for (int rt = 0; rt < N; ++rt)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) m = __builtin_fmaxf(m, __builtin_fabsf(X[rt][v]));
-    const Halves h(wave_max(m));
-    f = h.to;
-    keep_factor(by, rows, cp, c, g, h.back);
-  }
+__device__ __forceinline__ void keep(char* dst, int rows, int cp, int c, int g, const f32x4 (&X)[N]) {
+  const Rsrc r = make_rsrc(dst, static_cast<uint32_t>(rows * cp * 4));
+  const uint32_t off = c < cp ? c * 4 : kOOB;
 #pragma unroll
   for (int rt = 0; rt < N; ++rt)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const uint32_t to = off + state_row<IO>(rt, g, v) * cp * KB;
-      if constexpr (KB == 2)
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<_Float16>(X[rt][v] * f)), r, to, 0, 0);
-      else
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(X[rt][v]), r, to, 0, 0);
-    }
-}
-// The E kept values of 16 bytes and their factor
-template <typename IO>
-__device__ __forceinline__ void widen(const uint4& r, float by, float* v) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
-#pragma unroll
-  for (int e = 0; e < HeadCfg<IO>::E; ++e) {
-    if constexpr (HeadCfg<IO>::ES == 2)
-      v[e] = by * static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu)));
-    else
-      v[e] = __uint_as_float(w[e]);
-  }
+    for (int v = 0; v < 4; ++v)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(X[rt][v]), r, off + state_row<IO>(rt, g, v) * cp * 4, 0, 0);
 }
 
 // A chunk at a time, a workgroup for a (batch row, head, segment) and 16 NW columns of d_value: its chunks follow each
@@ -857,8 +815,8 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     if constexpr (QUERY) {
       store_out(reinterpret_cast<const f32x4(&)[IB]>(none), 0, 0, li, g);
     } else if constexpr (MODE == kDeltaStates) {
-      keep<IO, RT>(p.kept, p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
-      keep<IO, IB>(p.kept, p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
+      keep<IO, RT>(p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
+      keep<IO, IB>(p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
     }
   }
   for (int kk = 0; kk < nc; ++kk) {
@@ -884,7 +842,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
       if (trans && end_dec == 0.f && __builtin_amdgcn_ballot_w64(lane < C && rt[kAnew * C + lane % C] != 0.f) != 0) kind = kSegAnew;
 
     if constexpr (MODE == kDeltaStates)
-      keep<IO, RT>(record + kept.state(0), record + kept.by(0), p.rp, p.cp, cw + li, g, S);
+      keep<IO, RT>(record + kept.state(0), p.rp, p.cp, cw + li, g, S);
 
     __builtin_amdgcn_s_setprio(3);
     // ---- what the state before the chunk gives: X = K S (rows are tokens, by state_row), O = Q S (transposed).  The
@@ -1030,7 +988,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (MODE == kDeltaStates)
-      keep<IO, IB>(record + kept.rows(0), record + kept.by(2), C, p.cp, cw + li, g, X);
+      keep<IO, IB>(record + kept.rows(0), C, p.cp, cw + li, g, X);
 
     __builtin_amdgcn_s_setprio(1);
     // ---- u = b r as an operand of o, e^{G_C - G} u as one of the state's update
@@ -1221,9 +1179,8 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
       // as many stores behind the first loads as the loop has behind its own (see keep)
       const f32x4 none[RT > IB ? RT : IB] = {};
       const int li = tid & 15, g = (tid & 63) >> 4;
-      keep<IO, RT>(p.kept, p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
-      if constexpr (PP == 2) keep_factor(p.kept, 0, p.cp, cw + li, g, 1.f);
-      keep<IO, IB>(p.kept, p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
+      keep<IO, RT>(p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[RT]>(none));
+      keep<IO, IB>(p.kept, 0, p.cp, cw + li, g, reinterpret_cast<const f32x4(&)[IB]>(none));
     }
   }
   for (int kk = 0; kk < nc; ++kk) {
@@ -1243,7 +1200,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     const float end_dec = ek[C - 1];
     const int lane = opaque(tid) & 63, g = lane >> 4, li = lane & 15;
     if (kk + 1 < nc) load_chunk(pc - 1);
-    if constexpr (!SEG) keep<IO, RT>(record + kept.state(1), record + kept.by(1), p.rp, p.cp, cw + li, g, R);
+    if constexpr (!SEG) keep<IO, RT>(record + kept.state(1), p.rp, p.cp, cw + li, g, R);
 
     // ---- X = K R (rows are tokens); the operands of step s + 1 are read and split under the matrix instructions of step s
     constexpr int LOW = IB == 2 ? 3 : 6;  // operand steps on and below the diagonal
@@ -1307,7 +1264,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     if constexpr (PP == 2) read_square(tp + C * C * ES, fl);
     __builtin_amdgcn_sched_barrier(0);
     auto half = [](const uint4& a, const uint4& b, f32x4 acc) { return Halves::mma(a, b, acc); };
-    float yb = 1.f, ob = 1.f;
+    float yb = 1.f;
     if constexpr (PP == 2) {
       // dO as float16 over a power of two: exact but for what is below 2^-32 of the column's largest
       uint4 fo[JS];
@@ -1322,7 +1279,6 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
       yb = h.back * rt[kBy * C + 1];
 #pragma unroll
       for (int js = 0; js < JS; ++js) fo[js] = Halves::one(d[js], h.to);
-      if constexpr (!SEG) ob = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, Halves(wave_max(most)).back)));
       times_square(ft, fo, Y, half);
       times_square(fl, fo, Y, half);
     } else {
@@ -1406,8 +1362,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
       __builtin_amdgcn_sched_barrier(0);
     }
     if (kk + 1 < nc) load_late(pc - 1);
-    if constexpr (!SEG) keep<IO, IB>(record + kept.rows(1), record + kept.by(3), C, p.cp, cw + li, g, X);
-    if constexpr (!SEG && PP == 2) keep_factor(record + kept.by(4), 1, p.cp, cw + li, g, ob);
+    if constexpr (!SEG) keep<IO, IB>(record + kept.rows(1), C, p.cp, cw + li, g, X);
 
     const int yb0 = state_col_base<IO, NK>(li, g);
 #pragma unroll
@@ -1465,12 +1420,16 @@ struct DeltaGradDev {
 };
 
 // The scores' gradients take the place of the slab once it is done with.
-template <typename IO, int ROWS, int NW>
+// The sums over the heads of a key head lie in LDS where the registers do not hold them and it has room.
+template <typename IO, int ROWS, bool MULTI>
+constexpr bool sums_in_lds() { return MULTI && ROWS == 128 && HeadCfg<IO>::ES == 2; }
+template <typename IO, int ROWS, int NW, bool MULTI>
 constexpr size_t grad_lds_bytes() {
   using K = HeadCfg<IO>;
-  constexpr size_t slab = size_t(K::C) * kSlab * K::ES * 3;
+  constexpr size_t slab = size_t(K::C) * kSlab * K::ES * (1 + 2 * DeltaCfg<IO>::PAIR);
   constexpr size_t sc = size_t(2) * K::C * K::C * K::ES * DeltaCfg<IO>::PAIR;
-  return 2 * size_t(K::C) * ROWS * K::ES + (slab > sc ? slab : sc) + (size_t(2) * NW + kRates + 1) * K::C * 4 + NW * 4;
+  constexpr size_t sums = sums_in_lds<IO, ROWS, MULTI>() ? 2 * size_t(K::C) * ROWS * 4 : 0;
+  return 2 * size_t(K::C) * ROWS * K::ES + (slab > sc ? slab : sc) + (size_t(2) * NW + kRates + 1) * K::C * 4 + NW * 4 + sums;
 }
 
 // Running sum from the last lane as a pair of floats (scan_pair's, the other way round)
@@ -1501,16 +1460,16 @@ __device__ __forceinline__ void scan_back(float& hi, float& lo) {
 // last two), each without a token's own pair scale (q . k)(do . u), which is in both and cancels.  Where the state
 // starts anew (a decay of -inf) dg is zero and the sum of the tokens before begins there.
 //
-// In bfloat16 the states, r and e are operands as they are kept, float16 over powers of two, brought to the largest of a
-// chunk's (the products of several columns add up), and dO beside them: 260 us, in two bfloat16 parts each 321 (4 x 2048
-// tokens, 32 heads of 128 x 128 on 16 key heads, which is 2.6 TB/s).  A workgroup a CU, so that nothing covers what it
-// waits for at its start (68 us of these) and between its barriers; loads are two steps of states and a slab ahead.
+// In bfloat16 the states, r and e are two bfloat16 parts each, off by 2^-17 at most: dg cancels, and with one part of float16
+// (261 us for 330, 4 x 2048 tokens, 32 heads of 128 x 128 on 16 key heads) its error is twice its own rounding.  <R_C, S_0>
+// is of the float32 values.  A workgroup a CU, so that nothing covers what it waits for at its start and between its
+// barriers; 3.0 TB/s.  Loads are one or two steps of states and, where the registers hold it, a slab ahead.
 //
-// MULTI adds up the d.hn heads of a key head in the workgroup: 4 x 2048 tokens, 32 heads of 128 x 128 on 8 key heads,
-// bfloat16, 558 us for the whole backward, 641 with key heads of their own (more loads and stores of keys' gradients).
-// A workgroup is on its CU alone in bfloat16 (its registers), two or three in float32 with one head, where that many fit
-// with few spills (4 x 2048 tokens, 32 heads of 64 x 64: the backward 490 us, with the registers of two 516; bfloat16
-// 304 with two, 422 with three).
+// MULTI adds up the heads of a key head in the workgroup: 4 x 2048 tokens, 32 heads of 128 x 128 on 8 key heads, bfloat16,
+// 629 us for the whole backward, 691 with key heads of their own (more loads and stores of keys' gradients).  The next
+// slab's loads then go out behind the products (64 keys: 304 us, ahead of them, with 42 spilled registers, 347).
+// A workgroup is on its CU alone in bfloat16 past 64 keys (its registers), two or three in float32 with one head (4 x 2048
+// tokens, 32 heads of 64 x 64: the backward 462 us; bfloat16 308 with two).
 template <typename IO, int ROWS, int NW, bool MULTI>
 constexpr int grad_waves() { return HeadCfg<IO>::ES == 4 && !MULTI ? (ROWS == 128 ? 4 : ROWS == 64 ? 3 : 2) : 2; }
 
@@ -1522,8 +1481,11 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
   constexpr int NK = ROWS * ES / 16, NS = kSlab * ES / 16, NP = C * ES / 16;
   constexpr int IB = C / 16, JS = C / KS, SS = kSlab / KS, CT = ROWS / 16 / NW;
   constexpr int PP = DeltaCfg<IO>::PAIR, SB = C * kSlab * ES, PB = C * C * ES, GAP = KS == 32 ? IB / 2 : 0;  // tiles above the diagonal that a product step covers
-  constexpr bool HALF = ES == 2;
   constexpr int TILES = IB * (IB + 1) / 2, MINE = (2 * TILES + NW - 1) / NW;
+  // loads of states under way, and operands of blocks and of scores read ahead: two where the registers hold them
+  constexpr int AHEAD = PP == 1 || (!MULTI && ROWS <= 128) ? 2 : 1, NB = AHEAD, NT = AHEAD;
+  constexpr bool LATE = MULTI && PP == 2;  // the next slab's loads behind the products, for their registers
+  constexpr bool SUMS = sums_in_lds<IO, ROWS, MULTI>();
   constexpr int TASKS = C * NS / T;  // staging tasks a thread, rows tid / NS + i T / NS
   static_assert(C * NS % T == 0 && CT >= 1 && SS % 2 == 0, "shares are even");
   using TK = Tile<IO, NK, T>;
@@ -1534,10 +1496,10 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
   char* const ty = tx + C * ROWS * ES;
   char* const tdo = ty + C * ROWS * ES;  // dO, b r, b e of kSlab columns
   char* const tu = tdo + SB;
-  char* const te = tu + SB;
+  char* const te = tu + PP * SB;
   char* const tp = tdo;                  // in their place dP, then dN
   char* const tn = tp + PP * PB;
-  float* const rt = reinterpret_cast<float*>(tdo + (3 * SB > 2 * PP * PB ? 3 * SB : 2 * PP * PB));  // [kRates][C]
+  float* const rt = reinterpret_cast<float*>(tdo + ((1 + 2 * PP) * SB > 2 * PP * PB ? (1 + 2 * PP) * SB : 2 * PP * PB));  // [kRates][C]
   const float* const ghi = rt + kGHi * C;
   const float* const glo = rt + kGLo * C;
   const float* const ek = rt + kEk * C;
@@ -1548,10 +1510,12 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
   float* const red = own + C;       // [NW][C]
   float* const redc = red + NW * C;
   float* const rs = redc + NW * C;  // [NW]
+  f32x4* const sums = reinterpret_cast<f32x4*>(rs + NW) + threadIdx.x;  // [CT][IB][2][T]: the thread's DQ and DK
 
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, li = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int groups = p.H / d.hn;
+  const int heads = MULTI ? d.hn : 1;  // of a key head that the workgroup adds up
+  const int groups = p.H / heads;
   const int pc = blockIdx.x % p.nch, bg = blockIdx.x / p.nch, hg = bg % groups, b = bg / groups, t0 = pc * C;
   const int len = length_of(p, b);
   const int oes = d.parts ? 4 : ES;
@@ -1559,97 +1523,72 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
   const int64_t row0 = static_cast<int64_t>(b) * p.L + t0;
 
   // the head's, and the sums over the heads that share a key head (one head: none)
-  f32x4 dq[CT][IB], ur[CT][IB], DQ[MULTI ? CT : 1][IB], DK[MULTI ? CT : 1][IB];
+  f32x4 dq[CT][IB], ur[CT][IB], DQ[MULTI && !SUMS ? CT : 1][IB], DK[MULTI && !SUMS ? CT : 1][IB];
 #pragma unroll
   for (int c = 0; c < CT; ++c)
 #pragma unroll
     for (int i = 0; i < IB; ++i) {
       dq[c][i] = ur[c][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (MULTI) DQ[c][i] = DK[c][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (SUMS) sums[2 * (c * IB + i) * T] = sums[(2 * (c * IB + i) + 1) * T] = f32x4{0.f, 0.f, 0.f, 0.f};
+      else if (MULTI) DQ[c][i] = DK[c][i] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
   if (t0 < len) {
-    constexpr int KB = kept_size<IO>();
-    const int hk = hg * d.hn / p.rep, nslab = p.cp / kSlab;
+    constexpr int KW = E / 4;  // 16-byte loads for the E kept values of an operand
+    const int hk = hg * heads / p.rep, nslab = p.cp / kSlab;
     const Kept<IO> kept(p.rp, p.cp);
-    const int64_t chunk0 = (static_cast<int64_t>(b) * p.H + hg * d.hn) * p.nch + pc;  // of head hh: hh nch further
+    const int64_t chunk0 = (static_cast<int64_t>(b) * p.H + hg * heads) * p.nch + pc;  // of head hh: hh nch further
     // What a thread has in flight: its part of a slab's dO, r and e, and the operands S_0 and R_C of its wavefront for
     // the next two steps.
-    uint4 go[TASKS], gr[TASKS], ge[TASKS], s0[2][CT], r1[2][CT], rr[TR::CNT];
-    float gr_by[TASKS], ge_by[TASKS], s0_by[2], r1_by[2], most[5] = {};
+    uint4 go[TASKS], gr[TASKS][KW], ge[TASKS][KW], s0[AHEAD][CT][KW], r1[AHEAD][CT][KW], rr[TR::CNT];
     auto record = [&](int hh) {
       return make_rsrc(p.kept + (chunk0 + static_cast<int64_t>(hh) * p.nch) * kept.bytes(), kept.bytes());
     };
-    auto values_at = [](Rsrc r, uint32_t off, uint32_t part) {
-      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off, part, 0);
-      return make_uint4(v.x, v.y, v.z, v.w);
-    };
-    auto factor_at = [](Rsrc r, uint32_t off, uint32_t part) {
-      return __uint_as_float(HALF ? __builtin_amdgcn_raw_buffer_load_b32(r, off, part, 0) : 0x3f800000u);
+    auto values_at = [](Rsrc r, uint32_t off, uint32_t part, uint4* to) {
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, off + 16 * i, part, 0);
+        to[i] = make_uint4(v.x, v.y, v.z, v.w);
+      }
     };
     auto load_slab = [&](Rsrc rec, int hh, int v0) {
-      const Rsrc rdo = make_rsrc(p.v + b * p.v_b + static_cast<int64_t>(t0) * p.v_t + static_cast<int64_t>(hg * d.hn + hh) * p.cols * ES,
+      const Rsrc rdo = make_rsrc(p.v + b * p.v_b + static_cast<int64_t>(t0) * p.v_t + static_cast<int64_t>(hg * heads + hh) * p.cols * ES,
                                  row_bytes(len - t0, C, p.v_t));
 #pragma unroll
       for (int i = 0; i < TASKS; ++i) {
         const int me = opaque(tid), r = me / NS + i * (T / NS), col = v0 + me % NS * E;
         go[i] = load16<IO, VEC>(rdo, r * p.v_t + col * ES, p.cols - col);
-        gr[i] = values_at(rec, (r * p.cp + col) * KB, kept.rows(0));
-        ge[i] = values_at(rec, (r * p.cp + col) * KB, kept.rows(1));
-        gr_by[i] = factor_at(rec, col / 16 * 4, kept.by(2));
-        ge_by[i] = factor_at(rec, col / 16 * 4, kept.by(3));
+        values_at(rec, (r * p.cp + col) * 4, kept.rows(0), gr[i]);
+        values_at(rec, (r * p.cp + col) * 4, kept.rows(1), ge[i]);
       }
     };
-    // a head's factors, those of 16 columns a lane
-    auto load_factors = [&](int hh) {
-      const Rsrc rec = record(hh);
-      const uint32_t off = 16 * lane < p.cp ? 4 * lane : kOOB;
-#pragma unroll
-      for (int i = 0; i < 5; ++i) most[i] = factor_at(rec, off, kept.by(i));
-    };
-    // step n of a head
-    auto load_states = [&](Rsrc rec, int n, int to) {
-      const int me = opaque(lane), col = KS * n + E * (me >> 4);
-#pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        const int row = (wave * CT + c) * 16;
-        const uint32_t off = row < p.rp ? static_cast<uint32_t>((row + (me & 15)) * p.cp + col) * KB : kOOB;
-        s0[to][c] = values_at(rec, off, kept.state(0));
-        r1[to][c] = values_at(rec, off, kept.state(1));
-      }
-      s0_by[to] = factor_at(rec, col / 16 * 4, kept.by(0));
-      r1_by[to] = factor_at(rec, col / 16 * 4, kept.by(1));
+    // rows' block c of step n of a head
+    auto load_states = [&](Rsrc rec, int n, int to, int c) {
+      const int me = opaque(lane), col = KS * n + E * (me >> 4), row = (wave * CT + c) * 16;
+      const uint32_t off = row < p.rp ? static_cast<uint32_t>((row + (me & 15)) * p.cp + col) * 4 : kOOB;
+      values_at(rec, off, kept.state(0), s0[to][c]);
+      values_at(rec, off, kept.state(1), r1[to][c]);
     };
     {
       uint4 rx[TK::CNT], ry[TK::CNT];
       TK::template load<VEC>(p.q + b * p.q_b + static_cast<int64_t>(hk) * p.rows * ES, p.q_t, t0, len, p.rows, tid, rx);
       TK::template load<VEC>(p.k + b * p.k_b + static_cast<int64_t>(hk) * p.rows * ES, p.k_t, t0, len, p.rows, tid, ry);
       TR::load(reinterpret_cast<const char*>(p.rates + chunk0 * kRates * C), tid, rr);
-      if constexpr (HALF) load_factors(0);
       load_slab(record(0), 0, 0);
-      load_states(record(0), 0, 0);
-      load_states(record(0), 1, 1);
+#pragma unroll
+      for (int n = 0; n < AHEAD; ++n)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) load_states(record(0), n, n, c);
       TK::store(tx, tid, rx);
       TK::store(ty, tid, ry);
     }
-    for (int hh = 0; hh < d.hn; ++hh) {
-      const int h = hg * d.hn + hh;
+    for (int hh = 0; hh < heads; ++hh) {
+      const int h = hg * heads + hh;
       __syncthreads();  // the head before is done with the rates
       TR::store(reinterpret_cast<char*>(rt), tid, rr);
       __syncthreads();
-      if (hh + 1 < d.hn) TR::load(reinterpret_cast<const char*>(p.rates + (chunk0 + (hh + 1) * static_cast<int64_t>(p.nch)) * kRates * C), tid, rr);
+      if (hh + 1 < heads) TR::load(reinterpret_cast<const char*>(p.rates + (chunk0 + (hh + 1) * static_cast<int64_t>(p.nch)) * kRates * C), tid, rr);
 
-      // float16 operands: over the largest of all columns' powers of two, b's at least 1
-      float sb = 1.f, rb = 1.f, ub = 1.f, eb = 1.f, ob = 1.f, si = 1.f, ri = 1.f, ui = 1.f, ei = 1.f, oi = 1.f;
-      if constexpr (HALF) {
-        auto inverse = [](float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); };
-        const float bm = wave_max(__builtin_fabsf(lane < C ? bt[lane] : 0.f));
-        const float bb = __uint_as_float(bm < 1.f ? 127u << 23 : (__float_as_uint(bm) & 0x7f800000u) + (1u << 23));
-        sb = wave_max(most[0]); rb = wave_max(most[1]); ub = wave_max(most[2]) * bb; eb = wave_max(most[3]) * bb;
-        ob = wave_max(most[4]);
-        si = inverse(sb); ri = inverse(rb); ui = inverse(ub); ei = inverse(eb); oi = inverse(ob);
-        if (hh + 1 < d.hn) load_factors(hh + 1);
-      }
       f32x4 vs[CT][IB], sc[MINE];
 #pragma unroll
       for (int c = 0; c < CT; ++c)
@@ -1662,6 +1601,9 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
       for (int v = 0; v < nslab; ++v) {
         const int v0 = v * kSlab;
         if (v > 0) __syncthreads();  // the slab before is done with
+        auto floats = [](const uint4* r, float* v) {
+          for (int i = 0; i < E; ++i) v[i] = reinterpret_cast<const float*>(r)[i];
+        };
         // ---- dO, b r and b e of 64 columns, as parts; dv and the sums of db on the way
         const Rsrc rdv = make_rsrc(d.dv + row0 * vts + static_cast<int64_t>(h) * p.cols * ES, row_bytes(p.L - t0, C, vts));
 #pragma unroll
@@ -1669,8 +1611,8 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
           const int me = opaque(tid), r = me / NS + i * (T / NS), c = me % NS, col = v0 + c * E;
           const float bb = bt[r];
           float x[E], y[E];
-          widen<IO>(gr[i], gr_by[i], x);
-          widen<IO>(ge[i], ge_by[i], y);
+          floats(gr[i], x);
+          floats(ge[i], y);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             dot_b[i] = __builtin_fmaf(x[e], y[e], dot_b[i]);
@@ -1685,84 +1627,92 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
             for (int e = 0; e < E; ++e) BufOf<IO>::type::template st<1>(rdv, col + e < p.cols ? off + e * ES : kOOB, y + e);
           }
           const int to = 16 * (NS * r + (c ^ swz<IO, NS>(r)));
-          if constexpr (HALF) {
-            *reinterpret_cast<uint4*>(tu + to) = Halves::one(x, ui);
-            *reinterpret_cast<uint4*>(te + to) = Halves::one(y, ei);
-            unpack<IO>(go[i], x);
-            *reinterpret_cast<uint4*>(tdo + to) = Halves::one(x, oi);
-          } else {
-            *reinterpret_cast<uint4*>(tdo + to) = go[i];
-            *reinterpret_cast<float4*>(tu + to) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4*>(te + to) = make_float4(y[0], y[1], y[2], y[3]);
-          }
+          uint4 w[PP];
+          *reinterpret_cast<uint4*>(tdo + to) = go[i];
+          split<IO, PP>(x, w);
+#pragma unroll
+          for (int q = 0; q < PP; ++q) *reinterpret_cast<uint4*>(tu + q * SB + to) = w[q];
+          split<IO, PP>(y, w);
+#pragma unroll
+          for (int q = 0; q < PP; ++q) *reinterpret_cast<uint4*>(te + q * SB + to) = w[q];
         }
         __syncthreads();
         // the next slab is this head's or the next one's
-        const bool more = v + 1 < nslab, any = more || hh + 1 < d.hn;
+        const bool more = v + 1 < nslab, any = more || hh + 1 < heads;
         const int hn = more ? hh : hh + 1, vn = more ? v + 1 : 0;
         const Rsrc rec = record(hn);
-        if (any) load_slab(rec, hn, vn * kSlab);
+        if (!LATE && any) load_slab(rec, hn, vn * kSlab);
         const int fb = opaque(lane_base<IO, NS>(li, g));
 #pragma unroll
         for (int s = 0; s < SS; ++s) {
-          uint4 fs[CT], fr[CT];
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            fs[c] = s0[s & 1][c];
-            fr[c] = r1[s & 1][c];
-            if constexpr (HALF) {
-              const _Float16 x = static_cast<_Float16>(s0_by[s & 1] * si), y = static_cast<_Float16>(r1_by[s & 1] * ri);
-              fs[c] = __builtin_bit_cast(uint4, __builtin_bit_cast(half8, fs[c]) * x);
-              fr[c] = __builtin_bit_cast(uint4, __builtin_bit_cast(half8, fr[c]) * y);
-            }
-            float x[E], y[E];
-            widen<IO>(fs[c], 1.f, x);
-            widen<IO>(fr[c], 1.f, y);
-#pragma unroll
-            for (int e = 0; e < E; ++e) dot_rs = __builtin_fmaf(x[e], y[e], dot_rs);
-          }
-          if (s + 2 < SS) load_states(record(hh), v * SS + s + 2, s & 1);
-          else if (any) load_states(rec, vn * SS + s + 2 - SS, s & 1);
-          auto add = [](const uint4& a, const uint4& b, f32x4 acc) {
-            if constexpr (HALF) return Halves::mma(a, b, acc);
-            else return mma<IO>(a, b, acc);
-          };
           // the next block's operands are read before the present one's products
-          uint4 fo[2], fu[2], fe[2], fx[MINE], fy[MINE];
+          uint4 fo[NB], fu[NB][PP], fe[NB][PP], fx[NT][PP], fy[NT][PP];
           auto read = [&](int ib) {
-            fo[ib & 1] = frag_row<NS>(tdo, fb, ib, s);
-            fu[ib & 1] = frag_row<NS>(tu, fb, ib, s);
-            fe[ib & 1] = frag_row<NS>(te, fb, ib, s);
+            fo[ib % NB] = frag_row<NS>(tdo, fb, ib, s);
+#pragma unroll
+            for (int q = 0; q < PP; ++q) {
+              fu[ib % NB][q] = frag_row<NS>(tu + q * SB, fb, ib, s);
+              fe[ib % NB][q] = frag_row<NS>(te + q * SB, fb, ib, s);
+            }
           };
-          // tiles of dP, then of dN, dealt to the wavefronts: lane holds j = 4 g + v of i = li
+          // tiles of dP, then of dN, dealt to the wavefronts: lane holds j = 4 g + v of i = li.  dO is one part: its second
+          // is b e's, which is not multiplied.
           auto read_scores = [&](int m) {
             const int job = wave + m * NW < 2 * TILES ? wave + m * NW : 0;
             int ib, jb;
             score_tile<IB>(job < TILES ? job : job - TILES, ib, jb);
-            fx[m] = frag_row<NS>(tu, fb, jb, s);
-            fy[m] = frag_row<NS>(job < TILES ? tdo : te, fb, ib, s);
+#pragma unroll
+            for (int q = 0; q < PP; ++q) {
+              fx[m % NT][q] = frag_row<NS>(tu + q * SB, fb, jb, s);
+              fy[m % NT][q] = frag_row<NS>(job < TILES && q == 0 ? tdo : te + q * SB, fb, ib, s);
+            }
           };
-          read(0);
 #pragma unroll
-          for (int ib = 0; ib < IB; ++ib) {
-            if (ib + 1 < IB) {
-              read(ib + 1);
-            } else {
+          for (int c = 0; c < CT; ++c) {
+            uint4 fs[PP], fr[PP];
+            {
+              float x[E], y[E];
+              floats(s0[s % AHEAD][c], x);
+              floats(r1[s % AHEAD][c], y);
 #pragma unroll
-              for (int m = 0; m < MINE; ++m) read_scores(m);
+              for (int e = 0; e < E; ++e) dot_rs = __builtin_fmaf(x[e], y[e], dot_rs);
+              split<IO, PP>(x, fs);
+              split<IO, PP>(y, fr);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            if (s + AHEAD < SS) load_states(record(hh), v * SS + s + AHEAD, s % AHEAD, c);
+            else if (any) load_states(rec, vn * SS + s + AHEAD - SS, s % AHEAD, c);
+            if (NB == 2) read(0);
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-              dq[c][ib] = add(fs[c], fo[ib & 1], dq[c][ib]);
-              ur[c][ib] = add(fr[c], fu[ib & 1], ur[c][ib]);
-              vs[c][ib] = add(fs[c], fe[ib & 1], vs[c][ib]);
+            for (int ib = 0; ib < IB; ++ib) {
+              if (NB == 1) read(ib);
+              else if (ib + 1 < IB) read(ib + 1);
+              if (c + 1 == CT && ib + 1 == IB && NT == 2) read_scores(0);
+              __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+              for (int q = 0; q < PP; ++q) {
+                dq[c][ib] = mma<IO>(fs[q], fo[ib % NB], dq[c][ib]);
+                ur[c][ib] = mma<IO>(fr[q], fu[ib % NB][0], ur[c][ib]);
+                vs[c][ib] = mma<IO>(fs[q], fe[ib % NB][0], vs[c][ib]);
+                if (q > 0) {
+                  ur[c][ib] = mma<IO>(fr[0], fu[ib % NB][q], ur[c][ib]);
+                  vs[c][ib] = mma<IO>(fs[0], fe[ib % NB][q], vs[c][ib]);
+                }
+              }
+              __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
           }
 #pragma unroll
-          for (int m = 0; m < MINE; ++m) sc[m] = add(fx[m], fy[m], sc[m]);
+          for (int m = 0; m < MINE; ++m) {
+            if (NT == 1) read_scores(m);
+            else if (m + 1 < MINE) read_scores(m + 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int q = 0; q < PP; ++q) sc[m] = mma<IO>(fx[m % NT][q], fy[m % NT][0], sc[m]);
+            if (PP == 2 && wave + m * NW >= TILES) sc[m] = mma<IO>(fx[m % NT][0], fy[m % NT][PP - 1], sc[m]);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
+        if (LATE && any) load_slab(rec, hn, vn * kSlab);
       }
 
       // ---- the scores' gradients to LDS, below the diagonal, and zeros in the tiles above it that a product step covers
@@ -1782,7 +1732,7 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
         int ib, jb;
         score_tile<IB>(job < TILES ? job : job - TILES, ib, jb);
         const int me = opaque(lane), g = me >> 4, i = 16 * ib + (me & 15), j0 = 16 * jb + 4 * g;
-        const float by = (job < TILES ? p.scale * ob : -eb) * ub;
+        const float by = job < TILES ? p.scale : -1.f;
         float w[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -1804,7 +1754,7 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
       // <R_C, S_0> of the wavefront
 #pragma unroll
       for (int x = 1; x < 64; x *= 2) dot_rs += __shfl_xor(dot_rs, x);
-      if (lane == 0) rs[wave] = dot_rs * sb * rb;
+      if (lane == 0) rs[wave] = dot_rs;
       // db: the NS lanes of a row
       if (d.db != nullptr) {
 #pragma unroll
@@ -1831,9 +1781,9 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
         float dot = 0.f;
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-          scale(dq[c][ib], p.scale * fe * (sb * ob));
-          scale(vs[c][ib], -fe * (sb * eb));
-          scale(ur[c][ib], fw * (rb * ub));
+          scale(dq[c][ib], p.scale * fe);
+          scale(vs[c][ib], -fe);
+          scale(ur[c][ib], fw);
           float kv[4];
           values(ty, c, ib, kv);
 #pragma unroll
@@ -1898,10 +1848,14 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
             dot = __builtin_fmaf(kv[v], vs[c][ib][v] - ur[c][ib][v], dot);
             dq[c][ib][v] = __builtin_fmaf(o, kv[v], dq[c][ib][v]);
             ur[c][ib][v] = __builtin_fmaf(o, qv[v], ur[c][ib][v] + vs[c][ib][v]);
-            if (MULTI) {
+            if (MULTI && !SUMS) {
               DQ[c][ib][v] += dq[c][ib][v];
               DK[c][ib][v] += ur[c][ib][v];
             }
+          }
+          if (SUMS) {
+            sums[2 * (c * IB + ib) * T] += dq[c][ib];
+            sums[(2 * (c * IB + ib) + 1) * T] += ur[c][ib];
           }
         }
         dot += __shfl_xor(dot, 16);
@@ -1954,8 +1908,8 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
   } else {
     // nothing of the chunk exists
     for (int r = wave; r < C && t0 + r < p.L; r += NW) {
-      for (int hh = 0; hh < d.hn; ++hh) {
-        const int64_t at = (row0 + r) * p.H + hg * d.hn + hh;
+      for (int hh = 0; hh < heads; ++hh) {
+        const int64_t at = (row0 + r) * p.H + hg * heads + hh;
         const float z = 0.f;
         for (int c = lane; c < p.cols; c += 64) IO::template st<1>(reinterpret_cast<typename IO::T*>(d.dv) + at * p.cols + c, &z);
         if (lane == 0 && d.dg != nullptr) IO::template st<1>(reinterpret_cast<typename IO::T*>(d.dg) + at, &z);
@@ -1975,7 +1929,9 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
     for (int c = 0; c < CT; ++c) {
       const int col = 16 * (wave * CT + c) + 4 * g;
       const uint32_t off = li * ots + col * oes;
-      const f32x4 xq = MULTI ? DQ[MULTI ? c : 0][ib] : dq[c][ib], xk = MULTI ? DK[MULTI ? c : 0][ib] : ur[c][ib];
+      constexpr bool IN = MULTI && !SUMS;
+      const f32x4 xq = SUMS ? sums[2 * (c * IB + ib) * T] : IN ? DQ[IN ? c : 0][ib] : dq[c][ib];
+      const f32x4 xk = SUMS ? sums[(2 * (c * IB + ib) + 1) * T] : IN ? DK[IN ? c : 0][ib] : ur[c][ib];
       const float vq[4] = {xq[0], xq[1], xq[2], xq[3]}, vk[4] = {xk[0], xk[1], xk[2], xk[3]};
       if (VEC && !d.parts) {
         BufOf<IO>::type::template st<4>(rq, col < p.rows ? off : kOOB, vq);
@@ -2062,7 +2018,7 @@ hipError_t launch_both_t(const DeltaDev& p, const DeltaDev& r, hipStream_t st) {
 template <typename IO, int ROWS, int NW, bool MULTI, bool VEC>
 hipError_t launch_grad_t(const DeltaGradDev& d, hipStream_t st) {
   static std::atomic<uint64_t> allowed{0};
-  constexpr size_t smem = grad_lds_bytes<IO, ROWS, NW>();
+  constexpr size_t smem = grad_lds_bytes<IO, ROWS, NW, MULTI>();
   auto kern = ssm_delta_grad_kernel<IO, ROWS, NW, MULTI, VEC>;
   if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
   const int64_t wgs = static_cast<int64_t>(d.f.batch) * (d.f.H / d.hn) * d.f.nch;
