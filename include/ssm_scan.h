@@ -502,11 +502,10 @@ int ssm_head_step(const void *q, const void *k, const void *v, const void *g, co
  *          bytes, the caller's; calls that may run at the same time need one each.
  * All other arguments, limits and errors as ssm_head_scan_fwd (no g_head: a fixed
  * decay is expanded to g).
- * Rounding: sums, decays, r and the state are float32.  With SSM_BF16 the state
- * and what is added to it enter products as three parts of bfloat16 (all of a
- * float32), the corrections among a chunk's tokens as two of float16 over a power
- * of two for each column (off by 2^-22 of themselves, or 2^-39 of the chunk's
- * largest in that column), and what ends in o as two of bfloat16 (2^-17).
+ * Rounding: sums, decays, r and the state are float32.  With SSM_BF16 the state,
+ * what is added to it and the corrections among a chunk's tokens enter products
+ * as three parts of bfloat16 (all of a float32), and what ends in o as two
+ * (2^-17).
  * Values that are not finite reach every later result of their head in their
  * batch row, and those of their chunk (64 tokens from a multiple of 64, float32:
  * 32) before them, until the state starts anew at a chunk's first token (a decay

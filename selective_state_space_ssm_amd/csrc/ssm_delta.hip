@@ -286,9 +286,10 @@ bool all_vec(const DeltaArgs& a, bool bf16) {
          vec16(a.v, a.v_b, a.v_t, es);
 }
 
-// M or P of every chunk
-int64_t square_bytes(const DeltaArgs& a, const Plan& pl, bool bf16) {
-  return a.batch * a.H * pl.nch * (bf16 ? deltak::Square<BF16>::BYTES : deltak::Square<F32>::BYTES);
+// M (and, backwards, P) of every chunk, or forwards P
+int64_t square_bytes(const DeltaArgs& a, const Plan& pl, bool bf16, bool query) {
+  using deltak::Square;
+  return a.batch * a.H * pl.nch * (bf16 ? (query ? Square<BF16, 2>::BYTES : Square<BF16, 3>::BYTES) : Square<F32, 1>::BYTES);
 }
 
 // Heads whose parts of dq and dk a workgroup adds: all that share a key head, unless that leaves CUs idle (4 x 2048
@@ -318,8 +319,8 @@ Space space_of(const DeltaArgs& a, const Plan& pl, bool bf16, bool backward) {
     return r;
   };
   const int64_t bh = a.batch * a.H;
-  w.m = take(square_bytes(a, pl, bf16));
-  w.s = take(square_bytes(a, pl, bf16));
+  w.m = take(square_bytes(a, pl, bf16, false));
+  w.s = take(square_bytes(a, pl, bf16, !backward));
   w.rates = take(bh * pl.nch * pl.C * deltak::kRates * 4);
   if (pl.nseg > 1) {
     w.ss = take(4 * bh * pl.nseg * pl.rp * pl.cp);

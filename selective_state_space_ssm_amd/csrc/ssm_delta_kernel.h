@@ -67,7 +67,7 @@ struct DeltaDev {
   const int32_t* lengths;      // [b], nullable
   const float* h0;             // state at the first token (backwards: after the last), nullable
   float* last;                 // state after the last token (backwards: at the first), nullable
-  char* m;                     // -M of every chunk, [b][H][nch][parts][C][C]
+  char* m;                     // -M of every chunk, [b][H][nch] (see Square)
   char* s;                     // P of every chunk, as m
   float* rates;                // [b][H][nch][kRates][C]
   float* seg_state;            // [b][H][nseg][rp][cp]
@@ -82,83 +82,19 @@ struct DeltaDev {
   float scale;
 };
 
-// Parts that a float32 value enters a product in (bfloat16 storage): the state
-// and what is added to it in three, which is exact to float32; what ends in a
-// bfloat16 result in two (2^-17 of themselves).  M (b x), where both are such
-// values, is made of float16 parts instead, two of each over powers of two (see
-// Halves): exact to 2^-22 with three products of the four, where two bfloat16
-// parts of M leave the state off by 2^-18 of what the chunk's tokens give each
-// other (1114 tokens, keys of 16: the last state 1.4e-6, so 1.5e-7), and a third part, six
-// products, does not fit LDS beside a second workgroup.
+// Parts that a float32 value enters a product in (bfloat16 storage): the state,
+// what is added to it and the corrections among a chunk's tokens in three, which
+// is exact to float32 at any size; what ends in a bfloat16 result in two (2^-17
+// of themselves).  Of the nine products of M's parts with (b x)'s the six of
+// 2^-16 and more are made.  (Two parts of each leave the last state off by 1.4e-6
+// after 1114 tokens with keys of 16, three by 1.3e-7.  Two of float16 over a power
+// of two do not, with half the products, but lose what is 2^-39 of the largest
+// among the 64 tokens.)
 template <typename IO>
 struct DeltaCfg {
   static constexpr int STATE = HeadCfg<IO>::ES == 2 ? 3 : 1;
   static constexpr int PAIR = HeadCfg<IO>::ES == 2 ? 2 : 1;
 };
-
-// Float32 values as two float16 parts over a power of two that takes the largest of them to 2^14 .. 2^15: the parts
-// together are off by 2^-24 of a value, or by 2^-39 of the largest.
-typedef _Float16 half2 __attribute__((ext_vector_type(2)));
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-struct Halves {
-  float to, back;  // the power of two and its inverse
-  // of values whose largest magnitude is m: its exponent, at least that whose factor back is no denormal
-  __device__ __forceinline__ explicit Halves(float m) {
-    uint32_t e = __float_as_uint(m) & 0x7f800000u;
-    e = e < 15u << 23 ? 15u << 23 : e;
-    to = __uint_as_float((268u << 23) - e);
-    back = __uint_as_float(e - (14u << 23));
-  }
-  // v (times the power of two) as parts
-  static __device__ __forceinline__ void split(const float* v, uint4* out) {
-    uint32_t* const hi = reinterpret_cast<uint32_t*>(&out[0]);
-    uint32_t* const lo = reinterpret_cast<uint32_t*>(&out[1]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const half2 h = {static_cast<_Float16>(v[2 * i]), static_cast<_Float16>(v[2 * i + 1])};
-      const half2 l = {static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h.x), -1.f, v[2 * i])),
-                       static_cast<_Float16>(__builtin_fmaf(static_cast<float>(h.y), -1.f, v[2 * i + 1]))};
-      hi[i] = __builtin_bit_cast(uint32_t, h);
-      lo[i] = __builtin_bit_cast(uint32_t, l);
-    }
-  }
-  // one part, for what is rounded no further (2^-11 of a value)
-  static __device__ __forceinline__ uint4 one(const float* v, float by) {
-    uint4 out;
-    uint32_t* const w = reinterpret_cast<uint32_t*>(&out);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const half2 h = {static_cast<_Float16>(v[2 * i] * by), static_cast<_Float16>(v[2 * i + 1] * by)};
-      w[i] = __builtin_bit_cast(uint32_t, h);
-    }
-    return out;
-  }
-  static __device__ __forceinline__ f32x4 mma(const uint4& a, const uint4& b, f32x4 acc) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), acc, 0, 0, 0);
-  }
-};
-// The largest of a column's values, one of an accumulator's: over the lanes li, li + 16, ..
-__device__ __forceinline__ float column_max(float m) {
-  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-  m = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  a = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-  return __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-}
-// The largest of a wavefront's values that are not negative, in every lane
-__device__ __forceinline__ float wave_max(float m) {
-  auto take = [&](auto ctrl, auto mask) {
-    constexpr int CTRL = decltype(ctrl)::value, ROWS = decltype(mask)::value;
-    m = __builtin_fmaxf(m, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m), CTRL, ROWS, 0xf, false)));
-  };
-  using std::integral_constant;
-  take(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // up within a row of 16, then over the rows
-  take(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
-  take(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
-  take(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
-  take(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});
-  take(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(m), 63));
-}
 
 // E values (one operand register of a lane) as N parts
 template <typename IO, int N>
@@ -283,24 +219,32 @@ struct Flat {
 };
 
 // A chunk's M or P in the workspace: of a [C][C] matrix the 16-byte chunks of the 16 x 16 blocks on and below the
-// diagonal, block row by block row (five eighths of it for 64 tokens), a part after the other.
-template <typename IO>
+// diagonal, block row by block row (five eighths of it for 64 tokens), a part after the other.  In LDS (bfloat16) the upper
+// half of the rows holds the left half of the columns only, which is what product steps of 32 read of them.
+template <typename IO, int PARTS>
 struct Square {
   using K = HeadCfg<IO>;
-  static constexpr int PER = 16 / K::E, IB = K::C / 16, CHUNKS = 8 * PER * IB * (IB + 1), PARTS = DeltaCfg<IO>::PAIR;
-  static constexpr int BYTES = 16 * CHUNKS * PARTS, LDS = PARTS * K::C * K::C * K::ES;
+  static constexpr bool HALVES = K::ES == 2;
+  static constexpr int PER = 16 / K::E, IB = K::C / 16, CHUNKS = 8 * PER * IB * (IB + 1), N = K::C / K::E;
+  static constexpr int TOP = HALVES ? K::C / 2 * (N / 2) * 16 : 0;  // bytes of the upper half
+  static constexpr int PART = HALVES ? TOP + K::C / 2 * N * 16 : K::C * N * 16;
+  static constexpr int BYTES = 16 * CHUNKS * PARTS, LDS = PARTS * PART;
   static __device__ __forceinline__ void place(int i, int& row, int& c) {
     const int rb = (i >= 16 * PER) + (IB > 2 && i >= 48 * PER) + (IB > 2 && i >= 96 * PER), at = i - 8 * PER * rb * (rb + 1);
     row = 16 * rb + at / (PER * (rb + 1));
     c = at % (PER * (rb + 1));
   }
+  static __device__ __forceinline__ int in_lds(int part, int row, int c) {
+    if (HALVES && row < K::C / 2) return part * PART + 16 * (N / 2 * row + (c ^ swz<IO, N / 2>(row)));
+    return part * PART + TOP + 16 * (N * (row - (HALVES ? K::C / 2 : 0)) + (c ^ swz<IO, N>(row)));
+  }
 };
 
-// The same dealt to T threads for LDS tiles of whole rows; where a thread's chunks go there is worked out once.
-template <typename IO, int T>
+// The same dealt to T threads for LDS tiles; where a thread's chunks go there is worked out once.
+template <typename IO, int T, int PARTS>
 struct TileM {
-  using S = Square<IO>;
-  static constexpr int N = HeadCfg<IO>::C / HeadCfg<IO>::E, CNT = (S::CHUNKS * S::PARTS + T - 1) / T;
+  using S = Square<IO, PARTS>;
+  static constexpr int CNT = (S::CHUNKS * PARTS + T - 1) / T;
   int to[CNT];
   __device__ __forceinline__ explicit TileM(int tid) {
 #pragma unroll
@@ -308,7 +252,7 @@ struct TileM {
       const int at = tid + i * T, part = at / S::CHUNKS;
       int row, c;
       S::place(at % S::CHUNKS, row, c);
-      to[i] = part < S::PARTS ? 16 * (N * (HeadCfg<IO>::C * part + row) + (c ^ swz<IO, N>(row))) : -1;
+      to[i] = part < PARTS ? S::in_lds(part, row, c) : -1;
     }
   }
   static __device__ __forceinline__ void load(const char* base, int tid, uint4* reg) {
@@ -322,7 +266,7 @@ struct TileM {
   __device__ __forceinline__ void store(char* tile, const uint4* reg) const {
 #pragma unroll
     for (int i = 0; i < CNT; ++i)
-      if (S::CHUNKS * S::PARTS % T == 0 || to[i] >= 0) *reinterpret_cast<uint4*>(tile + to[i]) = reg[i];
+      if (S::CHUNKS * PARTS % T == 0 || to[i] >= 0) *reinterpret_cast<uint4*>(tile + to[i]) = reg[i];
   }
   // what lies above the blocks is never written again
   static __device__ __forceinline__ void clear(char* tile, int tid) {
@@ -330,10 +274,32 @@ struct TileM {
   }
 };
 
+// Operands from such a tile (a part of it): rows by state_row, rows as they follow each other, and columns by state_row;
+// block i and product step s on or below the diagonal.
+template <typename IO>
+struct SquareFrag {
+  using S = Square<IO, 1>;
+  static constexpr int N = S::N, H = S::HALVES ? N / 2 : N, IH = S::HALVES ? S::IB / 2 : 0;
+  enum { kStateRow, kRow, kStateCol };
+  int top, low;  // the lane's bases
+  __device__ __forceinline__ SquareFrag(int kind, int li, int g)
+      : top(kind == kStateRow ? state_row_base<IO, H>(li, g) : kind == kRow ? lane_base<IO, H>(li, g) : state_col_base<IO, H>(li, g)),
+        low(kind == kStateRow ? state_row_base<IO, N>(li, g) : kind == kRow ? lane_base<IO, N>(li, g) : state_col_base<IO, N>(li, g)) {}
+  __device__ __forceinline__ uint4 state_row_of(const char* tile, int i, int s) const {
+    return i < IH ? frag_state_row<IO, H>(tile, top, i, s) : frag_state_row<IO, N>(tile + S::TOP, low, i - IH, s);
+  }
+  __device__ __forceinline__ uint4 row_of(const char* tile, int i, int s) const {
+    return i < IH ? frag_row<H>(tile, top, i, s) : frag_row<N>(tile + S::TOP, low, i - IH, s);
+  }
+  __device__ __forceinline__ uint4 state_col_of(const char* tile, int i, int s) const {
+    if (!S::HALVES) return frag_state_col<IO, N>(tile, low, i, s);
+    return s == 0 ? frag_state_col<IO, H>(tile, top, i, 0) : frag_state_col<IO, N>(tile + S::TOP, low, i, 0);
+  }
+};
+
 // What is kept of a chunk's decays and b, a row of C floats each: G_i as a pair (log2 units), e^{G_i}, e^{G_C - G_i},
-// b_i, 1 where the state starts anew, and what the values of M and (backwards) of P are to be multiplied with, the first
-// two of the last row.
-enum { kGHi, kGLo, kEk, kWe, kBeta, kAnew, kBy, kRates };
+// b_i, and 1 where the state starts anew.
+enum { kGHi, kGLo, kEk, kWe, kBeta, kAnew, kRates };
 
 // A chunk's decays and b, one token a lane of one wavefront: asked for, then scanned.  A token past the length has
 // neither decay nor b.
@@ -386,26 +352,20 @@ __device__ __forceinline__ void score_tile(int tile, int& ib, int& jb) {
   jb = tile - ib * (ib + 1) / 2;
 }
 
-// A float32 matrix [C][LD] in LDS to global memory as parts; HALF: times `by` as parts of float16 (see Halves)
-template <typename IO, int LD, int T, bool HALF>
-__device__ __forceinline__ void store_parts(const float* n, char* dst, int tid, float by) {
-  using S = Square<IO>;
+// A float32 matrix [C][LD] in LDS to global memory as parts
+template <typename IO, int LD, int T, int PARTS>
+__device__ __forceinline__ void store_parts(const float* n, char* dst, int tid) {
+  using S = Square<IO, PARTS>;
   constexpr int E = HeadCfg<IO>::E;
   for (int i = tid; i < S::CHUNKS; i += T) {
     int r, c;
     S::place(i, r, c);
     float v[E];
     F32::ld<E>(n + r * LD + c * E, v);
-    uint4 w[S::PARTS];
-    if constexpr (HALF) {
+    uint4 w[PARTS];
+    split<IO, PARTS>(v, w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] *= by;
-      Halves::split(v, w);
-    } else {
-      split<IO, S::PARTS>(v, w);
-    }
-#pragma unroll
-    for (int q = 0; q < S::PARTS; ++q) *reinterpret_cast<uint4*>(dst + 16 * (q * S::CHUNKS + i)) = w[q];
+    for (int q = 0; q < PARTS; ++q) *reinterpret_cast<uint4*>(dst + 16 * (q * S::CHUNKS + i)) = w[q];
   }
 }
 
@@ -426,8 +386,8 @@ template <typename IO, int ROWS, bool VEC>
 __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char* lds) {
   using K = HeadCfg<IO>;
   constexpr int ES = K::ES, C = K::C, T = 256, IB = C / 16, NK = ROWS * ES / 16, RS = ROWS / K::KS;
-  constexpr int LD = C + 4, TILES = IB * (IB + 1) / 2, MINE = (TILES + 3) / 4, MB = Square<IO>::BYTES;
-  constexpr bool HALF = ES == 2;
+  constexpr int LD = C + 4, TILES = IB * (IB + 1) / 2, MINE = (TILES + 3) / 4;
+  constexpr int PP = DeltaCfg<IO>::PAIR, PS = DeltaCfg<IO>::STATE;
   using TK = Tile<IO, NK, T>;
   float* const rt = reinterpret_cast<float*>(lds);  // [kRates][C]
   char* const ty = reinterpret_cast<char*>(rt + kRates * C);
@@ -464,7 +424,7 @@ __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char
   TK::store(ty, tid, ry);
   TK::store(tx, tid, rx);
   __syncthreads();
-  if (tid < kBy * C / 4)
+  if (tid < kRates * C / 4)
     reinterpret_cast<float4*>(p.rates + chunk * kRates * C)[tid] = reinterpret_cast<const float4*>(rt)[tid];
 
   // lane holds j = 4 g + v of i = li
@@ -546,47 +506,18 @@ __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char
   }
   __syncthreads();
   if (wave < IB) {
-    float most = 0.f;
 #pragma unroll
     for (int I = 0; I < IB; ++I)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        n[(16 * I + 4 * g + v) * LD + 16 * wave + li] = -M[I][v];
-        if constexpr (HALF) most = __builtin_fmaxf(most, __builtin_fabsf(M[I][v]));
-      }
-    if constexpr (HALF) {
-      most = wave_max(most);
-      if (lane == 0) inv[wave] = most;
-    }
+      for (int v = 0; v < 4; ++v) n[(16 * I + 4 * g + v) * LD + 16 * wave + li] = -M[I][v];
   }
   __syncthreads();
-  // the factor of the four wavefronts' largest value, left for the walk
-  auto factor = [&](const float* most, int at) {
-    const Halves h(__builtin_fmaxf(__builtin_fmaxf(most[0], most[1]), __builtin_fmaxf(most[2], most[3])));
-    if (tid == 0) p.rates[(chunk * kRates + kBy) * C + at] = h.back;
-    return h.to;
-  };
-  float by = 1.f;
-  if constexpr (HALF) by = factor(inv, 0);
-  store_parts<IO, LD, T, HALF>(n, p.m + chunk * MB, tid, by);
+  store_parts<IO, LD, T, PS>(n, p.m + chunk * Square<IO, PS>::BYTES, tid);
   __syncthreads();
   put_scores(sq);  // above the diagonal -M holds zeros, and so does P
-  if constexpr (HALF) {
-    float most = 0.f;
-#pragma unroll
-    for (int m = 0; m < MINE; ++m)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) most = __builtin_fmaxf(most, __builtin_fabsf(sq[m][v]));
-    most = wave_max(most);
-    if (lane == 0) inv[4 + wave] = most;
-  }
   __syncthreads();
-  if (HALF && p.back) {
-    by = factor(inv + 4, 1);
-    store_parts<IO, LD, T, HALF>(n, p.s + chunk * MB, tid, by);
-  } else {
-    store_parts<IO, LD, T, false>(n, p.s + chunk * MB, tid, 1.f);
-  }
+  if (p.back) store_parts<IO, LD, T, PS>(n, p.s + chunk * Square<IO, PS>::BYTES, tid);
+  else store_parts<IO, LD, T, PP>(n, p.s + chunk * Square<IO, PP>::BYTES, tid);
 }
 
 template <typename IO, int ROWS, bool VEC>
@@ -611,12 +542,13 @@ constexpr int kDeltaOut = 0, kDeltaSeg = 1, kDeltaStates = 2;
 // not finite.
 constexpr int kSegWhole = 0, kSegAnew = 1, kSegEmpty = 2;
 
-template <typename IO, int ROWS, int NW, bool QUERY>
+// KIND: 0 without queries, 1 with those of o, 2 with those of the walk backwards
+template <typename IO, int ROWS, int NW, int KIND>
 constexpr size_t delta_lds_bytes() {
   using K = HeadCfg<IO>;
   constexpr size_t xy = size_t(K::C) * ROWS * K::ES, z = size_t(K::C) * 16 * NW * K::ES;
-  constexpr size_t sq = size_t(K::C) * K::C * K::ES * DeltaCfg<IO>::PAIR;
-  return xy + z + sq + kRates * K::C * 4 + (QUERY ? xy + sq : 0);
+  constexpr size_t m = Square<IO, DeltaCfg<IO>::STATE>::LDS, s = Square<IO, KIND == 1 ? DeltaCfg<IO>::PAIR : DeltaCfg<IO>::STATE>::LDS;
+  return xy + z + m + kRates * K::C * 4 + (KIND != 0 ? xy + s : 0);
 }
 
 // The batch row of place b: the longest first, and where all workgroups are on the CUs at once, two on each, the second
@@ -713,19 +645,20 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
   using K = HeadCfg<IO>;
   constexpr bool QUERY = MODE == kDeltaOut;
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
-  constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
+  constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16;
   constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
   constexpr int PP = DeltaCfg<IO>::PAIR, PS = DeltaCfg<IO>::STATE;
-  constexpr int MB = Square<IO>::BYTES, ML = Square<IO>::LDS;  // bytes of a chunk's M, and in LDS
+  constexpr int MPART = Square<IO, 1>::PART;  // bytes of a part of M or P in LDS
   using TK = Tile<IO, NK, T>;
   using TZ = Tile<IO, NZ, T>;
-  using TM = TileM<IO, T>;
+  using TM = TileM<IO, T, PS>;
+  using TP = TileM<IO, T, PP>;
   using TR = Flat<kRates * C * 4, T>;
 
   char* const ty = lds;
   char* const tz = ty + C * ROWS * ES;
   char* const tm = tz + C * COLS * ES;
-  float* const rt = reinterpret_cast<float*>(tm + ML);  // [kRates][C]
+  float* const rt = reinterpret_cast<float*>(tm + PS * MPART);  // [kRates][C]
   const float* const ek = rt + kEk * C;
   const float* const we = rt + kWe * C;
   const float* const bt = rt + kBeta * C;
@@ -765,22 +698,23 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
   const char* const zb = p.v + b * p.v_b + (static_cast<int64_t>(h) * p.cols + col0) * ES;
 
   const TM square(tid);
+  const TP query_square(tid);
   TM::clear(tm, tid);
-  if constexpr (QUERY) TM::clear(tp, tid);
-  uint4 rx[TK::CNT], ry[TK::CNT], rz[TZ::CNT], rm[TM::CNT], rp[TM::CNT], rr[TR::CNT];
+  if constexpr (QUERY) TP::clear(tp, tid);
+  uint4 rx[TK::CNT], ry[TK::CNT], rz[TZ::CNT], rm[TM::CNT], rp[TP::CNT], rr[TR::CNT];
   auto load_chunk = [&](int pc) {
     const int t0 = pc * C, me = ROWS == 256 || !VEC ? opaque(tid) : tid;
     const int64_t chunk = bh * p.nch + pc;
     TK::template load<VEC>(yb, p.k_t, t0, len, p.rows, me, ry);
     TR::load(reinterpret_cast<const char*>(p.rates + chunk * kRates * C), me, rr);
     if (!trans) TZ::template load<VEC>(zb, p.v_t, t0, len, p.cols - col0, me, rz);
-    TM::load(p.m + chunk * MB, me, rm);
+    TM::load(p.m + chunk * TM::S::BYTES, me, rm);
   };
   // these are asked for half a chunk later: with them the registers do not hold the products' operands
   auto load_queries = [&](int pc) {
     const int t0 = pc * C, me = ROWS == 256 || !VEC ? opaque(tid) : tid;
     TK::template load<VEC>(xb, p.q_t, t0, len, p.rows, me, rx);
-    TM::load(p.s + (bh * p.nch + pc) * MB, me, rp);
+    TP::load(p.s + (bh * p.nch + pc) * TP::S::BYTES, me, rp);
   };
 
   // A chunk's outputs: lane holds columns cw + 4 g + v of token 16 ib + li; nothing is written with rows = 0.
@@ -831,7 +765,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
       TR::store(reinterpret_cast<char*>(rt), me, rr);
       if constexpr (QUERY) {
         TK::store(tx, me, rx);
-        square.store(tp, rp);
+        query_square.store(tp, rp);
       }
     }
     __syncthreads();
@@ -903,51 +837,32 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
     __builtin_amdgcn_s_setprio(2);
     // ---- x, then r = x - M (b x)
     constexpr int LOW = IB == 2 ? 3 : 6;  // operand steps on and below the diagonal
-    uint4 bx[JS][PP], fm[LOW];
-    float back = 1.f;
-    const int mb0 = state_row_base<IO, NP>(li, g);
-#pragma unroll
-    for (int i = 0, n = 0; i < IB; ++i)
-#pragma unroll
-      for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) fm[n] = frag_state_row<IO, NP>(tm, mb0, i, js);
-    __builtin_amdgcn_sched_barrier(0);
-    {
-      float w[JS][E], most = 0.f;
-#pragma unroll
-      for (int js = 0; js < JS; ++js) {
-        float v[E] = {}, bb[E];
-        F32::ld<E>(bt + KS * js + E * g, bb);
-        if (!trans) unpack<IO>(fz[js], v);
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const int t = tile_of<IO>(js, i);
-          v[i] -= times(e[js][i], X[t][i & 3]);
-          X[t][i & 3] = v[i];
-          w[js][i] = bb[i] * v[i];
-          most = __builtin_fmaxf(most, __builtin_fabsf(w[js][i]));
-        }
-      }
-      if constexpr (PP == 2) {
-        const Halves by(column_max(most));
-        back = by.back * rt[kBy * C];
-#pragma unroll
-        for (int js = 0; js < JS; ++js) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) w[js][i] *= by.to;
-          Halves::split(w[js], bx[js]);
-        }
-      } else {
-#pragma unroll
-        for (int js = 0; js < JS; ++js) split<IO, 1>(w[js], bx[js]);
-      }
-    }
-    uint4 fl[LOW];
-    if constexpr (PP == 2) {
+    uint4 bx[JS][PS], fm[LOW], fl[LOW];
+    using Frag = SquareFrag<IO>;
+    const Frag mb0(Frag::kStateRow, li, g);
+    auto read_m = [&](int part, uint4 (&f)[LOW]) {
 #pragma unroll
       for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
-        for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) fl[n] = frag_state_row<IO, NP>(tm + C * C * ES, mb0, i, js);
+        for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) f[n] = mb0.state_row_of(tm + part * MPART, i, js);
+    };
+    read_m(0, fm);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int js = 0; js < JS; ++js) {
+      float v[E] = {}, w[E];
+      F32::ld<E>(bt + KS * js + E * g, w);
+      if (!trans) unpack<IO>(fz[js], v);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int t = tile_of<IO>(js, i);
+        v[i] -= times(e[js][i], X[t][i & 3]);
+        X[t][i & 3] = v[i];
+        w[i] *= v[i];
+      }
+      split<IO, PS>(w, bx[js]);
     }
+    if constexpr (PS == 3) read_m(1, fl);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) scale(S[rt], end_dec);
@@ -955,36 +870,35 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
 #pragma unroll
       for (int ib = 0; ib < IB; ++ib) scale(O[ib], p.scale * ek[16 * ib + li]);
     }
-    if constexpr (PP == 2) {
-      f32x4 Y[IB] = {};
-#pragma unroll
-      for (int q = 0; q < 3; ++q)
-#pragma unroll
-        for (int i = 0, n = 0; i < IB; ++i)
-#pragma unroll
-          for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n)
-            Y[i] = q < 2 ? Halves::mma(fm[n], bx[js][1 - q], Y[i]) : Halves::mma(fl[n], bx[js][0], Y[i]);
-      mix<LOW * 3, 3>();
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < IB; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) X[i][v] = __builtin_fmaf(Y[i][v], back, X[i][v]);
-    } else {
+    auto times_m = [&](const uint4 (&f)[LOW], int part) {
 #pragma unroll
       for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
-        for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) X[i] = mma<IO>(fm[n], bx[js][0], X[i]);
-      mix<LOW, 2>();
+        for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) X[i] = mma<IO>(f[n], bx[js][part], X[i]);
+    };
+    if constexpr (PS == 3) {
+#pragma unroll
+      for (int q = 2; q >= 0; --q) times_m(fm, q);
+      mix<LOW * 3, 3>();
       __builtin_amdgcn_sched_barrier(0);
+      read_m(2, fm);
+      __builtin_amdgcn_sched_barrier(0);
+      times_m(fl, 1);
+      times_m(fl, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      times_m(fm, 0);
+    } else {
+      times_m(fm, 0);
+      mix<LOW, 2>();
     }
+    __builtin_amdgcn_sched_barrier(0);
     if (QUERY && kk + 1 < nc) load_queries(pc + 1);
-    const int pb = lane_base<IO, NP>(li, g);
+    const Frag pb(Frag::kRow, li, g);
     if constexpr (QUERY) {
 #pragma unroll
       for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
-        for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) fm[n] = frag_row<NP>(tp, pb, i, js);
+        for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) fm[n] = pb.row_of(tp, i, js);
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (MODE == kDeltaStates)
@@ -1014,7 +928,7 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
 #pragma unroll
         for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
-          for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) fl[n] = frag_row<NP>(tp + C * C * ES, pb, i, js);
+          for (int js = 0; js * KS < 16 * (i + 1); ++js, ++n) fl[n] = pb.row_of(tp + MPART, i, js);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -1083,15 +997,20 @@ __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char
   }
 }
 
+// Wavefronts per SIMD that the registers leave room for: two workgroups of four or one of eight; one of four in bfloat16
+// past 128 keys, of which LDS holds no second.
+template <typename IO, int ROWS, int NW>
+constexpr int walk_waves() { return HeadCfg<IO>::ES == 2 && ROWS == 256 && NW == 4 ? 1 : 2; }
+
 template <typename IO, int ROWS, int NW, int MODE, bool VEC>
-__global__ void __launch_bounds__((64 * NW), 2) ssm_delta_kernel(const DeltaDev p) {
+__global__ void __launch_bounds__((64 * NW), (walk_waves<IO, ROWS, NW>())) ssm_delta_kernel(const DeltaDev p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   delta_walk<IO, ROWS, NW, MODE, VEC>(p, blockIdx.x, lds);
 }
 
 // One chunk and one column tile: a launch for both (17 tokens, 4 heads of 32 x 32: 12.7 us, two launches 15.6).
 template <typename IO, int ROWS, bool VEC>
-__global__ void __launch_bounds__(256, 2) ssm_delta_one_kernel(const DeltaDev p) {
+__global__ void __launch_bounds__(256, (walk_waves<IO, ROWS, 4>())) ssm_delta_one_kernel(const DeltaDev p) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   // the walk's workgroup of a (batch row, head) makes that one's M
   int ct, seg, h, b;
@@ -1109,19 +1028,19 @@ template <typename IO, int ROWS, int NW, bool SEG, bool VEC>
 __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid, char* lds) {
   using K = HeadCfg<IO>;
   constexpr int ES = K::ES, E = K::E, KS = K::KS, C = K::C, T = 64 * NW, COLS = 16 * NW;
-  constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16, NP = C * ES / 16;
+  constexpr int NK = ROWS * ES / 16, NZ = COLS * ES / 16;
   constexpr int RT = ROWS / 16, IB = C / 16, JS = C / KS, RS = ROWS / KS;
-  constexpr int PP = DeltaCfg<IO>::PAIR, PS = DeltaCfg<IO>::STATE;
-  constexpr int MB = Square<IO>::BYTES, ML = Square<IO>::LDS;
+  constexpr int PS = DeltaCfg<IO>::STATE;
+  constexpr int MPART = Square<IO, 1>::PART;
   using TK = Tile<IO, NK, T>;
   using TZ = Tile<IO, NZ, T>;
-  using TM = TileM<IO, T>;
+  using TM = TileM<IO, T, PS>;
   using TR = Flat<kRates * C * 4, T>;
 
   char* const ty = lds;
   char* const tz = ty + C * ROWS * ES;
   char* const tm = tz + C * COLS * ES;
-  float* const rt = reinterpret_cast<float*>(tm + ML);  // [kRates][C]
+  float* const rt = reinterpret_cast<float*>(tm + PS * MPART);  // [kRates][C]
   const float* const ek = rt + kEk * C;
   const float* const we = rt + kWe * C;
   const float* const bt = rt + kBeta * C;
@@ -1160,13 +1079,13 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     const int64_t chunk = bh * p.nch + pc;
     TK::template load<VEC>(yb, p.k_t, t0, len, p.rows, me, ry);
     TR::load(reinterpret_cast<const char*>(p.rates + chunk * kRates * C), me, rr);
-    TM::load(p.s + chunk * MB, me, rp);
+    TM::load(p.s + chunk * TM::S::BYTES, me, rp);
     TZ::template load<VEC>(zb, p.v_t, t0, len, p.cols - col0, me, rz);
   };
   // these are asked for half a chunk later: with them the registers do not hold the products' operands
   auto load_late = [&](int pc) {
     const int t0 = pc * C, me = ROWS >= 128 || !VEC ? opaque(tid) : tid;
-    TM::load(p.m + (bh * p.nch + pc) * MB, me, rm);
+    TM::load(p.m + (bh * p.nch + pc) * TM::S::BYTES, me, rm);
     TK::template load<VEC>(xb, p.q_t, t0, len, p.rows, me, rx);
   };
 
@@ -1208,21 +1127,21 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
 #pragma unroll
     for (int i = 0; i < IB; ++i) X[i] = Y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     uint4 fz[JS], ft[LOW], fl[LOW];
-    const int mc0 = state_col_base<IO, NP>(li, g);
+    const SquareFrag<IO> mc0(SquareFrag<IO>::kStateCol, li, g);
     // columns of a square matrix, its rows as the contraction: what lies below the diagonal of the transposed
     auto read_square = [&](const char* tile, uint4 (&f)[LOW]) {
 #pragma unroll
       for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
         for (int js = 0; js < JS; ++js)
-          if (KS * (js + 1) > 16 * i) f[n++] = frag_state_col<IO, NP>(tile, mc0, i, js);
+          if (KS * (js + 1) > 16 * i) f[n++] = mc0.state_col_of(tile, i, js);
     };
-    auto times_square = [&](const uint4 (&f)[LOW], const uint4 (&by)[JS], f32x4 (&acc)[IB], auto&& add) {
+    auto times_square = [&](const uint4 (&f)[LOW], const uint4 (&by)[JS], f32x4 (&acc)[IB]) {
 #pragma unroll
       for (int i = 0, n = 0; i < IB; ++i)
 #pragma unroll
         for (int js = 0; js < JS; ++js)
-          if (KS * (js + 1) > 16 * i) acc[i] = add(f[n++], by[js], acc[i]);
+          if (KS * (js + 1) > 16 * i) acc[i] = mma<IO>(f[n++], by[js], acc[i]);
     };
     {
       const int sb = state_row_base<IO, NK>(li, g), zb0 = col_base<IO, NZ>(li, g);
@@ -1261,66 +1180,39 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
       }
     }
     // ---- y = P^T dO + e^{G_C - G} X
-    if constexpr (PP == 2) read_square(tp + C * C * ES, fl);
+    if constexpr (PS == 3) read_square(tp + MPART, fl);
     __builtin_amdgcn_sched_barrier(0);
-    auto half = [](const uint4& a, const uint4& b, f32x4 acc) { return Halves::mma(a, b, acc); };
-    float yb = 1.f;
-    if constexpr (PP == 2) {
-      // dO as float16 over a power of two: exact but for what is below 2^-32 of the column's largest
-      uint4 fo[JS];
-      float d[JS][E], most = 0.f;
-#pragma unroll
-      for (int js = 0; js < JS; ++js) {
-        unpack<IO>(fz[js], d[js]);
-#pragma unroll
-        for (int i = 0; i < E; ++i) most = __builtin_fmaxf(most, __builtin_fabsf(d[js][i]));
-      }
-      const Halves h(column_max(most));
-      yb = h.back * rt[kBy * C + 1];
-#pragma unroll
-      for (int js = 0; js < JS; ++js) fo[js] = Halves::one(d[js], h.to);
-      times_square(ft, fo, Y, half);
-      times_square(fl, fo, Y, half);
-    } else {
-      times_square(ft, fz, Y, mma<IO>);
+    times_square(ft, fz, Y);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (PS == 3) {
+      read_square(tp + 2 * MPART, ft);
+      __builtin_amdgcn_sched_barrier(0);
+      times_square(fl, fz, Y);
+      __builtin_amdgcn_sched_barrier(0);
+      read_square(tm + MPART, fl);
+      __builtin_amdgcn_sched_barrier(0);
+      times_square(ft, fz, Y);
+      __builtin_amdgcn_sched_barrier(0);
     }
     read_square(tm, ft);
-    if constexpr (PP == 2) read_square(tm + C * C * ES, fl);
     __builtin_amdgcn_sched_barrier(0);
     // ---- e = y - M^T (b y)
-    uint4 by[PP][JS];
-    float back = 1.f;
-    {
-      float bb[JS][E], most = 0.f;
+    uint4 by[PS][JS];
 #pragma unroll
-      for (int js = 0; js < JS; ++js) {
-        float w[E];
-        F32::ld<E>(we + KS * js + E * g, w);
-        F32::ld<E>(bt + KS * js + E * g, bb[js]);
+    for (int js = 0; js < JS; ++js) {
+      float w[E], b[E];
+      F32::ld<E>(we + KS * js + E * g, w);
+      F32::ld<E>(bt + KS * js + E * g, b);
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const int t = tile_of<IO>(js, i);
-          X[t][i & 3] = __builtin_fmaf(Y[t][i & 3], yb, times(w[i], X[t][i & 3]));
-          bb[js][i] *= X[t][i & 3];
-          most = __builtin_fmaxf(most, __builtin_fabsf(bb[js][i]));
-        }
+      for (int i = 0; i < E; ++i) {
+        const int t = tile_of<IO>(js, i);
+        X[t][i & 3] = Y[t][i & 3] + times(w[i], X[t][i & 3]);
+        b[i] *= X[t][i & 3];
       }
-      if constexpr (PP == 2) {
-        const Halves h(column_max(most));
-        back = h.back * rt[kBy * C];
+      uint4 f[PS];
+      split<IO, PS>(b, f);
 #pragma unroll
-        for (int js = 0; js < JS; ++js) {
-          uint4 f[2];
-#pragma unroll
-          for (int i = 0; i < E; ++i) bb[js][i] *= h.to;
-          Halves::split(bb[js], f);
-          by[0][js] = f[0];
-          by[1][js] = f[1];
-        }
-      } else {
-#pragma unroll
-        for (int js = 0; js < JS; ++js) split<IO, 1>(bb[js], &by[0][js]);
-      }
+      for (int q = 0; q < PS; ++q) by[q][js] = f[q];
     }
     __builtin_amdgcn_sched_barrier(0);
     // What the state before the chunk is made of, one operand after the other: scale e^G dO (with Q's rows), then
@@ -1344,23 +1236,22 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
     parts(0);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) scale(R[rt], end_dec);
-    if constexpr (PP == 2) {
+    if constexpr (PS == 3) {
 #pragma unroll
-      for (int i = 0; i < IB; ++i) Y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      times_square(ft, by[1], Y, half);
-      times_square(fl, by[0], Y, half);
-      times_square(ft, by[0], Y, half);
+      for (int q = 2; q >= 0; --q) times_square(ft, by[q], X);
       mix<LOW * 3, 3>();
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < IB; ++i)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) X[i][v] = __builtin_fmaf(Y[i][v], back, X[i][v]);
-    } else {
-      times_square(ft, by[0], X, mma<IO>);
-      mix<LOW, 3>();
+      read_square(tm + 2 * MPART, ft);
       __builtin_amdgcn_sched_barrier(0);
+      times_square(fl, by[1], X);
+      times_square(fl, by[0], X);
+      __builtin_amdgcn_sched_barrier(0);
+      times_square(ft, by[0], X);
+    } else {
+      times_square(ft, by[0], X);
+      mix<LOW, 3>();
     }
+    __builtin_amdgcn_sched_barrier(0);
     if (kk + 1 < nc) load_late(pc - 1);
     if constexpr (!SEG) keep<IO, IB>(record + kept.rows(1), C, p.cp, cw + li, g, X);
 
@@ -1400,7 +1291,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
 // heads of 128 x 128, bfloat16, 903 us for 983 with a launch each; of 4 x 1999 ragged tokens, 24 heads of 64, float32, 571
 // for 706).  Now 283 and 214 of it.  SEG: the segments' own ends.
 template <typename IO, int ROWS, int NW, bool SEG, bool VEC>
-__global__ void __launch_bounds__((64 * NW), 2) ssm_delta_both_kernel(const DeltaDev p, const DeltaDev r, uint32_t first) {
+__global__ void __launch_bounds__((64 * NW), (walk_waves<IO, ROWS, NW>())) ssm_delta_both_kernel(const DeltaDev p, const DeltaDev r, uint32_t first) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   if (blockIdx.x < first) delta_walk<IO, ROWS, NW, SEG ? kDeltaSeg : kDeltaStates, VEC>(p, blockIdx.x, lds);
   else delta_walk_back<IO, ROWS, NW, SEG, VEC>(r, blockIdx.x - first, lds);
@@ -1984,7 +1875,7 @@ hipError_t launch_prep_t(const DeltaDev& p, hipStream_t st) {
 template <typename IO, int ROWS, bool VEC>
 hipError_t launch_one_t(const DeltaDev& p, hipStream_t st) {
   static std::atomic<uint64_t> allowed{0};
-  constexpr size_t prep = prep_lds_bytes<IO, ROWS>(), walk = delta_lds_bytes<IO, ROWS, 4, true>();
+  constexpr size_t prep = prep_lds_bytes<IO, ROWS>(), walk = delta_lds_bytes<IO, ROWS, 4, 1>();
   constexpr size_t smem = prep > walk ? prep : walk;
   auto kern = ssm_delta_one_kernel<IO, ROWS, VEC>;
   if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
@@ -1995,7 +1886,7 @@ hipError_t launch_one_t(const DeltaDev& p, hipStream_t st) {
 template <typename IO, int ROWS, int NW, int MODE, bool VEC>
 hipError_t launch_walk_t(const DeltaDev& p, hipStream_t st) {
   static std::atomic<uint64_t> allowed{0};
-  constexpr size_t smem = delta_lds_bytes<IO, ROWS, NW, MODE == kDeltaOut>();
+  constexpr size_t smem = delta_lds_bytes<IO, ROWS, NW, MODE == kDeltaOut ? 1 : 0>();
   const int64_t nrun = MODE == kDeltaSeg ? p.nseg - 1 : p.nseg;
   auto kern = ssm_delta_kernel<IO, ROWS, NW, MODE, VEC>;
   if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
@@ -2006,7 +1897,7 @@ hipError_t launch_walk_t(const DeltaDev& p, hipStream_t st) {
 template <typename IO, int ROWS, int NW, bool SEG, bool VEC>
 hipError_t launch_both_t(const DeltaDev& p, const DeltaDev& r, hipStream_t st) {
   static std::atomic<uint64_t> allowed{0};
-  constexpr size_t smem = delta_lds_bytes<IO, ROWS, NW, true>();
+  constexpr size_t smem = delta_lds_bytes<IO, ROWS, NW, 2>();
   const int64_t runs = (SEG ? p.nseg - 1 : p.nseg) * static_cast<int64_t>(p.H) * p.batch;
   auto kern = ssm_delta_both_kernel<IO, ROWS, NW, SEG, VEC>;
   if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;

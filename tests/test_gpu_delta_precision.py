@@ -13,7 +13,7 @@ import torch
 import selective_state_space_ssm_amd as ssm
 from oracle import delta
 
-from test_gpu_delta import IDS, TYPES, f64, make
+from test_gpu_delta import IDS, TYPES, close, f64, kappa, make
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,62 @@ def test_gradients_are_rounded_once(case, decay, dtype):
         past, most = np.linalg.norm(past_rounding(got[n], want[n])), by * np.linalg.norm(spread[n])
         print(f"[delta precision] {n} {past / most:.3f}", flush=True)
         assert past <= most, (n, past / most)
+
+
+def bounds(x, dtype, do, dlast):
+    """test_gpu_delta's, with nothing for what the gradients find kept: float32."""
+    y = f64(x)
+    dk, dv = y["q"].shape[3], y["v"].shape[3]
+    return y, delta.delta_scan_errors(**y, do=do.double().cpu().numpy(), dlast=None if dlast is None else dlast.double().cpu().numpy(),
+                                      step=6 * np.sqrt(dk + dv + 160) * 2.0 ** -24,
+                                      pair=2.0 ** -16 * kappa(y, dtype) if dtype == torch.bfloat16 else 0.0,
+                                      chunk=64 if dtype == torch.bfloat16 else 32)
+
+
+def check(x, do, dlast, dtype, names=NAMES + ("dh0",)):
+    y, e = bounds(x, dtype, do, dlast)
+    o, last = ssm.ssm_delta_scan_fwd(**x)
+    got = ssm.ssm_delta_scan_bwd(**x, do=do, dlast=dlast)
+    wo, wl = delta.delta_scan(**y)
+    want = delta.delta_scan_bwd(**y, do=do.double().cpu().numpy(), dlast=None if dlast is None else dlast.double().cpu().numpy())
+    close("o", o, wo, e["o"])
+    close("last", last, wl, e["last"])
+    for n in names:
+        close(n, got[n], want[n], e[n])
+    return got, want
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("by", [1e10, 1e-10], ids=["large", "small"])
+def test_later_tokens_of_another_size(by, dtype):
+    """The second half of each chunk's values far larger or smaller than the first's: what comes first does not know of it."""
+    x, do, dlast = make(2, 192, 2, 2, 48, 64, dtype, seed=31, h0=False)
+    late = (torch.arange(192, device=do.device) // 16 % 2).bool()
+    x["v"][:, late] = (x["v"][:, late].float() * by).to(dtype)
+    x["g"][:, ::32] = float("-inf")
+    check(x, do, dlast, dtype, ())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("by", [1e12, 1e-12], ids=["large", "small"])
+def test_packed_sequences_of_different_sizes(by, dtype):
+    """Two sequences that share a chunk, values and gradients of the first times and over a factor: each is as exact as by
+    itself."""
+    x, do, dlast = make(1, 128, 2, 2, 64, 64, dtype, seed=32)
+    at = 41
+    x["g"][:, at] = float("-inf")
+    x["v"][:, :at] = (x["v"][:, :at].float() * by).to(dtype)
+    x["h0"] *= by
+    do[:, at:] = (do[:, at:].float() * by).to(dtype)
+    dlast *= by
+    check(x, do, dlast, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("rate", [0.5, 1.0, 2.0])
+def test_a_loss_on_the_last_tokens_alone(rate, dtype):
+    """With a decay at every token the gradients of those before are as much smaller, and as exact."""
+    x, do, _ = make(1, 64, 2, 2, 64, 64, dtype, seed=33, h0=False)
+    x["g"][:] = -rate
+    do[:, :-2] = 0
+    check(x, do, None, dtype, ("dq", "dk", "dv", "dbeta", "dh0"))
