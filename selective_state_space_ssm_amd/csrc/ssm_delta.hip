@@ -44,13 +44,16 @@ constexpr int64_t kDeltaMaxSegments = 64;  // the carry's wavefronts hold someth
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
-// Columns of a workgroup's tile: 128 in bfloat16 past 128 keys, where there are more than 64 and every operand row is
-// whole vectors (LDS then holds one workgroup a CU either way; 4 x 2048 tokens, 32 heads of 192 x 128, forward and
-// backward 376 and 1389 us, with tiles of 64 455 and 1897; 2 x 2048, 16 heads of 256 x 256 250 and 887, 324 and 953),
-// else 64 (float32, the latter 544 and 1249, with 128 596 and 1811; the former 629 and 2373, 993 and 2223).
-bool wide_for(int64_t rows, int64_t cols, bool vec, bool bf16) { return bf16 && rows > 128 && cols > 64 && vec; }
-int64_t tiles_for(int64_t rows, int64_t cols, bool vec, bool bf16) {
-  return cdiv(cols, wide_for(rows, cols, vec, bf16) ? 128 : 64);
+// Columns of a workgroup's tile: 128 in bfloat16 past 128 keys, where every operand row is whole vectors and tiles of 64
+// are more than the CUs (LDS holds one workgroup either way, and with tiles of 64 a second round would be needed: 8 x 2048
+// tokens, 32 heads of 192 x 128, forward and backward 499 and 2518 us, with tiles of 64 563 and 2706; 8 x 2048, 16 heads of
+// 256 x 256 429 and 2398, 505 and 2584; 4 x 2048, 32 heads of 192 x 128 373 and 1422, 296 and 1381; 2 x 2048, 16 heads of
+// 256 x 256 244 and 994, 229 and 710), else 64 (float32, the latter 538 and 1220, with 128 596 and 1811).
+bool wide_for(int64_t rows, int64_t cols, int64_t bh, bool vec, bool bf16) {
+  return bf16 && rows > 128 && cols > 64 && vec && bh * cdiv(cols, 64) > kDeltaCUs;
+}
+int64_t tiles_for(int64_t rows, int64_t cols, int64_t bh, bool vec, bool bf16) {
+  return cdiv(cols, wide_for(rows, cols, bh, vec, bf16) ? 128 : 64);
 }
 
 // States carried over the segments, in order, 16 columns a workgroup: state <- A carried + own, or A^T carried + own
@@ -258,7 +261,8 @@ Plan plan_of(const DeltaArgs& a, bool bf16) {
   // segments' own walk 0.8, with the transitions' tiles beside the state's in all but the first, a step of the carry
   // 0.8, two more launches 3.  16 heads of 128 x 128 over 32768 tokens: 634 us in 16 segments (605 since), 637 in 8, 712
   // in 24, whole some 2.2 ms; 128 heads of 128 x 128 over 2048 tokens are better off whole.  A tenth has to be gained.
-  const int64_t tv = tiles_for(a.dk, a.dv, true, bf16), tt = cdiv(p.rp, wide_for(a.dk, a.dv, true, bf16) ? 128 : 64), bh = a.batch * a.H;
+  const int64_t bh = a.batch * a.H, tv = tiles_for(a.dk, a.dv, bh, true, bf16);
+  const int64_t tt = cdiv(p.rp, wide_for(a.dk, a.dv, bh, true, bf16) ? 128 : 64);
   const double pair = bf16 ? 1.75 : 2.;
   auto rate = [pair](double wgs) { return wgs <= kDeltaCUs ? 1. : std::max(pair, wgs * pair / (2 * kDeltaCUs)); };
   double best = 0.9 * p.nch * rate(bh * tv);
@@ -362,13 +366,13 @@ DeltaDev dev_of(const DeltaArgs& a, const Plan& pl, const Space& w, char* work, 
   d.rows = static_cast<int>(a.dk); d.cols = static_cast<int>(a.dv);
   d.rp = static_cast<int>(pl.rp); d.cp = static_cast<int>(pl.cp);
   d.nch = static_cast<int>(pl.nch); d.cps = static_cast<int>(pl.cps); d.nseg = static_cast<int>(pl.nseg);
-  d.nvt = d.ntile = static_cast<int>(tiles_for(a.dk, a.dv, vec, bf16));
+  d.nvt = d.ntile = static_cast<int>(tiles_for(a.dk, a.dv, a.batch * a.H, vec, bf16));
   d.scale = a.scale;
   return d;
 }
 
 hipError_t launch_pass(const DeltaDev& d, const DeltaDev& r, bool bf16, int pass, bool vec, hipStream_t st) {
-  return bf16 ? launch_delta_bf16(d, r, pass, wide_for(d.rows, d.cols, vec, true), vec, st) : launch_delta_f32(d, r, pass, vec, st);
+  return bf16 ? launch_delta_bf16(d, r, pass, wide_for(d.rows, d.cols, int64_t(d.batch) * d.H, vec, true), vec, st) : launch_delta_f32(d, r, pass, vec, st);
 }
 
 hipError_t launch_carry(const DeltaDev& d, bool rev, hipStream_t st) {
@@ -383,7 +387,7 @@ hipError_t launch_carry(const DeltaDev& d, bool rev, hipStream_t st) {
 
 // with the tiles of the transitions
 DeltaDev with_transitions(DeltaDev d, bool vec, bool bf16) {
-  d.ntile = d.nvt + static_cast<int>(cdiv(d.rp, wide_for(d.rows, d.cols, vec, bf16) ? 128 : 64));
+  d.ntile = d.nvt + static_cast<int>(cdiv(d.rp, wide_for(d.rows, d.cols, int64_t(d.batch) * d.H, vec, bf16) ? 128 : 64));
   return d;
 }
 
@@ -403,7 +407,7 @@ hipError_t launch_delta_fwd(const DeltaArgs& a, bool bf16, char* work, hipStream
   const Plan pl = plan_of(a, bf16);
   const bool vec = all_vec(a, bf16);
   const DeltaDev d = dev_of(a, pl, space_of(a, pl, bf16, false), work, bf16, vec);
-  if (pl.nch == 1 && d.ntile == 1 && !wide_for(d.rows, d.cols, vec, bf16))  // that kernel's tile has 64 columns
+  if (pl.nch == 1 && d.ntile == 1 && !wide_for(d.rows, d.cols, a.batch * a.H, vec, bf16))  // that kernel's tile has 64 columns
     return launch_pass(d, d, bf16, deltak::kPassOne, vec, st);
   hipError_t e = launch_pass(d, d, bf16, deltak::kPassPrep, vec, st);
   if (e == hipSuccess && pl.nseg > 1) {
