@@ -6,7 +6,8 @@ import torch
 
 import selective_state_space_ssm_amd as ssm
 
-from test_gpu_delta import IDS, TYPES, make
+import test_gpu_delta as base
+from test_gpu_delta import DEV, IDS, TYPES, make
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +88,27 @@ def test_rows_without_tokens_hand_on_what_they_are_given(case, dtype):
         r = both(x, do, dlast)
         assert torch.equal(r["last"][0], x["h0"][0]) and torch.equal(r["dh0"][0], dlast[0])
         assert bool(torch.isfinite(r["o"]).all()) and bool(torch.isfinite(r["dh0"][1]).all())
+
+
+def starts_of_their_own(x, seed):
+    r = torch.Generator().manual_seed(seed)
+    x["g"][(torch.rand(x["g"].shape, generator=r) < 0.03).to(DEV)] = float("-inf")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("case", [(2, 200, 4, 2, 48, 64), (1, 1500, 2, 1, 16, 33), (1, 130, 2, 2, 128, 128), (1, 100, 1, 1, 256, 40),
+                                  (16, 200, 32, 8, 64, 64), (3, 130, 6, 3, 136, 72)], ids=CASE_IDS)
+def test_heads_that_start_at_tokens_of_their_own(case, dtype, monkeypatch):
+    """Starts drawn for every head and token by itself, ragged rows, against the oracle: forward and gradients with the
+    bounds of the plain cases."""
+    made = base.make
+
+    def with_starts(*a, **kw):
+        x, do, dlast = made(*a, **kw)
+        if x["g"] is not None:
+            starts_of_their_own(x, 45)
+        return x, do, dlast
+
+    monkeypatch.setattr(base, "make", with_starts)
+    base.test_forward(case, dtype, "full")
+    base.test_backward(case, dtype, "full")
