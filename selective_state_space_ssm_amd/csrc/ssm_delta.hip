@@ -367,6 +367,7 @@ DeltaDev dev_of(const DeltaArgs& a, const Plan& pl, const Space& w, char* work, 
   d.rp = static_cast<int>(pl.rp); d.cp = static_cast<int>(pl.cp);
   d.nch = static_cast<int>(pl.nch); d.cps = static_cast<int>(pl.cps); d.nseg = static_cast<int>(pl.nseg);
   d.nvt = d.ntile = static_cast<int>(tiles_for(a.dk, a.dv, a.batch * a.H, vec, bf16));
+  d.places = static_cast<int>(a.dk > 128 ? kDeltaCUs : 2 * kDeltaCUs);  // past 128 keys LDS has room for one a CU
   d.scale = a.scale;
   return d;
 }

@@ -51,7 +51,6 @@ namespace deltak {
 
 using namespace headk;
 
-constexpr int kDeltaPlaces = 512;  // workgroups of the walks that the CUs hold at once
 constexpr int kSlab = 64;  // columns of d_value that the gradient kernel takes at a time; padded widths go by it
 
 struct DeltaDev {
@@ -79,6 +78,7 @@ struct DeltaDev {
   int nch, cps, nseg;          // chunks, chunks per segment, segments
   int ntile, nvt;              // column tiles, those of the state (the others: of the transition)
   int back;                    // P is for the walk backwards
+  int places;                  // workgroups of the walk that the CUs hold at once
   float scale;
 };
 
@@ -551,11 +551,12 @@ constexpr size_t delta_lds_bytes() {
   return xy + z + m + kRates * K::C * 4 + (KIND != 0 ? xy + s : 0);
 }
 
-// The batch row of place b: the longest first, and where all workgroups are on the CUs at once, two on each, the second
-// half of the places from the shortest on, so that a long row shares its CU with a short one (8 ragged rows of up to 2048
-// tokens, 32 heads of 128 x 128, the mean of eight draws: 205 us, 208 with the longest first throughout, 217 in the rows'
-// own order).  Up to 64 rows, a lane each.
-__device__ __forceinline__ int by_length(const DeltaDev& p, int b) {
+// The batch row of place b: the longest first, and where all workgroups are on the CUs at once the second half of the places
+// from the shortest on, so that of two on a CU a long row is beside a short one (8 ragged rows of up to 2048 tokens, 32
+// heads of 128 x 128, the mean of eight draws: 205 us, 208 with the longest first throughout, 217 in the rows' own order;
+// where they are not, float32, 8 rows of up to 1024 tokens, 16 heads of 256 x 256, the mean of six: longest first 398, the
+// other order 432).  Up to 64 rows, a lane each.
+__device__ __forceinline__ int by_length(const DeltaDev& p, int b, int workgroups) {
   const int lane = threadIdx.x & 63, n = lane < p.batch ? length_of(p, lane) : -1;
   int rank = 0;  // of the lane's row
   for (int j = 0; j < p.batch; ++j) {
@@ -563,7 +564,7 @@ __device__ __forceinline__ int by_length(const DeltaDev& p, int b) {
     rank += o > n || (o == n && j < lane);
   }
   const int half = (p.batch + 1) / 2;
-  if (b >= half && p.ntile * p.H * p.batch <= kDeltaPlaces) b = p.batch - 1 - (b - half);
+  if (b >= half && workgroups <= p.places) b = p.batch - 1 - (b - half);
   return __builtin_ctzll(__builtin_amdgcn_ballot_w64(rank == b && lane < p.batch));
 }
 
@@ -582,7 +583,7 @@ __device__ __forceinline__ void place(const DeltaDev& p, uint32_t pid, int nrun,
   idx /= nrun;
   h = idx % p.H;
   b = idx / p.H;
-  if (p.lengths != nullptr && p.batch <= 64) b = by_length(p, b);
+  if (p.lengths != nullptr && p.batch <= 64) b = by_length(p, b, p.ntile * nrun * p.H * p.batch);
 }
 
 template <typename IO, int RT>
