@@ -483,7 +483,8 @@ int ssm_head_scan_workspace(int64_t batch, int64_t L, int64_t n_heads, int64_t n
  *   nullable; state_in, state_out: [batch, n_heads, d_key, d_value] float32,
  *   state_out equal to state_in (in place) or disjoint from it.  All dense and
  *   16-byte aligned.
- * Sizes and errors as ssm_head_scan_fwd.
+ * Sizes and errors as ssm_head_scan_fwd, but that batch * n_heads has no bound of
+ * its own: batch * n_heads * ceil(d_value / 32) < 2^24.
  */
 int ssm_head_step(const void *q, const void *k, const void *v, const void *g, const float *g_head, float scale,
                   const float *state_in, float *state_out, void *o, int64_t batch, int64_t n_heads, int64_t n_qk_heads,

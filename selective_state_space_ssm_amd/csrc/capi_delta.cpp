@@ -17,7 +17,7 @@ int ssm_delta_scan_workspace(int64_t batch, int64_t L, int64_t n_heads, int64_t 
                              int64_t d_value, int dtype, int backward, int64_t* bytes) {
   g_err.clear();
   if (!bytes) return fail(SSM_EINVAL, "bytes must not be NULL");
-  if (int rc = check_head_sizes(batch, L, n_heads, n_qk_heads, d_key, d_value, dtype)) return rc;
+  if (int rc = check_scan_sizes(batch, L, n_heads, n_qk_heads, d_key, d_value, dtype)) return rc;
   ssm::DeltaArgs a{};
   a.batch = batch; a.L = L; a.H = n_heads; a.Hk = n_qk_heads; a.dk = d_key; a.dv = d_value;
   *bytes = ssm::delta_workspace_bytes(a, dtype == SSM_BF16, backward != 0);
@@ -31,7 +31,7 @@ int ssm_delta_scan_fwd(const void* q, int64_t q_batch, int64_t q_token, const vo
                        int64_t n_qk_heads, int64_t d_key, int64_t d_value, int dtype, void* stream) {
   g_err.clear();
   if (!q || !k || !v || !o) return fail(SSM_EINVAL, "q, k, v and o must not be NULL");
-  if (int rc = check_head_sizes(batch, L, n_heads, n_qk_heads, d_key, d_value, dtype)) return rc;
+  if (int rc = check_scan_sizes(batch, L, n_heads, n_qk_heads, d_key, d_value, dtype)) return rc;
   ssm::DeltaArgs a{};
   a.q = q; a.q_b = q_batch; a.q_t = q_token; a.k = k; a.k_b = k_batch; a.k_t = k_token;
   a.v = v; a.v_b = v_batch; a.v_t = v_token;
@@ -69,7 +69,7 @@ int ssm_delta_scan_bwd(const void* q, int64_t q_batch, int64_t q_token, const vo
                        int64_t d_key, int64_t d_value, int dtype, void* stream) {
   g_err.clear();
   if (!q || !k || !v || !dout || !dq || !dk || !dv) return fail(SSM_EINVAL, "q, k, v, do, dq, dk and dv must not be NULL");
-  if (int rc = check_head_sizes(batch, L, n_heads, n_qk_heads, d_key, d_value, dtype)) return rc;
+  if (int rc = check_scan_sizes(batch, L, n_heads, n_qk_heads, d_key, d_value, dtype)) return rc;
   if (dg && !g) return fail(SSM_EINVAL, "dg needs g");
   if (dbeta && !beta) return fail(SSM_EINVAL, "dbeta needs beta");
   ssm::DeltaArgs a{};
@@ -110,7 +110,7 @@ int ssm_delta_step(const void* q, const void* k, const void* v, const void* g, c
   g_err.clear();
   if (!q || !k || !v || !state_in || !state_out || !o)
     return fail(SSM_EINVAL, "q, k, v, state_in, state_out and o must not be NULL");
-  if (int rc = check_head_sizes(batch, 1, n_heads, n_qk_heads, d_key, d_value, dtype)) return rc;
+  if (int rc = check_step_sizes(batch, n_heads, n_qk_heads, d_key, d_value, dtype)) return rc;
   if (!std::isfinite(scale)) return fail(SSM_EINVAL, "scale must be finite");
   for (const void* r : {q, k, v, g, beta, (const void*)state_in, (const void*)state_out, (const void*)o})
     if (r && !aligned16(r)) return fail(SSM_EINVAL, "every pointer must be 16-byte aligned");

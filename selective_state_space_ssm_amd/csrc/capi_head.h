@@ -31,7 +31,20 @@ inline int check_head_sizes(int64_t batch, int64_t L, int64_t H, int64_t Hk, int
   if (!mul_ok(batch, H, &bh) || !mul_ok(bh, L, &n) || !mul_ok(n, kHeadMaxDim, &n) || n > (int64_t(1) << 58))
     return fail(SSM_EINVAL, "tensor sizes overflow");
   if (L > (int64_t(1) << 30)) return fail(SSM_EUNSUPPORTED, "L=%lld > 2^30 is not supported", (long long)L);
-  if (bh > 65535) return fail(SSM_EUNSUPPORTED, "batch * n_heads = %lld > 65535 is not supported", (long long)bh);
+  return SSM_OK;
+}
+
+inline int check_scan_sizes(int64_t batch, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv, int dtype) {
+  if (int rc = check_head_sizes(batch, L, H, Hk, dk, dv, dtype)) return rc;
+  if (batch * H > 65535)
+    return fail(SSM_EUNSUPPORTED, "batch * n_heads = %lld > 65535 is not supported", (long long)(batch * H));
+  return SSM_OK;
+}
+
+// One token of every sequence: a workgroup for 32 columns of a head
+inline int check_step_sizes(int64_t batch, int64_t H, int64_t Hk, int64_t dk, int64_t dv, int dtype) {
+  if (int rc = check_head_sizes(batch, 1, H, Hk, dk, dv, dtype)) return rc;
+  if (batch * H * ((dv + 31) / 32) >= kMaxWorkgroups) return fail(SSM_EUNSUPPORTED, "too many workgroups for one launch");
   return SSM_OK;
 }
 
