@@ -40,8 +40,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "ssm_device.h"
 #include "ssm_head_kernel.h"
 #include "ssm_kernels.h"
@@ -1846,22 +1844,6 @@ __global__ void __launch_bounds__((64 * NW), (grad_waves<IO, ROWS, NW, MULTI>())
 }
 
 // ---------------------------------------------------------------- launches
-
-// More than 64 KB of LDS is asked for once per device and kernel (the call costs as much as a launch).
-template <typename Kern>
-hipError_t allow_lds(Kern kern, size_t smem, std::atomic<uint64_t>& allowed) {
-  if (smem <= 65536) return hipSuccess;
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  const uint64_t bit = uint64_t(1) << (dev & 63);
-  if (dev > 63 || (allowed.load(std::memory_order_relaxed) & bit) == 0) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
-                            static_cast<int>(smem));
-    if (e == hipSuccess && dev <= 63) allowed.fetch_or(bit, std::memory_order_relaxed);
-  }
-  return e;
-}
 
 template <typename IO, int ROWS, bool VEC>
 hipError_t launch_prep_t(const DeltaDev& p, hipStream_t st) {

@@ -855,6 +855,22 @@ ssm_head_kernel(const HeadDev p) {
   }
 }
 
+// More than 64 KB of LDS is asked for once per device and kernel (the call costs as much as a launch).
+template <typename Kern>
+hipError_t allow_lds(Kern kern, size_t smem, std::atomic<uint64_t>& allowed) {
+  if (smem <= 65536) return hipSuccess;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev > 63 || (allowed.load(std::memory_order_relaxed) & bit) == 0) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            static_cast<int>(smem));
+    if (e == hipSuccess && dev <= 63) allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return e;
+}
+
 template <typename IO, int ROWS, int NW, int NC, int MODE, bool DOT, bool VEC>
 hipError_t launch_head_t(const HeadDev& p, hipStream_t st) {
   const int64_t nrun = MODE == kState ? p.nseg - 1 : p.nseg;
@@ -862,20 +878,8 @@ hipError_t launch_head_t(const HeadDev& p, hipStream_t st) {
   const int64_t wgs = nrun * p.ntile * (p.H / HEADS) * p.batch;
   constexpr size_t smem = HEADS * head_lds_bytes<IO, ROWS, NW, NC, MODE, DOT>() + pair_lds_bytes<IO, NW, NC, MODE>();
   auto kern = ssm_head_kernel<IO, ROWS, NW, NC, MODE, DOT, VEC>;
-  if constexpr (smem > 65536) {
-    // asked for once per device (the call costs as much as a launch)
-    static std::atomic<uint64_t> allowed{0};
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return e;
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (dev > 63 || (allowed.load(std::memory_order_relaxed) & bit) == 0) {
-      e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(smem));
-      if (e != hipSuccess) return e;
-      if (dev <= 63) allowed.fetch_or(bit, std::memory_order_relaxed);
-    }
-  }
+  static std::atomic<uint64_t> allowed{0};
+  if (hipError_t e = allow_lds(kern, smem, allowed); e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(wgs)), dim3(64 * NW * HEADS), smem, st, p);
   return hipGetLastError();
 }
