@@ -60,7 +60,7 @@ int64_t tiles_for(int64_t rows, int64_t cols, int64_t bh, bool vec, bool bf16) {
 // from the end.  Float32 matrix instructions, 16 rows a wavefront; the carried columns are in LDS.  A segment's rows of
 // A are asked for while the segment before is worked on: each operand takes its successor once it is used.  The column
 // tiles of a head are a multiple of the heads apart, so that with 8 or more heads they share an XCD's L2 for A.  16 heads
-// of 128 x 128 in 16 segments: 49 us, 3.5 a segment, from load to load.  A segment in which the state starts anew, or which
+// of 128 x 128 in 16 segments: 56 us, 4 a segment, from load to load.  A segment in which the state starts anew, or which
 // has no tokens, takes no product (see kSegWhole).
 template <int NW, bool REV>
 __global__ void __launch_bounds__(64 * NW) ssm_delta_carry_kernel(float* state, const float* trans, const int* kinds, int nseg,
@@ -257,9 +257,9 @@ Plan plan_of(const DeltaArgs& a, bool bf16) {
   p.rp = up(a.dk, 16);
   p.cp = up(a.dv, deltak::kSlab);
   // The number of segments that the model below finds shortest, in chunks of a workgroup alone on its CU (4.2 us,
-  // bfloat16, 128 x 128): two workgroups a CU take 1.75 of that (float32: 2, the matrix instructions bound it), the
+  // bfloat16, 128 x 128, M in two parts): two workgroups a CU take 1.75 of that (float32: 2, the matrix instructions bound it), the
   // segments' own walk 0.8, with the transitions' tiles beside the state's in all but the first, a step of the carry
-  // 0.8, two more launches 3.  16 heads of 128 x 128 over 32768 tokens: 634 us in 16 segments (605 since), 637 in 8, 712
+  // 0.8, two more launches 3.  16 heads of 128 x 128 over 32768 tokens: 634 us in 16 segments, 637 in 8, 712
   // in 24, whole some 2.2 ms; 128 heads of 128 x 128 over 2048 tokens are better off whole.  A tenth has to be gained.
   const int64_t bh = a.batch * a.H, tv = tiles_for(a.dk, a.dv, bh, true, bf16);
   const int64_t tt = cdiv(p.rp, wide_for(a.dk, a.dv, bh, true, bf16) ? 128 : 64);
@@ -297,7 +297,8 @@ int64_t square_bytes(const DeltaArgs& a, const Plan& pl, bool bf16, bool query) 
 }
 
 // Heads whose parts of dq and dk a workgroup adds: all that share a key head, unless that leaves CUs idle (4 x 2048
-// tokens, 32 heads of 128 x 128 on 16 key heads, bfloat16: backward 583 us, with parts for every head 778; 2048 tokens,
+// tokens, 32 heads of 128 x 128 on 16 key heads, bfloat16: backward 583 us, with parts for every head 778, since
+// float32 states 673; 2048 tokens,
 // 16 heads of 64 x 64 on one: 105 us, with all in a workgroup 262), and one past 128 keys, where the sums do not fit the
 // registers.
 int64_t grad_heads(const DeltaArgs& a, const Plan& pl) {

@@ -378,7 +378,7 @@ __device__ __forceinline__ void store_parts(const float* n, char* dst, int tid) 
 // A chunk needs nothing of the others, and a workgroup's steps wait for each
 // other: what counts is how many share a CU, hence the scores in the place of the
 // tiles.  It reads k and q and writes five eighths of M and P: 8 x 2048 ragged
-// tokens, 32 heads of 128, bfloat16, 60 us (chunks of a head one after the other,
+// tokens, 32 heads of 128, bfloat16, 58 us (chunks of a head one after the other,
 // each its own rows apart: 84), 4 x 2048 tokens 48.
 template <typename IO, int ROWS, bool VEC>
 __device__ __forceinline__ void delta_prep(const DeltaDev& p, uint32_t pid, char* lds) {
@@ -636,9 +636,9 @@ __device__ __forceinline__ void keep(char* dst, int rows, int cp, int c, int g, 
 // other, and every wavefront's products too (S into x, x into r, r into S), so that a chunk takes what its longest chain
 // takes.  The next chunk's operands are under way meanwhile, those of a product are read and split under the product
 // before.  Two workgroups share a CU (80 KB of LDS, 256 registers): alone a chunk takes 4.2 us, two 7.3 (128 x 128,
-// bfloat16), of which the vector unit is busy for 39 %, the matrix unit for 30 % and 18 % are waits.  A wavefront's
-// priority falls from product to product of a chunk, so that two on a SIMD are in different ones: 8 x 2048 ragged tokens,
-// 32 heads of 128 x 128, bfloat16, 163 us, all alike 175 (rising priorities 174; backwards no order gains anything).
+// bfloat16, M in two parts).  A wavefront's priority falls from product to product of a chunk, so that two on a SIMD are
+// in different ones: 8 x 2048 ragged tokens, 32 heads, 163 us, all alike 175 (rising priorities 174; backwards no order
+// gains anything).  With M in three parts 168, of the busy CUs' time the matrix unit's 39 %.
 template <typename IO, int ROWS, int NW, int MODE, bool VEC>
 __device__ __forceinline__ void delta_walk(const DeltaDev& p, uint32_t pid, char* lds) {
   using K = HeadCfg<IO>;
@@ -1288,7 +1288,7 @@ __device__ __forceinline__ void delta_walk_back(const DeltaDev& p, uint32_t pid,
 // The backward's two walks need nothing of each other: the first half of the workgroups walks forwards, the second half
 // backwards, so that the stores of one lie under the products of the other (forward and backward of 4 x 2048 tokens, 32
 // heads of 128 x 128, bfloat16, 903 us for 983 with a launch each; of 4 x 1999 ragged tokens, 24 heads of 64, float32, 571
-// for 706).  Now 283 and 214 of it.  SEG: the segments' own ends.
+// for 706).  Now 306 and 213 of it.  SEG: the segments' own ends.
 template <typename IO, int ROWS, int NW, bool SEG, bool VEC>
 __global__ void __launch_bounds__((64 * NW), (walk_waves<IO, ROWS, NW>())) ssm_delta_both_kernel(const DeltaDev p, const DeltaDev r, uint32_t first) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
