@@ -1356,10 +1356,10 @@ __device__ __forceinline__ void scan_back(float& hi, float& lo) {
 // barriers; 3.0 TB/s.  Loads are one or two steps of states and, where the registers hold it, a slab ahead.
 //
 // MULTI adds up the heads of a key head in the workgroup: 4 x 2048 tokens, 32 heads of 128 x 128 on 8 key heads, bfloat16,
-// 629 us for the whole backward, 691 with key heads of their own (more loads and stores of keys' gradients).  The next
-// slab's loads then go out behind the products (64 keys: 304 us, ahead of them, with 42 spilled registers, 347).
+// 637 us for the whole backward, 709 with key heads of their own (more loads and stores of keys' gradients).  The next
+// slab's loads then go out behind the products (64 keys, M in two parts: 304 us, ahead of them, with 42 spilled registers, 347).
 // A workgroup is on its CU alone in bfloat16 past 64 keys (its registers), two or three in float32 with one head (4 x 2048
-// tokens, 32 heads of 64 x 64: the backward 462 us; bfloat16 308 with two).
+// tokens, 32 heads of 64 x 64: the backward 468 us; bfloat16 335 with two).
 template <typename IO, int ROWS, int NW, bool MULTI>
 constexpr int grad_waves() { return HeadCfg<IO>::ES == 4 && !MULTI ? (ROWS == 128 ? 4 : ROWS == 64 ? 3 : 2) : 2; }
 
